@@ -16,9 +16,13 @@ from ._binding import (  # noqa: F401
     gdr_fwd_conv,
     gdr_fwd_dense,
     gdr_fwd_snapshots,
+    gdr_gate_norm,
     gdr_get_status,
+    gdr_linattn_fwd,
+    gdr_linattn_workspace_bytes,
     gdr_output_shape,
     gdr_probe_fma,
+    gdr_residual_norm,
     gdr_ring_record_elements,
     gdr_rollback,
     gdr_verify_ring,
@@ -28,6 +32,7 @@ from ._binding import (  # noqa: F401
     prepare_fwd,
     prepare_fwd_conv,
     prepare_fwd_snapshots,
+    prepare_linattn_fwd,
     prepare_rollback,
     prepare_verify_ring,
     status_names,

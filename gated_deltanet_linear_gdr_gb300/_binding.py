@@ -23,7 +23,7 @@ GDR_OK, GDR_ERR_INVALID_ARG, GDR_ERR_UNSUPPORTED, GDR_ERR_CUDA = 0, -1, -2, -3
 GDR_F32, GDR_BF16 = 0, 1
 STATUS_BITS = {
     0x1: "BAD_SLOT", 0x2: "BAD_OFFSETS", 0x4: "BAD_RING_SLOT", 0x8: "BAD_COUNT",
-    0x10: "ROW_TOO_LONG", 0x20: "BAD_ACCEPTED", 0x40: "SNAPSHOT_OVERFLOW",
+    0x10: "ROW_TOO_LONG", 0x20: "BAD_ACCEPTED", 0x40: "SNAPSHOT_OVERFLOW", 0x80: "BAD_DECAY",
 }
 
 
@@ -76,6 +76,44 @@ class gdr_conv_args(ctypes.Structure):
     ]
 
 
+class gdr_linattn_args(ctypes.Structure):
+    """Mirror of struct gdr_linattn_args in include/gdr.h."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("nv", ctypes.c_int32), ("nk", ctypes.c_int32), ("K", ctypes.c_int32),
+        ("V", ctypes.c_int32), ("decay_is_log", ctypes.c_int32), ("token_dtype", ctypes.c_int32),
+        ("state_dtype", ctypes.c_int32), ("total_tokens", ctypes.c_int64), ("max_row_len", ctypes.c_int64),
+        ("q", ctypes.c_void_p), ("q_seq_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+        ("k", ctypes.c_void_p), ("k_seq_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+        ("v", ctypes.c_void_p), ("v_seq_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+        ("decay", ctypes.c_void_p), ("decay_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("out_seq_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+        ("state", ctypes.c_void_p), ("state_slot_stride", ctypes.c_int64), ("state_head_stride", ctypes.c_int64),
+        ("state_kdim_stride", ctypes.c_int64), ("state_vdim_stride", ctypes.c_int64), ("max_slots", ctypes.c_int64),
+        ("slot_idx", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64), ("scale", ctypes.c_float),
+    ]
+
+
+class gdr_norm_args(ctypes.Structure):
+    """Mirror of struct gdr_norm_args in include/gdr.h."""
+    _fields_ = [
+        ("tokens", ctypes.c_int64), ("heads", ctypes.c_int32), ("D", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("gate_first", ctypes.c_int32),
+        ("has_post_norm", ctypes.c_int32), ("has_pre_norm", ctypes.c_int32), ("centered", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+        ("x", ctypes.c_void_p), ("x_seq_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+        ("gate", ctypes.c_void_p), ("gate_seq_stride", ctypes.c_int64), ("gate_head_stride", ctypes.c_int64),
+        ("gate_elem_stride", ctypes.c_int64),
+        ("residual", ctypes.c_void_p), ("residual_seq_stride", ctypes.c_int64),
+        ("residual_head_stride", ctypes.c_int64),
+        ("residual_out", ctypes.c_void_p), ("residual_out_seq_stride", ctypes.c_int64),
+        ("residual_out_head_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("out_seq_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+        ("post_weight", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -107,6 +145,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                 "gdr_fold": ([A, vp, i32, i64, i32, i64, vp, vp, vp], ctypes.c_int),
                 "gdr_fwd_snapshots": ([A, vp, i64, i64, i64, i32, i32, vp], ctypes.c_int),
                 "gdr_rollback": ([A, vp, i64, i64, i64, i32, vp, vp], ctypes.c_int),
+                "gdr_linattn_fwd": ([ctypes.POINTER(gdr_linattn_args), vp], ctypes.c_int),
+                "gdr_linattn_workspace_bytes": ([ctypes.POINTER(gdr_linattn_args)], ctypes.c_int64),
+                "gdr_block_norm": ([ctypes.POINTER(gdr_norm_args), vp], ctypes.c_int),
                 "gdr_get_status": ([ctypes.POINTER(ctypes.c_uint32), i32], ctypes.c_int),
                 "gdr_probe_fma": ([i32, i32, i32, vp, i64, ctypes.POINTER(ctypes.c_int32), vp], ctypes.c_int),
             }
@@ -477,6 +518,242 @@ def gdr_rollback(state, slot_idx, inter, accepted):
     a = make_args(None, None, None, state, slot_idx, None, None, nk=1)
     _check(load_library().gdr_rollback(ctypes.byref(a), inter.data_ptr(), ss, st, sh, n_inter,
                                        accepted.data_ptr(), _stream(state.device)))
+
+
+_DTYPES = {torch.float32: GDR_F32, torch.bfloat16: GDR_BF16}
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
+    return d
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the call on {device}")
+
+
+def make_linattn_args(q, k, v, decay, state, slot_idx, offsets, out, *, decay_is_log=False, scale=0.0,
+                      max_row_len=0) -> gdr_linattn_args:
+    """Pack tensors into gdr_linattn_args (no copies; strides passed through;
+    no workspace)."""
+    td, sd = _dtype(q, "q"), _dtype(state, "state")
+    _dev(k, "k", q.dtype)
+    _dev(v, "v", q.dtype)
+    _dev(out, "out", q.dtype)
+    _dev(decay, "decay", torch.float32)
+    _dev(slot_idx, "slot_idx", torch.int32)
+    _dev(offsets, "offsets", torch.int32)
+    if state.dim() != 4:
+        raise ValueError("state must be [max_slots, nv, K, V]")
+    slots, nv, K, V = state.shape
+    if q.dim() != 3 or q.shape != k.shape or q.shape[2] != K:
+        raise ValueError(f"q and k must both be [T, nk, {K}]")
+    T, nk = q.shape[:2]
+    if v.shape != (T, nv, V) or out.shape != (T, nv, V):
+        raise ValueError(f"v and out must be [T, nv, V] = [{T}, {nv}, {V}]")
+    if decay.shape != (nv,):
+        raise ValueError(f"decay must be [nv] = [{nv}]")
+    if slot_idx.dim() != 1 or not slot_idx.is_contiguous():
+        raise ValueError("slot_idx must be a contiguous [batch] int32 tensor")
+    batch = slot_idx.shape[0]
+    if offsets.shape != (batch + 1,) or not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous [batch+1] int32 tensor")
+    _same_device(q.device, k=k, v=v, out=out, decay=decay, state=state, slot_idx=slot_idx, offsets=offsets)
+    (qt, qh, qc), (kt, kh, kc), (vt, vh, vc), (ot, oh, oc) = q.stride(), k.stride(), v.stride(), out.stride()
+    if qc != 1 or kc != 1 or vc != 1 or oc != 1:
+        raise ValueError("q, k, v and out must have a unit channel stride")
+    ss, sh, sk, sv = state.stride()
+    return gdr_linattn_args(batch, nv, nk, K, V, 1 if decay_is_log else 0, td, sd, T, int(max_row_len),
+                            q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                            decay.data_ptr(), decay.stride(0), out.data_ptr(), ot, oh,
+                            state.data_ptr(), ss, sh, sk, sv, slots, slot_idx.data_ptr(), offsets.data_ptr(),
+                            None, 0, float(scale))
+
+
+def _linattn_workspace(lib, a: gdr_linattn_args, device, workspace):
+    """Give the call its workspace: the caller's, or a new one of the size it asks for."""
+    if workspace is None:
+        need = lib.gdr_linattn_workspace_bytes(ctypes.byref(a))
+        if need < 0:
+            _check(need)
+        if need == 0:
+            return None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _dev(workspace, "workspace")
+        _same_device(device, workspace=workspace)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    a.workspace = workspace.data_ptr()
+    a.workspace_bytes = workspace.numel() * workspace.element_size()
+    return workspace
+
+
+def gdr_linattn_workspace_bytes(q, k, v, decay, state, slot_idx, offsets, *, max_row_len=0) -> int:
+    """Workspace bytes gdr_linattn_fwd would use for these tensors (0: none)."""
+    a = make_linattn_args(q, k, v, decay, state, slot_idx, offsets, v, max_row_len=max_row_len)
+    n = load_library().gdr_linattn_workspace_bytes(ctypes.byref(a))
+    if n < 0:
+        _check(n)
+    return int(n)
+
+
+def gdr_linattn_fwd(q, k, v, decay, state, slot_idx, offsets, out=None, *, decay_is_log=False, scale=0.0,
+                    max_row_len=0, workspace=None):
+    """Decayed linear attention, S <- lambda_h S + k v^T and out = scale S^T q
+    per token, over ragged rows and a slot-indexed pool (include/gdr.h,
+    gdr_linattn_args); state updated in place; returns out.
+
+    q, k [T, nk, K], v [T, nv, V] of one dtype (bfloat16 or float32), decay
+    [nv] float32 (lambda, or ln lambda with decay_is_log), state
+    [max_slots, nv, K, V].  max_row_len = 1 is the single-token step.
+    `workspace` is a device tensor to use instead of a new one of
+    gdr_linattn_workspace_bytes() bytes."""
+    if out is None:
+        out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    a = make_linattn_args(q, k, v, decay, state, slot_idx, offsets, out, decay_is_log=decay_is_log, scale=scale,
+                          max_row_len=max_row_len)
+    lib = load_library()
+    if max_row_len != 1:
+        workspace = _linattn_workspace(lib, a, q.device, workspace)
+    _check(lib.gdr_linattn_fwd(ctypes.byref(a), _stream(q.device)))
+    return out
+
+
+def prepare_linattn_fwd(q, k, v, decay, state, slot_idx, offsets, out, *, decay_is_log=False, scale=0.0,
+                        max_row_len=0, workspace=None) -> "Prepared":
+    a = make_linattn_args(q, k, v, decay, state, slot_idx, offsets, out, decay_is_log=decay_is_log, scale=scale,
+                          max_row_len=max_row_len)
+    lib = load_library()
+    workspace = _linattn_workspace(lib, a, q.device, workspace)
+    return Prepared(lib.gdr_linattn_fwd, a, (), (q, k, v, decay, state, slot_idx, offsets, out, workspace), q.device)
+
+
+_ACTIVATIONS = {None: 0, "silu": 1, "sigmoid": 2}
+
+
+def _activation(name) -> int:
+    if name not in _ACTIVATIONS:
+        raise ValueError('activation must be None, "silu" or "sigmoid"')
+    return _ACTIVATIONS[name]
+
+
+def _weight(w, D: int, name: str, device):
+    if w is None:
+        return None
+    _dev(w, name, torch.float32)
+    if w.shape != (D,) or (D > 1 and w.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous [{D}] float32 tensor")
+    _same_device(device, **{name: w})
+    return w.data_ptr()
+
+
+def _rows(t, name: str):
+    """(seq stride, head stride) of a [T, H, D] or [T, D] tensor."""
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must have a unit channel stride")
+    return (st[0], st[1]) if len(st) == 3 else (st[0], 0)
+
+
+def gdr_gate_norm(x, gate, weight=None, out=None, *, eps=1e-6, activation="silu", gate_first=False, centered=False,
+                  out_dtype=None):
+    """Norm of a recurrence's output times its activated gate, per token and
+    head: out = N(x) * act(gate), or N(x * act(gate)) with gate_first
+    (include/gdr.h, gdr_norm_args).  x and gate [T, H, D] or [T, D] (gate may
+    also be None, or broadcast over the last dimension), float32 or bfloat16;
+    weight [D] float32 or None.  Returns out, of x's shape and out_dtype (by
+    default the gate's dtype, or x's)."""
+    xd = _dtype(x, "x")
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [T, H, D] or [T, D]")
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or (x if gate is None else gate).dtype, device=x.device)
+    elif out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out must have x's shape and dtype out_dtype")
+    od = _dtype(out, "out")
+    _same_device(x.device, gate=gate, out=out)
+    T, D = x.shape[0], x.shape[-1]
+    xt, xh = _rows(x, "x")
+    ot, oh = _rows(out, "out")
+    gp, gd, gt, gh, ge = None, 0, 0, 0, 0
+    if gate is not None:
+        gd = _dtype(gate, "gate")
+        if gate.shape[:-1] != x.shape[:-1] or gate.shape[-1] not in (1, D):
+            raise ValueError("gate must have x's shape, or 1 in its last dimension")
+        gp, (gt, gh), ge = gate.data_ptr(), _rows(gate, "gate"), int(gate.shape[-1] == D)
+    elif gate_first:
+        raise ValueError("gate_first needs a gate")
+    a = gdr_norm_args(T, x.shape[1] if x.dim() == 3 else 1, D, xd, gd, 0, od, _activation(activation),
+                      1 if gate_first else 0, 1, 0, 1 if centered else 0, eps, 1.0, x.data_ptr(), xt, xh, gp, gt, gh, ge,
+                      None, 0, 0, None, 0, 0, out.data_ptr(), ot, oh, _weight(weight, D, "weight", x.device), None)
+    _check(load_library().gdr_block_norm(ctypes.byref(a), _stream(x.device)))
+    return out
+
+
+def gdr_residual_norm(block, residual, weight, *, post_weight=None, gate=None, activation=None, residual_scale=1.0,
+                      eps=1e-6, centered=False, residual_out=None, out=None, out_dtype=None):
+    """Block boundary in one pass: h = residual + residual_scale * act(gate) *
+    N(block; post_weight), out = N(h; weight) (include/gdr.h, gdr_norm_args).
+
+    residual [T, D]; block [T, D], or None for the first norm of a stack (out
+    = N(residual)); post_weight [D] float32, or None for no norm of the
+    block's output; gate [T, D], [T, 1], [D] or None; weight [D] float32, or
+    None for a norm without one.  Returns (residual_out, out): residual_out
+    may be residual itself (in place) and is residual where block is None;
+    out has out_dtype (by default the block's dtype, or residual's)."""
+    rd = _dtype(residual, "residual")
+    if residual.dim() != 2:
+        raise ValueError("residual must be [T, D]")
+    dev = residual.device
+    T, D = residual.shape
+    if out is None:
+        out = torch.empty((T, D), dtype=out_dtype or (residual if block is None else block).dtype, device=dev)
+    elif out.shape != (T, D) or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out must be [T, D] of dtype out_dtype")
+    od = _dtype(out, "out")
+    ot, oh = _rows(out, "out")
+    rt, rh = _rows(residual, "residual")
+    xp, xd, xt, rop, rot = None, 0, 0, None, 0
+    if block is None:
+        if gate is not None or post_weight is not None or residual_out is not None:
+            raise ValueError("gate, post_weight and residual_out need a block")
+        h = residual
+    else:
+        xd = _dtype(block, "block")
+        if block.shape != (T, D):
+            raise ValueError("block must have residual's shape")
+        xp, xt = block.data_ptr(), _rows(block, "block")[0]
+        h = torch.empty((T, D), dtype=residual.dtype, device=dev) if residual_out is None else residual_out
+        if h.shape != (T, D) or h.dtype != residual.dtype:
+            raise ValueError("residual_out must have residual's shape and dtype")
+        rop, rot = h.data_ptr(), _rows(h, "residual_out")[0]
+    _same_device(dev, block=block, gate=gate, residual_out=h, out=out)
+    gp, gd, gt, ge = None, 0, 0, 0
+    if gate is not None:
+        gd, gp = _dtype(gate, "gate"), gate.data_ptr()
+        if gate.shape == (D,):
+            ge = 1
+            if D > 1 and gate.stride(0) != 1:
+                raise ValueError("gate must have a unit channel stride")
+        elif gate.shape in ((T, D), (T, 1)):
+            gt, ge = _rows(gate, "gate")[0], int(gate.shape[1] == D)
+        else:
+            raise ValueError("gate must be [T, D], [T, 1] or [D]")
+    a = gdr_norm_args(T, 1, D, xd, gd, rd, od, _activation(activation), 0, 0 if post_weight is None else 1, 1,
+                      1 if centered else 0, eps, residual_scale, xp, xt, 0, gp, gt, 0, ge, residual.data_ptr(), rt, rh,
+                      rop, rot, 0, out.data_ptr(), ot, oh, _weight(post_weight, D, "post_weight", dev),
+                      _weight(weight, D, "weight", dev))
+    _check(load_library().gdr_block_norm(ctypes.byref(a), _stream(dev)))
+    return h, out
 
 
 def gdr_get_status(clear: bool = True) -> int:

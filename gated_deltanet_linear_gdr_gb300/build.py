@@ -20,8 +20,10 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdr.so")
 SOURCES = ["api.cu", "k_decode.cu", "k_short.cu", "k_chain.cu", "k_chain_fwd.cu", "k_chain_fwd_kv.cu", "k_chain_conv.cu", "k_chain_verify.cu",
-           "k_chain_snap.cu", "k_fold.cu", "k_probe.cu"]
-HEADERS = ["gdr_internal.h", "gdr_device.cuh", "gdr_pipe.cuh", "gdr_state.cuh", "k_chain.cuh", "gdr.map"]
+           "k_chain_snap.cu", "k_fold.cu", "k_probe.cu",
+           "layer/api_layer.cu", "layer/k_norm.cu", "layer/k_la_step.cu"]
+HEADERS = ["gdr_internal.h", "gdr_device.cuh", "gdr_pipe.cuh", "gdr_state.cuh", "k_chain.cuh", "gdr.map",
+           "layer/layer_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -55,7 +57,7 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False) 
     objs, jobs = [], []
     for s in SOURCES:
         src = os.path.join(CSRC, s)
-        obj = os.path.join(BUILD, s.replace(".cu", ".o"))
+        obj = os.path.join(BUILD, s.replace("/", "_").replace(".cu", ".o"))
         objs.append(obj)
         if force or _stale(obj, [src, *hdrs]):
             cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-c", src, "-o", obj]

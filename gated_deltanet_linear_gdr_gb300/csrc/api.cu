@@ -9,6 +9,7 @@
 #include <string>
 
 #include "gdr_internal.h"
+#include "layer/layer_internal.h"
 
 namespace {
 
@@ -53,6 +54,20 @@ int status_ptr(unsigned **out) {
     *out = g_status_ptr[dev];
     return GDR_OK;
 }
+
+}  // namespace
+
+// The same error text and status word for the entry points of other files.
+namespace gdr {
+int api_fail(int code, const char *text) {
+    g_err = text;
+    return code;
+}
+int api_ok() { return ok(); }
+int api_status(unsigned **out) { return status_ptr(out); }
+}  // namespace gdr
+
+namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -1,0 +1,64 @@
+// Internal launch parameters of the layer operators around the recurrence:
+// decayed linear attention and the fused block norms.  Host code (api_layer.cu)
+// validates the public argument structs and lowers them into these.
+#pragma once
+
+#include "../gdr_internal.h"
+
+namespace gdr {
+
+// Error text and status word shared by every entry point (api.cu).
+int api_fail(int code, const char *text);
+int api_ok();
+int api_status(unsigned **out);
+
+// One decayed linear attention call, after validation.  Strides in elements.
+struct LaParams {
+    int batch, nv, nk, r;  // r = nv / nk
+    int K, V;
+    int tiles;             // column tiles of up to 128 values a (row, head) is cut into
+    int decay_is_log;
+    long long T;
+    long long max_len;     // the caller's bound on row lengths, or <= 0
+    const void *q, *k, *v;
+    long long q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;
+    const float *decay;
+    long long decay_s;
+    float scale;
+    void *out;
+    long long o_ts, o_hs;
+    void *state;
+    long long st_slot, st_head, st_k;
+    long long max_slots;
+    const int *slot_idx, *offsets;
+    int tok_vec;           // q, k, v and out rows may be moved as 16-byte vectors
+    unsigned *status;
+};
+
+// Recurrent form on the FP32 pipes: any alignment, any row length; what single
+// tokens, short rows and float32 tokens run on.
+cudaError_t launch_la_step(const LaParams &p, bool tok_bf16, bool state_bf16, cudaStream_t s);
+
+// One fused norm call, after validation.
+struct NormParams {
+    long long tokens;
+    int heads, D;
+    int x_bf16, gate_bf16, res_bf16, out_bf16;
+    int act, gate_first, post, pre, centered;
+    float eps, scale, inv_d;
+    const void *x;
+    long long x_ts, x_hs;
+    const void *gate;
+    long long g_ts, g_hs, g_es;
+    const void *res;
+    long long r_ts, r_hs;
+    void *res_out;
+    long long ro_ts, ro_hs;
+    void *out;
+    long long o_ts, o_hs;
+    const float *post_w, *pre_w;
+};
+// vec: every row, gate and weight may be moved as vectors of 8 elements.
+cudaError_t launch_norm(const NormParams &p, bool vec, cudaStream_t s);
+
+}  // namespace gdr

@@ -69,6 +69,7 @@ extern "C" {
 #define GDR_STATUS_ROW_TOO_LONG 0x10u     /* a row longer than args.max_row_len        */
 #define GDR_STATUS_BAD_ACCEPTED 0x20u     /* rollback index outside [-1, n_inter)      */
 #define GDR_STATUS_SNAPSHOT_OVERFLOW 0x40u /* a row has more complete drafts than n_inter */
+#define GDR_STATUS_BAD_DECAY 0x80u        /* gdr_linattn_fwd: a head's lambda outside [0, 1] */
 
 /* ---- dtypes ------------------------------------------------------------- */
 typedef enum gdr_dtype { GDR_F32 = 0, GDR_BF16 = 1 } gdr_dtype;
@@ -341,6 +342,139 @@ int gdr_fwd_snapshots(const gdr_step_args *args, void *inter, int64_t inter_slot
 int gdr_rollback(const gdr_step_args *args, const void *inter, int64_t inter_slot_stride,
                  int64_t inter_token_stride, int64_t inter_head_stride, int32_t n_inter,
                  const int32_t *accepted, void *stream);
+
+/*
+ * Decayed linear attention (no counterpart on the pages; the sibling layer of
+ * the recurrence above, on the same pool, rows, heads and padding convention).
+ * For every live row b and value head h, key head hk = h / (nv / nk), with one
+ * decay lambda_h in [0, 1] for each value head and the state
+ * S = pool[slot_idx[b], h] stored [key index, value index], each token t does
+ *
+ *     S = lambda_h * S + k_t v_t^T
+ *     out[t, h] = scale * S^T q_t
+ *
+ * q, k     [total_tokens, nk, K] in token_dtype; element (t, hk, i) at
+ *          t*seq_stride + hk*head_stride + i (unit channel stride).
+ * v, out   [total_tokens, nv, V] in token_dtype, the same way.
+ * decay    [nv] float32, element h at h*decay_stride: lambda, or ln lambda
+ *          (decay_is_log; -inf is lambda = 0, where a token sees itself only).
+ *          A value outside [0, 1] (or NaN) skips the head: zero output, state
+ *          untouched, GDR_STATUS_BAD_DECAY.
+ * state, slot_idx, offsets, scale, max_row_len   as in gdr_step_args.
+ * workspace  device memory the call may use, 16-byte aligned, or NULL;
+ *          gdr_linattn_workspace_bytes() says how much pays off.  A call with
+ *          less is right too, and slower where few rows are long.
+ * K and V are multiples of 16, K up to 128 and V up to 256, in any
+ * combination.  State and sums are float32 inside a call; a bfloat16 pool and
+ * bfloat16 outputs are rounded to nearest-even once.  A non-finite value in a
+ * token's q, k or v spoils outputs of its own row only, but there also those of
+ * up to 63 tokens before it (prompts are computed 64 tokens at a time).
+ */
+typedef struct gdr_linattn_args {
+    int32_t batch;
+    int32_t nv;
+    int32_t nk;
+    int32_t K;
+    int32_t V;
+    int32_t decay_is_log;
+    int32_t token_dtype; /* gdr_dtype of q, k, v and out */
+    int32_t state_dtype; /* gdr_dtype of the pool        */
+    int64_t total_tokens;
+    int64_t max_row_len;
+    const void *q;
+    int64_t q_seq_stride;
+    int64_t q_head_stride;
+    const void *k;
+    int64_t k_seq_stride;
+    int64_t k_head_stride;
+    const void *v;
+    int64_t v_seq_stride;
+    int64_t v_head_stride;
+    const float *decay;
+    int64_t decay_stride;
+    void *out;
+    int64_t out_seq_stride;
+    int64_t out_head_stride;
+    void *state;
+    int64_t state_slot_stride;
+    int64_t state_head_stride;
+    int64_t state_kdim_stride;
+    int64_t state_vdim_stride;
+    int64_t max_slots;
+    const int32_t *slot_idx;
+    const int32_t *offsets;
+    void *workspace;
+    int64_t workspace_bytes;
+    float scale;
+} gdr_linattn_args;
+
+/* Runs every row over its tokens, writes out for every token (zeros for padding
+ * rows) and each live row's final state back to its slot; rows of length 0
+ * leave their slot untouched.  The form (single tokens, short rows, chunks on
+ * the tensor cores, chunks of segments computed apart and joined) is chosen
+ * from the sizes, types and alignment; forms differ in rounding only. */
+int gdr_linattn_fwd(const gdr_linattn_args *args, void *stream);
+
+/* Workspace bytes that gdr_linattn_fwd would use for these arguments (0 where
+ * it needs none), or a negative code.  Reads sizes, types, strides and the
+ * token pointers' alignment only. */
+int64_t gdr_linattn_workspace_bytes(const gdr_linattn_args *args);
+
+/*
+ * Norms around a block (no counterpart on the pages), fused with the block's
+ * gate, residual scale and residual add.  For every (token, head) row of D
+ * values, in float32, each output rounded once:
+ *
+ *     N(x; w) = (x - m) / sqrt(mean((x - m)^2) + eps) * w,  m = mean(x) if centered, else 0
+ *     u = x                        (has_post_norm: u = N(x; post_weight))
+ *     u = u * act(gate)            (gate given; gate_first: u = N(x * act(gate); post_weight))
+ *     h = residual + residual_scale * u   (residual given; else h = u)
+ *     residual_out = h             (given)
+ *     out = h                      (has_pre_norm: out = N(h; pre_weight))
+ *
+ * x        [tokens, heads, D] or NULL (then u = 0 and a residual is needed).
+ * gate     element (t, h, j) at t*gate_seq_stride + h*gate_head_stride +
+ *          j*gate_elem_stride; strides of 0 broadcast it.
+ * residual, residual_out, out   [tokens, heads, D]; residual_out may be residual.
+ * weights  [D] float32, or NULL for 1.
+ * Channel strides are 1 (gate: 0 or 1); D is at most 16384.
+ */
+typedef struct gdr_norm_args {
+    int64_t tokens;
+    int32_t heads;
+    int32_t D;
+    int32_t x_dtype;
+    int32_t gate_dtype;
+    int32_t residual_dtype; /* of residual and residual_out */
+    int32_t out_dtype;
+    int32_t activation; /* 0: none, 1: SiLU, 2: sigmoid */
+    int32_t gate_first;
+    int32_t has_post_norm;
+    int32_t has_pre_norm;
+    int32_t centered;
+    float eps;
+    float residual_scale;
+    const void *x;
+    int64_t x_seq_stride;
+    int64_t x_head_stride;
+    const void *gate;
+    int64_t gate_seq_stride;
+    int64_t gate_head_stride;
+    int64_t gate_elem_stride;
+    const void *residual;
+    int64_t residual_seq_stride;
+    int64_t residual_head_stride;
+    void *residual_out;
+    int64_t residual_out_seq_stride;
+    int64_t residual_out_head_stride;
+    void *out;
+    int64_t out_seq_stride;
+    int64_t out_head_stride;
+    const float *post_weight;
+    const float *pre_weight;
+} gdr_norm_args;
+
+int gdr_block_norm(const gdr_norm_args *args, void *stream);
 
 /* Reads the current device's status word (GDR_STATUS_* bits) into *status and,
  * if clear != 0, resets it.  Synchronises the device. */
