@@ -24,6 +24,7 @@ GDR_F32, GDR_BF16 = 0, 1
 STATUS_BITS = {
     0x1: "BAD_SLOT", 0x2: "BAD_OFFSETS", 0x4: "BAD_RING_SLOT", 0x8: "BAD_COUNT",
     0x10: "ROW_TOO_LONG", 0x20: "BAD_ACCEPTED", 0x40: "SNAPSHOT_OVERFLOW", 0x80: "BAD_DECAY",
+    0x100: "TIMEOUT",
 }
 
 

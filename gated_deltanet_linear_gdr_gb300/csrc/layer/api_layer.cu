@@ -124,6 +124,9 @@ gdr::LaParams lower(const gdr_linattn_args *a, unsigned *status) {
     return p;
 }
 
+// Rows of at most this many tokens (by the caller's bound) take the recurrent form.
+constexpr long long kStepRowMax = 16;
+
 int launched(cudaError_t e, const char *fn) {
     if (e != cudaSuccess) return fail(GDR_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
     return gdr::api_ok();
@@ -146,6 +149,12 @@ int gdr_linattn_fwd(const gdr_linattn_args *a, void *stream) {
     unsigned *st = nullptr;
     if ((rc = gdr::api_status(&st))) return rc;
     const gdr::LaParams p = lower(a, st);
+    if (a->token_dtype == GDR_BF16 && p.tok_vec && p.T > 0 && (p.max_len <= 0 || p.max_len > kStepRowMax)) {
+        bool used = false;
+        const cudaError_t e = gdr::launch_la_chunk(p, a->state_dtype == GDR_BF16, 0, nullptr,
+                                                   static_cast<cudaStream_t>(stream), &used);
+        if (used || e != cudaSuccess) return launched(e, fn);
+    }
     return launched(gdr::launch_la_step(p, a->token_dtype == GDR_BF16, a->state_dtype == GDR_BF16,
                                         static_cast<cudaStream_t>(stream)),
                     fn);

@@ -70,6 +70,7 @@ extern "C" {
 #define GDR_STATUS_BAD_ACCEPTED 0x20u     /* rollback index outside [-1, n_inter)      */
 #define GDR_STATUS_SNAPSHOT_OVERFLOW 0x40u /* a row has more complete drafts than n_inter */
 #define GDR_STATUS_BAD_DECAY 0x80u        /* gdr_linattn_fwd: a head's lambda outside [0, 1] */
+#define GDR_STATUS_TIMEOUT 0x100u         /* a wait inside a kernel ran out: the call's results are not valid */
 
 /* ---- dtypes ------------------------------------------------------------- */
 typedef enum gdr_dtype { GDR_F32 = 0, GDR_BF16 = 1 } gdr_dtype;
