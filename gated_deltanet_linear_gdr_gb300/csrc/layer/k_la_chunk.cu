@@ -11,15 +11,21 @@
 // Everything is kept transposed (value index = tensor memory lane), so that
 // the state, which a warp's lanes hold in float32 registers, goes back into
 // tensor memory as the A operand of S0^T Q^T, and V^T serves two products.
-// Rounding to bfloat16: P~ once (as the output is).  The state operand is split
-// into two bfloat16 parts and K~ into two (bfloat16 pool) or three (float32
-// pool), which keeps 16 and 24 bits: the state itself never loses any.
+// Rounding to bfloat16: P~ and the state as operand of the readout, once each,
+// as the output itself is; their errors are independent of the output's, so an
+// output is at most sqrt(2) as far off as its own rounding makes it (measured
+// 2.1e-3 against 1.7e-3).  The state itself loses nothing: it stays in
+// float32, and K~ is split into two (bfloat16 pool) or three (float32 pool)
+// bfloat16 parts, which keep 16 and 24 bits.
 //
 // One CTA per SM walks (row segment, value head, 128-column tile) units, with
-// a warp role for each step: TMA loads three chunks ahead, one thread issues
-// the matrix products, 4 warps make K~, 8 warps keep S, 4 warps make P~ and
-// write the output.  Roles hand over through mbarriers, so the products of a
-// chunk run under the elementwise work of its neighbours.
+// a warp role for each step: 8 warps keep S, 4 make K~, 4 make P~, 4 write the
+// output, one each issues K Q^T, the state's product and the output's two, and
+// one loads three chunks ahead by TMA.  Roles hand over through mbarriers, so
+// the products of a chunk run under the elementwise work of its neighbours.
+// (A product of 64 x 128 x 16 holds the tensor cores for 32 to 64 cycles, but
+// its issuer, with its waits, for about 110: one issuing warp for all 28 of a
+// chunk measured 3100 cycles a chunk, the slowest of the roles.)
 //
 // Bound: a chunk of one head with K = V = 128 moves 64 KiB (1.47 us of an SM's
 // share of HBM) and holds the tensor cores for about 1400 (bfloat16 pool) to
@@ -33,6 +39,8 @@ namespace {
 
 using namespace tc;
 
+// Key channels are padded to KP = 64 or 128: TMA reads zeros past K, and zeros
+// add nothing to any of the products.
 constexpr int kC = 64;        // tokens a chunk
 constexpr int kStages = 3;
 constexpr int kSub = kC * 128;        // bytes of a 64-token x 64-channel operand block
@@ -40,24 +48,27 @@ constexpr int kTile = 2 * kSub;       // bytes of a 64-token x 128-channel opera
 constexpr int kStage = 3 * kTile;     // Q | K | V
 constexpr int kMaxRows = 128;         // rows whose order and segments are worked out in shared memory
 
-constexpr int kWarpsS = 8, kWarpsP = 4, kWarpsK = 4;
-constexpr int kWarpMma = kWarpsS + kWarpsP + kWarpsK, kWarpTma = kWarpMma + 1;
-constexpr int kThreads = 32 * (kWarpTma + 1);
+// Warps by role, in warpgroups of 4.
+constexpr int kWarpsS = 8, kWarpsO = 4, kWarpsP = 4, kWarpsK = 4;
+constexpr int kWarpO = kWarpsS, kWarpP = kWarpO + kWarpsO, kWarpK = kWarpP + kWarpsP, kWarpMma = kWarpK + kWarpsK;
+constexpr int kThreads = 32 * (kWarpMma + 4);  // the last warpgroup: three issuers and the loader
+// Registers a thread: 768 threads are launched with 80, and the roles share them out anew.
+constexpr int kRegsS = 96, kRegsO = 80, kRegsP = 96, kRegsK = 72, kRegsRest = 40;
+static_assert(2 * kRegsS + kRegsO + kRegsP + kRegsK + kRegsRest == 6 * 80, "shares");
 
 // tensor memory columns
-constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 192, kColDS = 256, kColHi = 384, kColLo = 448;
+constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 192, kColDS = 256, kColS = 384;
 
 enum Bar {
-    kFull = 0, kEmpty = kFull + kStages, kPFull = kEmpty + kStages, kPFree = kPFull + 2, kPtFull = kPFree + 2,
-    kSFull, kSFree, kDsFull, kDsFree, kKtFull, kOFull, kOFree, kDrain, kBars
+    kLoaded = 0, kStageFree = kLoaded + kStages, kPFull = kStageFree + kStages, kPFree = kPFull + 2, kPtFull = kPFree + 2, kSFull, kDsFull = kSFull + 2,
+    kDsFree = kDsFull + 2, kKtFull, kOFull = kKtFull + 2, kOFree = kOFull + 2, kDrain, kBars
 };
 
 struct Smem {
     unsigned char stage[kStages][kStage];
-    unsigned char kt[3][kTile];   // K~, its bfloat16 parts
-    unsigned char pt[kSub];       // P~^T
-    unsigned char ost[kWarpsP][kC * 64];  // output on its way out, [token][32 columns] a warp
-    float factor[kWarpsP][2][kC];         // scale lambda^(i+1), by unit parity
+    unsigned char kt[2][2][kTile];        // second and third part of K~, two chunks; the first takes K's place
+    unsigned char pt[kSub];               // P~^T
+    unsigned char ost[kWarpsO][32 * 64];  // output on its way out, 32 tokens x 32 columns a warp
     uint64_t bar[kBars];
     int order[kMaxRows], first[kMaxRows + 1];
     uint32_t tmem;
@@ -70,6 +81,7 @@ struct ChunkParams {
     int seg;    // tokens a segment (a multiple of kC), or 0: rows are whole
     int parts;  // bfloat16 parts of K~
     float *ws;  // start states of the segments [segment, nv, K, V] (seg != 0)
+    FastDiv per, tiles;  // units a segment (nv * tiles), column tiles
 };
 
 // A unit of work, the same for every role: one segment of a row, one head, one column tile.
@@ -93,16 +105,26 @@ template <bool STATES> struct Walk {
     int i = 0;
     __device__ Walk(const ChunkParams &c_, const Smem &sm_) : c(c_), sm(sm_) {}
 
-    __device__ bool next(Unit &u, bool report) {
+    // The next unit; every lane has the same, and the compiler is told so.
+    __device__ __forceinline__ bool next(Unit &u, bool report) {
+        const bool more = find(u, report);
+        u.h = (int)uniform(u.h);
+        u.tile = (int)uniform(u.tile);
+        u.t0 = (int)uniform(u.t0);
+        u.len = (int)uniform(u.len);
+        u.chunks = (int)uniform(u.chunks);
+        u.x = (int)uniform(u.x);
+        return uniform(more) != 0;
+    }
+    __device__ bool find(Unit &u, bool report) {
         const LaParams &p = c.p;
-        const unsigned per = (unsigned)(p.nv * p.tiles), G = gridDim.x;
-        const long long pos = (long long)i * G + ((i & 1) ? G - 1 - blockIdx.x : blockIdx.x);
+        u.t0 = u.x = u.h = u.tile = u.len = u.chunks = u.skip_len = 0;
+        const unsigned G = gridDim.x, pos = (unsigned)i * G + ((i & 1) ? G - 1 - blockIdx.x : blockIdx.x);
         ++i;
-        const long long xx = pos / per;
-        const int ht = (int)(pos - xx * per);
-        u.h = ht / p.tiles;
-        u.tile = ht - u.h * p.tiles;
-        u.x = (int)xx;
+        u.x = (int)c.per.div(pos);  // positions are below 2^31 and a walk ends at the first one past the units
+        const unsigned ht = pos - (unsigned)u.x * c.per.d;
+        u.h = (int)c.tiles.div(ht);
+        u.tile = (int)(ht - (unsigned)u.h * c.tiles.d);
         int seg_i = 0;
         if (p.batch <= kMaxRows) {
             int r = u.x;
@@ -116,10 +138,9 @@ template <bool STATES> struct Walk {
             }
             u.b = sm.order[r];
         } else {
-            if (xx >= p.batch) return false;
+            if (u.x >= p.batch) return false;
             u.b = u.x;
         }
-        u.len = u.chunks = u.skip_len = 0;
         u.first = u.last = true;
         const int r0 = p.offsets[u.b], r1 = p.offsets[u.b + 1];
         u.slot = p.slot_idx[u.b];
@@ -183,7 +204,7 @@ __device__ __forceinline__ void plan_rows(const ChunkParams &c, Smem &sm) {
         int end = n;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const int o = __shfl_up_sync(kFull, end, m);
+            const int o = __shfl_up_sync(0xffffffffu, end, m);
             if (lane >= m) end += o;
         }
         __syncwarp();
@@ -195,6 +216,9 @@ __device__ __forceinline__ void plan_rows(const ChunkParams &c, Smem &sm) {
 
 // ---- the roles ----------------------------------------------------------------
 
+// A phase's parity is never ambiguous: a barrier completes its phase for chunk
+// g + 1 (of a pair of barriers: g + 2) only after every waiter has passed the
+// one for chunk g, since each waiter's own work for g is among what that takes.
 struct Ctx {
     const ChunkParams &c;
     Smem &sm;
@@ -202,7 +226,10 @@ struct Ctx {
     uint32_t bars;
     uint32_t tmem;
     __device__ uint32_t bar(int i) const { return bars + 8u * (uint32_t)i; }
-    __device__ bool wait(int i, uint32_t parity) const { return mbar_wait(bar(i), parity & 1u, &sm.gave_up); }
+    // The answer is the warp's, so that loops that end by it keep the warp together.
+    __device__ bool wait(int i, uint32_t parity) const {
+        return __all_sync(0xffffffffu, mbar_wait(bar(i), parity & 1u, &sm.gave_up));
+    }
     __device__ uint32_t stage(unsigned g) const { return base + (uint32_t)(g % kStages) * kStage; }
     // one arrival for the warp, once every lane has got here
     __device__ void arrive(int i) const {
@@ -211,337 +238,325 @@ struct Ctx {
     }
 };
 
-template <bool STATES>
-__device__ void role_tma(const Ctx &x, const CUtensorMap *mq, const CUtensorMap *mk, const CUtensorMap *mv) {
-    const LaParams &p = x.c.p;
-    const int nk = p.K > 64 ? 2 : 1;
-    Walk<STATES> walk(x.c, x.sm);
+// Chunks in order, into the stages.
+template <int KP, bool STATES> struct Loader {
+    const Ctx &x;
+    const CUtensorMap *mq, *mk, *mv;
+    Walk<STATES> walk;
     Unit u;
+    int j;
     unsigned g = 0;
-    bool good = true;
-    while (good && walk.next(u, false)) {
-        const int hk = u.h / p.r, v0 = u.tile * 128, nv = p.V - v0 > 64 ? 2 : 1;
-        const uint32_t bytes = (uint32_t)((STATES ? 1 : 2) * nk + nv) * kSub;
-        for (int j = 0; j < u.chunks; ++j, ++g) {
-            const int s = g % kStages;
-            if (g >= kStages && !(good = x.wait(kEmpty + s, g / kStages - 1))) break;
-            const uint32_t dst = x.stage(g), full = x.bar(kFull + s);
-            mbar_expect(full, bytes);
-            const int t = u.t0 + j * kC;
-            for (int i = 0; i < nk; ++i) tma_load3(dst + kTile + i * kSub, mk, i * 64, hk, t, full);
-            for (int i = 0; i < nv; ++i) tma_load3(dst + 2 * kTile + i * kSub, mv, v0 + i * 64, u.h, t, full);
-            if (!STATES)
-                for (int i = 0; i < nk; ++i) tma_load3(dst + i * kSub, mq, i * 64, hk, t, full);
-        }
-    }
-    // no copy is in flight when the CTA ends
-    for (unsigned o = g > kStages ? g - kStages : 0; o < g; ++o) {
-        volatile int never = 0;
-        mbar_wait(x.bar(kFull + o % kStages), (o / kStages) & 1u, &never);
-    }
-}
-
-template <bool STATES> __device__ void role_mma(const Ctx &x) {
-    const LaParams &p = x.c.p;
-    const int ksteps = p.K / 16;
-    const uint32_t id_p = idesc_bf16(64, kC, false, false);    // P^T = K Q^T
-    const uint32_t id_o1 = idesc_bf16(128, kC, false, false);  // S0^T Q^T
-    const uint32_t id_o2 = idesc_bf16(128, kC, true, true);    // V^T P~^T
-    const uint32_t id_s = idesc_bf16(128, p.K, true, true);    // V^T K~
-    const uint32_t pt = x.base + offsetof(Smem, pt), kt = x.base + offsetof(Smem, kt);
-    auto scores = [&](unsigned g) {
-        if (!x.wait(kFull + g % kStages, g / kStages)) return false;
-        if (g >= 2 && !x.wait(kPFree + (g & 1), (g >> 1) - 1)) return false;
-        fence_after();
-        const uint32_t q = x.stage(g), k = q + kTile, d = x.tmem + kColP + (g & 1) * kC;
-        for (int i = 0; i < ksteps; ++i) {
-            const uint32_t at = (uint32_t)(i >> 2) * kSub + (uint32_t)(i & 3) * 32;
-            mma_ss(d, desc128(k + at, 16, 1024), desc128(q + at, 16, 1024), id_p, i > 0);
-        }
-        mma_commit(x.bar(kPFull + (g & 1)));
-        return true;
-    };
-    Walk<STATES> walk(x.c, x.sm);
-    Unit u;
-    unsigned g = 0;
-    int left = 0;  // chunks of the current unit that are still to do
     bool more = true;
-    auto next_unit = [&]() {  // moves on to a unit with chunks
-        while (left == 0 && (more = walk.next(u, false))) left = u.chunks;
-        return left > 0;
-    };
-    bool good = next_unit() && (STATES || scores(0));
-    while (good) {
-        const uint32_t q = x.stage(g), v = q + 2 * kTile;
-        // V^T K~ over all parts of K~
-        good = x.wait(kKtFull, g) && (g == 0 || x.wait(kDsFree, g - 1));
-        if (!good) break;
-        fence_after();
-        for (int part = 0; part < x.c.parts; ++part)
-            for (int i = 0; i < kC / 16; ++i)
-                mma_ss(x.tmem + kColDS, desc128(v + i * 2048, kSub, 1024), desc128(kt + part * kTile + i * 2048, kSub, 1024),
-                       id_s, part + i > 0);
-        mma_commit(x.bar(kDsFull));
-        if (STATES) {
-            mma_commit(x.bar(kEmpty + g % kStages));
-        } else {
-            // S0^T Q^T, both parts of the state
-            good = x.wait(kSFull, g) && (g == 0 || x.wait(kOFree, g - 1));
-            if (!good) break;
-            fence_after();
-            for (int half = 0; half < 2; ++half)
-                for (int i = 0; i < ksteps; ++i) {
-                    const uint32_t at = (uint32_t)(i >> 2) * kSub + (uint32_t)(i & 3) * 32;
-                    mma_ts(x.tmem + kColO1, x.tmem + (half ? kColLo : kColHi) + i * 8, desc128(q + at, 16, 1024), id_o1,
-                           half + i > 0);
-                }
-            mma_commit(x.bar(kSFree));
-            if (!(good = x.wait(kPtFull, g))) break;
-            fence_after();
-            for (int i = 0; i < kC / 16; ++i)
-                mma_ss(x.tmem + kColO2, desc128(v + i * 2048, kSub, 1024), desc128(pt + i * 2048, kSub, 1024), id_o2, i > 0);
-            mma_commit(x.bar(kOFull));
-            mma_commit(x.bar(kEmpty + g % kStages));
-        }
-        ++g;
-        --left;
-        if (!next_unit()) break;
-        if (!STATES) good = scores(g);
+    __device__ Loader(const Ctx &x_, const CUtensorMap *q, const CUtensorMap *k, const CUtensorMap *v)
+        : x(x_), mq(q), mk(k), mv(v), walk(x_.c, x_.sm), j(0) {
+        u.chunks = 0;
     }
-    // no matrix instruction is in flight when tensor memory is freed
-    mma_commit(x.bar(kDrain));
+
+    // Loads the next chunk, if there is one, once its stage is free; false where a wait gave up.
+    __device__ bool step() {
+        while (more && j >= u.chunks) {
+            more = walk.next(u, false);
+            j = 0;
+        }
+        if (!more) return true;
+        const int s = g % kStages;
+        if (g >= kStages && !x.wait(kStageFree + s, g / kStages - 1)) return false;
+        if (elect_one()) {
+            const LaParams &p = x.c.p;
+            constexpr int nk = KP / 64;
+            const int v0 = u.tile * 128, nv = p.V - v0 > 64 ? 2 : 1, hk = u.h / p.r, t = u.t0 + j * kC;
+            const uint32_t dst = x.stage(g), full = x.bar(kLoaded + s);
+            mbar_expect(full, (uint32_t)((STATES ? 1 : 2) * nk + nv) * kSub);
+#pragma unroll
+            for (int i = 0; i < nk; ++i) {
+                tma_load3(dst + kTile + i * kSub, mk, i * 64, hk, t, full);
+                if (!STATES) tma_load3(dst + i * kSub, mq, i * 64, hk, t, full);
+            }
+            for (int i = 0; i < nv; ++i) tma_load3(dst + 2 * kTile + i * kSub, mv, v0 + i * 64, u.h, t, full);
+        }
+        __syncwarp();
+        ++g;
+        ++j;
+        return true;
+    }
+    // No copy is in flight when the CTA ends.
+    __device__ void drain() {
+        volatile int never = 0;
+        for (unsigned o = g > kStages ? g - kStages : 0; o < g; ++o)
+            mbar_wait(x.bar(kLoaded + o % kStages), (o / kStages) & 1u, &never);
+    }
+};
+
+// The issuing warps.  How many chunks this CTA has:
+template <bool STATES> __device__ __forceinline__ unsigned count_chunks(const Ctx &x) {
+    Walk<STATES> walk(x.c, x.sm);
+    Unit u;
+    unsigned total = 0;
+    while (walk.next(u, false)) total += (unsigned)u.chunks;
+    return total;
+}
+// No product is under way when tensor memory is freed.
+__device__ __forceinline__ void drain_mma(const Ctx &x) {
+    __syncwarp();
+    mma_commit(elect_one(), x.bar(kDrain));
     volatile int never = 0;
     mbar_wait(x.bar(kDrain), 0, &never);
 }
 
+// P^T = K Q^T
+template <int KP> __device__ void role_mma_scores(const Ctx &x) {
+    const uint32_t id = idesc_bf16(64, kC, false, false);
+    const uint64_t d_km = desc128(x.base, 16, 1024);  // stage 0, K-major
+    const unsigned total = count_chunks<false>(x);
+    for (unsigned g = 0; g < total; ++g) {
+        // the buffer has been read, and the last product into it has been seen by both its waiters
+        if (g > 1 && (!x.wait(kPFree + (g & 1), (g >> 1) - 1) || !x.wait(kKtFull + (g & 1), (g >> 1) - 1))) break;
+        if (!x.wait(kLoaded + g % kStages, g / kStages)) break;
+        fence_after();
+        const uint32_t me = elect_one(), st = uniform(g % kStages), odd = uniform(g & 1);
+        const uint64_t q = d_km + (st * kStage >> 4);
+        mma_ss_k<KP / 16>(me, x.tmem + kColP + odd * kC, q + (kTile >> 4), q, id, kSub);
+        mma_commit(me, x.bar(kPFull) + 8 * odd);
+    }
+    drain_mma(x);
+}
+
+// V^T K~
+template <int KP, bool STATES> __device__ void role_mma_state(const Ctx &x) {
+    const uint32_t id = idesc_bf16(128, KP, true, true);
+    const uint64_t d_mn = desc128(x.base, kSub, 1024);  // stage 0, MN-major
+    const uint64_t d_kt = desc128(x.base + (uint32_t)offsetof(Smem, kt), kSub, 1024);
+    const unsigned total = count_chunks<STATES>(x);
+    for (unsigned g = 0; g < total; ++g) {
+        if (!x.wait(kLoaded + g % kStages, g / kStages) || !x.wait(kKtFull + (g & 1), g >> 1) ||
+            (g > 0 && !x.wait(kDsFree, g - 1)))
+            break;
+        fence_after();
+        const uint32_t me = elect_one(), st = uniform(g % kStages), odd = uniform(g & 1);
+        const uint64_t k = d_mn + ((st * kStage + kTile) >> 4), v = k + (kTile >> 4), kt = d_kt + (odd * 2 * kTile >> 4);
+        mma_ss_mn64<false>(me, x.tmem + kColDS, v, k, id);
+        mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt, id);
+        if (x.c.parts == 3) mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt + (kTile >> 4), id);
+        mma_commit(me, x.bar(kDsFull) + 8 * odd);
+        mma_commit(me, x.bar(kStageFree) + 8 * st);
+    }
+    drain_mma(x);
+}
+
+// S0^T Q^T and V^T P~^T
+template <int KP> __device__ void role_mma_out(const Ctx &x) {
+    const uint32_t id1 = idesc_bf16(128, kC, false, false), id2 = idesc_bf16(128, kC, true, true);
+    const uint64_t d_km = desc128(x.base, 16, 1024), d_v = desc128(x.base + 2 * kTile, kSub, 1024);
+    const uint64_t d_pt = desc128(x.base + (uint32_t)offsetof(Smem, pt), kSub, 1024);
+    const unsigned total = count_chunks<false>(x);
+    for (unsigned g = 0; g < total; ++g) {
+        if (!x.wait(kLoaded + g % kStages, g / kStages) || (g > 0 && !x.wait(kOFree, g - 1)) ||
+            !x.wait(kSFull + (g & 1), g >> 1))
+            break;
+        fence_after();
+        const uint32_t me = elect_one(), st = uniform(g % kStages), odd = uniform(g & 1);
+        const uint64_t q = d_km + (st * kStage >> 4);
+        mma_ts_k<KP / 16>(me, x.tmem + kColO1, x.tmem + kColS + odd * 64, q, id1, kSub);
+        if (!x.wait(kPtFull, g)) break;
+        fence_after();
+        mma_ss_mn64<false>(me, x.tmem + kColO2, d_v + (st * kStage >> 4), d_pt, id2);
+        mma_commit(me, x.bar(kOFull) + 8 * odd);
+        mma_commit(me, x.bar(kStageFree) + 8 * st);
+    }
+    drain_mma(x);
+}
+
+// In a row's last chunk the tokens past its end belong to somebody else.  They
+// are cleared in V, since zero times infinity is not zero, by both roles
+// whose products read V, each before its own.
+__device__ __forceinline__ void clear_tail(unsigned char *v, int n, int nv, int tid, int threads) {
+    for (int i = n * 8 + tid; i < kC * 8; i += threads)
+        for (int sub = 0; sub < nv; ++sub) *reinterpret_cast<uint4 *>(v + sub * kSub + i * 16) = make_uint4(0, 0, 0, 0);
+}
+
 // K~[j] = lambda^(n-1-j) k_j in bfloat16 parts, at the places K has in its
-// swizzled block: a thread has 16-byte vectors of 4 tokens.  In a row's last
-// chunk the tokens past its end, which belong to somebody else, become zero,
-// in V as well: a product of zero and infinity would not.
-template <bool STATES> __device__ void role_keys(const Ctx &x, int tid) {
+// swizzled block: a thread has 16-byte vectors of 4 tokens.
+template <int KP, bool STATES> __device__ void role_keys(const Ctx &x, int warp, int lane) {
     const LaParams &p = x.c.p;
-    const int nk = p.K > 64 ? 2 : 1;
+    const int tid = warp * 32 + lane, row = tid / 8, parts = x.c.parts;
     Walk<STATES> walk(x.c, x.sm);
     Unit u;
     unsigned g = 0;
     while (walk.next(u, false)) {
-        float w[4];
         const int nv = p.V - u.tile * 128 > 64 ? 2 : 1;
+        const float lam16 = power(u.lg2, 16);
+        float w3 = 0.0f;  // weight of this thread's last token
         for (int j = 0; j < u.chunks; ++j, ++g) {
             const int n = min(kC, u.len - j * kC);
-            if (j == 0 || n < kC) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int back = n - 1 - (i * 16 + tid / 8);
-                    w[i] = back < 0 ? 0.0f : power(u.lg2, back);
-                }
-            }
-            if (!x.wait(kFull + g % kStages, g / kStages)) return;
-            if (g > 0 && !x.wait(kDsFull, g - 1)) return;  // the products that read the last K~ are done
+            if (j == 0 || n < kC) w3 = power(u.lg2, max(n - 1 - (48 + row), 0));
+            if (!x.wait(kLoaded + g % kStages, g / kStages)) return;
             unsigned char *stage = x.sm.stage[g % kStages];
-            for (int sub = 0; sub < nk; ++sub) {
+            if (__builtin_expect(n < kC, 0)) clear_tail(stage + 2 * kTile, n, nv, tid, 32 * kWarpsK);
+            if (!STATES && !x.wait(kPFull + (g & 1), g >> 1)) return;           // K Q^T has read K
+            if (g > 1 && !x.wait(kDsFull + (g & 1), (g >> 1) - 1)) return;  // and the product before last its K~
+            unsigned char *const rest = x.sm.kt[g & 1][0];
+            // small loops: the roles share the instruction caches
+            float w = w3;
+#pragma unroll 1
+            for (int i = 3; i >= 0; --i) {
+                const int back = n - 1 - (i * 16 + row);
+                if (n < kC) w = back < 0 ? 0.0f : power(u.lg2, back);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = sub * kSub + (i * 128 + tid) * 16;
-                    const uint4 raw = *reinterpret_cast<const uint4 *>(stage + kTile + at);
+                for (int sub = 0; sub < KP / 64; ++sub) {
+                    const int at = sub * kSub + tid * 16 + i * 2048;
+                    uint4 *const here = reinterpret_cast<uint4 *>(stage + kTile + at);
+                    uint4 raw = *here;
+                    if (back < 0) raw = make_uint4(0, 0, 0, 0);
                     const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-                    const bool keep = i * 16 + tid / 8 < n;
-                    uint32_t o[3][4];
+                    float2 r[4];
+                    uint32_t o[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float a = keep ? __uint_as_float(in[e] << 16) * w[i] : 0.0f;
-                        float b = keep ? __uint_as_float(in[e] & 0xffff0000u) * w[i] : 0.0f;
-                        o[0][e] = pack_bf16(a, b);
-                        a -= __uint_as_float(o[0][e] << 16);
-                        b -= __uint_as_float(o[0][e] & 0xffff0000u);
-                        o[1][e] = pack_bf16(a, b);
-                        if (x.c.parts == 3) {
-                            a -= __uint_as_float(o[1][e] << 16);
-                            b -= __uint_as_float(o[1][e] & 0xffff0000u);
-                            o[2][e] = pack_bf16(a, b);
-                        }
+                        r[e] = __fmul2_rn(unpack_bf16(in[e]), make_float2(w, w));
+                        o[e] = pack_bf16(r[e]);
+                        r[e] = rest_bf16(r[e], o[e]);
                     }
+                    *here = make_uint4(o[0], o[1], o[2], o[3]);
 #pragma unroll
-                    for (int part = 0; part < 3; ++part)
-                        if (part < x.c.parts)
-                            *reinterpret_cast<uint4 *>(x.sm.kt[part] + at) =
-                                make_uint4(o[part][0], o[part][1], o[part][2], o[part][3]);
+                    for (int e = 0; e < 4; ++e) {
+                        o[e] = pack_bf16(r[e]);
+                        r[e] = rest_bf16(r[e], o[e]);
+                    }
+                    *reinterpret_cast<uint4 *>(rest + at) = make_uint4(o[0], o[1], o[2], o[3]);
+                    if (parts == 3) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[e] = pack_bf16(r[e]);
+                        *reinterpret_cast<uint4 *>(rest + kTile + at) = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
                 }
-            }
-            if (n < kC) {
-                for (int i = n * 8 + tid; i < kC * 8; i += 32 * kWarpsK)
-                    for (int sub = 0; sub < nv; ++sub)
-                        *reinterpret_cast<uint4 *>(stage + 2 * kTile + sub * kSub + i * 16) = make_uint4(0, 0, 0, 0);
+                w *= lam16;
             }
             fence_async_smem();
-            x.arrive(kKtFull);
+            x.arrive(kKtFull + (g & 1));
         }
     }
 }
 
 // The state: lane = value index, 64 of its key indices in a thread's
 // registers (warps 0-3: 0..63, warps 4-7: 64..127).
-template <typename ST, bool STATES> __device__ void role_state(const Ctx &x, int warp, int lane) {
+template <typename ST, int KP, bool STATES> __device__ void role_state(const Ctx &x, int warp, int lane) {
     const LaParams &p = x.c.p;
     const int quad = warp & 3, half = warp >> 2, v = quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const bool mine = half * 64 < p.K;
+    const bool mine = half * 64 < KP;
     Walk<STATES> walk(x.c, x.sm);
     Unit u;
     unsigned g = 0;
-    float s[64];
+    float2 s[32];
     while (walk.next(u, false)) {
         if (u.chunks == 0) continue;
         const bool on = mine && u.tile * 128 + v < p.V;
         const int k0 = half * 64, kn = min(64, p.K - k0);
         ST *pool = static_cast<ST *>(p.state) + (long long)u.slot * p.st_slot + (long long)u.h * p.st_head + u.tile * 128 + v;
         float *ws = x.c.ws + ((long long)u.x * p.nv + u.h) * p.K * p.V + u.tile * 128 + v;
-        if (STATES) {
+        // in groups of 16 key indices (K is a multiple of 16), each asked for at once
 #pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = 0.0f;
-        } else if (x.c.seg) {
+        for (int i = 0; i < 32; ++i) s[i] = make_float2(0.0f, 0.0f);
+        if (!STATES && on) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = on && i < kn ? ws[(long long)(k0 + i) * p.V] : 0.0f;
-        } else {
+            for (int b = 0; b < 4; ++b) {
+                if (16 * b >= kn) break;
+                if (x.c.seg) {
+                    const float *from = ws + (long long)(k0 + 16 * b) * p.V;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = on && i < kn ? to_f32(pool[(long long)(k0 + i) * p.st_k]) : 0.0f;
+                    for (int i = 0; i < 8; ++i) s[8 * b + i] = make_float2(from[2 * i * p.V], from[(2 * i + 1) * p.V]);
+                } else {
+                    const ST *from = pool + (long long)(k0 + 16 * b) * p.st_k;
+                    ST raw[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) raw[i] = from[i * p.st_k];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) s[8 * b + i] = make_float2(to_f32(raw[2 * i]), to_f32(raw[2 * i + 1]));
+                }
+            }
         }
         const float lam_c = power(u.lg2, kC);
         for (int j = 0; j < u.chunks; ++j, ++g) {
             const int n = min(kC, u.len - j * kC);
             if (!STATES) {
-                // the start state as matrix operand: s = hi + lo to 16 bits
-                if (g > 0 && !x.wait(kSFree, g - 1)) return;
+                // the start state as matrix operand, in one of two buffers
+                if (g > 1 && !x.wait(kOFull + (g & 1), (g >> 1) - 1)) return;  // the product that read it last is done
                 if (mine) {
                     fence_after();
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        uint32_t hi[16], lo[16];
+                        uint32_t h[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float a = s[32 * i + 2 * e], b = s[32 * i + 2 * e + 1];
-                            hi[e] = pack_bf16(a, b);
-                            lo[e] = pack_bf16(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xffff0000u));
-                        }
-                        tmem_st16(x.tmem + lanes + kColHi + half * 32 + i * 16, hi);
-                        tmem_st16(x.tmem + lanes + kColLo + half * 32 + i * 16, lo);
+                        for (int e = 0; e < 16; ++e) h[e] = pack_bf16(s[16 * i + e]);
+                        tmem_st16(x.tmem + lanes + kColS + (g & 1) * 64 + half * 32 + i * 16, h);
                     }
                     wait_st();
                     fence_before();
                 }
-                x.arrive(kSFull);
+                x.arrive(kSFull + (g & 1));
             }
             const float lam_n = n == kC ? lam_c : power(u.lg2, n);
-            if (!x.wait(kDsFull, g)) return;
+            if (!x.wait(kDsFull + (g & 1), g >> 1)) return;
             if (mine) {
                 fence_after();
+                const float2 l2 = make_float2(lam_n, lam_n);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t d[16];
                     tmem_ld16(x.tmem + lanes + kColDS + half * 64 + i * 16, d);
                     wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) s[16 * i + e] = fmaf(lam_n, s[16 * i + e], __uint_as_float(d[e]));
+                    for (int e = 0; e < 8; ++e)
+                        s[8 * i + e] = __ffma2_rn(l2, s[8 * i + e],
+                                                  make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
                 }
                 fence_before();
             }
             x.arrive(kDsFree);
         }
-        if (STATES) {
+        if (on && (STATES || u.last)) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (on && i < kn) ws[(long long)(k0 + i) * p.V] = s[i];
-        } else if (u.last) {
+            for (int b = 0; b < 4; ++b) {
+                if (16 * b >= kn) break;
+                if (STATES) {
+                    float *to = ws + (long long)(k0 + 16 * b) * p.V;
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (on && i < kn) pool[(long long)(k0 + i) * p.st_k] = from_f32<ST>(s[i]);
+                    for (int i = 0; i < 16; ++i) to[i * p.V] = (i & 1) ? s[8 * b + i / 2].y : s[8 * b + i / 2].x;
+                } else {
+                    ST *to = pool + (long long)(k0 + 16 * b) * p.st_k;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        to[i * p.st_k] = from_f32<ST>((i & 1) ? s[8 * b + i / 2].y : s[8 * b + i / 2].x);
+                }
+            }
         }
     }
 }
 
-// P~ and the output.  A warp has 16 keys of P^T and 32 columns of O^T.
-__device__ void role_out(const Ctx &x, int warp, int lane) {
+// P~: a warp has 16 keys of P^T.  Its blocks of 8 queries are wholly masked
+// before its own 16, mixed there, and wholly kept after.
+__device__ void role_scores(const Ctx &x, int warp, int lane) {
     const LaParams &p = x.c.p;
-    uint16_t *const out = static_cast<uint16_t *>(p.out);
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     const int row0 = warp * 16 + lane / 4;  // this thread's keys: row0 and row0 + 8
-    const uint32_t pt = x.base + offsetof(Smem, pt);
-    unsigned char *const ost = x.sm.ost[warp];
-    // stmatrix: lane l names row l % 8 of matrix l / 8: keys +0, +8, +0, +8 of column blocks n, n, n + 1, n + 1
+    const uint32_t pt = x.base + (uint32_t)offsetof(Smem, pt);
+    // stmatrix: lane l names row l % 8 of matrix l / 8: keys +0, +8, +0, +8 of query blocks n, n, n + 1, n + 1
     const int srow = warp * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, sblk = lane >> 4;
+    const uint32_t to = pt + srow * 128;
     Walk<false> walk(x.c, x.sm);
     Unit u;
     unsigned g = 0;
-    int parity = 0;
-    uint16_t *prev = nullptr;  // where the chunk before this one goes, its tokens and its factors
-    int prev_n = 0, prev_w = 0;
-    const float *prev_f = nullptr;
-    // O^T of chunk g - 1 -> staging; tensor memory is free again when every lane has read
-    auto collect = [&]() {
-        if (!x.wait(kOFull, g - 1)) return false;
-        fence_after();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t a[16], b[16];
-            tmem_ld16(x.tmem + lanes + kColO1 + i * 16, a);
-            tmem_ld16(x.tmem + lanes + kColO2 + i * 16, b);
-            wait_ld();
-            if (i == 3) {
-                fence_before();
-                x.arrive(kOFree);
-            }
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                const float4 f = *reinterpret_cast<const float4 *>(prev_f + i * 16 + e);
-                const float o0 = fmaf(f.x, __uint_as_float(a[e]), __uint_as_float(b[e]));
-                const float o1 = fmaf(f.y, __uint_as_float(a[e + 1]), __uint_as_float(b[e + 1]));
-                const float o2 = fmaf(f.z, __uint_as_float(a[e + 2]), __uint_as_float(b[e + 2]));
-                const float o3 = fmaf(f.w, __uint_as_float(a[e + 3]), __uint_as_float(b[e + 3]));
-                const uint32_t lo = pack_bf16(o0, o1), hi = pack_bf16(o2, o3);
-                uint16_t *to = reinterpret_cast<uint16_t *>(ost) + (i * 16 + e) * 32 + lane;
-                to[0] = (uint16_t)lo;
-                to[32] = (uint16_t)(lo >> 16);
-                to[64] = (uint16_t)hi;
-                to[96] = (uint16_t)(hi >> 16);
-            }
-        }
-        return true;
-    };
-    auto write = [&]() {
-        __syncwarp();
-        const int c0 = (lane & 3) * 8;
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const int t = r * 8 + lane / 4;
-            if (t < prev_n && c0 < prev_w)
-                *reinterpret_cast<uint4 *>(prev + (long long)t * p.o_ts + c0) =
-                    *reinterpret_cast<const uint4 *>(ost + t * 64 + c0 * 2);
-        }
-        __syncwarp();
-    };
-    while (walk.next(u, warp == 0 && lane == 0)) {
-        const int col = u.tile * 128 + warp * 32;
-        if (u.skip_len) {
-            const int w = min(32, p.V - col);
-            if (lane < w)
-                for (int t = 0; t < u.skip_len; ++t)
-                    out[(long long)(u.skip_t0 + t) * p.o_ts + (long long)u.h * p.o_hs + col + lane] = 0;
-        }
+    while (walk.next(u, false)) {
         if (u.chunks == 0) continue;
-        parity ^= 1;
-        float *factor = x.sm.factor[warp][parity];
-        factor[lane] = p.scale * power(u.lg2, lane + 1);
-        factor[lane + 32] = p.scale * power(u.lg2, lane + 33);
-        float w[32];
+        float2 w[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const int gap = 8 * (i >> 2) + 2 * (lane & 3) + (i & 1) - (row0 + ((i >> 1) & 1) * 8);
-            w[i] = gap < 0 ? 0.0f : p.scale * power(u.lg2, gap);
+        for (int i = 0; i < 16; ++i) {
+            const int gap = 8 * (i >> 1) + 2 * (lane & 3) - (row0 + (i & 1) * 8);
+            w[i].x = gap < 0 ? 0.0f : p.scale * power(u.lg2, gap);
+            w[i].y = gap < -1 ? 0.0f : p.scale * power(u.lg2, gap + 1);
         }
-        __syncwarp();
         for (int j = 0; j < u.chunks; ++j, ++g) {
             const int n = min(kC, u.len - j * kC);
-            if (g > 0 && !collect()) return;
             if (!x.wait(kPFull + (g & 1), g >> 1)) return;
             fence_after();
             uint32_t r[32];
@@ -549,53 +564,149 @@ __device__ void role_out(const Ctx &x, int warp, int lane) {
             wait_ld();
             fence_before();
             x.arrive(kPFree + (g & 1));
-            // masked places are chosen, not multiplied: whatever they hold stays out
-            const bool on0 = row0 < n, on1 = row0 + 8 < n;
             uint32_t h[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const bool on = (i & 1) ? on1 : on0;
-                const float a = on && w[2 * i] != 0.0f ? __uint_as_float(r[2 * i]) * w[2 * i] : 0.0f;
-                const float b = on && w[2 * i + 1] != 0.0f ? __uint_as_float(r[2 * i + 1]) * w[2 * i + 1] : 0.0f;
-                h[i] = pack_bf16(a, b);
+            for (int b = 0; b < 8; ++b) {
+                if (b < 2 * warp) {
+                    h[2 * b] = h[2 * b + 1] = 0;
+                    continue;
+                }
+                float2 e[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    e[i] = __fmul2_rn(make_float2(__uint_as_float(r[4 * b + 2 * i]), __uint_as_float(r[4 * b + 2 * i + 1])),
+                                      w[2 * b + i]);
+                if (b < 2 * warp + 2) {  // chosen, not multiplied: whatever a masked place holds stays out
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int gap = 8 * b + 2 * (lane & 3) - (row0 + i * 8);
+                        if (gap < 0) e[i].x = 0.0f;
+                        if (gap < -1) e[i].y = 0.0f;
+                    }
+                }
+                h[2 * b] = pack_bf16(e[0]);
+                h[2 * b + 1] = pack_bf16(e[1]);
             }
+            if (__builtin_expect(n < kC, 0)) {
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    if (row0 >= n) h[2 * b] = 0;
+                    if (row0 + 8 >= n) h[2 * b + 1] = 0;
+                }
+                clear_tail(x.sm.stage[g % kStages] + 2 * kTile, n, p.V - u.tile * 128 > 64 ? 2 : 1, warp * 32 + lane,
+                           32 * kWarpsP);
+            }
+            if (g > 0 && !x.wait(kOFull + ((g - 1) & 1), (g - 1) >> 1)) return;  // the product that read the last P~ is done
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                stmatrix4(pt + srow * 128 + (((2 * i + sblk) ^ (srow & 7)) << 4), h[4 * i], h[4 * i + 1], h[4 * i + 2],
-                          h[4 * i + 3]);
+                stmatrix4(to + (((2 * i + sblk) ^ (srow & 7)) << 4), h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
             fence_async_smem();
             x.arrive(kPtFull);
-            if (g > 0) write();
-            prev = out + (long long)(u.t0 + j * kC) * p.o_ts + (long long)u.h * p.o_hs + col;
-            prev_n = n;
-            prev_w = p.V - col;
-            prev_f = factor;
         }
     }
-    if (g > 0 && collect()) write();
 }
 
-template <typename ST, bool STATES>
+// The output: a warp has 32 columns of O^T, which it turns through shared
+// memory into rows of 64 bytes a token.
+__device__ void role_out(const Ctx &x, int warp, int lane) {
+    const LaParams &p = x.c.p;
+    uint16_t *const out = static_cast<uint16_t *>(p.out);
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    unsigned char *const ost = x.sm.ost[warp];
+    const uint32_t ost_a = x.base + (uint32_t)offsetof(Smem, ost) + warp * (32 * 64);
+    // staging: 16-byte block c of token t lies at block c ^ (t / 2 % 4) of its 64 bytes
+    const int st_tok = (lane >> 4) * 8 + (lane & 7), st_blk = (lane >> 3) & 1;
+    Walk<false> walk(x.c, x.sm);
+    Unit u;
+    unsigned g = 0;
+    while (walk.next(u, warp == 0 && lane == 0)) {
+        const int col = u.tile * 128 + warp * 32;
+        if (u.skip_len && col + lane < p.V)
+            for (int t = 0; t < u.skip_len; ++t)
+                out[(long long)(u.skip_t0 + t) * p.o_ts + (long long)u.h * p.o_hs + col + lane] = 0;
+        if (u.chunks == 0) continue;
+        float2 f[8];
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+            const int i = 8 * b + 2 * (lane & 3);
+            f[b] = make_float2(p.scale * power(u.lg2, i + 1), p.scale * power(u.lg2, i + 2));
+        }
+        const bool on = col + (lane & 3) * 8 < p.V;
+        uint16_t *to = out + (long long)(u.t0 + lane / 4) * p.o_ts + (long long)u.h * p.o_hs + col + (lane & 3) * 8;
+        for (int j = 0; j < u.chunks; ++j, ++g) {
+            const int n = min(kC, u.len - j * kC);
+            if (!x.wait(kOFull + (g & 1), g >> 1)) return;
+            fence_after();
+            uint32_t h[2][16];
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {  // 32 of the tokens
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {  // 16 of the columns
+                    uint32_t a[16], b[16];
+                    tmem_ld_16x32(x.tmem + lanes + ((uint32_t)(hh * 16) << 16) + kColO1 + ch * 32, a);
+                    tmem_ld_16x32(x.tmem + lanes + ((uint32_t)(hh * 16) << 16) + kColO2 + ch * 32, b);
+                    wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        h[ch][hh * 8 + i] =
+                            pack_bf16(__ffma2_rn(f[ch * 4 + i / 2],
+                                                 make_float2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1])),
+                                                 make_float2(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]))));
+                }
+            }
+            fence_before();
+            x.arrive(kOFree);
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+                __syncwarp();
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int t = i * 16 + st_tok;
+                        const uint32_t *w = h[ch] + hh * 8 + i * 4;
+                        stmatrix4_t(ost_a + t * 64 + (((hh * 2 + st_blk) ^ ((t >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
+                    }
+                __syncwarp();
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = r * 8 + lane / 4;
+                    if (on && ch * 32 + t < n)
+                        *reinterpret_cast<uint4 *>(to + (long long)(ch * 32 + r * 8) * p.o_ts) =
+                            *reinterpret_cast<const uint4 *>(ost + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
+                }
+            }
+            to += (long long)kC * p.o_ts;
+        }
+    }
+}
+
+template <typename ST, int KP, bool STATES>
 __global__ void __launch_bounds__(kThreads, 1)
     k_la_chunk(const __grid_constant__ ChunkParams c, const __grid_constant__ CUtensorMap mq,
                const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw), pad = (1024u - (raw & 1023u)) & 1023u;
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw + pad);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t base = raw + pad, bars = base + (uint32_t)offsetof(Smem, bar);
     if (threadIdx.x == 0) {
         sm.gave_up = 0;
         for (int i = 0; i < kBars; ++i) {
-            const bool by_p = i == kPFree || i == kPFree + 1 || i == kPtFull || i == kOFree;
-            const bool by_s = i == kSFull || i == kDsFree;
-            mbar_init(bars + 8 * i, by_p ? kWarpsP : by_s ? kWarpsS : i == kKtFull ? kWarpsK : 1);
+            int n = 1;
+            if (i >= kStageFree && i < kStageFree + kStages) n = STATES ? 1 : 2;  // the products that read a stage last
+            if (i == kPFree || i == kPFree + 1 || i == kPtFull) n = kWarpsP;
+            if (i == kDrain) n = STATES ? 1 : 3;
+            if (i == kSFull || i == kSFull + 1 || i == kDsFree) n = kWarpsS;
+            if (i == kKtFull || i == kKtFull + 1) n = kWarpsK;
+            if (i == kOFree) n = kWarpsO;
+            mbar_init(bars + 8 * i, n);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async_smem();
     }
     if (warp == kWarpMma) tmem_alloc(base + (uint32_t)offsetof(Smem, tmem), 512);
-    if (warp == kWarpTma && lane == 0) {
+    if (warp == kWarpMma + 3 && lane == 0) {
         tma_prefetch_map(&mk);
         tma_prefetch_map(&mv);
         if (!STATES) tma_prefetch_map(&mq);
@@ -604,17 +715,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_before();
     __syncthreads();
     fence_after();
-    const Ctx x{c, sm, base, bars, sm.tmem};
-    if (warp < kWarpsS) {
-        role_state<ST, STATES>(x, warp, lane);
-    } else if (warp < kWarpsS + kWarpsP) {
-        if (!STATES) role_out(x, warp - kWarpsS, lane);
+    const Ctx x{c, sm, base, bars, uniform(sm.tmem)};
+    if (warp < kWarpO) {
+        regs_up<kRegsS>();
+        role_state<ST, KP, STATES>(x, warp, lane);
+    } else if (warp < kWarpP) {
+        if (!STATES) role_out(x, warp - kWarpO, lane);
+    } else if (warp < kWarpK) {
+        regs_up<kRegsP>();
+        if (!STATES) role_scores(x, warp - kWarpP, lane);
     } else if (warp < kWarpMma) {
-        role_keys<STATES>(x, (int)threadIdx.x - 32 * (kWarpsS + kWarpsP));
-    } else if (warp == kWarpMma) {
-        if (lane == 0) role_mma<STATES>(x);
+        regs_down<kRegsK>();
+        role_keys<KP, STATES>(x, warp - kWarpK, lane);
     } else {
-        if (lane == 0) role_tma<STATES>(x, &mq, &mk, &mv);
+        regs_down<kRegsRest>();
+        if (warp == kWarpMma) {
+            role_mma_state<KP, STATES>(x);
+        } else if (warp == kWarpMma + 1) {
+            if (!STATES) role_mma_out<KP>(x);
+        } else if (warp == kWarpMma + 2) {
+            if (!STATES) role_mma_scores<KP>(x);
+        } else {
+            Loader<KP, STATES> load(x, &mq, &mk, &mv);
+            while (load.more && load.step()) {
+            }
+            load.drain();
+        }
     }
     __syncwarp();
     fence_before();
@@ -704,14 +830,14 @@ bool encode(EncodeFn fn, CUtensorMap *map, const void *base, int dim, int heads,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename ST> cudaError_t go(ChunkParams c, const CUtensorMap *m, cudaStream_t s) {
+template <typename ST, int KP> cudaError_t go(ChunkParams c, const CUtensorMap *m, cudaStream_t s) {
     static LaunchCache cache;
     LaunchInfo li;
     constexpr int smem = (int)sizeof(Smem) + 1024;
     cudaError_t e = launch_info(cache, &li, [](LaunchInfo &) {
-        cudaError_t r = cudaFuncSetAttribute(k_la_chunk<ST, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaError_t r = cudaFuncSetAttribute(k_la_chunk<ST, KP, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(k_la_chunk<ST, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            r = cudaFuncSetAttribute(k_la_chunk<ST, KP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         return r;
     });
     if (e != cudaSuccess) return e;
@@ -720,11 +846,11 @@ template <typename ST> cudaError_t go(ChunkParams c, const CUtensorMap *m, cudaS
     const long long rows = c.seg ? p.batch + p.T / c.seg : p.batch;
     const unsigned grid = (unsigned)(rows * per < li.sms ? rows * per : li.sms);
     if (c.seg) {
-        k_la_chunk<ST, true><<<grid, kThreads, smem, s>>>(c, m[0], m[1], m[2]);
+        k_la_chunk<ST, KP, true><<<grid, kThreads, smem, s>>>(c, m[0], m[1], m[2]);
         const dim3 jg((unsigned)((p.K * p.V + 1023) / 1024), (unsigned)p.nv, (unsigned)p.batch);
         k_la_join<ST><<<jg, 256, 0, s>>>(c);
     }
-    k_la_chunk<ST, false><<<grid, kThreads, smem, s>>>(c, m[0], m[1], m[2]);
+    k_la_chunk<ST, KP, false><<<grid, kThreads, smem, s>>>(c, m[0], m[1], m[2]);
     return cudaGetLastError();
 }
 
@@ -738,8 +864,10 @@ cudaError_t launch_la_chunk(const LaParams &p, bool state_bf16, int seg, void *w
         !encode(fn, &m[1], p.k, p.K, p.nk, p.T, p.k_hs, p.k_ts) || !encode(fn, &m[2], p.v, p.V, p.nv, p.T, p.v_hs, p.v_ts))
         return cudaSuccess;
     *used = true;
-    ChunkParams c{p, seg, state_bf16 ? 2 : 3, static_cast<float *>(ws)};
-    return state_bf16 ? go<uint16_t>(c, m, s) : go<float>(c, m, s);
+    const ChunkParams c{p, seg, state_bf16 ? 2 : 3, static_cast<float *>(ws), FastDiv((unsigned)(p.nv * p.tiles)),
+                        FastDiv((unsigned)p.tiles)};
+    if (p.K > 64) return state_bf16 ? go<uint16_t, 128>(c, m, s) : go<float, 128>(c, m, s);
+    return state_bf16 ? go<uint16_t, 64>(c, m, s) : go<float, 64>(c, m, s);
 }
 
 }  // namespace gdr

@@ -1,7 +1,8 @@
 // Tensor core (tcgen05), TMA and mbarrier instructions as inline PTX.
 //
-// Every wait is bounded: after kWaitLimit nanoseconds, or once another warp of
-// the CTA has given up, it returns false and the caller leaves its loop.
+// Every wait is bounded: after kWaitLimit clock cycles (about a second), or once
+// another warp of the CTA has given up, it returns false and the caller leaves
+// its loop.
 #pragma once
 
 #include <cuda.h>
@@ -11,13 +12,7 @@
 namespace gdr {
 namespace tc {
 
-constexpr unsigned long long kWaitLimit = 2000000000ull;
-
-__device__ __forceinline__ unsigned long long now_ns() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
-}
+constexpr unsigned kWaitLimit = 2000000000u;
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -30,27 +25,29 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// One attempt; the hardware may suspend the warp for up to about a millisecond.
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(bar), "r"(parity)
+        : "r"(bar), "r"(parity), "r"(1000000u)
         : "memory");
     return ok != 0;
 }
 // Waits for the phase of this parity; false if the limit ran out or *gave_up is set.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int *gave_up) {
-    if (mbar_try(bar, parity)) return true;
-    const unsigned long long start = now_ns();
-    do {
-        if (mbar_try(bar, parity)) return true;
+    const unsigned start = (unsigned)clock();
+    while (!mbar_try(bar, parity)) {
         if (*gave_up) return false;
-    } while (now_ns() - start < kWaitLimit);
-    *gave_up = 1;
-    return false;
+        if ((unsigned)clock() - start > kWaitLimit) {
+            *gave_up = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
 // Generic-proxy writes to shared memory become visible to TMA and the tensor cores.
@@ -108,6 +105,33 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t a, uint32_t (&r)[32]) {
         : "r"(a));
 }
 
+// The same for 32 columns.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t a, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a));
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok;
+}
+
+// Moves a warpgroup's registers a thread; every warp of it executes this, and
+// the shares of all warpgroups add up to no more than the launch gave out.
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// The value of lane 0, for all lanes: tells the compiler that a number is the
+// same in the whole warp, so that descriptors made from it stay in uniform
+// registers (a matrix instruction takes no others).
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // ---- matrix instructions --------------------------------------------------------
 // Shared-memory operand of 128-byte rows in 8-row swizzled atoms (1024 bytes,
 // 1024-byte aligned).  K-major: sbo = bytes between groups of 8 rows.
@@ -122,23 +146,56 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool 
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// `me`: elect_one() of a converged warp.  The instruction is predicated, not
+// branched around, so that the warp stays converged and the operands, which
+// have to lie in uniform registers, are computed there: behind a branch each
+// of them is moved over first, which measured 60 to 110 cycles a product of 32.
+template <bool ACC> __device__ __forceinline__ void mma_ss(uint32_t me, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-        "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "n"(ACC ? 1 : 0), "r"(me)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+template <bool ACC> __device__ __forceinline__ void mma_ts(uint32_t me, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-        "r"((uint32_t)accumulate)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "n"(ACC ? 1 : 0), "r"(me)
         : "memory");
+}
+// D = A B over STEPS steps of 16 along K, both operands K-major in blocks of 64
+// (`block` bytes apart).  Written out by the compiler: a counted loop costs
+// about as much a step as the product itself.
+template <int STEPS> __device__ __forceinline__ void mma_ss_k(uint32_t me, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                                             uint32_t block) {
+    mma_ss<false>(me, d, a, b, idesc);
+#pragma unroll
+    for (int i = 1; i < STEPS; ++i) {
+        const uint32_t at = ((uint32_t)(i >> 2) * block + (uint32_t)(i & 3) * 32) >> 4;
+        mma_ss<true>(me, d, a + at, b + at, idesc);
+    }
+}
+// The same with A in tensor memory, 8 columns a step.
+template <int STEPS>
+__device__ __forceinline__ void mma_ts_k(uint32_t me, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t block) {
+    mma_ts<false>(me, d, a, b, idesc);
+#pragma unroll
+    for (int i = 1; i < STEPS; ++i)
+        mma_ts<true>(me, d, a + i * 8, b + (((uint32_t)(i >> 2) * block + (uint32_t)(i & 3) * 32) >> 4), idesc);
+}
+// D = A B over 64 along K, both operands MN-major (2048 bytes a step of 16).
+template <bool ACC> __device__ __forceinline__ void mma_ss_mn64(uint32_t me, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    mma_ss<ACC>(me, d, a, b, idesc);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) mma_ss<true>(me, d, a + (i * 2048 >> 4), b + (i * 2048 >> 4), idesc);
 }
 // The barrier gets one arrival once every matrix instruction this thread has issued is done.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t me, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(me)
+        : "memory");
 }
 
 __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -146,12 +203,23 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b,
                  "r"(d)
                  : "memory");
 }
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+// The same with each 8x8 matrix transposed.
+__device__ __forceinline__ void stmatrix4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 h2 = __floats2bfloat162_rn(lo, hi);
+// A pair of bfloat16 in one register, lower half first, and back.
+__device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float2 x) {
+    const __nv_bfloat162 h2 = __floats2bfloat162_rn(x.x, x.y);
     return *reinterpret_cast<const uint32_t *>(&h2);
+}
+// x - (what its bfloat16 rounding w holds): exact
+__device__ __forceinline__ float2 rest_bf16(float2 x, uint32_t w) {
+    return __ffma2_rn(unpack_bf16(w), make_float2(-1.0f, -1.0f), x);
 }
 
 }  // namespace tc
