@@ -82,6 +82,21 @@ int check_linattn(const gdr_linattn_args *a, const char *fn) {
     return GDR_OK;
 }
 
+// Rows of at most this many tokens (by the caller's bound) take the recurrent form.
+constexpr long long kStepRowMax = 16;
+
+bool takes_chunks(const gdr_linattn_args *a, bool tok_vec) {
+    return a->token_dtype == GDR_BF16 && tok_vec && a->total_tokens > 0 &&
+           (a->max_row_len <= 0 || a->max_row_len > kStepRowMax);
+}
+
+bool token_vectors(const gdr_linattn_args *a) {
+    return vector_rows(a->q, a->token_dtype, a->q_seq_stride, a->q_head_stride) &&
+           vector_rows(a->k, a->token_dtype, a->k_seq_stride, a->k_head_stride) &&
+           vector_rows(a->v, a->token_dtype, a->v_seq_stride, a->v_head_stride) &&
+           vector_rows(a->out, a->token_dtype, a->out_seq_stride, a->out_head_stride);
+}
+
 gdr::LaParams lower(const gdr_linattn_args *a, unsigned *status) {
     gdr::LaParams p{};
     p.batch = a->batch;
@@ -116,16 +131,43 @@ gdr::LaParams lower(const gdr_linattn_args *a, unsigned *status) {
     p.max_slots = a->max_slots;
     p.slot_idx = a->slot_idx;
     p.offsets = a->offsets;
-    p.tok_vec = vector_rows(a->q, a->token_dtype, a->q_seq_stride, a->q_head_stride) &&
-                vector_rows(a->k, a->token_dtype, a->k_seq_stride, a->k_head_stride) &&
-                vector_rows(a->v, a->token_dtype, a->v_seq_stride, a->v_head_stride) &&
-                vector_rows(a->out, a->token_dtype, a->out_seq_stride, a->out_head_stride);
+    p.tok_vec = token_vectors(a);
     p.status = status;
     return p;
 }
 
-// Rows of at most this many tokens (by the caller's bound) take the recurrent form.
-constexpr long long kStepRowMax = 16;
+// Tokens a segment for rows that are cut, or 0.  One CTA does a (row, head,
+// column tile) from end to end, so a call lasts about as many chunks as its
+// longest row has, or as the fullest SM gets.  Cut rows spread evenly, and
+// cost a pass over k and v for the segments' own states and the states'
+// traffic: about 0.6 of a chunk's time a chunk more and two chunks' a unit.
+int plan_segments(const gdr_linattn_args *a) {
+    constexpr double kSms = 152.0, kChunk = 64.0, kStatePass = 0.6, kUnit = 2.0;
+    if (a->batch < 1 || a->batch > 32) return 0;
+    const double tiles = (a->V + 127) / 128, heads = a->nv * tiles, T = (double)a->total_tokens;
+    const double mean = std::ceil(T / a->batch / kChunk);
+    double longest = a->max_row_len > 0 ? std::ceil((double)a->max_row_len / kChunk) : mean;
+    if (longest > std::ceil(T / kChunk)) longest = std::ceil(T / kChunk);
+    const double waves = std::ceil(a->batch * heads / kSms);
+    double best = std::fmax(longest + kUnit, waves * (mean + kUnit));
+    int seg = 0;
+    for (int n = 2; n <= 64; ++n) {
+        const double chunks = std::ceil(longest / n);
+        if (chunks < 4) break;
+        // a row's last segment is half full on average
+        const double units = std::ceil(T / (chunks * kChunk) + 0.5 * (a->batch - 1)) * heads;
+        const double cost = std::ceil(units / kSms) * (chunks * (1 + kStatePass) + 2 * kUnit) + 4;
+        if (cost < 0.9 * best) {
+            best = cost / 0.9;
+            seg = (int)(chunks * kChunk);
+        }
+    }
+    return seg;
+}
+
+int64_t segments_bytes(const gdr_linattn_args *a, int seg) {
+    return (a->total_tokens / seg + a->batch) * (int64_t)a->nv * a->K * a->V * 4;
+}
 
 int launched(cudaError_t e, const char *fn) {
     if (e != cudaSuccess) return fail(GDR_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
@@ -138,7 +180,9 @@ extern "C" {
 
 int64_t gdr_linattn_workspace_bytes(const gdr_linattn_args *a) {
     const int rc = check_linattn_sizes(a, "gdr_linattn_workspace_bytes");
-    return rc ? rc : 0;
+    if (rc) return rc;
+    const int seg = takes_chunks(a, token_vectors(a)) ? plan_segments(a) : 0;
+    return seg ? segments_bytes(a, seg) : 0;
 }
 
 int gdr_linattn_fwd(const gdr_linattn_args *a, void *stream) {
@@ -149,9 +193,11 @@ int gdr_linattn_fwd(const gdr_linattn_args *a, void *stream) {
     unsigned *st = nullptr;
     if ((rc = gdr::api_status(&st))) return rc;
     const gdr::LaParams p = lower(a, st);
-    if (a->token_dtype == GDR_BF16 && p.tok_vec && p.T > 0 && (p.max_len <= 0 || p.max_len > kStepRowMax)) {
+    if (takes_chunks(a, p.tok_vec)) {
+        int seg = plan_segments(a);
+        if (seg && (!a->workspace || a->workspace_bytes < segments_bytes(a, seg))) seg = 0;
         bool used = false;
-        const cudaError_t e = gdr::launch_la_chunk(p, a->state_dtype == GDR_BF16, 0, nullptr,
+        const cudaError_t e = gdr::launch_la_chunk(p, a->state_dtype == GDR_BF16, seg, a->workspace,
                                                    static_cast<cudaStream_t>(stream), &used);
         if (used || e != cudaSuccess) return launched(e, fn);
     }

@@ -48,12 +48,13 @@ constexpr int kTile = 2 * kSub;       // bytes of a 64-token x 128-channel opera
 constexpr int kStage = 3 * kTile;     // Q | K | V
 constexpr int kMaxRows = 128;         // rows whose order and segments are worked out in shared memory
 
-// Warps by role, in warpgroups of 4.
+// Warps by role, in warpgroups of 4.  The issuers and the loader come first:
+// between ready warps the scheduler prefers the older.
 constexpr int kWarpsS = 8, kWarpsO = 4, kWarpsP = 4, kWarpsK = 4;
-constexpr int kWarpO = kWarpsS, kWarpP = kWarpO + kWarpsO, kWarpK = kWarpP + kWarpsP, kWarpMma = kWarpK + kWarpsK;
-constexpr int kThreads = 32 * (kWarpMma + 4);  // the last warpgroup: three issuers and the loader
+constexpr int kWarpMma = 0, kWarpS = 4, kWarpO = kWarpS + kWarpsS, kWarpP = kWarpO + kWarpsO, kWarpK = kWarpP + kWarpsP;
+constexpr int kThreads = 32 * (kWarpK + kWarpsK);
 // Registers a thread: 768 threads are launched with 80, and the roles share them out anew.
-constexpr int kRegsS = 96, kRegsO = 80, kRegsP = 96, kRegsK = 72, kRegsRest = 40;
+constexpr int kRegsS = 104, kRegsO = 96, kRegsP = 96, kRegsK = 48, kRegsRest = 32;
 static_assert(2 * kRegsS + kRegsO + kRegsP + kRegsK + kRegsRest == 6 * 80, "shares");
 
 // tensor memory columns
@@ -79,7 +80,6 @@ static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory");
 struct ChunkParams {
     LaParams p;
     int seg;    // tokens a segment (a multiple of kC), or 0: rows are whole
-    int parts;  // bfloat16 parts of K~
     float *ws;  // start states of the segments [segment, nv, K, V] (seg != 0)
     FastDiv per, tiles;  // units a segment (nv * tiles), column tiles
 };
@@ -322,7 +322,7 @@ template <int KP> __device__ void role_mma_scores(const Ctx &x) {
 }
 
 // V^T K~
-template <int KP, bool STATES> __device__ void role_mma_state(const Ctx &x) {
+template <int KP, int PARTS, bool STATES> __device__ void role_mma_state(const Ctx &x) {
     const uint32_t id = idesc_bf16(128, KP, true, true);
     const uint64_t d_mn = desc128(x.base, kSub, 1024);  // stage 0, MN-major
     const uint64_t d_kt = desc128(x.base + (uint32_t)offsetof(Smem, kt), kSub, 1024);
@@ -336,7 +336,7 @@ template <int KP, bool STATES> __device__ void role_mma_state(const Ctx &x) {
         const uint64_t k = d_mn + ((st * kStage + kTile) >> 4), v = k + (kTile >> 4), kt = d_kt + (odd * 2 * kTile >> 4);
         mma_ss_mn64<false>(me, x.tmem + kColDS, v, k, id);
         mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt, id);
-        if (x.c.parts == 3) mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt + (kTile >> 4), id);
+        if (PARTS == 3) mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt + (kTile >> 4), id);
         mma_commit(me, x.bar(kDsFull) + 8 * odd);
         mma_commit(me, x.bar(kStageFree) + 8 * st);
     }
@@ -374,11 +374,15 @@ __device__ __forceinline__ void clear_tail(unsigned char *v, int n, int nv, int 
         for (int sub = 0; sub < nv; ++sub) *reinterpret_cast<uint4 *>(v + sub * kSub + i * 16) = make_uint4(0, 0, 0, 0);
 }
 
-// K~[j] = lambda^(n-1-j) k_j in bfloat16 parts, at the places K has in its
-// swizzled block: a thread has 16-byte vectors of 4 tokens.
-template <int KP, bool STATES> __device__ void role_keys(const Ctx &x, int warp, int lane) {
+// K~[j] = w_j k_j, w_j = lambda^(n-1-j), in PARTS bfloat16 parts, at the places K
+// has in its swizzled block: a thread has 16-byte vectors of 4 tokens.
+// Two parts in bfloat16 arithmetic: with w = a + b (a, b bfloat16, b the rest),
+//     hi = rn(k a),  k a - hi exactly (it has 8 bits),  mid = rn(k b + (k a - hi)),
+// three instructions a pair, off by 2^-17 of the product.  Three parts in
+// float32, each the rounding of what the ones before leave.
+template <int KP, int PARTS, bool STATES> __device__ void role_keys(const Ctx &x, int warp, int lane) {
     const LaParams &p = x.c.p;
-    const int tid = warp * 32 + lane, row = tid / 8, parts = x.c.parts;
+    const int tid = warp * 32 + lane, row = tid / 8;
     Walk<STATES> walk(x.c, x.sm);
     Unit u;
     unsigned g = 0;
@@ -401,6 +405,8 @@ template <int KP, bool STATES> __device__ void role_keys(const Ctx &x, int warp,
             for (int i = 3; i >= 0; --i) {
                 const int back = n - 1 - (i * 16 + row);
                 if (n < kC) w = back < 0 ? 0.0f : power(u.lg2, back);
+                const __nv_bfloat162 wa = __float2bfloat162_rn(w);
+                const __nv_bfloat162 wb = __float2bfloat162_rn(w - __low2float(wa));
 #pragma unroll
                 for (int sub = 0; sub < KP / 64; ++sub) {
                     const int at = sub * kSub + tid * 16 + i * 2048;
@@ -408,26 +414,30 @@ template <int KP, bool STATES> __device__ void role_keys(const Ctx &x, int warp,
                     uint4 raw = *here;
                     if (back < 0) raw = make_uint4(0, 0, 0, 0);
                     const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-                    float2 r[4];
-                    uint32_t o[4];
+                    uint32_t o[3][4];
+                    if constexpr (PARTS == 2) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        r[e] = __fmul2_rn(unpack_bf16(in[e]), make_float2(w, w));
-                        o[e] = pack_bf16(r[e]);
-                        r[e] = rest_bf16(r[e], o[e]);
-                    }
-                    *here = make_uint4(o[0], o[1], o[2], o[3]);
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 k = *reinterpret_cast<const __nv_bfloat162 *>(&in[e]);
+                            const __nv_bfloat162 hi = __hmul2_rn(k, wa), mid = __hfma2(k, wb, __hfma2(k, wa, __hneg2(hi)));
+                            o[0][e] = *reinterpret_cast<const uint32_t *>(&hi);
+                            o[1][e] = *reinterpret_cast<const uint32_t *>(&mid);
+                        }
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        o[e] = pack_bf16(r[e]);
-                        r[e] = rest_bf16(r[e], o[e]);
+                        for (int e = 0; e < 4; ++e) {
+                            float2 r = __fmul2_rn(unpack_bf16(in[e]), make_float2(w, w));
+                            o[0][e] = pack_bf16(r);
+                            r = rest_bf16(r, o[0][e]);
+                            o[1][e] = pack_bf16(r);
+                            o[2][e] = pack_bf16(rest_bf16(r, o[1][e]));
+                        }
                     }
-                    *reinterpret_cast<uint4 *>(rest + at) = make_uint4(o[0], o[1], o[2], o[3]);
-                    if (parts == 3) {
+                    *here = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[e] = pack_bf16(r[e]);
-                        *reinterpret_cast<uint4 *>(rest + kTile + at) = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
+                    for (int part = 1; part < PARTS; ++part)
+                        *reinterpret_cast<uint4 *>(rest + (part - 1) * kTile + at) =
+                            make_uint4(o[part][0], o[part][1], o[part][2], o[part][3]);
                 }
                 w *= lam16;
             }
@@ -685,6 +695,7 @@ template <typename ST, int KP, bool STATES>
 __global__ void __launch_bounds__(kThreads, 1)
     k_la_chunk(const __grid_constant__ ChunkParams c, const __grid_constant__ CUtensorMap mq,
                const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    constexpr int PARTS = sizeof(ST) == 2 ? 2 : 3;  // bfloat16 parts of K~
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw), pad = (1024u - (raw & 1023u)) & 1023u;
     Smem &sm = *reinterpret_cast<Smem *>(smem_raw + pad);
@@ -716,21 +727,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     fence_after();
     const Ctx x{c, sm, base, bars, uniform(sm.tmem)};
-    if (warp < kWarpO) {
-        regs_up<kRegsS>();
-        role_state<ST, KP, STATES>(x, warp, lane);
-    } else if (warp < kWarpP) {
-        if (!STATES) role_out(x, warp - kWarpO, lane);
-    } else if (warp < kWarpK) {
-        regs_up<kRegsP>();
-        if (!STATES) role_scores(x, warp - kWarpP, lane);
-    } else if (warp < kWarpMma) {
-        regs_down<kRegsK>();
-        role_keys<KP, STATES>(x, warp - kWarpK, lane);
-    } else {
+    if (warp < kWarpS) {
         regs_down<kRegsRest>();
         if (warp == kWarpMma) {
-            role_mma_state<KP, STATES>(x);
+            role_mma_state<KP, PARTS, STATES>(x);
         } else if (warp == kWarpMma + 1) {
             if (!STATES) role_mma_out<KP>(x);
         } else if (warp == kWarpMma + 2) {
@@ -741,6 +741,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             load.drain();
         }
+    } else if (warp < kWarpO) {
+        regs_up<kRegsS>();
+        role_state<ST, KP, STATES>(x, warp - kWarpS, lane);
+    } else if (warp < kWarpP) {
+        if (kRegsO > 80) regs_up<kRegsO>();
+        if (!STATES) role_out(x, warp - kWarpO, lane);
+    } else if (warp < kWarpK) {
+        if (kRegsP > 80) regs_up<kRegsP>();
+        if (!STATES) role_scores(x, warp - kWarpP, lane);
+    } else {
+        regs_down<kRegsK>();
+        role_keys<KP, PARTS, STATES>(x, warp - kWarpK, lane);
     }
     __syncwarp();
     fence_before();
@@ -864,7 +876,7 @@ cudaError_t launch_la_chunk(const LaParams &p, bool state_bf16, int seg, void *w
         !encode(fn, &m[1], p.k, p.K, p.nk, p.T, p.k_hs, p.k_ts) || !encode(fn, &m[2], p.v, p.V, p.nv, p.T, p.v_hs, p.v_ts))
         return cudaSuccess;
     *used = true;
-    const ChunkParams c{p, seg, state_bf16 ? 2 : 3, static_cast<float *>(ws), FastDiv((unsigned)(p.nv * p.tiles)),
+    const ChunkParams c{p, seg, static_cast<float *>(ws), FastDiv((unsigned)(p.nv * p.tiles)),
                         FastDiv((unsigned)p.tiles)};
     if (p.K > 64) return state_bf16 ? go<uint16_t, 128>(c, m, s) : go<float, 128>(c, m, s);
     return state_bf16 ? go<uint16_t, 64>(c, m, s) : go<float, 64>(c, m, s);
