@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -115,6 +116,19 @@ class gdr_norm_args(ctypes.Structure):
     ]
 
 
+def _packer(cls):
+    """Packs a call's values into the bytes of `cls` in one step (a ctypes
+    structure costs several microseconds to fill; a decode step's call is
+    bound by what the host does)."""
+    codes = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_void_p: "P", ctypes.c_float: "f"}
+    p = struct.Struct("@" + "".join(codes[t] for _, t in cls._fields_) + "0q")
+    assert p.size == ctypes.sizeof(cls)
+    return p.pack
+
+
+_pack_linattn = _packer(gdr_linattn_args)
+_pack_norm = _packer(gdr_norm_args)
+
 _lock = threading.Lock()
 _lib = None
 
@@ -146,9 +160,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                 "gdr_fold": ([A, vp, i32, i64, i32, i64, vp, vp, vp], ctypes.c_int),
                 "gdr_fwd_snapshots": ([A, vp, i64, i64, i64, i32, i32, vp], ctypes.c_int),
                 "gdr_rollback": ([A, vp, i64, i64, i64, i32, vp, vp], ctypes.c_int),
-                "gdr_linattn_fwd": ([ctypes.POINTER(gdr_linattn_args), vp], ctypes.c_int),
-                "gdr_linattn_workspace_bytes": ([ctypes.POINTER(gdr_linattn_args)], ctypes.c_int64),
-                "gdr_block_norm": ([ctypes.POINTER(gdr_norm_args), vp], ctypes.c_int),
+                "gdr_linattn_fwd": ([vp, vp], ctypes.c_int),  # structs as packed bytes or by reference
+                "gdr_linattn_workspace_bytes": ([vp], ctypes.c_int64),
+                "gdr_block_norm": ([vp, vp], ctypes.c_int),
                 "gdr_get_status": ([ctypes.POINTER(ctypes.c_uint32), i32], ctypes.c_int),
                 "gdr_probe_fma": ([i32, i32, i32, vp, i64, ctypes.POINTER(ctypes.c_int32), vp], ctypes.c_int),
             }
@@ -522,43 +536,54 @@ def gdr_rollback(state, slot_idx, inter, accepted):
 
 
 _DTYPES = {torch.float32: GDR_F32, torch.bfloat16: GDR_BF16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _dtype(t: torch.Tensor, name: str) -> int:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    d = _DTYPES.get(t.dtype)
-    if d is None:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
-    return d
+def _current(t: torch.Tensor) -> int:
+    """The current stream of a CUDA tensor's device."""
+    return _raw_stream(t.get_device()) if _raw_stream is not None else _stream(t.device)
 
 
-def _same_device(device, **tensors):
+def _refuse(device, dtypes, **tensors):
+    """Says what is wrong with one of a call's tensors: not one, not on the
+    call's device, or not of the wanted dtype (of float32 and bfloat16 where
+    dtypes has none for it)."""
     for name, t in tensors.items():
-        if t is not None and t.device != device:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device != device:
             raise ValueError(f"{name} is on {t.device}, the call on {device}")
+        want = dtypes.get(name)
+        if want is None and t.dtype not in _DTYPES:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
+        if want is not None and t.dtype != want:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {want}")
 
 
-def make_linattn_args(q, k, v, decay, state, slot_idx, offsets, out, *, decay_is_log=False, scale=0.0,
-                      max_row_len=0) -> gdr_linattn_args:
-    """Pack tensors into gdr_linattn_args (no copies; strides passed through;
-    no workspace)."""
-    td, sd = _dtype(q, "q"), _dtype(state, "state")
-    _dev(k, "k", q.dtype)
-    _dev(v, "v", q.dtype)
-    _dev(out, "out", q.dtype)
-    _dev(decay, "decay", torch.float32)
-    _dev(slot_idx, "slot_idx", torch.int32)
-    _dev(offsets, "offsets", torch.int32)
+def _linattn_values(q, k, v, decay, state, slot_idx, offsets, out, decay_is_log, scale, max_row_len):
+    """The values of gdr_linattn_args for a call's tensors (no workspace), checked."""
+    try:
+        dev, tok = q.device, q.dtype
+        td, sd = _DTYPES[tok], _DTYPES[state.dtype]
+        good = (q.is_cuda and k.dtype is tok and v.dtype is tok and out.dtype is tok and decay.dtype is torch.float32 and
+                slot_idx.dtype is torch.int32 and offsets.dtype is torch.int32 and
+                dev == k.device == v.device == decay.device == state.device == slot_idx.device == offsets.device == out.device)
+    except (AttributeError, KeyError):
+        good = False
+    if not good:
+        _refuse(getattr(q, "device", None), {"k": getattr(q, "dtype", None), "v": getattr(q, "dtype", None),
+                                             "out": getattr(q, "dtype", None), "decay": torch.float32,
+                                             "slot_idx": torch.int32, "offsets": torch.int32},
+                q=q, k=k, v=v, decay=decay, state=state, slot_idx=slot_idx, offsets=offsets, out=out)
     if state.dim() != 4:
         raise ValueError("state must be [max_slots, nv, K, V]")
     slots, nv, K, V = state.shape
     if q.dim() != 3 or q.shape != k.shape or q.shape[2] != K:
         raise ValueError(f"q and k must both be [T, nk, {K}]")
-    T, nk = q.shape[:2]
-    if v.shape != (T, nv, V) or out.shape != (T, nv, V):
+    T, nk, _ = q.shape
+    if v.shape != (T, nv, V) or out.shape != v.shape:
         raise ValueError(f"v and out must be [T, nv, V] = [{T}, {nv}, {V}]")
     if decay.shape != (nv,):
         raise ValueError(f"decay must be [nv] = [{nv}]")
@@ -567,41 +592,38 @@ def make_linattn_args(q, k, v, decay, state, slot_idx, offsets, out, *, decay_is
     batch = slot_idx.shape[0]
     if offsets.shape != (batch + 1,) or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous [batch+1] int32 tensor")
-    _same_device(q.device, k=k, v=v, out=out, decay=decay, state=state, slot_idx=slot_idx, offsets=offsets)
     (qt, qh, qc), (kt, kh, kc), (vt, vh, vc), (ot, oh, oc) = q.stride(), k.stride(), v.stride(), out.stride()
     if qc != 1 or kc != 1 or vc != 1 or oc != 1:
         raise ValueError("q, k, v and out must have a unit channel stride")
     ss, sh, sk, sv = state.stride()
-    return gdr_linattn_args(batch, nv, nk, K, V, 1 if decay_is_log else 0, td, sd, T, int(max_row_len),
-                            q.data_ptr(), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
-                            decay.data_ptr(), decay.stride(0), out.data_ptr(), ot, oh,
-                            state.data_ptr(), ss, sh, sk, sv, slots, slot_idx.data_ptr(), offsets.data_ptr(),
-                            None, 0, float(scale))
+    return (batch, nv, nk, K, V, 1 if decay_is_log else 0, td, sd, T, max_row_len, q.data_ptr(), qt, qh, k.data_ptr(), kt,
+            kh, v.data_ptr(), vt, vh, decay.data_ptr(), decay.stride(0), out.data_ptr(), ot, oh, state.data_ptr(), ss, sh,
+            sk, sv, slots, slot_idx.data_ptr(), offsets.data_ptr(), 0, 0, scale)
 
 
-def _linattn_workspace(lib, a: gdr_linattn_args, device, workspace):
-    """Give the call its workspace: the caller's, or a new one of the size it asks for."""
+def _linattn_workspace(lib, args: bytes, device, workspace):
+    """The arguments with a workspace, the caller's or a new one of the size the call asks for, and that tensor."""
     if workspace is None:
-        need = lib.gdr_linattn_workspace_bytes(ctypes.byref(a))
+        need = lib.gdr_linattn_workspace_bytes(args)
         if need < 0:
             _check(need)
         if need == 0:
-            return None
+            return args, None
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
     else:
-        _dev(workspace, "workspace")
-        _same_device(device, workspace=workspace)
+        _refuse(device, {"workspace": workspace.dtype}, workspace=workspace)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
+    a = gdr_linattn_args.from_buffer_copy(args)
     a.workspace = workspace.data_ptr()
     a.workspace_bytes = workspace.numel() * workspace.element_size()
-    return workspace
+    return bytes(a), workspace
 
 
 def gdr_linattn_workspace_bytes(q, k, v, decay, state, slot_idx, offsets, *, max_row_len=0) -> int:
     """Workspace bytes gdr_linattn_fwd would use for these tensors (0: none)."""
-    a = make_linattn_args(q, k, v, decay, state, slot_idx, offsets, v, max_row_len=max_row_len)
-    n = load_library().gdr_linattn_workspace_bytes(ctypes.byref(a))
+    n = load_library().gdr_linattn_workspace_bytes(
+        _pack_linattn(*_linattn_values(q, k, v, decay, state, slot_idx, offsets, v, False, 0.0, max_row_len)))
     if n < 0:
         _check(n)
     return int(n)
@@ -620,22 +642,23 @@ def gdr_linattn_fwd(q, k, v, decay, state, slot_idx, offsets, out=None, *, decay
     gdr_linattn_workspace_bytes() bytes."""
     if out is None:
         out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-    a = make_linattn_args(q, k, v, decay, state, slot_idx, offsets, out, decay_is_log=decay_is_log, scale=scale,
-                          max_row_len=max_row_len)
-    lib = load_library()
+    args = _pack_linattn(*_linattn_values(q, k, v, decay, state, slot_idx, offsets, out, decay_is_log, scale, max_row_len))
+    lib = _lib or load_library()
     if max_row_len != 1:
-        workspace = _linattn_workspace(lib, a, q.device, workspace)
-    _check(lib.gdr_linattn_fwd(ctypes.byref(a), _stream(q.device)))
+        args, workspace = _linattn_workspace(lib, args, q.device, workspace)
+    rc = lib.gdr_linattn_fwd(args, _current(q))
+    if rc:
+        _check(rc)
     return out
 
 
 def prepare_linattn_fwd(q, k, v, decay, state, slot_idx, offsets, out, *, decay_is_log=False, scale=0.0,
                         max_row_len=0, workspace=None) -> "Prepared":
-    a = make_linattn_args(q, k, v, decay, state, slot_idx, offsets, out, decay_is_log=decay_is_log, scale=scale,
-                          max_row_len=max_row_len)
+    args = _pack_linattn(*_linattn_values(q, k, v, decay, state, slot_idx, offsets, out, decay_is_log, scale, max_row_len))
     lib = load_library()
-    workspace = _linattn_workspace(lib, a, q.device, workspace)
-    return Prepared(lib.gdr_linattn_fwd, a, (), (q, k, v, decay, state, slot_idx, offsets, out, workspace), q.device)
+    args, workspace = _linattn_workspace(lib, args, q.device, workspace)
+    return Prepared(lib.gdr_linattn_fwd, gdr_linattn_args.from_buffer_copy(args), (),
+                    (q, k, v, decay, state, slot_idx, offsets, out, workspace), q.device)
 
 
 _ACTIVATIONS = {None: 0, "silu": 1, "sigmoid": 2}
@@ -649,11 +672,11 @@ def _activation(name) -> int:
 
 def _weight(w, D: int, name: str, device):
     if w is None:
-        return None
-    _dev(w, name, torch.float32)
+        return 0
+    if not (isinstance(w, torch.Tensor) and w.dtype is torch.float32 and w.device == device):
+        _refuse(device, {name: torch.float32}, **{name: w})
     if w.shape != (D,) or (D > 1 and w.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous [{D}] float32 tensor")
-    _same_device(device, **{name: w})
     return w.data_ptr()
 
 
@@ -665,6 +688,14 @@ def _rows(t, name: str):
     return (st[0], st[1]) if len(st) == 3 else (st[0], 0)
 
 
+def _float(t, name: str, device) -> int:
+    """The gdr_dtype of a float32 or bfloat16 tensor on the call's device."""
+    d = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) and t.is_cuda and t.device == device else None
+    if d is None:
+        _refuse(device, {}, **{name: t})
+    return d
+
+
 def gdr_gate_norm(x, gate, weight=None, out=None, *, eps=1e-6, activation="silu", gate_first=False, centered=False,
                   out_dtype=None):
     """Norm of a recurrence's output times its activated gate, per token and
@@ -673,30 +704,31 @@ def gdr_gate_norm(x, gate, weight=None, out=None, *, eps=1e-6, activation="silu"
     also be None, or broadcast over the last dimension), float32 or bfloat16;
     weight [D] float32 or None.  Returns out, of x's shape and out_dtype (by
     default the gate's dtype, or x's)."""
-    xd = _dtype(x, "x")
-    if x.dim() not in (2, 3):
+    dev = x.device
+    xd, shape = _float(x, "x", dev), x.shape
+    if len(shape) not in (2, 3):
         raise ValueError("x must be [T, H, D] or [T, D]")
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or (x if gate is None else gate).dtype, device=x.device)
-    elif out.shape != x.shape or (out_dtype is not None and out.dtype != out_dtype):
+        out = torch.empty(shape, dtype=out_dtype or (x if gate is None else gate).dtype, device=dev)
+    elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must have x's shape and dtype out_dtype")
-    od = _dtype(out, "out")
-    _same_device(x.device, gate=gate, out=out)
-    T, D = x.shape[0], x.shape[-1]
-    xt, xh = _rows(x, "x")
-    ot, oh = _rows(out, "out")
-    gp, gd, gt, gh, ge = None, 0, 0, 0, 0
+    od = _float(out, "out", dev)
+    T, D = shape[0], shape[-1]
+    (xt, xh), (ot, oh) = _rows(x, "x"), _rows(out, "out")
+    gp, gd, gt, gh, ge = 0, 0, 0, 0, 0
     if gate is not None:
-        gd = _dtype(gate, "gate")
-        if gate.shape[:-1] != x.shape[:-1] or gate.shape[-1] not in (1, D):
+        gd = _float(gate, "gate", dev)
+        if gate.shape != shape and (gate.shape[:-1] != shape[:-1] or gate.shape[-1] != 1):
             raise ValueError("gate must have x's shape, or 1 in its last dimension")
         gp, (gt, gh), ge = gate.data_ptr(), _rows(gate, "gate"), int(gate.shape[-1] == D)
     elif gate_first:
         raise ValueError("gate_first needs a gate")
-    a = gdr_norm_args(T, x.shape[1] if x.dim() == 3 else 1, D, xd, gd, 0, od, _activation(activation),
+    args = _pack_norm(T, shape[1] if len(shape) == 3 else 1, D, xd, gd, 0, od, _activation(activation),
                       1 if gate_first else 0, 1, 0, 1 if centered else 0, eps, 1.0, x.data_ptr(), xt, xh, gp, gt, gh, ge,
-                      None, 0, 0, None, 0, 0, out.data_ptr(), ot, oh, _weight(weight, D, "weight", x.device), None)
-    _check(load_library().gdr_block_norm(ctypes.byref(a), _stream(x.device)))
+                      0, 0, 0, 0, 0, 0, out.data_ptr(), ot, oh, _weight(weight, D, "weight", dev), 0)
+    rc = (_lib or load_library()).gdr_block_norm(args, _current(x))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -711,36 +743,34 @@ def gdr_residual_norm(block, residual, weight, *, post_weight=None, gate=None, a
     None for a norm without one.  Returns (residual_out, out): residual_out
     may be residual itself (in place) and is residual where block is None;
     out has out_dtype (by default the block's dtype, or residual's)."""
-    rd = _dtype(residual, "residual")
-    if residual.dim() != 2:
-        raise ValueError("residual must be [T, D]")
     dev = residual.device
-    T, D = residual.shape
+    rd, shape = _float(residual, "residual", dev), residual.shape
+    if len(shape) != 2:
+        raise ValueError("residual must be [T, D]")
+    T, D = shape
     if out is None:
-        out = torch.empty((T, D), dtype=out_dtype or (residual if block is None else block).dtype, device=dev)
-    elif out.shape != (T, D) or (out_dtype is not None and out.dtype != out_dtype):
+        out = torch.empty(shape, dtype=out_dtype or (residual if block is None else block).dtype, device=dev)
+    elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must be [T, D] of dtype out_dtype")
-    od = _dtype(out, "out")
-    ot, oh = _rows(out, "out")
-    rt, rh = _rows(residual, "residual")
-    xp, xd, xt, rop, rot = None, 0, 0, None, 0
+    od = _float(out, "out", dev)
+    ot, rt = _rows(out, "out")[0], _rows(residual, "residual")[0]
+    xp, xd, xt, rop, rot = 0, 0, 0, 0, 0
     if block is None:
         if gate is not None or post_weight is not None or residual_out is not None:
             raise ValueError("gate, post_weight and residual_out need a block")
         h = residual
     else:
-        xd = _dtype(block, "block")
-        if block.shape != (T, D):
+        xd = _float(block, "block", dev)
+        if block.shape != shape:
             raise ValueError("block must have residual's shape")
         xp, xt = block.data_ptr(), _rows(block, "block")[0]
-        h = torch.empty((T, D), dtype=residual.dtype, device=dev) if residual_out is None else residual_out
-        if h.shape != (T, D) or h.dtype != residual.dtype:
+        h = torch.empty(shape, dtype=residual.dtype, device=dev) if residual_out is None else residual_out
+        if h is not residual and (_float(h, "residual_out", dev) != rd or h.shape != shape):
             raise ValueError("residual_out must have residual's shape and dtype")
         rop, rot = h.data_ptr(), _rows(h, "residual_out")[0]
-    _same_device(dev, block=block, gate=gate, residual_out=h, out=out)
-    gp, gd, gt, ge = None, 0, 0, 0
+    gp, gd, gt, ge = 0, 0, 0, 0
     if gate is not None:
-        gd, gp = _dtype(gate, "gate"), gate.data_ptr()
+        gd, gp = _float(gate, "gate", dev), gate.data_ptr()
         if gate.shape == (D,):
             ge = 1
             if D > 1 and gate.stride(0) != 1:
@@ -749,11 +779,13 @@ def gdr_residual_norm(block, residual, weight, *, post_weight=None, gate=None, a
             gt, ge = _rows(gate, "gate")[0], int(gate.shape[1] == D)
         else:
             raise ValueError("gate must be [T, D], [T, 1] or [D]")
-    a = gdr_norm_args(T, 1, D, xd, gd, rd, od, _activation(activation), 0, 0 if post_weight is None else 1, 1,
-                      1 if centered else 0, eps, residual_scale, xp, xt, 0, gp, gt, 0, ge, residual.data_ptr(), rt, rh,
-                      rop, rot, 0, out.data_ptr(), ot, oh, _weight(post_weight, D, "post_weight", dev),
+    args = _pack_norm(T, 1, D, xd, gd, rd, od, _activation(activation), 0, 0 if post_weight is None else 1, 1,
+                      1 if centered else 0, eps, residual_scale, xp, xt, 0, gp, gt, 0, ge, residual.data_ptr(), rt, 0,
+                      rop, rot, 0, out.data_ptr(), ot, 0, _weight(post_weight, D, "post_weight", dev),
                       _weight(weight, D, "weight", dev))
-    _check(load_library().gdr_block_norm(ctypes.byref(a), _stream(dev)))
+    rc = (_lib or load_library()).gdr_block_norm(args, _current(residual))
+    if rc:
+        _check(rc)
     return h, out
 
 

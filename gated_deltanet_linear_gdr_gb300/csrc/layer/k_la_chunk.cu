@@ -96,6 +96,12 @@ struct Unit {
 };
 
 __device__ __forceinline__ float power(float lg2, int n) { return n == 0 ? 1.0f : exp2f(lg2 * (float)n); }
+// The same to 2^-22, 0 below float32's normal range: for weights that end in bfloat16.
+__device__ __forceinline__ float power_fast(float lg2, int n) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(lg2 * (float)n));
+    return n == 0 ? 1.0f : y;
+}
 
 // Walks this CTA's units: positions blockIdx.x, then back and forth, so that
 // units sorted by length are dealt evenly.
@@ -114,11 +120,12 @@ template <bool STATES> struct Walk {
         u.len = (int)uniform(u.len);
         u.chunks = (int)uniform(u.chunks);
         u.x = (int)uniform(u.x);
+        u.slot = (int)uniform(u.slot);
         return uniform(more) != 0;
     }
     __device__ bool find(Unit &u, bool report) {
         const LaParams &p = c.p;
-        u.t0 = u.x = u.h = u.tile = u.len = u.chunks = u.skip_len = 0;
+        u.t0 = u.x = u.h = u.tile = u.len = u.chunks = u.skip_len = u.slot = 0;
         const unsigned G = gridDim.x, pos = (unsigned)i * G + ((i & 1) ? G - 1 - blockIdx.x : blockIdx.x);
         ++i;
         u.x = (int)c.per.div(pos);  // positions are below 2^31 and a walk ends at the first one past the units
@@ -239,7 +246,7 @@ struct Ctx {
 };
 
 // Chunks in order, into the stages.
-template <int KP, bool STATES> struct Loader {
+template <int KP, bool ST2, bool STATES> struct Loader {  // ST2: a bfloat16 pool
     const Ctx &x;
     const CUtensorMap *mq, *mk, *mv;
     Walk<STATES> walk;
@@ -252,11 +259,32 @@ template <int KP, bool STATES> struct Loader {
         u.chunks = 0;
     }
 
+    // Asks L2 for the unit's start state, which its warps will want in up to
+    // three chunks' time: 4 lanes a key index, 128 bytes of it each.
+    __device__ void fetch_state() {
+        const LaParams &p = x.c.p;
+        const int lane = threadIdx.x & 31, es = x.c.seg || !ST2 ? 4 : 2, bytes = min(128, p.V - u.tile * 128) * es;
+        const char *from;
+        long long step;
+        if (x.c.seg) {
+            from = reinterpret_cast<const char *>(x.c.ws + ((long long)u.x * p.nv + u.h) * p.K * p.V + u.tile * 128);
+            step = (long long)p.V * 4;
+        } else {
+            from = static_cast<const char *>(p.state) + ((long long)u.slot * p.st_slot + (long long)u.h * p.st_head + u.tile * 128) * es;
+            step = p.st_k * es;
+        }
+        const int at = (lane & 3) * 128;
+        if (at < bytes)
+            for (int k = lane >> 2; k < p.K; k += 8)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(from + (long long)k * step + at));
+    }
+
     // Loads the next chunk, if there is one, once its stage is free; false where a wait gave up.
     __device__ bool step() {
         while (more && j >= u.chunks) {
             more = walk.next(u, false);
             j = 0;
+            if (!STATES && more && u.chunks > 0) fetch_state();
         }
         if (!more) return true;
         const int s = g % kStages;
@@ -562,8 +590,8 @@ __device__ void role_scores(const Ctx &x, int warp, int lane) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int gap = 8 * (i >> 1) + 2 * (lane & 3) - (row0 + (i & 1) * 8);
-            w[i].x = gap < 0 ? 0.0f : p.scale * power(u.lg2, gap);
-            w[i].y = gap < -1 ? 0.0f : p.scale * power(u.lg2, gap + 1);
+            w[i].x = gap < 0 ? 0.0f : p.scale * power_fast(u.lg2, gap);
+            w[i].y = gap < -1 ? 0.0f : p.scale * power_fast(u.lg2, gap + 1);
         }
         for (int j = 0; j < u.chunks; ++j, ++g) {
             const int n = min(kC, u.len - j * kC);
@@ -639,7 +667,7 @@ __device__ void role_out(const Ctx &x, int warp, int lane) {
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
             const int i = 8 * b + 2 * (lane & 3);
-            f[b] = make_float2(p.scale * power(u.lg2, i + 1), p.scale * power(u.lg2, i + 2));
+            f[b] = make_float2(p.scale * power_fast(u.lg2, i + 1), p.scale * power_fast(u.lg2, i + 2));
         }
         const bool on = col + (lane & 3) * 8 < p.V;
         uint16_t *to = out + (long long)(u.t0 + lane / 4) * p.o_ts + (long long)u.h * p.o_hs + col + (lane & 3) * 8;
@@ -736,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == kWarpMma + 2) {
             if (!STATES) role_mma_scores<KP>(x);
         } else {
-            Loader<KP, STATES> load(x, &mq, &mk, &mv);
+            Loader<KP, sizeof(ST) == 2, STATES> load(x, &mq, &mk, &mv);
             while (load.more && load.step()) {
             }
             load.drain();
