@@ -244,8 +244,8 @@ int gdr_block_norm(const gdr_norm_args *a, void *stream) {
         return fail(GDR_ERR_UNSUPPORTED, "%s: buffers must be aligned to their elements", fn);
 
     gdr::NormParams p{};
-    p.tokens = a->tokens;
-    p.heads = a->heads;
+    p.rows = (unsigned)(a->tokens * a->heads);
+    p.heads_div = gdr::FastDiv((unsigned)a->heads);
     p.D = a->D;
     p.x_bf16 = a->x_dtype == GDR_BF16;
     p.gate_bf16 = a->gate_dtype == GDR_BF16;

@@ -47,8 +47,9 @@ cudaError_t launch_la_chunk(const LaParams &p, bool state_bf16, int seg, void *w
 
 // One fused norm call, after validation.
 struct NormParams {
-    long long tokens;
-    int heads, D;
+    unsigned rows;     // tokens * heads
+    FastDiv heads_div;
+    int D;
     int x_bf16, gate_bf16, res_bf16, out_bf16;
     int act, gate_first, post, pre, centered;
     float eps, scale, inv_d;
@@ -66,5 +67,6 @@ struct NormParams {
 };
 // vec: every row, gate and weight may be moved as vectors of 8 elements.
 cudaError_t launch_norm(const NormParams &p, bool vec, cudaStream_t s);
+cudaError_t launch_norm_odd(const NormParams &p, cudaStream_t s);
 
 }  // namespace gdr
