@@ -46,7 +46,7 @@ constexpr int kStages = 3;
 constexpr int kSub = kC * 128;        // bytes of a 64-token x 64-channel operand block
 constexpr int kTile = 2 * kSub;       // bytes of a 64-token x 128-channel operand
 constexpr int kStage = 3 * kTile;     // Q | K | V
-constexpr int kMaxRows = 128;         // rows whose order and segments are worked out in shared memory
+constexpr int kMaxRows = 64, kMaxHeads = 64;  // rows and heads whose facts are kept in shared memory
 
 // Warps by role, in warpgroups of 4.  The issuers and the loader come first:
 // between ready warps the scheduler prefers the older.
@@ -54,7 +54,7 @@ constexpr int kWarpsS = 8, kWarpsO = 4, kWarpsP = 4, kWarpsK = 4;
 constexpr int kWarpMma = 0, kWarpS = 4, kWarpO = kWarpS + kWarpsS, kWarpP = kWarpO + kWarpsO, kWarpK = kWarpP + kWarpsP;
 constexpr int kThreads = 32 * (kWarpK + kWarpsK);
 // Registers a thread: 768 threads are launched with 80, and the roles share them out anew.
-constexpr int kRegsS = 104, kRegsO = 96, kRegsP = 96, kRegsK = 48, kRegsRest = 32;
+constexpr int kRegsS = 112, kRegsO = 96, kRegsP = 80, kRegsK = 48, kRegsRest = 32;
 static_assert(2 * kRegsS + kRegsO + kRegsP + kRegsK + kRegsRest == 6 * 80, "shares");
 
 // tensor memory columns
@@ -62,18 +62,21 @@ constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 192, kColDS = 256, kColS = 
 
 enum Bar {
     kLoaded = 0, kStageFree = kLoaded + kStages, kPFull = kStageFree + kStages, kPFree = kPFull + 2, kPtFull = kPFree + 2, kSFull, kDsFull = kSFull + 2,
-    kDsFree = kDsFull + 2, kKtFull, kOFull = kKtFull + 2, kOFree = kOFull + 2, kDrain, kBars
+    kDsFree = kDsFull + 2, kKtFull, kOFull = kKtFull + 2, kOFree = kOFull + 2, kStateIn, kStateRead, kDrain, kBars
 };
 
 struct Smem {
     unsigned char stage[kStages][kStage];
-    unsigned char kt[2][2][kTile];        // second and third part of K~, two chunks; the first takes K's place
+    unsigned char kt[4 * kTile];          // K~ but for its first part, which takes K's place, of two chunks: with two
+                                          // parts it fills half of this, and the rest holds a state on its way
     unsigned char pt[kSub];               // P~^T
     unsigned char ost[kWarpsO][32 * 64];  // output on its way out, 32 tokens x 32 columns a warp
     uint64_t bar[kBars];
-    int order[kMaxRows], first[kMaxRows + 1];
+    int row_t0[kMaxRows], row_len[kMaxRows], row_slot[kMaxRows];  // by rank: the longest row first; len -1: bad offsets
+    int first[kMaxRows + 1];                                      // a ranked row's first segment
+    float lg2[kMaxHeads];                                         // log2 lambda, NaN where the decay is bad
     uint32_t tmem;
-    int gave_up;
+    int gave_up, state_loads;
 };
 static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory");
 
@@ -86,11 +89,11 @@ struct ChunkParams {
 
 // A unit of work, the same for every role: one segment of a row, one head, one column tile.
 struct Unit {
-    int h, tile, b, slot;
+    int h, tile, slot;
     int t0, len;  // tokens of the segment; len 0: nothing to compute
     int chunks;
     int x;        // segment number
-    bool first, last;          // of its row
+    bool last;                 // of its row
     int skip_t0, skip_len;     // a skipped row's tokens, whose output is zero
     float lg2;                 // log2 lambda
 };
@@ -101,6 +104,17 @@ __device__ __forceinline__ float power_fast(float lg2, int n) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(lg2 * (float)n));
     return n == 0 ? 1.0f : y;
+}
+
+// A row's length, or -1 where its offsets are not sound.
+__device__ __forceinline__ int sound_len(const LaParams &p, int t0, int t1) {
+    return t0 < 0 || t1 < t0 || t1 > p.T ? -1 : t1 - t0;
+}
+// log2 of a head's decay; NaN for one outside [0, 1].
+__device__ __forceinline__ float log2_lambda(const LaParams &p, int h) {
+    const float d = p.decay[(long long)h * p.decay_s];
+    const bool ok = p.decay_is_log ? d <= 0.0f : (d >= 0.0f && d <= 1.0f);
+    return !ok ? __int_as_float(0x7fffffff) : p.decay_is_log ? d * 1.44269504088896340736f : log2f(d);
 }
 
 // Walks this CTA's units: positions blockIdx.x, then back and forth, so that
@@ -132,7 +146,7 @@ template <bool STATES> struct Walk {
         const unsigned ht = pos - (unsigned)u.x * c.per.d;
         u.h = (int)c.tiles.div(ht);
         u.tile = (int)(ht - (unsigned)u.h * c.tiles.d);
-        int seg_i = 0;
+        int seg_i = 0, r0, len;
         if (p.batch <= kMaxRows) {
             int r = u.x;
             if (c.seg) {
@@ -140,26 +154,27 @@ template <bool STATES> struct Walk {
                 r = 0;
                 while (sm.first[r + 1] <= u.x) ++r;
                 seg_i = u.x - sm.first[r];
-            } else if (u.x >= p.batch) {
+            } else if (r >= p.batch) {
                 return false;
             }
-            u.b = sm.order[r];
+            r0 = sm.row_t0[r];
+            len = sm.row_len[r];
+            u.slot = sm.row_slot[r];
         } else {
             if (u.x >= p.batch) return false;
-            u.b = u.x;
+            r0 = p.offsets[u.x];
+            len = sound_len(p, r0, p.offsets[u.x + 1]);
+            u.slot = p.slot_idx[u.x];
         }
-        u.first = u.last = true;
-        const int r0 = p.offsets[u.b], r1 = p.offsets[u.b + 1];
-        u.slot = p.slot_idx[u.b];
-        const float d = p.decay[(long long)u.h * p.decay_s];
+        u.lg2 = u.h < kMaxHeads ? sm.lg2[u.h] : log2_lambda(p, u.h);
+        u.last = true;
         const bool leader = report && u.h == 0 && u.tile == 0 && seg_i == 0;
-        if (r0 < 0 || r1 < r0 || r1 > p.T) {
+        if (len < 0) {
             if (leader) flag(p.status, GDR_STATUS_BAD_OFFSETS);
             return true;
         }
-        const bool too_long = p.max_len > 0 && r1 - r0 > p.max_len;
-        const bool decay_ok = p.decay_is_log ? d <= 0.0f : (d >= 0.0f && d <= 1.0f);
-        if (r1 > r0 && (u.slot < 0 || u.slot >= p.max_slots || !decay_ok || too_long)) {
+        const bool too_long = p.max_len > 0 && len > p.max_len, bad_decay = isnan(u.lg2);
+        if (len > 0 && (u.slot < 0 || u.slot >= p.max_slots || bad_decay || too_long)) {
             if (too_long) {
                 if (leader) flag(p.status, GDR_STATUS_ROW_TOO_LONG);
             } else if (u.slot < -1 || u.slot >= p.max_slots) {
@@ -169,16 +184,14 @@ template <bool STATES> struct Walk {
             }
             if (seg_i == 0) {
                 u.skip_t0 = r0;
-                u.skip_len = r1 - r0;
+                u.skip_len = len;
             }
             return true;
         }
-        u.lg2 = p.decay_is_log ? d * 1.44269504088896340736f : log2f(d);
         u.t0 = r0;
-        u.len = r1 - r0;
+        u.len = len;
         if (c.seg) {
             const int at = seg_i * c.seg;
-            u.first = seg_i == 0;
             u.last = u.len - at <= c.seg;
             u.t0 += at;
             u.len = u.last ? u.len - at : c.seg;
@@ -189,34 +202,36 @@ template <bool STATES> struct Walk {
     }
 };
 
-// Rows by descending length, and the number of each one's first segment.
+// Facts of the rows, by descending length, and of the heads; the number of each row's first segment.
 __device__ __forceinline__ void plan_rows(const ChunkParams &c, Smem &sm) {
-    const int B = c.p.batch;
-    if (B > kMaxRows) return;
-    for (int b = threadIdx.x; b < B; b += kThreads) {
-        const int t0 = c.p.offsets[b], t1 = c.p.offsets[b + 1];
-        sm.first[b] = t0 < 0 || t1 < t0 || t1 > c.p.T ? 0 : t1 - t0;
+    const LaParams &p = c.p;
+    const int B = p.batch, tid = threadIdx.x;
+    if (tid >= 128 && tid < 128 + min(p.nv, kMaxHeads)) sm.lg2[tid - 128] = log2_lambda(p, tid - 128);
+    int len = -1, t0 = 0, slot = -1;
+    if (B <= kMaxRows && tid < B) {
+        t0 = p.offsets[tid];
+        len = sound_len(p, t0, p.offsets[tid + 1]);
+        slot = p.slot_idx[tid];
+        sm.first[tid] = len;
     }
     __syncthreads();
-    if (threadIdx.x < B) {
-        const int b = threadIdx.x, len = sm.first[b];
-        int rank = 0;
-        for (int o = 0; o < B; ++o) rank += sm.first[o] > len || (sm.first[o] == len && o < b);
-        sm.order[rank] = b;
+    int rank = 0;
+    if (B <= kMaxRows && tid < B) {
+        for (int o = 0; o < B; ++o) rank += sm.first[o] > len || (sm.first[o] == len && o < tid);
+        sm.row_t0[rank] = t0;
+        sm.row_len[rank] = len;
+        sm.row_slot[rank] = slot;
     }
     __syncthreads();
-    if (c.seg && threadIdx.x < 32) {  // batch <= 32: one lane a row
-        const int lane = threadIdx.x;
-        const int n = lane < B ? max(1, (sm.first[sm.order[lane]] + c.seg - 1) / c.seg) : 0;
-        int end = n;
+    if (c.seg && tid < 32) {  // batch <= 32: one lane a row
+        int end = tid < B ? max(1, (sm.row_len[tid] + c.seg - 1) / c.seg) : 0;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, end, m);
-            if (lane >= m) end += o;
+            if (tid >= m) end += o;
         }
-        __syncwarp();
-        if (lane < B) sm.first[lane + 1] = end;
-        if (lane == 0) sm.first[0] = 0;
+        if (tid < B) sm.first[tid + 1] = end;
+        if (tid == 0) sm.first[0] = 0;
     }
     __syncthreads();
 }
@@ -263,15 +278,15 @@ template <int KP, bool ST2, bool STATES> struct Loader {  // ST2: a bfloat16 poo
     // three chunks' time: 4 lanes a key index, 128 bytes of it each.
     __device__ void fetch_state() {
         const LaParams &p = x.c.p;
-        const int lane = threadIdx.x & 31, es = x.c.seg || !ST2 ? 4 : 2, bytes = min(128, p.V - u.tile * 128) * es;
+        const int lane = threadIdx.x & 31, bytes = min(128, p.V - u.tile * 128) * 4;
         const char *from;
         long long step;
         if (x.c.seg) {
             from = reinterpret_cast<const char *>(x.c.ws + ((long long)u.x * p.nv + u.h) * p.K * p.V + u.tile * 128);
             step = (long long)p.V * 4;
         } else {
-            from = static_cast<const char *>(p.state) + ((long long)u.slot * p.st_slot + (long long)u.h * p.st_head + u.tile * 128) * es;
-            step = p.st_k * es;
+            from = static_cast<const char *>(p.state) + ((long long)u.slot * p.st_slot + (long long)u.h * p.st_head + u.tile * 128) * 4;
+            step = p.st_k * 4;
         }
         const int at = (lane & 3) * 128;
         if (at < bytes)
@@ -284,7 +299,7 @@ template <int KP, bool ST2, bool STATES> struct Loader {  // ST2: a bfloat16 poo
         while (more && j >= u.chunks) {
             more = walk.next(u, false);
             j = 0;
-            if (!STATES && more && u.chunks > 0) fetch_state();
+            if (!STATES && more && u.chunks > 0 && (!ST2 || x.c.seg)) fetch_state();
         }
         if (!more) return true;
         const int s = g % kStages;
@@ -361,7 +376,7 @@ template <int KP, int PARTS, bool STATES> __device__ void role_mma_state(const C
             break;
         fence_after();
         const uint32_t me = elect_one(), st = uniform(g % kStages), odd = uniform(g & 1);
-        const uint64_t k = d_mn + ((st * kStage + kTile) >> 4), v = k + (kTile >> 4), kt = d_kt + (odd * 2 * kTile >> 4);
+        const uint64_t k = d_mn + ((st * kStage + kTile) >> 4), v = k + (kTile >> 4), kt = d_kt + (odd * (PARTS - 1) * kTile >> 4);
         mma_ss_mn64<false>(me, x.tmem + kColDS, v, k, id);
         mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt, id);
         if (PARTS == 3) mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt + (kTile >> 4), id);
@@ -426,7 +441,7 @@ template <int KP, int PARTS, bool STATES> __device__ void role_keys(const Ctx &x
             if (__builtin_expect(n < kC, 0)) clear_tail(stage + 2 * kTile, n, nv, tid, 32 * kWarpsK);
             if (!STATES && !x.wait(kPFull + (g & 1), g >> 1)) return;           // K Q^T has read K
             if (g > 1 && !x.wait(kDsFull + (g & 1), (g >> 1) - 1)) return;  // and the product before last its K~
-            unsigned char *const rest = x.sm.kt[g & 1][0];
+            unsigned char *const rest = x.sm.kt + (g & 1) * (PARTS - 1) * kTile;
             // small loops: the roles share the instruction caches
             float w = w3;
 #pragma unroll 1
@@ -476,15 +491,21 @@ template <int KP, int PARTS, bool STATES> __device__ void role_keys(const Ctx &x
 }
 
 // The state: lane = value index, 64 of its key indices in a thread's
-// registers (warps 0-3: 0..63, warps 4-7: 64..127).
+// registers (warps 0-3: 0..63, warps 4-7: 64..127).  The states of a bfloat16
+// pool come and go through a 32 KiB buffer by TMA: while a unit is computed the
+// next one's start state comes in; between units each thread takes its elements
+// of that and puts the finished ones in their places, and they leave.  Read and
+// written from here instead, a unit of one chunk took 7 us, most of it waiting.
 template <typename ST, int KP, bool STATES> __device__ void role_state(const Ctx &x, int warp, int lane) {
     const LaParams &p = x.c.p;
     const int quad = warp & 3, half = warp >> 2, v = quad * 32 + lane;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const bool mine = half * 64 < KP;
+    const bool staged = sizeof(ST) == 2 && !STATES && !x.c.seg;
+    const ST *const buf = reinterpret_cast<const ST *>(x.sm.kt + 2 * kTile) + half * 64 * 128 + v;  // [KP][128]
     Walk<STATES> walk(x.c, x.sm);
     Unit u;
-    unsigned g = 0;
+    unsigned g = 0, units = 0;
     float2 s[32];
     while (walk.next(u, false)) {
         if (u.chunks == 0) continue;
@@ -492,27 +513,34 @@ template <typename ST, int KP, bool STATES> __device__ void role_state(const Ctx
         const int k0 = half * 64, kn = min(64, p.K - k0);
         ST *pool = static_cast<ST *>(p.state) + (long long)u.slot * p.st_slot + (long long)u.h * p.st_head + u.tile * 128 + v;
         float *ws = x.c.ws + ((long long)u.x * p.nv + u.h) * p.K * p.V + u.tile * 128 + v;
-        // in groups of 16 key indices (K is a multiple of 16), each asked for at once
+        if (staged) {
+            if (!x.wait(kStateIn, units)) return;
+            if (mine) {  // what lies outside the pool's rows and columns came in as zero
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] = make_float2(0.0f, 0.0f);
-        if (!STATES && on) {
+                for (int i = 0; i < 32; ++i) s[i] = make_float2(to_f32(buf[2 * i * 128]), to_f32(buf[(2 * i + 1) * 128]));
+            }
+            x.arrive(kStateRead);
+        } else {
+            // in groups of 16 key indices (K is a multiple of 16), each asked for at once
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                if (16 * b >= kn) break;
-                if (x.c.seg) {
-                    const float *from = ws + (long long)(k0 + 16 * b) * p.V;
+            for (int i = 0; i < 32; ++i) s[i] = make_float2(0.0f, 0.0f);
+            if (!STATES && on) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s[8 * b + i] = make_float2(from[2 * i * p.V], from[(2 * i + 1) * p.V]);
-                } else {
-                    const ST *from = pool + (long long)(k0 + 16 * b) * p.st_k;
-                    ST raw[16];
+                for (int b = 0; b < 4; ++b) {
+                    if (16 * b >= kn) break;
+                    if (x.c.seg) {
+                        const float *from = ws + (long long)(k0 + 16 * b) * p.V;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) raw[i] = from[i * p.st_k];
+                        for (int i = 0; i < 8; ++i) s[8 * b + i] = make_float2(from[2 * i * p.V], from[(2 * i + 1) * p.V]);
+                    } else if constexpr (sizeof(ST) == 4) {
+                        const float *from = pool + (long long)(k0 + 16 * b) * p.st_k;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) s[8 * b + i] = make_float2(to_f32(raw[2 * i]), to_f32(raw[2 * i + 1]));
+                        for (int i = 0; i < 8; ++i) s[8 * b + i] = make_float2(from[2 * i * p.st_k], from[(2 * i + 1) * p.st_k]);
+                    }
                 }
             }
         }
+        ++units;
         const float lam_c = power(u.lg2, kC);
         for (int j = 0; j < u.chunks; ++j, ++g) {
             const int n = min(kC, u.len - j * kC);
@@ -644,9 +672,37 @@ __device__ void role_scores(const Ctx &x, int warp, int lane) {
     }
 }
 
+// Loads of a bfloat16 pool's start states into their one buffer.
+template <int KP> struct StateLoads {
+    const Ctx &x;
+    const CUtensorMap *map;
+    Walk<false> ahead;
+    unsigned units = 0;
+    __device__ StateLoads(const Ctx &x_, const CUtensorMap *m) : x(x_), map(m), ahead(x_.c, x_.sm) {}
+
+    // The next unit's, once every thread has taken what the buffer holds; false where a wait gave up.
+    __device__ bool next() {
+        if (units > 0 && !x.wait(kStateRead, units - 1)) return false;
+        Unit u;
+        while (ahead.next(u, false)) {
+            if (u.chunks == 0) continue;
+            if ((threadIdx.x & 31) == 0) {
+                ++x.sm.state_loads;
+                mbar_expect(x.bar(kStateIn), KP * 256);
+                tma_load4(x.base + (uint32_t)offsetof(Smem, kt) + 2 * kTile, map, u.tile * 128, 0, u.h, u.slot,
+                          x.bar(kStateIn));
+            }
+            break;
+        }
+        __syncwarp();
+        ++units;
+        return true;
+    }
+};
+
 // The output: a warp has 32 columns of O^T, which it turns through shared
 // memory into rows of 64 bytes a token.
-__device__ void role_out(const Ctx &x, int warp, int lane) {
+template <int KP> __device__ void role_out(const Ctx &x, int warp, int lane, StateLoads<KP> *states) {
     const LaParams &p = x.c.p;
     uint16_t *const out = static_cast<uint16_t *>(p.out);
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
@@ -657,12 +713,14 @@ __device__ void role_out(const Ctx &x, int warp, int lane) {
     Walk<false> walk(x.c, x.sm);
     Unit u;
     unsigned g = 0;
+    if (states && !states->next()) return;
     while (walk.next(u, warp == 0 && lane == 0)) {
         const int col = u.tile * 128 + warp * 32;
         if (u.skip_len && col + lane < p.V)
             for (int t = 0; t < u.skip_len; ++t)
                 out[(long long)(u.skip_t0 + t) * p.o_ts + (long long)u.h * p.o_hs + col + lane] = 0;
         if (u.chunks == 0) continue;
+        if (states && !states->next()) return;
         float2 f[8];
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
@@ -675,9 +733,8 @@ __device__ void role_out(const Ctx &x, int warp, int lane) {
             const int n = min(kC, u.len - j * kC);
             if (!x.wait(kOFull + (g & 1), g >> 1)) return;
             fence_after();
-            uint32_t h[2][16];
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {  // 32 of the tokens
+            uint32_t h[16];  // 32 tokens, packed; the first 32 go to staging before the others are read
+            auto collect = [&](int ch) {
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {  // 16 of the columns
                     uint32_t a[16], b[16];
@@ -686,26 +743,25 @@ __device__ void role_out(const Ctx &x, int warp, int lane) {
                     wait_ld();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        h[ch][hh * 8 + i] =
+                        h[hh * 8 + i] =
                             pack_bf16(__ffma2_rn(f[ch * 4 + i / 2],
                                                  make_float2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1])),
                                                  make_float2(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]))));
                 }
-            }
-            fence_before();
-            x.arrive(kOFree);
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
+            };
+            auto stage = [&]() {
                 __syncwarp();
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int t = i * 16 + st_tok;
-                        const uint32_t *w = h[ch] + hh * 8 + i * 4;
+                        const uint32_t *w = h + hh * 8 + i * 4;
                         stmatrix4_t(ost_a + t * 64 + (((hh * 2 + st_blk) ^ ((t >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
                     }
                 __syncwarp();
+            };
+            auto write = [&](int ch) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int t = r * 8 + lane / 4;
@@ -713,7 +769,15 @@ __device__ void role_out(const Ctx &x, int warp, int lane) {
                         *reinterpret_cast<uint4 *>(to + (long long)(ch * 32 + r * 8) * p.o_ts) =
                             *reinterpret_cast<const uint4 *>(ost + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
                 }
-            }
+            };
+            collect(0);
+            stage();
+            collect(1);
+            fence_before();
+            x.arrive(kOFree);
+            write(0);
+            stage();
+            write(1);
             to += (long long)kC * p.o_ts;
         }
     }
@@ -722,7 +786,8 @@ __device__ void role_out(const Ctx &x, int warp, int lane) {
 template <typename ST, int KP, bool STATES>
 __global__ void __launch_bounds__(kThreads, 1)
     k_la_chunk(const __grid_constant__ ChunkParams c, const __grid_constant__ CUtensorMap mq,
-               const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+               const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+               const __grid_constant__ CUtensorMap ms) {
     constexpr int PARTS = sizeof(ST) == 2 ? 2 : 3;  // bfloat16 parts of K~
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw), pad = (1024u - (raw & 1023u)) & 1023u;
@@ -730,13 +795,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = (int)uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const uint32_t base = raw + pad, bars = base + (uint32_t)offsetof(Smem, bar);
     if (threadIdx.x == 0) {
-        sm.gave_up = 0;
+        sm.gave_up = sm.state_loads = 0;
         for (int i = 0; i < kBars; ++i) {
             int n = 1;
             if (i >= kStageFree && i < kStageFree + kStages) n = STATES ? 1 : 2;  // the products that read a stage last
             if (i == kPFree || i == kPFree + 1 || i == kPtFull) n = kWarpsP;
             if (i == kDrain) n = STATES ? 1 : 3;
-            if (i == kSFull || i == kSFull + 1 || i == kDsFree) n = kWarpsS;
+            if (i == kSFull || i == kSFull + 1 || i == kDsFree || i == kStateRead) n = kWarpsS;
             if (i == kKtFull || i == kKtFull + 1) n = kWarpsK;
             if (i == kOFree) n = kWarpsO;
             mbar_init(bars + 8 * i, n);
@@ -774,7 +839,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         role_state<ST, KP, STATES>(x, warp - kWarpS, lane);
     } else if (warp < kWarpP) {
         if (kRegsO > 80) regs_up<kRegsO>();
-        if (!STATES) role_out(x, warp - kWarpO, lane);
+        if constexpr (!STATES) {
+            StateLoads<KP> states(x, &ms);
+            const bool mine = warp == kWarpO && sizeof(ST) == 2 && !c.seg;
+            role_out<KP>(x, warp - kWarpO, lane, mine ? &states : nullptr);
+            if (mine && lane == 0 && sm.state_loads) {  // no state's copy is in flight when the CTA ends
+                volatile int never = 0;
+                mbar_wait(x.bar(kStateIn), (uint32_t)(sm.state_loads - 1) & 1u, &never);
+            }
+        }
     } else if (warp < kWarpK) {
         if (kRegsP > 80) regs_up<kRegsP>();
         if (!STATES) role_scores(x, warp - kWarpP, lane);
@@ -800,8 +873,7 @@ template <typename ST> __global__ void __launch_bounds__(256) k_la_join(const __
     if (threadIdx.x < 32) {
         int len = -1;
         if ((int)threadIdx.x < B) {
-            const int t0 = p.offsets[threadIdx.x], t1 = p.offsets[threadIdx.x + 1];
-            len = t0 < 0 || t1 < t0 || t1 > p.T ? 0 : t1 - t0;
+            len = sound_len(p, p.offsets[threadIdx.x], p.offsets[threadIdx.x + 1]);
         }
         s_len[threadIdx.x] = len;
     }
@@ -815,10 +887,9 @@ template <typename ST> __global__ void __launch_bounds__(256) k_la_join(const __
         if (rank < r) before += max(1, (s_len[o] + c.seg - 1) / c.seg);
     }
     const int n = (s_len[b] + c.seg - 1) / c.seg, slot = p.slot_idx[b];
-    const float d = p.decay[(long long)h * p.decay_s];
-    const bool decay_ok = p.decay_is_log ? d <= 0.0f : (d >= 0.0f && d <= 1.0f);
-    if (n == 0 || slot < 0 || slot >= p.max_slots || !decay_ok || (p.max_len > 0 && s_len[b] > p.max_len)) return;
-    const float lam = power(p.decay_is_log ? d * 1.44269504088896340736f : log2f(d), c.seg);
+    const float lg2 = log2_lambda(p, h);
+    if (n <= 0 || slot < 0 || slot >= p.max_slots || isnan(lg2) || (p.max_len > 0 && s_len[b] > p.max_len)) return;
+    const float lam = power(lg2, c.seg);
     const int i = (blockIdx.x * 256 + threadIdx.x) * 4;  // V is a multiple of 16: four columns of one row
     if (i >= p.K * p.V) return;
     const int k = i / p.V, v = i - k * p.V;
@@ -870,6 +941,15 @@ bool encode(EncodeFn fn, CUtensorMap *map, const void *base, int dim, int heads,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A bfloat16 pool [slots, nv, K, V] in boxes of one head's 128 columns.
+bool encode_pool(EncodeFn fn, CUtensorMap *map, const LaParams &p) {
+    const cuuint64_t dims[4] = {(cuuint64_t)p.V, (cuuint64_t)p.K, (cuuint64_t)p.nv, (cuuint64_t)p.max_slots};
+    const cuuint64_t strides[3] = {(cuuint64_t)p.st_k * 2, (cuuint64_t)p.st_head * 2, (cuuint64_t)p.st_slot * 2};
+    const cuuint32_t box[4] = {128, p.K > 64 ? 128u : 64u, 1, 1}, one[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, p.state, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename ST, int KP> cudaError_t go(ChunkParams c, const CUtensorMap *m, cudaStream_t s) {
     static LaunchCache cache;
     LaunchInfo li;
@@ -886,11 +966,11 @@ template <typename ST, int KP> cudaError_t go(ChunkParams c, const CUtensorMap *
     const long long rows = c.seg ? p.batch + p.T / c.seg : p.batch;
     const unsigned grid = (unsigned)(rows * per < li.sms ? rows * per : li.sms);
     if (c.seg) {
-        k_la_chunk<ST, KP, true><<<grid, kThreads, smem, s>>>(c, m[0], m[1], m[2]);
+        k_la_chunk<ST, KP, true><<<grid, kThreads, smem, s>>>(c, m[0], m[1], m[2], m[3]);
         const dim3 jg((unsigned)((p.K * p.V + 1023) / 1024), (unsigned)p.nv, (unsigned)p.batch);
         k_la_join<ST><<<jg, 256, 0, s>>>(c);
     }
-    k_la_chunk<ST, KP, false><<<grid, kThreads, smem, s>>>(c, m[0], m[1], m[2]);
+    k_la_chunk<ST, KP, false><<<grid, kThreads, smem, s>>>(c, m[0], m[1], m[2], m[3]);
     return cudaGetLastError();
 }
 
@@ -899,10 +979,11 @@ template <typename ST, int KP> cudaError_t go(ChunkParams c, const CUtensorMap *
 cudaError_t launch_la_chunk(const LaParams &p, bool state_bf16, int seg, void *ws, cudaStream_t s, bool *used) {
     *used = false;
     const EncodeFn fn = encode_fn();
-    CUtensorMap m[3];
+    CUtensorMap m[4] = {};
     if (!fn || !encode(fn, &m[0], p.q, p.K, p.nk, p.T, p.q_hs, p.q_ts) ||
         !encode(fn, &m[1], p.k, p.K, p.nk, p.T, p.k_hs, p.k_ts) || !encode(fn, &m[2], p.v, p.V, p.nv, p.T, p.v_hs, p.v_ts))
         return cudaSuccess;
+    if (state_bf16 && !seg && !encode_pool(fn, &m[3], p)) return cudaSuccess;
     *used = true;
     const ChunkParams c{p, seg, static_cast<float *>(ws), FastDiv((unsigned)(p.nv * p.tiles)),
                         FastDiv((unsigned)p.tiles)};
