@@ -62,7 +62,7 @@ constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 192, kColDS = 256, kColS = 
 
 enum Bar {
     kLoaded = 0, kStageFree = kLoaded + kStages, kPFull = kStageFree + kStages, kPFree = kPFull + 2, kPtFull = kPFree + 2, kSFull, kDsFull = kSFull + 2,
-    kDsFree = kDsFull + 2, kKtFull, kOFull = kKtFull + 2, kOFree = kOFull + 2, kStateIn, kStateRead, kDrain, kBars
+    kDsFree = kDsFull + 2, kKtFull, kOFull = kKtFull + 2, kOFree = kOFull + 2, kStateIn, kStateTurn, kDrain, kBars
 };
 
 struct Smem {
@@ -76,7 +76,8 @@ struct Smem {
     int first[kMaxRows + 1];                                      // a ranked row's first segment
     float lg2[kMaxHeads];                                         // log2 lambda, NaN where the decay is bad
     uint32_t tmem;
-    int gave_up, state_loads;
+    int gave_up, state_loads, next_len;
+    float next_lg2;
 };
 static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory");
 
@@ -278,15 +279,15 @@ template <int KP, bool ST2, bool STATES> struct Loader {  // ST2: a bfloat16 poo
     // three chunks' time: 4 lanes a key index, 128 bytes of it each.
     __device__ void fetch_state() {
         const LaParams &p = x.c.p;
-        const int lane = threadIdx.x & 31, bytes = min(128, p.V - u.tile * 128) * 4;
+        const int lane = threadIdx.x & 31, es = x.c.seg || !ST2 ? 4 : 2, bytes = min(128, p.V - u.tile * 128) * es;
         const char *from;
         long long step;
         if (x.c.seg) {
             from = reinterpret_cast<const char *>(x.c.ws + ((long long)u.x * p.nv + u.h) * p.K * p.V + u.tile * 128);
             step = (long long)p.V * 4;
         } else {
-            from = static_cast<const char *>(p.state) + ((long long)u.slot * p.st_slot + (long long)u.h * p.st_head + u.tile * 128) * 4;
-            step = p.st_k * 4;
+            from = static_cast<const char *>(p.state) + ((long long)u.slot * p.st_slot + (long long)u.h * p.st_head + u.tile * 128) * es;
+            step = p.st_k * es;
         }
         const int at = (lane & 3) * 128;
         if (at < bytes)
@@ -299,7 +300,7 @@ template <int KP, bool ST2, bool STATES> struct Loader {  // ST2: a bfloat16 poo
         while (more && j >= u.chunks) {
             more = walk.next(u, false);
             j = 0;
-            if (!STATES && more && u.chunks > 0 && (!ST2 || x.c.seg)) fetch_state();
+            if (!STATES && more && u.chunks > 0) fetch_state();
         }
         if (!more) return true;
         const int s = g % kStages;
@@ -490,96 +491,121 @@ template <int KP, int PARTS, bool STATES> __device__ void role_keys(const Ctx &x
     }
 }
 
-// The state: lane = value index, 64 of its key indices in a thread's
-// registers (warps 0-3: 0..63, warps 4-7: 64..127).  The states of a bfloat16
-// pool come and go through a 32 KiB buffer by TMA: while a unit is computed the
-// next one's start state comes in; between units each thread takes its elements
-// of that and puts the finished ones in their places, and they leave.  Read and
-// written from here instead, a unit of one chunk took 7 us, most of it waiting.
+// The state: lane = value index, 64 of its key indices in a thread's registers
+// (warps 0-3: 0..63, warps 4-7: 64..127).
+struct StateRole {
+    int half, v;
+    uint32_t lanes;
+    bool mine;
+    template <int KP> __device__ static StateRole of(int warp, int lane) {
+        return {warp >> 2, (warp & 3) * 32 + lane, (uint32_t)((warp & 3) * 32) << 16, (warp >> 2) * 64 < KP};
+    }
+};
+
+// A unit's chunks; false where a wait gave up.
+template <bool STATES> __device__ __forceinline__ bool state_chunks(const Ctx &x, const StateRole &r, float2 (&s)[32], unsigned &g, int len, float lg2) {
+    const float lam_c = power(lg2, kC);
+    for (int at = 0; at < len; at += kC, ++g) {
+        if (!STATES) {
+            // the start state as matrix operand, in one of two buffers
+            if (g > 1 && !x.wait(kOFull + (g & 1), (g >> 1) - 1)) return false;  // the product that read it last is done
+            if (r.mine) {
+                fence_after();
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t h[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) h[e] = pack_bf16(s[16 * i + e]);
+                    tmem_st16(x.tmem + r.lanes + kColS + (g & 1) * 64 + r.half * 32 + i * 16, h);
+                }
+                wait_st();
+                fence_before();
+            }
+            x.arrive(kSFull + (g & 1));
+        }
+        const float lam_n = len - at >= kC ? lam_c : power(lg2, len - at);
+        if (!x.wait(kDsFull + (g & 1), g >> 1)) return false;
+        if (r.mine) {
+            fence_after();
+            const float2 l2 = make_float2(lam_n, lam_n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t d[16];
+                tmem_ld16(x.tmem + r.lanes + kColDS + r.half * 64 + i * 16, d);
+                wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    s[8 * i + e] = __ffma2_rn(l2, s[8 * i + e],
+                                              make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
+            }
+            fence_before();
+        }
+        x.arrive(kDsFree);
+    }
+    return true;
+}
+
+// A bfloat16 pool's states come and go through a 32 KiB buffer by TMA: while a
+// unit is computed the next one's start state comes in; between units each
+// thread takes its elements of that and puts the finished ones in their places,
+// and they leave (role_out issues the copies, having time to wait for them, and
+// says what the next unit is).  Written from the registers instead, a state's
+// 64 stores a thread took 6000 cycles of the 8500 of a unit of one chunk:
+// instructions that run once a unit come from far away.
+template <int KP> __device__ void role_state_staged(const Ctx &x, int warp, int lane) {
+    const StateRole r = StateRole::of<KP>(warp, lane);
+    const uint32_t buf = x.base + (uint32_t)offsetof(Smem, kt) + 2 * kTile + (r.half * 64 * 128 + r.v) * 2;  // [KP][128]
+    unsigned g = 0;
+    float2 s[32] = {};
+    for (unsigned units = 0;; ++units) {
+        if (!x.wait(kStateIn, units)) return;
+        const int len = (int)uniform((uint32_t)x.sm.next_len);
+        const float lg2 = x.sm.next_lg2;
+        if (r.mine) {  // what lies outside the pool's rows and columns came in as zero; the first time nothing finished goes out
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) exchange_bf16(buf + 2 * i * 256, s[i], s[i + 1], s[i + 2], s[i + 3]);
+        }
+        fence_async_smem();
+        x.arrive(kStateTurn);
+        if (len == 0 || !state_chunks<false>(x, r, s, g, len, lg2)) return;
+    }
+}
+
+// Other states: a float32 pool, the segments' start states, and the segments' own (STATES).
 template <typename ST, int KP, bool STATES> __device__ void role_state(const Ctx &x, int warp, int lane) {
     const LaParams &p = x.c.p;
-    const int quad = warp & 3, half = warp >> 2, v = quad * 32 + lane;
-    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const bool mine = half * 64 < KP;
-    const bool staged = sizeof(ST) == 2 && !STATES && !x.c.seg;
-    const ST *const buf = reinterpret_cast<const ST *>(x.sm.kt + 2 * kTile) + half * 64 * 128 + v;  // [KP][128]
+    const StateRole r = StateRole::of<KP>(warp, lane);
     Walk<STATES> walk(x.c, x.sm);
     Unit u;
-    unsigned g = 0, units = 0;
+    unsigned g = 0;
     float2 s[32];
     while (walk.next(u, false)) {
         if (u.chunks == 0) continue;
-        const bool on = mine && u.tile * 128 + v < p.V;
-        const int k0 = half * 64, kn = min(64, p.K - k0);
-        ST *pool = static_cast<ST *>(p.state) + (long long)u.slot * p.st_slot + (long long)u.h * p.st_head + u.tile * 128 + v;
-        float *ws = x.c.ws + ((long long)u.x * p.nv + u.h) * p.K * p.V + u.tile * 128 + v;
-        if (staged) {
-            if (!x.wait(kStateIn, units)) return;
-            if (mine) {  // what lies outside the pool's rows and columns came in as zero
+        const bool on = r.mine && u.tile * 128 + r.v < p.V;
+        const int k0 = r.half * 64, kn = min(64, p.K - k0);
+        ST *pool = static_cast<ST *>(p.state) + (long long)u.slot * p.st_slot + (long long)u.h * p.st_head + u.tile * 128 + r.v;
+        float *ws = x.c.ws + ((long long)u.x * p.nv + u.h) * p.K * p.V + u.tile * 128 + r.v;
+        // in groups of 16 key indices (K is a multiple of 16), each asked for at once
 #pragma unroll
-                for (int i = 0; i < 32; ++i) s[i] = make_float2(to_f32(buf[2 * i * 128]), to_f32(buf[(2 * i + 1) * 128]));
-            }
-            x.arrive(kStateRead);
-        } else {
-            // in groups of 16 key indices (K is a multiple of 16), each asked for at once
+        for (int i = 0; i < 32; ++i) s[i] = make_float2(0.0f, 0.0f);
+        if (!STATES && on) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = make_float2(0.0f, 0.0f);
-            if (!STATES && on) {
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (16 * b >= kn) break;
-                    if (x.c.seg) {
-                        const float *from = ws + (long long)(k0 + 16 * b) * p.V;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) s[8 * b + i] = make_float2(from[2 * i * p.V], from[(2 * i + 1) * p.V]);
-                    } else if constexpr (sizeof(ST) == 4) {
-                        const float *from = pool + (long long)(k0 + 16 * b) * p.st_k;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) s[8 * b + i] = make_float2(from[2 * i * p.st_k], from[(2 * i + 1) * p.st_k]);
-                    }
+            for (int b = 0; b < 4; ++b) {
+                if (16 * b >= kn) break;
+                const float *from;
+                long long step;
+                if (sizeof(ST) == 2 || x.c.seg) {
+                    from = ws + (long long)(k0 + 16 * b) * p.V;
+                    step = p.V;
+                } else {
+                    from = reinterpret_cast<const float *>(pool) + (long long)(k0 + 16 * b) * p.st_k;
+                    step = p.st_k;
                 }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[8 * b + i] = make_float2(from[2 * i * step], from[(2 * i + 1) * step]);
             }
         }
-        ++units;
-        const float lam_c = power(u.lg2, kC);
-        for (int j = 0; j < u.chunks; ++j, ++g) {
-            const int n = min(kC, u.len - j * kC);
-            if (!STATES) {
-                // the start state as matrix operand, in one of two buffers
-                if (g > 1 && !x.wait(kOFull + (g & 1), (g >> 1) - 1)) return;  // the product that read it last is done
-                if (mine) {
-                    fence_after();
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t h[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) h[e] = pack_bf16(s[16 * i + e]);
-                        tmem_st16(x.tmem + lanes + kColS + (g & 1) * 64 + half * 32 + i * 16, h);
-                    }
-                    wait_st();
-                    fence_before();
-                }
-                x.arrive(kSFull + (g & 1));
-            }
-            const float lam_n = n == kC ? lam_c : power(u.lg2, n);
-            if (!x.wait(kDsFull + (g & 1), g >> 1)) return;
-            if (mine) {
-                fence_after();
-                const float2 l2 = make_float2(lam_n, lam_n);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t d[16];
-                    tmem_ld16(x.tmem + lanes + kColDS + half * 64 + i * 16, d);
-                    wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        s[8 * i + e] = __ffma2_rn(l2, s[8 * i + e],
-                                                  make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
-                }
-                fence_before();
-            }
-            x.arrive(kDsFree);
-        }
+        if (!state_chunks<STATES>(x, r, s, g, u.len, u.lg2)) return;
         if (on && (STATES || u.last)) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
@@ -672,37 +698,60 @@ __device__ void role_scores(const Ctx &x, int warp, int lane) {
     }
 }
 
-// Loads of a bfloat16 pool's start states into their one buffer.
-template <int KP> struct StateLoads {
+// The copies of a bfloat16 pool's states, in and out of their one buffer.
+template <int KP> struct StateCopies {
     const Ctx &x;
     const CUtensorMap *map;
     Walk<false> ahead;
+    int now[3], next[3];  // tile, head, slot: of the unit being computed, and of the one whose start state is on its way
     unsigned units = 0;
-    __device__ StateLoads(const Ctx &x_, const CUtensorMap *m) : x(x_), map(m), ahead(x_.c, x_.sm) {}
+    __device__ StateCopies(const Ctx &x_, const CUtensorMap *m) : x(x_), map(m), ahead(x_.c, x_.sm) {}
+    __device__ uint32_t buf() const { return x.base + (uint32_t)offsetof(Smem, kt) + 2 * kTile; }
 
-    // The next unit's, once every thread has taken what the buffer holds; false where a wait gave up.
-    __device__ bool next() {
-        if (units > 0 && !x.wait(kStateRead, units - 1)) return false;
+    // Announces the next unit, and that there is none by a length of 0.
+    __device__ void load() {
         Unit u;
-        while (ahead.next(u, false)) {
-            if (u.chunks == 0) continue;
-            if ((threadIdx.x & 31) == 0) {
-                ++x.sm.state_loads;
+        bool more;
+        while ((more = ahead.next(u, false)) && u.chunks == 0) {
+        }
+        next[0] = u.tile;
+        next[1] = u.h;
+        next[2] = u.slot;
+        if ((threadIdx.x & 31) == 0) {
+            ++x.sm.state_loads;
+            x.sm.next_len = more ? u.len : 0;
+            x.sm.next_lg2 = u.lg2;
+            if (more) {
                 mbar_expect(x.bar(kStateIn), KP * 256);
-                tma_load4(x.base + (uint32_t)offsetof(Smem, kt) + 2 * kTile, map, u.tile * 128, 0, u.h, u.slot,
-                          x.bar(kStateIn));
+                tma_load4(buf(), map, u.tile * 128, 0, u.h, u.slot, x.bar(kStateIn));
+            } else {
+                mbar_arrive(x.bar(kStateIn));
             }
-            break;
         }
         __syncwarp();
+    }
+    // Once every thread has taken its part of the buffer and put the finished
+    // state's there, that leaves; false where a wait gave up.
+    __device__ bool store() {
+        if (!x.wait(kStateTurn, units)) return false;
+        if (units > 0 && (threadIdx.x & 31) == 0) tma_store4(map, now[0] * 128, 0, now[1], now[2], buf());
+        __syncwarp();
         ++units;
+        return true;
+    }
+    __device__ bool turn() {
+        if (!store()) return false;
+        for (int i = 0; i < 3; ++i) now[i] = next[i];
+        if ((threadIdx.x & 31) == 0) tma_stores_read();
+        __syncwarp();
+        load();
         return true;
     }
 };
 
 // The output: a warp has 32 columns of O^T, which it turns through shared
 // memory into rows of 64 bytes a token.
-template <int KP> __device__ void role_out(const Ctx &x, int warp, int lane, StateLoads<KP> *states) {
+template <int KP> __device__ void role_out(const Ctx &x, int warp, int lane, StateCopies<KP> *states) {
     const LaParams &p = x.c.p;
     uint16_t *const out = static_cast<uint16_t *>(p.out);
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
@@ -713,14 +762,14 @@ template <int KP> __device__ void role_out(const Ctx &x, int warp, int lane, Sta
     Walk<false> walk(x.c, x.sm);
     Unit u;
     unsigned g = 0;
-    if (states && !states->next()) return;
+    if (states) states->load();
     while (walk.next(u, warp == 0 && lane == 0)) {
         const int col = u.tile * 128 + warp * 32;
         if (u.skip_len && col + lane < p.V)
             for (int t = 0; t < u.skip_len; ++t)
                 out[(long long)(u.skip_t0 + t) * p.o_ts + (long long)u.h * p.o_hs + col + lane] = 0;
         if (u.chunks == 0) continue;
-        if (states && !states->next()) return;
+        if (states && !states->turn()) return;
         float2 f[8];
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
@@ -781,6 +830,7 @@ template <int KP> __device__ void role_out(const Ctx &x, int warp, int lane, Sta
             to += (long long)kC * p.o_ts;
         }
     }
+    if (states) states->store();
 }
 
 template <typename ST, int KP, bool STATES>
@@ -801,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= kStageFree && i < kStageFree + kStages) n = STATES ? 1 : 2;  // the products that read a stage last
             if (i == kPFree || i == kPFree + 1 || i == kPtFull) n = kWarpsP;
             if (i == kDrain) n = STATES ? 1 : 3;
-            if (i == kSFull || i == kSFull + 1 || i == kDsFree || i == kStateRead) n = kWarpsS;
+            if (i == kSFull || i == kSFull + 1 || i == kDsFree || i == kStateTurn) n = kWarpsS;
             if (i == kKtFull || i == kKtFull + 1) n = kWarpsK;
             if (i == kOFree) n = kWarpsO;
             mbar_init(bars + 8 * i, n);
@@ -836,16 +886,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < kWarpO) {
         regs_up<kRegsS>();
-        role_state<ST, KP, STATES>(x, warp - kWarpS, lane);
+        if (sizeof(ST) == 2 && !STATES && !c.seg)
+            role_state_staged<KP>(x, warp - kWarpS, lane);
+        else
+            role_state<ST, KP, STATES>(x, warp - kWarpS, lane);
     } else if (warp < kWarpP) {
         if (kRegsO > 80) regs_up<kRegsO>();
         if constexpr (!STATES) {
-            StateLoads<KP> states(x, &ms);
+            StateCopies<KP> states(x, &ms);
             const bool mine = warp == kWarpO && sizeof(ST) == 2 && !c.seg;
             role_out<KP>(x, warp - kWarpO, lane, mine ? &states : nullptr);
             if (mine && lane == 0 && sm.state_loads) {  // no state's copy is in flight when the CTA ends
                 volatile int never = 0;
                 mbar_wait(x.bar(kStateIn), (uint32_t)(sm.state_loads - 1) & 1u, &never);
+                tma_stores_done();
             }
         }
     } else if (warp < kWarpK) {

@@ -60,11 +60,70 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, 
         ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-// The same in 4 dimensions.
+// The same in 4 dimensions, and back.  Stores of a thread are waited for by that thread.
 __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
         ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store4(const CUtensorMap *map, int x, int y, int z, int w, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(map),
+                 "r"(x), "r"(y), "r"(z), "r"(w), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// Takes the eight bfloat16 values at a, a + 256, ... and puts the roundings of
+// x there; x becomes what was taken.  One piece, so that each value keeps its
+// register and the loads wait once.
+__device__ __forceinline__ void exchange_bf16(uint32_t a, float2 &x, float2 &y, float2 &z, float2 &w) {
+    asm volatile(
+        "{\n\t.reg .b16 p<8>, q<8>, z;\n\t.reg .b32 w;\n\tmov.b16 z, 0;\n\t"
+        "ld.shared.b16 p0, [%8+0];\n\t"
+        "ld.shared.b16 p1, [%8+256];\n\t"
+        "ld.shared.b16 p2, [%8+512];\n\t"
+        "ld.shared.b16 p3, [%8+768];\n\t"
+        "ld.shared.b16 p4, [%8+1024];\n\t"
+        "ld.shared.b16 p5, [%8+1280];\n\t"
+        "ld.shared.b16 p6, [%8+1536];\n\t"
+        "ld.shared.b16 p7, [%8+1792];\n\t"
+        "cvt.rn.bf16x2.f32 w, %1, %0;\n\t"
+        "mov.b32 {q0, q1}, w;\n\t"
+        "cvt.rn.bf16x2.f32 w, %3, %2;\n\t"
+        "mov.b32 {q2, q3}, w;\n\t"
+        "cvt.rn.bf16x2.f32 w, %5, %4;\n\t"
+        "mov.b32 {q4, q5}, w;\n\t"
+        "cvt.rn.bf16x2.f32 w, %7, %6;\n\t"
+        "mov.b32 {q6, q7}, w;\n\t"
+        "st.shared.b16 [%8+0], q0;\n\t"
+        "st.shared.b16 [%8+256], q1;\n\t"
+        "st.shared.b16 [%8+512], q2;\n\t"
+        "st.shared.b16 [%8+768], q3;\n\t"
+        "st.shared.b16 [%8+1024], q4;\n\t"
+        "st.shared.b16 [%8+1280], q5;\n\t"
+        "st.shared.b16 [%8+1536], q6;\n\t"
+        "st.shared.b16 [%8+1792], q7;\n\t"
+        "mov.b32 w, {z, p0};\n\t"
+        "mov.b32 %0, w;\n\t"
+        "mov.b32 w, {z, p1};\n\t"
+        "mov.b32 %1, w;\n\t"
+        "mov.b32 w, {z, p2};\n\t"
+        "mov.b32 %2, w;\n\t"
+        "mov.b32 w, {z, p3};\n\t"
+        "mov.b32 %3, w;\n\t"
+        "mov.b32 w, {z, p4};\n\t"
+        "mov.b32 %4, w;\n\t"
+        "mov.b32 w, {z, p5};\n\t"
+        "mov.b32 %5, w;\n\t"
+        "mov.b32 w, {z, p6};\n\t"
+        "mov.b32 %6, w;\n\t"
+        "mov.b32 w, {z, p7};\n\t"
+        "mov.b32 %7, w;\n\t"
+        "}"
+        : "+f"(x.x), "+f"(x.y), "+f"(y.x), "+f"(y.y), "+f"(z.x), "+f"(z.y), "+f"(w.x), "+f"(w.y)
+        : "r"(a)
         : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
