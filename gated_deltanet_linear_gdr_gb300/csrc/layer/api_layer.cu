@@ -43,8 +43,8 @@ int check_linattn_sizes(const gdr_linattn_args *a, const char *fn) {
     if (a->total_tokens < 0) return fail(GDR_ERR_INVALID_ARG, "%s: total_tokens < 0", fn);
     if (a->total_tokens >= (1ll << 31))
         return fail(GDR_ERR_UNSUPPORTED, "%s: total_tokens must be < 2^31", fn);
-    if ((int64_t)a->batch * a->nv * 2 >= (1ll << 31))
-        return fail(GDR_ERR_UNSUPPORTED, "%s: batch * nv must be < 2^30", fn);
+    if ((int64_t)a->batch * a->nv * 4 >= (1ll << 31))  // units: up to four column tiles a head
+        return fail(GDR_ERR_UNSUPPORTED, "%s: batch * nv must be < 2^29", fn);
     return GDR_OK;
 }
 
@@ -82,12 +82,12 @@ int check_linattn(const gdr_linattn_args *a, const char *fn) {
     return GDR_OK;
 }
 
-// Rows of at most this many tokens (by the caller's bound) take the recurrent form.
-constexpr long long kStepRowMax = 16;
+// Rows of at most this many tokens (by the caller's bound) are one chunk of k_la_small.cu.
+constexpr long long kShortRowMax = 16;
 
 bool takes_chunks(const gdr_linattn_args *a, bool tok_vec) {
     return a->token_dtype == GDR_BF16 && tok_vec && a->total_tokens > 0 &&
-           (a->max_row_len <= 0 || a->max_row_len > kStepRowMax);
+           (a->max_row_len <= 0 || a->max_row_len > kShortRowMax);
 }
 
 bool token_vectors(const gdr_linattn_args *a) {
@@ -193,6 +193,8 @@ int gdr_linattn_fwd(const gdr_linattn_args *a, void *stream) {
     unsigned *st = nullptr;
     if ((rc = gdr::api_status(&st))) return rc;
     const gdr::LaParams p = lower(a, st);
+    if (a->token_dtype == GDR_BF16 && p.tok_vec && p.max_len > 1 && p.max_len <= kShortRowMax)
+        return launched(gdr::launch_la_small(p, a->state_dtype == GDR_BF16, static_cast<cudaStream_t>(stream)), fn);
     if (takes_chunks(a, p.tok_vec)) {
         int seg = plan_segments(a);
         if (seg && (!a->workspace || a->workspace_bytes < segments_bytes(a, seg))) seg = 0;

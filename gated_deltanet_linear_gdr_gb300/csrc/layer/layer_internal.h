@@ -39,6 +39,10 @@ struct LaParams {
 // tokens, short rows and float32 tokens run on.
 cudaError_t launch_la_step(const LaParams &p, bool tok_bf16, bool state_bf16, cudaStream_t s);
 
+// Chunked form in warp-level matrix instructions: bfloat16 tokens whose rows are
+// 16-byte vectors; for short rows and small heads.
+cudaError_t launch_la_small(const LaParams &p, bool state_bf16, cudaStream_t s);
+
 // Chunked form on the tensor cores: bfloat16 tokens whose rows are 16-byte
 // vectors.  seg > 0 cuts rows into segments of that many tokens (a multiple of
 // 64; batch <= 32) whose start states are worked out first, in ws.  Launches
