@@ -9,9 +9,9 @@
 // A warp keeps its columns of S, transposed (value index = row), as float32
 // accumulators.  Their layout is that of an A operand once rounded, and P's is
 // that of a B operand, so that everything chains in registers; tokens and
-// states pass through shared memory.  Rounding as in k_la_chunk.cu: P~ and the
-// state as operand once to bfloat16, V~ in two (bfloat16 pool) or three parts,
-// the state itself never.
+// states pass through shared memory.  Operands made here go in as two bfloat16
+// parts (V~ for a float32 pool as three), which keep 16 (24) bits: nothing is
+// rounded to fewer but the results.
 //
 // Bound: HBM, a state in and out for a few tokens.  A CTA asks for its next
 // unit's state and tokens before it computes the current one's, two of them a
@@ -60,6 +60,8 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 }
 __device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// The rounding of what the pair w leaves of (x, y).
+__device__ __forceinline__ uint32_t rest(uint32_t w, float x, float y) { return pack(x - low(w), y - high(w)); }
 __device__ __forceinline__ float power(float lg2, int n) { return n == 0 ? 1.0f : exp2f(lg2 * (float)n); }
 
 // Shared memory of a CTA: two units' tokens and states, one unit's output.
@@ -214,10 +216,16 @@ __global__ void __launch_bounds__(Lay<ST, KP, VT, MT>::THREADS, 2) k_la_small(co
                     const uint32_t a[4] = {pack(x[0], x[1]), pack(x[2], x[3]), pack(y[0], y[1]), pack(y[2], y[3])};
                     mma(o[mt][0], a, q[0], q[2]);
                     mma(o[mt][1], a, q[1], q[3]);
+                    if constexpr (sizeof(ST) == 4) {  // a bfloat16 pool's start state is exact as it is
+                        const uint32_t e[4] = {rest(a[0], x[0], x[1]), rest(a[1], x[2], x[3]), rest(a[2], y[0], y[1]),
+                                               rest(a[3], y[2], y[3])};
+                        mma(o[mt][0], e, q[0], q[2]);
+                        mma(o[mt][1], e, q[1], q[3]);
+                    }
                 }
             }
             // P~ as B operand [j, i]: chosen where j <= i, whatever the other places hold
-            uint32_t pb[2][2];
+            uint32_t pb[2][2], pc[2][2];  // and what its rounding leaves
 #pragma unroll
             for (int ih = 0; ih < 2; ++ih)
 #pragma unroll
@@ -226,6 +234,7 @@ __global__ void __launch_bounds__(Lay<ST, KP, VT, MT>::THREADS, 2) k_la_small(co
                     const float x = gap < 0 ? 0.0f : P[jt][2 * ih] * (p.scale * power(u.lg2, gap));
                     const float y = gap < 1 ? 0.0f : P[jt][2 * ih + 1] * (p.scale * power(u.lg2, gap - 1));
                     pb[ih][jt] = pack(x, y);
+                    pc[ih][jt] = rest(pb[ih][jt], x, y);
                 }
             const float lam_n = power(u.lg2, n);
             float f[2][2], wt[2][2];  // factors of outputs, and weights of values, of tokens 8 i + c2 + e
@@ -247,6 +256,7 @@ __global__ void __launch_bounds__(Lay<ST, KP, VT, MT>::THREADS, 2) k_la_small(co
 #pragma unroll
                     for (int i = 0; i < 4; ++i) o[mt][nt][i] *= f[nt][i & 1];
                     mma(o[mt][nt], v, pb[nt][0], pb[nt][1]);
+                    mma(o[mt][nt], v, pc[nt][0], pc[nt][1]);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -254,7 +264,7 @@ __global__ void __launch_bounds__(Lay<ST, KP, VT, MT>::THREADS, 2) k_la_small(co
                     va[mt][0][i] = pack(x, y);
                     const float x1 = x - low(va[mt][0][i]), y1 = y - high(va[mt][0][i]);
                     va[mt][1][i] = pack(x1, y1);
-                    if constexpr (sizeof(ST) == 4) va[mt][2][i] = pack(x1 - low(va[mt][1][i]), y1 - high(va[mt][1][i]));
+                    if constexpr (sizeof(ST) == 4) va[mt][2][i] = rest(va[mt][1][i], x1, y1);
                 }
                 // the output, turned: blocks (columns +0, tokens +0), (+8, +0), (+0, +8), (+8, +8)
                 stm4_t(s_out + x_row * L::SO + (mt * 16 + x_col) * 2, pack(o[mt][0][0], o[mt][0][1]), pack(o[mt][0][2], o[mt][0][3]),
