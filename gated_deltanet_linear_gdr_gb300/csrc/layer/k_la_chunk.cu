@@ -42,11 +42,15 @@ using namespace tc;
 // Key channels are padded to KP = 64 or 128: TMA reads zeros past K, and zeros
 // add nothing to any of the products.
 constexpr int kC = 64;        // tokens a chunk
-constexpr int kStages = 3;
 constexpr int kSub = kC * 128;        // bytes of a 64-token x 64-channel operand block
 constexpr int kTile = 2 * kSub;       // bytes of a 64-token x 128-channel operand
-constexpr int kStage = 3 * kTile;     // Q | K | V
+// The chunks on their way in: K | V | Q, or K | V where only states are computed.
+template <bool STATES> struct Ring {
+    static constexpr int N = STATES ? 4 : 3, BYTES = (STATES ? 2 : 3) * kTile;
+};
+constexpr int kMaxStages = 4;
 constexpr int kMaxRows = 64, kMaxHeads = 64;  // rows and heads whose facts are kept in shared memory
+constexpr int kPlanned = 16;                  // rows whose units are dealt by load
 
 // Warps by role, in warpgroups of 4.  The issuers and the loader come first:
 // between ready warps the scheduler prefers the older.
@@ -57,16 +61,19 @@ constexpr int kThreads = 32 * (kWarpK + kWarpsK);
 constexpr int kRegsS = 112, kRegsO = 96, kRegsP = 80, kRegsK = 48, kRegsRest = 32;
 static_assert(2 * kRegsS + kRegsO + kRegsP + kRegsK + kRegsRest == 6 * 80, "shares");
 
+// Without output to make, the warps of P~ and O make K~ too.
+template <bool STATES> constexpr int kTeams = STATES ? 3 : 1;
+
 // tensor memory columns
 constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 192, kColDS = 256, kColS = 384;
 
 enum Bar {
-    kLoaded = 0, kStageFree = kLoaded + kStages, kPFull = kStageFree + kStages, kPFree = kPFull + 2, kPtFull = kPFree + 2, kSFull, kDsFull = kSFull + 2,
+    kLoaded = 0, kStageFree = kLoaded + kMaxStages, kPFull = kStageFree + kMaxStages, kPFree = kPFull + 2, kPtFull = kPFree + 2, kSFull, kDsFull = kSFull + 2,
     kDsFree = kDsFull + 2, kKtFull, kOFull = kKtFull + 2, kOFree = kOFull + 2, kStateIn, kStateTurn, kDrain, kBars
 };
 
 struct Smem {
-    unsigned char stage[kStages][kStage];
+    unsigned char stage[Ring<false>::N * Ring<false>::BYTES];
     unsigned char kt[4 * kTile];          // K~ but for its first part, which takes K's place, of two chunks: with two
                                           // parts it fills half of this, and the rest holds a state on its way
     unsigned char pt[kSub];               // P~^T
@@ -75,6 +82,8 @@ struct Smem {
     int row_t0[kMaxRows], row_len[kMaxRows], row_slot[kMaxRows];  // by rank: the longest row first; len -1: bad offsets
     int first[kMaxRows + 1];                                      // a ranked row's first segment
     float lg2[kMaxHeads];                                         // log2 lambda, NaN where the decay is bad
+    int rank[kPlanned];                                           // of this CTA, for each planned row
+    int planned;
     uint32_t tmem;
     int gave_up, state_loads, next_len;
     float next_lg2;
@@ -118,12 +127,14 @@ __device__ __forceinline__ float log2_lambda(const LaParams &p, int h) {
     return !ok ? __int_as_float(0x7fffffff) : p.decay_is_log ? d * 1.44269504088896340736f : log2f(d);
 }
 
-// Walks this CTA's units: positions blockIdx.x, then back and forth, so that
-// units sorted by length are dealt evenly.
+// Walks this CTA's units.  Few rows: row by row, the longest first, each row's
+// units to the CTAs with the least to do so far (plan_rows).  Otherwise
+// positions blockIdx.x, then back and forth, so that units sorted by length are
+// dealt evenly.
 template <bool STATES> struct Walk {
     const ChunkParams &c;
     const Smem &sm;
-    int i = 0;
+    int i = 0, row = 0;
     __device__ Walk(const ChunkParams &c_, const Smem &sm_) : c(c_), sm(sm_) {}
 
     // The next unit; every lane has the same, and the compiler is told so.
@@ -141,10 +152,22 @@ template <bool STATES> struct Walk {
     __device__ bool find(Unit &u, bool report) {
         const LaParams &p = c.p;
         u.t0 = u.x = u.h = u.tile = u.len = u.chunks = u.skip_len = u.slot = 0;
-        const unsigned G = gridDim.x, pos = (unsigned)i * G + ((i & 1) ? G - 1 - blockIdx.x : blockIdx.x);
-        ++i;
-        u.x = (int)c.per.div(pos);  // positions are below 2^31 and a walk ends at the first one past the units
-        const unsigned ht = pos - (unsigned)u.x * c.per.d;
+        const unsigned G = gridDim.x;
+        unsigned ht;
+        if (sm.planned) {
+            for (;; ++row, i = 0) {
+                if (row >= p.batch) return false;
+                ht = (unsigned)sm.rank[row] + (unsigned)i * G;
+                if (ht < c.per.d) break;
+            }
+            ++i;
+            u.x = row;
+        } else {
+            const unsigned pos = (unsigned)i * G + ((i & 1) ? G - 1 - blockIdx.x : blockIdx.x);
+            ++i;
+            u.x = (int)c.per.div(pos);  // positions are below 2^31 and a walk ends at the first one past the units
+            ht = pos - (unsigned)u.x * c.per.d;
+        }
         u.h = (int)c.tiles.div(ht);
         u.tile = (int)(ht - (unsigned)u.h * c.tiles.d);
         int seg_i = 0, r0, len;
@@ -224,6 +247,34 @@ __device__ __forceinline__ void plan_rows(const ChunkParams &c, Smem &sm) {
         sm.row_slot[rank] = slot;
     }
     __syncthreads();
+    // few rows, one of them long: every CTA works out the same deal.  (Back and
+    // forth alone, 8 rows of 512 to 4096 tokens x 32 heads lasted 80 chunks
+    // where 66 are possible.)
+    const int G = (int)gridDim.x;
+    const bool planned = !c.seg && B <= kPlanned && (unsigned)B * c.per.d > gridDim.x && 4 * G <= kThreads && sm.row_len[0] >= 8 * kC;
+    if (tid == 0) sm.planned = planned;
+    if (planned) {
+        int *const load = reinterpret_cast<int *>(sm.stage);  // by CTA, in chunks; nothing is on its way yet
+        const int cta = tid >> 2, part = tid & 3;             // four threads compare for a CTA
+        for (int o = tid; o < G; o += kThreads) load[o] = 0;
+        __syncthreads();
+        for (int r = 0; r < B; ++r) {
+            int n = 0;
+            if (cta < G) {
+                const int mine = load[cta];
+                for (int o = part; o < G; o += 4) n += load[o] < mine || (load[o] == mine && o < cta);
+            }
+            n += __shfl_xor_sync(0xffffffffu, n, 1);
+            n += __shfl_xor_sync(0xffffffffu, n, 2);
+            __syncthreads();
+            if (cta < G && part == 0) {
+                const int heads = (int)c.per.d, units = n < heads ? (heads - n - 1) / G + 1 : 0;
+                load[cta] += units * ((max(sm.row_len[r], 0) + kC - 1) / kC + 2);  // two chunks' time to begin and end one
+                if (cta == (int)blockIdx.x) sm.rank[r] = n;
+            }
+            __syncthreads();
+        }
+    }
     if (c.seg && tid < 32) {  // batch <= 32: one lane a row
         int end = tid < B ? max(1, (sm.row_len[tid] + c.seg - 1) / c.seg) : 0;
 #pragma unroll
@@ -253,7 +304,6 @@ struct Ctx {
     __device__ bool wait(int i, uint32_t parity) const {
         return __all_sync(0xffffffffu, mbar_wait(bar(i), parity & 1u, &sm.gave_up));
     }
-    __device__ uint32_t stage(unsigned g) const { return base + (uint32_t)(g % kStages) * kStage; }
     // one arrival for the warp, once every lane has got here
     __device__ void arrive(int i) const {
         __syncwarp();
@@ -303,20 +353,21 @@ template <int KP, bool ST2, bool STATES> struct Loader {  // ST2: a bfloat16 poo
             if (!STATES && more && u.chunks > 0) fetch_state();
         }
         if (!more) return true;
-        const int s = g % kStages;
-        if (g >= kStages && !x.wait(kStageFree + s, g / kStages - 1)) return false;
+        using R = Ring<STATES>;
+        const int s = g % R::N;
+        if (g >= R::N && !x.wait(kStageFree + s, g / R::N - 1)) return false;
         if (elect_one()) {
             const LaParams &p = x.c.p;
             constexpr int nk = KP / 64;
             const int v0 = u.tile * 128, nv = p.V - v0 > 64 ? 2 : 1, hk = u.h / p.r, t = u.t0 + j * kC;
-            const uint32_t dst = x.stage(g), full = x.bar(kLoaded + s);
+            const uint32_t dst = x.base + s * R::BYTES, full = x.bar(kLoaded + s);
             mbar_expect(full, (uint32_t)((STATES ? 1 : 2) * nk + nv) * kSub);
 #pragma unroll
             for (int i = 0; i < nk; ++i) {
-                tma_load3(dst + kTile + i * kSub, mk, i * 64, hk, t, full);
-                if (!STATES) tma_load3(dst + i * kSub, mq, i * 64, hk, t, full);
+                tma_load3(dst + i * kSub, mk, i * 64, hk, t, full);
+                if (!STATES) tma_load3(dst + 2 * kTile + i * kSub, mq, i * 64, hk, t, full);
             }
-            for (int i = 0; i < nv; ++i) tma_load3(dst + 2 * kTile + i * kSub, mv, v0 + i * 64, u.h, t, full);
+            for (int i = 0; i < nv; ++i) tma_load3(dst + kTile + i * kSub, mv, v0 + i * 64, u.h, t, full);
         }
         __syncwarp();
         ++g;
@@ -326,8 +377,8 @@ template <int KP, bool ST2, bool STATES> struct Loader {  // ST2: a bfloat16 poo
     // No copy is in flight when the CTA ends.
     __device__ void drain() {
         volatile int never = 0;
-        for (unsigned o = g > kStages ? g - kStages : 0; o < g; ++o)
-            mbar_wait(x.bar(kLoaded + o % kStages), (o / kStages) & 1u, &never);
+        constexpr unsigned N = Ring<STATES>::N;
+        for (unsigned o = g > N ? g - N : 0; o < g; ++o) mbar_wait(x.bar(kLoaded + o % N), (o / N) & 1u, &never);
     }
 };
 
@@ -349,61 +400,75 @@ __device__ __forceinline__ void drain_mma(const Ctx &x) {
 
 // P^T = K Q^T
 template <int KP> __device__ void role_mma_scores(const Ctx &x) {
+    using R = Ring<false>;
     const uint32_t id = idesc_bf16(64, kC, false, false);
     const uint64_t d_km = desc128(x.base, 16, 1024);  // stage 0, K-major
     const unsigned total = count_chunks<false>(x);
     for (unsigned g = 0; g < total; ++g) {
         // the buffer has been read, and the last product into it has been seen by both its waiters
         if (g > 1 && (!x.wait(kPFree + (g & 1), (g >> 1) - 1) || !x.wait(kKtFull + (g & 1), (g >> 1) - 1))) break;
-        if (!x.wait(kLoaded + g % kStages, g / kStages)) break;
+        if (!x.wait(kLoaded + g % R::N, g / R::N)) break;
         fence_after();
-        const uint32_t me = elect_one(), st = uniform(g % kStages), odd = uniform(g & 1);
-        const uint64_t q = d_km + (st * kStage >> 4);
-        mma_ss_k<KP / 16>(me, x.tmem + kColP + odd * kC, q + (kTile >> 4), q, id, kSub);
+        const uint32_t me = elect_one(), st = uniform(g % R::N), odd = uniform(g & 1);
+        const uint64_t k = d_km + (st * R::BYTES >> 4), q = k + (2 * kTile >> 4);
+        mma_ss_k<KP / 16>(me, x.tmem + kColP + odd * kC, k, q, id, kSub);
         mma_commit(me, x.bar(kPFull) + 8 * odd);
     }
     drain_mma(x);
 }
 
-// V^T K~
+// V^T K~.  For a segment's own state (STATES) the weights count to the segment's
+// end and all of its chunks add up in tensor memory; else each chunk's is read.
 template <int KP, int PARTS, bool STATES> __device__ void role_mma_state(const Ctx &x) {
+    using R = Ring<STATES>;
     const uint32_t id = idesc_bf16(128, KP, true, true);
     const uint64_t d_mn = desc128(x.base, kSub, 1024);  // stage 0, MN-major
     const uint64_t d_kt = desc128(x.base + (uint32_t)offsetof(Smem, kt), kSub, 1024);
-    const unsigned total = count_chunks<STATES>(x);
-    for (unsigned g = 0; g < total; ++g) {
-        if (!x.wait(kLoaded + g % kStages, g / kStages) || !x.wait(kKtFull + (g & 1), g >> 1) ||
-            (g > 0 && !x.wait(kDsFree, g - 1)))
-            break;
-        fence_after();
-        const uint32_t me = elect_one(), st = uniform(g % kStages), odd = uniform(g & 1);
-        const uint64_t k = d_mn + ((st * kStage + kTile) >> 4), v = k + (kTile >> 4), kt = d_kt + (odd * (PARTS - 1) * kTile >> 4);
-        mma_ss_mn64<false>(me, x.tmem + kColDS, v, k, id);
-        mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt, id);
-        if (PARTS == 3) mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt + (kTile >> 4), id);
-        mma_commit(me, x.bar(kDsFull) + 8 * odd);
-        mma_commit(me, x.bar(kStageFree) + 8 * st);
+    Walk<STATES> walk(x.c, x.sm);
+    Unit u;
+    unsigned g = 0, reads = 0;
+    while (walk.next(u, false)) {
+        for (int j = 0; j < u.chunks; ++j, ++g) {
+            const bool fresh = !STATES || j == 0;
+            if (!x.wait(kLoaded + g % R::N, g / R::N) || !x.wait(kKtFull + (g & 1), g >> 1)) return;
+            if (fresh) {
+                if (reads > 0 && !x.wait(kDsFree, reads - 1)) return;
+                ++reads;
+            }
+            fence_after();
+            const uint32_t me = elect_one(), st = uniform(g % R::N), odd = uniform(g & 1);
+            const uint64_t k = d_mn + (st * R::BYTES >> 4), v = k + (kTile >> 4), kt = d_kt + (odd * (PARTS - 1) * kTile >> 4);
+            if (fresh)
+                mma_ss_mn64<false>(me, x.tmem + kColDS, v, k, id);
+            else
+                mma_ss_mn64<true>(me, x.tmem + kColDS, v, k, id);
+            mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt, id);
+            if (PARTS == 3) mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt + (kTile >> 4), id);
+            mma_commit(me, x.bar(kDsFull) + 8 * odd);
+            if (STATES && j + 1 == u.chunks) mma_commit(me, x.bar(kOFull));
+            mma_commit(me, x.bar(kStageFree) + 8 * st);
+        }
     }
-    drain_mma(x);
 }
 
 // S0^T Q^T and V^T P~^T
 template <int KP> __device__ void role_mma_out(const Ctx &x) {
+    using R = Ring<false>;
     const uint32_t id1 = idesc_bf16(128, kC, false, false), id2 = idesc_bf16(128, kC, true, true);
-    const uint64_t d_km = desc128(x.base, 16, 1024), d_v = desc128(x.base + 2 * kTile, kSub, 1024);
+    const uint64_t d_km = desc128(x.base + 2 * kTile, 16, 1024), d_v = desc128(x.base + kTile, kSub, 1024);
     const uint64_t d_pt = desc128(x.base + (uint32_t)offsetof(Smem, pt), kSub, 1024);
     const unsigned total = count_chunks<false>(x);
     for (unsigned g = 0; g < total; ++g) {
-        if (!x.wait(kLoaded + g % kStages, g / kStages) || (g > 0 && !x.wait(kOFree, g - 1)) ||
+        if (!x.wait(kLoaded + g % R::N, g / R::N) || (g > 0 && !x.wait(kOFree, g - 1)) ||
             !x.wait(kSFull + (g & 1), g >> 1))
             break;
         fence_after();
-        const uint32_t me = elect_one(), st = uniform(g % kStages), odd = uniform(g & 1);
-        const uint64_t q = d_km + (st * kStage >> 4);
+        const uint32_t me = elect_one(), st = uniform(g % R::N), odd = uniform(g & 1);
+        const uint64_t q = d_km + (st * R::BYTES >> 4);
         mma_ts_k<KP / 16>(me, x.tmem + kColO1, x.tmem + kColS + odd * 64, q, id1, kSub);
         if (!x.wait(kPtFull, g)) break;
         fence_after();
-        mma_ss_mn64<false>(me, x.tmem + kColO2, d_v + (st * kStage >> 4), d_pt, id2);
+        mma_ss_mn64<false>(me, x.tmem + kColO2, d_v + (st * R::BYTES >> 4), d_pt, id2);
         mma_commit(me, x.bar(kOFull) + 8 * odd);
         mma_commit(me, x.bar(kStageFree) + 8 * st);
     }
@@ -424,7 +489,8 @@ __device__ __forceinline__ void clear_tail(unsigned char *v, int n, int nv, int 
 //     hi = rn(k a),  k a - hi exactly (it has 8 bits),  mid = rn(k b + (k a - hi)),
 // three instructions a pair, off by 2^-17 of the product.  Three parts in
 // float32, each the rounding of what the ones before leave.
-template <int KP, int PARTS, bool STATES> __device__ void role_keys(const Ctx &x, int warp, int lane) {
+// `team` of TEAMS warpgroups takes the 16-token blocks team, team + TEAMS, ..
+template <int KP, int PARTS, bool STATES, int TEAMS> __device__ void role_keys(const Ctx &x, int team, int warp, int lane) {
     const LaParams &p = x.c.p;
     const int tid = warp * 32 + lane, row = tid / 8;
     Walk<STATES> walk(x.c, x.sm);
@@ -432,21 +498,24 @@ template <int KP, int PARTS, bool STATES> __device__ void role_keys(const Ctx &x
     unsigned g = 0;
     while (walk.next(u, false)) {
         const int nv = p.V - u.tile * 128 > 64 ? 2 : 1;
-        const float lam16 = power(u.lg2, 16);
-        float w3 = 0.0f;  // weight of this thread's last token
+        const int last = (3 - team) / TEAMS * TEAMS + team;  // this team's last block
+        const float lam_b = power(u.lg2, 16 * TEAMS);
+        float w_last = 0.0f;  // weight of this thread's token there
         for (int j = 0; j < u.chunks; ++j, ++g) {
             const int n = min(kC, u.len - j * kC);
-            if (j == 0 || n < kC) w3 = power(u.lg2, max(n - 1 - (48 + row), 0));
-            if (!x.wait(kLoaded + g % kStages, g / kStages)) return;
-            unsigned char *stage = x.sm.stage[g % kStages];
-            if (__builtin_expect(n < kC, 0)) clear_tail(stage + 2 * kTile, n, nv, tid, 32 * kWarpsK);
+            if (STATES || j == 0 || n < kC)
+                w_last = power(u.lg2, max((STATES ? u.len - j * kC : n) - 1 - (16 * last + row), 0));
+            using R = Ring<STATES>;
+            if (!x.wait(kLoaded + g % R::N, g / R::N)) return;
+            unsigned char *stage = x.sm.stage + g % R::N * R::BYTES;
+            if (__builtin_expect(n < kC, 0)) clear_tail(stage + kTile, n, nv, tid, 32 * kWarpsK);
             if (!STATES && !x.wait(kPFull + (g & 1), g >> 1)) return;           // K Q^T has read K
             if (g > 1 && !x.wait(kDsFull + (g & 1), (g >> 1) - 1)) return;  // and the product before last its K~
             unsigned char *const rest = x.sm.kt + (g & 1) * (PARTS - 1) * kTile;
             // small loops: the roles share the instruction caches
-            float w = w3;
+            float w = w_last;
 #pragma unroll 1
-            for (int i = 3; i >= 0; --i) {
+            for (int i = last; i >= 0; i -= TEAMS) {
                 const int back = n - 1 - (i * 16 + row);
                 if (n < kC) w = back < 0 ? 0.0f : power(u.lg2, back);
                 const __nv_bfloat162 wa = __float2bfloat162_rn(w);
@@ -454,7 +523,7 @@ template <int KP, int PARTS, bool STATES> __device__ void role_keys(const Ctx &x
 #pragma unroll
                 for (int sub = 0; sub < KP / 64; ++sub) {
                     const int at = sub * kSub + tid * 16 + i * 2048;
-                    uint4 *const here = reinterpret_cast<uint4 *>(stage + kTile + at);
+                    uint4 *const here = reinterpret_cast<uint4 *>(stage + at);
                     uint4 raw = *here;
                     if (back < 0) raw = make_uint4(0, 0, 0, 0);
                     const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -483,7 +552,7 @@ template <int KP, int PARTS, bool STATES> __device__ void role_keys(const Ctx &x
                         *reinterpret_cast<uint4 *>(rest + (part - 1) * kTile + at) =
                             make_uint4(o[part][0], o[part][1], o[part][2], o[part][3]);
                 }
-                w *= lam16;
+                w *= lam_b;
             }
             fence_async_smem();
             x.arrive(kKtFull + (g & 1));
@@ -502,45 +571,48 @@ struct StateRole {
     }
 };
 
+// s = lam s + what V^T K~ has left in tensor memory.
+__device__ __forceinline__ void state_add(const Ctx &x, const StateRole &r, float2 (&s)[32], float lam) {
+    if (r.mine) {
+        fence_after();
+        const float2 l2 = make_float2(lam, lam);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t d[16];
+            tmem_ld16(x.tmem + r.lanes + kColDS + r.half * 64 + i * 16, d);
+            wait_ld();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                s[8 * i + e] = __ffma2_rn(l2, s[8 * i + e],
+                                          make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
+        }
+        fence_before();
+    }
+    x.arrive(kDsFree);
+}
+
 // A unit's chunks; false where a wait gave up.
-template <bool STATES> __device__ __forceinline__ bool state_chunks(const Ctx &x, const StateRole &r, float2 (&s)[32], unsigned &g, int len, float lg2) {
+__device__ __forceinline__ bool state_chunks(const Ctx &x, const StateRole &r, float2 (&s)[32], unsigned &g, int len, float lg2) {
     const float lam_c = power(lg2, kC);
     for (int at = 0; at < len; at += kC, ++g) {
-        if (!STATES) {
-            // the start state as matrix operand, in one of two buffers
-            if (g > 1 && !x.wait(kOFull + (g & 1), (g >> 1) - 1)) return false;  // the product that read it last is done
-            if (r.mine) {
-                fence_after();
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t h[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) h[e] = pack_bf16(s[16 * i + e]);
-                    tmem_st16(x.tmem + r.lanes + kColS + (g & 1) * 64 + r.half * 32 + i * 16, h);
-                }
-                wait_st();
-                fence_before();
-            }
-            x.arrive(kSFull + (g & 1));
-        }
-        const float lam_n = len - at >= kC ? lam_c : power(lg2, len - at);
-        if (!x.wait(kDsFull + (g & 1), g >> 1)) return false;
+        // the start state as matrix operand, in one of two buffers
+        if (g > 1 && !x.wait(kOFull + (g & 1), (g >> 1) - 1)) return false;  // the product that read it last is done
         if (r.mine) {
             fence_after();
-            const float2 l2 = make_float2(lam_n, lam_n);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t d[16];
-                tmem_ld16(x.tmem + r.lanes + kColDS + r.half * 64 + i * 16, d);
-                wait_ld();
+            for (int i = 0; i < 2; ++i) {
+                uint32_t h[16];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    s[8 * i + e] = __ffma2_rn(l2, s[8 * i + e],
-                                              make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
+                for (int e = 0; e < 16; ++e) h[e] = pack_bf16(s[16 * i + e]);
+                tmem_st16(x.tmem + r.lanes + kColS + (g & 1) * 64 + r.half * 32 + i * 16, h);
             }
+            wait_st();
             fence_before();
         }
-        x.arrive(kDsFree);
+        x.arrive(kSFull + (g & 1));
+        const float lam_n = len - at >= kC ? lam_c : power(lg2, len - at);
+        if (!x.wait(kDsFull + (g & 1), g >> 1)) return false;
+        state_add(x, r, s, lam_n);
     }
     return true;
 }
@@ -567,7 +639,7 @@ template <int KP> __device__ void role_state_staged(const Ctx &x, int warp, int 
         }
         fence_async_smem();
         x.arrive(kStateTurn);
-        if (len == 0 || !state_chunks<false>(x, r, s, g, len, lg2)) return;
+        if (len == 0 || !state_chunks(x, r, s, g, len, lg2)) return;
     }
 }
 
@@ -605,7 +677,12 @@ template <typename ST, int KP, bool STATES> __device__ void role_state(const Ctx
                 for (int i = 0; i < 8; ++i) s[8 * b + i] = make_float2(from[2 * i * step], from[(2 * i + 1) * step]);
             }
         }
-        if (!state_chunks<STATES>(x, r, s, g, u.len, u.lg2)) return;
+        if constexpr (STATES) {  // all of the segment's chunks have added up
+            if (!x.wait(kOFull, g++)) return;
+            state_add(x, r, s, 0.0f);
+        } else {
+            if (!state_chunks(x, r, s, g, u.len, u.lg2)) return;
+        }
         if (on && (STATES || u.last)) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
@@ -685,7 +762,7 @@ __device__ void role_scores(const Ctx &x, int warp, int lane) {
                     if (row0 >= n) h[2 * b] = 0;
                     if (row0 + 8 >= n) h[2 * b + 1] = 0;
                 }
-                clear_tail(x.sm.stage[g % kStages] + 2 * kTile, n, p.V - u.tile * 128 > 64 ? 2 : 1, warp * 32 + lane,
+                clear_tail(x.sm.stage + g % Ring<false>::N * Ring<false>::BYTES + kTile, n, p.V - u.tile * 128 > 64 ? 2 : 1, warp * 32 + lane,
                            32 * kWarpsP);
             }
             if (g > 0 && !x.wait(kOFull + ((g - 1) & 1), (g - 1) >> 1)) return;  // the product that read the last P~ is done
@@ -848,11 +925,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm.gave_up = sm.state_loads = 0;
         for (int i = 0; i < kBars; ++i) {
             int n = 1;
-            if (i >= kStageFree && i < kStageFree + kStages) n = STATES ? 1 : 2;  // the products that read a stage last
+            if (i >= kStageFree && i < kStageFree + kMaxStages) n = STATES ? 1 : 2;  // the products that read a stage last
             if (i == kPFree || i == kPFree + 1 || i == kPtFull) n = kWarpsP;
             if (i == kDrain) n = STATES ? 1 : 3;
             if (i == kSFull || i == kSFull + 1 || i == kDsFree || i == kStateTurn) n = kWarpsS;
-            if (i == kKtFull || i == kKtFull + 1) n = kWarpsK;
+            if (i == kKtFull || i == kKtFull + 1) n = kWarpsK * kTeams<STATES>;
             if (i == kOFree) n = kWarpsO;
             mbar_init(bars + 8 * i, n);
         }
@@ -874,6 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_down<kRegsRest>();
         if (warp == kWarpMma) {
             role_mma_state<KP, PARTS, STATES>(x);
+            drain_mma(x);
         } else if (warp == kWarpMma + 1) {
             if (!STATES) role_mma_out<KP>(x);
         } else if (warp == kWarpMma + 2) {
@@ -901,13 +979,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait(x.bar(kStateIn), (uint32_t)(sm.state_loads - 1) & 1u, &never);
                 tma_stores_done();
             }
+        } else {
+            role_keys<KP, PARTS, STATES, kTeams<STATES>>(x, 2, warp - kWarpO, lane);
         }
     } else if (warp < kWarpK) {
         if (kRegsP > 80) regs_up<kRegsP>();
-        if (!STATES) role_scores(x, warp - kWarpP, lane);
+        if constexpr (STATES)
+            role_keys<KP, PARTS, STATES, kTeams<STATES>>(x, 1, warp - kWarpP, lane);
+        else
+            role_scores(x, warp - kWarpP, lane);
     } else {
         regs_down<kRegsK>();
-        role_keys<KP, PARTS, STATES>(x, warp - kWarpK, lane);
+        role_keys<KP, PARTS, STATES, kTeams<STATES>>(x, 0, warp - kWarpK, lane);
     }
     __syncwarp();
     fence_before();
@@ -952,13 +1035,21 @@ template <typename ST> __global__ void __launch_bounds__(256) k_la_join(const __
     float4 s = make_float4(to_f32(pool[0]), to_f32(pool[1]), to_f32(pool[2]), to_f32(pool[3]));
     const long long step = (long long)p.nv * p.K * p.V;
     float *ws = c.ws + (long long)before * step + (long long)h * p.K * p.V + i;
-    for (int j = 0; j < n; ++j, ws += step) {
-        const float4 own = j + 1 < n ? *reinterpret_cast<const float4 *>(ws) : make_float4(0, 0, 0, 0);
-        *reinterpret_cast<float4 *>(ws) = s;
-        s.x = fmaf(lam, s.x, own.x);
-        s.y = fmaf(lam, s.y, own.y);
-        s.z = fmaf(lam, s.z, own.z);
-        s.w = fmaf(lam, s.w, own.w);
+    // eight segments' loads at a time: one after the other they took 33 us for 14 segments
+    for (int j0 = 0; j0 < n; j0 += 8, ws += 8 * step) {
+        float4 own[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            own[j] = j0 + j + 1 < n ? *reinterpret_cast<const float4 *>(ws + j * step) : make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j0 + j >= n) break;
+            *reinterpret_cast<float4 *>(ws + j * step) = s;
+            s.x = fmaf(lam, s.x, own[j].x);
+            s.y = fmaf(lam, s.y, own[j].y);
+            s.z = fmaf(lam, s.z, own[j].z);
+            s.w = fmaf(lam, s.w, own[j].w);
+        }
     }
 }
 
