@@ -161,6 +161,35 @@ def test_long_rows_with_and_without_a_workspace(lens):
     c.check()
 
 
+@pytest.mark.parametrize("pool", [BF16, F32])
+@pytest.mark.parametrize("lens,nk,nv,K,V", [([(7 * i) % 90 for i in range(75)], 1, 2, 64, 64),  # many rows
+                                            ([100, 20, 1], 2, 72, 64, 128),                      # many heads
+                                            ([900, 530, 512, 64, 7, 0], 5, 40, 128, 128),        # units dealt by load
+                                            ([600, 90], 1, 80, 64, 256),                         # two column tiles, more heads than CTAs
+                                            ([65] * 16, 11, 11, 96, 144)])
+def test_batches(lens, nk, nv, K, V, pool):
+    """Every way units are dealt out, with padding rows among them."""
+    Case(lens, nk, nv, K, V, BF16, pool, pad=(1,), seed=len(lens) + nv).check(max_row_len=max(lens))
+
+
+def test_positions_past_32_bits():
+    """A pool and token strides whose element offsets pass 2^31."""
+    for hint in (1, 5, 70):
+        lens = [hint, 1]
+        c = Case(lens, 1, 1, 128, 256, BF16, BF16, seed=43)
+        big = torch.zeros(66000, 1, 128, 256, dtype=BF16, device=DEV)  # 2.2e9 elements
+        slots = torch.tensor([65999, 1], dtype=torch.int32, device=DEV)
+        big[65999], big[1] = c.pool[0], c.pool[1]
+        T, stride = sum(lens), 2 ** 31 // (hint + 1) // 8 * 8 + 1024
+        far = torch.zeros(T * stride, dtype=BF16, device=DEV)
+        v = far.as_strided((T, 1, 256), (stride, 256, 1))
+        v.copy_(c.v)
+        out = gdr.gdr_linattn_fwd(c.q, c.k, v, c.decay, big, slots, c.off, max_row_len=hint)
+        ref = linattn_ref(c.q, c.k, c.v, c.decay, c.pool, torch.tensor([0, 1]), c.off)
+        check_linattn(out, big[[65999, 1]], (ref[0], ref[1][:2], ref[2], ref[3][:2]), hint, hint > 1)
+        del big, far, v
+
+
 def test_a_row_of_nan_spoils_no_other():
     """Rows that share a chunk's loads with a neighbour full of NaN and infinities."""
     for hint in (0, 9):
