@@ -120,6 +120,19 @@ __device__ __forceinline__ float power_fast(float lg2, int n) {
 __device__ __forceinline__ int sound_len(const LaParams &p, int t0, int t1) {
     return t0 < 0 || t1 < t0 || t1 > p.T ? -1 : t1 - t0;
 }
+// Cut rows, one a lane of a warp: -1 too for a row that begins before an earlier
+// one's end.  Rows that lie apart have at most T / seg + batch segments, which
+// is what the workspace holds.
+__device__ __forceinline__ int apart(int t0, int len) {
+    int end = max(len < 0 ? 0 : t0 + len, 0);
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, end, m);
+        if ((int)(threadIdx.x & 31) >= m) end = max(end, o);
+    }
+    const int before = __shfl_up_sync(0xffffffffu, end, 1);
+    return (threadIdx.x & 31) && t0 < before ? -1 : len;
+}
 // log2 of a head's decay; NaN for one outside [0, 1].
 __device__ __forceinline__ float log2_lambda(const LaParams &p, int h) {
     const float d = p.decay[(long long)h * p.decay_s];
@@ -236,8 +249,9 @@ __device__ __forceinline__ void plan_rows(const ChunkParams &c, Smem &sm) {
         t0 = p.offsets[tid];
         len = sound_len(p, t0, p.offsets[tid + 1]);
         slot = p.slot_idx[tid];
-        sm.first[tid] = len;
     }
+    if (c.seg && tid < 32) len = apart(t0, len);  // batch <= 32
+    if (B <= kMaxRows && tid < B) sm.first[tid] = len;
     __syncthreads();
     int rank = 0;
     if (B <= kMaxRows && tid < B) {
@@ -275,7 +289,7 @@ __device__ __forceinline__ void plan_rows(const ChunkParams &c, Smem &sm) {
             __syncthreads();
         }
     }
-    if (c.seg && tid < 32) {  // batch <= 32: one lane a row
+    if (c.seg && tid < 32) {  // one lane a row
         int end = tid < B ? max(1, (sm.row_len[tid] + c.seg - 1) / c.seg) : 0;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
@@ -1008,11 +1022,12 @@ template <typename ST> __global__ void __launch_bounds__(256) k_la_join(const __
     __shared__ int s_len[32];
     const int B = p.batch;
     if (threadIdx.x < 32) {
-        int len = -1;
+        int t0 = 0, len = -1;
         if ((int)threadIdx.x < B) {
-            len = sound_len(p, p.offsets[threadIdx.x], p.offsets[threadIdx.x + 1]);
+            t0 = p.offsets[threadIdx.x];
+            len = sound_len(p, t0, p.offsets[threadIdx.x + 1]);
         }
-        s_len[threadIdx.x] = len;
+        s_len[threadIdx.x] = apart(t0, len);
     }
     __syncthreads();
     // the row of this rank, and the segments of the rows before it

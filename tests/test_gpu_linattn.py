@@ -162,6 +162,68 @@ def test_long_rows_with_and_without_a_workspace(lens):
 
 
 @pytest.mark.parametrize("pool", [BF16, F32])
+@pytest.mark.parametrize("lens,nk,nv,K,V,pad", [([2400], 1, 2, 128, 128, ()), ([2100, 0, 2300, 5], 2, 2, 64, 64, (2,)),
+                                                ([64 * 40 + 1, 64 * 20], 1, 3, 96, 144, ()), ([3001], 2, 4, 128, 256, ()),
+                                                ([64 * 36] + [70] * 8, 1, 4, 64, 128, (3,))])
+def test_rows_cut_into_segments(lens, nk, nv, K, V, pad, pool):
+    c = Case(lens, nk, nv, K, V, BF16, pool, pad=pad, seed=sum(lens))
+    assert gdr.gdr_linattn_workspace_bytes(c.q, c.k, c.v, c.decay, c.pool, c.slot, c.off, max_row_len=max(lens)) > 0
+    c.check(max_row_len=max(lens))
+
+
+def test_problems_in_rows_cut_into_segments():
+    c = Case([2400, 40, 2300], 1, 3, 64, 64, BF16, F32, seed=83)
+    good, good_pool = c.run(2400)
+    c.decay[1] = 2.0
+    out, pool = _flags(lambda: c.run(2400), "BAD_DECAY")
+    assert not out[:, 1].any() and torch.equal(pool[:, 1], c.pool[:, 1])
+    assert torch.equal(out[:, [0, 2]], good[:, [0, 2]]) and torch.equal(pool[:, [0, 2]], good_pool[:, [0, 2]])
+    c.decay[:] = c.lam
+    out, pool = _flags(lambda: c.run(2350), "ROW_TOO_LONG")
+    assert not out[:2400].any() and torch.equal(pool[int(c.slot[0])], c.pool[int(c.slot[0])])
+    slot = c.slot.clone()
+    c.slot[2] = -7
+    out, pool = _flags(lambda: c.run(2400), "BAD_SLOT")
+    assert not out[2440:].any() and torch.equal(out[:2440], good[:2440])
+    c.slot[:] = slot
+    # rows that lie on one another are not all done, and never ask for more segments than there is room for
+    c = Case([2400] + [0] * 14, 1, 3, 64, 64, BF16, F32, seed=84)
+    want, want_pool = c.run(2400)
+    c.off[1::2] = 2400
+    c.off[2::2] = 0
+    out, pool = _flags(lambda: c.run(2400), "BAD_OFFSETS")
+    assert torch.equal(out, want) and torch.equal(pool, want_pool)
+
+
+def test_problems_in_short_rows():
+    c = Case([9, 5, 12], 1, 3, 64, 64, BF16, BF16, seed=85)
+    good, good_pool = c.run(12)
+    c.decay[1] = -1.0
+    out, pool = _flags(lambda: c.run(12), "BAD_DECAY")
+    assert not out[:, 1].any() and torch.equal(pool[:, 1], c.pool[:, 1])
+    assert torch.equal(out[:, [0, 2]], good[:, [0, 2]]) and torch.equal(pool[:, [0, 2]], good_pool[:, [0, 2]])
+    c.decay[:] = c.lam
+    out, pool = _flags(lambda: c.run(10), "ROW_TOO_LONG")
+    assert not out[14:].any() and torch.equal(out[:14], good[:14])
+    assert torch.equal(pool[int(c.slot[2])], c.pool[int(c.slot[2])])
+    c.off[-1] = 10 ** 6
+    out, pool = _flags(lambda: c.run(12), "BAD_OFFSETS")
+    assert torch.equal(out[:14], good[:14]) and torch.equal(pool[int(c.slot[2])], c.pool[int(c.slot[2])])
+    c.off[-1] = 26
+    c.slot[0] = 5
+    out, pool = _flags(lambda: c.run(12), "BAD_SLOT")
+    assert not out[:9].any() and torch.equal(out[9:], good[9:])
+
+
+@pytest.mark.parametrize("pool", [BF16, F32])
+@pytest.mark.parametrize("K,V,nk,nv", [(128, 256, 4, 8), (16, 16, 1, 8), (96, 144, 8, 8), (64, 64, 8, 8), (48, 80, 2, 8)])
+def test_short_rows_by_the_hundred(K, V, nk, nv, pool):
+    """More units than the GPU takes at once, padding rows and rows of nothing among them."""
+    lens = [(5 * i) % 17 for i in range(120)]
+    Case(lens, nk, nv, K, V, BF16, pool, pad=(7, 40), seed=K + V).check(max_row_len=16)
+
+
+@pytest.mark.parametrize("pool", [BF16, F32])
 @pytest.mark.parametrize("lens,nk,nv,K,V", [([(7 * i) % 90 for i in range(75)], 1, 2, 64, 64),  # many rows
                                             ([100, 20, 1], 2, 72, 64, 128),                      # many heads
                                             ([900, 530, 512, 64, 7, 0], 5, 40, 128, 128),        # units dealt by load
