@@ -138,11 +138,16 @@ gdr::LaParams lower(const gdr_linattn_args *a, unsigned *status) {
 
 // Tokens a segment for rows that are cut, or 0.  One CTA does a (row, head,
 // column tile) from end to end, so a call lasts about as many chunks as its
-// longest row has, or as the fullest SM gets.  Cut rows spread evenly, and
-// cost a pass over k and v for the segments' own states and the states'
-// traffic: about 0.6 of a chunk's time a chunk more and two chunks' a unit.
+// longest row has, or as the fullest SM gets, and three chunks' time to fill
+// and drain a unit.  Cut rows spread evenly, and cost a pass over k and v for
+// the segments' own states (with the slower clock and memory of a full GPU,
+// 0.75 of a chunk's time a chunk), two more launches and the states' traffic
+// (12 chunks' time).  Measured, cut against whole, K = V = 128, bfloat16 pool:
+// 16383 tokens x 32 heads 179 us against 332, 4000 x 32 70 / 92, 2000 x 4 37 /
+// 52; left whole by this rule: 1000 x 16 38 / 33, 2 rows of 2000 x 16 54 / 52,
+// 8000 x 64 191 / 173.
 int plan_segments(const gdr_linattn_args *a) {
-    constexpr double kSms = 152.0, kChunk = 64.0, kStatePass = 0.6, kUnit = 2.0;
+    constexpr double kSms = 152.0, kChunk = 64.0, kStatePass = 0.75, kUnit = 3.0, kExtra = 12.0;
     if (a->batch < 1 || a->batch > 32) return 0;
     const double tiles = (a->V + 127) / 128, heads = a->nv * tiles, T = (double)a->total_tokens;
     const double mean = std::ceil(T / a->batch / kChunk);
@@ -156,7 +161,7 @@ int plan_segments(const gdr_linattn_args *a) {
         if (chunks < 4) break;
         // a row's last segment is half full on average
         const double units = std::ceil(T / (chunks * kChunk) + 0.5 * (a->batch - 1)) * heads;
-        const double cost = std::ceil(units / kSms) * (chunks * (1 + kStatePass) + 2 * kUnit) + 4;
+        const double cost = std::ceil(units / kSms) * (chunks * (1 + kStatePass) + 2 * kUnit) + kExtra;
         if (cost < 0.9 * best) {
             best = cost / 0.9;
             seg = (int)(chunks * kChunk);
