@@ -44,11 +44,21 @@ using namespace tc;
 constexpr int kC = 64;        // tokens a chunk
 constexpr int kSub = kC * 128;        // bytes of a 64-token x 64-channel operand block
 constexpr int kTile = 2 * kSub;       // bytes of a 64-token x 128-channel operand
-// The chunks on their way in: K | V | Q, or K | V where only states are computed.
-template <bool STATES> struct Ring {
-    static constexpr int N = STATES ? 4 : 3, BYTES = (STATES ? 2 : 3) * kTile;
+// The chunks on their way in, K | V | Q, or K | V where only states are computed,
+// and after them K~ but for its first part, which takes K's place, of two
+// chunks: with two parts it fills half of its room, and a state on its way has
+// the rest.  Half as many key channels leave room for more chunks, without which
+// loads, not roles, set the pace (4 rows of 4096 tokens x 38 heads of 64 x 64: 85
+// us with three, 76 with five).
+template <int KP, bool STATES> struct Ring {
+    static constexpr int KB = KP / 64 * kSub;  // K's bytes, or Q's
+    static constexpr int V = KB, Q = KB + kTile, BYTES = STATES ? KB + kTile : 2 * KB + kTile;
+    static constexpr int N = KP == 64 ? (STATES ? 6 : 5) : (STATES ? 4 : 3);
+    static constexpr int KT = KP == 64 ? 10 * kTile : 9 * kTile;  // of both kinds
+    static constexpr int STATE = KT + 2 * KB;
+    static_assert(N * BYTES <= KT, "ring");
 };
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 6;
 constexpr int kMaxRows = 64, kMaxHeads = 64;  // rows and heads whose facts are kept in shared memory
 constexpr int kPlanned = 16;                  // rows whose units are dealt by load
 
@@ -73,9 +83,7 @@ enum Bar {
 };
 
 struct Smem {
-    unsigned char stage[Ring<false>::N * Ring<false>::BYTES];
-    unsigned char kt[4 * kTile];          // K~ but for its first part, which takes K's place, of two chunks: with two
-                                          // parts it fills half of this, and the rest holds a state on its way
+    unsigned char ring[13 * kTile];       // Ring
     unsigned char pt[kSub];               // P~^T
     unsigned char ost[kWarpsO][32 * 64];  // output on its way out, 32 tokens x 32 columns a warp
     uint64_t bar[kBars];
@@ -88,7 +96,7 @@ struct Smem {
     int gave_up, state_loads, next_len;
     float next_lg2;
 };
-static_assert(sizeof(Smem) + 1024 <= 232448, "shared memory");
+static_assert(sizeof(Smem) + 1024 <= 232448 && offsetof(Smem, ring) == 0, "shared memory");
 
 struct ChunkParams {
     LaParams p;
@@ -268,7 +276,7 @@ __device__ __forceinline__ void plan_rows(const ChunkParams &c, Smem &sm) {
     const bool planned = !c.seg && B <= kPlanned && (unsigned)B * c.per.d > gridDim.x && 4 * G <= kThreads && sm.row_len[0] >= 8 * kC;
     if (tid == 0) sm.planned = planned;
     if (planned) {
-        int *const load = reinterpret_cast<int *>(sm.stage);  // by CTA, in chunks; nothing is on its way yet
+        int *const load = reinterpret_cast<int *>(sm.ring);  // by CTA, in chunks; nothing is on its way yet
         const int cta = tid >> 2, part = tid & 3;             // four threads compare for a CTA
         for (int o = tid; o < G; o += kThreads) load[o] = 0;
         __syncthreads();
@@ -367,7 +375,7 @@ template <int KP, bool ST2, bool STATES> struct Loader {  // ST2: a bfloat16 poo
             if (!STATES && more && u.chunks > 0) fetch_state();
         }
         if (!more) return true;
-        using R = Ring<STATES>;
+        using R = Ring<KP, STATES>;
         const int s = g % R::N;
         if (g >= R::N && !x.wait(kStageFree + s, g / R::N - 1)) return false;
         if (elect_one()) {
@@ -379,9 +387,9 @@ template <int KP, bool ST2, bool STATES> struct Loader {  // ST2: a bfloat16 poo
 #pragma unroll
             for (int i = 0; i < nk; ++i) {
                 tma_load3(dst + i * kSub, mk, i * 64, hk, t, full);
-                if (!STATES) tma_load3(dst + 2 * kTile + i * kSub, mq, i * 64, hk, t, full);
+                if (!STATES) tma_load3(dst + R::Q + i * kSub, mq, i * 64, hk, t, full);
             }
-            for (int i = 0; i < nv; ++i) tma_load3(dst + kTile + i * kSub, mv, v0 + i * 64, u.h, t, full);
+            for (int i = 0; i < nv; ++i) tma_load3(dst + R::V + i * kSub, mv, v0 + i * 64, u.h, t, full);
         }
         __syncwarp();
         ++g;
@@ -391,7 +399,7 @@ template <int KP, bool ST2, bool STATES> struct Loader {  // ST2: a bfloat16 poo
     // No copy is in flight when the CTA ends.
     __device__ void drain() {
         volatile int never = 0;
-        constexpr unsigned N = Ring<STATES>::N;
+        constexpr unsigned N = Ring<KP, STATES>::N;
         for (unsigned o = g > N ? g - N : 0; o < g; ++o) mbar_wait(x.bar(kLoaded + o % N), (o / N) & 1u, &never);
     }
 };
@@ -414,7 +422,7 @@ __device__ __forceinline__ void drain_mma(const Ctx &x) {
 
 // P^T = K Q^T
 template <int KP> __device__ void role_mma_scores(const Ctx &x) {
-    using R = Ring<false>;
+    using R = Ring<KP, false>;
     const uint32_t id = idesc_bf16(64, kC, false, false);
     const uint64_t d_km = desc128(x.base, 16, 1024);  // stage 0, K-major
     const unsigned total = count_chunks<false>(x);
@@ -424,7 +432,7 @@ template <int KP> __device__ void role_mma_scores(const Ctx &x) {
         if (!x.wait(kLoaded + g % R::N, g / R::N)) break;
         fence_after();
         const uint32_t me = elect_one(), st = uniform(g % R::N), odd = uniform(g & 1);
-        const uint64_t k = d_km + (st * R::BYTES >> 4), q = k + (2 * kTile >> 4);
+        const uint64_t k = d_km + (st * R::BYTES >> 4), q = k + (R::Q >> 4);
         mma_ss_k<KP / 16>(me, x.tmem + kColP + odd * kC, k, q, id, kSub);
         mma_commit(me, x.bar(kPFull) + 8 * odd);
     }
@@ -434,10 +442,10 @@ template <int KP> __device__ void role_mma_scores(const Ctx &x) {
 // V^T K~.  For a segment's own state (STATES) the weights count to the segment's
 // end and all of its chunks add up in tensor memory; else each chunk's is read.
 template <int KP, int PARTS, bool STATES> __device__ void role_mma_state(const Ctx &x) {
-    using R = Ring<STATES>;
+    using R = Ring<KP, STATES>;
     const uint32_t id = idesc_bf16(128, KP, true, true);
     const uint64_t d_mn = desc128(x.base, kSub, 1024);  // stage 0, MN-major
-    const uint64_t d_kt = desc128(x.base + (uint32_t)offsetof(Smem, kt), kSub, 1024);
+    const uint64_t d_kt = desc128(x.base + R::KT, kSub, 1024);
     Walk<STATES> walk(x.c, x.sm);
     Unit u;
     unsigned g = 0, reads = 0;
@@ -451,13 +459,13 @@ template <int KP, int PARTS, bool STATES> __device__ void role_mma_state(const C
             }
             fence_after();
             const uint32_t me = elect_one(), st = uniform(g % R::N), odd = uniform(g & 1);
-            const uint64_t k = d_mn + (st * R::BYTES >> 4), v = k + (kTile >> 4), kt = d_kt + (odd * (PARTS - 1) * kTile >> 4);
+            const uint64_t k = d_mn + (st * R::BYTES >> 4), v = k + (R::V >> 4), kt = d_kt + (odd * (PARTS - 1) * R::KB >> 4);
             if (fresh)
                 mma_ss_mn64<false>(me, x.tmem + kColDS, v, k, id);
             else
                 mma_ss_mn64<true>(me, x.tmem + kColDS, v, k, id);
             mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt, id);
-            if (PARTS == 3) mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt + (kTile >> 4), id);
+            if (PARTS == 3) mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt + (R::KB >> 4), id);
             mma_commit(me, x.bar(kDsFull) + 8 * odd);
             if (STATES && j + 1 == u.chunks) mma_commit(me, x.bar(kOFull));
             mma_commit(me, x.bar(kStageFree) + 8 * st);
@@ -467,9 +475,9 @@ template <int KP, int PARTS, bool STATES> __device__ void role_mma_state(const C
 
 // S0^T Q^T and V^T P~^T
 template <int KP> __device__ void role_mma_out(const Ctx &x) {
-    using R = Ring<false>;
+    using R = Ring<KP, false>;
     const uint32_t id1 = idesc_bf16(128, kC, false, false), id2 = idesc_bf16(128, kC, true, true);
-    const uint64_t d_km = desc128(x.base + 2 * kTile, 16, 1024), d_v = desc128(x.base + kTile, kSub, 1024);
+    const uint64_t d_km = desc128(x.base + R::Q, 16, 1024), d_v = desc128(x.base + R::V, kSub, 1024);
     const uint64_t d_pt = desc128(x.base + (uint32_t)offsetof(Smem, pt), kSub, 1024);
     const unsigned total = count_chunks<false>(x);
     for (unsigned g = 0; g < total; ++g) {
@@ -519,13 +527,13 @@ template <int KP, int PARTS, bool STATES, int TEAMS> __device__ void role_keys(c
             const int n = min(kC, u.len - j * kC);
             if (STATES || j == 0 || n < kC)
                 w_last = power(u.lg2, max((STATES ? u.len - j * kC : n) - 1 - (16 * last + row), 0));
-            using R = Ring<STATES>;
+            using R = Ring<KP, STATES>;
             if (!x.wait(kLoaded + g % R::N, g / R::N)) return;
-            unsigned char *stage = x.sm.stage + g % R::N * R::BYTES;
-            if (__builtin_expect(n < kC, 0)) clear_tail(stage + kTile, n, nv, tid, 32 * kWarpsK);
+            unsigned char *stage = x.sm.ring + g % R::N * R::BYTES;
+            if (__builtin_expect(n < kC, 0)) clear_tail(stage + R::V, n, nv, tid, 32 * kWarpsK);
             if (!STATES && !x.wait(kPFull + (g & 1), g >> 1)) return;           // K Q^T has read K
             if (g > 1 && !x.wait(kDsFull + (g & 1), (g >> 1) - 1)) return;  // and the product before last its K~
-            unsigned char *const rest = x.sm.kt + (g & 1) * (PARTS - 1) * kTile;
+            unsigned char *const rest = x.sm.ring + R::KT + (g & 1) * (PARTS - 1) * R::KB;
             // small loops: the roles share the instruction caches
             float w = w_last;
 #pragma unroll 1
@@ -563,7 +571,7 @@ template <int KP, int PARTS, bool STATES, int TEAMS> __device__ void role_keys(c
                     *here = make_uint4(o[0][0], o[0][1], o[0][2], o[0][3]);
 #pragma unroll
                     for (int part = 1; part < PARTS; ++part)
-                        *reinterpret_cast<uint4 *>(rest + (part - 1) * kTile + at) =
+                        *reinterpret_cast<uint4 *>(rest + (part - 1) * R::KB + at) =
                             make_uint4(o[part][0], o[part][1], o[part][2], o[part][3]);
                 }
                 w *= lam_b;
@@ -640,7 +648,7 @@ __device__ __forceinline__ bool state_chunks(const Ctx &x, const StateRole &r, f
 // instructions that run once a unit come from far away.
 template <int KP> __device__ void role_state_staged(const Ctx &x, int warp, int lane) {
     const StateRole r = StateRole::of<KP>(warp, lane);
-    const uint32_t buf = x.base + (uint32_t)offsetof(Smem, kt) + 2 * kTile + (r.half * 64 * 128 + r.v) * 2;  // [KP][128]
+    const uint32_t buf = x.base + Ring<KP, false>::STATE + (r.half * 64 * 128 + r.v) * 2;  // [KP][128]
     unsigned g = 0;
     float2 s[32] = {};
     for (unsigned units = 0;; ++units) {
@@ -718,7 +726,8 @@ template <typename ST, int KP, bool STATES> __device__ void role_state(const Ctx
 
 // P~: a warp has 16 keys of P^T.  Its blocks of 8 queries are wholly masked
 // before its own 16, mixed there, and wholly kept after.
-__device__ void role_scores(const Ctx &x, int warp, int lane) {
+template <int KP> __device__ void role_scores(const Ctx &x, int warp, int lane) {
+    using R = Ring<KP, false>;
     const LaParams &p = x.c.p;
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
     const int row0 = warp * 16 + lane / 4;  // this thread's keys: row0 and row0 + 8
@@ -776,7 +785,7 @@ __device__ void role_scores(const Ctx &x, int warp, int lane) {
                     if (row0 >= n) h[2 * b] = 0;
                     if (row0 + 8 >= n) h[2 * b + 1] = 0;
                 }
-                clear_tail(x.sm.stage + g % Ring<false>::N * Ring<false>::BYTES + kTile, n, p.V - u.tile * 128 > 64 ? 2 : 1, warp * 32 + lane,
+                clear_tail(x.sm.ring + g % R::N * R::BYTES + R::V, n, p.V - u.tile * 128 > 64 ? 2 : 1, warp * 32 + lane,
                            32 * kWarpsP);
             }
             if (g > 0 && !x.wait(kOFull + ((g - 1) & 1), (g - 1) >> 1)) return;  // the product that read the last P~ is done
@@ -797,7 +806,7 @@ template <int KP> struct StateCopies {
     int now[3], next[3];  // tile, head, slot: of the unit being computed, and of the one whose start state is on its way
     unsigned units = 0;
     __device__ StateCopies(const Ctx &x_, const CUtensorMap *m) : x(x_), map(m), ahead(x_.c, x_.sm) {}
-    __device__ uint32_t buf() const { return x.base + (uint32_t)offsetof(Smem, kt) + 2 * kTile; }
+    __device__ uint32_t buf() const { return x.base + Ring<KP, false>::STATE; }
 
     // Announces the next unit, and that there is none by a length of 0.
     __device__ void load() {
@@ -856,9 +865,10 @@ template <int KP> __device__ void role_out(const Ctx &x, int warp, int lane, Sta
     if (states) states->load();
     while (walk.next(u, warp == 0 && lane == 0)) {
         const int col = u.tile * 128 + warp * 32;
-        if (u.skip_len && col + lane < p.V)
-            for (int t = 0; t < u.skip_len; ++t)
-                out[(long long)(u.skip_t0 + t) * p.o_ts + (long long)u.h * p.o_hs + col + lane] = 0;
+        if (col + (lane & 3) * 8 < p.V)
+            for (int t = lane / 4; t < u.skip_len; t += 8)
+                *reinterpret_cast<uint4 *>(out + (long long)(u.skip_t0 + t) * p.o_ts + (long long)u.h * p.o_hs + col +
+                                           (lane & 3) * 8) = make_uint4(0, 0, 0, 0);
         if (u.chunks == 0) continue;
         if (states && !states->turn()) return;
         float2 f[8];
@@ -1001,7 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (STATES)
             role_keys<KP, PARTS, STATES, kTeams<STATES>>(x, 1, warp - kWarpP, lane);
         else
-            role_scores(x, warp - kWarpP, lane);
+            role_scores<KP>(x, warp - kWarpP, lane);
     } else {
         regs_down<kRegsK>();
         role_keys<KP, PARTS, STATES, kTeams<STATES>>(x, 0, warp - kWarpK, lane);
