@@ -82,12 +82,25 @@ int check_linattn(const gdr_linattn_args *a, const char *fn) {
     return GDR_OK;
 }
 
-// Rows of at most this many tokens (by the caller's bound) are one chunk of k_la_small.cu.
-constexpr long long kShortRowMax = 16;
+// Rows of at most this many tokens (by the caller's bound) are for
+// k_la_small.cu, whose time grows with a row's 16-token pieces, where
+// k_la_chunk.cu's for a unit hardly does.  Measured, 64 rows x 16 heads of K x V,
+// us, small against chunk: 64 x 64 41 / 52 at 96 tokens, 50 / 52 at 128; 64 x 128
+// 39 / 46 at 48, 46 / 44 at 64 (128 x 64: 38 / 46, 48 / 46); 128 x 128, bfloat16
+// pool, 42 / 46 at 32, 56 / 48 at 48; float32 pool 40 / 54 at 16, 58 / 56 at 32.
+long long short_row_max(const gdr_linattn_args *a) {
+    const bool wide_k = a->K > 64, wide_v = a->V > 64;
+    if (wide_k && wide_v) return a->state_dtype == GDR_BF16 ? 32 : 16;
+    return wide_k || wide_v ? 48 : 96;
+}
+
+bool takes_pieces(const gdr_linattn_args *a, bool tok_vec) {
+    return a->token_dtype == GDR_BF16 && tok_vec && a->max_row_len > 1 && a->max_row_len <= short_row_max(a);
+}
 
 bool takes_chunks(const gdr_linattn_args *a, bool tok_vec) {
     return a->token_dtype == GDR_BF16 && tok_vec && a->total_tokens > 0 &&
-           (a->max_row_len <= 0 || a->max_row_len > kShortRowMax);
+           (a->max_row_len <= 0 || a->max_row_len > short_row_max(a));
 }
 
 bool token_vectors(const gdr_linattn_args *a) {
@@ -198,7 +211,7 @@ int gdr_linattn_fwd(const gdr_linattn_args *a, void *stream) {
     unsigned *st = nullptr;
     if ((rc = gdr::api_status(&st))) return rc;
     const gdr::LaParams p = lower(a, st);
-    if (a->token_dtype == GDR_BF16 && p.tok_vec && p.max_len > 1 && p.max_len <= kShortRowMax)
+    if (takes_pieces(a, p.tok_vec))
         return launched(gdr::launch_la_small(p, a->state_dtype == GDR_BF16, static_cast<cudaStream_t>(stream)), fn);
     if (takes_chunks(a, p.tok_vec)) {
         int seg = plan_segments(a);

@@ -224,6 +224,16 @@ def test_short_rows_by_the_hundred(K, V, nk, nv, pool):
 
 
 @pytest.mark.parametrize("pool", [BF16, F32])
+@pytest.mark.parametrize("hint,nk,nv,K,V", [(32, 2, 4, 128, 128), (33, 2, 4, 128, 144), (17, 1, 8, 96, 256), (48, 4, 4, 64, 128),
+                                            (49, 1, 4, 48, 80), (47, 2, 8, 128, 64), (96, 8, 8, 64, 64), (97, 8, 8, 64, 64),
+                                            (80, 1, 16, 16, 16)])
+def test_rows_of_a_few_pieces(hint, nk, nv, K, V, pool):
+    """Either side of where rows stop being short; lengths around multiples of 16, more units than fit at once."""
+    lens = [min(n, hint) for n in (hint, 0, 1, 15, 16, 17, 31, 32, 33, 48, 49, 64, 65, 80, 95, 96)] * 4
+    Case(lens, nk, nv, K, V, BF16, pool, pad=(6, 30), seed=hint + K).check(max_row_len=hint)
+
+
+@pytest.mark.parametrize("pool", [BF16, F32])
 @pytest.mark.parametrize("lens,nk,nv,K,V", [([(7 * i) % 90 for i in range(75)], 1, 2, 64, 64),  # many rows
                                             ([100, 20, 1], 2, 72, 64, 128),                      # many heads
                                             ([900, 530, 512, 64, 7, 0], 5, 40, 128, 128),        # units dealt by load
