@@ -35,15 +35,15 @@ template <class C> cudaError_t go_wide(const NormParams &p, cudaStream_t s) {
 
 cudaError_t launch_norm(const NormParams &p, bool vec, cudaStream_t s) {
     if (!vec) return launch_norm_odd(p, s);
-    const bool bf_gate = p.gate && p.g_es && p.gate_bf16;
+    const bool elem_gate = p.gate && p.g_es, bf_gate = elem_gate && p.gate_bf16;
     if (p.x && !p.res && bf_gate && p.post && !p.pre && p.out && p.out_bf16 && p.D <= 256)
         return p.x_bf16 ? go_heads<Cfg<1, 1, 1, 0, 0, 1, 0, 1>>(p, s) : go_heads<Cfg<0, 1, 1, 0, 0, 1, 0, 1>>(p, s);
-    if (p.x && p.x_bf16 && p.res && p.pre && p.out && p.out_bf16 && (bf_gate || !p.gate) && p.D > 256) {
+    if (p.x && p.x_bf16 && p.res && p.pre && p.out && p.out_bf16 && (bf_gate || !elem_gate) && p.D > 256) {
         if (p.res_bf16) {
-            if (p.gate) return p.post ? go_wide<Cfg<1, 1, 1, 1, 1, 1, 1, 1>>(p, s) : go_wide<Cfg<1, 1, 1, 1, 1, 0, 1, 1>>(p, s);
+            if (elem_gate) return p.post ? go_wide<Cfg<1, 1, 1, 1, 1, 1, 1, 1>>(p, s) : go_wide<Cfg<1, 1, 1, 1, 1, 0, 1, 1>>(p, s);
             return p.post ? go_wide<Cfg<1, 0, 0, 1, 1, 1, 1, 1>>(p, s) : go_wide<Cfg<1, 0, 0, 1, 1, 0, 1, 1>>(p, s);
         }
-        if (p.gate) return p.post ? go_wide<Cfg<1, 1, 1, 1, 0, 1, 1, 1>>(p, s) : go_wide<Cfg<1, 1, 1, 1, 0, 0, 1, 1>>(p, s);
+        if (elem_gate) return p.post ? go_wide<Cfg<1, 1, 1, 1, 0, 1, 1, 1>>(p, s) : go_wide<Cfg<1, 1, 1, 1, 0, 0, 1, 1>>(p, s);
         return p.post ? go_wide<Cfg<1, 0, 0, 1, 0, 1, 1, 1>>(p, s) : go_wide<Cfg<1, 0, 0, 1, 0, 0, 1, 1>>(p, s);
     }
     return p.D <= 64 ? go<Any, 8, 1, 8>(p, s) : p.D <= 128 ? go<Any, 8, 1, 16>(p, s) : go_wide<Any>(p, s);

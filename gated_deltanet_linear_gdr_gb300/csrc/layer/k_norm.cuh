@@ -111,10 +111,10 @@ __device__ __forceinline__ float row_sum(float v, float *buf) {
 // what it reads from the parameters.  Bounds first: a vector of 8 elements
 // takes about 250 instructions with everything read from the parameters, which
 // at 128 values a row is twice what HBM allows; about 90 with it known.
+// GATE: 1 a gate with a value for each channel, 0 none or one with a value for each row.
 template <int XB, int GATE, int GB, int RES, int RB, int POST, int PRE, int OB> struct Cfg {
-    static constexpr int x = XB < 0 ? -1 : 1, x_bf16 = XB, gate = GATE, gate_bf16 = GB, res = RES, res_bf16 = RB, post = POST,
-                         pre = PRE, out_bf16 = OB;
-    static constexpr int gate_elem = GATE < 0 ? -1 : 1;
+    static constexpr int x = XB < 0 ? -1 : 1, x_bf16 = XB, gate = GATE == 1 ? 1 : -1, gate_elem = GATE, gate_bf16 = GB, res = RES,
+                         res_bf16 = RB, post = POST, pre = PRE, out_bf16 = OB;
 };
 using Any = Cfg<-1, -1, -1, -1, -1, -1, -1, -1>;
 template <int F> __device__ __forceinline__ bool is(bool runtime) { return F < 0 ? runtime : F != 0; }
@@ -251,8 +251,11 @@ template <class C, int VEC, int NV, int TPR> struct Row {
     }
 };
 
+// With everything read from the parameters, 512 threads of two vectors would
+// take 82 registers each, one CTA a multiprocessor (7682 rows of 6168, float32:
+// 210 us; 193 with two).
 template <class C, int VEC, int NV, int TPR, int NR>
-__global__ void __launch_bounds__(TPR <= 32 ? 256 : TPR) k_norm(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(TPR <= 32 ? 256 : TPR, TPR == 512 && VEC * NV <= 16 ? 2 : 1) k_norm(const __grid_constant__ NormParams p) {
     static_assert(NR == 1 || TPR <= 32, "several rows a slice of a warp, or one a CTA");
     __shared__ float buf[4][32];
     constexpr unsigned RPC = TPR <= 32 ? 256 / TPR : 1;  // slices a CTA

@@ -76,6 +76,22 @@ def test_residual_norm(D, x, h, y, gate):
         check(out, rout, D)
 
 
+@pytest.mark.parametrize("D", [4097, 6001, 8191, 8193, 16383, 6168, 8200])
+@pytest.mark.parametrize("x,h", [(BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("gate", ["element", "token"])
+@pytest.mark.parametrize("centered", [False, True])
+def test_wide_rows(D, x, h, gate, centered):
+    block, res = _randn(3, D, dtype=x), _randn(3, D, dtype=h, seed=1)
+    z = _randn(3, D if gate == "element" else 1, dtype=x, seed=2)
+    w, pw = 1 + 0.1 * _randn(D, seed=3), 1 + 0.1 * _randn(D, seed=4)
+    got_h, got = gdr.gdr_residual_norm(block, res, w, post_weight=pw, gate=z, activation="sigmoid", residual_scale=0.7,
+                                       centered=centered, out_dtype=BF16)
+    rh, rout = norm_ref(block, gate=z, act="sigmoid", post=True, post_w=pw, residual=res, scale=0.7, pre=True, pre_w=w,
+                        centered=centered)
+    check(got_h, rh, D)
+    check(got, rout, D)
+
+
 def test_residual_norm_first_of_a_stack_and_in_place():
     res, w = _randn(5, 512, dtype=BF16), 1 + 0.1 * _randn(512, seed=1)
     h, out = gdr.gdr_residual_norm(None, res, w)
