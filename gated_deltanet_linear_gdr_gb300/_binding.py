@@ -637,7 +637,8 @@ def gdr_linattn_fwd(q, k, v, decay, state, slot_idx, offsets, out=None, *, decay
 
     q, k [T, nk, K], v [T, nv, V] of one dtype (bfloat16 or float32), decay
     [nv] float32 (lambda, or ln lambda with decay_is_log), state
-    [max_slots, nv, K, V].  max_row_len = 1 is the single-token step.
+    [max_slots, nv, K, V].  max_row_len = 1 is the single-token step; a tight
+    bound lets short rows (drafts, last pieces of prompts) take their own form.
     `workspace` is a device tensor to use instead of a new one of
     gdr_linattn_workspace_bytes() bytes."""
     if out is None:

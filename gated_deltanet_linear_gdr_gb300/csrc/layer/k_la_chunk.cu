@@ -27,9 +27,15 @@
 // its issuer, with its waits, for about 110: one issuing warp for all 28 of a
 // chunk measured 3100 cycles a chunk, the slowest of the roles.)
 //
-// Bound: a chunk of one head with K = V = 128 moves 64 KiB (1.47 us of an SM's
-// share of HBM) and holds the tensor cores for about 1400 (bfloat16 pool) to
-// 1660 cycles.
+// Bound: with every SM at work, HBM.  A chunk of one head with K = V = 128 moves
+// 64 KiB, 1.47 us of an SM's share, beside which shared memory (about 2200
+// cycles) and the tensor cores (37% of the time) fit.  4 rows of 4096 tokens x 38
+// heads, a unit an SM, take 112 us with a bfloat16 pool (85% of the measured copy
+// rate) and 120 with a float32 pool; heads of 64 x 64 76 us (63%), where the
+// roles' instructions (the SM issues in 39% of the cycles, waits for fetches) and
+// latencies set the pace, 1.2 us a chunk.  A row alone on its SM takes 1.3 us a
+// chunk (64 x 64: 1.0).  A unit costs 5 us to begin and end, of which its state's
+// exchange takes 1.5: rows of one chunk are the costly ones.
 #include "tc.cuh"
 
 #include "layer_internal.h"

@@ -14,7 +14,8 @@
 // on an element: HBM bound.  What counts is bytes in flight: a thread asks for
 // all of its state before anything else, and R is 8 rows of bfloat16 or 4 of
 // float32 (32 registers of state), so that a multiprocessor holds three to four
-// 32 or 64 KiB blocks at a time.
+// 32 or 64 KiB blocks at a time.  256 rows x 32 heads of 128 x 128, bfloat16: 85
+// us, 91% of the measured copy rate.
 #include "../gdr_device.cuh"
 #include "layer_internal.h"
 

@@ -36,11 +36,11 @@ struct LaParams {
 };
 
 // Recurrent form on the FP32 pipes: any alignment, any row length; what single
-// tokens, short rows and float32 tokens run on.
+// tokens, float32 tokens and rows that are not 16-byte vectors run on.
 cudaError_t launch_la_step(const LaParams &p, bool tok_bf16, bool state_bf16, cudaStream_t s);
 
 // Chunked form in warp-level matrix instructions: bfloat16 tokens whose rows are
-// 16-byte vectors; for short rows and small heads.
+// 16-byte vectors; for short rows (max_len bounds them).
 cudaError_t launch_la_small(const LaParams &p, bool state_bf16, cudaStream_t s);
 
 // Chunked form on the tensor cores: bfloat16 tokens whose rows are 16-byte
