@@ -21,7 +21,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdr.so")
 SOURCES = ["api.cu", "k_decode.cu", "k_short.cu", "k_chain.cu", "k_chain_fwd.cu", "k_chain_fwd_kv.cu", "k_chain_conv.cu", "k_chain_verify.cu",
            "k_chain_snap.cu", "k_fold.cu", "k_probe.cu",
-           "layer/api_layer.cu", "layer/k_norm.cu", "layer/k_norm_odd.cu", "layer/k_la_step.cu", "layer/k_la_chunk.cu", "layer/k_la_small.cu"]
+           "layer/api_layer.cu", "layer/k_norm.cu", "layer/k_norm_odd.cu", "layer/k_norm_pairs.cu", "layer/k_la_step.cu", "layer/k_la_chunk.cu", "layer/k_la_small.cu"]
 HEADERS = ["gdr_internal.h", "gdr_device.cuh", "gdr_pipe.cuh", "gdr_state.cuh", "k_chain.cuh", "gdr.map",
            "layer/layer_internal.h", "layer/tc.cuh", "layer/k_norm.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

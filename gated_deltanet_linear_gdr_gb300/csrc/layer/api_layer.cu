@@ -297,12 +297,19 @@ int gdr_block_norm(const gdr_norm_args *a, void *stream) {
     p.o_hs = a->out_head_stride;
     p.post_w = a->post_weight;
     p.pre_w = a->pre_weight;
-    const bool vec = a->D % 8 == 0 && (!a->x || vector_rows(a->x, a->x_dtype, p.x_ts, p.x_hs)) &&
-                     (!a->gate || p.g_es == 0 || vector_rows(a->gate, a->gate_dtype, p.g_ts, p.g_hs)) &&
-                     (!a->residual || vector_rows(a->residual, a->residual_dtype, p.r_ts, p.r_hs)) &&
-                     (!a->residual_out || vector_rows(a->residual_out, a->residual_dtype, p.ro_ts, p.ro_hs)) &&
-                     (!a->out || vector_rows(a->out, a->out_dtype, p.o_ts, p.o_hs)) && aligned(a->post_weight, 16) &&
-                     aligned(a->pre_weight, 16);
+    // whether everything may be moved as vectors of `width` elements
+    const auto by = [&](int width) {
+        const auto rows = [&](const void *base, int dtype, int64_t ts, int64_t hs) {
+            const int es = esize(dtype);
+            return !base || (aligned(base, width * es < 16 ? width * es : 16) && ts % width == 0 && hs % width == 0);
+        };
+        return a->D % width == 0 && rows(a->x, a->x_dtype, p.x_ts, p.x_hs) &&
+               (p.g_es == 0 || rows(a->gate, a->gate_dtype, p.g_ts, p.g_hs)) &&
+               rows(a->residual, a->residual_dtype, p.r_ts, p.r_hs) &&
+               rows(a->residual_out, a->residual_dtype, p.ro_ts, p.ro_hs) && rows(a->out, a->out_dtype, p.o_ts, p.o_hs) &&
+               rows(a->post_weight, GDR_F32, 0, 0) && rows(a->pre_weight, GDR_F32, 0, 0);
+    };
+    const int vec = by(8) ? 8 : by(2) ? 2 : 1;
     return launched(gdr::launch_norm(p, vec, static_cast<cudaStream_t>(stream)), fn);
 }
 

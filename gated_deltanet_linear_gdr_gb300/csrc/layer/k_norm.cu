@@ -33,8 +33,8 @@ template <class C> cudaError_t go_wide(const NormParams &p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_norm(const NormParams &p, bool vec, cudaStream_t s) {
-    if (!vec) return launch_norm_odd(p, s);
+cudaError_t launch_norm(const NormParams &p, int vec, cudaStream_t s) {
+    if (vec < 8) return vec == 2 ? launch_norm_pairs(p, s) : launch_norm_odd(p, s);
     const bool elem_gate = p.gate && p.g_es, bf_gate = elem_gate && p.gate_bf16;
     if (p.x && !p.res && bf_gate && p.post && !p.pre && p.out && p.out_bf16 && p.D <= 256)
         return p.x_bf16 ? go_heads<Cfg<1, 1, 1, 0, 0, 1, 0, 1>>(p, s) : go_heads<Cfg<0, 1, 1, 0, 0, 1, 0, 1>>(p, s);

@@ -49,6 +49,19 @@ template <> struct Raw<8> {
         }
     }
 };
+template <> struct Raw<2> {
+    uint2 a;
+    __device__ __forceinline__ void load(const void *base, long long at, bool bf16) {
+        if (bf16)
+            a.x = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(base) + at);
+        else
+            a = *reinterpret_cast<const uint2 *>(static_cast<const float *>(base) + at);
+    }
+    __device__ __forceinline__ void get(bool bf16, float (&x)[2]) const {
+        x[0] = __uint_as_float(bf16 ? a.x << 16 : a.x);
+        x[1] = __uint_as_float(bf16 ? a.x & 0xffff0000u : a.y);
+    }
+};
 template <> struct Raw<1> {
     float a;
     __device__ __forceinline__ void load(const void *base, long long at, bool bf16) {
@@ -73,6 +86,13 @@ __device__ __forceinline__ void put(void *base, long long at, bool bf16, const f
             float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + at);
             p[0] = make_float4(x[0], x[1], x[2], x[3]);
             p[1] = make_float4(x[4], x[5], x[6], x[7]);
+        }
+    } else if constexpr (VEC == 2) {
+        if (bf16) {
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(x[0], x[1]);
+            *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(base) + at) = *reinterpret_cast<const uint32_t *>(&h2);
+        } else {
+            *reinterpret_cast<float2 *>(static_cast<float *>(base) + at) = make_float2(x[0], x[1]);
         }
     } else {
         if (bf16)
@@ -273,6 +293,19 @@ template <class C, int VEC, int NV, int TPR, int NR = 1> cudaError_t go(const No
     constexpr unsigned RPC = (TPR <= 32 ? 256 / TPR : 1) * NR;
     k_norm<C, VEC, NV, TPR, NR><<<(p.rows + RPC - 1) / RPC, TPR <= 32 ? 256 : TPR, 0, s>>>(p);
     return cudaGetLastError();
+}
+
+// Which kernel a call of rows that are not 16-byte vectors gets.
+template <class Width> cudaError_t go_narrow(const NormParams &p, cudaStream_t s) {
+    const bool elem_gate = p.gate && p.g_es, bf_gate = elem_gate && p.gate_bf16;
+    if (p.x && p.x_bf16 && p.res && p.pre && p.out && p.out_bf16 && (bf_gate || !elem_gate) && p.D > 256) {
+        if (p.res_bf16)
+            return elem_gate ? Width::template rows<Cfg<1, 1, 1, 1, 1, -1, 1, 1>>(p, s)
+                             : Width::template rows<Cfg<1, 0, 0, 1, 1, -1, 1, 1>>(p, s);
+        return elem_gate ? Width::template rows<Cfg<1, 1, 1, 1, 0, -1, 1, 1>>(p, s)
+                         : Width::template rows<Cfg<1, 0, 0, 1, 0, -1, 1, 1>>(p, s);
+    }
+    return Width::template rows<Any>(p, s);
 }
 
 }  // namespace

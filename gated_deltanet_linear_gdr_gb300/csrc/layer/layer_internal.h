@@ -69,8 +69,9 @@ struct NormParams {
     long long o_ts, o_hs;
     const float *post_w, *pre_w;
 };
-// vec: every row, gate and weight may be moved as vectors of 8 elements.
-cudaError_t launch_norm(const NormParams &p, bool vec, cudaStream_t s);
+// vec: every row, gate and weight may be moved as vectors of 8 elements (16 bytes), of 2, or of 1.
+cudaError_t launch_norm(const NormParams &p, int vec, cudaStream_t s);
+cudaError_t launch_norm_pairs(const NormParams &p, cudaStream_t s);
 cudaError_t launch_norm_odd(const NormParams &p, cudaStream_t s);
 
 }  // namespace gdr

@@ -92,6 +92,24 @@ def test_wide_rows(D, x, h, gate, centered):
     check(got, rout, D)
 
 
+@pytest.mark.parametrize("D", [2, 66, 130, 510, 514, 2046, 2050, 4094, 4098, 8190, 8194, 16382])
+@pytest.mark.parametrize("x,h", [(BF16, BF16), (BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("gate", ["none", "element", "channel"])
+def test_even_widths(D, x, h, gate):
+    """Rows of pairs, among them views whose rows begin on an even element, and on an odd one."""
+    T, w = 5, 1 + 0.1 * _randn(D, seed=3)
+    for first in (0, 2, 1):
+        block = _randn(T, D + 4, dtype=x)[:, first:first + D]
+        res = _randn(T, D + 2, dtype=h, seed=1)[:, :D]
+        z = {"none": None, "element": _randn(T, D, dtype=x, seed=2), "channel": _randn(D, dtype=x, seed=2)}[gate]
+        act = None if z is None else "silu"
+        got_h, got = gdr.gdr_residual_norm(block, res, w, post_weight=w, gate=z, activation=act, residual_scale=0.7,
+                                           out_dtype=BF16)
+        rh, rout = norm_ref(block, gate=z, act=act, post=True, post_w=w, residual=res, scale=0.7, pre=True, pre_w=w)
+        check(got_h, rh, D)
+        check(got, rout, D)
+
+
 def test_residual_norm_first_of_a_stack_and_in_place():
     res, w = _randn(5, 512, dtype=BF16), 1 + 0.1 * _randn(512, seed=1)
     h, out = gdr.gdr_residual_norm(None, res, w)
