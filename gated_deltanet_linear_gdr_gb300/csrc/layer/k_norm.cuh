@@ -295,16 +295,21 @@ template <class C, int VEC, int NV, int TPR, int NR = 1> cudaError_t go(const No
     return cudaGetLastError();
 }
 
+// A block boundary as models have it: what the kernels know when compiled.
+inline bool is_boundary(const NormParams &p) {
+    return p.x && p.res && p.pre && p.out && p.out_bf16 && p.D > 256 && (!p.gate || !p.g_es || p.gate_bf16 == p.x_bf16);
+}
+
 // Which kernel a call of rows that are not 16-byte vectors gets.
+template <class Width, int XB> cudaError_t go_narrow_boundary(const NormParams &p, cudaStream_t s) {
+    if (p.gate && p.g_es)
+        return p.res_bf16 ? Width::template rows<Cfg<XB, 1, XB, 1, 1, -1, 1, 1>>(p, s)
+                          : Width::template rows<Cfg<XB, 1, XB, 1, 0, -1, 1, 1>>(p, s);
+    return p.res_bf16 ? Width::template rows<Cfg<XB, 0, 0, 1, 1, -1, 1, 1>>(p, s)
+                      : Width::template rows<Cfg<XB, 0, 0, 1, 0, -1, 1, 1>>(p, s);
+}
 template <class Width> cudaError_t go_narrow(const NormParams &p, cudaStream_t s) {
-    const bool elem_gate = p.gate && p.g_es, bf_gate = elem_gate && p.gate_bf16;
-    if (p.x && p.x_bf16 && p.res && p.pre && p.out && p.out_bf16 && (bf_gate || !elem_gate) && p.D > 256) {
-        if (p.res_bf16)
-            return elem_gate ? Width::template rows<Cfg<1, 1, 1, 1, 1, -1, 1, 1>>(p, s)
-                             : Width::template rows<Cfg<1, 0, 0, 1, 1, -1, 1, 1>>(p, s);
-        return elem_gate ? Width::template rows<Cfg<1, 1, 1, 1, 0, -1, 1, 1>>(p, s)
-                         : Width::template rows<Cfg<1, 0, 0, 1, 0, -1, 1, 1>>(p, s);
-    }
+    if (is_boundary(p)) return p.x_bf16 ? go_narrow_boundary<Width, 1>(p, s) : go_narrow_boundary<Width, 0>(p, s);
     return Width::template rows<Any>(p, s);
 }
 

@@ -10,8 +10,7 @@ namespace {
 
 struct Single {
     // Wide rows: 1024 threads of 8 values take 126 us for 4000 rows of 6001, 512
-    // threads of up to 32 took 187 (with everything read from the parameters 191
-    // and 455).
+    // threads of up to 32 took 187.
     template <class C> static cudaError_t rows(const NormParams &p, cudaStream_t s) {
         if (p.D <= 128) return go<C, 1, 4, 32>(p, s);
         if (p.D <= 512) return go<C, 1, 16, 32>(p, s);
