@@ -82,25 +82,29 @@ int check_linattn(const gdr_linattn_args *a, const char *fn) {
     return GDR_OK;
 }
 
-// Rows of at most this many tokens (by the caller's bound) are for
-// k_la_small.cu, whose time grows with a row's 16-token pieces, where
-// k_la_chunk.cu's for a unit hardly does.  Measured, 64 rows x 16 heads of K x V,
-// us, small against chunk: 64 x 64 41 / 52 at 96 tokens, 50 / 52 at 128; 64 x 128
-// 39 / 46 at 48, 46 / 44 at 64 (128 x 64: 38 / 46, 48 / 46); 128 x 128, bfloat16
-// pool, 42 / 46 at 32, 56 / 48 at 48; float32 pool 40 / 54 at 16, 58 / 56 at 32.
-long long short_row_max(const gdr_linattn_args *a) {
+// Whether rows are short enough for k_la_small.cu, whose time grows with a row's
+// 16-token pieces, where k_la_chunk.cu's for a unit hardly does.  Measured, 64 rows x
+// 16 heads of K x V, us, small against chunk: 64 x 64 41 / 52 at 96 tokens, 50 / 52 at
+// 128; 64 x 128 39 / 46 at 48, 46 / 44 at 64 (128 x 64: 38 / 46, 48 / 46); 128 x 128,
+// bfloat16 pool, 42 / 46 at 32, 56 / 48 at 48; float32 pool 40 / 54 at 16, 58 / 56 at 32.
+// Where all units run at once (two a multiprocessor) the longest row, by the caller's
+// bound, decides; where they queue, its mean with the average: 52 rows of 1 to 64 x 21
+// heads of 64 x 128 38 / 50, of 1 to 96 54 / 52, 8 rows of 1 to 128 x 16 of 64 x 64 19 / 15.
+bool short_rows(const gdr_linattn_args *a) {
     const bool wide_k = a->K > 64, wide_v = a->V > 64;
-    if (wide_k && wide_v) return a->state_dtype == GDR_BF16 ? 32 : 16;
-    return wide_k || wide_v ? 48 : 96;
+    const int most = wide_k && wide_v ? (a->state_dtype == GDR_BF16 ? 32 : 16) : wide_k || wide_v ? 48 : 96;
+    if (a->max_row_len <= 0 || a->batch <= 0) return false;
+    const double units = (double)a->batch * a->nv * ((a->V + 127) / 128), longest = (double)a->max_row_len;
+    const double mean = std::fmin((double)a->total_tokens / a->batch, longest);
+    return (units > 2 * 152 ? 0.5 * (longest + mean) : longest) <= most;
 }
 
 bool takes_pieces(const gdr_linattn_args *a, bool tok_vec) {
-    return a->token_dtype == GDR_BF16 && tok_vec && a->max_row_len > 1 && a->max_row_len <= short_row_max(a);
+    return a->token_dtype == GDR_BF16 && tok_vec && a->max_row_len > 1 && short_rows(a);
 }
 
 bool takes_chunks(const gdr_linattn_args *a, bool tok_vec) {
-    return a->token_dtype == GDR_BF16 && tok_vec && a->total_tokens > 0 &&
-           (a->max_row_len <= 0 || a->max_row_len > short_row_max(a));
+    return a->token_dtype == GDR_BF16 && tok_vec && a->total_tokens > 0 && a->max_row_len != 1 && !short_rows(a);
 }
 
 bool token_vectors(const gdr_linattn_args *a) {

@@ -225,7 +225,7 @@ def test_short_rows_by_the_hundred(K, V, nk, nv, pool):
 
 @pytest.mark.parametrize("pool", [BF16, F32])
 @pytest.mark.parametrize("hint,nk,nv,K,V", [(32, 2, 4, 128, 128), (33, 2, 4, 128, 144), (17, 1, 8, 96, 256), (48, 4, 4, 64, 128),
-                                            (49, 1, 4, 48, 80), (47, 2, 8, 128, 64), (96, 8, 8, 64, 64), (97, 8, 8, 64, 64),
+                                            (49, 1, 4, 48, 80), (47, 2, 8, 128, 64), (56, 2, 16, 64, 128), (130, 2, 16, 48, 64), (96, 8, 8, 64, 64), (97, 8, 8, 64, 64),
                                             (80, 1, 16, 16, 16)])
 def test_rows_of_a_few_pieces(hint, nk, nv, K, V, pool):
     """Either side of where rows stop being short; lengths around multiples of 16, more units than fit at once."""
