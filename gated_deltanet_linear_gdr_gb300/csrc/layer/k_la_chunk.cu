@@ -84,8 +84,9 @@ template <bool STATES> constexpr int kTeams = STATES ? 3 : 1;
 constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 192, kColDS = 256, kColS = 384;
 
 enum Bar {
-    kLoaded = 0, kStageFree = kLoaded + kMaxStages, kPFull = kStageFree + kMaxStages, kPFree = kPFull + 2, kPtFull = kPFree + 2, kSFull, kDsFull = kSFull + 2,
-    kDsFree = kDsFull + 2, kKtFull, kOFull = kKtFull + 2, kOFree = kOFull + 2, kStateIn, kStateTurn, kDrain, kBars
+    kLoaded = 0, kStageFree = kLoaded + kMaxStages, kPFull = kStageFree + kMaxStages, kPFree = kPFull + 2,
+    kPtFull = kPFree + 2, kSFull, kDsFull = kSFull + 2, kDsFree = kDsFull + 2, kKtFull, kOFull = kKtFull + 2,
+    kOFree = kOFull + 2, kStateIn, kStateTurn, kDrain, kBars
 };
 
 struct Smem {

@@ -86,7 +86,8 @@ struct ShortUnit {
 // MANY: rows of more than 16 tokens, a chunk after the other.  Compiled apart, for the one-chunk form has no register
 // to spare (8 bytes spilled: 46 us for 40).
 template <typename ST, int KP, int VT, int MT, bool MANY>
-__global__ void __launch_bounds__(Lay<ST, KP, VT, MT>::THREADS, 2) k_la_small(const __grid_constant__ LaParams p, FastDiv per, FastDiv tiles) {
+__global__ void __launch_bounds__(Lay<ST, KP, VT, MT>::THREADS, 2)
+    k_la_small(const __grid_constant__ LaParams p, FastDiv per, FastDiv tiles) {
     using L = Lay<ST, KP, VT, MT>;
     constexpr int NT = L::THREADS, NK = KP / 8, CPS = 16 / (int)sizeof(ST);
     extern __shared__ __align__(16) unsigned char sm[];
@@ -221,8 +222,9 @@ __global__ void __launch_bounds__(Lay<ST, KP, VT, MT>::THREADS, 2) k_la_small(co
                             for (int nk = 0; nk < NK; ++nk)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
-                                    s[mt][nk][i] = *reinterpret_cast<const float *>(sm + 2 * L::TOK + buf * L::STATE + (8 * nk + c2 + (i & 1)) * L::SS +
-                                                                                    (v0 + mt * 16 + r4 + (i >> 1) * 8) * 4);
+                                    s[mt][nk][i] = *reinterpret_cast<const float *>(
+                                        sm + 2 * L::TOK + buf * L::STATE + (8 * nk + c2 + (i & 1)) * L::SS +
+                                        (v0 + mt * 16 + r4 + (i >> 1) * 8) * 4);
                         }
                     }
                 }
@@ -307,7 +309,8 @@ __global__ void __launch_bounds__(Lay<ST, KP, VT, MT>::THREADS, 2) k_la_small(co
 #pragma unroll
                             for (int i = 0; i < 4; ++i) s[mt][nk + e][i] *= lam_n;
 #pragma unroll
-                            for (int part = 0; part < (sizeof(ST) == 2 ? 2 : 3); ++part) mma(s[mt][nk + e], va[mt][part], k[2 * e], k[2 * e + 1]);
+                            for (int part = 0; part < (sizeof(ST) == 2 ? 2 : 3); ++part)
+                                mma(s[mt][nk + e], va[mt][part], k[2 * e], k[2 * e + 1]);
                         }
                 }
                 if (last) {  // the state goes back through its place in shared memory (a warp's columns are its own)
@@ -361,7 +364,9 @@ template <typename ST, int KP, int VT, int MT, bool MANY> cudaError_t go_form(co
     const cudaError_t e = launch_info(cache, &li, [](LaunchInfo &l) {
         const cudaError_t r =
             cudaFuncSetAttribute(k_la_small<ST, KP, VT, MT, MANY>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALL);
-        return r != cudaSuccess ? r : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&l.occ, k_la_small<ST, KP, VT, MT, MANY>, L::THREADS, L::ALL);
+        return r != cudaSuccess ? r
+                                : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&l.occ, k_la_small<ST, KP, VT, MT, MANY>,
+                                                                                L::THREADS, L::ALL);
     });
     if (e != cudaSuccess) return e;
     const unsigned tiles = (unsigned)(p.V + VT - 1) / VT, per = (unsigned)p.nv * tiles, units = (unsigned)p.batch * per;

@@ -285,6 +285,21 @@ def test_nothing_to_do():
     c.run()
 
 
+@pytest.mark.parametrize("hint", [0, 1, 5, 90, 5000])
+@pytest.mark.parametrize("tok", [BF16, F32])
+def test_no_tokens_at_all(hint, tok):
+    c = Case([0, 0, 0], 1, 2, 64, 64, tok, BF16, pad=(1,), seed=53)
+    out, pool = c.run(hint)
+    assert out.shape == (0, 2, 64) and torch.equal(pool, c.pool)
+
+
+@pytest.mark.parametrize("lens,hint", [([5, 9, 16, 1] * 9, 16), ([40, 3, 47] * 5, 48), ([3000, 5], 3000), ([700, 64] * 9, 700)])
+def test_every_form_repeats_bit_for_bit(lens, hint):
+    c = Case(lens, 2, 4, 64, 128, BF16, F32, seed=63)
+    a, b = c.run(hint), c.run(hint)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("hint", [0, 1])
 def test_repeats_bit_for_bit(hint):
     c = Case([1] * 9 if hint else [513, 64, 9], 2, 4, 128, 128, BF16, F32, seed=61)
