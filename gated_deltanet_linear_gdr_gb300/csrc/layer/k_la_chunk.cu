@@ -92,7 +92,10 @@ enum Bar {
 struct Smem {
     unsigned char ring[13 * kTile];       // Ring
     unsigned char pt[kSub];               // P~^T
-    unsigned char ost[kWarpsO][32 * 64];  // output on its way out, 32 tokens x 32 columns a warp
+    union {
+        unsigned char ost[kWarpsO][32 * 64];  // output on its way out, 32 tokens x 32 columns a warp
+        int load[kThreads / 4];               // before any: what each CTA has to do so far, in chunks (plan_rows)
+    };
     uint64_t bar[kBars];
     int row_t0[kMaxRows], row_len[kMaxRows], row_slot[kMaxRows];  // by rank: the longest row first; len -1: bad offsets
     int first[kMaxRows + 1];                                      // a ranked row's first segment
@@ -104,6 +107,10 @@ struct Smem {
     float next_lg2;
 };
 static_assert(sizeof(Smem) + 1024 <= 232448 && offsetof(Smem, ring) == 0, "shared memory");
+// Ordinary accesses are ordered before a TMA copy into the same bytes by a proxy
+// fence only; nothing but barriers lies between the deal and the first copies,
+// so it keeps to bytes that no copy writes.
+static_assert(offsetof(Smem, load) >= sizeof(Smem::ring), "the deal's memory is not TMA's");
 
 struct ChunkParams {
     LaParams p;
@@ -283,8 +290,8 @@ __device__ __forceinline__ void plan_rows(const ChunkParams &c, Smem &sm) {
     const bool planned = !c.seg && B <= kPlanned && (unsigned)B * c.per.d > gridDim.x && 4 * G <= kThreads && sm.row_len[0] >= 8 * kC;
     if (tid == 0) sm.planned = planned;
     if (planned) {
-        int *const load = reinterpret_cast<int *>(sm.ring);  // by CTA, in chunks; nothing is on its way yet
-        const int cta = tid >> 2, part = tid & 3;             // four threads compare for a CTA
+        int *const load = sm.load;
+        const int cta = tid >> 2, part = tid & 3;  // four threads compare for a CTA
         for (int o = tid; o < G; o += kThreads) load[o] = 0;
         __syncthreads();
         for (int r = 0; r < B; ++r) {
