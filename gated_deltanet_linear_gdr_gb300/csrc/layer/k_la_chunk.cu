@@ -4,38 +4,35 @@
 // tokens, i and j counted inside it:
 //
 //     P^T[j, i]  = k_j . q_i                                   (K Q^T)
-//     P~^T[j, i] = scale lambda^(i-j) P^T[j, i] for j <= i, else 0   -> bfloat16
+//     P~^T[j, i] = scale lambda^(i-j) P^T[j, i] for j <= i, else 0
 //     O^T[:, i]  = scale lambda^(i+1) (S0^T q_i)  +  V^T P~^T[:, i]
 //     S^T        = lambda^n S0^T + V^T K~,  K~[j] = lambda^(n-1-j) k_j
 //
 // Everything is kept transposed (value index = tensor memory lane), so that
 // the state, which a warp's lanes hold in float32 registers, goes back into
 // tensor memory as the A operand of S0^T Q^T, and V^T serves two products.
-// Rounding to bfloat16: P~ and the state as operand of the readout, once each,
-// as the output itself is; their errors are independent of the output's, so an
-// output is at most sqrt(2) as far off as its own rounding makes it (measured
-// 2.1e-3 against 1.7e-3).  The state itself loses nothing: it stays in
-// float32, and K~ is split into two (bfloat16 pool) or three (float32 pool)
-// bfloat16 parts, which keep 16 and 24 bits.
+// Operands made here go in as bfloat16 parts, each the rounding of what the ones
+// before leave: P~ and the state as operand of the readout in two (16 bits), K~
+// in two (bfloat16 pool) or three (float32 pool).  So results are rounded once,
+// whatever cancels in their sums.  (One part for P~ and the state, 8 bits, made
+// outputs off by 2.1e-3 of their norm for 1.7e-3, and by all of it where the
+// history cancels; it was 7 to 13% faster with 128 key channels.)
 //
 // One CTA per SM walks (row segment, value head, 128-column tile) units, with
 // a warp role for each step: 8 warps keep S, 4 make K~, 4 make P~, 4 write the
 // output, one each issues K Q^T, the state's product and the output's two, and
 // one loads three chunks ahead by TMA.  Roles hand over through mbarriers, so
 // the products of a chunk run under the elementwise work of its neighbours.
-// (A product of 64 x 128 x 16 holds the tensor cores for 32 to 64 cycles, but
-// its issuer, with its waits, for about 110: one issuing warp for all 28 of a
-// chunk measured 3100 cycles a chunk, the slowest of the roles.)
+// (One issuing warp for all products of a chunk was the slowest of the roles.)
 //
-// Bound: with every SM at work, HBM.  A chunk of one head with K = V = 128 moves
-// 64 KiB, 1.47 us of an SM's share, beside which shared memory (about 2200
-// cycles) and the tensor cores (37% of the time) fit.  4 rows of 4096 tokens x 38
-// heads, a unit an SM, take 112 us with a bfloat16 pool (85% of the measured copy
-// rate) and 120 with a float32 pool; heads of 64 x 64 76 us (63%), where the
-// roles' instructions (the SM issues in 39% of the cycles, waits for fetches) and
-// latencies set the pace, 1.2 us a chunk.  A row alone on its SM takes 1.3 us a
-// chunk (64 x 64: 1.0).  A unit costs 5 us to begin and end, of which its state's
-// exchange takes 1.5: rows of one chunk are the costly ones.
+// Bound: shared memory and HBM.  A chunk of one head with K = V = 128 moves 64 KiB,
+// 1.47 us of an SM's share of HBM, and about 280 KiB through shared memory, 2200
+// cycles; the role that makes K~ waits for that most.  4 rows of 4096 tokens x 38
+// heads, a unit an SM, take 126 us with a bfloat16 pool (76% of the measured copy
+// rate) and 132 with a float32 pool; heads of 64 x 64 79 us (61%), where the roles'
+// instructions and latencies set the pace, 1.2 us a chunk.  A row alone on its SM
+// takes 1.5 us a chunk (64 x 64: 1.1).  A unit costs 5 us to begin and end, of which
+// its state's exchange takes 1.5: rows of one chunk are the costly ones.
 #include "tc.cuh"
 
 #include "layer_internal.h"
@@ -55,14 +52,15 @@ constexpr int kTile = 2 * kSub;       // bytes of a 64-token x 128-channel opera
 // chunks: with two parts it fills half of its room, and a state on its way has
 // the rest.  Half as many key channels leave room for more chunks, without which
 // loads, not roles, set the pace (4 rows of 4096 tokens x 38 heads of 64 x 64: 85
-// us with three, 76 with five).
+// us with three, 76 with five, both with one part of the readout's operands).
 template <int KP, bool STATES> struct Ring {
     static constexpr int KB = KP / 64 * kSub;  // K's bytes, or Q's
     static constexpr int V = KB, Q = KB + kTile, BYTES = STATES ? KB + kTile : 2 * KB + kTile;
     static constexpr int N = KP == 64 ? (STATES ? 6 : 5) : (STATES ? 4 : 3);
     static constexpr int KT = KP == 64 ? 10 * kTile : 9 * kTile;  // of both kinds
     static constexpr int STATE = KT + 2 * KB;
-    static_assert(N * BYTES <= KT, "ring");
+    static constexpr int OST = 12 * kTile;  // with 64 key channels, where output is turned
+    static_assert(N * BYTES <= KT && KT + 4 * KB <= (KP == 64 ? OST : 13 * kTile) && STATE + KP * 256 <= (KP == 64 ? OST : 13 * kTile), "ring");
 };
 constexpr int kMaxStages = 6;
 constexpr int kMaxRows = 64, kMaxHeads = 64;  // rows and heads whose facts are kept in shared memory
@@ -80,21 +78,28 @@ static_assert(2 * kRegsS + kRegsO + kRegsP + kRegsK + kRegsRest == 6 * 80, "shar
 // Without output to make, the warps of P~ and O make K~ too.
 template <bool STATES> constexpr int kTeams = STATES ? 3 : 1;
 
-// tensor memory columns
-constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 192, kColDS = 256, kColS = 384;
+// Tensor memory columns: P^T, S0^T Q^T, V^T P~^T, V^T K~, the start state's two
+// parts.  All 512 are in use: with 64 key channels P^T and the start state have
+// two places, for one chunk and the next, with 128 only one.
+template <int KP> struct Cols {
+    static constexpr bool TWO = KP == 64;
+    static constexpr uint32_t P = 0, O1 = TWO ? 128 : 64, O2 = O1 + 128, DS = O2 + 64, S = 384, PART = KP / 2;
+    static constexpr uint32_t next(uint32_t odd) { return TWO ? odd * 64 : 0; }  // of P^T or the start state
+    static_assert(DS + KP <= S && S + (TWO ? 2 : 1) * 2 * PART <= 512, "tensor memory");
+};
 
 enum Bar {
     kLoaded = 0, kStageFree = kLoaded + kMaxStages, kPFull = kStageFree + kMaxStages, kPFree = kPFull + 2,
     kPtFull = kPFree + 2, kSFull, kDsFull = kSFull + 2, kDsFree = kDsFull + 2, kKtFull, kOFull = kKtFull + 2,
-    kOFree = kOFull + 2, kStateIn, kStateTurn, kDrain, kBars
+    kOFree = kOFull + 2, kO1Full, kStateIn = kO1Full + 2, kStateTurn, kDrain, kBars
 };
 
 struct Smem {
     unsigned char ring[13 * kTile];       // Ring
-    unsigned char pt[kSub];               // P~^T
+    unsigned char pt[kSub];               // P~^T, its first part
     union {
-        unsigned char ost[kWarpsO][32 * 64];  // output on its way out, 32 tokens x 32 columns a warp
-        int load[kThreads / 4];               // before any: what each CTA has to do so far, in chunks (plan_rows)
+        unsigned char pt_rest[kSub];      // and its second
+        int load[kThreads / 4];           // before any: what each CTA has to do so far, in chunks (plan_rows)
     };
     uint64_t bar[kBars];
     int row_t0[kMaxRows], row_len[kMaxRows], row_slot[kMaxRows];  // by rank: the longest row first; len -1: bad offsets
@@ -441,13 +446,15 @@ template <int KP> __device__ void role_mma_scores(const Ctx &x) {
     const uint64_t d_km = desc128(x.base, 16, 1024);  // stage 0, K-major
     const unsigned total = count_chunks<false>(x);
     for (unsigned g = 0; g < total; ++g) {
-        // the buffer has been read, and the last product into it has been seen by both its waiters
-        if (g > 1 && (!x.wait(kPFree + (g & 1), (g >> 1) - 1) || !x.wait(kKtFull + (g & 1), (g >> 1) - 1))) break;
+        // the place has been read, and the product before last, whose barrier this one's is, seen by both its waiters
+        constexpr unsigned ago = Cols<KP>::TWO ? 2 : 1;
+        if (g >= ago && !x.wait(kPFree + ((g - ago) & 1), (g - ago) >> 1)) break;
+        if (g > 1 && !x.wait(kKtFull + (g & 1), (g >> 1) - 1)) break;
         if (!x.wait(kLoaded + g % R::N, g / R::N)) break;
         fence_after();
         const uint32_t me = elect_one(), st = uniform(g % R::N), odd = uniform(g & 1);
         const uint64_t k = d_km + (st * R::BYTES >> 4), q = k + (R::Q >> 4);
-        mma_ss_k<KP / 16>(me, x.tmem + kColP + odd * kC, k, q, id, kSub);
+        mma_ss_k<KP / 16>(me, x.tmem + Cols<KP>::P + Cols<KP>::next(odd), k, q, id, kSub);
         mma_commit(me, x.bar(kPFull) + 8 * odd);
     }
     drain_mma(x);
@@ -474,12 +481,13 @@ template <int KP, int PARTS, bool STATES> __device__ void role_mma_state(const C
             fence_after();
             const uint32_t me = elect_one(), st = uniform(g % R::N), odd = uniform(g & 1);
             const uint64_t k = d_mn + (st * R::BYTES >> 4), v = k + (R::V >> 4), kt = d_kt + (odd * (PARTS - 1) * R::KB >> 4);
+            const uint32_t ds = x.tmem + Cols<KP>::DS;
             if (fresh)
-                mma_ss_mn64<false>(me, x.tmem + kColDS, v, k, id);
+                mma_ss_mn64<false>(me, ds, v, k, id);
             else
-                mma_ss_mn64<true>(me, x.tmem + kColDS, v, k, id);
-            mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt, id);
-            if (PARTS == 3) mma_ss_mn64<true>(me, x.tmem + kColDS, v, kt + (R::KB >> 4), id);
+                mma_ss_mn64<true>(me, ds, v, k, id);
+            mma_ss_mn64<true>(me, ds, v, kt, id);
+            if (PARTS == 3) mma_ss_mn64<true>(me, ds, v, kt + (R::KB >> 4), id);
             mma_commit(me, x.bar(kDsFull) + 8 * odd);
             if (STATES && j + 1 == u.chunks) mma_commit(me, x.bar(kOFull));
             mma_commit(me, x.bar(kStageFree) + 8 * st);
@@ -487,24 +495,29 @@ template <int KP, int PARTS, bool STATES> __device__ void role_mma_state(const C
     }
 }
 
-// S0^T Q^T and V^T P~^T
+// S0^T Q^T and V^T P~^T, two parts each.
 template <int KP> __device__ void role_mma_out(const Ctx &x) {
     using R = Ring<KP, false>;
     const uint32_t id1 = idesc_bf16(128, kC, false, false), id2 = idesc_bf16(128, kC, true, true);
     const uint64_t d_km = desc128(x.base + R::Q, 16, 1024), d_v = desc128(x.base + R::V, kSub, 1024);
     const uint64_t d_pt = desc128(x.base + (uint32_t)offsetof(Smem, pt), kSub, 1024);
+    const uint64_t d_rest = desc128(x.base + (uint32_t)offsetof(Smem, pt_rest), kSub, 1024);
     const unsigned total = count_chunks<false>(x);
     for (unsigned g = 0; g < total; ++g) {
-        if (!x.wait(kLoaded + g % R::N, g / R::N) || (g > 0 && !x.wait(kOFree, g - 1)) ||
-            !x.wait(kSFull + (g & 1), g >> 1))
-            break;
+        if (!x.wait(kLoaded + g % R::N, g / R::N) || !x.wait(kSFull + (g & 1), g >> 1)) break;
         fence_after();
         const uint32_t me = elect_one(), st = uniform(g % R::N), odd = uniform(g & 1);
-        const uint64_t q = d_km + (st * R::BYTES >> 4);
-        mma_ts_k<KP / 16>(me, x.tmem + kColO1, x.tmem + kColS + odd * 64, q, id1, kSub);
-        if (!x.wait(kPtFull, g)) break;
+        const uint64_t q = d_km + (st * R::BYTES >> 4), v = d_v + (st * R::BYTES >> 4);
+        using C = Cols<KP>;
+        const uint32_t o1 = x.tmem + C::O1 + odd * kC;  // read for the chunk before last, as kOFree has said for the last one
+        const uint32_t s0 = x.tmem + C::S + C::next(odd);
+        mma_ts_k<KP / 16, false>(me, o1, s0, q, id1, kSub);
+        mma_ts_k<KP / 16, true>(me, o1, s0 + C::PART, q, id1, kSub);
+        mma_commit(me, x.bar(kO1Full) + 8 * odd);
+        if (!x.wait(kPtFull, g) || (g > 0 && !x.wait(kOFree, g - 1))) break;
         fence_after();
-        mma_ss_mn64<false>(me, x.tmem + kColO2, d_v + (st * R::BYTES >> 4), d_pt, id2);
+        mma_ss_mn64<false>(me, x.tmem + C::O2, v, d_pt, id2);
+        mma_ss_mn64<true>(me, x.tmem + C::O2, v, d_rest, id2);
         mma_commit(me, x.bar(kOFull) + 8 * odd);
         mma_commit(me, x.bar(kStageFree) + 8 * st);
     }
@@ -596,59 +609,62 @@ template <int KP, int PARTS, bool STATES, int TEAMS> __device__ void role_keys(c
     }
 }
 
-// The state: lane = value index, 64 of its key indices in a thread's registers
-// (warps 0-3: 0..63, warps 4-7: 64..127).
-struct StateRole {
+// The state: lane = value index, half of its key indices in a thread's
+// registers (warps 0-3 the first half, warps 4-7 the second).
+template <int KP> struct StateRole {
+    static constexpr int KEYS = KP / 2, N = KEYS / 2;  // a thread's keys, and pairs of them
     int half, v;
     uint32_t lanes;
-    bool mine;
-    template <int KP> __device__ static StateRole of(int warp, int lane) {
-        return {warp >> 2, (warp & 3) * 32 + lane, (uint32_t)((warp & 3) * 32) << 16, (warp >> 2) * 64 < KP};
-    }
+    __device__ StateRole(int warp, int lane)
+        : half(warp >> 2), v((warp & 3) * 32 + lane), lanes((uint32_t)((warp & 3) * 32) << 16) {}
 };
 
 // s = lam s + what V^T K~ has left in tensor memory.
-__device__ __forceinline__ void state_add(const Ctx &x, const StateRole &r, float2 (&s)[32], float lam) {
-    if (r.mine) {
-        fence_after();
-        const float2 l2 = make_float2(lam, lam);
+template <int KP>
+__device__ __forceinline__ void state_add(const Ctx &x, const StateRole<KP> &r, float2 (&s)[KP / 4], float lam) {
+    fence_after();
+    const float2 l2 = make_float2(lam, lam);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t d[16];
-            tmem_ld16(x.tmem + r.lanes + kColDS + r.half * 64 + i * 16, d);
-            wait_ld();
+    for (int i = 0; i < r.KEYS / 16; ++i) {
+        uint32_t d[16];
+        tmem_ld16(x.tmem + r.lanes + Cols<KP>::DS + r.half * r.KEYS + i * 16, d);
+        wait_ld();
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                s[8 * i + e] = __ffma2_rn(l2, s[8 * i + e],
-                                          make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
-        }
-        fence_before();
+        for (int e = 0; e < 8; ++e)
+            s[8 * i + e] = __ffma2_rn(l2, s[8 * i + e], make_float2(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1])));
     }
+    fence_before();
     x.arrive(kDsFree);
 }
 
 // A unit's chunks; false where a wait gave up.
-__device__ __forceinline__ bool state_chunks(const Ctx &x, const StateRole &r, float2 (&s)[32], unsigned &g, int len, float lg2) {
+template <int KP>
+__device__ __forceinline__ bool state_chunks(const Ctx &x, const StateRole<KP> &r, float2 (&s)[KP / 4], unsigned &g, int len,
+                                             float lg2) {
+    using C = Cols<KP>;
     const float lam_c = power(lg2, kC);
-    for (int at = 0; at < len; at += kC, ++g) {
-        // the start state as matrix operand, in one of two buffers
-        if (g > 1 && !x.wait(kOFull + (g & 1), (g >> 1) - 1)) return false;  // the product that read it last is done
-        if (r.mine) {
-            fence_after();
+    for (int left = len; left > 0; left -= kC, ++g) {
+        // the start state as matrix operand, in two parts, once the product that read its place last is done
+        constexpr unsigned ago = C::TWO ? 2 : 1;
+        if (g >= ago && !x.wait(kO1Full + ((g - ago) & 1), (g - ago) >> 1)) return false;
+        fence_after();
+        const uint32_t to = x.tmem + r.lanes + C::S + C::next(g & 1) + r.half * r.N;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t h[16];
+        for (int i = 0; i < r.N / 8; ++i) {  // in pieces of 8 columns: registers are short
+            uint32_t h[8];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) h[e] = pack_bf16(s[16 * i + e]);
-                tmem_st16(x.tmem + r.lanes + kColS + (g & 1) * 64 + r.half * 32 + i * 16, h);
-            }
-            wait_st();
-            fence_before();
+            for (int e = 0; e < 8; ++e) h[e] = pack_bf16(s[8 * i + e]);
+            tmem_st8(to + i * 8, h);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] = pack_bf16(rest_bf16(s[8 * i + e], h[e]));
+            tmem_st8(to + C::PART + i * 8, h);
         }
+        wait_st();
+        fence_before();
         x.arrive(kSFull + (g & 1));
-        const float lam_n = len - at >= kC ? lam_c : power(lg2, len - at);
+        const float lam_n = left >= kC ? lam_c : power(lg2, left);
         if (!x.wait(kDsFull + (g & 1), g >> 1)) return false;
-        state_add(x, r, s, lam_n);
+        state_add<KP>(x, r, s, lam_n);
     }
     return true;
 }
@@ -661,44 +677,43 @@ __device__ __forceinline__ bool state_chunks(const Ctx &x, const StateRole &r, f
 // 64 stores a thread took 6000 cycles of the 8500 of a unit of one chunk:
 // instructions that run once a unit come from far away.
 template <int KP> __device__ void role_state_staged(const Ctx &x, int warp, int lane) {
-    const StateRole r = StateRole::of<KP>(warp, lane);
-    const uint32_t buf = x.base + Ring<KP, false>::STATE + (r.half * 64 * 128 + r.v) * 2;  // [KP][128]
+    const StateRole<KP> r(warp, lane);
+    const uint32_t buf = x.base + Ring<KP, false>::STATE + (r.half * r.KEYS * 128 + r.v) * 2;  // [KP][128]
     unsigned g = 0;
-    float2 s[32] = {};
+    float2 s[r.N] = {};
     for (unsigned units = 0;; ++units) {
         if (!x.wait(kStateIn, units)) return;
         const int len = (int)uniform((uint32_t)x.sm.next_len);
         const float lg2 = x.sm.next_lg2;
-        if (r.mine) {  // what lies outside the pool's rows and columns came in as zero; the first time nothing finished goes out
+        // what lies outside the pool's rows and columns came in as zero; the first time nothing finished goes out
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) exchange_bf16(buf + 2 * i * 256, s[i], s[i + 1], s[i + 2], s[i + 3]);
-        }
+        for (int i = 0; i < r.N; i += 4) exchange_bf16(buf + 2 * i * 256, s[i], s[i + 1], s[i + 2], s[i + 3]);
         fence_async_smem();
         x.arrive(kStateTurn);
-        if (len == 0 || !state_chunks(x, r, s, g, len, lg2)) return;
+        if (len == 0 || !state_chunks<KP>(x, r, s, g, len, lg2)) return;
     }
 }
 
 // Other states: a float32 pool, the segments' start states, and the segments' own (STATES).
 template <typename ST, int KP, bool STATES> __device__ void role_state(const Ctx &x, int warp, int lane) {
     const LaParams &p = x.c.p;
-    const StateRole r = StateRole::of<KP>(warp, lane);
+    const StateRole<KP> r(warp, lane);
     Walk<STATES> walk(x.c, x.sm);
     Unit u;
     unsigned g = 0;
-    float2 s[32];
+    float2 s[r.N];
     while (walk.next(u, false)) {
         if (u.chunks == 0) continue;
-        const bool on = r.mine && u.tile * 128 + r.v < p.V;
-        const int k0 = r.half * 64, kn = min(64, p.K - k0);
+        const bool on = u.tile * 128 + r.v < p.V;
+        const int k0 = r.half * r.KEYS, kn = min(r.KEYS, p.K - k0);
         ST *pool = static_cast<ST *>(p.state) + (long long)u.slot * p.st_slot + (long long)u.h * p.st_head + u.tile * 128 + r.v;
         float *ws = x.c.ws + ((long long)u.x * p.nv + u.h) * p.K * p.V + u.tile * 128 + r.v;
         // in groups of 16 key indices (K is a multiple of 16), each asked for at once
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] = make_float2(0.0f, 0.0f);
+        for (int i = 0; i < r.N; ++i) s[i] = make_float2(0.0f, 0.0f);
         if (!STATES && on) {
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < r.KEYS / 16; ++b) {
                 if (16 * b >= kn) break;
                 const float *from;
                 long long step;
@@ -715,13 +730,13 @@ template <typename ST, int KP, bool STATES> __device__ void role_state(const Ctx
         }
         if constexpr (STATES) {  // all of the segment's chunks have added up
             if (!x.wait(kOFull, g++)) return;
-            state_add(x, r, s, 0.0f);
+            state_add<KP>(x, r, s, 0.0f);
         } else {
-            if (!state_chunks(x, r, s, g, u.len, u.lg2)) return;
+            if (!state_chunks<KP>(x, r, s, g, u.len, u.lg2)) return;
         }
         if (on && (STATES || u.last)) {
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < r.KEYS / 16; ++b) {
                 if (16 * b >= kn) break;
                 if (STATES) {
                     float *to = ws + (long long)(k0 + 16 * b) * p.V;
@@ -748,16 +763,15 @@ template <int KP> __device__ void role_scores(const Ctx &x, int warp, int lane) 
     const uint32_t pt = x.base + (uint32_t)offsetof(Smem, pt);
     // stmatrix: lane l names row l % 8 of matrix l / 8: keys +0, +8, +0, +8 of query blocks n, n, n + 1, n + 1
     const int srow = warp * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, sblk = lane >> 4;
-    const uint32_t to = pt + srow * 128;
     Walk<false> walk(x.c, x.sm);
     Unit u;
     unsigned g = 0;
     while (walk.next(u, false)) {
         if (u.chunks == 0) continue;
-        float2 w[16];
+        float2 w[9];  // of block b and key row0 + 8 i: w[b + 1 - i]
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int gap = 8 * (i >> 1) + 2 * (lane & 3) - (row0 + (i & 1) * 8);
+        for (int i = 0; i < 9; ++i) {
+            const int gap = 8 * (i - 1) + 2 * (lane & 3) - row0;
             w[i].x = gap < 0 ? 0.0f : p.scale * power_fast(u.lg2, gap);
             w[i].y = gap < -1 ? 0.0f : p.scale * power_fast(u.lg2, gap + 1);
         }
@@ -766,22 +780,22 @@ template <int KP> __device__ void role_scores(const Ctx &x, int warp, int lane) 
             if (!x.wait(kPFull + (g & 1), g >> 1)) return;
             fence_after();
             uint32_t r[32];
-            tmem_ld_16x64(x.tmem + lanes + kColP + (g & 1) * kC, r);
+            tmem_ld_16x64(x.tmem + lanes + Cols<KP>::P + Cols<KP>::next(g & 1), r);
             wait_ld();
             fence_before();
             x.arrive(kPFree + (g & 1));
-            uint32_t h[16];
+            uint32_t h[16], rest[16];
 #pragma unroll
             for (int b = 0; b < 8; ++b) {
                 if (b < 2 * warp) {
-                    h[2 * b] = h[2 * b + 1] = 0;
+                    h[2 * b] = h[2 * b + 1] = rest[2 * b] = rest[2 * b + 1] = 0;
                     continue;
                 }
                 float2 e[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     e[i] = __fmul2_rn(make_float2(__uint_as_float(r[4 * b + 2 * i]), __uint_as_float(r[4 * b + 2 * i + 1])),
-                                      w[2 * b + i]);
+                                      w[b + 1 - i]);
                 if (b < 2 * warp + 2) {  // chosen, not multiplied: whatever a masked place holds stays out
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -790,22 +804,29 @@ template <int KP> __device__ void role_scores(const Ctx &x, int warp, int lane) 
                         if (gap < -1) e[i].y = 0.0f;
                     }
                 }
-                h[2 * b] = pack_bf16(e[0]);
-                h[2 * b + 1] = pack_bf16(e[1]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    h[2 * b + i] = pack_bf16(e[i]);
+                    rest[2 * b + i] = pack_bf16(rest_bf16(e[i], h[2 * b + i]));
+                }
             }
             if (__builtin_expect(n < kC, 0)) {
 #pragma unroll
                 for (int b = 0; b < 8; ++b) {
-                    if (row0 >= n) h[2 * b] = 0;
-                    if (row0 + 8 >= n) h[2 * b + 1] = 0;
+                    if (row0 >= n) h[2 * b] = rest[2 * b] = 0;
+                    if (row0 + 8 >= n) h[2 * b + 1] = rest[2 * b + 1] = 0;
                 }
                 clear_tail(x.sm.ring + g % R::N * R::BYTES + R::V, n, p.V - u.tile * 128 > 64 ? 2 : 1, warp * 32 + lane,
                            32 * kWarpsP);
             }
-            if (g > 0 && !x.wait(kOFull + ((g - 1) & 1), (g - 1) >> 1)) return;  // the product that read the last P~ is done
+            auto put = [&](uint32_t to, const uint32_t (&w)[16]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                stmatrix4(to + (((2 * i + sblk) ^ (srow & 7)) << 4), h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+                for (int i = 0; i < 4; ++i)
+                    stmatrix4(to + srow * 128 + (((2 * i + sblk) ^ (srow & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            };
+            if (g > 0 && !x.wait(kOFull + ((g - 1) & 1), (g - 1) >> 1)) return;  // the product that read the last P~ is done
+            put(pt, h);
+            put(x.base + (uint32_t)offsetof(Smem, pt_rest), rest);
             fence_async_smem();
             x.arrive(kPtFull);
         }
@@ -863,14 +884,17 @@ template <int KP> struct StateCopies {
     }
 };
 
-// The output: a warp has 32 columns of O^T, which it turns through shared
-// memory into rows of 64 bytes a token.
+// The output: a warp has 32 columns of O^T, which it turns into rows of 64 bytes
+// a token.  With 64 key channels it does so through shared memory; with 128 there is
+// no room left beside P~'s second part, and 8x8 blocks are turned in registers,
+// which takes 400 cycles more.
 template <int KP> __device__ void role_out(const Ctx &x, int warp, int lane, StateCopies<KP> *states) {
     const LaParams &p = x.c.p;
     uint16_t *const out = static_cast<uint16_t *>(p.out);
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    unsigned char *const ost = x.sm.ost[warp];
-    const uint32_t ost_a = x.base + (uint32_t)offsetof(Smem, ost) + warp * (32 * 64);
+    constexpr bool kStaged = KP == 64;
+    unsigned char *const ost = x.sm.ring + Ring<KP, false>::OST + warp * (32 * 64);  // 32 tokens x 32 columns
+    const uint32_t ost_a = x.base + Ring<KP, false>::OST + warp * (32 * 64);
     // staging: 16-byte block c of token t lies at block c ^ (t / 2 % 4) of its 64 bytes
     const int st_tok = (lane >> 4) * 8 + (lane & 7), st_blk = (lane >> 3) & 1;
     Walk<false> walk(x.c, x.sm);
@@ -885,30 +909,34 @@ template <int KP> __device__ void role_out(const Ctx &x, int warp, int lane, Sta
                                            (lane & 3) * 8) = make_uint4(0, 0, 0, 0);
         if (u.chunks == 0) continue;
         if (states && !states->turn()) return;
-        float2 f[8];
+        float2 f0[4];  // of the first 32 tokens; the others' are lambda^32 of theirs
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
+        for (int b = 0; b < 4; ++b) {
             const int i = 8 * b + 2 * (lane & 3);
-            f[b] = make_float2(p.scale * power_fast(u.lg2, i + 1), p.scale * power_fast(u.lg2, i + 2));
+            f0[b] = make_float2(p.scale * power_fast(u.lg2, i + 1), p.scale * power_fast(u.lg2, i + 2));
         }
+        const float lam32 = power_fast(u.lg2, 32);
         const bool on = col + (lane & 3) * 8 < p.V;
-        uint16_t *to = out + (long long)(u.t0 + lane / 4) * p.o_ts + (long long)u.h * p.o_hs + col + (lane & 3) * 8;
+        const bool on2[2] = {col < p.V, col + 16 < p.V};  // V is a multiple of 16
+        uint16_t *to = out + (long long)(u.t0 + lane / 4) * p.o_ts + (long long)u.h * p.o_hs + col +
+                       (kStaged ? (lane & 3) * 8 : (lane & 1) * 8 + (lane & 2) * 2);
         for (int j = 0; j < u.chunks; ++j, ++g) {
             const int n = min(kC, u.len - j * kC);
             if (!x.wait(kOFull + (g & 1), g >> 1)) return;
             fence_after();
-            uint32_t h[16];  // 32 tokens, packed; the first 32 go to staging before the others are read
+            // 32 tokens, packed; the first 32 leave the warp's registers before the others are read
+            uint32_t h[16];
             auto collect = [&](int ch) {
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {  // 16 of the columns
                     uint32_t a[16], b[16];
-                    tmem_ld_16x32(x.tmem + lanes + ((uint32_t)(hh * 16) << 16) + kColO1 + ch * 32, a);
-                    tmem_ld_16x32(x.tmem + lanes + ((uint32_t)(hh * 16) << 16) + kColO2 + ch * 32, b);
+                    tmem_ld_16x32(x.tmem + lanes + ((uint32_t)(hh * 16) << 16) + Cols<KP>::O1 + (g & 1) * kC + ch * 32, a);
+                    tmem_ld_16x32(x.tmem + lanes + ((uint32_t)(hh * 16) << 16) + Cols<KP>::O2 + ch * 32, b);
                     wait_ld();
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         h[hh * 8 + i] =
-                            pack_bf16(__ffma2_rn(f[ch * 4 + i / 2],
+                            pack_bf16(__ffma2_rn(ch ? __fmul2_rn(f0[i / 2], make_float2(lam32, lam32)) : f0[i / 2],
                                                  make_float2(__uint_as_float(a[2 * i]), __uint_as_float(a[2 * i + 1])),
                                                  make_float2(__uint_as_float(b[2 * i]), __uint_as_float(b[2 * i + 1]))));
                 }
@@ -929,18 +957,31 @@ template <int KP> __device__ void role_out(const Ctx &x, int warp, int lane, Sta
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int t = r * 8 + lane / 4;
-                    if (on && ch * 32 + t < n)
-                        *reinterpret_cast<uint4 *>(to + (long long)(ch * 32 + r * 8) * p.o_ts) =
-                            *reinterpret_cast<const uint4 *>(ost + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
+                    uint16_t *const here = to + (long long)(ch * 32 + r * 8) * p.o_ts;
+                    if constexpr (kStaged) {
+                        if (on && ch * 32 + t < n)
+                            *reinterpret_cast<uint4 *>(here) =
+                                *reinterpret_cast<const uint4 *>(ost + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
+                    } else {
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {  // 16 columns: words 0, 1 or 2, 3 of one of their two blocks
+                            uint32_t w0 = turn8x8(h[hh * 8 + r * 2]), w1 = turn8x8(h[hh * 8 + r * 2 + 1]);
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, lane & 1 ? w0 : w1, 1);
+                            (lane & 1 ? w0 : w1) = got;
+                            if (on2[hh] && ch * 32 + t < n) *reinterpret_cast<uint2 *>(here + hh * 16) = make_uint2(w0, w1);
+                        }
+                    }
                 }
             };
             collect(0);
-            stage();
+            if constexpr (kStaged) stage(); else write(0);
             collect(1);
             fence_before();
             x.arrive(kOFree);
-            write(0);
-            stage();
+            if constexpr (kStaged) {
+                write(0);
+                stage();
+            }
             write(1);
             to += (long long)kC * p.o_ts;
         }
@@ -948,7 +989,10 @@ template <int KP> __device__ void role_out(const Ctx &x, int warp, int lane, Sta
     if (states) states->store();
 }
 
-template <typename ST, int KP, bool STATES>
+// STAGED: a bfloat16 pool's states by TMA; compiled apart from the other form of
+// the state's role, beside which neither has the registers it needs (4 rows of
+// 4096 tokens x 38 heads, bfloat16 pool: 136 us together).
+template <typename ST, int KP, bool STATES, bool STAGED>
 __global__ void __launch_bounds__(kThreads, 1)
     k_la_chunk(const __grid_constant__ ChunkParams c, const __grid_constant__ CUtensorMap mq,
                const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -1002,7 +1046,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < kWarpO) {
         regs_up<kRegsS>();
-        if (sizeof(ST) == 2 && !STATES && !c.seg)
+        if constexpr (STAGED)
             role_state_staged<KP>(x, warp - kWarpS, lane);
         else
             role_state<ST, KP, STATES>(x, warp - kWarpS, lane);
@@ -1010,7 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kRegsO > 80) regs_up<kRegsO>();
         if constexpr (!STATES) {
             StateCopies<KP> states(x, &ms);
-            const bool mine = warp == kWarpO && sizeof(ST) == 2 && !c.seg;
+            const bool mine = STAGED && warp == kWarpO;
             role_out<KP>(x, warp - kWarpO, lane, mine ? &states : nullptr);
             if (mine && lane == 0 && sm.state_loads) {  // no state's copy is in flight when the CTA ends
                 volatile int never = 0;
@@ -1138,10 +1182,12 @@ template <typename ST, int KP> cudaError_t go(ChunkParams c, const CUtensorMap *
     static LaunchCache cache;
     LaunchInfo li;
     constexpr int smem = (int)sizeof(Smem) + 1024;
+    constexpr bool kStages = sizeof(ST) == 2;
     cudaError_t e = launch_info(cache, &li, [](LaunchInfo &) {
-        cudaError_t r = cudaFuncSetAttribute(k_la_chunk<ST, KP, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (r == cudaSuccess)
-            r = cudaFuncSetAttribute(k_la_chunk<ST, KP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaError_t r = cudaSuccess;
+        for (const void *f : {(const void *)k_la_chunk<ST, KP, false, false>, (const void *)k_la_chunk<ST, KP, true, false>,
+                              (const void *)k_la_chunk<ST, KP, false, kStages>})
+            if (r == cudaSuccess) r = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         return r;
     });
     if (e != cudaSuccess) return e;
@@ -1150,11 +1196,13 @@ template <typename ST, int KP> cudaError_t go(ChunkParams c, const CUtensorMap *
     const long long rows = c.seg ? p.batch + p.T / c.seg : p.batch;
     const unsigned grid = (unsigned)(rows * per < li.sms ? rows * per : li.sms);
     if (c.seg) {
-        k_la_chunk<ST, KP, true><<<grid, kThreads, smem, s>>>(c, m[0], m[1], m[2], m[3]);
+        k_la_chunk<ST, KP, true, false><<<grid, kThreads, smem, s>>>(c, m[0], m[1], m[2], m[3]);
         const dim3 jg((unsigned)((p.K * p.V + 1023) / 1024), (unsigned)p.nv, (unsigned)p.batch);
         k_la_join<ST><<<jg, 256, 0, s>>>(c);
+        k_la_chunk<ST, KP, false, false><<<grid, kThreads, smem, s>>>(c, m[0], m[1], m[2], m[3]);
+    } else {
+        k_la_chunk<ST, KP, false, kStages><<<grid, kThreads, smem, s>>>(c, m[0], m[1], m[2], m[3]);
     }
-    k_la_chunk<ST, KP, false><<<grid, kThreads, smem, s>>>(c, m[0], m[1], m[2], m[3]);
     return cudaGetLastError();
 }
 

@@ -151,12 +151,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(a));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-        ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+// The same back, 8 columns.
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 // 16 lanes x 64 columns in the layout of an m16n8 accumulator, eight times over:
 // r[4n], r[4n+1]: lane t/4, columns 8n + 2(t%4), +1; r[4n+2], r[4n+3]: lane t/4 + 8.
@@ -243,9 +242,9 @@ template <int STEPS> __device__ __forceinline__ void mma_ss_k(uint32_t me, uint3
     }
 }
 // The same with A in tensor memory, 8 columns a step.
-template <int STEPS>
+template <int STEPS, bool ACC>
 __device__ __forceinline__ void mma_ts_k(uint32_t me, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t block) {
-    mma_ts<false>(me, d, a, b, idesc);
+    mma_ts<ACC>(me, d, a, b, idesc);
 #pragma unroll
     for (int i = 1; i < STEPS; ++i)
         mma_ts<true>(me, d, a + i * 8, b + (((uint32_t)(i >> 2) * block + (uint32_t)(i & 3) * 32) >> 4), idesc);
@@ -269,7 +268,13 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b,
                  "r"(d)
                  : "memory");
 }
-// The same with each 8x8 matrix transposed.
+// An 8x8 matrix of 16-bit values, two neighbours of row lane / 4 in a lane, transposed.
+__device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// stmatrix4 with each 8x8 matrix transposed.
 __device__ __forceinline__ void stmatrix4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
                  "r"(c), "r"(d)
