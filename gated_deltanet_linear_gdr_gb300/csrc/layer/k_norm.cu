@@ -47,7 +47,7 @@ template <int XB> cudaError_t go_boundary(const NormParams &p, cudaStream_t s) {
 
 cudaError_t launch_norm(const NormParams &p, int vec, cudaStream_t s) {
     if (vec < 8) return vec == 2 ? launch_norm_pairs(p, s) : launch_norm_odd(p, s);
-    if (p.x && !p.res && p.gate && p.g_es && p.post && !p.pre && p.out && p.out_bf16 && p.D <= 256) {
+    if (p.x && !p.res && !p.res_out && p.gate && p.g_es && p.post && !p.pre && p.out && p.out_bf16 && p.D <= 256) {
         if (p.gate_bf16)
             return p.x_bf16 ? go_heads<Cfg<1, 1, 1, 0, 0, 1, 0, 1>>(p, s) : go_heads<Cfg<0, 1, 1, 0, 0, 1, 0, 1>>(p, s);
         return p.x_bf16 ? go_heads<Cfg<1, 1, 0, 0, 0, 1, 0, 1>>(p, s) : go_heads<Cfg<0, 1, 0, 0, 0, 1, 0, 1>>(p, s);

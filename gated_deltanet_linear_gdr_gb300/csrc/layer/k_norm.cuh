@@ -132,6 +132,7 @@ __device__ __forceinline__ float row_sum(float v, float *buf) {
 // takes about 250 instructions with everything read from the parameters, which
 // at 128 values a row is twice what HBM allows; about 90 with it known.
 // GATE: 1 a gate with a value for each channel, 0 none or one with a value for each row.
+// RES: 0 neither a residual nor a residual_out.
 template <int XB, int GATE, int GB, int RES, int RB, int POST, int PRE, int OB> struct Cfg {
     static constexpr int x = XB < 0 ? -1 : 1, x_bf16 = XB, gate = GATE == 1 ? 1 : -1, gate_elem = GATE, gate_bf16 = GB, res = RES,
                          res_bf16 = RB, post = POST, pre = PRE, out_bf16 = OB;
@@ -250,13 +251,13 @@ template <class C, int VEC, int NV, int TPR> struct Row {
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) u[i][j] = is<C::x>(p.x != nullptr) ? fmaf(p.scale, u[i][j], y[j]) : y[j];
             }
-            if (p.res_out && live) {
-                const long long at = t * p.ro_ts + h * p.ro_hs;
+        }
+        if (C::res != 0 && p.res_out && live) {  // h, with a residual or without
+            const long long at = t * p.ro_ts + h * p.ro_hs;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    const int e = (i * TPR + lane) * VEC;
-                    if (e < p.D) put<VEC>(p.res_out, at + e, is<C::res_bf16>(p.res_bf16), u[i]);
-                }
+            for (int i = 0; i < NV; ++i) {
+                const int e = (i * TPR + lane) * VEC;
+                if (e < p.D) put<VEC>(p.res_out, at + e, is<C::res_bf16>(p.res_bf16), u[i]);
             }
         }
         if (!p.out) return;

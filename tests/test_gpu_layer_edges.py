@@ -1,11 +1,14 @@
 """Corners of the layer operators that a call meets seldom."""
 from __future__ import annotations
 
+import ctypes
+
 import pytest
 import torch
 
 import gated_deltanet_linear_gdr_gb300 as gdr
-from tests.layer_helpers import check_linattn, linattn_ref
+from gated_deltanet_linear_gdr_gb300 import _binding as B
+from tests.layer_helpers import U16, U32, check_linattn, linattn_ref, norm_ref
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -39,3 +42,36 @@ def test_units_dealt_by_load(K, pool):
             check_linattn(out, state, linattn_ref(q, k, v, lam, start, slot, off), 700, True)
         assert torch.equal(out, first[0]) and torch.equal(state, first[1])
     assert gdr.gdr_get_status() == 0
+
+
+@pytest.mark.parametrize("heads,D", [(3, 64), (2, 128), (1, 1024), (1, 4096), (2, 66), (1, 2047)])
+@pytest.mark.parametrize("x_dtype,h_dtype", [(BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("post", [False, True])
+@pytest.mark.parametrize("with_out", [False, True])
+def test_residual_out_without_a_residual(heads, D, x_dtype, h_dtype, post, with_out):
+    """The C entry's residual_out is h, and h is u where there is no residual; rows past the last stay as they were."""
+    T = 5
+    x, gate, w = _randn(T, heads, D, dtype=x_dtype), _randn(T, heads, D, dtype=x_dtype, seed=1), 1 + 0.1 * _randn(D, seed=2)
+    h = torch.full((T + 1, heads, D), 7.0, dtype=h_dtype, device=DEV)
+    out = torch.full((T + 1, heads, D), 7.0, dtype=BF16, device=DEV)
+    a = B.gdr_norm_args()
+    types = {BF16: B.GDR_BF16, F32: B.GDR_F32}
+    for n, value in dict(tokens=T, heads=heads, D=D, eps=1e-6, residual_scale=0.3, has_post_norm=post, has_pre_norm=True,
+                         activation=1, x_dtype=types[x_dtype], gate_dtype=types[x_dtype], residual_dtype=types[h_dtype],
+                         out_dtype=B.GDR_BF16, x=x.data_ptr(), gate=gate.data_ptr(), gate_elem_stride=1,
+                         residual_out=h.data_ptr(), post_weight=w.data_ptr(), pre_weight=w.data_ptr()).items():
+        setattr(a, n, value)
+    for n in ("x", "gate", "residual_out") + (("out",) if with_out else ()):
+        setattr(a, n + "_seq_stride", heads * D)
+        setattr(a, n + "_head_stride", D)
+    if with_out:
+        a.out = out.data_ptr()
+    assert B.load_library().gdr_block_norm(ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == B.GDR_OK
+    rh, rout = norm_ref(x, gate=gate, act="silu", post=post, post_w=w, pre=True, pre_w=w)
+    for got, want in [(h, rh)] + ([(out, rout)] if with_out else []):
+        rms = want.pow(2).mean(-1, keepdim=True).sqrt()  # a row's statistics: as in the tests of the norms
+        tol = 32 * (D + 40) * U32 * (want.abs() + rms) + (U16 if got.dtype == BF16 else 0.0) * want.abs() + 1e-30
+        assert bool(((got[:T].double() - want).abs() <= tol).all())
+        assert bool((got[T:] == 7.0).all())
+    if not with_out:
+        assert bool((out == 7.0).all())
