@@ -123,10 +123,8 @@ __global__ void __launch_bounds__(Lay<ST, KP, VT, MT>::THREADS, 2)
             } else if (u.slot >= 0 && tid == 0) {
                 flag(p.status, GDR_STATUS_BAD_DECAY);
             }
-            const int w8 = min(VT, p.V - u.col0) / 8;
             uint16_t *out = static_cast<uint16_t *>(p.out) + (long long)t0 * p.o_ts + (long long)u.h * p.o_hs + u.col0;
-            for (int i = tid; i < len * w8; i += NT)
-                *reinterpret_cast<uint4 *>(out + (long long)(i / w8) * p.o_ts + i % w8 * 8) = make_uint4(0, 0, 0, 0);
+            clear_rows(out, p.o_ts, len, min(VT, p.V - u.col0), true, tid, NT);
             return u;
         }
         u.len = len;

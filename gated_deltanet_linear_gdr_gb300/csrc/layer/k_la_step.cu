@@ -106,7 +106,7 @@ template <typename TT> __device__ __forceinline__ bool step_unit(const LaParams 
             flag(p.status, GDR_STATUS_BAD_DECAY);
         }
         TT *out = static_cast<TT *>(p.out) + (long long)t0 * p.o_ts + (long long)u.h * p.o_hs + u.col0;
-        for (int i = tid; i < u.len * u.W; i += nt) out[(long long)(i / u.W) * p.o_ts + i % u.W] = from_f32<TT>(0.0f);
+        clear_rows(out, p.o_ts, u.len, u.W, p.tok_vec, tid, nt);
         return false;
     }
     u.lam = p.decay_is_log ? expf(d) : d;

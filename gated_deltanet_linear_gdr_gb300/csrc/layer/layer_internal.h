@@ -74,4 +74,22 @@ cudaError_t launch_norm(const NormParams &p, int vec, cudaStream_t s);
 cudaError_t launch_norm_pairs(const NormParams &p, cudaStream_t s);
 cudaError_t launch_norm_odd(const NormParams &p, cudaStream_t s);
 
+#ifdef __CUDACC__
+// A skipped row's output: zeros over rows x width elements (a multiple of 8 up to
+// 128), by the whole CTA of at least 32 threads.  vec: rows are 16-byte vectors.
+template <typename TT>
+__device__ __forceinline__ void clear_rows(TT *out, long long row_stride, int rows, int width, bool vec, int tid, int threads) {
+    const int across = width / 8, down = threads / across, c = tid % across * 8;
+    if (tid >= across * down) return;
+    for (unsigned t = (unsigned)(tid / across); t < (unsigned)rows; t += (unsigned)down) {
+        TT *const to = out + (long long)t * row_stride + c;
+        if (vec) {
+            for (int j = 0; j < 8 * (int)sizeof(TT) / 16; ++j) reinterpret_cast<uint4 *>(to)[j] = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int j = 0; j < 8; ++j) to[j] = TT(0);  // all bits zero in either type
+        }
+    }
+}
+#endif
+
 }  // namespace gdr

@@ -75,3 +75,36 @@ def test_residual_out_without_a_residual(heads, D, x_dtype, h_dtype, post, with_
         assert bool((got[T:] == 7.0).all())
     if not with_out:
         assert bool((out == 7.0).all())
+
+
+def _token(heads, dim, T, seed):
+    """One token's values for all T, by a stride of 0."""
+    return _randn(1, heads, dim, dtype=BF16, seed=seed).expand(T, heads, dim)
+
+
+def _skipped(T, K, V, out, slot, max_row_len, flags):
+    """A call of one row that is skipped: its output has to be cleared."""
+    off = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    pool = _randn(1, 1, K, V, dtype=BF16)
+    keep = pool.clone()
+    gdr.gdr_get_status(clear=True)
+    args = _token(1, K, T, 1), _token(1, K, T, 2), _token(1, V, T, 3), torch.ones(1, device=DEV), pool
+    gdr.gdr_linattn_fwd(*args, torch.tensor([slot], dtype=torch.int32, device=DEV), off, out, max_row_len=max_row_len)
+    assert gdr.status_names(gdr.gdr_get_status()) == flags
+    assert torch.equal(pool, keep)
+
+
+def test_a_skipped_row_of_more_than_2_to_the_31_outputs():
+    T = 2 ** 24 + 5
+    out = torch.full((T + 1, 1, 128), 7.0, dtype=BF16, device=DEV)
+    _skipped(T, 128, 128, out[:T], -1, 0, [])
+    assert not bool(out[:T].any()) and bool((out[T] == 7.0).all())
+
+
+def test_a_row_far_past_its_bound():
+    """The short form, whose rows are told apart by their length: zeros of 2^31 + 48 vectors, on top of one another."""
+    T = 2 ** 27 + 3
+    buf = torch.full((T * 8 + 136,), 7.0, dtype=BF16, device=DEV)
+    _skipped(T, 64, 128, buf.as_strided((T, 1, 128), (8, 128, 1)), 0, 16, ["ROW_TOO_LONG"])
+    end = (T - 1) * 8 + 128
+    assert not bool(buf[:end].any()) and bool((buf[end:] == 7.0).all())
