@@ -261,7 +261,7 @@ template <bool STATES> struct Walk {
             u.len = u.last ? u.len - at : c.seg;
             if (STATES && u.last) u.len = 0;
         }
-        u.chunks = (u.len + kC - 1) / kC;
+        u.chunks = pieces(u.len, kC);
         return true;
     }
 };
@@ -310,14 +310,14 @@ __device__ __forceinline__ void plan_rows(const ChunkParams &c, Smem &sm) {
             __syncthreads();
             if (cta < G && part == 0) {
                 const int heads = (int)c.per.d, units = n < heads ? (heads - n - 1) / G + 1 : 0;
-                load[cta] += units * ((max(sm.row_len[r], 0) + kC - 1) / kC + 2);  // two chunks' time to begin and end one
+                load[cta] += units * (pieces(sm.row_len[r], kC) + 2);  // two chunks' time to begin and end one
                 if (cta == (int)blockIdx.x) sm.rank[r] = n;
             }
             __syncthreads();
         }
     }
     if (c.seg && tid < 32) {  // one lane a row
-        int end = tid < B ? max(1, (sm.row_len[tid] + c.seg - 1) / c.seg) : 0;
+        int end = tid < B ? max(1, pieces(sm.row_len[tid], c.seg)) : 0;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, end, m);
@@ -904,8 +904,8 @@ template <int KP> __device__ void role_out(const Ctx &x, int warp, int lane, Sta
     while (walk.next(u, warp == 0 && lane == 0)) {
         const int col = u.tile * 128 + warp * 32;
         if (col + (lane & 3) * 8 < p.V)
-            for (int t = lane / 4; t < u.skip_len; t += 8)
-                *reinterpret_cast<uint4 *>(out + (long long)(u.skip_t0 + t) * p.o_ts + (long long)u.h * p.o_hs + col +
+            for (unsigned t = lane / 4; t < (unsigned)u.skip_len; t += 8)
+                *reinterpret_cast<uint4 *>(out + ((long long)u.skip_t0 + t) * p.o_ts + (long long)u.h * p.o_hs + col +
                                            (lane & 3) * 8) = make_uint4(0, 0, 0, 0);
         if (u.chunks == 0) continue;
         if (states && !states->turn()) return;
@@ -1104,9 +1104,9 @@ template <typename ST> __global__ void __launch_bounds__(256) k_la_join(const __
         int rank = 0;
         for (int q = 0; q < B; ++q) rank += s_len[q] > s_len[o] || (s_len[q] == s_len[o] && q < o);
         if (rank == r) b = o;
-        if (rank < r) before += max(1, (s_len[o] + c.seg - 1) / c.seg);
+        if (rank < r) before += max(1, pieces(s_len[o], c.seg));
     }
-    const int n = (s_len[b] + c.seg - 1) / c.seg, slot = p.slot_idx[b];
+    const int n = pieces(s_len[b], c.seg), slot = p.slot_idx[b];
     const float lg2 = log2_lambda(p, h);
     if (n <= 0 || slot < 0 || slot >= p.max_slots || isnan(lg2) || (p.max_len > 0 && s_len[b] > p.max_len)) return;
     const float lam = power(lg2, c.seg);

@@ -243,8 +243,9 @@ __global__ void __launch_bounds__(2048 / R, 2) k_la_rows(const __grid_constant__
 #pragma unroll
             for (int j = 0; j < C; ++j) s[r][i][j] = on[i] ? raw[r][i].get(j) : 0.0f;
 
-    for (int base = 0; base < u.len; base += kTok) {
-        const int n = min(kTok, u.len - base);
+    const unsigned len = (unsigned)u.len;
+    for (unsigned base = 0; base < len; base += kTok) {
+        const int n = (int)min((unsigned)kTok, len - base);
         for (int t = 0; t < n; ++t) {
             float o[NC][C];
 #pragma unroll
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(2048 / R, 2) k_la_rows(const __grid_constant__
                     }
                     o[i][j] = acc;
                 }
-            if (base + t + 1 < u.len) fetch();
+            if (base + t + 1 < len) fetch();
             if (pair) {
 #pragma unroll
                 for (int i = 0; i < NC; ++i)

@@ -12,6 +12,13 @@ int api_fail(int code, const char *text);
 int api_ok();
 int api_status(unsigned **out);
 
+// How many pieces of `size` make up n, which may be as large as an int gets: rows
+// may have up to 2^31 - 1 tokens.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+constexpr int pieces(int n, int size) { return n <= 0 ? 0 : (n - 1) / size + 1; }
+
 // One decayed linear attention call, after validation.  Strides in elements.
 struct LaParams {
     int batch, nv, nk, r;  // r = nv / nk
