@@ -539,9 +539,16 @@ _DTYPES = {torch.float32: GDR_F32, torch.bfloat16: GDR_BF16}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _current(t: torch.Tensor) -> int:
-    """The current stream of a CUDA tensor's device."""
-    return _raw_stream(t.get_device()) if _raw_stream is not None else _stream(t.device)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _launch(fn, args, device: int) -> int:
+    """fn(args, stream) on a device's current stream; a C entry launches on the
+    current device, which is changed around the call where it is another."""
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return fn(args, _stream(device))
+    return fn(args, _raw_stream(device) if _raw_stream is not None else _stream(device))
 
 
 def _refuse(device, dtypes, **tensors):
@@ -647,7 +654,7 @@ def gdr_linattn_fwd(q, k, v, decay, state, slot_idx, offsets, out=None, *, decay
     lib = _lib or load_library()
     if max_row_len != 1:
         args, workspace = _linattn_workspace(lib, args, q.device, workspace)
-    rc = lib.gdr_linattn_fwd(args, _current(q))
+    rc = _launch(lib.gdr_linattn_fwd, args, q.get_device())
     if rc:
         _check(rc)
     return out
@@ -727,7 +734,7 @@ def gdr_gate_norm(x, gate, weight=None, out=None, *, eps=1e-6, activation="silu"
     args = _pack_norm(T, shape[1] if len(shape) == 3 else 1, D, xd, gd, 0, od, _activation(activation),
                       1 if gate_first else 0, 1, 0, 1 if centered else 0, eps, 1.0, x.data_ptr(), xt, xh, gp, gt, gh, ge,
                       0, 0, 0, 0, 0, 0, out.data_ptr(), ot, oh, _weight(weight, D, "weight", dev), 0)
-    rc = (_lib or load_library()).gdr_block_norm(args, _current(x))
+    rc = _launch((_lib or load_library()).gdr_block_norm, args, x.get_device())
     if rc:
         _check(rc)
     return out
@@ -784,7 +791,7 @@ def gdr_residual_norm(block, residual, weight, *, post_weight=None, gate=None, a
                       1 if centered else 0, eps, residual_scale, xp, xt, 0, gp, gt, 0, ge, residual.data_ptr(), rt, 0,
                       rop, rot, 0, out.data_ptr(), ot, 0, _weight(post_weight, D, "post_weight", dev),
                       _weight(weight, D, "weight", dev))
-    rc = (_lib or load_library()).gdr_block_norm(args, _current(residual))
+    rc = _launch((_lib or load_library()).gdr_block_norm, args, residual.get_device())
     if rc:
         _check(rc)
     return h, out
@@ -832,6 +839,9 @@ class Prepared:
 
     def __call__(self, stream: Optional[int] = None):
         s = _stream(self._device) if stream is None else stream
+        if self._device.index not in (None, _current_device()):  # a C entry launches on the current device
+            with torch.cuda.device(self._device):
+                return _check(self._fn(ctypes.byref(self._args), *self._extra, s))
         _check(self._fn(ctypes.byref(self._args), *self._extra, s))
 
 
