@@ -102,11 +102,26 @@ __device__ __forceinline__ void put(void *base, long long at, bool bf16, const f
     }
 }
 
+// exp(x) to 2^-22: what rounding x log2(e) loses, which an fma gives exactly, and
+// log2(e)'s own next digits are put right behind the power of two.
+__device__ __forceinline__ float exp_near(float x) {
+    constexpr float kL = 1.44269502f, kRest = 1.92596299e-8f, kLn2 = 0.693147181f;  // log2(e) = kL + kRest
+    const float t = x * kL, lost = fabsf(x) < 200.0f ? fmaf(x, kRest, fmaf(x, kL, -t)) : 0.0f;  // past that e^x is 0 or infinity
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(t));
+    return y * fmaf(lost, kLn2, 1.0f);
+}
 // act(g): g, g / (1 + exp(-g)) or 1 / (1 + exp(-g)); exp(-g) may overflow to
-// infinity, whose quotient is the right limit of 0.
-__device__ __forceinline__ float activate(float g, int act) {
+// infinity, whose quotient is the right limit of 0; a quotient below 2^-126 is 0
+// too.  FAST: where every output is rounded to bfloat16, the exponential is good to
+// 2^-22 and |g| 2^-24, which otherwise would show (7 units of float32 at -80).
+template <bool FAST> __device__ __forceinline__ float activate(float g, int act) {
     if (act == 0) return g;
-    const float s = __fdividef(1.0f, 1.0f + __expf(-g));  // 0 where the quotient is below 2^-126
+    float s;
+    if (FAST)
+        s = __fdividef(1.0f, 1.0f + __expf(-g));
+    else
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + exp_near(-g)));
     return act == 1 ? g * s : s;
 }
 
@@ -136,6 +151,7 @@ __device__ __forceinline__ float row_sum(float v, float *buf) {
 template <int XB, int GATE, int GB, int RES, int RB, int POST, int PRE, int OB> struct Cfg {
     static constexpr int x = XB < 0 ? -1 : 1, x_bf16 = XB, gate = GATE == 1 ? 1 : -1, gate_elem = GATE, gate_bf16 = GB, res = RES,
                          res_bf16 = RB, post = POST, pre = PRE, out_bf16 = OB;
+    static constexpr bool coarse = OB == 1 && (RES == 0 || RB == 1);  // no output in float32
 };
 using Any = Cfg<-1, -1, -1, -1, -1, -1, -1, -1>;
 template <int F> __device__ __forceinline__ bool is(bool runtime) { return F < 0 ? runtime : F != 0; }
@@ -207,7 +223,7 @@ template <class C, int VEC, int NV, int TPR> struct Row {
     }
 
     __device__ __forceinline__ void gate_by(const NormParams &p, float (&u)[NV][VEC], int lane) const {
-        const float all = is<C::gate_elem>(p.g_es) ? 1.0f : activate(g0, p.act);
+        const float all = is<C::gate_elem>(p.g_es) ? 1.0f : activate<C::coarse>(g0, p.act);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if ((i * TPR + lane) * VEC >= p.D) continue;
@@ -216,7 +232,7 @@ template <class C, int VEC, int NV, int TPR> struct Row {
                 g[i].get(is<C::gate_bf16>(p.gate_bf16), y);
                 if (p.act) {
 #pragma unroll
-                    for (int j = 0; j < VEC; ++j) y[j] = activate(y[j], p.act);
+                    for (int j = 0; j < VEC; ++j) y[j] = activate<C::coarse>(y[j], p.act);
                 }
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) u[i][j] *= y[j];

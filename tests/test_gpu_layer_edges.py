@@ -108,3 +108,36 @@ def test_a_row_far_past_its_bound():
     _skipped(T, 64, 128, buf.as_strided((T, 1, 128), (8, 128, 1)), 0, 16, ["ROW_TOO_LONG"])
     end = (T - 1) * 8 + 128
     assert not bool(buf[:end].any()) and bool((buf[end:] == 7.0).all())
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+@pytest.mark.parametrize("D,form", [(64, "gate"), (1024, "gate"), (66, "gate"), (2047, "gate"), (64, "row"), (1024, "residual"),
+                                    (2047, "residual")])
+def test_activations_in_float32(act, D, form):
+    """Values of 1 and -1, whose norm is themselves, so that what a float32 output is off by is the activation's error:
+    two units of the exponential, the sum's, the quotient's and the product's rounding, under 2^-21 altogether."""
+    T = 64
+    x = torch.where(_randn(T, D) > 0, 1.0, -1.0)
+    g = torch.linspace(-80.0, 80.0, T * (1 if form == "row" else D), device=DEV).view(T, -1)
+    if form == "residual":
+        out = gdr.gdr_residual_norm(x, torch.zeros(T, D, device=DEV), None, gate=g, activation=act, out_dtype=BF16)[0]
+    else:
+        out = gdr.gdr_gate_norm(x, g, activation=act, eps=0.0)
+    assert out.dtype == F32
+    gd = g.double()
+    want = x.double() * (gd / (1 + torch.exp(-gd)) if act == "silu" else 1 / (1 + torch.exp(-gd)))
+    err = float(((out.double() - want).abs() / want.abs()).nan_to_num(0.0).max())
+    assert err <= 2.0 ** -21, f"{err * 2 ** 21:.3g} x the bound"
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_activations_far_out(dtype):
+    """Gates of infinity, NaN and past where the exponential overflows, as the formula has them."""
+    inf = float("inf")
+    g = torch.tensor([inf, -inf, float("nan"), 1e30, -1e30, 100.0, -100.0, 0.0], device=DEV).to(dtype)[:, None].expand(8, 64)
+    x = torch.ones(8, 64, dtype=dtype, device=DEV)
+    got = gdr.gdr_gate_norm(x, g.contiguous(), activation="sigmoid", eps=0.0)[:, 0].tolist()
+    assert got[:2] == [1.0, 0.0] and got[2] != got[2] and got[3:6] == [1.0, 0.0, 1.0] and abs(got[6]) <= 1e-30 and got[7] == 0.5
+    got = gdr.gdr_gate_norm(x, g.contiguous(), activation="silu", eps=0.0)[:, 0].double().tolist()
+    assert got[0] == inf and got[1] != got[1] and got[2] != got[2] and got[3] >= 9e29 and got[4] == 0.0
+    assert got[5] == 100.0 and abs(got[6]) <= 1e-30 and got[7] == 0.0
