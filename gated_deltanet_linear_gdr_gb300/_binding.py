@@ -551,13 +551,19 @@ def _launch(fn, args, device: int) -> int:
     return fn(args, _raw_stream(device) if _raw_stream is not None else _stream(device))
 
 
+def _tensors(**tensors):
+    """Refuses what is no tensor, before anything is asked of it."""
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+
+
 def _refuse(device, dtypes, **tensors):
     """Says what is wrong with one of a call's tensors: not one, not on the
     call's device, or not of the wanted dtype (of float32 and bfloat16 where
     dtypes has none for it)."""
+    _tensors(**tensors)
     for name, t in tensors.items():
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
         if t.device != device:
@@ -603,9 +609,9 @@ def _linattn_values(q, k, v, decay, state, slot_idx, offsets, out, decay_is_log,
     if qc != 1 or kc != 1 or vc != 1 or oc != 1:
         raise ValueError("q, k, v and out must have a unit channel stride")
     ss, sh, sk, sv = state.stride()
-    return (batch, nv, nk, K, V, 1 if decay_is_log else 0, td, sd, T, max_row_len, q.data_ptr(), qt, qh, k.data_ptr(), kt,
+    return (batch, nv, nk, K, V, 1 if decay_is_log else 0, td, sd, T, int(max_row_len), q.data_ptr(), qt, qh, k.data_ptr(), kt,
             kh, v.data_ptr(), vt, vh, decay.data_ptr(), decay.stride(0), out.data_ptr(), ot, oh, state.data_ptr(), ss, sh,
-            sk, sv, slots, slot_idx.data_ptr(), offsets.data_ptr(), 0, 0, scale)
+            sk, sv, slots, slot_idx.data_ptr(), offsets.data_ptr(), 0, 0, float(scale))
 
 
 def _linattn_workspace(lib, args: bytes, device, workspace):
@@ -649,6 +655,7 @@ def gdr_linattn_fwd(q, k, v, decay, state, slot_idx, offsets, out=None, *, decay
     `workspace` is a device tensor to use instead of a new one of
     gdr_linattn_workspace_bytes() bytes."""
     if out is None:
+        _tensors(v=v)
         out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
     args = _pack_linattn(*_linattn_values(q, k, v, decay, state, slot_idx, offsets, out, decay_is_log, scale, max_row_len))
     lib = _lib or load_library()
@@ -712,13 +719,15 @@ def gdr_gate_norm(x, gate, weight=None, out=None, *, eps=1e-6, activation="silu"
     also be None, or broadcast over the last dimension), float32 or bfloat16;
     weight [D] float32 or None.  Returns out, of x's shape and out_dtype (by
     default the gate's dtype, or x's)."""
+    _tensors(x=x, gate=x if gate is None else gate)
     dev = x.device
     xd, shape = _float(x, "x", dev), x.shape
     if len(shape) not in (2, 3):
         raise ValueError("x must be [T, H, D] or [T, D]")
     if out is None:
         out = torch.empty(shape, dtype=out_dtype or (x if gate is None else gate).dtype, device=dev)
-    elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
+    elif not isinstance(out, torch.Tensor) or out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
+        _tensors(out=out)
         raise ValueError("out must have x's shape and dtype out_dtype")
     od = _float(out, "out", dev)
     T, D = shape[0], shape[-1]
@@ -751,6 +760,7 @@ def gdr_residual_norm(block, residual, weight, *, post_weight=None, gate=None, a
     None for a norm without one.  Returns (residual_out, out): residual_out
     may be residual itself (in place) and is residual where block is None;
     out has out_dtype (by default the block's dtype, or residual's)."""
+    _tensors(residual=residual, block=residual if block is None else block)
     dev = residual.device
     rd, shape = _float(residual, "residual", dev), residual.shape
     if len(shape) != 2:
@@ -758,7 +768,8 @@ def gdr_residual_norm(block, residual, weight, *, post_weight=None, gate=None, a
     T, D = shape
     if out is None:
         out = torch.empty(shape, dtype=out_dtype or (residual if block is None else block).dtype, device=dev)
-    elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
+    elif not isinstance(out, torch.Tensor) or out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
+        _tensors(out=out)
         raise ValueError("out must be [T, D] of dtype out_dtype")
     od = _float(out, "out", dev)
     ot, rt = _rows(out, "out")[0], _rows(residual, "residual")[0]
