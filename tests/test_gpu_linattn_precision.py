@@ -121,3 +121,49 @@ def test_a_chunk_that_cancels(form, pool):
     lam = torch.ones(1, device=DEV)
     out, state, ref = _call(form, q, k, v, lam, torch.zeros(2, 1, K, V, dtype=pool, device=DEV), off, scale=1.0)
     check(out, state, ref, max(lens), form != "any layout")
+
+
+@pytest.mark.parametrize("tok,shift", [(F32, 0), (F32, 1), (BF16, 1)])
+@pytest.mark.parametrize("pool", [BF16, F32])
+def test_long_rows_of_the_recurrent_form(tok, shift, pool):
+    """float32 tokens, and bfloat16 tokens one element off 16 bytes, past 300 tokens: float32 roundings and the last."""
+    lens, K, V = [777, 1, 401], 64, 96
+    T, off = sum(lens), _offsets(lens)
+
+    def lay(x):
+        buf = torch.zeros(x.numel() + 8, dtype=tok, device=DEV)
+        buf[shift:shift + x.numel()].view(x.shape).copy_(x)
+        return buf[shift:shift + x.numel()].view(x.shape)
+
+    q, k, v = lay(_randn(T, 1, K)), lay(_randn(T, 1, K, seed=1)), lay(_randn(T, 2, V, seed=2))
+    lam, slot = torch.tensor([0.999, 0.8], device=DEV), torch.arange(3, dtype=torch.int32, device=DEV)
+    start = _randn(3, 2, K, V, dtype=pool, seed=3)
+    state = start.clone()
+    out = gdr.gdr_linattn_fwd(q, k, v, lam, state, slot, off, max_row_len=777)
+    check(out, state, linattn_ref(q, k, v, lam, start, slot, off), 777, False)
+    assert gdr.gdr_get_status() == 0
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a pool, an output and a workspace of its own, as when nothing else runs."""
+    lens = [2400, 70, 900]
+    off, slot, lam = _offsets(lens), torch.arange(3, dtype=torch.int32, device=DEV), torch.tensor([0.99, 1.0], device=DEV)
+    T, jobs = sum(lens), []
+    for seed, (K, V, pool) in enumerate([(128, 128, BF16), (64, 128, F32)]):
+        q, k, v = (_randn(T, n, d, dtype=BF16, seed=10 * seed + i) for i, (n, d) in enumerate([(1, K), (1, K), (2, V)]))
+        start = _randn(3, 2, K, V, dtype=pool, seed=seed)
+        state = start.clone()
+        jobs.append(((q, k, v, lam), start, gdr.gdr_linattn_fwd(q, k, v, lam, state, slot, off, max_row_len=2400), state))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, ((q, k, v, d), start, _, _) in enumerate(jobs):
+            with torch.cuda.stream(streams[i]):
+                state = start.clone()
+                got[i].append((gdr.gdr_linattn_fwd(q, k, v, d, state, slot, off, max_row_len=2400), state))
+    torch.cuda.synchronize()
+    for i, (_, _, want, want_state) in enumerate(jobs):
+        for out, state in got[i]:
+            assert torch.equal(out, want) and torch.equal(state, want_state)
+    assert gdr.gdr_get_status() == 0
