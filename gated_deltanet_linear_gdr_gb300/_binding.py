@@ -655,7 +655,8 @@ def gdr_linattn_fwd(q, k, v, decay, state, slot_idx, offsets, out=None, *, decay
     `workspace` is a device tensor to use instead of a new one of
     gdr_linattn_workspace_bytes() bytes."""
     if out is None:
-        _tensors(v=v)
+        if not isinstance(v, torch.Tensor):
+            _tensors(v=v)
         out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
     args = _pack_linattn(*_linattn_values(q, k, v, decay, state, slot_idx, offsets, out, decay_is_log, scale, max_row_len))
     lib = _lib or load_library()
@@ -719,7 +720,8 @@ def gdr_gate_norm(x, gate, weight=None, out=None, *, eps=1e-6, activation="silu"
     also be None, or broadcast over the last dimension), float32 or bfloat16;
     weight [D] float32 or None.  Returns out, of x's shape and out_dtype (by
     default the gate's dtype, or x's)."""
-    _tensors(x=x, gate=x if gate is None else gate)
+    if not (isinstance(x, torch.Tensor) and (gate is None or isinstance(gate, torch.Tensor))):
+        _tensors(x=x, gate=gate)
     dev = x.device
     xd, shape = _float(x, "x", dev), x.shape
     if len(shape) not in (2, 3):
@@ -760,7 +762,8 @@ def gdr_residual_norm(block, residual, weight, *, post_weight=None, gate=None, a
     None for a norm without one.  Returns (residual_out, out): residual_out
     may be residual itself (in place) and is residual where block is None;
     out has out_dtype (by default the block's dtype, or residual's)."""
-    _tensors(residual=residual, block=residual if block is None else block)
+    if not (isinstance(residual, torch.Tensor) and (block is None or isinstance(block, torch.Tensor))):
+        _tensors(residual=residual, block=block)
     dev = residual.device
     rd, shape = _float(residual, "residual", dev), residual.shape
     if len(shape) != 2:

@@ -84,12 +84,12 @@ int check_linattn(const gdr_linattn_args *a, const char *fn) {
 
 // Whether rows are short enough for k_la_small.cu, whose time grows with a row's
 // 16-token pieces, where k_la_chunk.cu's for a unit hardly does.  Measured, 64 rows x
-// 16 heads of K x V, us, small against chunk: 64 x 64 41 / 52 at 96 tokens, 50 / 52 at
-// 128; 64 x 128 39 / 46 at 48, 46 / 44 at 64 (128 x 64: 38 / 46, 48 / 46); 128 x 128,
-// bfloat16 pool, 42 / 46 at 32, 56 / 48 at 48; float32 pool 40 / 54 at 16, 58 / 56 at 32.
+// 16 heads of K x V, us, small against chunk: 64 x 64 40 / 50 at 96 tokens, 50 / 48 at
+// 128; 64 x 128 38 / 42 at 48, 46 / 42 at 64 (128 x 64: 38 / 48, 46 / 46); 128 x 128,
+// bfloat16 pool, 42 / 48 at 32, 54 / 48 at 48; float32 pool 40 / 50 at 16, 58 / 52 at 32.
 // Where all units run at once (two a multiprocessor) the longest row, by the caller's
 // bound, decides; where they queue, its mean with the average: 52 rows of 1 to 64 x 21
-// heads of 64 x 128 38 / 50, of 1 to 96 54 / 52, 8 rows of 1 to 128 x 16 of 64 x 64 19 / 15.
+// heads of 64 x 128 46 / 44, of 1 to 96 58 / 50, 8 rows of 1 to 128 x 16 of 64 x 64 19 / 15.
 bool short_rows(const gdr_linattn_args *a) {
     const bool wide_k = a->K > 64, wide_v = a->V > 64;
     const int most = wide_k && wide_v ? (a->state_dtype == GDR_BF16 ? 32 : 16) : wide_k || wide_v ? 48 : 96;
@@ -160,9 +160,9 @@ gdr::LaParams lower(const gdr_linattn_args *a, unsigned *status) {
 // the segments' own states (with the slower clock and memory of a full GPU,
 // 0.75 of a chunk's time a chunk), two more launches and the states' traffic
 // (12 chunks' time).  Measured, cut against whole, K = V = 128, bfloat16 pool:
-// 16383 tokens x 32 heads 179 us against 332, 4000 x 32 70 / 92, 2000 x 4 37 /
-// 52; left whole by this rule: 1000 x 16 38 / 33, 2 rows of 2000 x 16 54 / 52,
-// 8000 x 64 191 / 173.
+// 16383 tokens x 32 heads 183 us against 365, 4000 x 32 70 / 101, 2000 x 4 36 /
+// 54; left whole by this rule: 1000 x 16 40 / 33, 2 rows of 2000 x 16 54 / 58,
+// 8000 x 64 174 / 191.
 int plan_segments(const gdr_linattn_args *a) {
     constexpr double kSms = 152.0, kChunk = 64.0, kStatePass = 0.75, kUnit = 3.0, kExtra = 12.0;
     if (a->batch < 1 || a->batch > 32) return 0;

@@ -25,14 +25,16 @@
 // the products of a chunk run under the elementwise work of its neighbours.
 // (One issuing warp for all products of a chunk was the slowest of the roles.)
 //
-// Bound: shared memory and HBM.  A chunk of one head with K = V = 128 moves 64 KiB,
-// 1.47 us of an SM's share of HBM, and about 280 KiB through shared memory, 2200
-// cycles; the role that makes K~ waits for that most.  4 rows of 4096 tokens x 38
-// heads, a unit an SM, take 126 us with a bfloat16 pool (76% of the measured copy
-// rate) and 132 with a float32 pool; heads of 64 x 64 79 us (61%), where the roles'
-// instructions and latencies set the pace, 1.2 us a chunk.  A row alone on its SM
-// takes 1.5 us a chunk (64 x 64: 1.1).  A unit costs 5 us to begin and end, of which
-// its state's exchange takes 1.5: rows of one chunk are the costly ones.
+// Bound: what an SM has beside its share of HBM.  A chunk of one head with K = V =
+// 128 moves 64 KiB, 1.47 us of that share; with every SM at work it takes 1.95.
+// The six roles' code does not fit the nearest instruction cache (17% of stalls),
+// and their loads and stores take 43% of shared memory's cycles beside the 45% in
+// which the tensor cores read it; the role that makes K~ waits for both most.
+// 4 rows of 4096 tokens x 38 heads, a unit an SM, take 126 us with a bfloat16 pool
+// (76% of the measured copy rate) and 132 with a float32 pool; heads of 64 x 64 79
+// us (60%).  A row alone on its SM takes 1.5 us a chunk (64 x 64: 1.1).  A unit costs
+// 5 us to begin and end, of which its state's exchange takes 1.5: rows of one chunk
+// are the costly ones.
 #include "tc.cuh"
 
 #include "layer_internal.h"

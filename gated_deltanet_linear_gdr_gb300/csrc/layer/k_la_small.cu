@@ -18,7 +18,7 @@
 // it computes the current one, two CTAs a multiprocessor.  1024 (row, head) pairs
 // of 128 x 256 take 40 us here at 5 tokens, 42 at 16 and 70 at 32 (floor 21, 23
 // and 27); the recurrent form of k_la_step.cu takes 30 + 11 a token, the roles of
-// k_la_chunk.cu, which fill and drain for each unit, 76 to 85.  A warp keeps 32
+// k_la_chunk.cu, which fill and drain for each unit, 87.  A warp keeps 32
 // columns (16, twice the warps: 44 us).
 #include "../gdr_device.cuh"
 #include "layer_internal.h"

@@ -366,10 +366,23 @@ int gdr_rollback(const gdr_step_args *args, const void *inter, int64_t inter_slo
  *          gdr_linattn_workspace_bytes() says how much pays off.  A call with
  *          less is right too, and slower where few rows are long.
  * K and V are multiples of 16, K up to 128 and V up to 256, in any
- * combination.  State and sums are float32 inside a call; a bfloat16 pool and
- * bfloat16 outputs are rounded to nearest-even once.  A non-finite value in a
- * token's q, k or v spoils outputs of its own row only, but there also those of
- * up to 63 tokens before it (prompts are computed 64 tokens at a time).
+ * combination.
+ *
+ * Precision.  State and sums are float32 inside a call; a bfloat16 pool and
+ * bfloat16 outputs are rounded to nearest-even once.  Where a form works by
+ * matrix instructions, what it makes to go into them (scores, weighted keys and
+ * values, the state as it is read out) keeps 16 bits at least, weighted keys and
+ * values 24 for a float32 pool: beside the roundings of float32 sums an output
+ * is off by at most 2^-16 (bfloat16 pool: 2^-14) of its terms' absolute sum, a
+ * float32 pool's state by 2^-24 and a bfloat16 pool's, before its own rounding,
+ * by 2^-14 of theirs.
+ * A non-finite value in a token or a start state spoils outputs of its own row
+ * only (NaN may stand where an infinity would), but there also those of up to
+ * 63 tokens before it (prompts are computed 64 tokens at a time).
+ *
+ * Rows must not lie on one another, which they do only where offsets decrease.
+ * Then GDR_STATUS_BAD_OFFSETS is set, and a row that begins before an earlier
+ * one's end is computed or skipped, whichever the call's form does.
  */
 typedef struct gdr_linattn_args {
     int32_t batch;
