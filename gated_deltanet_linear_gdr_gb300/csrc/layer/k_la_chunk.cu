@@ -16,7 +16,7 @@
 // in two (bfloat16 pool) or three (float32 pool).  So results are rounded once,
 // whatever cancels in their sums.  (One part for P~ and the state, 8 bits, made
 // outputs off by 2.1e-3 of their norm for 1.7e-3, and by all of it where the
-// history cancels; it was 7 to 13% faster with 128 key channels.)
+// history cancels; it was 4 to 13% faster with 128 key channels.)
 //
 // One CTA per SM walks (row segment, value head, 128-column tile) units, with
 // a warp role for each step: 8 warps keep S, 4 make K~, 4 make P~, 4 write the
