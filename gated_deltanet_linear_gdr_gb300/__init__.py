@@ -11,6 +11,7 @@ from ._binding import (  # noqa: F401
     GDR_F32,
     GdrError,
     HostForward,
+    gdr_accept_drafts,
     gdr_fold,
     gdr_fwd,
     gdr_fwd_conv,
@@ -25,15 +26,21 @@ from ._binding import (  # noqa: F401
     gdr_residual_norm,
     gdr_ring_record_elements,
     gdr_rollback,
+    gdr_selective_scan,
+    gdr_selective_scan_workspace_bytes,
+    gdr_short_conv,
     gdr_verify_ring,
     Prepared,
     load_library,
+    prepare_accept_drafts,
     prepare_fold,
     prepare_fwd,
     prepare_fwd_conv,
     prepare_fwd_snapshots,
     prepare_linattn_fwd,
     prepare_rollback,
+    prepare_selective_scan,
+    prepare_short_conv,
     prepare_verify_ring,
     status_names,
 )

@@ -25,7 +25,7 @@ GDR_F32, GDR_BF16 = 0, 1
 STATUS_BITS = {
     0x1: "BAD_SLOT", 0x2: "BAD_OFFSETS", 0x4: "BAD_RING_SLOT", 0x8: "BAD_COUNT",
     0x10: "ROW_TOO_LONG", 0x20: "BAD_ACCEPTED", 0x40: "SNAPSHOT_OVERFLOW", 0x80: "BAD_DECAY",
-    0x100: "TIMEOUT",
+    0x100: "TIMEOUT", 0x200: "NO_MASS",
 }
 
 
@@ -116,6 +116,59 @@ class gdr_norm_args(ctypes.Structure):
     ]
 
 
+class gdr_short_conv_args(ctypes.Structure):
+    """Mirror of struct gdr_short_conv_args in include/gdr.h."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("channels", ctypes.c_int32), ("width", ctypes.c_int32), ("activation", ctypes.c_int32),
+        ("token_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32), ("keep_state", ctypes.c_int32),
+        ("total_tokens", ctypes.c_int64), ("max_row_len", ctypes.c_int64),
+        ("x", ctypes.c_void_p), ("x_seq_stride", ctypes.c_int64),
+        ("weight", ctypes.c_void_p), ("weight_chan_stride", ctypes.c_int64), ("weight_tap_stride", ctypes.c_int64),
+        ("bias", ctypes.c_void_p), ("out", ctypes.c_void_p), ("out_seq_stride", ctypes.c_int64),
+        ("conv_state", ctypes.c_void_p), ("state_slot_stride", ctypes.c_int64), ("state_chan_stride", ctypes.c_int64),
+        ("state_tap_stride", ctypes.c_int64), ("max_slots", ctypes.c_int64),
+        ("slot_idx", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("counts", ctypes.c_void_p),
+    ]
+
+
+class gdr_scan_args(ctypes.Structure):
+    """Mirror of struct gdr_scan_args in include/gdr.h."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("nv", ctypes.c_int32), ("nk", ctypes.c_int32), ("K", ctypes.c_int32),
+        ("V", ctypes.c_int32), ("dt_softplus", ctypes.c_int32), ("token_dtype", ctypes.c_int32),
+        ("dt_dtype", ctypes.c_int32), ("state_dtype", ctypes.c_int32), ("keep_state", ctypes.c_int32),
+        ("total_tokens", ctypes.c_int64), ("max_row_len", ctypes.c_int64),
+        ("x", ctypes.c_void_p), ("x_seq_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+        ("dt", ctypes.c_void_p), ("dt_seq_stride", ctypes.c_int64), ("dt_head_stride", ctypes.c_int64),
+        ("dt_elem_stride", ctypes.c_int64),
+        ("B", ctypes.c_void_p), ("B_seq_stride", ctypes.c_int64), ("B_head_stride", ctypes.c_int64),
+        ("C", ctypes.c_void_p), ("C_seq_stride", ctypes.c_int64), ("C_head_stride", ctypes.c_int64),
+        ("z", ctypes.c_void_p), ("z_seq_stride", ctypes.c_int64), ("z_head_stride", ctypes.c_int64),
+        ("A", ctypes.c_void_p), ("A_head_stride", ctypes.c_int64), ("A_kdim_stride", ctypes.c_int64),
+        ("A_vdim_stride", ctypes.c_int64),
+        ("D", ctypes.c_void_p), ("D_head_stride", ctypes.c_int64), ("D_vdim_stride", ctypes.c_int64),
+        ("dt_bias", ctypes.c_void_p), ("dt_bias_head_stride", ctypes.c_int64), ("dt_bias_vdim_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("out_seq_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+        ("state", ctypes.c_void_p), ("state_slot_stride", ctypes.c_int64), ("state_head_stride", ctypes.c_int64),
+        ("state_kdim_stride", ctypes.c_int64), ("state_vdim_stride", ctypes.c_int64), ("max_slots", ctypes.c_int64),
+        ("slot_idx", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("counts", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
+class gdr_accept_args(ctypes.Structure):
+    """Mirror of struct gdr_accept_args in include/gdr.h."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("vocab", ctypes.c_int32), ("prob_dtype", ctypes.c_int32), ("max_row_len", ctypes.c_int32),
+        ("total_tokens", ctypes.c_int64),
+        ("target", ctypes.c_void_p), ("target_seq_stride", ctypes.c_int64),
+        ("draft", ctypes.c_void_p), ("draft_seq_stride", ctypes.c_int64),
+        ("tokens", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("uniforms", ctypes.c_void_p),
+        ("row_uniforms", ctypes.c_void_p), ("out_tokens", ctypes.c_void_p), ("out_seq_stride", ctypes.c_int64),
+        ("counts", ctypes.c_void_p),
+    ]
+
+
 def _packer(cls):
     """Packs a call's values into the bytes of `cls` in one step (a ctypes
     structure costs several microseconds to fill; a decode step's call is
@@ -128,6 +181,9 @@ def _packer(cls):
 
 _pack_linattn = _packer(gdr_linattn_args)
 _pack_norm = _packer(gdr_norm_args)
+_pack_short_conv = _packer(gdr_short_conv_args)
+_pack_scan = _packer(gdr_scan_args)
+_pack_accept = _packer(gdr_accept_args)
 
 _lock = threading.Lock()
 _lib = None
@@ -163,6 +219,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                 "gdr_linattn_fwd": ([vp, vp], ctypes.c_int),  # structs as packed bytes or by reference
                 "gdr_linattn_workspace_bytes": ([vp], ctypes.c_int64),
                 "gdr_block_norm": ([vp, vp], ctypes.c_int),
+                "gdr_short_conv": ([vp, vp], ctypes.c_int),
+                "gdr_selective_scan": ([vp, vp], ctypes.c_int),
+                "gdr_selective_scan_workspace_bytes": ([vp], ctypes.c_int64),
+                "gdr_accept_drafts": ([vp, vp], ctypes.c_int),
                 "gdr_get_status": ([ctypes.POINTER(ctypes.c_uint32), i32], ctypes.c_int),
                 "gdr_probe_fma": ([i32, i32, i32, vp, i64, ctypes.POINTER(ctypes.c_int32), vp], ctypes.c_int),
             }
@@ -809,6 +869,305 @@ def gdr_residual_norm(block, residual, weight, *, post_weight=None, gate=None, a
     if rc:
         _check(rc)
     return h, out
+
+
+def _ints(t, shape, name: str, device) -> int:
+    """The pointer of a contiguous int32 tensor of a call's rows or tokens."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == device):
+        _refuse(device, {name: torch.int32}, **{name: t})
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} int32 tensor")
+    return t.data_ptr()
+
+
+def _ragged(slot_idx, offsets, counts, keep_state, state_only, device):
+    """(batch, slot_idx, offsets, counts) of a call over ragged rows, as pointers."""
+    if not isinstance(slot_idx, torch.Tensor):
+        _tensors(slot_idx=slot_idx)
+    if slot_idx.dim() != 1:
+        raise ValueError("slot_idx must be a contiguous [batch] int32 tensor")
+    if not keep_state and (state_only or counts is not None):
+        raise ValueError("state_only and counts need keep_state")
+    n = slot_idx.shape[0]
+    return (n, _ints(slot_idx, (n,), "slot_idx", device), _ints(offsets, (n + 1,), "offsets", device),
+            0 if counts is None else _ints(counts, (n,), "counts", device))
+
+
+def _output(out, like, state_only):
+    """A call's output tensor: the caller's, a new one like `like`, or none."""
+    if state_only:
+        if out is not None:
+            raise ValueError("state_only has no out")
+        return None
+    if out is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if not isinstance(out, torch.Tensor):
+        _tensors(out=out)
+    if out.shape != like.shape or out.dtype != like.dtype or out.device != like.device:
+        raise ValueError("out must have x's shape, dtype and device")
+    return out
+
+
+def _short_conv_args(x, weight, bias, conv_state, slot_idx, offsets, out, activation, counts, keep_state, state_only, max_row_len):
+    """(packed gdr_short_conv_args, out)."""
+    if not isinstance(x, torch.Tensor):
+        _tensors(x=x)
+    dev = x.device
+    td = _float(x, "x", dev)
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be [T, channels] with a unit channel stride")
+    T, C = x.shape
+    if not (isinstance(weight, torch.Tensor) and weight.dtype is torch.float32 and weight.device == dev):
+        _refuse(dev, {"weight": torch.float32}, weight=weight)
+    if weight.dim() != 2 or weight.shape[0] != C:
+        raise ValueError(f"weight must be [channels, width] with {C} channels")
+    width = weight.shape[1]
+    if activation not in (None, "silu"):
+        raise ValueError('activation must be "silu" or None')
+    sp, sd, ss, sc, st, slots = 0, GDR_F32, 0, 0, 0, 1 << 30
+    if width > 1:
+        sd = _float(conv_state, "conv_state", dev)
+        if conv_state.dim() != 3 or conv_state.shape[1:] != (C, width - 1):
+            raise ValueError(f"conv_state must be [slots, {C}, {width - 1}]")
+        sp, (ss, sc, st), slots = conv_state.data_ptr(), conv_state.stride(), conv_state.shape[0]
+    elif conv_state is not None:
+        raise ValueError("a convolution of width 1 has no conv_state")
+    out = _output(out, x, state_only)
+    if out is not None and out.shape[1] > 1 and out.stride(1) != 1:
+        raise ValueError("out must have a unit channel stride")
+    n, slot, off, cnt = _ragged(slot_idx, offsets, counts, keep_state, state_only, dev)
+    ws = weight.stride()
+    return _pack_short_conv(n, C, width, 1 if activation == "silu" else 0, td, sd, 1 if keep_state else 0, T, int(max_row_len),
+                            x.data_ptr(), x.stride(0), weight.data_ptr(), ws[0], ws[1], _weight(bias, C, "bias", dev),
+                            0 if out is None else out.data_ptr(), 0 if out is None else out.stride(0), sp, ss, sc, st, slots,
+                            slot, off, cnt), out
+
+
+def gdr_short_conv(x, weight, bias, conv_state, slot_idx, offsets, out=None, *, activation="silu", counts=None,
+                   keep_state=True, state_only=False, max_row_len=0):
+    """Short causal depthwise convolution over ragged rows and a slot-indexed
+    state pool (include/gdr.h, gdr_short_conv_args); conv_state updated in
+    place; returns out.
+
+    x [T, channels] float32 or bfloat16, weight [channels, width] float32 (width
+    1 to 4), bias [channels] float32 or None, conv_state [slots, channels,
+    width-1] float32 or bfloat16 (None for width 1).  keep_state=False leaves
+    the pool as it is (a verify pass of drafts); counts [batch] int32 takes only
+    a row's first tokens into its slot; state_only=True computes no output and
+    returns None.  max_row_len bounds the rows' lengths (1: single tokens)."""
+    args, out = _short_conv_args(x, weight, bias, conv_state, slot_idx, offsets, out, activation, counts, keep_state,
+                                 state_only, max_row_len)
+    rc = _launch((_lib or load_library()).gdr_short_conv, args, x.get_device())
+    if rc:
+        _check(rc)
+    return out
+
+
+def prepare_short_conv(x, weight, bias, conv_state, slot_idx, offsets, out, *, activation="silu", counts=None,
+                       keep_state=True, state_only=False, max_row_len=0) -> "Prepared":
+    if out is None and not state_only:
+        raise ValueError("a prepared call needs its out")
+    args, out = _short_conv_args(x, weight, bias, conv_state, slot_idx, offsets, out, activation, counts, keep_state,
+                                 state_only, max_row_len)
+    return Prepared(load_library().gdr_short_conv, gdr_short_conv_args.from_buffer_copy(args), (),
+                    (x, weight, bias, conv_state, slot_idx, offsets, out, counts), x.device)
+
+
+def _per_channel(t, shape, name: str, device):
+    """(pointer, strides) of a float32 tensor of a layer's channels; broadcast dimensions as strides of 0."""
+    if t is None:
+        return 0, (0,) * len(shape)
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.device == device):
+        _refuse(device, {name: torch.float32}, **{name: t})
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} (expand what it shares)")
+    return t.data_ptr(), t.stride()
+
+
+def _scan_args(x, dt, A, B, C, state, slot_idx, offsets, out, D, z, dt_bias, dt_softplus, counts, keep_state, state_only,
+               max_row_len):
+    """(packed gdr_scan_args without a workspace, out)."""
+    if not (isinstance(x, torch.Tensor) and isinstance(dt, torch.Tensor) and isinstance(state, torch.Tensor)):
+        _tensors(x=x, dt=dt, state=state)
+    dev = x.device
+    td, dd, sd = _float(x, "x", dev), _float(dt, "dt", dev), _float(state, "state", dev)
+    if state.dim() != 4:
+        raise ValueError("state must be [max_slots, nv, K, V]")
+    slots, nv, K, V = state.shape
+    if x.dim() != 3 or x.shape[1:] != (nv, V):
+        raise ValueError(f"x must be [T, nv, V] = [T, {nv}, {V}]")
+    T = x.shape[0]
+    if dt.shape != x.shape:
+        raise ValueError("dt must have x's shape (expand what it shares)")
+    for name, t in (("B", B), ("C", C)):
+        if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != x.dtype:
+            _refuse(dev, {name: x.dtype}, **{name: t})
+        if t.dim() != 3 or t.shape[0] != T or t.shape[2] != K or t.shape != B.shape:
+            raise ValueError(f"B and C must both be [T, nk, K] = [{T}, nk, {K}]")
+        if K > 1 and t.stride(2) != 1:
+            raise ValueError(f"{name} must have a unit stride along K")
+    out = _output(out, x, state_only)
+    for name, t in (("x", x), ("out", out)):
+        if t is not None and V > 1 and t.stride(2) != 1:
+            raise ValueError(f"{name} must have a unit channel stride")
+    if V > 1 and dt.stride(2) not in (0, 1):
+        raise ValueError("dt must have a unit channel stride, or one value a head")
+    zp, zt, zh = 0, 0, 0
+    if z is not None:
+        if not isinstance(z, torch.Tensor) or z.device != dev or z.dtype != x.dtype:
+            _refuse(dev, {"z": x.dtype}, z=z)
+        if z.shape != x.shape or (V > 1 and z.stride(2) != 1):
+            raise ValueError("z must have x's shape and a unit channel stride")
+        zp, (zt, zh) = z.data_ptr(), z.stride()[:2]
+    ap, (ah, ak, av) = _per_channel(A, (nv, K, V), "A", dev)
+    if not ap:
+        _tensors(A=A)
+    dp, (dh, dv) = _per_channel(D, (nv, V), "D", dev)
+    bp, (bh, bv) = _per_channel(dt_bias, (nv, V), "dt_bias", dev)
+    n, slot, off, cnt = _ragged(slot_idx, offsets, counts, keep_state, state_only, dev)
+    (xt, xh, _), (tt, th, te), (Bt, Bh, _), (Ct, Ch, _) = x.stride(), dt.stride(), B.stride(), C.stride()
+    ot, oh = (0, 0) if out is None else out.stride()[:2]
+    ss, sh, sk, sv = state.stride()
+    return _pack_scan(n, nv, B.shape[1], K, V, 1 if dt_softplus else 0, td, dd, sd, 1 if keep_state else 0, T, int(max_row_len),
+                      x.data_ptr(), xt, xh, dt.data_ptr(), tt, th, te if V > 1 else 1, B.data_ptr(), Bt, Bh, C.data_ptr(), Ct,
+                      Ch, zp, zt, zh, ap, ah, ak, av, dp, dh, dv, bp, bh, bv, 0 if out is None else out.data_ptr(), ot, oh,
+                      state.data_ptr(), ss, sh, sk, sv, slots, slot, off, cnt, 0, 0), out
+
+
+def _scan_workspace(lib, args: bytes, device, workspace):
+    """The arguments with a workspace, the caller's or a new one of the size the call asks for, and that tensor."""
+    if workspace is None:
+        need = lib.gdr_selective_scan_workspace_bytes(args)
+        if need < 0:
+            _check(need)
+        if need == 0:
+            return args, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _refuse(device, {"workspace": getattr(workspace, "dtype", None)}, workspace=workspace)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    a = gdr_scan_args.from_buffer_copy(args)
+    a.workspace = workspace.data_ptr()
+    a.workspace_bytes = workspace.numel() * workspace.element_size()
+    return bytes(a), workspace
+
+
+def gdr_selective_scan_workspace_bytes(x, dt, A, B, C, state, slot_idx, offsets, *, max_row_len=0) -> int:
+    """Workspace bytes gdr_selective_scan would use for these tensors (0: none)."""
+    args, _ = _scan_args(x, dt, A, B, C, state, slot_idx, offsets, x, None, None, None, True, None, True, False, max_row_len)
+    n = load_library().gdr_selective_scan_workspace_bytes(args)
+    if n < 0:
+        _check(n)
+    return int(n)
+
+
+def gdr_selective_scan(x, dt, A, B, C, state, slot_idx, offsets, out=None, *, D=None, z=None, dt_bias=None, dt_softplus=True,
+                       counts=None, keep_state=True, state_only=False, max_row_len=0, workspace=None):
+    """Selective state space scan over ragged rows and a slot-indexed pool
+    (include/gdr.h, gdr_scan_args): per token d = softplus(dt + dt_bias), S <-
+    exp(d A) S + d x B, out = (C S + D x) silu(z); state updated in place;
+    returns out.
+
+    x, z [T, nv, V] and B, C [T, nk, K] of one dtype (bfloat16 or float32), dt [T,
+    nv, V] of that dtype or float32 (or one value a head, expanded), A [nv, K,
+    V], D and dt_bias [nv, V] float32 (expanded where shared), state [max_slots,
+    nv, K, V] bfloat16 or float32.  keep_state=False leaves the pool as it is (a
+    verify pass of drafts); counts [batch] int32 takes only a row's first tokens
+    into its slot; state_only=True computes no output and returns None.
+    max_row_len bounds the rows' lengths (1: single tokens).  `workspace` is a
+    device tensor to use instead of a new one of
+    gdr_selective_scan_workspace_bytes() bytes."""
+    args, out = _scan_args(x, dt, A, B, C, state, slot_idx, offsets, out, D, z, dt_bias, dt_softplus, counts, keep_state,
+                           state_only, max_row_len)
+    lib = _lib or load_library()
+    if max_row_len != 1:
+        args, workspace = _scan_workspace(lib, args, x.device, workspace)
+    rc = _launch(lib.gdr_selective_scan, args, x.get_device())
+    if rc:
+        _check(rc)
+    return out
+
+
+def prepare_selective_scan(x, dt, A, B, C, state, slot_idx, offsets, out, *, D=None, z=None, dt_bias=None, dt_softplus=True,
+                           counts=None, keep_state=True, state_only=False, max_row_len=0, workspace=None) -> "Prepared":
+    if out is None and not state_only:
+        raise ValueError("a prepared call needs its out")
+    args, out = _scan_args(x, dt, A, B, C, state, slot_idx, offsets, out, D, z, dt_bias, dt_softplus, counts, keep_state,
+                           state_only, max_row_len)
+    lib = load_library()
+    args, workspace = _scan_workspace(lib, args, x.device, workspace)
+    return Prepared(lib.gdr_selective_scan, gdr_scan_args.from_buffer_copy(args), (),
+                    (x, dt, A, B, C, state, slot_idx, offsets, out, D, z, dt_bias, counts, workspace), x.device)
+
+
+def _accept_args(target, draft, tokens, offsets, uniforms, row_uniforms, max_row_len, out, counts):
+    """(packed gdr_accept_args, out, counts)."""
+    if not isinstance(target, torch.Tensor):
+        _tensors(target=target)
+    dev = target.device
+    pd = _float(target, "target", dev)
+    if target.dim() != 2 or (target.shape[1] > 1 and target.stride(1) != 1):
+        raise ValueError("target must be [T, vocab] with a unit stride along the vocabulary")
+    T, vocab = target.shape
+    qp, qt = 0, 0
+    if draft is not None:
+        if not isinstance(draft, torch.Tensor) or draft.dtype != target.dtype or draft.device != dev:
+            _refuse(dev, {"draft": target.dtype}, draft=draft)
+        if draft.shape != target.shape or (vocab > 1 and draft.stride(1) != 1):
+            raise ValueError("draft must have target's shape and a unit stride along the vocabulary")
+        qp, qt = draft.data_ptr(), draft.stride(0)
+    if not isinstance(offsets, torch.Tensor):
+        _tensors(offsets=offsets)
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be a contiguous [batch+1] int32 tensor")
+    n, width = offsets.shape[0] - 1, int(max_row_len)
+    if width < 1:
+        raise ValueError("max_row_len must be at least 1 (it is the width of the returned tokens)")
+    off, tok = _ints(offsets, (n + 1,), "offsets", dev), _ints(tokens, (T,), "tokens", dev)
+    for name, t, size in (("uniforms", uniforms, T), ("row_uniforms", row_uniforms, n)):
+        if not (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.device == dev):
+            _refuse(dev, {name: torch.float32}, **{name: t})
+        if t.shape != (size,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [{size}] float32 tensor")
+    if out is None:
+        out = torch.empty((n, width), dtype=torch.int32, device=dev)
+    else:
+        if not (isinstance(out, torch.Tensor) and out.dtype is torch.int32 and out.device == dev):
+            _refuse(dev, {"out": torch.int32}, out=out)
+        if out.shape != (n, width) or (width > 1 and out.stride(1) != 1):
+            raise ValueError(f"out must be [{n}, {width}] with a unit stride along a row")
+    if counts is None:
+        counts = torch.empty(n, dtype=torch.int32, device=dev)
+    return _pack_accept(n, vocab, pd, width, T, target.data_ptr(), target.stride(0), qp, qt, tok, off, uniforms.data_ptr(),
+                        row_uniforms.data_ptr(), out.data_ptr(), out.stride(0), _ints(counts, (n,), "counts", dev)), out, counts
+
+
+def gdr_accept_drafts(target, draft, tokens, offsets, uniforms, row_uniforms, *, max_row_len, out=None, counts=None):
+    """Verification of drafted tokens by rejection (include/gdr.h,
+    gdr_accept_args): which of each row's drafts the target's probabilities let
+    through, and the token drawn behind them.  Returns (out, counts): out
+    [batch, max_row_len] int32 has each row's accepted drafts, the drawn token and
+    -1 behind it; counts [batch] int32 is their number, what gdr_fold and the
+    counts arguments of the state_only calls take (gdr_rollback: counts - 1).
+
+    target and draft [T, vocab] float32 or bfloat16 probabilities of what follows
+    each token (draft None: the drafts were not drawn from probabilities),
+    tokens [T] int32 (each row's last known token and its drafts), offsets
+    [batch+1] int32, uniforms [T] and row_uniforms [batch] float32 in [0, 1)."""
+    args, out, counts = _accept_args(target, draft, tokens, offsets, uniforms, row_uniforms, max_row_len, out, counts)
+    rc = _launch((_lib or load_library()).gdr_accept_drafts, args, target.get_device())
+    if rc:
+        _check(rc)
+    return out, counts
+
+
+def prepare_accept_drafts(target, draft, tokens, offsets, uniforms, row_uniforms, out, counts, *, max_row_len) -> "Prepared":
+    if out is None or counts is None:
+        raise ValueError("a prepared call needs its out and counts")
+    args, out, counts = _accept_args(target, draft, tokens, offsets, uniforms, row_uniforms, max_row_len, out, counts)
+    return Prepared(load_library().gdr_accept_drafts, gdr_accept_args.from_buffer_copy(args), (),
+                    (target, draft, tokens, offsets, uniforms, row_uniforms, out, counts), target.device)
 
 
 def gdr_get_status(clear: bool = True) -> int:

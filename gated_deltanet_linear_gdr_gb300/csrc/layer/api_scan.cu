@@ -1,0 +1,341 @@
+// C ABI of the state space layer's operators (short convolution, selective scan)
+// and of the verification of drafts: argument checks, lowering and the cut of
+// long rows.  As in api.cu, every check runs before anything is launched.
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "layer_internal.h"
+
+namespace {
+
+int fail(int code, const char *fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return gdr::api_fail(code, buf);
+}
+
+int launched(cudaError_t e, const char *fn) {
+    if (e != cudaSuccess) return fail(GDR_ERR_CUDA, "%s: launch failed: %s", fn, cudaGetErrorString(e));
+    return gdr::api_ok();
+}
+
+bool aligned(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+bool is_dtype(int d) { return d == GDR_F32 || d == GDR_BF16; }
+int64_t esize(int d) { return d == GDR_BF16 ? 2 : 4; }
+
+// Whether rows at p, with these strides in elements, may be moved as `bytes`-byte vectors.
+bool vector_rows(const void *p, int dtype, int64_t bytes, int64_t a, int64_t b = 0, int64_t c = 0) {
+    const int64_t es = esize(dtype);
+    return aligned(p, (uintptr_t)bytes) && (a * es) % bytes == 0 && (b * es) % bytes == 0 && (c * es) % bytes == 0;
+}
+
+int check_tokens(int64_t total, int32_t batch, const char *fn) {
+    if (batch < 0) return fail(GDR_ERR_INVALID_ARG, "%s: batch %d < 0", fn, batch);
+    if (total < 0) return fail(GDR_ERR_INVALID_ARG, "%s: total_tokens < 0", fn);
+    if (total >= (1ll << 31)) return fail(GDR_ERR_UNSUPPORTED, "%s: total_tokens must be < 2^31", fn);
+    return GDR_OK;
+}
+
+// Whether two buffers of rows (`width` elements, `rows` of them, strides in elements) have
+// bytes in common.  Rows of one stride may lie between one another's (parts of one
+// projection); with different strides their whole ranges must be apart.
+bool rows_overlap(const void *a, int64_t as, const void *b, int64_t bs, int64_t rows, int64_t width, int64_t es) {
+    if (rows <= 0 || width <= 0) return false;
+    const int64_t pa = (int64_t)reinterpret_cast<uintptr_t>(a), pb = (int64_t)reinterpret_cast<uintptr_t>(b);
+    const int64_t ea = pa + ((rows - 1) * as + width) * es, eb = pb + ((rows - 1) * bs + width) * es;
+    if (ea <= pb || eb <= pa) return false;
+    if (rows == 1 || as != bs || as < width) return true;
+    int64_t d = (pb - pa) % (as * es);
+    if (d < 0) d += as * es;
+    return d < width * es || d > (as - width) * es;
+}
+
+int check_conv(const gdr_short_conv_args *a, const char *fn) {
+    if (!a) return fail(GDR_ERR_INVALID_ARG, "%s: args is NULL", fn);
+    int rc = check_tokens(a->total_tokens, a->batch, fn);
+    if (rc) return rc;
+    if (a->channels <= 0) return fail(GDR_ERR_INVALID_ARG, "%s: channels %d", fn, a->channels);
+    if (a->channels > (1 << 28)) return fail(GDR_ERR_UNSUPPORTED, "%s: channels must be at most 2^28", fn);
+    if (a->width < 1 || a->width > 4) return fail(GDR_ERR_UNSUPPORTED, "%s: width %d must be 1 to 4", fn, a->width);
+    if (a->activation < 0 || a->activation > 1)
+        return fail(GDR_ERR_INVALID_ARG, "%s: activation %d (0 none, 1 SiLU)", fn, a->activation);
+    if (!is_dtype(a->token_dtype) || !is_dtype(a->state_dtype))
+        return fail(GDR_ERR_UNSUPPORTED, "%s: dtypes must be GDR_F32 or GDR_BF16", fn);
+    if (a->batch == 0) return GDR_OK;
+    if (!a->slot_idx || !a->offsets || !a->weight)
+        return fail(GDR_ERR_INVALID_ARG, "%s: slot_idx/offsets/weight is NULL", fn);
+    if (a->max_slots <= 0) return fail(GDR_ERR_INVALID_ARG, "%s: max_slots %lld", fn, (long long)a->max_slots);
+    if (a->weight_chan_stride < 0 || a->weight_tap_stride < 0)
+        return fail(GDR_ERR_INVALID_ARG, "%s: weight strides must not be negative", fn);
+    if (!aligned(a->weight, 4) || !aligned(a->bias, 4))
+        return fail(GDR_ERR_UNSUPPORTED, "%s: weight and bias must be aligned to their elements", fn);
+    if (a->counts && !a->keep_state) return fail(GDR_ERR_INVALID_ARG, "%s: counts without keep_state", fn);
+    if (!a->out && !a->keep_state) return fail(GDR_ERR_INVALID_ARG, "%s: neither out nor keep_state", fn);
+    if (a->width > 1) {
+        if (!a->conv_state) return fail(GDR_ERR_INVALID_ARG, "%s: conv_state is NULL", fn);
+        if (a->state_slot_stride <= 0 || a->state_chan_stride <= 0 || a->state_tap_stride <= 0)
+            return fail(GDR_ERR_INVALID_ARG, "%s: state strides must be positive", fn);
+        if (!aligned(a->conv_state, esize(a->state_dtype)))
+            return fail(GDR_ERR_UNSUPPORTED, "%s: conv_state must be aligned to its elements", fn);
+    }
+    if (a->total_tokens > 0) {
+        const int64_t es = esize(a->token_dtype);
+        if (!a->x) return fail(GDR_ERR_INVALID_ARG, "%s: x is NULL", fn);
+        if (a->x_seq_stride < 0) return fail(GDR_ERR_INVALID_ARG, "%s: x_seq_stride < 0", fn);
+        if (!aligned(a->x, es) || !aligned(a->out, es))
+            return fail(GDR_ERR_UNSUPPORTED, "%s: x and out must be aligned to their elements", fn);
+        if (a->out) {
+            if (a->total_tokens > 1 && a->out_seq_stride < a->channels)
+                return fail(GDR_ERR_INVALID_ARG, "%s: out_seq_stride must be at least channels", fn);
+            if (rows_overlap(a->x, a->x_seq_stride, a->out, a->out_seq_stride, a->total_tokens, a->channels, es))
+                return fail(GDR_ERR_INVALID_ARG, "%s: out lies on x", fn);
+        }
+    }
+    return GDR_OK;
+}
+
+int check_scan_sizes(const gdr_scan_args *a, const char *fn) {
+    if (!a) return fail(GDR_ERR_INVALID_ARG, "%s: args is NULL", fn);
+    int rc = check_tokens(a->total_tokens, a->batch, fn);
+    if (rc) return rc;
+    if (a->nv <= 0 || a->nk <= 0)
+        return fail(GDR_ERR_INVALID_ARG, "%s: nv=%d, nk=%d must be positive", fn, a->nv, a->nk);
+    if (a->nv % a->nk != 0)
+        return fail(GDR_ERR_INVALID_ARG, "%s: nv=%d is not a multiple of nk=%d", fn, a->nv, a->nk);
+    if (a->K < 1 || a->K > 128 || a->V < 1)
+        return fail(GDR_ERR_UNSUPPORTED, "%s: K=%d must be 1 to 128, V=%d at least 1", fn, a->K, a->V);
+    if ((int64_t)a->nv * a->V > (1 << 24))
+        return fail(GDR_ERR_UNSUPPORTED, "%s: nv * V must be at most 2^24", fn);
+    if (!is_dtype(a->token_dtype) || !is_dtype(a->state_dtype) ||
+        (a->dt_dtype != a->token_dtype && a->dt_dtype != GDR_F32))
+        return fail(GDR_ERR_UNSUPPORTED,
+                    "%s: token_dtype %d, dt_dtype %d, state_dtype %d (GDR_F32 or GDR_BF16; dt the tokens' or GDR_F32)", fn,
+                    a->token_dtype, a->dt_dtype, a->state_dtype);
+    return GDR_OK;
+}
+
+int check_scan(const gdr_scan_args *a, const char *fn) {
+    int rc = check_scan_sizes(a, fn);
+    if (rc) return rc;
+    if (a->batch == 0) return GDR_OK;
+    if (!a->state || !a->slot_idx || !a->offsets || !a->A)
+        return fail(GDR_ERR_INVALID_ARG, "%s: state/slot_idx/offsets/A is NULL", fn);
+    if (a->max_slots <= 0) return fail(GDR_ERR_INVALID_ARG, "%s: max_slots %lld", fn, (long long)a->max_slots);
+    if (a->state_vdim_stride != 1 && a->V > 1)
+        return fail(GDR_ERR_UNSUPPORTED, "%s: state_vdim_stride must be 1 (got %lld)", fn,
+                    (long long)a->state_vdim_stride);
+    if (a->state_slot_stride <= 0 || a->state_head_stride <= 0 || a->state_kdim_stride <= 0)
+        return fail(GDR_ERR_INVALID_ARG, "%s: state strides must be positive", fn);
+    if (a->A_head_stride < 0 || a->A_kdim_stride < 0 || a->A_vdim_stride < 0 || a->D_head_stride < 0 ||
+        a->D_vdim_stride < 0 || a->dt_bias_head_stride < 0 || a->dt_bias_vdim_stride < 0)
+        return fail(GDR_ERR_INVALID_ARG, "%s: A, D and dt_bias strides must not be negative", fn);
+    if (!aligned(a->state, esize(a->state_dtype)) || !aligned(a->A, 4) || !aligned(a->D, 4) || !aligned(a->dt_bias, 4))
+        return fail(GDR_ERR_UNSUPPORTED, "%s: state, A, D and dt_bias must be aligned to their elements", fn);
+    if (a->counts && !a->keep_state) return fail(GDR_ERR_INVALID_ARG, "%s: counts without keep_state", fn);
+    if (!a->out && !a->keep_state) return fail(GDR_ERR_INVALID_ARG, "%s: neither out nor keep_state", fn);
+    if (a->total_tokens > 0) {
+        if (!a->x || !a->dt || !a->B || (a->out && !a->C)) return fail(GDR_ERR_INVALID_ARG, "%s: x/dt/B/C is NULL", fn);
+        if (a->x_seq_stride < 0 || a->x_head_stride < 0 || a->dt_seq_stride < 0 || a->dt_head_stride < 0 ||
+            a->B_seq_stride < 0 || a->B_head_stride < 0 || a->C_seq_stride < 0 || a->C_head_stride < 0 ||
+            a->z_seq_stride < 0 || a->z_head_stride < 0)
+            return fail(GDR_ERR_INVALID_ARG, "%s: x/dt/B/C/z strides must not be negative", fn);
+        if (a->dt_elem_stride != 0 && a->dt_elem_stride != 1)
+            return fail(GDR_ERR_UNSUPPORTED, "%s: dt_elem_stride must be 0 or 1 (got %lld)", fn,
+                        (long long)a->dt_elem_stride);
+        if (a->out && ((a->total_tokens > 1 && a->out_seq_stride <= 0) || (a->nv > 1 && a->out_head_stride <= 0)))
+            return fail(GDR_ERR_INVALID_ARG, "%s: output strides must be positive", fn);
+        const uintptr_t e = esize(a->token_dtype);
+        if (!aligned(a->x, e) || !aligned(a->B, e) || !aligned(a->C, e) || !aligned(a->z, e) || !aligned(a->out, e) ||
+            !aligned(a->dt, esize(a->dt_dtype)))
+            return fail(GDR_ERR_UNSUPPORTED, "%s: x/dt/B/C/z/out must be aligned to their elements", fn);
+    }
+    if (a->workspace_bytes < 0) return fail(GDR_ERR_INVALID_ARG, "%s: workspace_bytes < 0", fn);
+    if (a->workspace && !aligned(a->workspace, 16))
+        return fail(GDR_ERR_UNSUPPORTED, "%s: workspace must be 16-byte aligned", fn);
+    return GDR_OK;
+}
+
+// Tokens a segment for rows that are cut, or 0.
+int plan_scan(const gdr_scan_args *a) {
+    if (a->batch < 1 || a->batch > 32 || a->max_row_len == 1 || !a->total_tokens) return 0;
+    const double warps = 152.0 * 4 * 6, lanes = 32.0 / (a->K <= 32 ? 4 : a->K <= 64 ? 8 : 16);
+    const double units = a->batch * std::ceil((double)a->nv * a->V / (4 * lanes));
+    const double longest = a->max_row_len > 0 ? (double)a->max_row_len : (double)a->total_tokens / a->batch;
+    if (units > 152.0 * 4 || longest < 1024) return 0;
+    double seg = std::ceil((double)a->total_tokens * (units / a->batch) / warps / 16) * 16;
+    if (seg < 256) seg = 256;
+    return seg * 2 > longest ? 0 : (int)seg;
+}
+
+int64_t scan_bytes(const gdr_scan_args *a, int seg) {
+    return gdr::scan_pieces(a->total_tokens, seg, a->batch) * (int64_t)a->nv * a->V * (a->K + 1) * 4;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gdr_short_conv(const gdr_short_conv_args *a, void *stream) {
+    const char *fn = "gdr_short_conv";
+    int rc = check_conv(a, fn);
+    if (rc) return rc;
+    if (a->batch == 0 || a->total_tokens == 0) return gdr::api_ok();
+    gdr::ConvOpParams p{};
+    if ((rc = gdr::api_status(&p.status))) return rc;
+    p.batch = a->batch;
+    p.channels = a->channels;
+    p.silu = a->activation;
+    p.keep = a->keep_state && a->width > 1;
+    p.st_bf16 = a->state_dtype == GDR_BF16;
+    p.T = a->total_tokens;
+    p.max_len = a->max_row_len;
+    p.x = a->x;
+    p.x_ts = a->x_seq_stride;
+    p.w = a->weight;
+    p.w_cs = a->weight_chan_stride;
+    p.w_ts = a->weight_tap_stride;
+    p.bias = a->bias;
+    p.out = a->out;
+    p.o_ts = a->out_seq_stride;
+    p.state = a->conv_state;
+    p.s_slot = a->state_slot_stride;
+    p.s_chan = a->state_chan_stride;
+    p.s_tap = a->state_tap_stride;
+    p.max_slots = a->max_slots;
+    p.slot_idx = a->slot_idx;
+    p.offsets = a->offsets;
+    p.counts = a->counts;
+    const int64_t es = esize(a->token_dtype);
+    p.vec = a->channels % (16 / es) == 0 && vector_rows(a->x, a->token_dtype, 16, a->x_seq_stride) &&
+            (!a->out || vector_rows(a->out, a->token_dtype, 16, a->out_seq_stride));
+    p.w_vec = a->weight_tap_stride == 1 && vector_rows(a->weight, GDR_F32, 16, a->weight_chan_stride);
+    p.st_run = a->width > 1 && (a->state_tap_stride == 1 || a->width == 2) && a->state_chan_stride == a->width - 1 &&
+               vector_rows(a->conv_state, a->state_dtype, 16, a->state_slot_stride);
+    return launched(gdr::launch_short_conv(p, a->width, a->token_dtype == GDR_BF16, static_cast<cudaStream_t>(stream)), fn);
+}
+
+int64_t gdr_selective_scan_workspace_bytes(const gdr_scan_args *a) {
+    const int rc = check_scan_sizes(a, "gdr_selective_scan_workspace_bytes");
+    if (rc) return rc;
+    const int seg = plan_scan(a);
+    return seg ? scan_bytes(a, seg) : 0;
+}
+
+int gdr_selective_scan(const gdr_scan_args *a, void *stream) {
+    const char *fn = "gdr_selective_scan";
+    int rc = check_scan(a, fn);
+    if (rc) return rc;
+    if (a->batch == 0 || a->total_tokens == 0) return gdr::api_ok();
+    gdr::ScanParams p{};
+    if ((rc = gdr::api_status(&p.status))) return rc;
+    p.batch = a->batch;
+    p.nv = a->nv;
+    p.nk = a->nk;
+    p.r = a->nv / a->nk;
+    p.K = a->K;
+    p.V = a->V;
+    p.softplus = a->dt_softplus ? 1 : 0;
+    p.keep = a->keep_state ? 1 : 0;
+    p.st_bf16 = a->state_dtype == GDR_BF16;
+    p.T = a->total_tokens;
+    p.max_len = a->max_row_len;
+    p.x = a->x;
+    p.x_ts = a->x_seq_stride;
+    p.x_hs = a->x_head_stride;
+    p.dt = a->dt;
+    p.dt_ts = a->dt_seq_stride;
+    p.dt_hs = a->dt_head_stride;
+    p.dt_es = a->dt_elem_stride;
+    p.B = a->B;
+    p.B_ts = a->B_seq_stride;
+    p.B_hs = a->B_head_stride;
+    p.C = a->C;
+    p.C_ts = a->C_seq_stride;
+    p.C_hs = a->C_head_stride;
+    p.z = a->z;
+    p.z_ts = a->z_seq_stride;
+    p.z_hs = a->z_head_stride;
+    p.A = a->A;
+    p.a_hs = a->A_head_stride;
+    p.a_ks = a->A_kdim_stride;
+    p.a_vs = a->A_vdim_stride;
+    p.D = a->D;
+    p.d_hs = a->D_head_stride;
+    p.d_vs = a->D_vdim_stride;
+    p.bias = a->dt_bias;
+    p.b_hs = a->dt_bias_head_stride;
+    p.b_vs = a->dt_bias_vdim_stride;
+    p.out = a->out;
+    p.o_ts = a->out_seq_stride;
+    p.o_hs = a->out_head_stride;
+    p.state = a->state;
+    p.st_slot = a->state_slot_stride;
+    p.st_head = a->state_head_stride;
+    p.st_k = a->state_kdim_stride;
+    p.max_slots = a->max_slots;
+    p.slot_idx = a->slot_idx;
+    p.offsets = a->offsets;
+    p.counts = a->counts;
+    const bool tb = a->token_dtype == GDR_BF16;
+    const bool vec = a->V % 8 == 0 && vector_rows(a->x, a->token_dtype, 16, p.x_ts, p.x_hs) &&
+                     (p.dt_es == 0 || vector_rows(a->dt, a->dt_dtype, 16, p.dt_ts, p.dt_hs)) &&
+                     (!a->out || vector_rows(a->out, a->token_dtype, 16, p.o_ts, p.o_hs)) &&
+                     (!a->z || vector_rows(a->z, a->token_dtype, 16, p.z_ts, p.z_hs)) &&
+                     vector_rows(a->state, a->state_dtype, 4 * esize(a->state_dtype), p.st_slot, p.st_head, p.st_k);
+    p.a_vec = p.a_vs == 1 && vector_rows(a->A, GDR_F32, 16, p.a_hs, p.a_ks);
+    p.seg = plan_scan(a);
+    if (p.seg && (!a->workspace || a->workspace_bytes < scan_bytes(a, p.seg))) p.seg = 0;
+    p.ws = static_cast<float *>(a->workspace);
+    return launched(gdr::launch_scan(p, tb, a->dt_dtype == GDR_BF16, vec, static_cast<cudaStream_t>(stream)), fn);
+}
+
+int gdr_accept_drafts(const gdr_accept_args *a, void *stream) {
+    const char *fn = "gdr_accept_drafts";
+    if (!a) return fail(GDR_ERR_INVALID_ARG, "%s: args is NULL", fn);
+    int rc = check_tokens(a->total_tokens, a->batch, fn);
+    if (rc) return rc;
+    if (a->vocab <= 0 || a->max_row_len <= 0)
+        return fail(GDR_ERR_INVALID_ARG, "%s: vocab=%d and max_row_len=%d must be positive", fn, a->vocab, a->max_row_len);
+    if (a->vocab > (1 << 28)) return fail(GDR_ERR_UNSUPPORTED, "%s: vocab must be at most 2^28", fn);
+    if (a->batch > (1 << 27)) return fail(GDR_ERR_UNSUPPORTED, "%s: batch must be at most 2^27", fn);
+    if (!is_dtype(a->prob_dtype)) return fail(GDR_ERR_UNSUPPORTED, "%s: prob_dtype must be GDR_F32 or GDR_BF16", fn);
+    if (a->batch == 0) return gdr::api_ok();
+    if (!a->offsets || !a->row_uniforms || !a->out_tokens || !a->counts)
+        return fail(GDR_ERR_INVALID_ARG, "%s: offsets/row_uniforms/out_tokens/counts is NULL", fn);
+    if (a->batch > 1 && a->out_seq_stride < a->max_row_len)
+        return fail(GDR_ERR_INVALID_ARG, "%s: out_seq_stride must be at least max_row_len", fn);
+    if (a->total_tokens > 0) {
+        if (!a->target || !a->tokens || !a->uniforms)
+            return fail(GDR_ERR_INVALID_ARG, "%s: target/tokens/uniforms is NULL", fn);
+        if (a->target_seq_stride < 0 || (a->draft && a->draft_seq_stride < 0))
+            return fail(GDR_ERR_INVALID_ARG, "%s: probability strides must not be negative", fn);
+        if (!aligned(a->target, esize(a->prob_dtype)) || !aligned(a->draft, esize(a->prob_dtype)))
+            return fail(GDR_ERR_UNSUPPORTED, "%s: target and draft must be aligned to their elements", fn);
+    }
+    gdr::AcceptParams p{};
+    if ((rc = gdr::api_status(&p.status))) return rc;
+    p.batch = a->batch;
+    p.vocab = a->vocab;
+    p.width = a->max_row_len;
+    p.T = a->total_tokens;
+    p.target = a->target;
+    p.t_ts = a->target_seq_stride;
+    p.draft = a->draft;
+    p.d_ts = a->draft_seq_stride;
+    p.tokens = a->tokens;
+    p.offsets = a->offsets;
+    p.u = a->uniforms;
+    p.row_u = a->row_uniforms;
+    p.out = a->out_tokens;
+    p.o_ts = a->out_seq_stride;
+    p.counts = a->counts;
+    p.vec = vector_rows(a->target, a->prob_dtype, 16, a->target_seq_stride) &&
+            (!a->draft || vector_rows(a->draft, a->prob_dtype, 16, a->draft_seq_stride));
+    return launched(gdr::launch_accept(p, a->prob_dtype == GDR_BF16, static_cast<cudaStream_t>(stream)), fn);
+}
+
+}  // extern "C"

@@ -1,0 +1,52 @@
+// Selective scan: the choice of types, and the join of a cut row's segments.
+#include "k_scan.cuh"
+
+namespace gdr {
+namespace {
+
+// A cut row's segments, one after the other, a thread an element (head, state, channel):
+// segment s starts from S, and S <- exp(A sum(d)) S + (its own state from zero).  Reads a
+// segment's own state and leaves its start state in its place.
+__global__ void __launch_bounds__(256) k_scan_join(const __grid_constant__ ScanParams p) {
+    const long long per = (long long)p.nv * p.K * p.V, i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= per) return;
+    const long long most = scan_pieces(p.T, p.seg, p.batch);
+    long long piece = 0;
+    ScanUnit u;
+    int n = 0;
+    for (int b = 0; b <= (int)blockIdx.y; ++b) {
+        piece += n;
+        n = scan_row(p, b, false, u) ? pieces(u.len, p.seg) : 0;
+    }
+    if (n == 0 || u.slot < 0) return;
+    const long long kv = (long long)p.K * p.V, kj = i % kv;
+    const int h = (int)(i / kv), k = (int)(kj / p.V), v = (int)(kj - (long long)k * p.V);
+    const float a = p.A[h * p.a_hs + k * p.a_ks + v * p.a_vs] * kLog2e;
+    const long long at = (long long)u.slot * p.st_slot + (long long)h * p.st_head + (long long)k * p.st_k + v;
+    float S = p.st_bf16 ? to_f32(static_cast<const uint16_t *>(p.state)[at]) : static_cast<const float *>(p.state)[at];
+    float *own = p.ws + piece * per + i;
+    const float *sum = p.ws + most * per + piece * p.nv * p.V + (long long)h * p.V + v;
+    for (int s = 0; s < n && piece + s < most; ++s) {
+        const bool last = s + 1 == n;
+        const float o = last ? 0.0f : *own, d = last ? 0.0f : *sum;
+        *own = S;
+        S = fmaf(ex2(a * d), S, o);
+        own += per;
+        sum += (long long)p.nv * p.V;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_scan_join(const ScanParams &p, cudaStream_t s) {
+    const long long per = (long long)p.nv * p.K * p.V;
+    k_scan_join<<<dim3((unsigned)((per + 255) / 256), (unsigned)p.batch), 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_scan(const ScanParams &p, bool tok_bf16, bool dt_bf16, bool vec, cudaStream_t s) {
+    if (!tok_bf16) return launch_scan_ff(p, vec, s);
+    return dt_bf16 ? launch_scan_bb(p, vec, s) : launch_scan_bf(p, vec, s);
+}
+
+}  // namespace gdr

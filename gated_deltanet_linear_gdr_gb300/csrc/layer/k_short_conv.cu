@@ -1,0 +1,305 @@
+// Short causal convolution over ragged rows, a few taps a channel:
+//
+//     y[j] = act(bias + sum_m w[m] xe[j + m]),  xe = (the slot's last inputs, the row's inputs)
+//
+// A thread owns VE neighbouring channels (a 16-byte vector of tokens, or one
+// channel where rows are not such vectors) and walks along tokens with the
+// last width-1 inputs in registers, so that an input is read once and a result
+// written once.  A few operations a byte: HBM bound; what counts is bytes in
+// flight, so kAhead tokens are asked for before the first is used.
+//
+// Two ways to deal the work out.  A block takes a whole row where rows are short
+// (single tokens, drafts).  Otherwise it takes a run of tokens, whichever rows
+// they are of, so that ragged rows fill the GPU evenly; what is read twice are the
+// width-1 tokens before a run.  The tokens of a row that need its slot's old
+// inputs (the first width-1) belong to the block that has the row's first
+// token, past the end of its run where they lie there.  Its threads also write
+// the slot, from the row's last inputs: nobody else touches it, so old inputs
+// are not overwritten before they are used, in one launch.
+#include "../gdr_device.cuh"
+#include "layer_internal.h"
+
+namespace gdr {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kAhead = 8;      // tokens on their way
+constexpr int kShortRow = 16;  // rows up to here are a block's unit
+
+__device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.0f + __expf(-y)); }
+
+struct ConvRow {
+    long long lo, hi;  // its tokens
+    int slot;          // -1: nothing to compute
+    int kept;          // inputs after which the slot is written, 0: it is not
+    bool inside;       // its tokens exist: its output may be written
+    unsigned problem;  // GDR_STATUS_* bit
+};
+
+__device__ __forceinline__ ConvRow conv_row(const ConvOpParams &p, int b) {
+    ConvRow r;
+    r.lo = p.offsets[b];
+    r.hi = p.offsets[b + 1];
+    r.slot = p.slot_idx[b];
+    const int count = p.counts ? p.counts[b] : 0;
+    const long long len = r.hi - r.lo;
+    r.inside = r.lo >= 0 && len >= 0 && r.hi <= p.T;
+    r.kept = 0;
+    r.problem = 0;
+    if (!r.inside) r.problem = GDR_STATUS_BAD_OFFSETS;
+    else if (len == 0) r.slot = -1;
+    else if (p.max_len > 0 && len > p.max_len) r.problem = GDR_STATUS_ROW_TOO_LONG;
+    else if (r.slot < -1 || r.slot >= p.max_slots) r.problem = GDR_STATUS_BAD_SLOT;
+    if (r.problem) r.slot = -1;
+    if (r.slot >= 0 && p.keep) {
+        if (!p.counts) r.kept = (int)len;
+        else if (count < 0 || count > len) r.problem = GDR_STATUS_BAD_COUNT;
+        else r.kept = count;
+    }
+    return r;
+}
+
+// The same N values a thread keeps together in memory, moved as vectors.
+template <typename ST, int N> struct Together {
+    static constexpr int C = N * (int)sizeof(ST) % 16 == 0 ? 16 / (int)sizeof(ST) : 8 / (int)sizeof(ST);
+    static_assert(N % C == 0, "whole vectors");
+    __device__ static __forceinline__ void load(const ST *p, float (&v)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; i += C) {
+            Pack<ST, C> q;
+            q.load(p + i);
+#pragma unroll
+            for (int j = 0; j < C; ++j) v[i + j] = q.get(j);
+        }
+    }
+    __device__ static __forceinline__ void store(ST *p, const float (&v)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; i += C) {
+            Pack<ST, C> q;
+#pragma unroll
+            for (int j = 0; j < C; ++j) q.set(j, v[i + j]);
+            q.store(p + i);
+        }
+    }
+};
+
+template <typename TT, int W, int VE> struct ConvThread {
+    static constexpr int N = W > 1 ? W - 1 : 1;  // inputs a row remembers
+    const ConvOpParams &p;
+    const int c0;
+    float w[W][VE], bias[VE];
+    float win[N][VE];  // the last inputs, oldest first
+
+    __device__ __forceinline__ ConvThread(const ConvOpParams &pp, int c) : p(pp), c0(c) {}
+
+    __device__ __forceinline__ const TT *x(long long t) const { return static_cast<const TT *>(p.x) + t * p.x_ts + c0; }
+    __device__ __forceinline__ TT *out(long long t) const { return static_cast<TT *>(p.out) + t * p.o_ts + c0; }
+
+    __device__ __forceinline__ void weights() {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            const float *wp = p.w + (long long)(c0 + e) * p.w_cs;
+            if (W == 4 && p.w_vec) {
+                const float4 q = *reinterpret_cast<const float4 *>(wp);
+                w[0][e] = q.x;
+                w[1 % W][e] = q.y;
+                w[2 % W][e] = q.z;
+                w[3 % W][e] = q.w;
+            } else {
+#pragma unroll
+                for (int m = 0; m < W; ++m) w[m][e] = wp[m * p.w_ts];
+            }
+            bias[e] = p.bias ? p.bias[c0 + e] : 0.0f;
+        }
+    }
+
+    // A slot's inputs of this thread's channels, channel by channel.
+    template <typename ST> __device__ __forceinline__ void read(int slot, float (&v)[VE * N]) const {
+        const ST *s = static_cast<const ST *>(p.state) + (long long)slot * p.s_slot + (long long)c0 * p.s_chan;
+        if (VE > 1 && p.st_run) {
+            if constexpr (VE > 1) Together<ST, VE * N>::load(s, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VE * N; ++i) v[i] = to_f32(s[(i / N) * p.s_chan + (i % N) * p.s_tap]);
+        }
+    }
+    template <typename ST> __device__ __forceinline__ void write(int slot, const float (&v)[VE * N]) const {
+        ST *s = static_cast<ST *>(p.state) + (long long)slot * p.s_slot + (long long)c0 * p.s_chan;
+        if (VE > 1 && p.st_run) {
+            if constexpr (VE > 1) Together<ST, VE * N>::store(s, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VE * N; ++i) s[(i / N) * p.s_chan + (i % N) * p.s_tap] = from_f32<ST>(v[i]);
+        }
+    }
+
+    // A row's beginning: the slot's inputs into the window, and the slot's new ones, which are
+    // entries kept .. kept + W - 2 of (old inputs, the row's inputs).
+    __device__ __forceinline__ void begin(const ConvRow &r) {
+        if constexpr (W > 1) {
+            float v[VE * N];
+            if (p.st_bf16) read<uint16_t>(r.slot, v);
+            else read<float>(r.slot, v);
+#pragma unroll
+            for (int i = 0; i < VE * N; ++i) win[i % N][i / N] = v[i];
+            if (r.kept <= 0) return;
+#pragma unroll
+            for (int m = 0; m < N; ++m) {
+                const int i = r.kept + m;  // entry of (old inputs, the row's)
+                Pack<TT, VE> in;
+                if (i >= N) in.load(x(r.lo + i - N));
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    float y = i >= N ? in.get(e) : 0.0f;
+#pragma unroll
+                    for (int j = 1; j < N; ++j)
+                        if (i == j) y = win[j][e];
+                    v[e * N + m] = y;
+                }
+            }
+            if (p.st_bf16) write<uint16_t>(r.slot, v);
+            else write<float>(r.slot, v);
+        }
+    }
+    // The window in front of token t, all of it in the row.
+    __device__ __forceinline__ void enter(long long t) {
+        if constexpr (W > 1) {
+#pragma unroll
+            for (int m = 0; m < N; ++m) {
+                Pack<TT, VE> in;
+                in.load(x(t - N + m));
+#pragma unroll
+                for (int e = 0; e < VE; ++e) win[m][e] = in.get(e);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void token(const Pack<TT, VE> &in, TT *to) {
+        Pack<TT, VE> o;
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+            const float v = in.get(e);
+            float y = bias[e];
+#pragma unroll
+            for (int m = 0; m < W - 1; ++m) y = fmaf(w[m][e], win[m][e], y);
+            y = fmaf(w[W - 1][e], v, y);
+            o.set(e, p.silu ? silu(y) : y);
+#pragma unroll
+            for (int m = 0; m + 1 < N; ++m) win[m][e] = win[m + 1][e];
+            win[N - 1][e] = v;
+        }
+        o.store(to);
+    }
+
+    __device__ __forceinline__ void run(long long s, long long e) {
+        const TT *from = x(s);
+        TT *to = out(s);
+        long long n = e - s;
+        for (; n >= kAhead; n -= kAhead) {
+            Pack<TT, VE> in[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) in[i].load(from + i * p.x_ts);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) token(in[i], to + i * p.o_ts);
+            from += kAhead * p.x_ts;
+            to += kAhead * p.o_ts;
+        }
+        for (; n > 0; --n) {
+            Pack<TT, VE> in;
+            in.load(from);
+            token(in, to);
+            from += p.x_ts;
+            to += p.o_ts;
+        }
+    }
+    __device__ __forceinline__ void clear(long long s, long long e) {
+        Pack<TT, VE> o;
+#pragma unroll
+        for (int i = 0; i < VE; ++i) o.u.e[i] = TT(0);
+        for (; s < e; ++s) o.store(out(s));
+    }
+};
+
+template <typename TT, int W, int VE>
+__global__ void __launch_bounds__(kThreads) k_short_conv(const __grid_constant__ ConvOpParams p) {
+    const unsigned block = blockIdx.x / (unsigned)p.tiles, tile = blockIdx.x - block * (unsigned)p.tiles;
+    const int tid = threadIdx.x, c0 = (int)(tile * kThreads + threadIdx.x) * VE;
+    const bool on = c0 < p.channels;
+    ConvThread<TT, W, VE> th(p, c0);
+    if (p.rows_form) {
+        const ConvRow r = conv_row(p, (int)block);
+        if (r.problem && tile == 0 && tid == 0) flag(p.status, r.problem);
+        if (!on || !r.inside) return;
+        if (r.slot < 0) {
+            if (p.out) th.clear(r.lo, r.hi);
+            return;
+        }
+        if (p.out) th.weights();
+        th.begin(r);
+        if (p.out) th.run(r.lo, r.hi);
+        return;
+    }
+    if (blockIdx.x == 0)  // one block looks at every row
+        for (int b = tid; b < p.batch; b += kThreads) {
+            const unsigned problem = conv_row(p, b).problem;
+            if (problem) flag(p.status, problem);
+        }
+    const long long t0 = (long long)block * p.run, t1 = t0 + p.run < p.T ? t0 + p.run : p.T;
+    // the row of the first token: the last one that does not begin behind it
+    int b = -1;
+    for (int i = 0; i <= p.batch; i += kThreads) {
+        const bool before = i + tid <= p.batch && p.offsets[i + tid] <= t0;
+        b += __syncthreads_count(before);
+    }
+    if (!on) return;
+    th.weights();
+    for (b = b < 0 ? 0 : b; b < p.batch && p.offsets[b] < t1; ++b) {
+        const ConvRow r = conv_row(p, b);
+        const bool first = r.lo >= t0;  // the row begins in this run
+        const long long head = r.lo + (W - 1);
+        const long long s = first ? r.lo : (t0 > head ? t0 : head), end = first && head > t1 ? head : t1;
+        const long long e = r.hi < end ? r.hi : end;
+        if (!r.inside || s >= e) continue;
+        if (r.slot < 0) {
+            th.clear(s, e);
+            continue;
+        }
+        if (first) th.begin(r);
+        else th.enter(s);
+        th.run(s, e);
+    }
+}
+
+template <typename TT, int W> cudaError_t go(ConvOpParams p, cudaStream_t s) {
+    constexpr int VE = 16 / (int)sizeof(TT);
+    const int wide = (p.vec ? VE : 1) * kThreads;
+    p.tiles = (p.channels + wide - 1) / wide;
+    // Rows' lengths as far as the caller bounds them: a block a row where none is longer than
+    // kShortRow tokens, and where only states move.
+    p.rows_form = !p.out || (p.max_len > 0 && p.max_len <= kShortRow);
+    long long blocks = p.batch;
+    if (!p.rows_form) {
+        // runs of up to 64 tokens, shorter ones where they would leave multiprocessors without work
+        p.run = 64;
+        while (p.run > 8 && (p.T + p.run - 1) / p.run * p.tiles < 152 * 12) p.run /= 2;
+        blocks = (p.T + p.run - 1) / p.run;
+    }
+    blocks *= p.tiles;
+    if (blocks <= 0) return cudaSuccess;
+    if (blocks >= (1ll << 31)) return cudaErrorInvalidConfiguration;
+    if (p.vec) k_short_conv<TT, W, VE><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+    else k_short_conv<TT, W, 1><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename TT> cudaError_t width(const ConvOpParams &p, int w, cudaStream_t s) {
+    return w == 4 ? go<TT, 4>(p, s) : w == 3 ? go<TT, 3>(p, s) : w == 2 ? go<TT, 2>(p, s) : go<TT, 1>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_short_conv(ConvOpParams p, int w, bool tok_bf16, cudaStream_t s) {
+    return tok_bf16 ? width<uint16_t>(p, w, s) : width<float>(p, w, s);
+}
+
+}  // namespace gdr

@@ -81,6 +81,85 @@ cudaError_t launch_norm(const NormParams &p, int vec, cudaStream_t s);
 cudaError_t launch_norm_pairs(const NormParams &p, cudaStream_t s);
 cudaError_t launch_norm_odd(const NormParams &p, cudaStream_t s);
 
+// One short convolution call, after validation.  Strides in elements.
+struct ConvOpParams {
+    int batch, channels, silu;
+    int rows_form;     // a block takes a whole row; else a run of `run` tokens, whichever rows they are of
+    int run, tiles;    // tiles: channel tiles
+    int keep;          // slots are written
+    int vec;           // token rows may be moved as 16-byte vectors
+    int w_vec;         // a channel's weights lie together, four of them as one vector
+    int st_run;        // a slot's [channels, width-1] lie together, 16-byte aligned
+    int st_bf16;
+    long long T, max_len;
+    const void *x;
+    long long x_ts;
+    const float *w;
+    long long w_cs, w_ts;
+    const float *bias;
+    void *out;         // or null: only states move
+    long long o_ts;
+    void *state;
+    long long s_slot, s_chan, s_tap;
+    long long max_slots;
+    const int *slot_idx, *offsets, *counts;
+    unsigned *status;
+};
+cudaError_t launch_short_conv(ConvOpParams p, int width, bool tok_bf16, cudaStream_t s);
+
+// One selective scan call, after validation.  Strides in elements.
+struct ScanParams {
+    int batch, nv, nk, r;  // r = nv / nk
+    int K, V;
+    int softplus, keep;
+    int st_bf16;
+    int a_vec;         // A may be read as vectors along V
+    int bc_vec;        // B and C rows may be moved as 16-byte vectors
+    long long T, max_len;
+    const void *x, *dt, *B, *C, *z;
+    long long x_ts, x_hs, dt_ts, dt_hs, dt_es, B_ts, B_hs, C_ts, C_hs, z_ts, z_hs;
+    const float *A, *D, *bias;
+    long long a_hs, a_ks, a_vs, d_hs, d_vs, b_hs, b_vs;
+    void *out;         // or null: only states move
+    long long o_ts, o_hs;
+    void *state;
+    long long st_slot, st_head, st_k;
+    long long max_slots;
+    const int *slot_idx, *offsets, *counts;
+    // rows cut into segments of `seg` tokens (0: whole): ws holds, for each of them,
+    // its own state from zero, which becomes its start state, and the sum of its step sizes
+    int seg;
+    float *ws;
+    unsigned *status;
+};
+// Most segments a call can have: rows end inside segments.
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline long long scan_pieces(long long T, int seg, int batch) { return T / seg + batch; }
+// vec: groups of 8 channels may be moved as vectors everywhere.
+cudaError_t launch_scan(const ScanParams &p, bool tok_bf16, bool dt_bf16, bool vec, cudaStream_t s);
+cudaError_t launch_scan_bb(const ScanParams &p, bool vec, cudaStream_t s);  // bfloat16 tokens and step sizes
+cudaError_t launch_scan_bf(const ScanParams &p, bool vec, cudaStream_t s);  // bfloat16 tokens, float32 step sizes
+cudaError_t launch_scan_ff(const ScanParams &p, bool vec, cudaStream_t s);  // float32
+cudaError_t launch_scan_join(const ScanParams &p, cudaStream_t s);
+
+// One verification of drafts, after validation.
+struct AcceptParams {
+    int batch, vocab, width;
+    int vec;           // probability rows may be moved as 16-byte vectors
+    long long T;
+    const void *target, *draft;
+    long long t_ts, d_ts;
+    const int *tokens, *offsets;
+    const float *u, *row_u;
+    int *out;
+    long long o_ts;
+    int *counts;
+    unsigned *status;
+};
+cudaError_t launch_accept(const AcceptParams &p, bool bf16, cudaStream_t s);
+
 #ifdef __CUDACC__
 // A skipped row's output: zeros over rows x width elements (a multiple of 8 up to
 // 128), by the whole CTA of at least 32 threads.  vec: rows are 16-byte vectors.

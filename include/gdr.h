@@ -65,12 +65,13 @@ extern "C" {
 #define GDR_STATUS_BAD_SLOT 0x1u          /* slot_idx[b] < -1 or >= max_slots          */
 #define GDR_STATUS_BAD_OFFSETS 0x2u       /* offsets not monotone or beyond T          */
 #define GDR_STATUS_BAD_RING_SLOT 0x4u     /* ring_slot_idx[b] outside [0, ring_rows)   */
-#define GDR_STATUS_BAD_COUNT 0x8u         /* fold count < 0                            */
+#define GDR_STATUS_BAD_COUNT 0x8u         /* fold count < 0; a kept count outside [0, row length] */
 #define GDR_STATUS_ROW_TOO_LONG 0x10u     /* a row longer than args.max_row_len        */
 #define GDR_STATUS_BAD_ACCEPTED 0x20u     /* rollback index outside [-1, n_inter)      */
 #define GDR_STATUS_SNAPSHOT_OVERFLOW 0x40u /* a row has more complete drafts than n_inter */
 #define GDR_STATUS_BAD_DECAY 0x80u        /* gdr_linattn_fwd: a head's lambda outside [0, 1] */
 #define GDR_STATUS_TIMEOUT 0x100u         /* a wait inside a kernel ran out: the call's results are not valid */
+#define GDR_STATUS_NO_MASS 0x200u         /* gdr_accept_drafts: a row's probabilities leave nothing to draw from */
 
 /* ---- dtypes ------------------------------------------------------------- */
 typedef enum gdr_dtype { GDR_F32 = 0, GDR_BF16 = 1 } gdr_dtype;
@@ -489,6 +490,211 @@ typedef struct gdr_norm_args {
 } gdr_norm_args;
 
 int gdr_block_norm(const gdr_norm_args *args, void *stream);
+
+/*
+ * Short causal convolution (gdr_conv_args describes the same convolution where
+ * gdr_fwd_conv runs it inside the recurrence; this entry is for layers whose
+ * projections stand between the two).  For every row b, channel c and token j of
+ * the row, with xe = the slot's last width-1 inputs (oldest first) followed by
+ * the row's inputs,
+ *
+ *     out[t0+j, c] = act(bias[c] + sum_m weight[c, m] * xe[j + m]),  m = 0 .. width-1
+ *
+ * in float32, rounded once.
+ *
+ * x, out   [total_tokens, channels] in token_dtype, unit channel stride; out must
+ *          not lie on x.  out NULL: only the states move (see counts).
+ * weight   [channels, width] float32; bias [channels] float32, unit stride, or NULL.
+ * conv_state [max_slots, channels, width-1] in state_dtype (bfloat16 loses
+ *          nothing of bfloat16 inputs), any positive strides, not lying on x or
+ *          out; unused when width == 1.
+ * slot_idx, offsets, max_row_len  as in gdr_step_args.
+ * keep_state, counts  which inputs a row leaves in its slot: with keep_state the
+ *          last width-1 of (old state, the row's first counts[b] inputs), where
+ *          counts NULL means all of the row; counts[b] = 0 leaves the slot as it
+ *          is, and so does a count outside [0, row length], which is flagged
+ *          GDR_STATUS_BAD_COUNT.  Without keep_state no slot is written.
+ * A verify pass of drafts runs without keep_state; the accepted tokens then go
+ * in by a second call with counts and out NULL, which reads only them.
+ */
+typedef struct gdr_short_conv_args {
+    int32_t batch;
+    int32_t channels;
+    int32_t width;       /* 1 .. 4 */
+    int32_t activation;  /* 0: none, 1: SiLU */
+    int32_t token_dtype; /* gdr_dtype of x and out */
+    int32_t state_dtype; /* gdr_dtype of conv_state */
+    int32_t keep_state;
+    int64_t total_tokens;
+    int64_t max_row_len;
+    const void *x;
+    int64_t x_seq_stride;
+    const float *weight;
+    int64_t weight_chan_stride;
+    int64_t weight_tap_stride;
+    const float *bias;
+    void *out;
+    int64_t out_seq_stride;
+    void *conv_state;
+    int64_t state_slot_stride;
+    int64_t state_chan_stride;
+    int64_t state_tap_stride;
+    int64_t max_slots;
+    const int32_t *slot_idx;
+    const int32_t *offsets;
+    const int32_t *counts;
+} gdr_short_conv_args;
+
+int gdr_short_conv(const gdr_short_conv_args *args, void *stream);
+
+/*
+ * Selective state space scan (no counterpart on the pages; the sibling of the
+ * recurrence whose decays belong to every single state and follow the token), on
+ * the same pools, rows and heads.  For every live row b, value head h, channel j
+ * and state i of S = pool[slot_idx[b], h], key head hk = h / (nv / nk), each token
+ * does, in float32,
+ *
+ *     d       = softplus(dt[t,h,j] + dt_bias[h,j])    (without dt_softplus: the sum itself)
+ *     S[i,j]  = exp(d * A[h,i,j]) * S[i,j] + d * x[t,h,j] * B[t,hk,i]
+ *     y       = sum_i C[t,hk,i] * S[i,j] + D[h,j] * x[t,h,j]
+ *     out     = y                  (z given: y * z / (1 + exp(-z)))
+ *
+ * x, z, out  [total_tokens, nv, V] in token_dtype, unit channel stride; z NULL: none.
+ * dt       [total_tokens, nv, V] in dt_dtype (token_dtype or float32); dt_elem_stride
+ *          1, or 0 for one step size a head.
+ * B, C     [total_tokens, nk, K] in token_dtype, unit stride along K.
+ * A        [nv, K, V] float32, D and dt_bias [nv, V] float32 (NULL: none), any
+ *          strides, 0 among them.  exp(d A) is taken as it comes: nothing asks
+ *          A to be negative.
+ * state    [max_slots, nv, K, V] pool of state_dtype, V contiguous.
+ * slot_idx, offsets, max_row_len  as in gdr_step_args.
+ * keep_state, counts  the state that goes back to a slot: with keep_state the one
+ *          behind the row's first counts[b] tokens (counts NULL: behind all of
+ *          them; 0 leaves the slot as it is, and so does a count outside
+ *          [0, row length], which is flagged GDR_STATUS_BAD_COUNT); without it none.
+ * out NULL only moves the states (C, D and z are not read; with counts only the
+ *          counted tokens are).  A verify pass of drafts runs without keep_state,
+ *          the accepted tokens then go in by such a call.
+ * workspace  as in gdr_linattn_args, by gdr_selective_scan_workspace_bytes().
+ * K is 1 to 128, V any.  A bfloat16 pool and bfloat16 outputs are rounded to
+ * nearest-even once.  A non-finite value spoils its own row only.
+ */
+typedef struct gdr_scan_args {
+    int32_t batch;
+    int32_t nv;
+    int32_t nk;
+    int32_t K;
+    int32_t V;
+    int32_t dt_softplus;
+    int32_t token_dtype; /* gdr_dtype of x, B, C, z and out */
+    int32_t dt_dtype;    /* gdr_dtype of dt: token_dtype or GDR_F32 */
+    int32_t state_dtype; /* gdr_dtype of the pool */
+    int32_t keep_state;
+    int64_t total_tokens;
+    int64_t max_row_len;
+    const void *x;
+    int64_t x_seq_stride;
+    int64_t x_head_stride;
+    const void *dt;
+    int64_t dt_seq_stride;
+    int64_t dt_head_stride;
+    int64_t dt_elem_stride;
+    const void *B;
+    int64_t B_seq_stride;
+    int64_t B_head_stride;
+    const void *C;
+    int64_t C_seq_stride;
+    int64_t C_head_stride;
+    const void *z;
+    int64_t z_seq_stride;
+    int64_t z_head_stride;
+    const float *A;
+    int64_t A_head_stride;
+    int64_t A_kdim_stride;
+    int64_t A_vdim_stride;
+    const float *D;
+    int64_t D_head_stride;
+    int64_t D_vdim_stride;
+    const float *dt_bias;
+    int64_t dt_bias_head_stride;
+    int64_t dt_bias_vdim_stride;
+    void *out;
+    int64_t out_seq_stride;
+    int64_t out_head_stride;
+    void *state;
+    int64_t state_slot_stride;
+    int64_t state_head_stride;
+    int64_t state_kdim_stride;
+    int64_t state_vdim_stride;
+    int64_t max_slots;
+    const int32_t *slot_idx;
+    const int32_t *offsets;
+    const int32_t *counts;
+    void *workspace;
+    int64_t workspace_bytes;
+} gdr_scan_args;
+
+int gdr_selective_scan(const gdr_scan_args *args, void *stream);
+
+/* Workspace bytes that gdr_selective_scan would use for these arguments (0 where
+ * it needs none), or a negative code. */
+int64_t gdr_selective_scan_workspace_bytes(const gdr_scan_args *args);
+
+/*
+ * Verification of drafted tokens (no counterpart on the pages): what turns the
+ * outputs of a verify pass into the counts that gdr_fold, gdr_rollback and the
+ * state_only calls above take.  Row b's tokens are the ones the verify pass
+ * ran: tokens[t0] the last one known, tokens[t0+1 ...] the drafts.  target[t] are
+ * the target model's probabilities for what follows token t, draft[t] those
+ * that draft t+1 was drawn from.  Drafts are taken one after the other while
+ *
+ *     uniforms[t] * draft[t, d] < target[t, d],   d = tokens[t+1]
+ *
+ * (draft NULL: the drafts were not drawn, draft[t, d] = 1 and 0 elsewhere).  At
+ * the first refused draft, position t, the next token is drawn with weights
+ * w(x) = max(target[t, x] - draft[t, x], 0), or target[t, x] where they are all 0;
+ * behind the last draft with w(x) = target[t, x]: the least x with
+ *
+ *     sum_{y <= x} w(y) > row_uniforms[b] * sum_y w(y)
+ *
+ * (none, by a number of 1 or more: the last x with a weight; numbers below 0 and
+ * NaN count as 0, for which it is the first).  So the tokens are distributed as
+ * the target's own.  Comparisons and differences are exact, sums carry 46 bits at
+ * least; weights need not sum to 1, but to less than 2^127.
+ *
+ * out_tokens [batch, max_row_len] int32: the accepted drafts, the drawn token, -1
+ *          behind it.  counts [batch] int32: the accepted drafts and 1, which is
+ *          how many of the row's tokens belong to the sequence now.
+ * target, draft [total_tokens, vocab] in prob_dtype, unit stride; their rows
+ *          that no rule above asks for are not read.  Values that are negative,
+ *          infinite or NaN count as 0.
+ * tokens [total_tokens] int32.  A draft outside [0, vocab) ends the row's drafts
+ *          before it.  uniforms [total_tokens], row_uniforms [batch] float32 in [0, 1).
+ * max_row_len  the width of out_tokens, at least 1; a longer row is skipped and
+ *          flagged.  A skipped or empty row has count 0 and tokens -1; a row
+ *          with nothing to draw from gets the token -1 behind its accepted drafts
+ *          and GDR_STATUS_NO_MASS.
+ */
+typedef struct gdr_accept_args {
+    int32_t batch;
+    int32_t vocab;
+    int32_t prob_dtype; /* gdr_dtype of target and draft */
+    int32_t max_row_len;
+    int64_t total_tokens;
+    const void *target;
+    int64_t target_seq_stride;
+    const void *draft;
+    int64_t draft_seq_stride;
+    const int32_t *tokens;
+    const int32_t *offsets;
+    const float *uniforms;
+    const float *row_uniforms;
+    int32_t *out_tokens;
+    int64_t out_seq_stride;
+    int32_t *counts;
+} gdr_accept_args;
+
+int gdr_accept_drafts(const gdr_accept_args *args, void *stream);
 
 /* Reads the current device's status word (GDR_STATUS_* bits) into *status and,
  * if clear != 0, resets it.  Synchronises the device. */
