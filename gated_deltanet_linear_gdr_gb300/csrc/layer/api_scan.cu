@@ -286,11 +286,14 @@ int gdr_selective_scan(const gdr_scan_args *a, void *stream) {
                      (!a->out || vector_rows(a->out, a->token_dtype, 16, p.o_ts, p.o_hs)) &&
                      (!a->z || vector_rows(a->z, a->token_dtype, 16, p.z_ts, p.z_hs)) &&
                      vector_rows(a->state, a->state_dtype, 4 * esize(a->state_dtype), p.st_slot, p.st_head, p.st_k);
+    p.bc_vec = vector_rows(a->B, a->token_dtype, 16, p.B_ts, p.B_hs) && (!a->C || vector_rows(a->C, a->token_dtype, 16, p.C_ts, p.C_hs));
     p.a_vec = p.a_vs == 1 && vector_rows(a->A, GDR_F32, 16, p.a_hs, p.a_ks);
     p.seg = plan_scan(a);
     if (p.seg && (!a->workspace || a->workspace_bytes < scan_bytes(a, p.seg))) p.seg = 0;
     p.ws = static_cast<float *>(a->workspace);
-    return launched(gdr::launch_scan(p, tb, a->dt_dtype == GDR_BF16, vec, static_cast<cudaStream_t>(stream)), fn);
+    const bool db = a->dt_dtype == GDR_BF16;
+    if (a->max_row_len == 1) return launched(gdr::launch_scan_step(p, tb, db, vec, static_cast<cudaStream_t>(stream)), fn);
+    return launched(gdr::launch_scan(p, tb, db, vec, static_cast<cudaStream_t>(stream)), fn);
 }
 
 int gdr_accept_drafts(const gdr_accept_args *a, void *stream) {

@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(256) k_scan_join(const __grid_constant__ ScanP
     if (n == 0 || u.slot < 0) return;
     const long long kv = (long long)p.K * p.V, kj = i % kv;
     const int h = (int)(i / kv), k = (int)(kj / p.V), v = (int)(kj - (long long)k * p.V);
-    const float a = p.A[h * p.a_hs + k * p.a_ks + v * p.a_vs] * kLog2e;
+    const float a = p.A[h * p.a_hs + k * p.a_ks + v * p.a_vs];
     const long long at = (long long)u.slot * p.st_slot + (long long)h * p.st_head + (long long)k * p.st_k + v;
     float S = p.st_bf16 ? to_f32(static_cast<const uint16_t *>(p.state)[at]) : static_cast<const float *>(p.state)[at];
     float *own = p.ws + piece * per + i;
@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(256) k_scan_join(const __grid_constant__ ScanP
         const bool last = s + 1 == n;
         const float o = last ? 0.0f : *own, d = last ? 0.0f : *sum;
         *own = S;
-        S = fmaf(ex2(a * d), S, o);
+        S = fmaf(expf(a * d), S, o);
         own += per;
         sum += (long long)p.nv * p.V;
     }

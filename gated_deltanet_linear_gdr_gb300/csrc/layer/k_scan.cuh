@@ -19,66 +19,12 @@
 // memory, to be finished (D x, the gate) and stored as vectors.
 #pragma once
 
-#include "../gdr_device.cuh"
-#include "layer_internal.h"
+#include "scan_device.cuh"
 
 namespace gdr {
 
 constexpr int kScanChunk = 16;
 constexpr int kScanWarps = 4;  // a block's
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-constexpr float kLog2e = 1.4426950408889634f;
-
-// log(1 + e^v) without cancellation: max(v, 0) + log1p(e^-|v|).
-__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.0f) + log1pf(__expf(-fabsf(v))); }
-
-struct ScanUnit {
-    int b;
-    long long t0;     // the unit's first token
-    int len;          // its tokens
-    int slot;         // -1: output cleared, nothing else
-    int kept;         // tokens of the unit after which the slot is written, 0: it is not
-    long long piece;  // segment index over all rows (segmented calls)
-    bool last;        // the row's last segment
-};
-
-// The row's facts; flags its problems where `leader`.  False: nothing to do.
-__device__ __forceinline__ bool scan_row(const ScanParams &p, int b, bool leader, ScanUnit &u) {
-    const int lo = p.offsets[b], hi = p.offsets[b + 1];
-    u.b = b;
-    u.slot = p.slot_idx[b];
-    const int count = p.counts ? p.counts[b] : 0;
-    if (lo < 0 || hi < lo || hi > p.T) {
-        if (leader) flag(p.status, GDR_STATUS_BAD_OFFSETS);
-        return false;
-    }
-    u.t0 = lo;
-    u.len = hi - lo;
-    u.kept = 0;
-    u.piece = 0;
-    u.last = true;
-    if (u.len == 0) return false;
-    unsigned problem = 0;
-    if (p.max_len > 0 && u.len > p.max_len) problem = GDR_STATUS_ROW_TOO_LONG;
-    else if (u.slot < -1 || u.slot >= p.max_slots) problem = GDR_STATUS_BAD_SLOT;
-    if (problem) u.slot = -1;
-    if (u.slot >= 0 && p.keep) {
-        if (!p.counts) u.kept = u.len;
-        else if (count < 0 || count > u.len) problem = GDR_STATUS_BAD_COUNT;
-        else u.kept = count;
-    }
-    if (problem && leader) flag(p.status, problem);
-    if (!p.out) {  // only states move: tokens that are not kept are not read
-        u.len = u.slot >= 0 ? u.kept : 0;
-        if (u.len == 0) return false;
-    }
-    return true;
-}
 
 // Segment `piece` of all rows' segments, for calls of at most 32 rows: lane l counts row l's.
 __device__ __forceinline__ bool scan_piece(const ScanParams &p, long long piece, bool leader, int lane, ScanUnit &u) {
@@ -106,20 +52,24 @@ __device__ __forceinline__ bool scan_piece(const ScanParams &p, long long piece,
     return true;
 }
 
-// Where a warp's chunk lies in shared memory, in floats.
-template <int KT, int LK> struct ScanShared {
-    static constexpr int W = 4 * (32 / LK), KP = KT * LK;
-    static constexpr int d = 0, x = d + kScanChunk * W, y = x + kScanChunk * W, B = y + kScanChunk * W,
-                         C = B + kScanChunk * KP, bias = C + kScanChunk * KP, D = bias + W, size = D + W;
+// A warp's piece of shared memory, in bytes: two stages of raw chunks, then the chunk in float32.
+template <typename TT, typename DT, int KT, int LK> struct ScanShared {
+    static constexpr int W = 4 * (32 / LK), KP = KT * LK, N = kScanChunk;
+    static constexpr bool wide = sizeof(TT) == 4;  // raw B and C are used as they are
+    static constexpr int x = 0, z = x + N * W * (int)sizeof(TT), dt = z + N * W * (int)sizeof(TT), B = dt + N * W * (int)sizeof(DT),
+                         C = B + N * KP * (int)sizeof(TT), stage = C + N * KP * (int)sizeof(TT);
+    static constexpr int fd = 2 * stage, fx = fd + 4 * N * W, fy = fx + 4 * N * W, fB = fy + 4 * N * W,
+                         fC = fB + (wide ? 0 : 4 * N * KP), bias = fC + (wide ? 0 : 4 * N * KP), D = bias + 4 * W,
+                         bytes = D + 4 * W;
 };
 
-// FIRST: the pass over segments that only works out their own states, from zero,
-// and the sums of their step sizes.
-template <typename TT, typename DT, int KT, int LK, bool VEC, bool FIRST>
-__global__ void __launch_bounds__(32 * kScanWarps) k_scan(const __grid_constant__ ScanParams p, int tiles, unsigned units) {
-    using Sh = ScanShared<KT, LK>;
-    constexpr int W = Sh::W, KP = Sh::KP, CH = 4;
-    extern __shared__ __align__(16) float shared[];
+// READ: with outputs.  Without them states move only: into the slots, or (first != 0)
+// each segment's own state, from zero, and the sum of its step sizes into the workspace.
+template <typename TT, typename DT, int KT, int LK, bool VEC, bool READ>
+__global__ void __launch_bounds__(32 * kScanWarps) k_scan(const __grid_constant__ ScanParams p, int tiles, unsigned units, int first) {
+    using Sh = ScanShared<TT, DT, KT, LK>;
+    constexpr int W = Sh::W, KP = Sh::KP, CH = 4, N = kScanChunk;
+    extern __shared__ __align__(16) unsigned char shared[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned unit = blockIdx.x * kScanWarps + warp;
     if (unit >= units) return;
@@ -127,14 +77,17 @@ __global__ void __launch_bounds__(32 * kScanWarps) k_scan(const __grid_constant_
     const int g = (int)(tg / (unsigned)tiles), tile = (int)(tg - (unsigned)g * (unsigned)tiles);
     ScanUnit u;
     if (p.seg) {
-        if (!scan_piece(p, row, tg == 0 && !FIRST, lane, u)) return;
-        if (FIRST && u.last) return;  // no segment starts from its state
+        if (!scan_piece(p, row, tg == 0 && !first, lane, u)) return;
+        if (first && u.last) return;  // no segment starts from its state
     } else if (!scan_row(p, (int)row, tg == 0 && lane == 0, u)) {
         return;
     }
     const int group = p.r * p.V, c0 = tile * W;  // channels of the key head's value heads, this warp's first
     const int width = min(W, group - c0);
-    float *const sh = shared + warp * Sh::size;
+    unsigned char *const sh = shared + warp * Sh::bytes;
+    float *const fd = reinterpret_cast<float *>(sh + Sh::fd), *const fx = reinterpret_cast<float *>(sh + Sh::fx);
+    float *const fy = reinterpret_cast<float *>(sh + Sh::fy);
+    float *const fbias = reinterpret_cast<float *>(sh + Sh::bias), *const fD = reinterpret_cast<float *>(sh + Sh::D);
 
     // A channel of the group as (value head, channel).
     auto head = [&](int c, int &j) {
@@ -143,40 +96,121 @@ __global__ void __launch_bounds__(32 * kScanWarps) k_scan(const __grid_constant_
         return g * p.r + h;
     };
 
-    // tokens by vectors: lane's piece of 8 channels, of token lane / PCS and every TPP-th behind it
-    constexpr int PCS = W / 8, TPP = 32 / PCS;
-    const int pc = lane % PCS, pt = lane / PCS;
-    int pj = 0, ph = 0;
-    bool pon = false;
-    // tokens one by one: channel lane % W, of token lane / W and every (32 / W)-th behind it
-    constexpr int TPS = 32 / W;
-    const int sc = lane % W, stt = lane / W;
-    if constexpr (VEC) {
-        pon = pc * 8 < width;
-        if (pon) ph = head(c0 + pc * 8, pj);
-    } else {
-        pon = sc < width;
-        if (pon) ph = head(c0 + sc, pj);
-    }
+    // A lane's part in moving tokens: vectors of 8 channels (piece pc of tokens pt, pt + TPP, ...), or
+    // one channel (sc of tokens ps, ps + TPS, ...) where rows are not such vectors.
+    constexpr int PCS = W / 8, TPP = 32 / PCS, TPS = 32 / W;
+    const int pc = lane % PCS, pt = lane / PCS, sc = lane % W, ps = lane / W;
+    int mj = 0, mh = 0;
+    const bool mon = (VEC ? pc * 8 : sc) < width;
+    if (mon) mh = head(c0 + (VEC ? pc * 8 : sc), mj);
 
     if (u.slot < 0) {  // padding: zeros
-        if constexpr (!FIRST) {
-            TT *o = static_cast<TT *>(p.out) + u.t0 * p.o_ts + (long long)ph * p.o_hs + pj;
-            if (pon) {
-                if constexpr (VEC) {
-                    for (int t = pt; t < u.len; t += TPP)
+        if (READ && mon) {
+            TT *o = static_cast<TT *>(p.out) + u.t0 * p.o_ts + (long long)mh * p.o_hs + mj;
+            if constexpr (VEC) {
+                for (int t = pt; t < u.len; t += TPP)
 #pragma unroll
-                        for (int i = 0; i < 8 * (int)sizeof(TT) / 16; ++i)
-                            reinterpret_cast<uint4 *>(o + (long long)t * p.o_ts)[i] = make_uint4(0, 0, 0, 0);
-                } else {
-                    for (int t = stt; t < u.len; t += TPS) o[(long long)t * p.o_ts] = TT(0);
-                }
+                    for (int i = 0; i < 8 * (int)sizeof(TT) / 16; ++i)
+                        reinterpret_cast<uint4 *>(o + (long long)t * p.o_ts)[i] = make_uint4(0, 0, 0, 0);
+            } else {
+                for (int t = ps; t < u.len; t += TPS) o[(long long)t * p.o_ts] = TT(0);
             }
         }
         return;
     }
 
-    // this lane's states and their rates, in pairs along K
+    // ---- chunks on their way to shared memory
+    const TT *const xp = static_cast<const TT *>(p.x) + u.t0 * p.x_ts + (long long)mh * p.x_hs + mj;
+    const TT *const zp = READ && p.z ? static_cast<const TT *>(p.z) + u.t0 * p.z_ts + (long long)mh * p.z_hs + mj : nullptr;
+    const DT *const dp = static_cast<const DT *>(p.dt) + u.t0 * p.dt_ts + (long long)mh * p.dt_hs + mj * p.dt_es;
+    const TT *const bp = static_cast<const TT *>(p.B) + u.t0 * p.B_ts + (long long)g * p.B_hs;
+    const TT *const cp = READ ? static_cast<const TT *>(p.C) + u.t0 * p.C_ts + (long long)g * p.C_hs : nullptr;
+
+    auto rows = [&](auto *to, const auto *from, long long stride, int n, bool vec) {
+        using T = std::remove_const_t<std::remove_pointer_t<decltype(from)>>;
+        if (!mon) return;
+        if constexpr (VEC) {
+            if (vec) {
+#pragma unroll
+                for (int i = 0; i < (N + TPP - 1) / TPP; ++i) {
+                    const int t = pt + i * TPP;
+                    if (t < n)
+#pragma unroll
+                        for (int v = 0; v < 8; v += 16 / (int)sizeof(T))
+                            cp_async16(to + t * W + pc * 8 + v, from + (long long)t * stride + v);
+                }
+            } else {  // one value for the head
+                for (int t = pt; t < n; t += TPP) {
+                    const T v = from[(long long)t * stride];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) to[t * W + pc * 8 + i] = v;
+                }
+            }
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll 4
+            for (int t = ps; t < n; t += TPS) cp_async4(to + t * W + sc, from + (long long)t * stride);
+        } else {
+            T v[N / TPS];
+#pragma unroll
+            for (int i = 0; i < N / TPS; ++i)
+                if (ps + i * TPS < n) v[i] = from[(long long)(ps + i * TPS) * stride];
+#pragma unroll
+            for (int i = 0; i < N / TPS; ++i)
+                if (ps + i * TPS < n) to[(ps + i * TPS) * W + sc] = v[i];
+        }
+    };
+    const bool bc_vec = p.bc_vec && p.K == KP;
+    auto states = [&](TT *to, const TT *from, long long stride, int n) {
+        if (bc_vec) {
+            constexpr int C = 16 / (int)sizeof(TT), VR = KP / C;
+#pragma unroll
+            for (int i = 0; i < (N * VR + 31) / 32; ++i) {
+                const int t = (lane + 32 * i) / VR, v = (lane + 32 * i) % VR;
+                if (t < n) cp_async16(to + t * KP + v * C, from + (long long)t * stride + v * C);
+            }
+        } else {
+            for (int k = lane; k < p.K; k += 32) {
+                if constexpr (sizeof(TT) == 4) {
+#pragma unroll 4
+                    for (int t = 0; t < n; ++t) cp_async4(to + t * KP + k, from + (long long)t * stride + k);
+                } else {
+                    TT v[N];
+#pragma unroll
+                    for (int t = 0; t < N; ++t)
+                        if (t < n) v[t] = from[(long long)t * stride + k];
+#pragma unroll
+                    for (int t = 0; t < N; ++t)
+                        if (t < n) to[t * KP + k] = v[t];
+                }
+            }
+        }
+    };
+    auto fetch = [&](int base, int stage) {
+        const int n = min(N, u.len - base);
+        if (n > 0) {
+            unsigned char *const to = sh + stage * Sh::stage;
+            rows(reinterpret_cast<DT *>(to + Sh::dt), dp + (long long)base * p.dt_ts, p.dt_ts, n, p.dt_es != 0);
+            rows(reinterpret_cast<TT *>(to + Sh::x), xp + (long long)base * p.x_ts, p.x_ts, n, true);
+            states(reinterpret_cast<TT *>(to + Sh::B), bp + (long long)base * p.B_ts, p.B_ts, n);
+            if (READ) {
+                states(reinterpret_cast<TT *>(to + Sh::C), cp + (long long)base * p.C_ts, p.C_ts, n);
+                if (zp) rows(reinterpret_cast<TT *>(to + Sh::z), zp + (long long)base * p.z_ts, p.z_ts, n, true);
+            }
+        }
+        cp_async_commit();
+    };
+    for (int i = lane; i < 2 * Sh::stage / 16; i += 32) reinterpret_cast<uint4 *>(sh)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = lane; i < W; i += 32) {
+        int j = 0, h = 0;
+        const bool in = i < width;
+        if (in) h = head(c0 + i, j);
+        fbias[i] = in && p.bias ? p.bias[h * p.b_hs + j * p.b_vs] : 0.0f;
+        fD[i] = in && p.D ? p.D[h * p.d_hs + j * p.d_vs] : 0.0f;
+    }
+    __syncwarp();
+    fetch(0, 0);
+
+    // ---- this lane's states and their rates, in pairs along K
     const int lk = lane % LK, cg = lane / LK;
     float2 S[CH][KT / 2], A[CH][KT / 2];
     long long st_at[CH];
@@ -185,61 +219,53 @@ __global__ void __launch_bounds__(32 * kScanWarps) k_scan(const __grid_constant_
 #pragma unroll
     for (int e = 0; e < CH; ++e) {
         on[e] = cg * 4 + e < width;
+        chan[e] = 0;
         chead[e] = on[e] ? head(c0 + cg * 4 + e, chan[e]) : 0;
-        if (!on[e]) chan[e] = 0;
         st_at[e] = (long long)u.slot * p.st_slot + (long long)chead[e] * p.st_head + chan[e];
     }
-    // a state row's four channels, from the pool or from float32 segments' states
-    auto get = [&](int k, float (&v)[CH]) {
-#pragma unroll
-        for (int e = 0; e < CH; ++e) v[e] = 0.0f;
-        if (k >= p.K) return;
-        if (p.seg) {
-            const float *w = p.ws + (u.piece * p.nv + chead[0]) * (long long)p.K * p.V + (long long)k * p.V;
-#pragma unroll
-            for (int e = 0; e < CH; ++e)
-                if (on[e]) v[e] = w[(long long)(chead[e] - chead[0]) * p.K * p.V + chan[e]];
-        } else if (VEC) {
-            if (!on[0]) return;
-            if (p.st_bf16) {
-                Pack<uint16_t, 4> q;
-                q.load(static_cast<const uint16_t *>(p.state) + st_at[0] + k * p.st_k);
-#pragma unroll
-                for (int e = 0; e < CH; ++e) v[e] = q.get(e);
-            } else {
-                Pack<float, 4> q;
-                q.load(static_cast<const float *>(p.state) + st_at[0] + k * p.st_k);
-#pragma unroll
-                for (int e = 0; e < CH; ++e) v[e] = q.get(e);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < CH; ++e)
-                if (on[e])
-                    v[e] = p.st_bf16 ? to_f32(static_cast<const uint16_t *>(p.state)[st_at[e] + k * p.st_k])
-                                     : static_cast<const float *>(p.state)[st_at[e] + k * p.st_k];
-        }
+    // a segment's state in the workspace: [nv, K, V]
+    auto segment = [&](int e, int k) {
+        return p.ws + ((u.piece * p.nv + chead[e]) * p.K + k) * (long long)p.V + chan[e];
     };
 #pragma unroll
     for (int i = 0; i < KT; ++i) {
         const int k = lk * KT + i;
         float v[CH], a[CH];
-        if constexpr (FIRST) {
 #pragma unroll
-            for (int e = 0; e < CH; ++e) v[e] = 0.0f;
-        } else {
-            get(k, v);
-        }
-#pragma unroll
-        for (int e = 0; e < CH; ++e) a[e] = 0.0f;
+        for (int e = 0; e < CH; ++e) v[e] = a[e] = 0.0f;
         if (k < p.K) {
+            if (first) {
+            } else if (p.seg) {
+#pragma unroll
+                for (int e = 0; e < CH; ++e)
+                    if (on[e]) v[e] = *segment(e, k);
+            } else if constexpr (VEC) {
+                if (on[0]) {
+                    if (p.st_bf16) {
+                        Pack<uint16_t, 4> q;
+                        q.load(static_cast<const uint16_t *>(p.state) + st_at[0] + k * p.st_k);
+#pragma unroll
+                        for (int e = 0; e < CH; ++e) v[e] = q.get(e);
+                    } else {
+                        Pack<float, 4> q;
+                        q.load(static_cast<const float *>(p.state) + st_at[0] + k * p.st_k);
+#pragma unroll
+                        for (int e = 0; e < CH; ++e) v[e] = q.get(e);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < CH; ++e)
+                    if (on[e])
+                        v[e] = p.st_bf16 ? to_f32(static_cast<const uint16_t *>(p.state)[st_at[e] + k * p.st_k])
+                                         : static_cast<const float *>(p.state)[st_at[e] + k * p.st_k];
+            }
             if (VEC && p.a_vec) {
                 if (on[0]) {
-                    const float4 q = *reinterpret_cast<const float4 *>(p.A + chead[0] * p.a_hs + k * p.a_ks + chan[0]);
-                    a[0] = q.x;
-                    a[1] = q.y;
-                    a[2] = q.z;
-                    a[3] = q.w;
+                    Pack<float, 4> q;
+                    q.load(p.A + chead[0] * p.a_hs + k * p.a_ks + chan[0]);
+#pragma unroll
+                    for (int e = 0; e < CH; ++e) a[e] = q.get(e);
                 }
             } else {
 #pragma unroll
@@ -250,10 +276,10 @@ __global__ void __launch_bounds__(32 * kScanWarps) k_scan(const __grid_constant_
 #pragma unroll
         for (int e = 0; e < CH; ++e) {
             (i & 1 ? S[e][i / 2].y : S[e][i / 2].x) = v[e];
-            (i & 1 ? A[e][i / 2].y : A[e][i / 2].x) = a[e] * kLog2e;
+            (i & 1 ? A[e][i / 2].y : A[e][i / 2].x) = rate<TT>(a[e]);
         }
     }
-    // the pool's new value
+    // the states into their slot, or a segment's into the workspace
     auto put = [&]() {
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
@@ -262,11 +288,10 @@ __global__ void __launch_bounds__(32 * kScanWarps) k_scan(const __grid_constant_
             float v[CH];
 #pragma unroll
             for (int e = 0; e < CH; ++e) v[e] = i & 1 ? S[e][i / 2].y : S[e][i / 2].x;
-            if constexpr (FIRST) {
-                float *w = p.ws + (u.piece * p.nv + chead[0]) * (long long)p.K * p.V + (long long)k * p.V;
+            if (first) {
 #pragma unroll
                 for (int e = 0; e < CH; ++e)
-                    if (on[e]) w[(long long)(chead[e] - chead[0]) * p.K * p.V + chan[e]] = v[e];
+                    if (on[e]) *segment(e, k) = v[e];
             } else if constexpr (VEC) {
                 if (!on[0]) continue;
                 if (p.st_bf16) {
@@ -291,191 +316,168 @@ __global__ void __launch_bounds__(32 * kScanWarps) k_scan(const __grid_constant_
         }
     };
 
-    for (int i = lane; i < W; i += 32) {
-        int j = 0, h = 0;
-        const bool in = i < width;
-        if (in) h = head(c0 + i, j);
-        sh[Sh::bias + i] = in && p.bias ? p.bias[h * p.b_hs + j * p.b_vs] : 0.0f;
-        sh[Sh::D + i] = in && p.D ? p.D[h * p.d_hs + j * p.d_vs] : 0.0f;
-    }
-    for (int i = lane; i < kScanChunk * KP; i += 32) {  // states past K, and what no token writes
-        sh[Sh::B + i] = 0.0f;
-        sh[Sh::C + i] = 0.0f;
-    }
-    for (int i = lane; i < kScanChunk * W; i += 32) {
-        sh[Sh::d + i] = 0.0f;
-        sh[Sh::x + i] = 0.0f;
-    }
-    __syncwarp();
-
-    const TT *const xp = static_cast<const TT *>(p.x) + u.t0 * p.x_ts + (long long)ph * p.x_hs + pj;
-    const DT *const dp = static_cast<const DT *>(p.dt) + u.t0 * p.dt_ts + (long long)ph * p.dt_hs + pj * p.dt_es;
-    const TT *const bp = static_cast<const TT *>(p.B) + u.t0 * p.B_ts + (long long)g * p.B_hs;
-    const TT *const cp = static_cast<const TT *>(p.C) + u.t0 * p.C_ts + (long long)g * p.C_hs;
-    const bool outputs = !FIRST && p.out;
-    float2 dsum[CH / 2];
+    float dsum[CH] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int base = 0, stage = 0; base < u.len; base += N, stage ^= 1) {
+        const int n = min(N, u.len - base);
+        fetch(base + N, stage ^ 1);
+        cp_async_wait<1>();
+        __syncwarp();
+        unsigned char *const raw = sh + stage * Sh::stage;
+        TT *const rx = reinterpret_cast<TT *>(raw + Sh::x);
+        const TT *const rz = reinterpret_cast<const TT *>(raw + Sh::z);
+        const DT *const rd = reinterpret_cast<const DT *>(raw + Sh::dt);
+        // ---- d and d x, B and C in float32
 #pragma unroll
-    for (int e = 0; e < CH / 2; ++e) dsum[e] = make_float2(0.0f, 0.0f);
-
-    for (int base = 0; base < u.len; base += kScanChunk) {
-        const int n = min(kScanChunk, u.len - base);
-        // ---- stage a chunk
-        if constexpr (VEC) {
-            for (int t = pt; t < n; t += TPP) {
-                if (!pon) continue;
-                float d[8], x[8];
-                if (p.dt_es) {
+        for (int i = 0; i < (N * PCS + 31) / 32; ++i) {
+            const int t = pt + i * TPP, at = t * W + pc * 8;
+            if (N * PCS % 32 && t >= N) continue;
 #pragma unroll
-                    for (int i = 0; i < 8; i += 16 / (int)sizeof(DT)) {
-                        Pack<DT, 16 / (int)sizeof(DT)> q;
-                        q.load(dp + (long long)(base + t) * p.dt_ts + i);
+            for (int v = 0; v < 8; v += 4) {
+                Pack<DT, 4> dq;
+                Pack<TT, 4> xq;
+                dq.load(rd + at + v);
+                xq.load(rx + at + v);
+                const float4 b = *reinterpret_cast<const float4 *>(fbias + pc * 8 + v);
+                float d[4] = {dq.get(0) + b.x, dq.get(1) + b.y, dq.get(2) + b.z, dq.get(3) + b.w}, x[4];
 #pragma unroll
-                        for (int j = 0; j < 16 / (int)sizeof(DT); ++j) d[i + j] = q.get(j);
-                    }
-                } else {
-                    const float v = to_f32(dp[(long long)(base + t) * p.dt_ts]);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) d[i] = v;
+                for (int j = 0; j < 4; ++j) {
+                    if (p.softplus) d[j] = softplus<TT>(d[j]);
+                    x[j] = d[j] * xq.get(j);
                 }
-#pragma unroll
-                for (int i = 0; i < 8; i += 16 / (int)sizeof(TT)) {
-                    Pack<TT, 16 / (int)sizeof(TT)> q;
-                    q.load(xp + (long long)(base + t) * p.x_ts + i);
-#pragma unroll
-                    for (int j = 0; j < 16 / (int)sizeof(TT); ++j) x[i + j] = q.get(j);
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    d[i] += sh[Sh::bias + pc * 8 + i];
-                    if (p.softplus) d[i] = softplus(d[i]);
-                    x[i] *= d[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                    *reinterpret_cast<float4 *>(sh + Sh::d + t * W + pc * 8 + i) = make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
-                    *reinterpret_cast<float4 *>(sh + Sh::x + t * W + pc * 8 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-                }
-            }
-        } else if (pon) {
-            for (int t = stt; t < n; t += TPS) {
-                float d = to_f32(dp[(long long)(base + t) * p.dt_ts]) + sh[Sh::bias + sc];
-                if (p.softplus) d = softplus(d);
-                sh[Sh::d + t * W + sc] = d;
-                sh[Sh::x + t * W + sc] = d * to_f32(xp[(long long)(base + t) * p.x_ts]);
+                *reinterpret_cast<float4 *>(fd + at + v) = make_float4(d[0], d[1], d[2], d[3]);
+                *reinterpret_cast<float4 *>(fx + at + v) = make_float4(x[0], x[1], x[2], x[3]);
             }
         }
-        for (int i = lane; i < n * p.K; i += 32) {
-            const int t = i / p.K, k = i - t * p.K;
-            sh[Sh::B + t * KP + k] = to_f32(bp[(long long)(base + t) * p.B_ts + k]);
-            if (outputs) sh[Sh::C + t * KP + k] = to_f32(cp[(long long)(base + t) * p.C_ts + k]);
+        const float *fB = reinterpret_cast<const float *>(raw + Sh::B), *fC = reinterpret_cast<const float *>(raw + Sh::C);
+        if constexpr (!Sh::wide) {
+            float *const tB = reinterpret_cast<float *>(sh + Sh::fB), *const tC = reinterpret_cast<float *>(sh + Sh::fC);
+#pragma unroll
+            for (int i = 0; i < (N * KP / 4 + 31) / 32; ++i) {
+                const int at = 4 * (lane + 32 * i);
+                Pack<TT, 4> q;
+                q.load(reinterpret_cast<const TT *>(raw + Sh::B) + at);
+                *reinterpret_cast<float4 *>(tB + at) = make_float4(q.get(0), q.get(1), q.get(2), q.get(3));
+                if (READ) {
+                    q.load(reinterpret_cast<const TT *>(raw + Sh::C) + at);
+                    *reinterpret_cast<float4 *>(tC + at) = make_float4(q.get(0), q.get(1), q.get(2), q.get(3));
+                }
+            }
+            fB = tB;
+            fC = tC;
         }
         __syncwarp();
-        // ---- its tokens, in two parts where the slot's state lies between them
+        // ---- the tokens, in two parts where the slot's state lies between them
+        struct Operands {
+            float4 d, x;
+            float2 B[KT / 2], C[KT / 2];
+        };
+        auto operands = [&](int t, Operands &o) {
+            o.d = *reinterpret_cast<const float4 *>(fd + t * W + cg * 4);
+            o.x = *reinterpret_cast<const float4 *>(fx + t * W + cg * 4);
+#pragma unroll
+            for (int i = 0; i < KT / 2; i += 2) {
+                const float4 b = *reinterpret_cast<const float4 *>(fB + t * KP + lk * KT + 2 * i);
+                o.B[i] = make_float2(b.x, b.y);
+                o.B[i + 1] = make_float2(b.z, b.w);
+                if (READ) {
+                    const float4 c = *reinterpret_cast<const float4 *>(fC + t * KP + lk * KT + 2 * i);
+                    o.C[i] = make_float2(c.x, c.y);
+                    o.C[i + 1] = make_float2(c.z, c.w);
+                }
+            }
+        };
         const int cut = u.kept - base;
-        const bool inside = !FIRST && cut > 0 && cut <= n;
+        const bool inside = !first && cut > 0 && cut <= n;
+        Operands now;
+        operands(0, now);
         int t = 0;
+#pragma unroll 1
         for (int part = 0; part < 2; ++part) {
             const int end = part == 0 && inside ? cut : n;
+#pragma unroll 2
             for (; t < end; ++t) {
-                const float4 d4 = *reinterpret_cast<const float4 *>(sh + Sh::d + t * W + cg * 4);
-                const float4 x4 = *reinterpret_cast<const float4 *>(sh + Sh::x + t * W + cg * 4);
-                const float d[CH] = {d4.x, d4.y, d4.z, d4.w}, x[CH] = {x4.x, x4.y, x4.z, x4.w};
-                float2 Bv[KT / 2], Cv[KT / 2];
-#pragma unroll
-                for (int i = 0; i < KT / 2; ++i) {
-                    Bv[i] = *reinterpret_cast<const float2 *>(sh + Sh::B + t * KP + lk * KT + 2 * i);
-                    Cv[i] = *reinterpret_cast<const float2 *>(sh + Sh::C + t * KP + lk * KT + 2 * i);
-                }
+                Operands next;
+                operands(t + 1 < N ? t + 1 : t, next);
+                const float d[CH] = {now.d.x, now.d.y, now.d.z, now.d.w}, x[CH] = {now.x.x, now.x.y, now.x.z, now.x.w};
                 float y[CH];
 #pragma unroll
                 for (int e = 0; e < CH; ++e) {
-                    float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
                     for (int i = 0; i < KT / 2; ++i) {
-                        float2 a = __fmul2_rn(make_float2(d[e], d[e]), A[e][i]);
-                        a.x = ex2(a.x);
-                        a.y = ex2(a.y);
-                        S[e][i] = __ffma2_rn(a, S[e][i], __fmul2_rn(make_float2(x[e], x[e]), Bv[i]));
-                        if (!FIRST) acc = __ffma2_rn(Cv[i], S[e][i], acc);
+                        const float2 a = __fmul2_rn(make_float2(d[e], d[e]), A[e][i]);
+                        const float2 in = __fmul2_rn(make_float2(x[e], x[e]), now.B[i]);
+                        S[e][i].x = fmaf(decay<TT>(a.x), S[e][i].x, in.x);
+                        S[e][i].y = fmaf(decay<TT>(a.y), S[e][i].y, in.y);
+                        if (READ) {
+                            y[e] = i == 0 ? now.C[i].x * S[e][i].x : fmaf(now.C[i].x, S[e][i].x, y[e]);
+                            y[e] = fmaf(now.C[i].y, S[e][i].y, y[e]);
+                        }
                     }
-                    y[e] = acc.x + acc.y;
+                    if (!READ) dsum[e] += d[e];
                 }
-                if constexpr (FIRST) {
-                    dsum[0] = __fadd2_rn(dsum[0], make_float2(d[0], d[1]));
-                    dsum[1] = __fadd2_rn(dsum[1], make_float2(d[2], d[3]));
-                } else if (outputs) {
-                    // over lk: two exchanges leave lane lk channel 4 cg + lk % 4, the rest add up
-                    const bool up = lk & 2;
-                    float a = up ? y[2] : y[0], b = up ? y[3] : y[1];
-                    a += __shfl_xor_sync(kFull, up ? y[0] : y[2], 2);
-                    b += __shfl_xor_sync(kFull, up ? y[1] : y[3], 2);
-                    const bool odd = lk & 1;
-                    float v = odd ? b : a;
-                    v += __shfl_xor_sync(kFull, odd ? a : b, 1);
-#pragma unroll
-                    for (int m = 4; m < LK; m <<= 1) v += __shfl_xor_sync(kFull, v, m);
-                    if (LK == 4 || lk < 4) sh[Sh::y + t * W + cg * 4 + (lk & 3)] = v;
+                if (READ) {
+                    const float v = scan_readout<LK>(y, lk);
+                    if (LK == 4 || lk < 4) fy[t * W + cg * 4 + (lk & 3)] = v;
                 }
+                now = next;
             }
             if (part == 0 && inside) put();
         }
         __syncwarp();
-        // ---- finish and store its outputs
-        if (outputs && pon) {
-            const TT *const zp = static_cast<const TT *>(p.z) + (p.z ? u.t0 * p.z_ts + (long long)ph * p.z_hs + pj : 0);
-            TT *const op = static_cast<TT *>(p.out) + u.t0 * p.o_ts + (long long)ph * p.o_hs + pj;
-            if constexpr (VEC) {
+        // ---- its outputs
+        if constexpr (READ) {
+#pragma unroll
+            for (int i = 0; i < (N * PCS + 31) / 32; ++i) {
+                const int t = pt + i * TPP, at = t * W + pc * 8;
+                if (t >= n) continue;
                 constexpr int C = 16 / (int)sizeof(TT);
-                for (int tt = pt; tt < n; tt += TPP) {
 #pragma unroll
-                    for (int i = 0; i < 8; i += C) {
-                        Pack<TT, C> x, z, o;
-                        x.load(xp + (long long)(base + tt) * p.x_ts + i);
-                        if (p.z) z.load(zp + (long long)(base + tt) * p.z_ts + i);
+                for (int v = 0; v < 8; v += C) {
+                    Pack<TT, C> x, z, o;
+                    x.load(rx + at + v);
+                    if (zp) z.load(rz + at + v);
 #pragma unroll
-                        for (int j = 0; j < C; ++j) {
-                            float y = fmaf(sh[Sh::D + pc * 8 + i + j], x.get(j), sh[Sh::y + tt * W + pc * 8 + i + j]);
-                            if (p.z) {
-                                const float zv = z.get(j);
-                                y *= __fdividef(zv, 1.0f + __expf(-zv));
-                            }
-                            o.set(j, y);
-                        }
-                        o.store(op + (long long)(base + tt) * p.o_ts + i);
+                    for (int j = 0; j < C; ++j) {
+                        float y = fmaf(fD[pc * 8 + v + j], x.get(j), fy[at + v + j]);
+                        if (zp) y *= silu(z.get(j));
+                        o.set(j, y);
+                    }
+                    if constexpr (VEC) {
+                        if (mon) o.store(static_cast<TT *>(p.out) + (u.t0 + base + t) * p.o_ts + (long long)mh * p.o_hs + mj + v);
+                    } else {
+                        o.store(rx + at + v);
                     }
                 }
-            } else {
-                for (int tt = stt; tt < n; tt += TPS) {
-                    float y = fmaf(sh[Sh::D + sc], to_f32(xp[(long long)(base + tt) * p.x_ts]), sh[Sh::y + tt * W + sc]);
-                    if (p.z) {
-                        const float zv = to_f32(zp[(long long)(base + tt) * p.z_ts]);
-                        y *= __fdividef(zv, 1.0f + __expf(-zv));
-                    }
-                    op[(long long)(base + tt) * p.o_ts] = from_f32<TT>(y);
+            }
+            if constexpr (!VEC) {
+                __syncwarp();
+                if (mon) {
+                    TT *const to = static_cast<TT *>(p.out) + (u.t0 + base) * p.o_ts + (long long)mh * p.o_hs + mj;
+#pragma unroll 4
+                    for (int t = ps; t < n; t += TPS) to[(long long)t * p.o_ts] = rx[t * W + sc];
                 }
             }
         }
         __syncwarp();
     }
-    if constexpr (FIRST) {
+    if (first) {
         put();
         if (lk == 0) {
             float *sum = p.ws + scan_pieces(p.T, p.seg, p.batch) * p.nv * p.K * p.V + u.piece * p.nv * p.V;
-            const float d[CH] = {dsum[0].x, dsum[0].y, dsum[1].x, dsum[1].y};
 #pragma unroll
             for (int e = 0; e < CH; ++e)
-                if (on[e]) sum[(long long)chead[e] * p.V + chan[e]] = d[e];
+                if (on[e]) sum[(long long)chead[e] * p.V + chan[e]] = dsum[e];
         }
     }
 }
 
 template <typename TT, typename DT, int KT, int LK, bool VEC> cudaError_t scan_go(const ScanParams &p, cudaStream_t s) {
-    using Sh = ScanShared<KT, LK>;
-    constexpr int bytes = 4 * kScanWarps * Sh::size;
+    using Sh = ScanShared<TT, DT, KT, LK>;
+    constexpr int bytes = kScanWarps * Sh::bytes;
+    static_assert(bytes <= 227 << 10, "a block's shared memory");
     static LaunchCache cache;
     LaunchInfo info;
     cudaError_t e = launch_info(cache, &info, [](LaunchInfo &) {
-        if (bytes <= 48 << 10) return cudaSuccess;
         const cudaError_t f = cudaFuncSetAttribute(k_scan<TT, DT, KT, LK, VEC, false>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (f != cudaSuccess) return f;
@@ -487,17 +489,17 @@ template <typename TT, typename DT, int KT, int LK, bool VEC> cudaError_t scan_g
     if (units >= 1ll << 31) return cudaErrorInvalidConfiguration;
     const unsigned blocks = (unsigned)((units + kScanWarps - 1) / kScanWarps);
     if (p.seg) {
-        k_scan<TT, DT, KT, LK, VEC, true><<<blocks, 32 * kScanWarps, bytes, s>>>(p, (int)tiles, (unsigned)units);
+        k_scan<TT, DT, KT, LK, VEC, false><<<blocks, 32 * kScanWarps, bytes, s>>>(p, (int)tiles, (unsigned)units, 1);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         if ((e = launch_scan_join(p, s)) != cudaSuccess) return e;
     }
-    k_scan<TT, DT, KT, LK, VEC, false><<<blocks, 32 * kScanWarps, bytes, s>>>(p, (int)tiles, (unsigned)units);
+    if (p.out) k_scan<TT, DT, KT, LK, VEC, true><<<blocks, 32 * kScanWarps, bytes, s>>>(p, (int)tiles, (unsigned)units, 0);
+    else k_scan<TT, DT, KT, LK, VEC, false><<<blocks, 32 * kScanWarps, bytes, s>>>(p, (int)tiles, (unsigned)units, 0);
     return cudaGetLastError();
 }
 
 // States a lane and lanes a channel, by K.
 template <typename TT, typename DT, bool VEC> cudaError_t scan_states(const ScanParams &p, cudaStream_t s) {
-    if (p.K <= 8) return scan_go<TT, DT, 2, 4, VEC>(p, s);
     if (p.K <= 16) return scan_go<TT, DT, 4, 4, VEC>(p, s);
     if (p.K <= 32) return scan_go<TT, DT, 8, 4, VEC>(p, s);
     if (p.K <= 64) return scan_go<TT, DT, 8, 8, VEC>(p, s);

@@ -137,7 +137,9 @@ struct ScanParams {
 __host__ __device__
 #endif
 inline long long scan_pieces(long long T, int seg, int batch) { return T / seg + batch; }
-// vec: groups of 8 channels may be moved as vectors everywhere.
+// Single tokens (max_len is 1), and everything else.  vec: groups of 8 channels may be
+// moved as vectors everywhere.
+cudaError_t launch_scan_step(const ScanParams &p, bool tok_bf16, bool dt_bf16, bool vec, cudaStream_t s);
 cudaError_t launch_scan(const ScanParams &p, bool tok_bf16, bool dt_bf16, bool vec, cudaStream_t s);
 cudaError_t launch_scan_bb(const ScanParams &p, bool vec, cudaStream_t s);  // bfloat16 tokens and step sizes
 cudaError_t launch_scan_bf(const ScanParams &p, bool vec, cudaStream_t s);  // bfloat16 tokens, float32 step sizes

@@ -1,0 +1,105 @@
+// What the selective scan's kernels share: a state's decay, softplus and SiLU, and a row's facts.
+#pragma once
+
+#include "../gdr_device.cuh"
+#include "layer_internal.h"
+
+#include <type_traits>
+
+namespace gdr {
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// A state's decay from d and its rate.  ex2.approx errs to one side by a fraction
+// of an ulp, which a slow state adds up over its memory (1000 tokens: 3e-5); that
+// is nothing beside bfloat16 tokens, and float32 tokens take expf, which does not.
+template <typename TT> __device__ __forceinline__ float rate(float a) { return sizeof(TT) == 2 ? a * kLog2e : a; }
+template <typename TT> __device__ __forceinline__ float decay(float e) { return sizeof(TT) == 2 ? ex2(e) : expf(e); }
+
+// log(1 + e^v) without cancellation: max(v, 0) + log1p(e^-|v|).  bfloat16 tokens: log1p(e) / e by its Chebyshev
+// interpolation of degree 8 over [0, 1], off by 2^-22 at most.
+template <typename TT> __device__ __forceinline__ float softplus(float v) {
+    if (sizeof(TT) == 4) return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v)));
+    const float e = ex2(-kLog2e * fabsf(v));
+    float q = 5.126102143e-03f;
+    q = fmaf(q, e, -2.907406469e-02f);
+    q = fmaf(q, e, 7.751608676e-02f);
+    q = fmaf(q, e, -1.360224762e-01f);
+    q = fmaf(q, e, 1.907688074e-01f);
+    q = fmaf(q, e, -2.483539899e-01f);
+    q = fmaf(q, e, 3.331812171e-01f);
+    q = fmaf(q, e, -4.999944498e-01f);
+    q = fmaf(q, e, 9.999999659e-01f);
+    return fmaf(q, e, fmaxf(v, 0.0f));
+}
+
+__device__ __forceinline__ float silu(float z) { return z * rcp(1.0f + ex2(-kLog2e * z)); }
+
+struct ScanUnit {
+    int b;
+    long long t0;     // the unit's first token
+    int len;          // its tokens
+    int slot;         // -1: output cleared, nothing else
+    int kept;         // tokens of the unit after which the slot is written, 0: it is not
+    long long piece;  // segment index over all rows (segmented calls)
+    bool last;        // the row's last segment
+};
+
+// The row's facts; flags its problems where `leader`.  False: nothing to do.
+__device__ __forceinline__ bool scan_row(const ScanParams &p, int b, bool leader, ScanUnit &u) {
+    const int lo = p.offsets[b], hi = p.offsets[b + 1];
+    u.b = b;
+    u.slot = p.slot_idx[b];
+    const int count = p.counts ? p.counts[b] : 0;
+    if (lo < 0 || hi < lo || hi > p.T) {
+        if (leader) flag(p.status, GDR_STATUS_BAD_OFFSETS);
+        return false;
+    }
+    u.t0 = lo;
+    u.len = hi - lo;
+    u.kept = 0;
+    u.piece = 0;
+    u.last = true;
+    if (u.len == 0) return false;
+    unsigned problem = 0;
+    if (p.max_len > 0 && u.len > p.max_len) problem = GDR_STATUS_ROW_TOO_LONG;
+    else if (u.slot < -1 || u.slot >= p.max_slots) problem = GDR_STATUS_BAD_SLOT;
+    if (problem) u.slot = -1;
+    if (u.slot >= 0 && p.keep) {
+        if (!p.counts) u.kept = u.len;
+        else if (count < 0 || count > u.len) problem = GDR_STATUS_BAD_COUNT;
+        else u.kept = count;
+    }
+    if (problem && leader) flag(p.status, problem);
+    if (!p.out) {  // only states move: tokens that are not kept are not read
+        u.len = u.slot >= 0 ? u.kept : 0;
+        if (u.len == 0) return false;
+    }
+    return true;
+}
+
+// The readout of four channels a lane, over the LK lanes that share them: two exchanges
+// leave lane lk channel lk % 4, the rest add up.
+template <int LK> __device__ __forceinline__ float scan_readout(const float (&y)[4], int lk) {
+    const bool up = lk & 2, odd = lk & 1;
+    float a = up ? y[2] : y[0], b = up ? y[3] : y[1];
+    a += __shfl_xor_sync(kFull, up ? y[0] : y[2], 2);
+    b += __shfl_xor_sync(kFull, up ? y[1] : y[3], 2);
+    float v = odd ? b : a;
+    v += __shfl_xor_sync(kFull, odd ? a : b, 1);
+#pragma unroll
+    for (int m = 4; m < LK; m <<= 1) v += __shfl_xor_sync(kFull, v, m);
+    return v;
+}
+
+}  // namespace gdr
