@@ -282,7 +282,7 @@ int gdr_selective_scan(const gdr_scan_args *a, void *stream) {
     p.counts = a->counts;
     const bool tb = a->token_dtype == GDR_BF16;
     const bool vec = a->V % 8 == 0 && vector_rows(a->x, a->token_dtype, 16, p.x_ts, p.x_hs) &&
-                     (p.dt_es == 0 || vector_rows(a->dt, a->dt_dtype, 16, p.dt_ts, p.dt_hs)) &&
+                     p.dt_es == 1 && vector_rows(a->dt, a->dt_dtype, 16, p.dt_ts, p.dt_hs) &&
                      (!a->out || vector_rows(a->out, a->token_dtype, 16, p.o_ts, p.o_hs)) &&
                      (!a->z || vector_rows(a->z, a->token_dtype, 16, p.z_ts, p.z_hs)) &&
                      vector_rows(a->state, a->state_dtype, 4 * esize(a->state_dtype), p.st_slot, p.st_head, p.st_k);

@@ -2,29 +2,32 @@
 //
 //     d = softplus(dt + bias);  S_i <- exp(d A_i) S_i + (d x) B_i;  y = sum_i C_i S_i + D x
 //
-// in float32.  Each state has a decay of its own that follows the token, so there
-// is no matrix product in it: 16 states cost a channel's token 16
-// exponentials and 64 float32 operations (half as many instructions in pairs).
+// in float32.  Each state has a decay of its own that follows the token, so there is no
+// matrix product in it: a state's step is an exponential and four float32 operations.
 //
-// A warp is a unit by itself: 4 * (32 / LK) channels of one row (or of one segment
-// of it).  Lane (cg, lk) keeps states lk KT .. lk KT + KT - 1 of channels 4 cg .. 4 cg + 3 in
-// registers for all of the unit's tokens, and their A.  Four channels by KT states
-// a lane are what keeps shared memory out of the way: a token's d and d x are read
-// for KT states each, its B and C for four channels each.
-//
-// Tokens go through in chunks of kChunk.  Lanes load a chunk as vectors along the
-// channels, work out d and d x once a channel, and leave them with B and C in the
-// warp's own piece of shared memory; the readout of a token is added up over lk by
-// shuffles that leave every lane one channel, and goes back through shared
-// memory, to be finished (D x, the gate) and stored as vectors.
+// A block has 64 channels of one row (or of one segment of it), and all of its tokens
+// follow one another, so what counts beside the work itself is how long a token takes.
+// Warps share it by kind.  NW warps run the recurrence, KT states each of all 64
+// channels, two channels a lane: a token is two vectors of d and d x a lane, KT values of B and
+// C that every lane reads alike, and nothing else.  Four helper warps do the rest, a
+// chunk of 8 tokens ahead and behind: they copy raw chunks into a ring, make d and d x of
+// them once a channel, add up the NW partial readouts, apply D and the gate and store.
+// One barrier a chunk hands both sides' buffers over.
 #pragma once
 
 #include "scan_device.cuh"
 
 namespace gdr {
 
-constexpr int kScanChunk = 16;
-constexpr int kScanWarps = 4;  // a block's
+constexpr int kScanChunk = 8;     // tokens
+constexpr int kScanTile = 64;     // a block's channels
+constexpr int kScanHelpers = 128; // threads beside the recurrence's own
+
+// An asynchronous copy of 4, 8 or 16 bytes to shared memory.
+template <int BYTES> __device__ __forceinline__ void cp_async(void *to, const void *from) {
+    const unsigned at = (unsigned)__cvta_generic_to_shared(to);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
+}
 
 // Segment `piece` of all rows' segments, for calls of at most 32 rows: lane l counts row l's.
 __device__ __forceinline__ bool scan_piece(const ScanParams &p, long long piece, bool leader, int lane, ScanUnit &u) {
@@ -52,458 +55,449 @@ __device__ __forceinline__ bool scan_piece(const ScanParams &p, long long piece,
     return true;
 }
 
-// A warp's piece of shared memory, in bytes: two stages of raw chunks, then the chunk in float32.
-template <typename TT, typename DT, int KT, int LK> struct ScanShared {
-    static constexpr int W = 4 * (32 / LK), KP = KT * LK, N = kScanChunk;
-    static constexpr bool wide = sizeof(TT) == 4;  // raw B and C are used as they are
+// A block's shared memory, in bytes: a ring of raw chunks, then two chunks' operands in
+// float32 and the readout's partial sums.
+template <typename TT, typename DT, int KT, int NW> struct ScanShared {
+    static constexpr int W = kScanTile, KP = KT * NW, N = kScanChunk, ring = sizeof(TT) == 2 && KP <= 32 ? 8 : 4;
     static constexpr int x = 0, z = x + N * W * (int)sizeof(TT), dt = z + N * W * (int)sizeof(TT), B = dt + N * W * (int)sizeof(DT),
                          C = B + N * KP * (int)sizeof(TT), stage = C + N * KP * (int)sizeof(TT);
-    static constexpr int fd = 2 * stage, fx = fd + 4 * N * W, fy = fx + 4 * N * W, fB = fy + 4 * N * W,
-                         fC = fB + (wide ? 0 : 4 * N * KP), bias = fC + (wide ? 0 : 4 * N * KP), D = bias + 4 * W,
-                         bytes = D + 4 * W;
+    static constexpr int fd = ring * stage, fx = fd + 2 * 4 * N * W, fB = fx + 2 * 4 * N * W, fC = fB + 2 * 4 * N * KP,
+                         fy = fC + 2 * 4 * N * KP, bytes = fy + 2 * 4 * NW * N * W;
 };
 
 // READ: with outputs.  Without them states move only: into the slots, or (first != 0)
 // each segment's own state, from zero, and the sum of its step sizes into the workspace.
-template <typename TT, typename DT, int KT, int LK, bool VEC, bool READ>
-__global__ void __launch_bounds__(32 * kScanWarps) k_scan(const __grid_constant__ ScanParams p, int tiles, unsigned units, int first) {
-    using Sh = ScanShared<TT, DT, KT, LK>;
-    constexpr int W = Sh::W, KP = Sh::KP, CH = 4, N = kScanChunk;
+template <typename TT, typename DT, int KT, int NW, bool VEC, bool READ>
+__global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 4 : KT * NW <= 32 ? 3 : 1)
+    k_scan(const __grid_constant__ ScanParams p, int tiles, int first) {
+    using Sh = ScanShared<TT, DT, KT, NW>;
+    constexpr int W = Sh::W, KP = Sh::KP, N = Sh::N, R = Sh::ring;
     extern __shared__ __align__(16) unsigned char shared[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned unit = blockIdx.x * kScanWarps + warp;
-    if (unit >= units) return;
-    const unsigned all = (unsigned)(p.nk * tiles), row = unit / all, tg = unit - row * all;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned all = (unsigned)(p.nk * tiles), row = blockIdx.x / all, tg = blockIdx.x - row * all;
     const int g = (int)(tg / (unsigned)tiles), tile = (int)(tg - (unsigned)g * (unsigned)tiles);
     ScanUnit u;
     if (p.seg) {
-        if (!scan_piece(p, row, tg == 0 && !first, lane, u)) return;
+        if (!scan_piece(p, row, tg == 0 && warp == 0 && !first, lane, u)) return;
         if (first && u.last) return;  // no segment starts from its state
-    } else if (!scan_row(p, (int)row, tg == 0 && lane == 0, u)) {
+    } else if (!scan_row(p, (int)row, tg == 0 && tid == 0, u)) {
         return;
     }
-    const int group = p.r * p.V, c0 = tile * W;  // channels of the key head's value heads, this warp's first
-    const int width = min(W, group - c0);
-    unsigned char *const sh = shared + warp * Sh::bytes;
-    float *const fd = reinterpret_cast<float *>(sh + Sh::fd), *const fx = reinterpret_cast<float *>(sh + Sh::fx);
-    float *const fy = reinterpret_cast<float *>(sh + Sh::fy);
-    float *const fbias = reinterpret_cast<float *>(sh + Sh::bias), *const fD = reinterpret_cast<float *>(sh + Sh::D);
-
-    // A channel of the group as (value head, channel).
+    const int c0 = tile * W, width = min(W, p.r * p.V - c0);  // channels of the key head's value heads, this block's first
+    // A channel of the block as (value head, channel).
     auto head = [&](int c, int &j) {
-        const int h = c / p.V;
-        j = c - h * p.V;
+        const int h = (c0 + c) / p.V;
+        j = c0 + c - h * p.V;
         return g * p.r + h;
     };
+    const int chunks = (u.len - 1) / N + 1;
+    auto floats = [&](int at) { return reinterpret_cast<float *>(shared + at); };
 
-    // A lane's part in moving tokens: vectors of 8 channels (piece pc of tokens pt, pt + TPP, ...), or
-    // one channel (sc of tokens ps, ps + TPS, ...) where rows are not such vectors.
-    constexpr int PCS = W / 8, TPP = 32 / PCS, TPS = 32 / W;
-    const int pc = lane % PCS, pt = lane / PCS, sc = lane % W, ps = lane / W;
-    int mj = 0, mh = 0;
-    const bool mon = (VEC ? pc * 8 : sc) < width;
-    if (mon) mh = head(c0 + (VEC ? pc * 8 : sc), mj);
-
-    if (u.slot < 0) {  // padding: zeros
-        if (READ && mon) {
-            TT *o = static_cast<TT *>(p.out) + u.t0 * p.o_ts + (long long)mh * p.o_hs + mj;
-            if constexpr (VEC) {
-                for (int t = pt; t < u.len; t += TPP)
+    if (warp < NW) {
+        // ---- the recurrence: states warp KT ... of channels 2 lane and 2 lane + 1, and their rates
+        if (u.slot < 0) return;
+        float2 S[KT], A[KT];
+        int ch[2], cj[2];
+        bool on[2];
 #pragma unroll
-                    for (int i = 0; i < 8 * (int)sizeof(TT) / 16; ++i)
-                        reinterpret_cast<uint4 *>(o + (long long)t * p.o_ts)[i] = make_uint4(0, 0, 0, 0);
+        for (int e = 0; e < 2; ++e) {
+            on[e] = 2 * lane + e < width;
+            cj[e] = 0;
+            ch[e] = on[e] ? head(2 * lane + e, cj[e]) : 0;
+        }
+        const int have = min(KT, p.K - warp * KT);  // states that there are
+        const long long k0 = (long long)warp * KT;
+        const long long st0 = (long long)u.slot * p.st_slot + (long long)ch[0] * p.st_head + cj[0] + k0 * p.st_k;
+        const long long st1 = (long long)u.slot * p.st_slot + (long long)ch[1] * p.st_head + cj[1] + k0 * p.st_k;
+        const long long ws0 = ((u.piece * p.nv + ch[0]) * p.K + k0) * p.V + cj[0];  // in the workspace, [nv, K, V] a segment
+        const long long ws1 = ((u.piece * p.nv + ch[1]) * p.K + k0) * p.V + cj[1];
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+            S[i] = A[i] = make_float2(0.0f, 0.0f);
+            if (i >= have) continue;
+            if (on[0]) A[i].x = rate<TT>(p.A[ch[0] * p.a_hs + cj[0] * p.a_vs + (k0 + i) * p.a_ks]);
+            if (on[1]) A[i].y = rate<TT>(p.A[ch[1] * p.a_hs + cj[1] * p.a_vs + (k0 + i) * p.a_ks]);
+            if (first) continue;
+            if (p.seg) {
+                if (on[0]) S[i].x = p.ws[ws0 + (long long)i * p.V];
+                if (on[1]) S[i].y = p.ws[ws1 + (long long)i * p.V];
+            } else if (p.st_bf16) {
+                const uint16_t *s = static_cast<const uint16_t *>(p.state);
+                if (on[0]) S[i].x = to_f32(s[st0 + i * p.st_k]);
+                if (on[1]) S[i].y = to_f32(s[st1 + i * p.st_k]);
             } else {
-                for (int t = ps; t < u.len; t += TPS) o[(long long)t * p.o_ts] = TT(0);
+                const float *s = static_cast<const float *>(p.state);
+                if (on[0]) S[i].x = s[st0 + i * p.st_k];
+                if (on[1]) S[i].y = s[st1 + i * p.st_k];
             }
         }
+        // the states into their slot, or a segment's into the workspace
+        auto put = [&]() {
+#pragma unroll
+            for (int i = 0; i < KT; ++i) {
+                if (i >= have) continue;
+                if (first) {
+                    if (on[0]) p.ws[ws0 + (long long)i * p.V] = S[i].x;
+                    if (on[1]) p.ws[ws1 + (long long)i * p.V] = S[i].y;
+                } else if (p.st_bf16) {
+                    uint16_t *s = static_cast<uint16_t *>(p.state);
+                    if (on[0]) s[st0 + i * p.st_k] = from_f32<uint16_t>(S[i].x);
+                    if (on[1]) s[st1 + i * p.st_k] = from_f32<uint16_t>(S[i].y);
+                } else {
+                    float *s = static_cast<float *>(p.state);
+                    if (on[0]) s[st0 + i * p.st_k] = S[i].x;
+                    if (on[1]) s[st1 + i * p.st_k] = S[i].y;
+                }
+            }
+        };
+        // one token: its d and d x, B and C from shared memory
+        auto token = [&](const float *d, const float *x, const float *b, const float *q) {
+            const float2 dv = *reinterpret_cast<const float2 *>(d), xv = *reinterpret_cast<const float2 *>(x);
+            float Bv[KT], Cv[KT];
+#pragma unroll
+            for (int i = 0; i < KT; i += KT < 4 ? 2 : 4) {
+                if constexpr (KT < 4) {
+                    *reinterpret_cast<float2 *>(Bv + i) = *reinterpret_cast<const float2 *>(b + i);
+                    if (READ) *reinterpret_cast<float2 *>(Cv + i) = *reinterpret_cast<const float2 *>(q + i);
+                } else {
+                    *reinterpret_cast<float4 *>(Bv + i) = *reinterpret_cast<const float4 *>(b + i);
+                    if (READ) *reinterpret_cast<float4 *>(Cv + i) = *reinterpret_cast<const float4 *>(q + i);
+                }
+            }
+            float2 y = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < KT; ++i) {
+                const float2 e = __fmul2_rn(dv, A[i]);
+                S[i].x = fmaf(decay<TT>(e.x), S[i].x, xv.x * Bv[i]);
+                S[i].y = fmaf(decay<TT>(e.y), S[i].y, xv.y * Bv[i]);
+                if (READ) {
+                    y.x = fmaf(Cv[i], S[i].x, y.x);
+                    y.y = fmaf(Cv[i], S[i].y, y.y);
+                }
+            }
+            return y;
+        };
+        __syncthreads();
+        for (int k = 0; k <= chunks; ++k) {
+            if (k < chunks) {
+                const int n = u.len - k * N, cut = u.kept - k * N;  // tokens behind n are d = 0, d x = 0
+                const float *d = floats(Sh::fd) + (k & 1) * N * W + 2 * lane, *x = floats(Sh::fx) + (k & 1) * N * W + 2 * lane;
+                const float *b = floats(Sh::fB) + (k & 1) * N * KP + warp * KT, *q = floats(Sh::fC) + (k & 1) * N * KP + warp * KT;
+                float *y = floats(Sh::fy) + ((k & 1) * NW + warp) * N * W + 2 * lane;
+                if (!first && cut > 0 && cut < N && cut < n) {  // the slot's state lies inside
+#pragma unroll 1
+                    for (int t = 0; t < N; ++t) {
+                        const float2 v = token(d + t * W, x + t * W, b + t * KP, q + t * KP);
+                        if (READ) *reinterpret_cast<float2 *>(y + t * W) = v;
+                        if (t + 1 == cut) put();
+                    }
+                } else {
+#pragma unroll 1
+                    for (int t0 = 0; t0 < N && t0 < n; t0 += 4) {
+                        float2 v[4];
+#pragma unroll
+                        for (int t = 0; t < 4; ++t)
+                            v[t] = token(d + (t0 + t) * W, x + (t0 + t) * W, b + (t0 + t) * KP, q + (t0 + t) * KP);
+                        if (READ)
+#pragma unroll
+                            for (int t = 0; t < 4; ++t) *reinterpret_cast<float2 *>(y + (t0 + t) * W) = v[t];
+                    }
+                    if (!first && cut > 0 && cut <= N) put();  // behind the chunk, or behind the row's last token
+                }
+            }
+            __syncthreads();
+        }
+        if (first) put();
         return;
     }
 
-    // ---- chunks on their way to shared memory
-    const TT *const xp = static_cast<const TT *>(p.x) + u.t0 * p.x_ts + (long long)mh * p.x_hs + mj;
-    const TT *const zp = READ && p.z ? static_cast<const TT *>(p.z) + u.t0 * p.z_ts + (long long)mh * p.z_hs + mj : nullptr;
-    const DT *const dp = static_cast<const DT *>(p.dt) + u.t0 * p.dt_ts + (long long)mh * p.dt_hs + mj * p.dt_es;
+    // ---- the helpers.  A thread has four values of a chunk: four channels of a token where rows are
+    // vectors, else one channel of four tokens; it copies them, makes d and d x of them, and finishes
+    // their outputs, so that raw values need no barrier.
+    const int id = tid - 32 * NW;
+    const int mt = VEC ? id / (W / 4) : id / W * 4, mc = VEC ? id % (W / 4) * 4 : id % W;
+    const bool mon = mc < width;
+    int mj = 0, mh = 0;
+    if (mon) mh = head(mc, mj);
+    auto at = [&](int i) { return VEC ? mt * W + mc + i : (mt + i) * W + mc; };
+    TT *const op = READ ? static_cast<TT *>(p.out) + (u.t0 + mt) * p.o_ts + (long long)mh * p.o_hs + mj : nullptr;
+    if (u.slot < 0) {  // padding: zeros
+        if (READ && mon)
+            for (int base = 0; base < u.len; base += N)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (base + mt + (VEC ? 0 : i) < u.len) op[(base + (VEC ? 0 : i)) * p.o_ts + (VEC ? i : 0)] = TT(0);
+        return;
+    }
+    const TT *const xp = static_cast<const TT *>(p.x) + (u.t0 + mt) * p.x_ts + (long long)mh * p.x_hs + mj;
+    const TT *const zp = READ && p.z ? static_cast<const TT *>(p.z) + (u.t0 + mt) * p.z_ts + (long long)mh * p.z_hs + mj : nullptr;
+    const DT *const dp = static_cast<const DT *>(p.dt) + (u.t0 + mt) * p.dt_ts + (long long)mh * p.dt_hs + mj * p.dt_es;
     const TT *const bp = static_cast<const TT *>(p.B) + u.t0 * p.B_ts + (long long)g * p.B_hs;
     const TT *const cp = READ ? static_cast<const TT *>(p.C) + u.t0 * p.C_ts + (long long)g * p.C_hs : nullptr;
-
-    auto rows = [&](auto *to, const auto *from, long long stride, int n, bool vec) {
-        using T = std::remove_const_t<std::remove_pointer_t<decltype(from)>>;
-        if (!mon) return;
-        if constexpr (VEC) {
-            if (vec) {
+    float bias[4], D[4];
 #pragma unroll
-                for (int i = 0; i < (N + TPP - 1) / TPP; ++i) {
-                    const int t = pt + i * TPP;
-                    if (t < n)
-#pragma unroll
-                        for (int v = 0; v < 8; v += 16 / (int)sizeof(T))
-                            cp_async16(to + t * W + pc * 8 + v, from + (long long)t * stride + v);
-                }
-            } else {  // one value for the head
-                for (int t = pt; t < n; t += TPP) {
-                    const T v = from[(long long)t * stride];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) to[t * W + pc * 8 + i] = v;
-                }
-            }
-        } else if constexpr (sizeof(T) == 4) {
-#pragma unroll 4
-            for (int t = ps; t < n; t += TPS) cp_async4(to + t * W + sc, from + (long long)t * stride);
-        } else {
-            T v[N / TPS];
-#pragma unroll
-            for (int i = 0; i < N / TPS; ++i)
-                if (ps + i * TPS < n) v[i] = from[(long long)(ps + i * TPS) * stride];
-#pragma unroll
-            for (int i = 0; i < N / TPS; ++i)
-                if (ps + i * TPS < n) to[(ps + i * TPS) * W + sc] = v[i];
-        }
-    };
+    for (int i = 0; i < 4; ++i) {
+        const int j = mj + (VEC ? i : 0);
+        bias[i] = mon && p.bias ? p.bias[mh * p.b_hs + j * p.b_vs] : 0.0f;
+        D[i] = READ && mon && p.D ? p.D[mh * p.d_hs + j * p.d_vs] : 0.0f;
+    }
+    constexpr int NB = (READ ? 2 : 1) * N * KP;  // values of B and C in a chunk
     const bool bc_vec = p.bc_vec && p.K == KP;
-    auto states = [&](TT *to, const TT *from, long long stride, int n) {
-        if (bc_vec) {
-            constexpr int C = 16 / (int)sizeof(TT), VR = KP / C;
-#pragma unroll
-            for (int i = 0; i < (N * VR + 31) / 32; ++i) {
-                const int t = (lane + 32 * i) / VR, v = (lane + 32 * i) % VR;
-                if (t < n) cp_async16(to + t * KP + v * C, from + (long long)t * stride + v * C);
-            }
+    // Values that no asynchronous copy can move (2 bytes, not as vectors) wait here for a chunk's time.
+    constexpr bool slow = sizeof(TT) == 2;
+    constexpr int NT = (NB + kScanHelpers - 1) / kScanHelpers, NS = slow ? NT : 1;  // a thread's of them
+    TT wx[4], wz[4], wbc[NS];
+    DT wd[4];
+    auto raw = [&](int k) { return shared + k % R * Sh::stage; };
+
+    auto copy = [&](auto *to, const auto *from, long long stride, auto (&wait)[4], int n) {
+        using T = std::remove_const_t<std::remove_pointer_t<decltype(from)>>;
+        if constexpr (VEC) {
+            if (mon && mt < n) cp_async<4 * (int)sizeof(T)>(to + at(0), from);
         } else {
-            for (int k = lane; k < p.K; k += 32) {
-                if constexpr (sizeof(TT) == 4) {
-#pragma unroll 4
-                    for (int t = 0; t < n; ++t) cp_async4(to + t * KP + k, from + (long long)t * stride + k);
-                } else {
-                    TT v[N];
 #pragma unroll
-                    for (int t = 0; t < N; ++t)
-                        if (t < n) v[t] = from[(long long)t * stride + k];
-#pragma unroll
-                    for (int t = 0; t < N; ++t)
-                        if (t < n) to[t * KP + k] = v[t];
+            for (int i = 0; i < 4; ++i)
+                if (mon && mt + i < n) {
+                    if constexpr (sizeof(T) == 4) cp_async<4>(to + at(i), from + i * stride);
+                    else wait[i] = from[i * stride];
                 }
-            }
         }
     };
-    auto fetch = [&](int base, int stage) {
-        const int n = min(N, u.len - base);
-        if (n > 0) {
-            unsigned char *const to = sh + stage * Sh::stage;
-            rows(reinterpret_cast<DT *>(to + Sh::dt), dp + (long long)base * p.dt_ts, p.dt_ts, n, p.dt_es != 0);
-            rows(reinterpret_cast<TT *>(to + Sh::x), xp + (long long)base * p.x_ts, p.x_ts, n, true);
-            states(reinterpret_cast<TT *>(to + Sh::B), bp + (long long)base * p.B_ts, p.B_ts, n);
-            if (READ) {
-                states(reinterpret_cast<TT *>(to + Sh::C), cp + (long long)base * p.C_ts, p.C_ts, n);
-                if (zp) rows(reinterpret_cast<TT *>(to + Sh::z), zp + (long long)base * p.z_ts, p.z_ts, n, true);
+    auto fetch = [&](int k) {
+        if (k < chunks) {
+            const int n = u.len - k * N;
+            const long long t = (long long)k * N;
+            unsigned char *const to = raw(k);
+            copy(reinterpret_cast<DT *>(to + Sh::dt), dp + t * p.dt_ts, p.dt_ts, wd, n);
+            copy(reinterpret_cast<TT *>(to + Sh::x), xp + t * p.x_ts, p.x_ts, wx, n);
+            if (READ && zp) copy(reinterpret_cast<TT *>(to + Sh::z), zp + t * p.z_ts, p.z_ts, wz, n);
+            if (bc_vec) {
+#pragma unroll
+                for (int i = 0; i < (NB / 4 + kScanHelpers - 1) / kScanHelpers; ++i) {
+                    const int v = 4 * (id + i * kScanHelpers), w = v % (N * KP), s = w / KP;
+                    if (v < NB && s < n)
+                        cp_async<4 * (int)sizeof(TT)>(reinterpret_cast<TT *>(to + Sh::B) + v,
+                                                      v < N * KP ? bp + (t + s) * p.B_ts + w % KP : cp + (t + s) * p.C_ts + w % KP);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const int v = id + i * kScanHelpers, w = v % (N * KP), s = w / KP;
+                    if (v < NB && s < n && w % KP < p.K) {
+                        const TT *from = v < N * KP ? bp + (t + s) * p.B_ts + w % KP : cp + (t + s) * p.C_ts + w % KP;
+                        if constexpr (!slow) cp_async<4>(reinterpret_cast<TT *>(to + Sh::B) + v, from);
+                        else wbc[i] = *from;
+                    }
+                }
             }
         }
         cp_async_commit();
     };
-    for (int i = lane; i < 2 * Sh::stage / 16; i += 32) reinterpret_cast<uint4 *>(sh)[i] = make_uint4(0, 0, 0, 0);
-    for (int i = lane; i < W; i += 32) {
-        int j = 0, h = 0;
-        const bool in = i < width;
-        if (in) h = head(c0 + i, j);
-        fbias[i] = in && p.bias ? p.bias[h * p.b_hs + j * p.b_vs] : 0.0f;
-        fD[i] = in && p.D ? p.D[h * p.d_hs + j * p.d_vs] : 0.0f;
-    }
-    __syncwarp();
-    fetch(0, 0);
-
-    // ---- this lane's states and their rates, in pairs along K
-    const int lk = lane % LK, cg = lane / LK;
-    float2 S[CH][KT / 2], A[CH][KT / 2];
-    long long st_at[CH];
-    int chan[CH], chead[CH];
-    bool on[CH];
+    // what waited for chunk k, to its place
+    auto land = [&](int k) {
+        if (k >= chunks) return;
+        unsigned char *const to = raw(k);
+        if constexpr (!VEC && sizeof(DT) == 2)
 #pragma unroll
-    for (int e = 0; e < CH; ++e) {
-        on[e] = cg * 4 + e < width;
-        chan[e] = 0;
-        chead[e] = on[e] ? head(c0 + cg * 4 + e, chan[e]) : 0;
-        st_at[e] = (long long)u.slot * p.st_slot + (long long)chead[e] * p.st_head + chan[e];
-    }
-    // a segment's state in the workspace: [nv, K, V]
-    auto segment = [&](int e, int k) {
-        return p.ws + ((u.piece * p.nv + chead[e]) * p.K + k) * (long long)p.V + chan[e];
+            for (int i = 0; i < 4; ++i) reinterpret_cast<DT *>(to + Sh::dt)[at(i)] = wd[i];
+        if constexpr (!VEC && slow)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                reinterpret_cast<TT *>(to + Sh::x)[at(i)] = wx[i];
+                if (READ && zp) reinterpret_cast<TT *>(to + Sh::z)[at(i)] = wz[i];
+            }
+        if constexpr (slow)
+            if (!bc_vec)
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+                    if (id + i * kScanHelpers < NB) reinterpret_cast<TT *>(to + Sh::B)[id + i * kScanHelpers] = wbc[i];
     };
+    float dsum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto convert = [&](int k) {
+        const int n = u.len - k * N;
+        const unsigned char *const from = raw(k);
+        const DT *const rd = reinterpret_cast<const DT *>(from + Sh::dt);
+        const TT *const rx = reinterpret_cast<const TT *>(from + Sh::x);
+        float *const fd = floats(Sh::fd) + (k & 1) * N * W, *const fx = floats(Sh::fx) + (k & 1) * N * W;
+        float d[4], x[4];
+        if constexpr (VEC) {
+            Pack<DT, 4> qd;
+            Pack<TT, 4> qx;
+            qd.load(rd + at(0));
+            qx.load(rx + at(0));
 #pragma unroll
-    for (int i = 0; i < KT; ++i) {
-        const int k = lk * KT + i;
-        float v[CH], a[CH];
-#pragma unroll
-        for (int e = 0; e < CH; ++e) v[e] = a[e] = 0.0f;
-        if (k < p.K) {
-            if (first) {
-            } else if (p.seg) {
-#pragma unroll
-                for (int e = 0; e < CH; ++e)
-                    if (on[e]) v[e] = *segment(e, k);
-            } else if constexpr (VEC) {
-                if (on[0]) {
-                    if (p.st_bf16) {
-                        Pack<uint16_t, 4> q;
-                        q.load(static_cast<const uint16_t *>(p.state) + st_at[0] + k * p.st_k);
-#pragma unroll
-                        for (int e = 0; e < CH; ++e) v[e] = q.get(e);
-                    } else {
-                        Pack<float, 4> q;
-                        q.load(static_cast<const float *>(p.state) + st_at[0] + k * p.st_k);
-#pragma unroll
-                        for (int e = 0; e < CH; ++e) v[e] = q.get(e);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < CH; ++e)
-                    if (on[e])
-                        v[e] = p.st_bf16 ? to_f32(static_cast<const uint16_t *>(p.state)[st_at[e] + k * p.st_k])
-                                         : static_cast<const float *>(p.state)[st_at[e] + k * p.st_k];
+            for (int i = 0; i < 4; ++i) {
+                d[i] = qd.get(i);
+                x[i] = qx.get(i);
             }
-            if (VEC && p.a_vec) {
-                if (on[0]) {
-                    Pack<float, 4> q;
-                    q.load(p.A + chead[0] * p.a_hs + k * p.a_ks + chan[0]);
+        } else {
 #pragma unroll
-                    for (int e = 0; e < CH; ++e) a[e] = q.get(e);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < CH; ++e)
-                    if (on[e]) a[e] = p.A[chead[e] * p.a_hs + k * p.a_ks + chan[e] * p.a_vs];
+            for (int i = 0; i < 4; ++i) {
+                d[i] = to_f32(rd[at(i)]);
+                x[i] = to_f32(rx[at(i)]);
             }
         }
 #pragma unroll
-        for (int e = 0; e < CH; ++e) {
-            (i & 1 ? S[e][i / 2].y : S[e][i / 2].x) = v[e];
-            (i & 1 ? A[e][i / 2].y : A[e][i / 2].x) = rate<TT>(a[e]);
+        for (int i = 0; i < 4; ++i) {
+            d[i] += bias[i];
+            if (p.softplus) d[i] = softplus<TT>(d[i]);
+            if (!mon || mt + (VEC ? 0 : i) >= n) d[i] = x[i] = 0.0f;
+            x[i] *= d[i];
+            if (!READ) dsum[i] += d[i];
         }
-    }
-    // the states into their slot, or a segment's into the workspace
-    auto put = [&]() {
+        if constexpr (VEC) {
+            *reinterpret_cast<float4 *>(fd + at(0)) = make_float4(d[0], d[1], d[2], d[3]);
+            *reinterpret_cast<float4 *>(fx + at(0)) = make_float4(x[0], x[1], x[2], x[3]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < KT; ++i) {
-            const int k = lk * KT + i;
-            if (k >= p.K) continue;
-            float v[CH];
+            for (int i = 0; i < 4; ++i) {
+                fd[at(i)] = d[i];
+                fx[at(i)] = x[i];
+            }
+        }
+        // B and C: this thread's own values again; states past K are 0
+        const TT *const rb = reinterpret_cast<const TT *>(from + Sh::B);
+        auto place = [&](int v) { return v < N * KP ? floats(Sh::fB) + (k & 1) * N * KP + v : floats(Sh::fC) + (k & 1) * N * KP + v - N * KP; };
+        if (bc_vec) {
 #pragma unroll
-            for (int e = 0; e < CH; ++e) v[e] = i & 1 ? S[e][i / 2].y : S[e][i / 2].x;
-            if (first) {
-#pragma unroll
-                for (int e = 0; e < CH; ++e)
-                    if (on[e]) *segment(e, k) = v[e];
-            } else if constexpr (VEC) {
-                if (!on[0]) continue;
-                if (p.st_bf16) {
-                    Pack<uint16_t, 4> q;
-#pragma unroll
-                    for (int e = 0; e < CH; ++e) q.set(e, v[e]);
-                    q.store(static_cast<uint16_t *>(p.state) + st_at[0] + k * p.st_k);
-                } else {
-                    Pack<float, 4> q;
-#pragma unroll
-                    for (int e = 0; e < CH; ++e) q.set(e, v[e]);
-                    q.store(static_cast<float *>(p.state) + st_at[0] + k * p.st_k);
+            for (int i = 0; i < (NB / 4 + kScanHelpers - 1) / kScanHelpers; ++i) {
+                const int v = 4 * (id + i * kScanHelpers);
+                if (v < NB) {
+                    Pack<TT, 4> q;
+                    q.load(rb + v);
+                    const bool some = v % (N * KP) / KP < n;
+                    *reinterpret_cast<float4 *>(place(v)) = some ? make_float4(q.get(0), q.get(1), q.get(2), q.get(3)) : make_float4(0, 0, 0, 0);
                 }
-            } else {
+            }
+        } else {
 #pragma unroll
-                for (int e = 0; e < CH; ++e) {
-                    if (!on[e]) continue;
-                    if (p.st_bf16) static_cast<uint16_t *>(p.state)[st_at[e] + k * p.st_k] = from_f32<uint16_t>(v[e]);
-                    else static_cast<float *>(p.state)[st_at[e] + k * p.st_k] = v[e];
-                }
+            for (int i = 0; i < NT; ++i) {
+                const int v = id + i * kScanHelpers, w = v % (N * KP);
+                if (v < NB) *place(v) = w / KP < n && w % KP < p.K ? to_f32(rb[v]) : 0.0f;
             }
         }
     };
-
-    float dsum[CH] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int base = 0, stage = 0; base < u.len; base += N, stage ^= 1) {
-        const int n = min(N, u.len - base);
-        fetch(base + N, stage ^ 1);
-        cp_async_wait<1>();
-        __syncwarp();
-        unsigned char *const raw = sh + stage * Sh::stage;
-        TT *const rx = reinterpret_cast<TT *>(raw + Sh::x);
-        const TT *const rz = reinterpret_cast<const TT *>(raw + Sh::z);
-        const DT *const rd = reinterpret_cast<const DT *>(raw + Sh::dt);
-        // ---- d and d x, B and C in float32
+    auto finish = [&](int k) {
+        const int n = u.len - k * N;
+        const TT *const rx = reinterpret_cast<const TT *>(raw(k) + Sh::x), *const rz = reinterpret_cast<const TT *>(raw(k) + Sh::z);
+        const float *const fy = floats(Sh::fy) + (k & 1) * NW * N * W;
+        float y[4], x[4], z[4];
+        if constexpr (VEC) {
+            Pack<TT, 4> qx, qz;
+            qx.load(rx + at(0));
+            if (zp) qz.load(rz + at(0));
 #pragma unroll
-        for (int i = 0; i < (N * PCS + 31) / 32; ++i) {
-            const int t = pt + i * TPP, at = t * W + pc * 8;
-            if (N * PCS % 32 && t >= N) continue;
+            for (int i = 0; i < 4; ++i) {
+                x[i] = qx.get(i);
+                z[i] = qz.get(i);
+            }
+        } else {
 #pragma unroll
-            for (int v = 0; v < 8; v += 4) {
-                Pack<DT, 4> dq;
-                Pack<TT, 4> xq;
-                dq.load(rd + at + v);
-                xq.load(rx + at + v);
-                const float4 b = *reinterpret_cast<const float4 *>(fbias + pc * 8 + v);
-                float d[4] = {dq.get(0) + b.x, dq.get(1) + b.y, dq.get(2) + b.z, dq.get(3) + b.w}, x[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (p.softplus) d[j] = softplus<TT>(d[j]);
-                    x[j] = d[j] * xq.get(j);
-                }
-                *reinterpret_cast<float4 *>(fd + at + v) = make_float4(d[0], d[1], d[2], d[3]);
-                *reinterpret_cast<float4 *>(fx + at + v) = make_float4(x[0], x[1], x[2], x[3]);
+            for (int i = 0; i < 4; ++i) {
+                x[i] = to_f32(rx[at(i)]);
+                z[i] = to_f32(rz[at(i)]);
             }
         }
-        const float *fB = reinterpret_cast<const float *>(raw + Sh::B), *fC = reinterpret_cast<const float *>(raw + Sh::C);
-        if constexpr (!Sh::wide) {
-            float *const tB = reinterpret_cast<float *>(sh + Sh::fB), *const tC = reinterpret_cast<float *>(sh + Sh::fC);
 #pragma unroll
-            for (int i = 0; i < (N * KP / 4 + 31) / 32; ++i) {
-                const int at = 4 * (lane + 32 * i);
-                Pack<TT, 4> q;
-                q.load(reinterpret_cast<const TT *>(raw + Sh::B) + at);
-                *reinterpret_cast<float4 *>(tB + at) = make_float4(q.get(0), q.get(1), q.get(2), q.get(3));
-                if (READ) {
-                    q.load(reinterpret_cast<const TT *>(raw + Sh::C) + at);
-                    *reinterpret_cast<float4 *>(tC + at) = make_float4(q.get(0), q.get(1), q.get(2), q.get(3));
-                }
-            }
-            fB = tB;
-            fC = tC;
-        }
-        __syncwarp();
-        // ---- the tokens, in two parts where the slot's state lies between them
-        struct Operands {
-            float4 d, x;
-            float2 B[KT / 2], C[KT / 2];
-        };
-        auto operands = [&](int t, Operands &o) {
-            o.d = *reinterpret_cast<const float4 *>(fd + t * W + cg * 4);
-            o.x = *reinterpret_cast<const float4 *>(fx + t * W + cg * 4);
+        for (int w = 0; w < NW; ++w) {
+            if constexpr (VEC) {
+                const float4 q = *reinterpret_cast<const float4 *>(fy + w * N * W + at(0));
+                y[0] = w ? y[0] + q.x : q.x;
+                y[1] = w ? y[1] + q.y : q.y;
+                y[2] = w ? y[2] + q.z : q.z;
+                y[3] = w ? y[3] + q.w : q.w;
+            } else {
 #pragma unroll
-            for (int i = 0; i < KT / 2; i += 2) {
-                const float4 b = *reinterpret_cast<const float4 *>(fB + t * KP + lk * KT + 2 * i);
-                o.B[i] = make_float2(b.x, b.y);
-                o.B[i + 1] = make_float2(b.z, b.w);
-                if (READ) {
-                    const float4 c = *reinterpret_cast<const float4 *>(fC + t * KP + lk * KT + 2 * i);
-                    o.C[i] = make_float2(c.x, c.y);
-                    o.C[i + 1] = make_float2(c.z, c.w);
-                }
-            }
-        };
-        const int cut = u.kept - base;
-        const bool inside = !first && cut > 0 && cut <= n;
-        Operands now;
-        operands(0, now);
-        int t = 0;
-#pragma unroll 1
-        for (int part = 0; part < 2; ++part) {
-            const int end = part == 0 && inside ? cut : n;
-#pragma unroll 2
-            for (; t < end; ++t) {
-                Operands next;
-                operands(t + 1 < N ? t + 1 : t, next);
-                const float d[CH] = {now.d.x, now.d.y, now.d.z, now.d.w}, x[CH] = {now.x.x, now.x.y, now.x.z, now.x.w};
-                float y[CH];
-#pragma unroll
-                for (int e = 0; e < CH; ++e) {
-#pragma unroll
-                    for (int i = 0; i < KT / 2; ++i) {
-                        const float2 a = __fmul2_rn(make_float2(d[e], d[e]), A[e][i]);
-                        const float2 in = __fmul2_rn(make_float2(x[e], x[e]), now.B[i]);
-                        S[e][i].x = fmaf(decay<TT>(a.x), S[e][i].x, in.x);
-                        S[e][i].y = fmaf(decay<TT>(a.y), S[e][i].y, in.y);
-                        if (READ) {
-                            y[e] = i == 0 ? now.C[i].x * S[e][i].x : fmaf(now.C[i].x, S[e][i].x, y[e]);
-                            y[e] = fmaf(now.C[i].y, S[e][i].y, y[e]);
-                        }
-                    }
-                    if (!READ) dsum[e] += d[e];
-                }
-                if (READ) {
-                    const float v = scan_readout<LK>(y, lk);
-                    if (LK == 4 || lk < 4) fy[t * W + cg * 4 + (lk & 3)] = v;
-                }
-                now = next;
-            }
-            if (part == 0 && inside) put();
-        }
-        __syncwarp();
-        // ---- its outputs
-        if constexpr (READ) {
-#pragma unroll
-            for (int i = 0; i < (N * PCS + 31) / 32; ++i) {
-                const int t = pt + i * TPP, at = t * W + pc * 8;
-                if (t >= n) continue;
-                constexpr int C = 16 / (int)sizeof(TT);
-#pragma unroll
-                for (int v = 0; v < 8; v += C) {
-                    Pack<TT, C> x, z, o;
-                    x.load(rx + at + v);
-                    if (zp) z.load(rz + at + v);
-#pragma unroll
-                    for (int j = 0; j < C; ++j) {
-                        float y = fmaf(fD[pc * 8 + v + j], x.get(j), fy[at + v + j]);
-                        if (zp) y *= silu(z.get(j));
-                        o.set(j, y);
-                    }
-                    if constexpr (VEC) {
-                        if (mon) o.store(static_cast<TT *>(p.out) + (u.t0 + base + t) * p.o_ts + (long long)mh * p.o_hs + mj + v);
-                    } else {
-                        o.store(rx + at + v);
-                    }
-                }
-            }
-            if constexpr (!VEC) {
-                __syncwarp();
-                if (mon) {
-                    TT *const to = static_cast<TT *>(p.out) + (u.t0 + base) * p.o_ts + (long long)mh * p.o_hs + mj;
-#pragma unroll 4
-                    for (int t = ps; t < n; t += TPS) to[(long long)t * p.o_ts] = rx[t * W + sc];
-                }
+                for (int i = 0; i < 4; ++i) y[i] = w ? y[i] + fy[w * N * W + at(i)] : fy[at(i)];
             }
         }
-        __syncwarp();
+        TT *const to = op + (long long)k * N * p.o_ts;
+        Pack<TT, 4> o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[i] = fmaf(D[i], x[i], y[i]);
+            if (zp) y[i] *= silu(z[i]);
+            o.set(i, y[i]);
+        }
+        if constexpr (VEC) {
+            if (mon && mt < n) o.store(to);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (mon && mt + i < n) to[i * p.o_ts] = o.u.e[i];
+        }
+    };
+    // chunk k + D is asked for in turn k, D = R - 1; the ring then holds chunks k - 1 ... k + D - 1
+    constexpr int Dist = R - 1;
+    for (int k = 0; k < Dist; ++k) {
+        fetch(k);
+        land(k);
+    }
+    cp_async_wait<Dist - 1>();
+    convert(0);
+    __syncthreads();
+    for (int k = 0; k <= chunks; ++k) {
+        if (READ && k > 0) finish(k - 1);
+        if (k > 0) land(k + Dist - 1);
+        if (k + 1 < chunks) {
+            cp_async_wait<Dist - 2>();
+            convert(k + 1);
+        }
+        fetch(k + Dist);
+        __syncthreads();
     }
     if (first) {
-        put();
-        if (lk == 0) {
-            float *sum = p.ws + scan_pieces(p.T, p.seg, p.batch) * p.nv * p.K * p.V + u.piece * p.nv * p.V;
+        // each channel's step sizes, over the threads that have its tokens
+        float *const part = floats(0);
+        cp_async_wait<0>();
 #pragma unroll
-            for (int e = 0; e < CH; ++e)
-                if (on[e]) sum[(long long)chead[e] * p.V + chan[e]] = dsum[e];
+        for (int i = 0; i < 4; ++i)
+            if (VEC) part[at(i)] = dsum[i];
+        if (!VEC) part[mt / 4 * W + mc] = dsum[0] + dsum[1] + dsum[2] + dsum[3];
+        asm volatile("bar.sync 1, %0;" ::"n"(kScanHelpers) : "memory");
+        if (id < width) {
+            float s = 0.0f;
+            for (int t = 0; t < (VEC ? N : N / 4); ++t) s += part[t * W + id];
+            int j;
+            const int h = head(id, j);
+            p.ws[scan_pieces(p.T, p.seg, p.batch) * p.nv * p.K * p.V + (u.piece * p.nv + h) * (long long)p.V + j] = s;
         }
     }
 }
 
-template <typename TT, typename DT, int KT, int LK, bool VEC> cudaError_t scan_go(const ScanParams &p, cudaStream_t s) {
-    using Sh = ScanShared<TT, DT, KT, LK>;
-    constexpr int bytes = kScanWarps * Sh::bytes;
-    static_assert(bytes <= 227 << 10, "a block's shared memory");
+template <typename TT, typename DT, int KT, int NW, bool VEC> cudaError_t scan_go(const ScanParams &p, cudaStream_t s) {
+    using Sh = ScanShared<TT, DT, KT, NW>;
+    static_assert(Sh::bytes <= 227 << 10, "a block's shared memory");
+    constexpr int threads = 32 * NW + kScanHelpers;
     static LaunchCache cache;
     LaunchInfo info;
     cudaError_t e = launch_info(cache, &info, [](LaunchInfo &) {
-        const cudaError_t f = cudaFuncSetAttribute(k_scan<TT, DT, KT, LK, VEC, false>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        const cudaError_t f = cudaFuncSetAttribute(k_scan<TT, DT, KT, NW, VEC, false>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::bytes);
         if (f != cudaSuccess) return f;
-        return cudaFuncSetAttribute(k_scan<TT, DT, KT, LK, VEC, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        return cudaFuncSetAttribute(k_scan<TT, DT, KT, NW, VEC, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::bytes);
     });
     if (e != cudaSuccess) return e;
     const long long tiles = ((long long)p.r * p.V + Sh::W - 1) / Sh::W;
-    const long long rows = p.seg ? scan_pieces(p.T, p.seg, p.batch) : p.batch, units = rows * p.nk * tiles;
-    if (units >= 1ll << 31) return cudaErrorInvalidConfiguration;
-    const unsigned blocks = (unsigned)((units + kScanWarps - 1) / kScanWarps);
+    const long long rows = p.seg ? scan_pieces(p.T, p.seg, p.batch) : p.batch, blocks = rows * p.nk * tiles;
+    if (blocks >= 1ll << 31) return cudaErrorInvalidConfiguration;
     if (p.seg) {
-        k_scan<TT, DT, KT, LK, VEC, false><<<blocks, 32 * kScanWarps, bytes, s>>>(p, (int)tiles, (unsigned)units, 1);
+        k_scan<TT, DT, KT, NW, VEC, false><<<(unsigned)blocks, threads, Sh::bytes, s>>>(p, (int)tiles, 1);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         if ((e = launch_scan_join(p, s)) != cudaSuccess) return e;
     }
-    if (p.out) k_scan<TT, DT, KT, LK, VEC, true><<<blocks, 32 * kScanWarps, bytes, s>>>(p, (int)tiles, (unsigned)units, 0);
-    else k_scan<TT, DT, KT, LK, VEC, false><<<blocks, 32 * kScanWarps, bytes, s>>>(p, (int)tiles, (unsigned)units, 0);
+    if (p.out) k_scan<TT, DT, KT, NW, VEC, true><<<(unsigned)blocks, threads, Sh::bytes, s>>>(p, (int)tiles, 0);
+    else k_scan<TT, DT, KT, NW, VEC, false><<<(unsigned)blocks, threads, Sh::bytes, s>>>(p, (int)tiles, 0);
     return cudaGetLastError();
 }
 
-// States a lane and lanes a channel, by K.
+// States a warp and warps, by K.
 template <typename TT, typename DT, bool VEC> cudaError_t scan_states(const ScanParams &p, cudaStream_t s) {
+    if (p.K <= 8) return scan_go<TT, DT, 2, 4, VEC>(p, s);
     if (p.K <= 16) return scan_go<TT, DT, 4, 4, VEC>(p, s);
     if (p.K <= 32) return scan_go<TT, DT, 8, 4, VEC>(p, s);
     if (p.K <= 64) return scan_go<TT, DT, 8, 8, VEC>(p, s);
-    return scan_go<TT, DT, 8, 16, VEC>(p, s);
+    return scan_go<TT, DT, 16, 8, VEC>(p, s);
 }
 template <typename TT, typename DT> cudaError_t scan_vec(const ScanParams &p, bool vec, cudaStream_t s) {
     return vec ? scan_states<TT, DT, true>(p, s) : scan_states<TT, DT, false>(p, s);
