@@ -210,8 +210,8 @@ int gdr_short_conv(const gdr_short_conv_args *a, void *stream) {
     p.offsets = a->offsets;
     p.counts = a->counts;
     const int64_t es = esize(a->token_dtype);
-    p.vec = a->channels % (16 / es) == 0 && vector_rows(a->x, a->token_dtype, 16, a->x_seq_stride) &&
-            (!a->out || vector_rows(a->out, a->token_dtype, 16, a->out_seq_stride));
+    p.vec = a->channels % 4 == 0 && vector_rows(a->x, a->token_dtype, 4 * es, a->x_seq_stride) &&
+            (!a->out || vector_rows(a->out, a->token_dtype, 4 * es, a->out_seq_stride));
     p.w_vec = a->weight_tap_stride == 1 && vector_rows(a->weight, GDR_F32, 16, a->weight_chan_stride);
     p.st_run = a->width > 1 && (a->state_tap_stride == 1 || a->width == 2) && a->state_chan_stride == a->width - 1 &&
                vector_rows(a->conv_state, a->state_dtype, 16, a->state_slot_stride);
@@ -292,7 +292,11 @@ int gdr_selective_scan(const gdr_scan_args *a, void *stream) {
     if (p.seg && (!a->workspace || a->workspace_bytes < scan_bytes(a, p.seg))) p.seg = 0;
     p.ws = static_cast<float *>(a->workspace);
     const bool db = a->dt_dtype == GDR_BF16;
-    if (a->max_row_len == 1) return launched(gdr::launch_scan_step(p, tb, db, vec, static_cast<cudaStream_t>(stream)), fn);
+    if (a->max_row_len == 1) {
+        const bool all = vec && a->K % (a->K <= 16 ? 4 : a->K <= 32 ? 8 : a->K <= 64 ? 16 : 32) == 0 && vector_rows(a->B, a->token_dtype, 4 * esize(a->token_dtype), p.B_ts, p.B_hs) &&
+                         (!a->out || vector_rows(a->C, a->token_dtype, 4 * esize(a->token_dtype), p.C_ts, p.C_hs));
+        return launched(gdr::launch_scan_step(p, tb, db, all, static_cast<cudaStream_t>(stream)), fn);
+    }
     return launched(gdr::launch_scan(p, tb, db, vec, static_cast<cudaStream_t>(stream)), fn);
 }
 
@@ -336,8 +340,6 @@ int gdr_accept_drafts(const gdr_accept_args *a, void *stream) {
     p.out = a->out_tokens;
     p.o_ts = a->out_seq_stride;
     p.counts = a->counts;
-    p.vec = vector_rows(a->target, a->prob_dtype, 16, a->target_seq_stride) &&
-            (!a->draft || vector_rows(a->draft, a->prob_dtype, 16, a->draft_seq_stride));
     return launched(gdr::launch_accept(p, a->prob_dtype == GDR_BF16, static_cast<cudaStream_t>(stream)), fn);
 }
 

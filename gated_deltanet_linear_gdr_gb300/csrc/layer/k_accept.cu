@@ -2,13 +2,13 @@
 // and the token drawn behind them.
 //
 // A row needs a handful of single probabilities and then one whole row of the
-// target's (and of the drafter's, where a draft was refused), twice: a sum, and
-// the place where the running sum passes its share.  The first reading is HBM
-// bound, the second finds its values in L2 and looks at one warp's part only.  A
-// row is a cluster of blocks, as many as it takes to fill the GPU with few rows;
-// every warp sums one stretch of the vocabulary, the blocks exchange their sums
-// through distributed shared memory, and the warp whose stretch has the place walks
-// through it.
+// target's (and of the drafter's, where a draft was refused): a sum, and the place
+// where the running sum passes its share.  The sum is HBM bound, or bound by its
+// chain of dependent steps where rows are few.  A row is a cluster of blocks, as
+// many as it takes to fill the GPU; every warp sums one stretch of the vocabulary,
+// the blocks exchange their sums through distributed shared memory, and the block
+// whose stretch has the place reads that stretch (out of L2) once more, all of its
+// threads side by side.
 //
 // The token has to be the one that exact arithmetic finds: with a vocabulary of
 // 1e5 a float32 sum would miss it in a few draws of a hundred.  Differences are
@@ -42,7 +42,7 @@ struct Sum {
     }
 };
 
-enum Weight { kTarget, kDifference, kWithout };  // p; max(p - q, 0); p but 0 at the refused token
+enum Weight { kTarget, kDifference };  // p (0 at a refused token that was not drawn); max(p - q, 0)
 
 // One token's weight as (value, rounding error).
 template <Weight M> __device__ __forceinline__ void add_weight(Sum &a, float p, float q) {
@@ -68,95 +68,70 @@ template <Weight M> __device__ __forceinline__ double exact_weight(float p, floa
     }
 }
 
-// C neighbouring probabilities from i on; those at `end` and behind it count as 0.
+// C neighbouring probabilities from i on; those outside [0, end) count as 0.
 template <typename PT, int C> __device__ __forceinline__ void take(const PT *row, int i, int end, bool vec, float (&v)[C]) {
-    if (vec && i + C <= end) {
+    if (vec && i >= 0 && i + C <= end) {
         Pack<PT, C> w;
         w.load(row + i);
 #pragma unroll
         for (int j = 0; j < C; ++j) v[j] = w.get(j);
     } else {
 #pragma unroll
-        for (int j = 0; j < C; ++j) v[j] = i + j < end ? to_f32(row[i + j]) : 0.0f;
+        for (int j = 0; j < C; ++j) v[j] = i + j >= 0 && i + j < end ? to_f32(row[i + j]) : 0.0f;
     }
 }
 
-__device__ __forceinline__ double warp_sum(double v) {
+// What a row's draw goes by: weights of tokens [0, vocab), read in vectors from an index at or
+// before 0 that is aligned in memory.
+template <typename PT> struct Weights {
+    static constexpr int C = 16 / (int)sizeof(PT);
+    const PT *p, *q;
+    Weight mode;
+    int no, vocab;
+    bool vec;
+    // C neighbouring weights as (value, rounding error)
+    __device__ __forceinline__ void load(int i, int end, float (&pv)[C], float (&qv)[C]) const {
+        take<PT, C>(p, i, end, vec, pv);
+        if (mode == kDifference) take<PT, C>(q, i, end, vec, qv);
+    }
+    __device__ __forceinline__ void add(Sum &a, int i, const float (&pv)[C], const float (&qv)[C]) const {
+        if (mode == kDifference) {
 #pragma unroll
-    for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(kFull, v, m);
-    return v;
-}
+            for (int j = 0; j < C; ++j) add_weight<kDifference>(a, pv[j], qv[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < C; ++j) add_weight<kTarget>(a, i + j == no ? 0.0f : pv[j], 0.0f);
+        }
+    }
+    __device__ __forceinline__ double exact(int i, float pv, float qv) const {
+        if (mode == kDifference) return exact_weight<kDifference>(pv, qv);
+        return i == no ? 0.0 : exact_weight<kTarget>(pv, 0.0f);
+    }
+};
 
-// The sum of a warp's stretch [i0, i1).
-template <typename PT, Weight M>
-__device__ __forceinline__ double stretch(const PT *p, const PT *q, int no, int i0, int i1, bool vec, int lane) {
-    constexpr int C = 16 / (int)sizeof(PT), U = 4;
+// The sum of a warp's stretch [i0, i1), in every lane.
+template <typename PT> __device__ __forceinline__ double stretch(const Weights<PT> &w, int i0, int i1, int lane) {
+    constexpr int C = Weights<PT>::C, U = 2;
     Sum a;
     for (int i = i0 + lane * C; i < i1; i += 32 * C * U) {
         float pv[U][C], qv[U][C];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            take<PT, C>(p, i + k * 32 * C, i1, vec, pv[k]);
-            if (M == kDifference) take<PT, C>(q, i + k * 32 * C, i1, vec, qv[k]);
-        }
+        for (int k = 0; k < U; ++k) w.load(i + k * 32 * C, i1, pv[k], qv[k]);
 #pragma unroll
-        for (int k = 0; k < U; ++k)
-#pragma unroll
-            for (int j = 0; j < C; ++j) {
-                if (M == kWithout && i + k * 32 * C + j == no) pv[k][j] = 0.0f;
-                add_weight<M>(a, pv[k][j], M == kDifference ? qv[k][j] : 0.0f);
-            }
+        for (int k = 0; k < U; ++k) w.add(a, i + k * 32 * C, pv[k], qv[k]);
     }
-    return warp_sum((double)a.s + (double)a.c);
+#pragma unroll
+    for (int m = 16; m; m >>= 1) {
+        const float s = __shfl_xor_sync(kFull, a.s, m), c = __shfl_xor_sync(kFull, a.c, m);
+        a.add(s, c);
+    }
+    return (double)a.s + (double)a.c;
 }
 
-// The least token of a stretch where base and the running sum pass `share`; its last one with a weight where none does.
-template <typename PT, Weight M>
-__device__ __forceinline__ int find(const PT *p, const PT *q, int no, int i0, int i1, bool vec, int lane, double base, double share) {
-    constexpr int C = 16 / (int)sizeof(PT);
-    int last = -1;
-    for (int at = i0; at < i1; at += 32 * C) {
-        const int i = at + lane * C;
-        float pv[C], qv[C];
-        take<PT, C>(p, i, i1, vec, pv);
-        if (M == kDifference) take<PT, C>(q, i, i1, vec, qv);
-        double w[C], own = 0.0;
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            if (M == kWithout && i + j == no) pv[j] = 0.0f;
-            w[j] = exact_weight<M>(pv[j], M == kDifference ? qv[j] : 0.0f);
-            own += w[j];
-        }
-        double upto = own;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const double o = __shfl_up_sync(kFull, upto, m);
-            if (lane >= m) upto += o;
-        }
-        double run = base + (upto - own);
-        int here = -1;
-#pragma unroll
-        for (int j = 0; j < C; ++j) {
-            run += w[j];
-            if (here < 0 && w[j] > 0.0 && run > share) here = i + j;
-        }
-        const unsigned found = __ballot_sync(kFull, here >= 0);
-        if (found) return __shfl_sync(kFull, here, __ffs(found) - 1);
-        int mine = -1;
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-            if (w[j] > 0.0) mine = i + j;
-        const int most = __reduce_max_sync(kFull, mine);
-        last = most > last ? most : last;
-        base += __shfl_sync(kFull, upto, 31);
-    }
-    return last;
-}
-
-template <typename PT> __global__ void __launch_bounds__(kThreads) k_accept(const __grid_constant__ AcceptParams p) {
-    __shared__ double sums[kWarps];  // of this block's stretches
+template <typename PT> __global__ void __launch_bounds__(kThreads, 2) k_accept(const __grid_constant__ AcceptParams p) {
+    __shared__ double sums[kWarps];  // of this block's stretches, then of a stretch's parts
     __shared__ double block_sum;
-    __shared__ int first_refused, first_none;
+    __shared__ int first_refused, first_none, found, last;
     cg::cluster_group cluster = cg::this_cluster();
     const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int b = (int)(blockIdx.x / (unsigned)blocks), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -173,85 +148,136 @@ template <typename PT> __global__ void __launch_bounds__(kThreads) k_accept(cons
     }
     // which drafts pass
     const int drafts = (int)(hi - lo) - 1;
-    if (tid == 0) first_refused = first_none = drafts;
+    const float v = p.row_u[b];
+    if (tid == 0) {
+        first_refused = first_none = drafts;
+        found = 0x7fffffff;
+        last = -1;
+    }
     __syncthreads();
     const PT *const target = static_cast<const PT *>(p.target), *const draft = static_cast<const PT *>(p.draft);
     for (int i = tid; i < drafts; i += kThreads) {
         const long long t = lo + i;
         const int d = p.tokens[t + 1];
+        const float u = p.u[t];
         if (d < 0 || d >= p.vocab) {
             atomicMin(&first_none, i);
             continue;
         }
         const float pd = clean(to_f32(target[t * p.t_ts + d])), qd = draft ? clean(to_f32(draft[t * p.d_ts + d])) : 1.0f;
-        if (!((double)p.u[t] * (double)qd < (double)pd)) atomicMin(&first_refused, i);
+        if (!((double)u * (double)qd < (double)pd)) atomicMin(&first_refused, i);
     }
     __syncthreads();
     const int accepted = min(first_refused, first_none);
     const bool refused = first_refused < first_none;
     const long long t = lo + accepted;
-    const int no = refused ? p.tokens[t + 1] : -1;
-    const PT *const tp = target + t * p.t_ts, *const dp = draft ? draft + t * p.d_ts : nullptr;
-    Weight mode = !refused ? kTarget : draft ? kDifference : kWithout;
+    Weights<PT> w;
+    constexpr int C = Weights<PT>::C;
+    w.p = target + t * p.t_ts;
+    w.q = draft ? draft + t * p.d_ts : w.p;
+    w.mode = !refused ? kTarget : draft ? kDifference : kTarget;
+    w.no = refused && !draft ? p.tokens[t + 1] : -1;
+    w.vocab = p.vocab;
+    const int off_p = (int)(reinterpret_cast<uintptr_t>(w.p) % 16), off_q = (int)(reinterpret_cast<uintptr_t>(w.q) % 16);
+    w.vec = w.mode == kTarget || off_p == off_q;
+    const int start = -(off_p / (int)sizeof(PT));  // aligned, at most C - 1 before the first token
 
-    // the sums: stretches of whole vectors
-    const int each = ((p.vocab - 1) / (blocks * kWarps) + 8) / 8 * 8;
-    const long long from = (long long)(rank * kWarps + warp) * each;
+    // the sums: a stretch of whole vectors a warp
+    const int each = ((p.vocab - start - 1) / (blocks * kWarps) + C) / C * C;
+    const long long from = (long long)(rank * kWarps + warp) * each + start;
     const int i0 = (int)(from < p.vocab ? from : p.vocab), i1 = p.vocab - i0 < each ? p.vocab : i0 + each;
-    const bool vec = p.vec != 0;
-    double total = 0.0, before = 0.0;
+    double total = 0.0, before = 0.0, share = 0.0;
     int owner = -1;
-    const float v = p.row_u[b];
-    double share = 0.0;
     for (int pass = 0; pass < 2; ++pass) {
-        const double s = mode == kTarget       ? stretch<PT, kTarget>(tp, dp, no, i0, i1, vec, lane)
-                         : mode == kDifference ? stretch<PT, kDifference>(tp, dp, no, i0, i1, vec, lane)
-                                               : stretch<PT, kWithout>(tp, dp, no, i0, i1, vec, lane);
+        const double s = stretch(w, i0, i1, lane);
         if (lane == 0) sums[warp] = s;
         __syncthreads();
-        if (tid == 0) {
-            double all = 0.0;
-            for (int w = 0; w < kWarps; ++w) all += sums[w];
-            block_sum = all;
+        if (warp == 0) {
+            double all = lane < kWarps ? sums[lane] : 0.0;
+#pragma unroll
+            for (int m = kWarps / 2; m; m >>= 1) all += __shfl_xor_sync(kFull, all, m);
+            if (lane == 0) block_sum = all;
         }
         cluster.sync();
-        total = 0.0;
-        for (int r = 0; r < blocks; ++r) total += *cluster.map_shared_rank(&block_sum, r);
-        if (total > 0.0 || mode == kTarget) break;
-        mode = kTarget;  // nothing left over of the target: drawn from the target itself
+        // every warp adds up the blocks' sums alike: lane r has block r's
+        const double mine = lane < blocks ? *cluster.map_shared_rank(&block_sum, lane) : 0.0;
+        double upto = mine;
+#pragma unroll
+        for (int m = 1; m < 8; m <<= 1) {
+            const double o = __shfl_up_sync(kFull, upto, m);
+            if (lane >= m) upto += o;
+        }
+        total = __shfl_sync(kFull, upto, 7);
+        if (total > 0.0) {
+            // the block whose part passes the share; the last one with a weight where none does
+            share = v > 0.0f ? (double)v * total : 0.0;
+            const unsigned some = __ballot_sync(kFull, mine > 0.0), past = __ballot_sync(kFull, mine > 0.0 && upto > share);
+            owner = past ? __ffs(past) - 1 : 31 - __clz(some);
+            before = __shfl_sync(kFull, upto - mine, owner);
+        }
+        if (total > 0.0 || (w.mode == kTarget && w.no < 0)) break;
+        w.mode = kTarget;  // nothing left over of the target: drawn from the target itself
+        w.no = -1;
+        w.vec = true;
         cluster.sync();  // before the sums are written again
     }
-    if (total > 0.0) {
-        // the block, and then the warp, whose stretch passes the share; the last one with a weight where none does
-        share = v > 0.0f ? (double)v * total : 0.0;
-        double run = 0.0;
-        bool passed = false;
-        for (int r = 0; r < blocks && !passed; ++r) {
-            const double s = *cluster.map_shared_rank(&block_sum, r);
-            if (!(s > 0.0)) continue;
-            owner = r;
-            before = run;
-            run += s;
-            passed = run > share;
-        }
-    }
     if (owner == rank) {
-        int mine = -1;
-        double run = before, base = 0.0;
-        bool passed = false;
-        for (int w = 0; w < kWarps && !passed; ++w) {
-            if (!(sums[w] > 0.0)) continue;
-            mine = w;
-            base = run;
-            run += sums[w];
-            passed = run > share;
+        // the stretch, the same way
+        const double mine = lane < kWarps ? sums[lane] : 0.0;
+        double upto = mine;
+#pragma unroll
+        for (int m = 1; m < kWarps; m <<= 1) {
+            const double o = __shfl_up_sync(kFull, upto, m);
+            if (lane >= m) upto += o;
         }
-        if (mine == warp) {
-            const int x = mode == kTarget       ? find<PT, kTarget>(tp, dp, no, i0, i1, vec, lane, base, share)
-                          : mode == kDifference ? find<PT, kDifference>(tp, dp, no, i0, i1, vec, lane, base, share)
-                                                : find<PT, kWithout>(tp, dp, no, i0, i1, vec, lane, base, share);
-            if (lane == 0) out[accepted] = x;
+        const unsigned some = __ballot_sync(kFull, mine > 0.0), past = __ballot_sync(kFull, mine > 0.0 && before + upto > share);
+        const int which = past ? __ffs(past) - 1 : 31 - __clz(some);
+        double base = before + __shfl_sync(kFull, upto - mine, which);
+        const long long s0 = (long long)(rank * kWarps + which) * each + start;
+        const int end = (int)(s0 + each < p.vocab ? s0 + each : p.vocab);
+        // and its least token at which the running sum passes, by all threads
+        for (int i = (int)s0; i < end; i += C * kThreads) {
+            const int at = i + tid * C;
+            float pv[C], qv[C];
+            double own = 0.0;
+#pragma unroll
+            for (int j = 0; j < C; ++j) pv[j] = qv[j] = 0.0f;
+            if (at < end) w.load(at, end, pv, qv);
+#pragma unroll
+            for (int j = 0; j < C; ++j) own += w.exact(at + j, pv[j], qv[j]);
+            double sum = own;
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) {
+                const double o = __shfl_up_sync(kFull, sum, m);
+                if (lane >= m) sum += o;
+            }
+            __syncthreads();  // sums is read no more
+            if (lane == 31) sums[warp] = sum;
+            __syncthreads();
+            double ahead = lane < warp ? sums[lane] : 0.0, all = lane < kWarps ? sums[lane] : 0.0;
+#pragma unroll
+            for (int m = kWarps / 2; m; m >>= 1) {
+                ahead += __shfl_xor_sync(kFull, ahead, m);
+                all += __shfl_xor_sync(kFull, all, m);
+            }
+            double run = base + ahead + (sum - own);
+            int here = -1, positive = -1;
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+                const double x = w.exact(at + j, pv[j], qv[j]);
+                run += x;
+                if (x > 0.0) {
+                    positive = at + j;
+                    if (here < 0 && run > share) here = at + j;
+                }
+            }
+            if (here >= 0) atomicMin(&found, here);
+            if (positive >= 0) atomicMax(&last, positive);
+            __syncthreads();
+            if (found != 0x7fffffff) break;
+            base += all;
         }
+        if (tid == 0) out[accepted] = found != 0x7fffffff ? found : last;
     }
     if (rank == 0) {
         for (int i = tid; i < p.width; i += kThreads)
@@ -264,13 +290,13 @@ template <typename PT> __global__ void __launch_bounds__(kThreads) k_accept(cons
             }
         }
     }
-    cluster.sync();  // a block's shared memory stays while others read it
+    if (blocks > 1) cluster.sync();  // a block's shared memory stays while others read it
 }
 
 template <typename PT> cudaError_t go(const AcceptParams &p, cudaStream_t s) {
-    // blocks a row: enough to fill the GPU twice over, up to the largest portable cluster
+    // blocks a row: as many as run at once (two a multiprocessor), up to the largest portable cluster
     int blocks = 1;
-    while (blocks < 8 && (long long)p.batch * blocks < 2 * 152) blocks *= 2;
+    while (blocks < 8 && (long long)p.batch * blocks * 2 <= 2 * 152) blocks *= 2;
     if ((long long)p.batch * blocks >= 1ll << 31) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t c{};
     c.gridDim = dim3((unsigned)p.batch * (unsigned)blocks);

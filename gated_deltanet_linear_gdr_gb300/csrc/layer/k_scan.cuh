@@ -68,7 +68,7 @@ template <typename TT, typename DT, int KT, int NW> struct ScanShared {
 // READ: with outputs.  Without them states move only: into the slots, or (first != 0)
 // each segment's own state, from zero, and the sum of its step sizes into the workspace.
 template <typename TT, typename DT, int KT, int NW, bool VEC, bool READ>
-__global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 4 : KT * NW <= 32 ? 3 : 1)
+__global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 3 : KT * NW <= 32 ? 2 : 1)
     k_scan(const __grid_constant__ ScanParams p, int tiles, int first) {
     using Sh = ScanShared<TT, DT, KT, NW>;
     constexpr int W = Sh::W, KP = Sh::KP, N = Sh::N, R = Sh::ring;
@@ -192,8 +192,9 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 4 : KT
                         if (t + 1 == cut) put();
                     }
                 } else {
-#pragma unroll 1
-                    for (int t0 = 0; t0 < N && t0 < n; t0 += 4) {
+#pragma unroll
+                    for (int t0 = 0; t0 < N; t0 += 4) {
+                        if (t0 >= n) break;
                         float2 v[4];
 #pragma unroll
                         for (int t = 0; t < 4; ++t)
@@ -243,60 +244,75 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 4 : KT
     }
     constexpr int NB = (READ ? 2 : 1) * N * KP;  // values of B and C in a chunk
     const bool bc_vec = p.bc_vec && p.K == KP;
+    // a thread's of them: NV vectors of four, or NT one by one
+    constexpr int NV = (NB / 4 + kScanHelpers - 1) / kScanHelpers, NT = (NB + kScanHelpers - 1) / kScanHelpers;
     // Values that no asynchronous copy can move (2 bytes, not as vectors) wait here for a chunk's time.
     constexpr bool slow = sizeof(TT) == 2;
-    constexpr int NT = (NB + kScanHelpers - 1) / kScanHelpers, NS = slow ? NT : 1;  // a thread's of them
-    TT wx[4], wz[4], wbc[NS];
+    TT wx[4], wz[4], wbc[slow ? NT : 1];
     DT wd[4];
-    auto raw = [&](int k) { return shared + k % R * Sh::stage; };
 
     auto copy = [&](auto *to, const auto *from, long long stride, auto (&wait)[4], int n) {
         using T = std::remove_const_t<std::remove_pointer_t<decltype(from)>>;
         if constexpr (VEC) {
-            if (mon && mt < n) cp_async<4 * (int)sizeof(T)>(to + at(0), from);
+            if (n > 0) cp_async<4 * (int)sizeof(T)>(to, from);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (mon && mt + i < n) {
-                    if constexpr (sizeof(T) == 4) cp_async<4>(to + at(i), from + i * stride);
+                if (i < n) {
+                    if constexpr (sizeof(T) == 4) cp_async<4>(to + i * W, from + i * stride);
                     else wait[i] = from[i * stride];
                 }
         }
     };
-    auto fetch = [&](int k) {
-        if (k < chunks) {
-            const int n = u.len - k * N;
-            const long long t = (long long)k * N;
-            unsigned char *const to = raw(k);
-            copy(reinterpret_cast<DT *>(to + Sh::dt), dp + t * p.dt_ts, p.dt_ts, wd, n);
-            copy(reinterpret_cast<TT *>(to + Sh::x), xp + t * p.x_ts, p.x_ts, wx, n);
-            if (READ && zp) copy(reinterpret_cast<TT *>(to + Sh::z), zp + t * p.z_ts, p.z_ts, wz, n);
+    // Asks for the next chunk: pointers and counts move on by one.
+    const TT *fx_at = xp, *fz_at = zp;
+    const DT *fd_at = dp;
+    const TT *fb_at[NV];
+    if (bc_vec)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = 4 * (id + i * kScanHelpers), w = v % (N * KP);
+            fb_at[i] = v < N * KP ? bp + w / KP * p.B_ts + w % KP : cp + w / KP * p.C_ts + w % KP;
+        }
+    const long long dx = N * p.x_ts, dz = N * p.z_ts, dd = N * p.dt_ts;
+    int ahead = 0, f_at = 0;  // tokens asked for, the ring's next place
+    auto fetch = [&]() {
+        const int n = u.len - ahead;
+        if (n > 0) {
+            unsigned char *const to = shared + f_at;
+            const int mine = mon ? n - mt : 0;
+            copy(reinterpret_cast<DT *>(to + Sh::dt) + at(0), fd_at, p.dt_ts, wd, mine);
+            copy(reinterpret_cast<TT *>(to + Sh::x) + at(0), fx_at, p.x_ts, wx, mine);
+            if (READ && zp) copy(reinterpret_cast<TT *>(to + Sh::z) + at(0), fz_at, p.z_ts, wz, mine);
             if (bc_vec) {
 #pragma unroll
-                for (int i = 0; i < (NB / 4 + kScanHelpers - 1) / kScanHelpers; ++i) {
-                    const int v = 4 * (id + i * kScanHelpers), w = v % (N * KP), s = w / KP;
-                    if (v < NB && s < n)
-                        cp_async<4 * (int)sizeof(TT)>(reinterpret_cast<TT *>(to + Sh::B) + v,
-                                                      v < N * KP ? bp + (t + s) * p.B_ts + w % KP : cp + (t + s) * p.C_ts + w % KP);
+                for (int i = 0; i < NV; ++i) {
+                    const int v = 4 * (id + i * kScanHelpers);
+                    if (v < NB && v % (N * KP) / KP < n) cp_async<4 * (int)sizeof(TT)>(reinterpret_cast<TT *>(to + Sh::B) + v, fb_at[i]);
+                    fb_at[i] += N * (v < N * KP ? p.B_ts : p.C_ts);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     const int v = id + i * kScanHelpers, w = v % (N * KP), s = w / KP;
                     if (v < NB && s < n && w % KP < p.K) {
-                        const TT *from = v < N * KP ? bp + (t + s) * p.B_ts + w % KP : cp + (t + s) * p.C_ts + w % KP;
+                        const TT *from = v < N * KP ? bp + (long long)(ahead + s) * p.B_ts + w % KP : cp + (long long)(ahead + s) * p.C_ts + w % KP;
                         if constexpr (!slow) cp_async<4>(reinterpret_cast<TT *>(to + Sh::B) + v, from);
                         else wbc[i] = *from;
                     }
                 }
             }
+            fx_at += dx;
+            fz_at += dz;
+            fd_at += dd;
         }
         cp_async_commit();
+        ahead += N;
+        f_at = f_at == (R - 1) * Sh::stage ? 0 : f_at + Sh::stage;
     };
-    // what waited for chunk k, to its place
-    auto land = [&](int k) {
-        if (k >= chunks) return;
-        unsigned char *const to = raw(k);
+    // What waited, to its place: that of the chunk asked for last.
+    auto land = [&]() {
+        unsigned char *const to = shared + (f_at == 0 ? R - 1 : f_at / Sh::stage - 1) * Sh::stage;
         if constexpr (!VEC && sizeof(DT) == 2)
 #pragma unroll
             for (int i = 0; i < 4; ++i) reinterpret_cast<DT *>(to + Sh::dt)[at(i)] = wd[i];
@@ -312,55 +328,53 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 4 : KT
                 for (int i = 0; i < NT; ++i)
                     if (id + i * kScanHelpers < NB) reinterpret_cast<TT *>(to + Sh::B)[id + i * kScanHelpers] = wbc[i];
     };
-    float dsum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto convert = [&](int k) {
-        const int n = u.len - k * N;
-        const unsigned char *const from = raw(k);
-        const DT *const rd = reinterpret_cast<const DT *>(from + Sh::dt);
-        const TT *const rx = reinterpret_cast<const TT *>(from + Sh::x);
-        float *const fd = floats(Sh::fd) + (k & 1) * N * W, *const fx = floats(Sh::fx) + (k & 1) * N * W;
-        float d[4], x[4];
+    // four values of this thread's
+    auto four = [&](const auto *from, float (&v)[4]) {
+        using T = std::remove_const_t<std::remove_pointer_t<decltype(from)>>;
         if constexpr (VEC) {
-            Pack<DT, 4> qd;
-            Pack<TT, 4> qx;
-            qd.load(rd + at(0));
-            qx.load(rx + at(0));
+            Pack<T, 4> q;
+            q.load(from + at(0));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                d[i] = qd.get(i);
-                x[i] = qx.get(i);
-            }
+            for (int i = 0; i < 4; ++i) v[i] = q.get(i);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                d[i] = to_f32(rd[at(i)]);
-                x[i] = to_f32(rx[at(i)]);
-            }
+            for (int i = 0; i < 4; ++i) v[i] = to_f32(from[at(i)]);
+        }
+    };
+    auto put4 = [&](float *to, const float (&v)[4]) {
+        if constexpr (VEC) {
+            *reinterpret_cast<float4 *>(to + at(0)) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[at(i)] = v[i];
+        }
+    };
+    float dsum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    // d and d x of raw values; n: the chunk's tokens
+    auto steps = [&](float (&d)[4], float (&x)[4], int n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] += bias[i];
+        if (p.softplus)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = softplus<TT>(d[i]);
+        if (n < N || width < W) {  // nothing there: states stay as they are
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (!mon || mt + (VEC ? 0 : i) >= n) d[i] = x[i] = 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            d[i] += bias[i];
-            if (p.softplus) d[i] = softplus<TT>(d[i]);
-            if (!mon || mt + (VEC ? 0 : i) >= n) d[i] = x[i] = 0.0f;
             x[i] *= d[i];
             if (!READ) dsum[i] += d[i];
         }
-        if constexpr (VEC) {
-            *reinterpret_cast<float4 *>(fd + at(0)) = make_float4(d[0], d[1], d[2], d[3]);
-            *reinterpret_cast<float4 *>(fx + at(0)) = make_float4(x[0], x[1], x[2], x[3]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                fd[at(i)] = d[i];
-                fx[at(i)] = x[i];
-            }
-        }
-        // B and C: this thread's own values again; states past K are 0
+    };
+    // B and C in float32: this thread's own values again; states past K are 0
+    auto states = [&](const unsigned char *from, int half, int n) {
         const TT *const rb = reinterpret_cast<const TT *>(from + Sh::B);
-        auto place = [&](int v) { return v < N * KP ? floats(Sh::fB) + (k & 1) * N * KP + v : floats(Sh::fC) + (k & 1) * N * KP + v - N * KP; };
+        auto place = [&](int v) { return v < N * KP ? floats(Sh::fB) + half * N * KP + v : floats(Sh::fC) + half * N * KP + v - N * KP; };
         if (bc_vec) {
 #pragma unroll
-            for (int i = 0; i < (NB / 4 + kScanHelpers - 1) / kScanHelpers; ++i) {
+            for (int i = 0; i < NV; ++i) {
                 const int v = 4 * (id + i * kScanHelpers);
                 if (v < NB) {
                     Pack<TT, 4> q;
@@ -377,73 +391,73 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 4 : KT
             }
         }
     };
-    auto finish = [&](int k) {
-        const int n = u.len - k * N;
-        const TT *const rx = reinterpret_cast<const TT *>(raw(k) + Sh::x), *const rz = reinterpret_cast<const TT *>(raw(k) + Sh::z);
-        const float *const fy = floats(Sh::fy) + (k & 1) * NW * N * W;
-        float y[4], x[4], z[4];
-        if constexpr (VEC) {
-            Pack<TT, 4> qx, qz;
-            qx.load(rx + at(0));
-            if (zp) qz.load(rz + at(0));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = qx.get(i);
-                z[i] = qz.get(i);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = to_f32(rx[at(i)]);
-                z[i] = to_f32(rz[at(i)]);
-            }
-        }
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            if constexpr (VEC) {
-                const float4 q = *reinterpret_cast<const float4 *>(fy + w * N * W + at(0));
-                y[0] = w ? y[0] + q.x : q.x;
-                y[1] = w ? y[1] + q.y : q.y;
-                y[2] = w ? y[2] + q.z : q.z;
-                y[3] = w ? y[3] + q.w : q.w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] = w ? y[i] + fy[w * N * W + at(i)] : fy[at(i)];
-            }
-        }
-        TT *const to = op + (long long)k * N * p.o_ts;
-        Pack<TT, 4> o;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            y[i] = fmaf(D[i], x[i], y[i]);
-            if (zp) y[i] *= silu(z[i]);
-            o.set(i, y[i]);
-        }
-        if constexpr (VEC) {
-            if (mon && mt < n) o.store(to);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (mon && mt + i < n) to[i * p.o_ts] = o.u.e[i];
-        }
-    };
-    // chunk k + D is asked for in turn k, D = R - 1; the ring then holds chunks k - 1 ... k + D - 1
+    // Turn k finishes chunk k - 1, makes chunk k + 1 ready and asks for chunk k + Dist: the ring
+    // holds chunks k - 1 ... k + Dist - 1.
     constexpr int Dist = R - 1;
     for (int k = 0; k < Dist; ++k) {
-        fetch(k);
-        land(k);
+        fetch();
+        land();
     }
     cp_async_wait<Dist - 1>();
-    convert(0);
+    {
+        float d[4], x[4];
+        four(reinterpret_cast<const DT *>(shared + Sh::dt), d);
+        four(reinterpret_cast<const TT *>(shared + Sh::x), x);
+        steps(d, x, u.len);
+        put4(floats(Sh::fd), d);
+        put4(floats(Sh::fx), x);
+        states(shared, 0, u.len);
+    }
     __syncthreads();
+    int done_at = (R - 1) * Sh::stage, next_at = Sh::stage;  // chunks k - 1 and k + 1 in the ring
+    TT *out = READ ? op - (long long)N * p.o_ts : nullptr;
+    const long long dout = N * p.o_ts;
     for (int k = 0; k <= chunks; ++k) {
-        if (READ && k > 0) finish(k - 1);
-        if (k > 0) land(k + Dist - 1);
-        if (k + 1 < chunks) {
-            cp_async_wait<Dist - 2>();
-            convert(k + 1);
+        if (k > 0) land();
+        cp_async_wait<Dist - 2>();
+        const int half = (k + 1) & 1;  // both neighbours' half of the buffers in pairs
+        float d[4], x[4], rx[4], rz[4], y[4];
+        const unsigned char *const next = shared + next_at, *const done = shared + done_at;
+        four(reinterpret_cast<const DT *>(next + Sh::dt), d);
+        four(reinterpret_cast<const TT *>(next + Sh::x), x);
+        if constexpr (READ) {
+            four(reinterpret_cast<const TT *>(done + Sh::x), rx);
+            if (zp) four(reinterpret_cast<const TT *>(done + Sh::z), rz);
+            const float *const fy = floats(Sh::fy) + half * NW * N * W;
+            four(fy, y);
+#pragma unroll
+            for (int w = 1; w < NW; ++w) {
+                float q[4];
+                four(fy + w * N * W, q);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] += q[i];
+            }
         }
-        fetch(k + Dist);
+        steps(d, x, u.len - (k + 1) * N);
+        put4(floats(Sh::fd) + half * N * W, d);
+        put4(floats(Sh::fx) + half * N * W, x);
+        states(next, half, u.len - (k + 1) * N);
+        if constexpr (READ) {
+            Pack<TT, 4> o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[i] = fmaf(D[i], rx[i], y[i]);
+                if (zp) y[i] *= silu(rz[i]);
+                o.set(i, y[i]);
+            }
+            const int n = mon && k > 0 ? u.len - (k - 1) * N - mt : 0;
+            if constexpr (VEC) {
+                if (n > 0) o.store(out);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i < n) out[i * p.o_ts] = o.u.e[i];
+            }
+            out += dout;
+        }
+        fetch();
+        done_at = done_at == (R - 1) * Sh::stage ? 0 : done_at + Sh::stage;
+        next_at = next_at == (R - 1) * Sh::stage ? 0 : next_at + Sh::stage;
         __syncthreads();
     }
     if (first) {

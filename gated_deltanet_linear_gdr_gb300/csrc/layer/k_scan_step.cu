@@ -1,217 +1,248 @@
 // Selective scan of single tokens: every state goes in and out once, with a
-// handful of operations on it: HBM bound.  A warp is 4 * (32 / LK) channels of one
-// row, dealt to its lanes as in k_scan.cuh; all of a lane's states and rates are
-// asked for before anything else, and nothing goes through shared memory.
+// handful of operations on it: HBM bound.  A block is 128 channels of some rows.
+// Its four warps share the states, KT each, four channels a lane, so that a warp
+// moves whole runs of 512 bytes.  What belongs to the channels (their places, the
+// rates, the bias) is worked out once for all the block's rows; the next row's
+// states are on their way while one is worked on.  The partial readouts meet in
+// shared memory, and every thread finishes one channel.
 #include "scan_device.cuh"
 
 namespace gdr {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kStepTile = 128;  // a block's channels, and its threads
+constexpr int kStepRows = 32;   // a block's rows at most
 
-template <typename TT, typename DT, int KT, int LK, bool VEC>
-__global__ void __launch_bounds__(32 * kWarps) k_scan_step(const __grid_constant__ ScanParams p, int tiles, unsigned units) {
-    constexpr int W = 4 * (32 / LK), CH = 4;
-    const int lane = threadIdx.x & 31;
-    const unsigned unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (unit >= units) return;
-    const unsigned all = (unsigned)(p.nk * tiles), row = unit / all, tg = unit - row * all;
-    const int g = (int)(tg / (unsigned)tiles), tile = (int)(tg - (unsigned)g * (unsigned)tiles);
-    const int group = p.r * p.V, c0 = tile * W, width = min(W, group - c0);
-    const int lk = lane % LK, cg = lane / LK;
-    // this lane's four channels, and the one it finishes
-    int chan[CH], chead[CH];
-    bool on[CH];
-#pragma unroll
-    for (int e = 0; e < CH; ++e) {
-        const int c = c0 + cg * 4 + e;
-        on[e] = cg * 4 + e < width;
-        chead[e] = on[e] ? g * p.r + c / p.V : 0;
-        chan[e] = on[e] ? c % p.V : 0;
+// Four neighbouring values as they came, one vector (VEC) or one by one, taken apart only where
+// they are used: a load that is on its way for long must not be waited for by what unpacks it.
+template <typename T, bool VEC> struct Four;
+template <> struct Four<uint16_t, true> {
+    uint2 v;
+    __device__ __forceinline__ void load(const uint16_t *p) { v = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ float get(int i) const {
+        const unsigned w = i < 2 ? v.x : v.y;
+        return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
     }
-    int mj = chan[0], mh = chead[0];
-    bool mon = on[0];
-#pragma unroll
-    for (int e = 1; e < CH; ++e)
-        if ((lk & 3) == e) {
-            mj = chan[e];
-            mh = chead[e];
-            mon = on[e];
-        }
-    mon = mon && lk < 4;
-
-    float A[KT][CH];
-#pragma unroll
-    for (int i = 0; i < KT; ++i) {
-        const int k = lk * KT + i;
-#pragma unroll
-        for (int e = 0; e < CH; ++e) A[i][e] = 0.0f;
-        if (k >= p.K) continue;
-        if (VEC && p.a_vec) {
-            if (on[0]) {
-                Pack<float, 4> q;
-                q.load(p.A + chead[0] * p.a_hs + k * p.a_ks + chan[0]);
-#pragma unroll
-                for (int e = 0; e < CH; ++e) A[i][e] = q.get(e);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < CH; ++e)
-                if (on[e]) A[i][e] = p.A[chead[e] * p.a_hs + k * p.a_ks + chan[e] * p.a_vs];
-        }
-    }
-    ScanUnit u;
-    if (!scan_row(p, (int)row, tg == 0 && lane == 0, u)) return;
-    TT *const out = static_cast<TT *>(p.out) + u.t0 * p.o_ts + (long long)mh * p.o_hs + mj;
-    if (u.slot < 0) {
-        if (mon) *out = TT(0);
-        return;
-    }
-    float S[KT][CH];
-    long long at[CH];
-#pragma unroll
-    for (int e = 0; e < CH; ++e) at[e] = (long long)u.slot * p.st_slot + (long long)chead[e] * p.st_head + chan[e];
-#pragma unroll
-    for (int i = 0; i < KT; ++i) {
-        const int k = lk * KT + i;
-#pragma unroll
-        for (int e = 0; e < CH; ++e) S[i][e] = 0.0f;
-        if (k >= p.K) continue;
-        if constexpr (VEC) {
-            if (!on[0]) continue;
-            if (p.st_bf16) {
-                Pack<uint16_t, 4> q;
-                q.load(static_cast<const uint16_t *>(p.state) + at[0] + k * p.st_k);
-#pragma unroll
-                for (int e = 0; e < CH; ++e) S[i][e] = q.get(e);
-            } else {
-                Pack<float, 4> q;
-                q.load(static_cast<const float *>(p.state) + at[0] + k * p.st_k);
-#pragma unroll
-                for (int e = 0; e < CH; ++e) S[i][e] = q.get(e);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < CH; ++e)
-                if (on[e])
-                    S[i][e] = p.st_bf16 ? to_f32(static_cast<const uint16_t *>(p.state)[at[e] + k * p.st_k])
-                                        : static_cast<const float *>(p.state)[at[e] + k * p.st_k];
-        }
-    }
-    // the token
-    const TT *const xp = static_cast<const TT *>(p.x) + u.t0 * p.x_ts;
-    const DT *const dp = static_cast<const DT *>(p.dt) + u.t0 * p.dt_ts;
-    const TT *const bp = static_cast<const TT *>(p.B) + u.t0 * p.B_ts + (long long)g * p.B_hs;
-    const TT *const cp = static_cast<const TT *>(p.C) + u.t0 * p.C_ts + (long long)g * p.C_hs;
-    float d[CH], x[CH], B[KT], C[KT];
-#pragma unroll
-    for (int e = 0; e < CH; ++e) d[e] = x[e] = 0.0f;
-    if (VEC && p.dt_es) {
-        if (on[0]) {
-            Pack<DT, 4> q;
-            q.load(dp + (long long)chead[0] * p.dt_hs + chan[0]);
-#pragma unroll
-            for (int e = 0; e < CH; ++e) d[e] = q.get(e);
-        }
+};
+template <> struct Four<float, true> {
+    float4 v;
+    __device__ __forceinline__ void load(const float *p) { v = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ float get(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+};
+template <typename T> struct Four<T, false> {
+    T e[4];
+    __device__ __forceinline__ float get(int i) const { return to_f32(e[i]); }
+};
+template <typename T, bool VEC>
+__device__ __forceinline__ void gather4(const T *base, const long long (&at)[4], const bool (&on)[4], Four<T, VEC> &v) {
+    if constexpr (VEC) {
+        if (on[0]) v.load(base + at[0]);
     } else {
 #pragma unroll
-        for (int e = 0; e < CH; ++e)
-            if (on[e]) d[e] = to_f32(dp[(long long)chead[e] * p.dt_hs + chan[e] * p.dt_es]);
+        for (int e = 0; e < 4; ++e)
+            if (on[e]) v.e[e] = base[at[e]];
     }
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void scatter4(T *base, const long long (&at)[4], const bool (&on)[4], const float (&v)[4]) {
     if constexpr (VEC) {
         if (on[0]) {
-            Pack<TT, 4> q;
-            q.load(xp + (long long)chead[0] * p.x_hs + chan[0]);
+            Pack<T, 4> q;
 #pragma unroll
-            for (int e = 0; e < CH; ++e) x[e] = q.get(e);
+            for (int e = 0; e < 4; ++e) q.set(e, v[e]);
+            q.store(base + at[0]);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < CH; ++e)
-            if (on[e]) x[e] = to_f32(xp[(long long)chead[e] * p.x_hs + chan[e]]);
+        for (int e = 0; e < 4; ++e)
+            if (on[e]) base[at[e]] = from_f32<T>(v[e]);
     }
-    if (p.bias)
-#pragma unroll
-        for (int e = 0; e < CH; ++e)
-            if (on[e]) d[e] += p.bias[chead[e] * p.b_hs + chan[e] * p.b_vs];
-#pragma unroll
-    for (int i = 0; i < KT; ++i) {
-        const int k = lk * KT + i;
-        B[i] = k < p.K ? to_f32(bp[k]) : 0.0f;
-        C[i] = k < p.K && p.out ? to_f32(cp[k]) : 0.0f;
-    }
-    const float D = mon && p.D ? p.D[mh * p.d_hs + mj * p.d_vs] : 0.0f;
-    const float mx = mon ? to_f32(xp[(long long)mh * p.x_hs + mj]) : 0.0f;
-    const bool gated = mon && p.z;
-    const float z = gated ? to_f32(static_cast<const TT *>(p.z)[u.t0 * p.z_ts + (long long)mh * p.z_hs + mj]) : 0.0f;
+}
 
-    float y[CH];
-#pragma unroll
-    for (int e = 0; e < CH; ++e) {
-        const float de = p.softplus ? softplus<TT>(d[e]) : d[e], in = de * x[e];
-        y[e] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < KT; ++i) {
-            S[i][e] = fmaf(decay<TT>(de * rate<TT>(A[i][e])), S[i][e], in * B[i]);
-            y[e] = fmaf(C[i], S[i][e], y[e]);
+// A row as the block's setup leaves it: where its token's values and its states begin.
+template <typename TT, typename DT, typename ST> struct StepRow {
+    ST *state;
+    const DT *dt;
+    const TT *x, *z, *B, *C;
+    TT *out;
+    int todo;  // 0: nothing, 1: zeros, 2: the token, 3: and its states are kept
+};
+
+// VEC: four channels are a vector everywhere, and so are four states of B and C; K is a multiple of KT.
+template <typename TT, typename DT, typename ST, int KT, bool VEC>
+__global__ void __launch_bounds__(kStepTile, KT <= 4 ? 4 : KT <= 8 ? 3 : 1)
+    k_scan_step(const __grid_constant__ ScanParams p, int tiles, int rows) {
+    __shared__ __align__(16) float part[2][4][kStepTile];
+    __shared__ StepRow<TT, DT, ST> info[kStepRows];
+    constexpr bool AHEAD = VEC && KT <= 8;  // there are registers for two rows' states
+    constexpr int KV = KT / 4;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned all = (unsigned)(p.nk * tiles), block = blockIdx.x / all, tg = blockIdx.x - block * all;
+    const int g = (int)(tg / (unsigned)tiles), tile = (int)(tg - (unsigned)g * (unsigned)tiles);
+    const int c0 = tile * kStepTile, width = min(kStepTile, p.r * p.V - c0);
+    const int b0 = (int)block * rows, nrows = min(rows, p.batch - b0);
+    if (tid < nrows) {
+        ScanUnit u;
+        StepRow<TT, DT, ST> r;
+        r.todo = 0;
+        if (scan_row(p, b0 + tid, tg == 0, u)) {
+            r.todo = u.slot < 0 ? 1 : u.kept > 0 ? 3 : 2;
+            r.state = static_cast<ST *>(p.state) + (u.slot < 0 ? 0 : u.slot * p.st_slot);
+            r.dt = static_cast<const DT *>(p.dt) + u.t0 * p.dt_ts;
+            r.x = static_cast<const TT *>(p.x) + u.t0 * p.x_ts;
+            r.z = static_cast<const TT *>(p.z) + (p.z ? u.t0 * p.z_ts : 0);
+            r.B = static_cast<const TT *>(p.B) + u.t0 * p.B_ts + (long long)g * p.B_hs;
+            r.C = static_cast<const TT *>(p.C) + (p.C ? u.t0 * p.C_ts + (long long)g * p.C_hs : 0);
+            r.out = static_cast<TT *>(p.out) + (p.out ? u.t0 * p.o_ts : 0);
         }
+        info[tid] = r;
     }
-    if (u.kept > 0) {
+    // this lane's four channels, and the one this thread finishes
+    const int have = min(KT, p.K - warp * KT);  // states that there are, 0 or less: none
+    const long long k0 = (long long)warp * KT;
+    long long st_at[4], x_at[4], d_at[4];
+    bool on[4];
+    float A[KT][4], bias[4];
 #pragma unroll
-        for (int i = 0; i < KT; ++i) {
-            const int k = lk * KT + i;
-            if (k >= p.K) continue;
-            if constexpr (VEC) {
-                if (!on[0]) continue;
-                if (p.st_bf16) {
-                    Pack<uint16_t, 4> q;
+    for (int e = 0; e < 4; ++e) {
+        on[e] = lane * 4 + e < width;
+        const int c = on[e] ? c0 + lane * 4 + e : 0, q = c / p.V, h = g * p.r + q, j = c - q * p.V;
+        st_at[e] = k0 * p.st_k + h * p.st_head + j;
+        x_at[e] = h * p.x_hs + j;
+        d_at[e] = h * p.dt_hs + j * p.dt_es;
+        bias[e] = p.bias && on[e] ? p.bias[h * p.b_hs + j * p.b_vs] : 0.0f;
+        const float *const ap = p.A + k0 * p.a_ks + h * p.a_hs + j * p.a_vs;
 #pragma unroll
-                    for (int e = 0; e < CH; ++e) q.set(e, S[i][e]);
-                    q.store(static_cast<uint16_t *>(p.state) + at[0] + k * p.st_k);
+        for (int i = 0; i < KT; ++i) A[i][e] = i < have && on[e] ? rate<TT>(ap[i * p.a_ks]) : 0.0f;
+    }
+    const bool mon = tid < width && p.out, gate = mon && p.z;
+    const int mq = mon ? (c0 + tid) / p.V : 0, mh = g * p.r + mq, mj = mon ? c0 + tid - mq * p.V : 0;
+    const long long mx_at = mh * p.x_hs + mj, mz_at = mh * p.z_hs + mj, mo_at = mh * p.o_hs + mj;
+    const float D = mon && p.D ? p.D[mh * p.d_hs + mj * p.d_vs] : 0.0f;
+    __syncthreads();
+
+    struct Row {
+        Four<ST, VEC> S[KT];
+        Four<DT, VEC> d;
+        Four<TT, VEC> x, B[KV], C[KV];
+        TT mx, mz;
+    };
+    auto ask = [&](int r, Row &v) {
+        const StepRow<TT, DT, ST> &w = info[r];
+        if (w.todo < 2) return;
+        if (have > 0) {
+#pragma unroll
+            for (int i = 0; i < KT; ++i)
+                if (VEC || i < have) gather4(w.state + i * p.st_k, st_at, on, v.S[i]);
+            gather4(w.dt, d_at, on, v.d);
+            gather4(w.x, x_at, on, v.x);
+            const TT *const b = w.B + k0, *const c = w.C + k0;
+#pragma unroll
+            for (int i = 0; i < KV; ++i) {
+                if constexpr (VEC) {
+                    v.B[i].load(b + 4 * i);
+                    if (p.out) v.C[i].load(c + 4 * i);
                 } else {
-                    Pack<float, 4> q;
 #pragma unroll
-                    for (int e = 0; e < CH; ++e) q.set(e, S[i][e]);
-                    q.store(static_cast<float *>(p.state) + at[0] + k * p.st_k);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < CH; ++e) {
-                    if (!on[e]) continue;
-                    if (p.st_bf16) static_cast<uint16_t *>(p.state)[at[e] + k * p.st_k] = from_f32<uint16_t>(S[i][e]);
-                    else static_cast<float *>(p.state)[at[e] + k * p.st_k] = S[i][e];
+                    for (int k = 0; k < 4; ++k)
+                        if (4 * i + k < have) {
+                            v.B[i].e[k] = b[4 * i + k];
+                            if (p.out) v.C[i].e[k] = c[4 * i + k];
+                        }
                 }
             }
         }
+        if (mon) v.mx = w.x[mx_at];
+        if (gate) v.mz = w.z[mz_at];
+    };
+    auto turn = [&](int r, const Row &v) {
+        const StepRow<TT, DT, ST> &w = info[r];
+        if (w.todo < 2) {
+            if (w.todo == 1 && mon) w.out[mo_at] = TT(0);
+            return;
+        }
+        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (have > 0) {
+            float S[KT][4], d[4], in[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                d[e] = v.d.get(e) + bias[e];
+                if (p.softplus) d[e] = softplus<TT>(d[e]);
+                in[e] = d[e] * v.x.get(e);
+            }
+#pragma unroll
+            for (int i = 0; i < KT; ++i) {
+                if (!VEC && i >= have) continue;
+                const float B = v.B[i / 4].get(i % 4), C = v.C[i / 4].get(i % 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    S[i][e] = fmaf(decay<TT>(d[e] * A[i][e]), v.S[i].get(e), in[e] * B);
+                    y[e] = fmaf(C, S[i][e], y[e]);  // of no meaning, and not used, where there are no outputs
+                }
+            }
+            if (w.todo == 3) {
+#pragma unroll
+                for (int i = 0; i < KT; ++i)
+                    if (VEC || i < have) scatter4<VEC>(w.state + i * p.st_k, st_at, on, S[i]);
+            }
+        }
+        if (!p.out) return;
+        *reinterpret_cast<float4 *>(&part[r & 1][warp][lane * 4]) = make_float4(y[0], y[1], y[2], y[3]);
+        __syncthreads();
+        if (!mon) return;
+        const float (&q)[4][kStepTile] = part[r & 1];
+        float o = fmaf(D, to_f32(v.mx), (q[0][tid] + q[1][tid]) + (q[2][tid] + q[3][tid]));
+        if (gate) o *= silu(to_f32(v.mz));
+        w.out[mo_at] = from_f32<TT>(o);
+    };
+    if constexpr (AHEAD) {
+        Row v[2];
+        ask(0, v[0]);
+        for (int r = 0; r < nrows; ++r) {
+            if (r + 1 < nrows) ask(r + 1, v[1]);
+            turn(r, v[0]);
+            if (++r >= nrows) break;
+            if (r + 1 < nrows) ask(r + 1, v[0]);
+            turn(r, v[1]);
+        }
+    } else {
+        Row v;
+        for (int r = 0; r < nrows; ++r) {
+            ask(r, v);
+            turn(r, v);
+        }
     }
-    float v = fmaf(D, mx, scan_readout<LK>(y, lk));
-    if (gated) v *= silu(z);
-    if (mon && p.out) *out = from_f32<TT>(v);
 }
 
-template <typename TT, typename DT, int KT, int LK> cudaError_t go(const ScanParams &p, bool vec, cudaStream_t s) {
-    constexpr int W = 4 * (32 / LK);
-    const long long tiles = ((long long)p.r * p.V + W - 1) / W, units = (long long)p.batch * p.nk * tiles;
-    if (units >= 1ll << 31) return cudaErrorInvalidConfiguration;
-    const unsigned blocks = (unsigned)((units + kWarps - 1) / kWarps);
-    if (vec) k_scan_step<TT, DT, KT, LK, true><<<blocks, 32 * kWarps, 0, s>>>(p, (int)tiles, (unsigned)units);
-    else k_scan_step<TT, DT, KT, LK, false><<<blocks, 32 * kWarps, 0, s>>>(p, (int)tiles, (unsigned)units);
+template <typename TT, typename DT, typename ST, int KT, bool VEC> cudaError_t go(const ScanParams &p, cudaStream_t s) {
+    const long long tiles = ((long long)p.r * p.V + kStepTile - 1) / kStepTile, heads = p.nk * tiles;
+    // as many rows a block as leaves each multiprocessor its blocks once over
+    const long long at_once = 152 * (KT <= 4 ? 4 : KT <= 8 ? 3 : 1);
+    long long rows = (p.batch * heads + at_once - 1) / at_once;
+    if (rows > kStepRows) rows = kStepRows;
+    const long long blocks = (p.batch + rows - 1) / rows * heads;
+    if (blocks >= 1ll << 31) return cudaErrorInvalidConfiguration;
+    k_scan_step<TT, DT, ST, KT, VEC><<<(unsigned)blocks, kStepTile, 0, s>>>(p, (int)tiles, (int)rows);
     return cudaGetLastError();
 }
 
-// States a lane and lanes a channel, by K.
-template <typename TT, typename DT> cudaError_t states(const ScanParams &p, bool vec, cudaStream_t s) {
-    if (p.K <= 16) return go<TT, DT, 4, 4>(p, vec, s);
-    if (p.K <= 32) return go<TT, DT, 8, 4>(p, vec, s);
-    if (p.K <= 64) return go<TT, DT, 8, 8>(p, vec, s);
-    return go<TT, DT, 8, 16>(p, vec, s);
+// States a warp has, by K.
+template <typename TT, typename DT, typename ST, bool VEC> cudaError_t states(const ScanParams &p, cudaStream_t s) {
+    if (p.K <= 16) return go<TT, DT, ST, 4, VEC>(p, s);
+    if (p.K <= 32) return go<TT, DT, ST, 8, VEC>(p, s);
+    if (p.K <= 64) return go<TT, DT, ST, 16, VEC>(p, s);
+    return go<TT, DT, ST, 32, VEC>(p, s);
+}
+template <typename TT, typename DT> cudaError_t pool(const ScanParams &p, bool vec, cudaStream_t s) {
+    if (p.st_bf16) return vec ? states<TT, DT, uint16_t, true>(p, s) : states<TT, DT, uint16_t, false>(p, s);
+    return vec ? states<TT, DT, float, true>(p, s) : states<TT, DT, float, false>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_scan_step(const ScanParams &p, bool tok_bf16, bool dt_bf16, bool vec, cudaStream_t s) {
-    if (!tok_bf16) return states<float, float>(p, vec, s);
-    return dt_bf16 ? states<uint16_t, uint16_t>(p, vec, s) : states<uint16_t, float>(p, vec, s);
+    if (!tok_bf16) return pool<float, float>(p, vec, s);
+    return dt_bf16 ? pool<uint16_t, uint16_t>(p, vec, s) : pool<uint16_t, float>(p, vec, s);
 }
 
 }  // namespace gdr

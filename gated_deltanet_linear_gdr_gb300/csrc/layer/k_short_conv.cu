@@ -2,8 +2,8 @@
 //
 //     y[j] = act(bias + sum_m w[m] xe[j + m]),  xe = (the slot's last inputs, the row's inputs)
 //
-// A thread owns VE neighbouring channels (a 16-byte vector of tokens, or one
-// channel where rows are not such vectors) and walks along tokens with the
+// A thread owns VE neighbouring channels (four as a vector, or one where rows are
+// not such vectors) and walks along tokens with the
 // last width-1 inputs in registers, so that an input is read once and a result
 // written once.  A few operations a byte: HBM bound; what counts is bytes in
 // flight, so kAhead tokens are asked for before the first is used.
@@ -16,17 +16,14 @@
 // token, past the end of its run where they lie there.  Its threads also write
 // the slot, from the row's last inputs: nobody else touches it, so old inputs
 // are not overwritten before they are used, in one launch.
-#include "../gdr_device.cuh"
-#include "layer_internal.h"
+#include "scan_device.cuh"
 
 namespace gdr {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kAhead = 8;      // tokens on their way
+constexpr int kAhead = 8;      // tokens of a batch
 constexpr int kShortRow = 16;  // rows up to here are a block's unit
-
-__device__ __forceinline__ float silu(float y) { return __fdividef(y, 1.0f + __expf(-y)); }
 
 struct ConvRow {
     long long lo, hi;  // its tokens
@@ -191,18 +188,44 @@ template <typename TT, int W, int VE> struct ConvThread {
         o.store(to);
     }
 
+    __device__ __forceinline__ void ask(Pack<TT, VE> (&in)[kAhead], const TT *&from) const {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            in[i].load(from);
+            from += p.x_ts;
+        }
+    }
+    __device__ __forceinline__ void tokens(const Pack<TT, VE> (&in)[kAhead], TT *&to) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            token(in[i], to);
+            to += p.o_ts;
+        }
+    }
+    // Two batches of kAhead tokens in turn: one is on its way while the other is worked on.
     __device__ __forceinline__ void run(long long s, long long e) {
         const TT *from = x(s);
         TT *to = out(s);
-        long long n = e - s;
-        for (; n >= kAhead; n -= kAhead) {
-            Pack<TT, VE> in[kAhead];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) in[i].load(from + i * p.x_ts);
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) token(in[i], to + i * p.o_ts);
-            from += kAhead * p.x_ts;
-            to += kAhead * p.o_ts;
+        int n = (int)(e - s);
+        Pack<TT, VE> a[kAhead], b[kAhead];
+        if (n >= kAhead) {
+            ask(a, from);
+            for (;;) {
+                n -= kAhead;
+                if (n < kAhead) {
+                    tokens(a, to);
+                    break;
+                }
+                ask(b, from);
+                tokens(a, to);
+                n -= kAhead;
+                if (n < kAhead) {
+                    tokens(b, to);
+                    break;
+                }
+                ask(a, from);
+                tokens(b, to);
+            }
         }
         for (; n > 0; --n) {
             Pack<TT, VE> in;
@@ -210,6 +233,22 @@ template <typename TT, int W, int VE> struct ConvThread {
             token(in, to);
             from += p.x_ts;
             to += p.o_ts;
+        }
+    }
+    // A short row, four tokens at a time.
+    __device__ __forceinline__ void short_run(long long s, int n) {
+        const TT *from = x(s);
+        TT *to = out(s);
+        for (; n > 0; n -= 4) {
+            Pack<TT, VE> in[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) in[i].load(from + i * p.x_ts);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) token(in[i], to + i * p.o_ts);
+            from += 4 * p.x_ts;
+            to += 4 * p.o_ts;
         }
     }
     __device__ __forceinline__ void clear(long long s, long long e) {
@@ -220,13 +259,15 @@ template <typename TT, int W, int VE> struct ConvThread {
     }
 };
 
-template <typename TT, int W, int VE>
+// ROWS: a block takes a row's channels; else a run of tokens.
+template <typename TT, int W, int VE, bool ROWS>
 __global__ void __launch_bounds__(kThreads) k_short_conv(const __grid_constant__ ConvOpParams p) {
     const unsigned block = blockIdx.x / (unsigned)p.tiles, tile = blockIdx.x - block * (unsigned)p.tiles;
     const int tid = threadIdx.x, c0 = (int)(tile * kThreads + threadIdx.x) * VE;
     const bool on = c0 < p.channels;
     ConvThread<TT, W, VE> th(p, c0);
-    if (p.rows_form) {
+    if constexpr (ROWS) {
+        if (on && p.out) th.weights();
         const ConvRow r = conv_row(p, (int)block);
         if (r.problem && tile == 0 && tid == 0) flag(p.status, r.problem);
         if (!on || !r.inside) return;
@@ -234,51 +275,51 @@ __global__ void __launch_bounds__(kThreads) k_short_conv(const __grid_constant__
             if (p.out) th.clear(r.lo, r.hi);
             return;
         }
-        if (p.out) th.weights();
         th.begin(r);
-        if (p.out) th.run(r.lo, r.hi);
+        if (p.out) th.short_run(r.lo, (int)(r.hi - r.lo));
         return;
-    }
-    if (blockIdx.x == 0)  // one block looks at every row
-        for (int b = tid; b < p.batch; b += kThreads) {
-            const unsigned problem = conv_row(p, b).problem;
-            if (problem) flag(p.status, problem);
+    } else {
+        if (blockIdx.x == 0)  // one block looks at every row
+            for (int b = tid; b < p.batch; b += kThreads) {
+                const unsigned problem = conv_row(p, b).problem;
+                if (problem) flag(p.status, problem);
+            }
+        const long long t0 = (long long)block * p.run, t1 = t0 + p.run < p.T ? t0 + p.run : p.T;
+        // the row of the first token: the last one that does not begin behind it
+        int b = -1;
+        for (int i = 0; i <= p.batch; i += kThreads) {
+            const bool before = i + tid <= p.batch && p.offsets[i + tid] <= t0;
+            b += __syncthreads_count(before);
         }
-    const long long t0 = (long long)block * p.run, t1 = t0 + p.run < p.T ? t0 + p.run : p.T;
-    // the row of the first token: the last one that does not begin behind it
-    int b = -1;
-    for (int i = 0; i <= p.batch; i += kThreads) {
-        const bool before = i + tid <= p.batch && p.offsets[i + tid] <= t0;
-        b += __syncthreads_count(before);
-    }
-    if (!on) return;
-    th.weights();
-    for (b = b < 0 ? 0 : b; b < p.batch && p.offsets[b] < t1; ++b) {
-        const ConvRow r = conv_row(p, b);
-        const bool first = r.lo >= t0;  // the row begins in this run
-        const long long head = r.lo + (W - 1);
-        const long long s = first ? r.lo : (t0 > head ? t0 : head), end = first && head > t1 ? head : t1;
-        const long long e = r.hi < end ? r.hi : end;
-        if (!r.inside || s >= e) continue;
-        if (r.slot < 0) {
-            th.clear(s, e);
-            continue;
+        if (!on) return;
+        th.weights();
+        for (b = b < 0 ? 0 : b; b < p.batch && p.offsets[b] < t1; ++b) {
+            const ConvRow r = conv_row(p, b);
+            const bool first = r.lo >= t0;  // the row begins in this run
+            const long long head = r.lo + (W - 1);
+            const long long s = first ? r.lo : (t0 > head ? t0 : head), end = first && head > t1 ? head : t1;
+            const long long e = r.hi < end ? r.hi : end;
+            if (!r.inside || s >= e) continue;
+            if (r.slot < 0) {
+                th.clear(s, e);
+                continue;
+            }
+            if (first) th.begin(r);
+            else th.enter(s);
+            th.run(s, e);
         }
-        if (first) th.begin(r);
-        else th.enter(s);
-        th.run(s, e);
     }
 }
 
 template <typename TT, int W> cudaError_t go(ConvOpParams p, cudaStream_t s) {
-    constexpr int VE = 16 / (int)sizeof(TT);
+    constexpr int VE = 4;
     const int wide = (p.vec ? VE : 1) * kThreads;
     p.tiles = (p.channels + wide - 1) / wide;
     // Rows' lengths as far as the caller bounds them: a block a row where none is longer than
     // kShortRow tokens, and where only states move.
-    p.rows_form = !p.out || (p.max_len > 0 && p.max_len <= kShortRow);
+    const bool rows = !p.out || (p.max_len > 0 && p.max_len <= kShortRow);
     long long blocks = p.batch;
-    if (!p.rows_form) {
+    if (!rows) {
         // runs of up to 64 tokens, shorter ones where they would leave multiprocessors without work
         p.run = 64;
         while (p.run > 8 && (p.T + p.run - 1) / p.run * p.tiles < 152 * 12) p.run /= 2;
@@ -287,8 +328,14 @@ template <typename TT, int W> cudaError_t go(ConvOpParams p, cudaStream_t s) {
     blocks *= p.tiles;
     if (blocks <= 0) return cudaSuccess;
     if (blocks >= (1ll << 31)) return cudaErrorInvalidConfiguration;
-    if (p.vec) k_short_conv<TT, W, VE><<<(unsigned)blocks, kThreads, 0, s>>>(p);
-    else k_short_conv<TT, W, 1><<<(unsigned)blocks, kThreads, 0, s>>>(p);
+    const unsigned n = (unsigned)blocks;
+    if (p.vec) {
+        if (rows) k_short_conv<TT, W, VE, true><<<n, kThreads, 0, s>>>(p);
+        else k_short_conv<TT, W, VE, false><<<n, kThreads, 0, s>>>(p);
+    } else {
+        if (rows) k_short_conv<TT, W, 1, true><<<n, kThreads, 0, s>>>(p);
+        else k_short_conv<TT, W, 1, false><<<n, kThreads, 0, s>>>(p);
+    }
     return cudaGetLastError();
 }
 

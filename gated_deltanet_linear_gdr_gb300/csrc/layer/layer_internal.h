@@ -84,10 +84,9 @@ cudaError_t launch_norm_odd(const NormParams &p, cudaStream_t s);
 // One short convolution call, after validation.  Strides in elements.
 struct ConvOpParams {
     int batch, channels, silu;
-    int rows_form;     // a block takes a whole row; else a run of `run` tokens, whichever rows they are of
-    int run, tiles;    // tiles: channel tiles
+    int run, tiles;    // a block's tokens where it takes a run of them; channel tiles
     int keep;          // slots are written
-    int vec;           // token rows may be moved as 16-byte vectors
+    int vec;           // token rows may be moved as vectors of four
     int w_vec;         // a channel's weights lie together, four of them as one vector
     int st_run;        // a slot's [channels, width-1] lie together, 16-byte aligned
     int st_bf16;
@@ -149,7 +148,6 @@ cudaError_t launch_scan_join(const ScanParams &p, cudaStream_t s);
 // One verification of drafts, after validation.
 struct AcceptParams {
     int batch, vocab, width;
-    int vec;           // probability rows may be moved as 16-byte vectors
     long long T;
     const void *target, *draft;
     long long t_ts, d_ts;
