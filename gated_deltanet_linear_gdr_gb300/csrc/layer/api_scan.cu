@@ -159,6 +159,11 @@ int check_scan(const gdr_scan_args *a, const char *fn) {
     return GDR_OK;
 }
 
+// Rows up to here go token by token (k_scan_step.cuh), longer ones by chunks (k_scan.cuh).  Measured, 64 rows x 32
+// heads of 128 channels, 16 states, a pass with outputs and one without, us, steps against chunks: rows of 2
+// 27 / 101, of 8 64 / 107, of 12 89 / 115, of 16 111 / 121.
+constexpr int kShortRow = 16;
+
 // Tokens a segment for rows that are cut, or 0.
 int plan_scan(const gdr_scan_args *a) {
     if (a->batch < 1 || a->batch > 32 || a->max_row_len == 1 || !a->total_tokens) return 0;
@@ -292,7 +297,7 @@ int gdr_selective_scan(const gdr_scan_args *a, void *stream) {
     if (p.seg && (!a->workspace || a->workspace_bytes < scan_bytes(a, p.seg))) p.seg = 0;
     p.ws = static_cast<float *>(a->workspace);
     const bool db = a->dt_dtype == GDR_BF16;
-    if (a->max_row_len == 1) {
+    if (a->max_row_len >= 1 && a->max_row_len <= kShortRow) {
         const bool all = vec && a->K % (a->K <= 16 ? 4 : a->K <= 32 ? 8 : a->K <= 64 ? 16 : 32) == 0 && vector_rows(a->B, a->token_dtype, 4 * esize(a->token_dtype), p.B_ts, p.B_hs) &&
                          (!a->out || vector_rows(a->C, a->token_dtype, 4 * esize(a->token_dtype), p.C_ts, p.C_hs));
         return launched(gdr::launch_scan_step(p, tb, db, all, static_cast<cudaStream_t>(stream)), fn);

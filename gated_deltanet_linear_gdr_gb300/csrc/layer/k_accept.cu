@@ -14,8 +14,9 @@
 // 1e5 a float32 sum would miss it in a few draws of a hundred.  Differences are
 // kept as (difference, its rounding error) and sums as (sum, error) of float32 pairs by
 // two-sum (Knuth, The Art of Computer Programming 2, 4.2.2), good to 46 bits and
-// more; the FP64 pipes (2 operations a cycle and multiprocessor) would take 2.5 times as long as
-// the memory.  What is left of a stretch's sums is added up in double.
+// more: 14 additions a token, which the FP32 pipes do while memory delivers it; the
+// FP64 pipes (2 operations a cycle and multiprocessor) would take several times as
+// long.  Only single warps, at the joints, work in double.
 #include <cooperative_groups.h>
 
 #include "../gdr_device.cuh"
@@ -40,98 +41,123 @@ struct Sum {
         c = __fadd_rn(c, __fadd_rn(e, low));
         s = t;
     }
-};
-
-enum Weight { kTarget, kDifference };  // p (0 at a refused token that was not drawn); max(p - q, 0)
-
-// One token's weight as (value, rounding error).
-template <Weight M> __device__ __forceinline__ void add_weight(Sum &a, float p, float q) {
-    p = clean(p);
-    if constexpr (M == kDifference) {
-        q = clean(q);
+    // p - q where that is positive, as (difference, its rounding error)
+    __device__ __forceinline__ void add_difference(float p, float q) {
         const float w = __fsub_rn(p, q), b = __fsub_rn(w, p);
         const float e = __fsub_rn(__fsub_rn(p, __fsub_rn(w, b)), __fadd_rn(q, b));
         const bool some = w > 0.0f;
-        a.add(some ? w : 0.0f, some ? e : 0.0f);
-    } else {
-        a.add(p, 0.0f);
+        add(some ? w : 0.0f, some ? e : 0.0f);
     }
-}
-
-template <Weight M> __device__ __forceinline__ double exact_weight(float p, float q) {
-    p = clean(p);
-    if constexpr (M == kDifference) {
-        q = clean(q);
-        return p > q ? (double)p - (double)q : 0.0;
-    } else {
-        return (double)p;
-    }
-}
-
-// C neighbouring probabilities from i on; those outside [0, end) count as 0.
-template <typename PT, int C> __device__ __forceinline__ void take(const PT *row, int i, int end, bool vec, float (&v)[C]) {
-    if (vec && i >= 0 && i + C <= end) {
-        Pack<PT, C> w;
-        w.load(row + i);
+    __device__ __forceinline__ Sum over_warp() const {
+        Sum a = *this;
 #pragma unroll
-        for (int j = 0; j < C; ++j) v[j] = w.get(j);
-    } else {
-#pragma unroll
-        for (int j = 0; j < C; ++j) v[j] = i + j >= 0 && i + j < end ? to_f32(row[i + j]) : 0.0f;
-    }
-}
-
-// What a row's draw goes by: weights of tokens [0, vocab), read in vectors from an index at or
-// before 0 that is aligned in memory.
-template <typename PT> struct Weights {
-    static constexpr int C = 16 / (int)sizeof(PT);
-    const PT *p, *q;
-    Weight mode;
-    int no, vocab;
-    bool vec;
-    // C neighbouring weights as (value, rounding error)
-    __device__ __forceinline__ void load(int i, int end, float (&pv)[C], float (&qv)[C]) const {
-        take<PT, C>(p, i, end, vec, pv);
-        if (mode == kDifference) take<PT, C>(q, i, end, vec, qv);
-    }
-    __device__ __forceinline__ void add(Sum &a, int i, const float (&pv)[C], const float (&qv)[C]) const {
-        if (mode == kDifference) {
-#pragma unroll
-            for (int j = 0; j < C; ++j) add_weight<kDifference>(a, pv[j], qv[j]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < C; ++j) add_weight<kTarget>(a, i + j == no ? 0.0f : pv[j], 0.0f);
+        for (int m = 16; m; m >>= 1) {
+            const float os = __shfl_xor_sync(kFull, a.s, m), oc = __shfl_xor_sync(kFull, a.c, m);
+            a.add(os, oc);
         }
+        return a;
     }
-    __device__ __forceinline__ double exact(int i, float pv, float qv) const {
-        if (mode == kDifference) return exact_weight<kDifference>(pv, qv);
-        return i == no ? 0.0 : exact_weight<kTarget>(pv, 0.0f);
+    __device__ __forceinline__ double value() const { return (double)s + (double)c; }
+};
+
+// What a row's draw goes by: the weights of tokens [0, vocab).
+template <typename PT> struct Weights {
+    static constexpr int C = 16 / (int)sizeof(PT);  // tokens of a vector
+    const PT *p, *q;
+    bool difference;  // max(p - q, 0); else p
+    int no;           // a token whose weight is 0, or -1
+    int start;        // the first vector's place, where p is aligned: at or up to C - 1 before token 0
+    bool vec;         // q is aligned where p is
+
+    __device__ __forceinline__ double exact(int i) const {
+        const float pi = clean(to_f32(p[i]));
+        if (!difference) return i == no ? 0.0 : (double)pi;
+        const float qi = clean(to_f32(q[i]));
+        return pi > qi ? (double)pi - (double)qi : 0.0;
+    }
+    __device__ __forceinline__ void one(Sum &a, int i) const {
+        const float pi = clean(to_f32(p[i]));
+        if (difference) a.add_difference(pi, clean(to_f32(q[i])));
+        else a.add(i == no ? 0.0f : pi, 0.0f);
+    }
+    // The sum of a lane's part of [i0, i1), C tokens or one at a time.
+    __device__ __forceinline__ Sum slow(int i0, int i1, int lane) const {
+        Sum a;
+        for (int i = i0 + lane; i < i1; i += 32)
+            if (i >= 0) one(a, i);
+        return a;
+    }
+    // The same by vectors.  Values that do not count leave a NaN in `odd`: then the sum is not to be used.
+    template <bool DIFF> __device__ __forceinline__ Sum fast(int i0, int i1, int lane, float &odd) const {
+        constexpr int U = 2;
+        Sum a;
+        // whole vectors lie in [a0, a1); before them there are tokens only at the row's beginning, behind them only at its end
+        const int a0 = i0 < 0 ? i0 + C : i0, a1 = i1 - (i1 - start) % C;
+        if (i0 < 0 && lane < a0 && lane < i1) one(a, lane);
+        if (a1 >= a0 && lane < i1 - a1) one(a, a1 + lane);
+        for (int i = a0 + lane * C; i < a1; i += 32 * C * U) {
+            Pack<PT, C> pv[U], qv[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int at = i + k * 32 * C;
+                if (at < a1) {
+                    pv[k].load(p + at);
+                    if (DIFF) qv[k].load(q + at);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const int at = i + k * 32 * C, gone = DIFF ? -1 : no - at;
+                if (at >= a1) break;
+#pragma unroll
+                for (int j = 0; j < C; ++j) {
+                    float x = pv[k].get(j);
+                    odd = fmaf(x, 0.0f, odd);
+                    x = fmaxf(x, 0.0f);
+                    if constexpr (DIFF) {
+                        const float y = qv[k].get(j);
+                        odd = fmaf(y, 0.0f, odd);
+                        a.add_difference(x, fmaxf(y, 0.0f));
+                    } else {
+                        a.add(j == gone ? 0.0f : x, 0.0f);
+                    }
+                }
+            }
+        }
+        return a;
+    }
+    // The sum of a warp's stretch [i0, i1), in every lane.
+    __device__ __forceinline__ Sum stretch(int i0, int i1, int lane) const {
+        Sum a;
+        float odd = 0.0f;
+        if (vec && i0 < i1) a = difference ? fast<true>(i0, i1, lane, odd) : fast<false>(i0, i1, lane, odd);
+        if (!vec || __any_sync(kFull, odd != 0.0f)) a = slow(i0, i1, lane);
+        return a.over_warp();
     }
 };
 
-// The sum of a warp's stretch [i0, i1), in every lane.
-template <typename PT> __device__ __forceinline__ double stretch(const Weights<PT> &w, int i0, int i1, int lane) {
-    constexpr int C = Weights<PT>::C, U = 2;
-    Sum a;
-    for (int i = i0 + lane * C; i < i1; i += 32 * C * U) {
-        float pv[U][C], qv[U][C];
+// Of up to 32 parts, part `lane`'s weight `mine`: the one at which `before` and the running sum pass `share`,
+// the last one with a weight where none does, -1 where there is no weight; `base`: the sum ahead of it;
+// `passed`: whether one does.
+__device__ __forceinline__ int part_of(double mine, double before, double share, int lane, double &base, bool &passed) {
+    double upto = mine;
 #pragma unroll
-        for (int k = 0; k < U; ++k) w.load(i + k * 32 * C, i1, pv[k], qv[k]);
-#pragma unroll
-        for (int k = 0; k < U; ++k) w.add(a, i + k * 32 * C, pv[k], qv[k]);
+    for (int m = 1; m < 32; m <<= 1) {
+        const double o = __shfl_up_sync(kFull, upto, m);
+        if (lane >= m) upto += o;
     }
-#pragma unroll
-    for (int m = 16; m; m >>= 1) {
-        const float s = __shfl_xor_sync(kFull, a.s, m), c = __shfl_xor_sync(kFull, a.c, m);
-        a.add(s, c);
-    }
-    return (double)a.s + (double)a.c;
+    const unsigned some = __ballot_sync(kFull, mine > 0.0), past = __ballot_sync(kFull, mine > 0.0 && before + upto > share);
+    const int which = past ? __ffs(past) - 1 : 31 - __clz(some);
+    passed = past != 0;
+    base = before + __shfl_sync(kFull, upto - mine, which < 0 ? 0 : which);
+    return which;
 }
 
 template <typename PT> __global__ void __launch_bounds__(kThreads, 2) k_accept(const __grid_constant__ AcceptParams p) {
-    __shared__ double sums[kWarps];  // of this block's stretches, then of a stretch's parts
-    __shared__ double block_sum;
-    __shared__ int first_refused, first_none, found, last;
+    __shared__ Sum sums[kWarps];  // of this block's stretches, then of a stretch's parts
+    __shared__ double block_sum, joint_base, joint_share, joint_sum;
+    __shared__ int first_refused, first_none, joint_owner, joint_part;
+    __shared__ bool joint_passed;
     cg::cluster_group cluster = cg::this_cluster();
     const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int b = (int)(blockIdx.x / (unsigned)blocks), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -149,11 +175,7 @@ template <typename PT> __global__ void __launch_bounds__(kThreads, 2) k_accept(c
     // which drafts pass
     const int drafts = (int)(hi - lo) - 1;
     const float v = p.row_u[b];
-    if (tid == 0) {
-        first_refused = first_none = drafts;
-        found = 0x7fffffff;
-        last = -1;
-    }
+    if (tid == 0) first_refused = first_none = drafts;
     __syncthreads();
     const PT *const target = static_cast<const PT *>(p.target), *const draft = static_cast<const PT *>(p.draft);
     for (int i = tid; i < drafts; i += kThreads) {
@@ -175,109 +197,107 @@ template <typename PT> __global__ void __launch_bounds__(kThreads, 2) k_accept(c
     constexpr int C = Weights<PT>::C;
     w.p = target + t * p.t_ts;
     w.q = draft ? draft + t * p.d_ts : w.p;
-    w.mode = !refused ? kTarget : draft ? kDifference : kTarget;
+    w.difference = refused && draft;
     w.no = refused && !draft ? p.tokens[t + 1] : -1;
-    w.vocab = p.vocab;
     const int off_p = (int)(reinterpret_cast<uintptr_t>(w.p) % 16), off_q = (int)(reinterpret_cast<uintptr_t>(w.q) % 16);
-    w.vec = w.mode == kTarget || off_p == off_q;
-    const int start = -(off_p / (int)sizeof(PT));  // aligned, at most C - 1 before the first token
+    w.vec = !w.difference || off_p == off_q;
+    w.start = -(off_p / (int)sizeof(PT));
 
     // the sums: a stretch of whole vectors a warp
-    const int each = ((p.vocab - start - 1) / (blocks * kWarps) + C) / C * C;
-    const long long from = (long long)(rank * kWarps + warp) * each + start;
+    const int each = ((p.vocab - w.start - 1) / (blocks * kWarps) + C) / C * C;
+    const long long from = (long long)(rank * kWarps + warp) * each + w.start;
     const int i0 = (int)(from < p.vocab ? from : p.vocab), i1 = p.vocab - i0 < each ? p.vocab : i0 + each;
-    double total = 0.0, before = 0.0, share = 0.0;
-    int owner = -1;
     for (int pass = 0; pass < 2; ++pass) {
-        const double s = stretch(w, i0, i1, lane);
+        const Sum s = w.stretch(i0, i1, lane);
         if (lane == 0) sums[warp] = s;
         __syncthreads();
         if (warp == 0) {
-            double all = lane < kWarps ? sums[lane] : 0.0;
+            double all = lane < kWarps ? sums[lane].value() : 0.0;
 #pragma unroll
             for (int m = kWarps / 2; m; m >>= 1) all += __shfl_xor_sync(kFull, all, m);
             if (lane == 0) block_sum = all;
         }
-        cluster.sync();
-        // every warp adds up the blocks' sums alike: lane r has block r's
-        const double mine = lane < blocks ? *cluster.map_shared_rank(&block_sum, lane) : 0.0;
-        double upto = mine;
+        if (blocks > 1) cluster.sync();
+        if (warp == 0) {
+            // lane r has block r's sum: every block finds the same place
+            const double mine = blocks == 1 ? (lane == 0 ? block_sum : 0.0) : lane < blocks ? *cluster.map_shared_rank(&block_sum, lane) : 0.0;
+            double total = mine, base;
+            bool passed;
 #pragma unroll
-        for (int m = 1; m < 8; m <<= 1) {
-            const double o = __shfl_up_sync(kFull, upto, m);
-            if (lane >= m) upto += o;
+            for (int m = 4; m; m >>= 1) total += __shfl_xor_sync(kFull, total, m);
+            total = __shfl_sync(kFull, total, 0);
+            const double share = v > 0.0f ? (double)v * total : 0.0;
+            const int owner = part_of(mine, 0.0, share, lane, base, passed);
+            if (owner == rank) {
+                const int part = part_of(lane < kWarps ? sums[lane].value() : 0.0, base, share, lane, base, passed);
+                if (lane == 0) joint_part = part;
+            }
+            if (lane == 0) {
+                joint_owner = owner;
+                joint_base = base;
+                joint_share = share;
+            }
         }
-        total = __shfl_sync(kFull, upto, 7);
-        if (total > 0.0) {
-            // the block whose part passes the share; the last one with a weight where none does
-            share = v > 0.0f ? (double)v * total : 0.0;
-            const unsigned some = __ballot_sync(kFull, mine > 0.0), past = __ballot_sync(kFull, mine > 0.0 && upto > share);
-            owner = past ? __ffs(past) - 1 : 31 - __clz(some);
-            before = __shfl_sync(kFull, upto - mine, owner);
-        }
-        if (total > 0.0 || (w.mode == kTarget && w.no < 0)) break;
-        w.mode = kTarget;  // nothing left over of the target: drawn from the target itself
+        __syncthreads();
+        if (joint_owner >= 0 || (!w.difference && w.no < 0)) break;
+        w.difference = false;  // nothing left over of the target: drawn from the target itself
         w.no = -1;
         w.vec = true;
-        cluster.sync();  // before the sums are written again
+        if (blocks > 1) cluster.sync();  // before the sums are written again
     }
+    const int owner = joint_owner;
     if (owner == rank) {
-        // the stretch, the same way
-        const double mine = lane < kWarps ? sums[lane] : 0.0;
-        double upto = mine;
-#pragma unroll
-        for (int m = 1; m < kWarps; m <<= 1) {
-            const double o = __shfl_up_sync(kFull, upto, m);
-            if (lane >= m) upto += o;
-        }
-        const unsigned some = __ballot_sync(kFull, mine > 0.0), past = __ballot_sync(kFull, mine > 0.0 && before + upto > share);
-        const int which = past ? __ffs(past) - 1 : 31 - __clz(some);
-        double base = before + __shfl_sync(kFull, upto - mine, which);
-        const long long s0 = (long long)(rank * kWarps + which) * each + start;
+        // the stretch again, in parts of a vector a lane: the warp's part, then the lane's, then the token
+        const double share = joint_share;
+        double base = joint_base;
+        const long long s0 = (long long)(rank * kWarps + joint_part) * each + w.start;
         const int end = (int)(s0 + each < p.vocab ? s0 + each : p.vocab);
-        // and its least token at which the running sum passes, by all threads
         for (int i = (int)s0; i < end; i += C * kThreads) {
             const int at = i + tid * C;
-            float pv[C], qv[C];
-            double own = 0.0;
+            Sum own;
 #pragma unroll
-            for (int j = 0; j < C; ++j) pv[j] = qv[j] = 0.0f;
-            if (at < end) w.load(at, end, pv, qv);
-#pragma unroll
-            for (int j = 0; j < C; ++j) own += w.exact(at + j, pv[j], qv[j]);
-            double sum = own;
-#pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const double o = __shfl_up_sync(kFull, sum, m);
-                if (lane >= m) sum += o;
-            }
-            __syncthreads();  // sums is read no more
-            if (lane == 31) sums[warp] = sum;
+            for (int j = 0; j < C; ++j)
+                if (at + j >= 0 && at + j < end) w.one(own, at + j);
+            const Sum part = own.over_warp();
+            __syncthreads();  // sums, and what hangs on it, are read no more
+            if (lane == 0) sums[warp] = part;
             __syncthreads();
-            double ahead = lane < warp ? sums[lane] : 0.0, all = lane < kWarps ? sums[lane] : 0.0;
+            if (warp == 0) {
+                double next;
+                bool passed;
+                const double mine = lane < kWarps ? sums[lane].value() : 0.0;
+                const int which = part_of(mine, base, share, lane, next, passed);
+                double all = mine;
 #pragma unroll
-            for (int m = kWarps / 2; m; m >>= 1) {
-                ahead += __shfl_xor_sync(kFull, ahead, m);
-                all += __shfl_xor_sync(kFull, all, m);
-            }
-            double run = base + ahead + (sum - own);
-            int here = -1, positive = -1;
-#pragma unroll
-            for (int j = 0; j < C; ++j) {
-                const double x = w.exact(at + j, pv[j], qv[j]);
-                run += x;
-                if (x > 0.0) {
-                    positive = at + j;
-                    if (here < 0 && run > share) here = at + j;
+                for (int m = 16; m; m >>= 1) all += __shfl_xor_sync(kFull, all, m);
+                if (lane == 0) {
+                    joint_part = which;
+                    joint_base = next;
+                    joint_sum = all;
+                    joint_passed = passed;
                 }
             }
-            if (here >= 0) atomicMin(&found, here);
-            if (positive >= 0) atomicMax(&last, positive);
             __syncthreads();
-            if (found != 0x7fffffff) break;
-            base += all;
+            const int which = joint_part;
+            const double ahead = joint_base;
+            if (which == warp) {
+                double first;
+                bool passed;
+                const int l = part_of(own.value(), ahead, share, lane, first, passed);
+                int found = -1;  // the token past the share; the last one with a weight, where rounding leaves none
+                if (lane == l) {
+#pragma unroll
+                    for (int j = 0; j < C; ++j) {
+                        const double x = at + j >= 0 && at + j < end ? w.exact(at + j) : 0.0;
+                        if (x > 0.0 && !(first > share)) found = at + j;
+                        first += x;
+                    }
+                    out[accepted] = found;
+                }
+            }
+            if (joint_passed) break;
+            base += joint_sum;
         }
-        if (tid == 0) out[accepted] = found != 0x7fffffff ? found : last;
     }
     if (rank == 0) {
         for (int i = tid; i < p.width; i += kThreads)

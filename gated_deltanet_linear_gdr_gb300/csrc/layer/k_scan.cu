@@ -1,5 +1,5 @@
 // Selective scan: the choice of types, and the join of a cut row's segments.
-#include "k_scan.cuh"
+#include "scan_device.cuh"
 
 namespace gdr {
 namespace {
@@ -47,6 +47,11 @@ cudaError_t launch_scan_join(const ScanParams &p, cudaStream_t s) {
 cudaError_t launch_scan(const ScanParams &p, bool tok_bf16, bool dt_bf16, bool vec, cudaStream_t s) {
     if (!tok_bf16) return launch_scan_ff(p, vec, s);
     return dt_bf16 ? launch_scan_bb(p, vec, s) : launch_scan_bf(p, vec, s);
+}
+
+cudaError_t launch_scan_step(const ScanParams &p, bool tok_bf16, bool dt_bf16, bool vec, cudaStream_t s) {
+    if (!tok_bf16) return launch_scan_step_ff(p, vec, s);
+    return dt_bf16 ? launch_scan_step_bb(p, vec, s) : launch_scan_step_bf(p, vec, s);
 }
 
 }  // namespace gdr

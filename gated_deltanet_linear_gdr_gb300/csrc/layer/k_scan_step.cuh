@@ -1,10 +1,13 @@
-// Selective scan of single tokens: every state goes in and out once, with a
-// handful of operations on it: HBM bound.  A block is 128 channels of some rows.
+// Selective scan of single tokens and short rows (drafts): every state goes in and
+// out once, with a handful of operations on it a token: HBM bound, or bound by the
+// steps that follow one another.  A block is 128 channels of some rows.
 // Its four warps share the states, KT each, four channels a lane, so that a warp
 // moves whole runs of 512 bytes.  What belongs to the channels (their places, the
 // rates, the bias) is worked out once for all the block's rows; the next row's
 // states are on their way while one is worked on.  The partial readouts meet in
 // shared memory, and every thread finishes one channel.
+#pragma once
+
 #include "scan_device.cuh"
 
 namespace gdr {
@@ -65,16 +68,18 @@ template <typename TT, typename DT, typename ST> struct StepRow {
     const DT *dt;
     const TT *x, *z, *B, *C;
     TT *out;
-    int todo;  // 0: nothing, 1: zeros, 2: the token, 3: and its states are kept
+    int len;   // tokens, 0: nothing to do
+    int kept;  // tokens after which the states are kept, 0: they are not; -1: zeros only
 };
 
 // VEC: four channels are a vector everywhere, and so are four states of B and C; K is a multiple of KT.
-template <typename TT, typename DT, typename ST, int KT, bool VEC>
+// ONE: rows of one token.
+template <typename TT, typename DT, typename ST, int KT, bool VEC, bool ONE>
 __global__ void __launch_bounds__(kStepTile, KT <= 4 ? 4 : KT <= 8 ? 3 : 1)
     k_scan_step(const __grid_constant__ ScanParams p, int tiles, int rows) {
     __shared__ __align__(16) float part[2][4][kStepTile];
     __shared__ StepRow<TT, DT, ST> info[kStepRows];
-    constexpr bool AHEAD = VEC && KT <= 8;  // there are registers for two rows' states
+    constexpr bool AHEAD = VEC && ONE && KT <= 8;  // there are registers for two rows' states
     constexpr int KV = KT / 4;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const unsigned all = (unsigned)(p.nk * tiles), block = blockIdx.x / all, tg = blockIdx.x - block * all;
@@ -84,9 +89,10 @@ __global__ void __launch_bounds__(kStepTile, KT <= 4 ? 4 : KT <= 8 ? 3 : 1)
     if (tid < nrows) {
         ScanUnit u;
         StepRow<TT, DT, ST> r;
-        r.todo = 0;
+        r.len = 0;
         if (scan_row(p, b0 + tid, tg == 0, u)) {
-            r.todo = u.slot < 0 ? 1 : u.kept > 0 ? 3 : 2;
+            r.len = u.len;
+            r.kept = u.slot < 0 ? -1 : u.kept;
             r.state = static_cast<ST *>(p.state) + (u.slot < 0 ? 0 : u.slot * p.st_slot);
             r.dt = static_cast<const DT *>(p.dt) + u.t0 * p.dt_ts;
             r.x = static_cast<const TT *>(p.x) + u.t0 * p.x_ts;
@@ -121,22 +127,20 @@ __global__ void __launch_bounds__(kStepTile, KT <= 4 ? 4 : KT <= 8 ? 3 : 1)
     const float D = mon && p.D ? p.D[mh * p.d_hs + mj * p.d_vs] : 0.0f;
     __syncthreads();
 
-    struct Row {
-        Four<ST, VEC> S[KT];
+    struct Token {
         Four<DT, VEC> d;
         Four<TT, VEC> x, B[KV], C[KV];
         TT mx, mz;
     };
-    auto ask = [&](int r, Row &v) {
-        const StepRow<TT, DT, ST> &w = info[r];
-        if (w.todo < 2) return;
+    struct Row {
+        Four<ST, VEC> S[KT];
+        Token t;  // its first token
+    };
+    auto ask_token = [&](const StepRow<TT, DT, ST> &w, int t, Token &v) {
         if (have > 0) {
-#pragma unroll
-            for (int i = 0; i < KT; ++i)
-                if (VEC || i < have) gather4(w.state + i * p.st_k, st_at, on, v.S[i]);
-            gather4(w.dt, d_at, on, v.d);
-            gather4(w.x, x_at, on, v.x);
-            const TT *const b = w.B + k0, *const c = w.C + k0;
+            gather4(w.dt + t * p.dt_ts, d_at, on, v.d);
+            gather4(w.x + t * p.x_ts, x_at, on, v.x);
+            const TT *const b = w.B + t * p.B_ts + k0, *const c = w.C + t * p.C_ts + k0;
 #pragma unroll
             for (int i = 0; i < KV; ++i) {
                 if constexpr (VEC) {
@@ -152,48 +156,74 @@ __global__ void __launch_bounds__(kStepTile, KT <= 4 ? 4 : KT <= 8 ? 3 : 1)
                 }
             }
         }
-        if (mon) v.mx = w.x[mx_at];
-        if (gate) v.mz = w.z[mz_at];
+        if (mon) v.mx = w.x[t * p.x_ts + mx_at];
+        if (gate) v.mz = w.z[t * p.z_ts + mz_at];
     };
+    auto ask = [&](int r, Row &v) {
+        const StepRow<TT, DT, ST> &w = info[r];
+        if (w.len == 0 || w.kept < 0) return;
+#pragma unroll
+        for (int i = 0; i < KT; ++i)
+            if (i < have) gather4(w.state + i * p.st_k, st_at, on, v.S[i]);
+        ask_token(w, 0, v.t);
+    };
+    int exchanges = 0;
     auto turn = [&](int r, const Row &v) {
         const StepRow<TT, DT, ST> &w = info[r];
-        if (w.todo < 2) {
-            if (w.todo == 1 && mon) w.out[mo_at] = TT(0);
+        const int len = w.len;
+        if (w.kept < 0) {
+            if (mon)
+                for (int t = 0; t < len; ++t) w.out[t * p.o_ts + mo_at] = TT(0);
             return;
         }
-        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (have > 0) {
-            float S[KT][4], d[4], in[4];
+        float S[KT][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                d[e] = v.d.get(e) + bias[e];
-                if (p.softplus) d[e] = softplus<TT>(d[e]);
-                in[e] = d[e] * v.x.get(e);
-            }
+        for (int i = 0; i < KT; ++i)
 #pragma unroll
-            for (int i = 0; i < KT; ++i) {
-                if (!VEC && i >= have) continue;
-                const float B = v.B[i / 4].get(i % 4), C = v.C[i / 4].get(i % 4);
+            for (int e = 0; e < 4; ++e) S[i][e] = v.S[i].get(e);
+        Token now = v.t;
+#pragma unroll 1
+        for (int t = 0; t < len; ++t) {
+            Token next;
+            if (!ONE && t + 1 < len) ask_token(w, t + 1, next);
+            float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (have > 0) {
+                float d[4], in[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    S[i][e] = fmaf(decay<TT>(d[e] * A[i][e]), v.S[i].get(e), in[e] * B);
-                    y[e] = fmaf(C, S[i][e], y[e]);  // of no meaning, and not used, where there are no outputs
+                    d[e] = now.d.get(e) + bias[e];
+                    if (p.softplus) d[e] = softplus<TT>(d[e]);
+                    in[e] = d[e] * now.x.get(e);
+                }
+#pragma unroll
+                for (int i = 0; i < KT; ++i) {
+                    if (!VEC && i >= have) continue;
+                    const float B = now.B[i / 4].get(i % 4), C = now.C[i / 4].get(i % 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        S[i][e] = fmaf(decay<TT>(d[e] * A[i][e]), S[i][e], in[e] * B);
+                        y[e] = fmaf(C, S[i][e], y[e]);  // of no meaning, and not used, where there are no outputs
+                    }
+                }
+                if (t + 1 == w.kept) {
+#pragma unroll
+                    for (int i = 0; i < KT; ++i)
+                        if (i < have) scatter4<VEC>(w.state + i * p.st_k, st_at, on, S[i]);
                 }
             }
-            if (w.todo == 3) {
-#pragma unroll
-                for (int i = 0; i < KT; ++i)
-                    if (VEC || i < have) scatter4<VEC>(w.state + i * p.st_k, st_at, on, S[i]);
+            if (p.out) {
+                float (&q)[4][kStepTile] = part[exchanges++ & 1];
+                *reinterpret_cast<float4 *>(&q[warp][lane * 4]) = make_float4(y[0], y[1], y[2], y[3]);
+                __syncthreads();
+                if (mon) {
+                    float o = fmaf(D, to_f32(now.mx), (q[0][tid] + q[1][tid]) + (q[2][tid] + q[3][tid]));
+                    if (gate) o *= silu(to_f32(now.mz));
+                    w.out[t * p.o_ts + mo_at] = from_f32<TT>(o);
+                }
             }
+            if (ONE) break;
+            now = next;
         }
-        if (!p.out) return;
-        *reinterpret_cast<float4 *>(&part[r & 1][warp][lane * 4]) = make_float4(y[0], y[1], y[2], y[3]);
-        __syncthreads();
-        if (!mon) return;
-        const float (&q)[4][kStepTile] = part[r & 1];
-        float o = fmaf(D, to_f32(v.mx), (q[0][tid] + q[1][tid]) + (q[2][tid] + q[3][tid]));
-        if (gate) o *= silu(to_f32(v.mz));
-        w.out[mo_at] = from_f32<TT>(o);
     };
     if constexpr (AHEAD) {
         Row v[2];
@@ -214,7 +244,7 @@ __global__ void __launch_bounds__(kStepTile, KT <= 4 ? 4 : KT <= 8 ? 3 : 1)
     }
 }
 
-template <typename TT, typename DT, typename ST, int KT, bool VEC> cudaError_t go(const ScanParams &p, cudaStream_t s) {
+template <typename TT, typename DT, typename ST, int KT, bool VEC, bool ONE> cudaError_t go(const ScanParams &p, cudaStream_t s) {
     const long long tiles = ((long long)p.r * p.V + kStepTile - 1) / kStepTile, heads = p.nk * tiles;
     // as many rows a block as leaves each multiprocessor its blocks once over
     const long long at_once = 152 * (KT <= 4 ? 4 : KT <= 8 ? 3 : 1);
@@ -222,27 +252,23 @@ template <typename TT, typename DT, typename ST, int KT, bool VEC> cudaError_t g
     if (rows > kStepRows) rows = kStepRows;
     const long long blocks = (p.batch + rows - 1) / rows * heads;
     if (blocks >= 1ll << 31) return cudaErrorInvalidConfiguration;
-    k_scan_step<TT, DT, ST, KT, VEC><<<(unsigned)blocks, kStepTile, 0, s>>>(p, (int)tiles, (int)rows);
+    k_scan_step<TT, DT, ST, KT, VEC, ONE><<<(unsigned)blocks, kStepTile, 0, s>>>(p, (int)tiles, (int)rows);
     return cudaGetLastError();
 }
-
-// States a warp has, by K.
-template <typename TT, typename DT, typename ST, bool VEC> cudaError_t states(const ScanParams &p, cudaStream_t s) {
-    if (p.K <= 16) return go<TT, DT, ST, 4, VEC>(p, s);
-    if (p.K <= 32) return go<TT, DT, ST, 8, VEC>(p, s);
-    if (p.K <= 64) return go<TT, DT, ST, 16, VEC>(p, s);
-    return go<TT, DT, ST, 32, VEC>(p, s);
+template <typename TT, typename DT, typename ST, int KT> cudaError_t step_form(const ScanParams &p, bool vec, cudaStream_t s) {
+    if (!vec) return go<TT, DT, ST, KT, false, false>(p, s);
+    return p.max_len == 1 ? go<TT, DT, ST, KT, true, true>(p, s) : go<TT, DT, ST, KT, true, false>(p, s);
 }
-template <typename TT, typename DT> cudaError_t pool(const ScanParams &p, bool vec, cudaStream_t s) {
-    if (p.st_bf16) return vec ? states<TT, DT, uint16_t, true>(p, s) : states<TT, DT, uint16_t, false>(p, s);
-    return vec ? states<TT, DT, float, true>(p, s) : states<TT, DT, float, false>(p, s);
+// States a warp has, by K.
+template <typename TT, typename DT, typename ST> cudaError_t step_states(const ScanParams &p, bool vec, cudaStream_t s) {
+    if (p.K <= 16) return step_form<TT, DT, ST, 4>(p, vec, s);
+    if (p.K <= 32) return step_form<TT, DT, ST, 8>(p, vec, s);
+    if (p.K <= 64) return step_form<TT, DT, ST, 16>(p, vec, s);
+    return step_form<TT, DT, ST, 32>(p, vec, s);
+}
+template <typename TT, typename DT> cudaError_t scan_step(const ScanParams &p, bool vec, cudaStream_t s) {
+    return p.st_bf16 ? step_states<TT, DT, uint16_t>(p, vec, s) : step_states<TT, DT, float>(p, vec, s);
 }
 
 }  // namespace
-
-cudaError_t launch_scan_step(const ScanParams &p, bool tok_bf16, bool dt_bf16, bool vec, cudaStream_t s) {
-    if (!tok_bf16) return pool<float, float>(p, vec, s);
-    return dt_bf16 ? pool<uint16_t, uint16_t>(p, vec, s) : pool<uint16_t, float>(p, vec, s);
-}
-
 }  // namespace gdr

@@ -136,7 +136,7 @@ struct ScanParams {
 __host__ __device__
 #endif
 inline long long scan_pieces(long long T, int seg, int batch) { return T / seg + batch; }
-// Single tokens (max_len is 1), and everything else.  vec: groups of 8 channels may be
+// Short rows (max_len bounds them), and any.  vec: groups of 8 channels may be
 // moved as vectors everywhere.
 cudaError_t launch_scan_step(const ScanParams &p, bool tok_bf16, bool dt_bf16, bool vec, cudaStream_t s);
 cudaError_t launch_scan(const ScanParams &p, bool tok_bf16, bool dt_bf16, bool vec, cudaStream_t s);
@@ -144,6 +144,9 @@ cudaError_t launch_scan_bb(const ScanParams &p, bool vec, cudaStream_t s);  // b
 cudaError_t launch_scan_bf(const ScanParams &p, bool vec, cudaStream_t s);  // bfloat16 tokens, float32 step sizes
 cudaError_t launch_scan_ff(const ScanParams &p, bool vec, cudaStream_t s);  // float32
 cudaError_t launch_scan_join(const ScanParams &p, cudaStream_t s);
+cudaError_t launch_scan_step_bb(const ScanParams &p, bool vec, cudaStream_t s);
+cudaError_t launch_scan_step_bf(const ScanParams &p, bool vec, cudaStream_t s);
+cudaError_t launch_scan_step_ff(const ScanParams &p, bool vec, cudaStream_t s);
 
 // One verification of drafts, after validation.
 struct AcceptParams {
