@@ -871,10 +871,13 @@ def gdr_residual_norm(block, residual, weight, *, post_weight=None, gate=None, a
     return h, out
 
 
+_F32, _I32 = torch.float32, torch.int32
+
+
 def _ints(t, shape, name: str, device) -> int:
     """The pointer of a contiguous int32 tensor of a call's rows or tokens."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == device):
-        _refuse(device, {name: torch.int32}, **{name: t})
+    if not (isinstance(t, torch.Tensor) and t.dtype is _I32 and t.device == device):
+        _refuse(device, {name: _I32}, **{name: t})
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} int32 tensor")
     return t.data_ptr()
@@ -884,28 +887,33 @@ def _ragged(slot_idx, offsets, counts, keep_state, state_only, device):
     """(batch, slot_idx, offsets, counts) of a call over ragged rows, as pointers."""
     if not isinstance(slot_idx, torch.Tensor):
         _tensors(slot_idx=slot_idx)
-    if slot_idx.dim() != 1:
+    shape = slot_idx.shape
+    if len(shape) != 1:
         raise ValueError("slot_idx must be a contiguous [batch] int32 tensor")
     if not keep_state and (state_only or counts is not None):
         raise ValueError("state_only and counts need keep_state")
-    n = slot_idx.shape[0]
-    return (n, _ints(slot_idx, (n,), "slot_idx", device), _ints(offsets, (n + 1,), "offsets", device),
-            0 if counts is None else _ints(counts, (n,), "counts", device))
+    n = shape[0]
+    return (n, _ints(slot_idx, shape, "slot_idx", device), _ints(offsets, (n + 1,), "offsets", device),
+            0 if counts is None else _ints(counts, shape, "counts", device))
 
 
 def _output(out, like, state_only):
-    """A call's output tensor: the caller's, a new one like `like`, or none."""
+    """(tensor, pointer, strides) of a call's output: the caller's, a new one like `like`, or none."""
     if state_only:
         if out is not None:
             raise ValueError("state_only has no out")
-        return None
+        return None, 0, (0,) * like.dim()
     if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    if not isinstance(out, torch.Tensor):
-        _tensors(out=out)
-    if out.shape != like.shape or out.dtype != like.dtype or out.device != like.device:
-        raise ValueError("out must have x's shape, dtype and device")
-    return out
+        out = torch.empty_like(like)
+    else:
+        if not isinstance(out, torch.Tensor):
+            _tensors(out=out)
+        if out.shape != like.shape or out.dtype != like.dtype or out.device != like.device:
+            raise ValueError("out must have x's shape, dtype and device")
+    st = out.stride()
+    if st[-1] != 1 and out.shape[-1] > 1:
+        raise ValueError("out must have a unit channel stride")
+    return out, out.data_ptr(), st
 
 
 def _short_conv_args(x, weight, bias, conv_state, slot_idx, offsets, out, activation, counts, keep_state, state_only, max_row_len):
@@ -913,34 +921,32 @@ def _short_conv_args(x, weight, bias, conv_state, slot_idx, offsets, out, activa
     if not isinstance(x, torch.Tensor):
         _tensors(x=x)
     dev = x.device
-    td = _float(x, "x", dev)
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+    td, shape, (xt, *xc) = _float(x, "x", dev), x.shape, x.stride() or (0,)
+    if len(shape) != 2 or (xc[0] != 1 and shape[1] > 1):
         raise ValueError("x must be [T, channels] with a unit channel stride")
-    T, C = x.shape
-    if not (isinstance(weight, torch.Tensor) and weight.dtype is torch.float32 and weight.device == dev):
-        _refuse(dev, {"weight": torch.float32}, weight=weight)
-    if weight.dim() != 2 or weight.shape[0] != C:
+    T, C = shape
+    if not (isinstance(weight, torch.Tensor) and weight.dtype is _F32 and weight.device == dev):
+        _refuse(dev, {"weight": _F32}, weight=weight)
+    ws, wst = weight.shape, weight.stride()
+    if len(ws) != 2 or ws[0] != C:
         raise ValueError(f"weight must be [channels, width] with {C} channels")
-    width = weight.shape[1]
-    if activation not in (None, "silu"):
+    width = ws[1]
+    if activation is not None and activation != "silu":
         raise ValueError('activation must be "silu" or None')
     sp, sd, ss, sc, st, slots = 0, GDR_F32, 0, 0, 0, 1 << 30
     if width > 1:
         sd = _float(conv_state, "conv_state", dev)
-        if conv_state.dim() != 3 or conv_state.shape[1:] != (C, width - 1):
+        cs = conv_state.shape
+        if len(cs) != 3 or cs[1] != C or cs[2] != width - 1:
             raise ValueError(f"conv_state must be [slots, {C}, {width - 1}]")
-        sp, (ss, sc, st), slots = conv_state.data_ptr(), conv_state.stride(), conv_state.shape[0]
+        sp, (ss, sc, st), slots = conv_state.data_ptr(), conv_state.stride(), cs[0]
     elif conv_state is not None:
         raise ValueError("a convolution of width 1 has no conv_state")
-    out = _output(out, x, state_only)
-    if out is not None and out.shape[1] > 1 and out.stride(1) != 1:
-        raise ValueError("out must have a unit channel stride")
     n, slot, off, cnt = _ragged(slot_idx, offsets, counts, keep_state, state_only, dev)
-    ws = weight.stride()
-    return _pack_short_conv(n, C, width, 1 if activation == "silu" else 0, td, sd, 1 if keep_state else 0, T, int(max_row_len),
-                            x.data_ptr(), x.stride(0), weight.data_ptr(), ws[0], ws[1], _weight(bias, C, "bias", dev),
-                            0 if out is None else out.data_ptr(), 0 if out is None else out.stride(0), sp, ss, sc, st, slots,
-                            slot, off, cnt), out
+    out, op, ost = _output(out, x, state_only)
+    return _pack_short_conv(n, C, width, 0 if activation is None else 1, td, sd, 1 if keep_state else 0, T, int(max_row_len),
+                            x.data_ptr(), xt, weight.data_ptr(), wst[0], wst[1], _weight(bias, C, "bias", dev), op, ost[0], sp,
+                            ss, sc, st, slots, slot, off, cnt), out
 
 
 def gdr_short_conv(x, weight, bias, conv_state, slot_idx, offsets, out=None, *, activation="silu", counts=None,
@@ -973,65 +979,68 @@ def prepare_short_conv(x, weight, bias, conv_state, slot_idx, offsets, out, *, a
                     (x, weight, bias, conv_state, slot_idx, offsets, out, counts), x.device)
 
 
+_NO2 = (0, 0)
+
+
 def _per_channel(t, shape, name: str, device):
     """(pointer, strides) of a float32 tensor of a layer's channels; broadcast dimensions as strides of 0."""
-    if t is None:
-        return 0, (0,) * len(shape)
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.device == device):
-        _refuse(device, {name: torch.float32}, **{name: t})
+    if not (isinstance(t, torch.Tensor) and t.dtype is _F32 and t.device == device):
+        _refuse(device, {name: _F32}, **{name: t})
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)} (expand what it shares)")
     return t.data_ptr(), t.stride()
 
 
+def _scan_refuse(x, dt, B, C, z, state):
+    """Says what is wrong with the tokens' tensors of a scan."""
+    _tensors(x=x, dt=dt, state=state, B=B, C=C)
+    dev, want = x.device, {"B": x.dtype, "C": x.dtype, "z": x.dtype}
+    _refuse(dev, want, x=x, dt=dt, state=state, B=B, C=C, **({} if z is None else {"z": z}))
+    if state.dim() != 4:
+        raise ValueError("state must be [max_slots, nv, K, V]")
+    _, nv, K, V = state.shape
+    if x.dim() != 3 or x.shape[1:] != (nv, V):
+        raise ValueError(f"x must be [T, nv, V] = [T, {nv}, {V}]")
+    if dt.shape != x.shape:
+        raise ValueError("dt must have x's shape (expand what it shares)")
+    if B.dim() != 3 or B.shape != C.shape or B.shape[0] != x.shape[0] or B.shape[2] != K or (K > 1 and (B.stride(2), C.stride(2)) != (1, 1)):
+        raise ValueError(f"B and C must both be [T, nk, K] = [{x.shape[0]}, nk, {K}] with a unit stride along K")
+    if z is not None and (z.shape != x.shape or (V > 1 and z.stride(2) != 1)):
+        raise ValueError("z must have x's shape and a unit channel stride")
+    raise ValueError("x must have a unit channel stride, and dt one or one value a head")
+
+
 def _scan_args(x, dt, A, B, C, state, slot_idx, offsets, out, D, z, dt_bias, dt_softplus, counts, keep_state, state_only,
                max_row_len):
     """(packed gdr_scan_args without a workspace, out)."""
-    if not (isinstance(x, torch.Tensor) and isinstance(dt, torch.Tensor) and isinstance(state, torch.Tensor)):
-        _tensors(x=x, dt=dt, state=state)
-    dev = x.device
-    td, dd, sd = _float(x, "x", dev), _float(dt, "dt", dev), _float(state, "state", dev)
-    if state.dim() != 4:
-        raise ValueError("state must be [max_slots, nv, K, V]")
-    slots, nv, K, V = state.shape
-    if x.dim() != 3 or x.shape[1:] != (nv, V):
-        raise ValueError(f"x must be [T, nv, V] = [T, {nv}, {V}]")
-    T = x.shape[0]
-    if dt.shape != x.shape:
-        raise ValueError("dt must have x's shape (expand what it shares)")
-    for name, t in (("B", B), ("C", C)):
-        if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype != x.dtype:
-            _refuse(dev, {name: x.dtype}, **{name: t})
-        if t.dim() != 3 or t.shape[0] != T or t.shape[2] != K or t.shape != B.shape:
-            raise ValueError(f"B and C must both be [T, nk, K] = [{T}, nk, {K}]")
-        if K > 1 and t.stride(2) != 1:
-            raise ValueError(f"{name} must have a unit stride along K")
-    out = _output(out, x, state_only)
-    for name, t in (("x", x), ("out", out)):
-        if t is not None and V > 1 and t.stride(2) != 1:
-            raise ValueError(f"{name} must have a unit channel stride")
-    if V > 1 and dt.stride(2) not in (0, 1):
-        raise ValueError("dt must have a unit channel stride, or one value a head")
     zp, zt, zh = 0, 0, 0
-    if z is not None:
-        if not isinstance(z, torch.Tensor) or z.device != dev or z.dtype != x.dtype:
-            _refuse(dev, {"z": x.dtype}, z=z)
-        if z.shape != x.shape or (V > 1 and z.stride(2) != 1):
-            raise ValueError("z must have x's shape and a unit channel stride")
-        zp, (zt, zh) = z.data_ptr(), z.stride()[:2]
+    try:
+        dev, tok, shape, bshape = x.device, x.dtype, x.shape, B.shape
+        td, dd, sd = _DTYPES[tok], _DTYPES[dt.dtype], _DTYPES[state.dtype]
+        slots, nv, K, V = state.shape
+        T, xn, xv = shape
+        (xt, xh, xc), (tt, th, te), (Bt, Bh, Bk), (Ct, Ch, Ck) = x.stride(), dt.stride(), B.stride(), C.stride()
+        good = (x.is_cuda and B.dtype is tok and C.dtype is tok and dev == dt.device == B.device == C.device == state.device and
+                xn == nv and xv == V and shape == dt.shape and bshape[0] == T and bshape[2] == K and bshape == C.shape and
+                (V == 1 or (xc == 1 and (te == 1 or te == 0))) and (K == 1 or (Bk == 1 and Ck == 1)))
+        if z is not None:
+            zt, zh, zc = z.stride()
+            zp = z.data_ptr()
+            good = good and z.dtype is tok and z.device == dev and z.shape == shape and (zc == 1 or V == 1)
+    except (AttributeError, KeyError, ValueError, TypeError, IndexError):
+        good = False
+    if not good:
+        _scan_refuse(x, dt, B, C, z, state)
     ap, (ah, ak, av) = _per_channel(A, (nv, K, V), "A", dev)
-    if not ap:
-        _tensors(A=A)
-    dp, (dh, dv) = _per_channel(D, (nv, V), "D", dev)
-    bp, (bh, bv) = _per_channel(dt_bias, (nv, V), "dt_bias", dev)
+    dp, (dh, dv) = (0, _NO2) if D is None else _per_channel(D, (nv, V), "D", dev)
+    bp, (bh, bv) = (0, _NO2) if dt_bias is None else _per_channel(dt_bias, (nv, V), "dt_bias", dev)
     n, slot, off, cnt = _ragged(slot_idx, offsets, counts, keep_state, state_only, dev)
-    (xt, xh, _), (tt, th, te), (Bt, Bh, _), (Ct, Ch, _) = x.stride(), dt.stride(), B.stride(), C.stride()
-    ot, oh = (0, 0) if out is None else out.stride()[:2]
+    out, op, (ot, oh, _) = _output(out, x, state_only)
     ss, sh, sk, sv = state.stride()
-    return _pack_scan(n, nv, B.shape[1], K, V, 1 if dt_softplus else 0, td, dd, sd, 1 if keep_state else 0, T, int(max_row_len),
+    return _pack_scan(n, nv, bshape[1], K, V, 1 if dt_softplus else 0, td, dd, sd, 1 if keep_state else 0, T, int(max_row_len),
                       x.data_ptr(), xt, xh, dt.data_ptr(), tt, th, te if V > 1 else 1, B.data_ptr(), Bt, Bh, C.data_ptr(), Ct,
-                      Ch, zp, zt, zh, ap, ah, ak, av, dp, dh, dv, bp, bh, bv, 0 if out is None else out.data_ptr(), ot, oh,
-                      state.data_ptr(), ss, sh, sk, sv, slots, slot, off, cnt, 0, 0), out
+                      Ch, zp, zt, zh, ap, ah, ak, av, dp, dh, dv, bp, bh, bv, op, ot, oh, state.data_ptr(), ss, sh, sk, sv, slots,
+                      slot, off, cnt, 0, 0), out
 
 
 def _scan_workspace(lib, args: bytes, device, workspace):
@@ -1081,7 +1090,7 @@ def gdr_selective_scan(x, dt, A, B, C, state, slot_idx, offsets, out=None, *, D=
     args, out = _scan_args(x, dt, A, B, C, state, slot_idx, offsets, out, D, z, dt_bias, dt_softplus, counts, keep_state,
                            state_only, max_row_len)
     lib = _lib or load_library()
-    if max_row_len != 1:
+    if workspace is not None or not 1 <= max_row_len <= 16:  # rows so short are never cut
         args, workspace = _scan_workspace(lib, args, x.device, workspace)
     rc = _launch(lib.gdr_selective_scan, args, x.get_device())
     if rc:
@@ -1101,20 +1110,29 @@ def prepare_selective_scan(x, dt, A, B, C, state, slot_idx, offsets, out, *, D=N
                     (x, dt, A, B, C, state, slot_idx, offsets, out, D, z, dt_bias, counts, workspace), x.device)
 
 
+def _floats(t, n: int, name: str, device) -> int:
+    """The pointer of a contiguous [n] float32 tensor."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _F32 and t.device == device):
+        _refuse(device, {name: _F32}, **{name: t})
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{n}] float32 tensor")
+    return t.data_ptr()
+
+
 def _accept_args(target, draft, tokens, offsets, uniforms, row_uniforms, max_row_len, out, counts):
     """(packed gdr_accept_args, out, counts)."""
     if not isinstance(target, torch.Tensor):
         _tensors(target=target)
-    dev = target.device
+    dev, shape, (pt, *pc) = target.device, target.shape, target.stride() or (0,)
     pd = _float(target, "target", dev)
-    if target.dim() != 2 or (target.shape[1] > 1 and target.stride(1) != 1):
+    if len(shape) != 2 or (pc[0] != 1 and shape[1] > 1):
         raise ValueError("target must be [T, vocab] with a unit stride along the vocabulary")
-    T, vocab = target.shape
+    T, vocab = shape
     qp, qt = 0, 0
     if draft is not None:
         if not isinstance(draft, torch.Tensor) or draft.dtype != target.dtype or draft.device != dev:
             _refuse(dev, {"draft": target.dtype}, draft=draft)
-        if draft.shape != target.shape or (vocab > 1 and draft.stride(1) != 1):
+        if draft.shape != shape or (vocab > 1 and draft.stride(1) != 1):
             raise ValueError("draft must have target's shape and a unit stride along the vocabulary")
         qp, qt = draft.data_ptr(), draft.stride(0)
     if not isinstance(offsets, torch.Tensor):
@@ -1125,22 +1143,21 @@ def _accept_args(target, draft, tokens, offsets, uniforms, row_uniforms, max_row
     if width < 1:
         raise ValueError("max_row_len must be at least 1 (it is the width of the returned tokens)")
     off, tok = _ints(offsets, (n + 1,), "offsets", dev), _ints(tokens, (T,), "tokens", dev)
-    for name, t, size in (("uniforms", uniforms, T), ("row_uniforms", row_uniforms, n)):
-        if not (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.device == dev):
-            _refuse(dev, {name: torch.float32}, **{name: t})
-        if t.shape != (size,) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous [{size}] float32 tensor")
+    up, vp = _floats(uniforms, T, "uniforms", dev), _floats(row_uniforms, n, "row_uniforms", dev)
     if out is None:
-        out = torch.empty((n, width), dtype=torch.int32, device=dev)
+        out, ot = torch.empty((n, width), dtype=_I32, device=dev), width
     else:
-        if not (isinstance(out, torch.Tensor) and out.dtype is torch.int32 and out.device == dev):
-            _refuse(dev, {"out": torch.int32}, out=out)
+        if not (isinstance(out, torch.Tensor) and out.dtype is _I32 and out.device == dev):
+            _refuse(dev, {"out": _I32}, out=out)
         if out.shape != (n, width) or (width > 1 and out.stride(1) != 1):
             raise ValueError(f"out must be [{n}, {width}] with a unit stride along a row")
+        ot = out.stride(0)
     if counts is None:
-        counts = torch.empty(n, dtype=torch.int32, device=dev)
-    return _pack_accept(n, vocab, pd, width, T, target.data_ptr(), target.stride(0), qp, qt, tok, off, uniforms.data_ptr(),
-                        row_uniforms.data_ptr(), out.data_ptr(), out.stride(0), _ints(counts, (n,), "counts", dev)), out, counts
+        counts = torch.empty(n, dtype=_I32, device=dev)
+        cp = counts.data_ptr()
+    else:
+        cp = _ints(counts, (n,), "counts", dev)
+    return _pack_accept(n, vocab, pd, width, T, target.data_ptr(), pt, qp, qt, tok, off, up, vp, out.data_ptr(), ot, cp), out, counts
 
 
 def gdr_accept_drafts(target, draft, tokens, offsets, uniforms, row_uniforms, *, max_row_len, out=None, counts=None):
