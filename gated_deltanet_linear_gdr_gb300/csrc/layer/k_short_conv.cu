@@ -8,7 +8,7 @@
 // written once.  A few operations a byte: HBM bound; what counts is bytes in
 // flight, so kAhead tokens are asked for before the first is used.
 //
-// Two ways to deal the work out.  A block takes a whole row where rows are short
+// Two ways to deal the work out.  A block takes whole rows where they are short
 // (single tokens, drafts).  Otherwise it takes a run of tokens, whichever rows
 // they are of, so that ragged rows fill the GPU evenly; what is read twice are the
 // width-1 tokens before a run.  The tokens of a row that need its slot's old
@@ -23,7 +23,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kAhead = 8;      // tokens of a batch
-constexpr int kShortRow = 16;  // rows up to here are a block's unit
+constexpr int kShortRow = 16;  // rows up to here are taken whole
+constexpr int kRows = 16;      // by blocks of so many at most
 
 struct ConvRow {
     long long lo, hi;  // its tokens
@@ -130,32 +131,42 @@ template <typename TT, int W, int VE> struct ConvThread {
         }
     }
 
+    // A slot's inputs, and a row's first token.
+    struct Start {
+        float v[VE * N];
+        Pack<TT, VE> x;
+    };
+    __device__ __forceinline__ void ask_start(Start &s, int slot, long long lo) const {
+        if constexpr (W > 1) {
+            if (p.st_bf16) read<uint16_t>(slot, s.v);
+            else read<float>(slot, s.v);
+        }
+        s.x.load(x(lo));
+    }
     // A row's beginning: the slot's inputs into the window, and the slot's new ones, which are
     // entries kept .. kept + W - 2 of (old inputs, the row's inputs).
-    __device__ __forceinline__ void begin(const ConvRow &r) {
+    __device__ __forceinline__ void begin(const Start &s, int slot, long long lo, int kept) {
         if constexpr (W > 1) {
-            float v[VE * N];
-            if (p.st_bf16) read<uint16_t>(r.slot, v);
-            else read<float>(r.slot, v);
 #pragma unroll
-            for (int i = 0; i < VE * N; ++i) win[i % N][i / N] = v[i];
-            if (r.kept <= 0) return;
+            for (int i = 0; i < VE * N; ++i) win[i % N][i / N] = s.v[i];
+            if (kept <= 0) return;
+            float v[VE * N];
 #pragma unroll
             for (int m = 0; m < N; ++m) {
-                const int i = r.kept + m;  // entry of (old inputs, the row's)
-                Pack<TT, VE> in;
-                if (i >= N) in.load(x(r.lo + i - N));
+                const int i = kept + m;  // entry of (old inputs, the row's)
+                Pack<TT, VE> in = s.x;
+                if (i > N) in.load(x(lo + i - N));
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    float y = i >= N ? in.get(e) : 0.0f;
+                    float y = in.get(e);
 #pragma unroll
                     for (int j = 1; j < N; ++j)
                         if (i == j) y = win[j][e];
                     v[e * N + m] = y;
                 }
             }
-            if (p.st_bf16) write<uint16_t>(r.slot, v);
-            else write<float>(r.slot, v);
+            if (p.st_bf16) write<uint16_t>(slot, v);
+            else write<float>(slot, v);
         }
     }
     // The window in front of token t, all of it in the row.
@@ -235,20 +246,19 @@ template <typename TT, int W, int VE> struct ConvThread {
             to += p.o_ts;
         }
     }
-    // A short row, four tokens at a time.
-    __device__ __forceinline__ void short_run(long long s, int n) {
+    // A short row behind its first token, four tokens at a time.
+    __device__ __forceinline__ void short_run(const Pack<TT, VE> &first, long long s, int n) {
         const TT *from = x(s);
         TT *to = out(s);
-        for (; n > 0; n -= 4) {
+        token(first, to);
+        for (int t = 1; t < n; t += 4) {
             Pack<TT, VE> in[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (i < n) in[i].load(from + i * p.x_ts);
+                if (t + i < n) in[i].load(from + (t + i) * p.x_ts);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (i < n) token(in[i], to + i * p.o_ts);
-            from += 4 * p.x_ts;
-            to += 4 * p.o_ts;
+                if (t + i < n) token(in[i], to + (t + i) * p.o_ts);
         }
     }
     __device__ __forceinline__ void clear(long long s, long long e) {
@@ -259,25 +269,44 @@ template <typename TT, int W, int VE> struct ConvThread {
     }
 };
 
-// ROWS: a block takes a row's channels; else a run of tokens.
+// ROWS: a block takes whole rows, `run` of them; else a run of tokens.
 template <typename TT, int W, int VE, bool ROWS>
 __global__ void __launch_bounds__(kThreads) k_short_conv(const __grid_constant__ ConvOpParams p) {
     const unsigned block = blockIdx.x / (unsigned)p.tiles, tile = blockIdx.x - block * (unsigned)p.tiles;
     const int tid = threadIdx.x, c0 = (int)(tile * kThreads + threadIdx.x) * VE;
     const bool on = c0 < p.channels;
-    ConvThread<TT, W, VE> th(p, c0);
+    using Thread = ConvThread<TT, W, VE>;
+    Thread th(p, c0);
     if constexpr (ROWS) {
-        if (on && p.out) th.weights();
-        const ConvRow r = conv_row(p, (int)block);
-        if (r.problem && tile == 0 && tid == 0) flag(p.status, r.problem);
-        if (!on || !r.inside) return;
-        if (r.slot < 0) {
-            if (p.out) th.clear(r.lo, r.hi);
-            return;
+        __shared__ ConvRow rows[kRows];
+        const int b0 = (int)block * p.run, n = min(p.run, p.batch - b0);
+        if (tid < n) {
+            const ConvRow r = conv_row(p, b0 + tid);
+            if (r.problem && tile == 0) flag(p.status, r.problem);
+            rows[tid] = r;
         }
-        th.begin(r);
-        if (p.out) th.short_run(r.lo, (int)(r.hi - r.lo));
-        return;
+        if (on && p.out) th.weights();
+        __syncthreads();
+        if (!on) return;
+        // two rows at a time, so that twice the bytes are on their way
+        auto live = [&](int i) { return i < n && rows[i].slot >= 0 && (p.out || rows[i].kept > 0); };
+        auto row = [&](int i, const typename Thread::Start &s) {
+            if (i >= n) return;
+            const ConvRow &r = rows[i];
+            if (live(i)) {
+                th.begin(s, r.slot, r.lo, r.kept);
+                if (p.out) th.short_run(s.x, r.lo, (int)(r.hi - r.lo));
+            } else if (p.out && r.inside) {
+                th.clear(r.lo, r.hi);
+            }
+        };
+        for (int i = 0; i < n; i += 2) {
+            typename Thread::Start a, b;
+            if (live(i)) th.ask_start(a, rows[i].slot, rows[i].lo);
+            if (live(i + 1)) th.ask_start(b, rows[i + 1].slot, rows[i + 1].lo);
+            row(i, a);
+            row(i + 1, b);
+        }
     } else {
         if (blockIdx.x == 0)  // one block looks at every row
             for (int b = tid; b < p.batch; b += kThreads) {
@@ -304,8 +333,13 @@ __global__ void __launch_bounds__(kThreads) k_short_conv(const __grid_constant__
                 th.clear(s, e);
                 continue;
             }
-            if (first) th.begin(r);
-            else th.enter(s);
+            if (first) {
+                typename Thread::Start start;
+                th.ask_start(start, r.slot, r.lo);
+                th.begin(start, r.slot, r.lo, r.kept);
+            } else {
+                th.enter(s);
+            }
             th.run(s, e);
         }
     }
@@ -318,8 +352,13 @@ template <typename TT, int W> cudaError_t go(ConvOpParams p, cudaStream_t s) {
     // Rows' lengths as far as the caller bounds them: a block a row where none is longer than
     // kShortRow tokens, and where only states move.
     const bool rows = !p.out || (p.max_len > 0 && p.max_len <= kShortRow);
-    long long blocks = p.batch;
-    if (!rows) {
+    long long blocks;
+    if (rows) {
+        // as many rows a block as leaves each multiprocessor eight blocks
+        const long long each = ((long long)p.batch * p.tiles + 152 * 8 - 1) / (152 * 8);
+        p.run = (int)(each < kRows ? each : kRows);
+        blocks = ((long long)p.batch + p.run - 1) / p.run;
+    } else {
         // runs of up to 64 tokens, shorter ones where they would leave multiprocessors without work
         p.run = 64;
         while (p.run > 8 && (p.T + p.run - 1) / p.run * p.tiles < 152 * 12) p.run /= 2;
