@@ -177,36 +177,43 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 3 : KT
             }
             return y;
         };
-        __syncthreads();
-        for (int k = 0; k <= chunks; ++k) {
-            if (k < chunks) {
-                const int n = u.len - k * N, cut = u.kept - k * N;  // tokens behind n are d = 0, d x = 0
-                const float *d = floats(Sh::fd) + (k & 1) * N * W + 2 * lane, *x = floats(Sh::fx) + (k & 1) * N * W + 2 * lane;
-                const float *b = floats(Sh::fB) + (k & 1) * N * KP + warp * KT, *q = floats(Sh::fC) + (k & 1) * N * KP + warp * KT;
-                float *y = floats(Sh::fy) + ((k & 1) * NW + warp) * N * W + 2 * lane;
-                if (!first && cut > 0 && cut < N && cut < n) {  // the slot's state lies inside
+        auto chunk = [&](auto half, int n, int cut) {  // tokens from the chunk on, and those of them before the slot's state
+            constexpr int H = decltype(half)::value;
+            const float *const d = floats(Sh::fd) + H * N * W + 2 * lane, *const x = floats(Sh::fx) + H * N * W + 2 * lane;
+            const float *const b = floats(Sh::fB) + H * N * KP + warp * KT, *const q = floats(Sh::fC) + H * N * KP + warp * KT;
+            float *const y = floats(Sh::fy) + (H * NW + warp) * N * W + 2 * lane;
+            const bool here = (unsigned)(cut - 1) < (unsigned)N;
+            if (here && cut < n && cut < N) {  // the slot's state lies inside
 #pragma unroll 1
-                    for (int t = 0; t < N; ++t) {
-                        const float2 v = token(d + t * W, x + t * W, b + t * KP, q + t * KP);
-                        if (READ) *reinterpret_cast<float2 *>(y + t * W) = v;
-                        if (t + 1 == cut) put();
-                    }
-                } else {
-#pragma unroll
-                    for (int t0 = 0; t0 < N; t0 += 4) {
-                        if (t0 >= n) break;
-                        float2 v[4];
-#pragma unroll
-                        for (int t = 0; t < 4; ++t)
-                            v[t] = token(d + (t0 + t) * W, x + (t0 + t) * W, b + (t0 + t) * KP, q + (t0 + t) * KP);
-                        if (READ)
-#pragma unroll
-                            for (int t = 0; t < 4; ++t) *reinterpret_cast<float2 *>(y + (t0 + t) * W) = v[t];
-                    }
-                    if (!first && cut > 0 && cut <= N) put();  // behind the chunk, or behind the row's last token
+                for (int t = 0; t < N; ++t) {
+                    const float2 v = token(d + t * W, x + t * W, b + t * KP, q + t * KP);
+                    if (READ) *reinterpret_cast<float2 *>(y + t * W) = v;
+                    if (t + 1 == cut) put();
                 }
+                return;
             }
+#pragma unroll
+            for (int t0 = 0; t0 < N; t0 += 4) {  // tokens behind the row's end are d = 0, d x = 0
+                float2 v[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    v[t] = token(d + (t0 + t) * W, x + (t0 + t) * W, b + (t0 + t) * KP, q + (t0 + t) * KP);
+                if (READ)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) *reinterpret_cast<float2 *>(y + (t0 + t) * W) = v[t];
+            }
+            if (here) put();  // behind the chunk, or behind the row's last token
+        };
+        __syncthreads();
+        int n = u.len, cut = first ? 0 : u.kept;
+        for (int k = 0; k <= chunks; ++k) {
+            if (k < chunks) chunk(std::integral_constant<int, 0>{}, n, cut);
             __syncthreads();
+            if (++k > chunks) break;
+            if (k < chunks) chunk(std::integral_constant<int, 1>{}, n - N, cut - N);
+            __syncthreads();
+            n -= 2 * N;
+            cut -= 2 * N;
         }
         if (first) put();
         return;
@@ -275,8 +282,8 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 3 : KT
             fb_at[i] = v < N * KP ? bp + w / KP * p.B_ts + w % KP : cp + w / KP * p.C_ts + w % KP;
         }
     const long long dx = N * p.x_ts, dz = N * p.z_ts, dd = N * p.dt_ts;
-    int ahead = 0, f_at = 0;  // tokens asked for, the ring's next place
-    auto fetch = [&]() {
+    int ahead = 0;  // tokens asked for
+    auto fetch = [&](int f_at) {
         const int n = u.len - ahead;
         if (n > 0) {
             unsigned char *const to = shared + f_at;
@@ -308,11 +315,10 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 3 : KT
         }
         cp_async_commit();
         ahead += N;
-        f_at = f_at == (R - 1) * Sh::stage ? 0 : f_at + Sh::stage;
     };
-    // What waited, to its place: that of the chunk asked for last.
-    auto land = [&]() {
-        unsigned char *const to = shared + (f_at == 0 ? R - 1 : f_at / Sh::stage - 1) * Sh::stage;
+    // What waited, to its place.
+    auto land = [&](int f_at) {
+        unsigned char *const to = shared + f_at;
         if constexpr (!VEC && sizeof(DT) == 2)
 #pragma unroll
             for (int i = 0; i < 4; ++i) reinterpret_cast<DT *>(to + Sh::dt)[at(i)] = wd[i];
@@ -391,12 +397,12 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 3 : KT
             }
         }
     };
-    // Turn k finishes chunk k - 1, makes chunk k + 1 ready and asks for chunk k + Dist: the ring
-    // holds chunks k - 1 ... k + Dist - 1.
+    // Turn k finishes chunk k - 1, makes chunk k + 1 ready and asks for chunk k + Dist, which takes chunk
+    // k - 1's place in the ring.
     constexpr int Dist = R - 1;
     for (int k = 0; k < Dist; ++k) {
-        fetch();
-        land();
+        fetch(k * Sh::stage);
+        land(k * Sh::stage);
     }
     cp_async_wait<Dist - 1>();
     {
@@ -412,12 +418,15 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 3 : KT
     int done_at = (R - 1) * Sh::stage, next_at = Sh::stage;  // chunks k - 1 and k + 1 in the ring
     TT *out = READ ? op - (long long)N * p.o_ts : nullptr;
     const long long dout = N * p.o_ts;
-    for (int k = 0; k <= chunks; ++k) {
-        if (k > 0) land();
+    // WHOLE: all three chunks are whole and all values vectors, so that nothing has to be asked
+    auto turn = [&](auto whole, int k) {
+        constexpr bool WHOLE = decltype(whole)::value;
         cp_async_wait<Dist - 2>();
-        const int half = (k + 1) & 1;  // both neighbours' half of the buffers in pairs
-        float d[4], x[4], rx[4], rz[4], y[4];
-        const unsigned char *const next = shared + next_at, *const done = shared + done_at;
+        const int half = (k + 1) & 1, left = u.len - k * N;  // both neighbours' half of the buffers in pairs
+        [[maybe_unused]] float rx[4], rz[4], y[4];
+        [[maybe_unused]] const unsigned char *const done = shared + done_at;
+        float d[4], x[4];
+        const unsigned char *const next = shared + next_at;
         four(reinterpret_cast<const DT *>(next + Sh::dt), d);
         four(reinterpret_cast<const TT *>(next + Sh::x), x);
         if constexpr (READ) {
@@ -433,10 +442,42 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 3 : KT
                 for (int i = 0; i < 4; ++i) y[i] += q[i];
             }
         }
-        steps(d, x, u.len - (k + 1) * N);
+        if constexpr (WHOLE) {
+            unsigned char *const to = shared + done_at;  // this thread's own values there are in registers by now
+            cp_async<4 * (int)sizeof(DT)>(reinterpret_cast<DT *>(to + Sh::dt) + at(0), fd_at);
+            cp_async<4 * (int)sizeof(TT)>(reinterpret_cast<TT *>(to + Sh::x) + at(0), fx_at);
+            if (READ && zp) cp_async<4 * (int)sizeof(TT)>(reinterpret_cast<TT *>(to + Sh::z) + at(0), fz_at);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int v = 4 * (id + i * kScanHelpers);
+                if (v < NB) {
+                    cp_async<4 * (int)sizeof(TT)>(reinterpret_cast<TT *>(to + Sh::B) + v, fb_at[i]);
+                    fb_at[i] += N * (v < N * KP ? p.B_ts : p.C_ts);
+                }
+            }
+            cp_async_commit();
+            fx_at += dx;
+            fz_at += dz;
+            fd_at += dd;
+            ahead += N;
+        }
+        steps(d, x, WHOLE ? N : left - N);
         put4(floats(Sh::fd) + half * N * W, d);
         put4(floats(Sh::fx) + half * N * W, x);
-        states(next, half, u.len - (k + 1) * N);
+        if constexpr (WHOLE) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int v = 4 * (id + i * kScanHelpers);
+                if (v < NB) {
+                    Pack<TT, 4> q;
+                    q.load(reinterpret_cast<const TT *>(next + Sh::B) + v);
+                    *reinterpret_cast<float4 *>(floats(v < N * KP ? Sh::fB : Sh::fC - 4 * N * KP) + half * N * KP + v) =
+                        make_float4(q.get(0), q.get(1), q.get(2), q.get(3));
+                }
+            }
+        } else {
+            states(next, half, left - N);
+        }
         if constexpr (READ) {
             Pack<TT, 4> o;
 #pragma unroll
@@ -445,21 +486,35 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 3 : KT
                 if (zp) y[i] *= silu(rz[i]);
                 o.set(i, y[i]);
             }
-            const int n = mon && k > 0 ? u.len - (k - 1) * N - mt : 0;
-            if constexpr (VEC) {
-                if (n > 0) o.store(out);
+            if constexpr (WHOLE) {
+                o.store(out);
             } else {
+                const int n = mon && k > 0 ? left + N - mt : 0;
+                if constexpr (VEC) {
+                    if (n > 0) o.store(out);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < n) out[i * p.o_ts] = o.u.e[i];
+                    for (int i = 0; i < 4; ++i)
+                        if (i < n) out[i * p.o_ts] = o.u.e[i];
+                }
             }
             out += dout;
         }
-        fetch();
+        if constexpr (!WHOLE) {
+            fetch(done_at);
+            land(done_at);
+        }
         done_at = done_at == (R - 1) * Sh::stage ? 0 : done_at + Sh::stage;
         next_at = next_at == (R - 1) * Sh::stage ? 0 : next_at + Sh::stage;
         __syncthreads();
-    }
+    };
+    // chunks k - 1 ... k + Dist are whole for 1 <= k <= last
+    const int last = VEC && bc_vec && width == W ? u.len / N - 1 - Dist : 0;
+    turn(std::false_type{}, 0);
+    int k = 1;
+    if constexpr (VEC)
+        for (; k <= last; ++k) turn(std::true_type{}, k);
+    for (; k <= chunks; ++k) turn(std::false_type{}, k);
     if (first) {
         // each channel's step sizes, over the threads that have its tokens
         float *const part = floats(0);
