@@ -164,16 +164,34 @@ int check_scan(const gdr_scan_args *a, const char *fn) {
 // 27 / 101, of 8 64 / 107, of 12 89 / 115, of 16 111 / 121.
 constexpr int kShortRow = 16;
 
-// Tokens a segment for rows that are cut, or 0.
+// Tokens a segment for rows that are cut, or 0.  A block does 64 channels of a row from end to end, so a call
+// lasts as long as its longest row, or as the fullest multiprocessor; a token of a block that has its
+// multiprocessor to itself takes 0.6 of the time of one that shares it with a second.  Cut rows spread evenly, and
+// cost a pass for the segments' own states (0.65 of a token's time a token), 48 tokens' time a segment to
+// begin and end and 250 tokens' for two more launches.  Measured, cut against whole, 16 states, us: 16383 tokens x 2048
+// channels 287 (864 tokens a segment; 2048: 330, 304: 320) against 915, 2048 x 2048 61 (256) / 123, 4 rows of 1024 to 4096 x 512 86 / 235;
+// left whole by this rule: 2 rows of 4096 x 4096 287 / 237.
 int plan_scan(const gdr_scan_args *a) {
-    if (a->batch < 1 || a->batch > 32 || a->max_row_len == 1 || !a->total_tokens) return 0;
-    const double warps = 152.0 * 4 * 6, lanes = 32.0 / (a->K <= 32 ? 4 : a->K <= 64 ? 8 : 16);
-    const double units = a->batch * std::ceil((double)a->nv * a->V / (4 * lanes));
-    const double longest = a->max_row_len > 0 ? (double)a->max_row_len : (double)a->total_tokens / a->batch;
-    if (units > 152.0 * 4 || longest < 1024) return 0;
-    double seg = std::ceil((double)a->total_tokens * (units / a->batch) / warps / 16) * 16;
-    if (seg < 256) seg = 256;
-    return seg * 2 > longest ? 0 : (int)seg;
+    if (a->batch < 1 || a->batch > 32 || !a->total_tokens || (a->max_row_len >= 1 && a->max_row_len <= kShortRow)) return 0;
+    const double tiles = a->nk * std::ceil((double)a->nv / a->nk * a->V / 64), T = (double)a->total_tokens;
+    const double sms = 152.0, slots = a->K <= 32 ? 2 * sms : sms;
+    double longest = a->max_row_len > 0 ? (double)a->max_row_len : std::ceil(T / a->batch);
+    if (longest > T) longest = T;
+    constexpr double kAlone = 0.6, kFirst = 0.65, kUnit = 48.0, kExtra = 250.0;
+    const auto share = [&](double blocks) { return blocks <= sms ? kAlone : 1.0; };
+    double best = std::fmax(longest * share(a->batch * tiles), T * tiles / slots);
+    int seg = 0;
+    for (int n = 2; n <= 64; ++n) {
+        const double len = std::ceil(longest / n / 8) * 8;
+        if (len < 128) break;
+        const double blocks = std::ceil(T / len + 0.5 * (a->batch - 1)) * tiles;
+        const double cost = std::ceil(blocks / slots) * (len + kUnit) * share(blocks) * (1 + kFirst) + kExtra;
+        if (cost < 0.9 * best) {
+            best = cost / 0.9;
+            seg = (int)len;
+        }
+    }
+    return seg;
 }
 
 int64_t scan_bytes(const gdr_scan_args *a, int seg) {

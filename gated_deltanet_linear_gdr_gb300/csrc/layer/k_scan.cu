@@ -26,13 +26,25 @@ __global__ void __launch_bounds__(256) k_scan_join(const __grid_constant__ ScanP
     float S = p.st_bf16 ? to_f32(static_cast<const uint16_t *>(p.state)[at]) : static_cast<const float *>(p.state)[at];
     float *own = p.ws + piece * per + i;
     const float *sum = p.ws + most * per + piece * p.nv * p.V + (long long)h * p.V + v;
-    for (int s = 0; s < n && piece + s < most; ++s) {
-        const bool last = s + 1 == n;
-        const float o = last ? 0.0f : *own, d = last ? 0.0f : *sum;
-        *own = S;
-        S = fmaf(expf(a * d), S, o);
-        own += per;
-        sum += (long long)p.nv * p.V;
+    // eight segments' values on their way at a time
+    constexpr int kAhead = 8;
+    n = (int)(most - piece < n ? most - piece : n);
+    for (int s = 0; s < n; s += kAhead) {
+        float o[kAhead], d[kAhead];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            const bool some = s + q + 1 < n;  // nothing starts from the last one's state
+            o[q] = some ? own[q * per] : 0.0f;
+            d[q] = some ? sum[q * (long long)p.nv * p.V] : 0.0f;
+        }
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q)
+            if (s + q < n) {
+                own[q * per] = S;
+                S = fmaf(expf(a * d[q]), S, o[q]);
+            }
+        own += kAhead * per;
+        sum += kAhead * (long long)p.nv * p.V;
     }
 }
 

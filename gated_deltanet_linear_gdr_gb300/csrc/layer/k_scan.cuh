@@ -55,10 +55,21 @@ __device__ __forceinline__ bool scan_piece(const ScanParams &p, long long piece,
     return true;
 }
 
+// The n-th longest of up to 32 rows: blocks run in their order, and what comes last should be short.
+__device__ __forceinline__ unsigned scan_longest(const ScanParams &p, unsigned n, int lane) {
+    const int len = lane < p.batch ? p.offsets[lane + 1] - p.offsets[lane] : 0;
+    unsigned rank = 0;
+    for (int j = 0; j < p.batch; ++j) {
+        const int o = __shfl_sync(kFull, len, j);
+        rank += o > len || (o == len && j < lane);
+    }
+    return (unsigned)__ffs(__ballot_sync(kFull, lane < p.batch && rank == n)) - 1;
+}
+
 // A block's shared memory, in bytes: a ring of raw chunks, then two chunks' operands in
 // float32 and the readout's partial sums.
 template <typename TT, typename DT, int KT, int NW> struct ScanShared {
-    static constexpr int W = kScanTile, KP = KT * NW, N = kScanChunk, ring = sizeof(TT) == 2 && KP <= 32 ? 8 : 4;
+    static constexpr int W = kScanTile, KP = KT * NW, N = kScanChunk, ring = 4;
     static constexpr int x = 0, z = x + N * W * (int)sizeof(TT), dt = z + N * W * (int)sizeof(TT), B = dt + N * W * (int)sizeof(DT),
                          C = B + N * KP * (int)sizeof(TT), stage = C + N * KP * (int)sizeof(TT);
     static constexpr int fd = ring * stage, fx = fd + 2 * 4 * N * W, fB = fx + 2 * 4 * N * W, fC = fB + 2 * 4 * N * KP,
@@ -68,15 +79,18 @@ template <typename TT, typename DT, int KT, int NW> struct ScanShared {
 // READ: with outputs.  Without them states move only: into the slots, or (first != 0)
 // each segment's own state, from zero, and the sum of its step sizes into the workspace.
 template <typename TT, typename DT, int KT, int NW, bool VEC, bool READ>
-__global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 3 : KT * NW <= 32 ? 2 : 1)
+__global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT * NW <= 32 ? 2 : 1)
     k_scan(const __grid_constant__ ScanParams p, int tiles, int first) {
     using Sh = ScanShared<TT, DT, KT, NW>;
     constexpr int W = Sh::W, KP = Sh::KP, N = Sh::N, R = Sh::ring;
     extern __shared__ __align__(16) unsigned char shared[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const unsigned all = (unsigned)(p.nk * tiles), row = blockIdx.x / all, tg = blockIdx.x - row * all;
+    const unsigned all = (unsigned)(p.nk * tiles);
+    unsigned row = blockIdx.x / all;
+    const unsigned tg = blockIdx.x - row * all;
     const int g = (int)(tg / (unsigned)tiles), tile = (int)(tg - (unsigned)g * (unsigned)tiles);
     ScanUnit u;
+    if (!p.seg && p.batch <= 32) row = scan_longest(p, row, lane);
     if (p.seg) {
         if (!scan_piece(p, row, tg == 0 && warp == 0 && !first, lane, u)) return;
         if (first && u.last) return;  // no segment starts from its state
@@ -168,11 +182,9 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 3 : KT
 #pragma unroll
             for (int i = 0; i < KT; ++i) {
                 const float2 e = __fmul2_rn(dv, A[i]);
-                S[i].x = fmaf(decay<TT>(e.x), S[i].x, xv.x * Bv[i]);
-                S[i].y = fmaf(decay<TT>(e.y), S[i].y, xv.y * Bv[i]);
+                S[i] = __ffma2_rn(make_float2(decay<TT>(e.x), decay<TT>(e.y)), S[i], __fmul2_rn(xv, make_float2(Bv[i], Bv[i])));
                 if (READ) {
-                    y.x = fmaf(Cv[i], S[i].x, y.x);
-                    y.y = fmaf(Cv[i], S[i].y, y.y);
+                    y = __ffma2_rn(make_float2(Cv[i], Cv[i]), S[i], y);
                 }
             }
             return y;
