@@ -304,20 +304,23 @@ int gdr_selective_scan(const gdr_scan_args *a, void *stream) {
     p.offsets = a->offsets;
     p.counts = a->counts;
     const bool tb = a->token_dtype == GDR_BF16;
-    const bool vec = a->V % 8 == 0 && vector_rows(a->x, a->token_dtype, 16, p.x_ts, p.x_hs) &&
-                     p.dt_es == 1 && vector_rows(a->dt, a->dt_dtype, 16, p.dt_ts, p.dt_hs) &&
-                     (!a->out || vector_rows(a->out, a->token_dtype, 16, p.o_ts, p.o_hs)) &&
-                     (!a->z || vector_rows(a->z, a->token_dtype, 16, p.z_ts, p.z_hs)) &&
+    // vectors of four values
+    const int64_t four = 4 * esize(a->token_dtype);
+    const bool vec = a->V % 4 == 0 && vector_rows(a->x, a->token_dtype, four, p.x_ts, p.x_hs) && p.dt_es == 1 &&
+                     vector_rows(a->dt, a->dt_dtype, 4 * esize(a->dt_dtype), p.dt_ts, p.dt_hs) &&
+                     (!a->out || vector_rows(a->out, a->token_dtype, four, p.o_ts, p.o_hs)) &&
+                     (!a->z || vector_rows(a->z, a->token_dtype, four, p.z_ts, p.z_hs)) &&
                      vector_rows(a->state, a->state_dtype, 4 * esize(a->state_dtype), p.st_slot, p.st_head, p.st_k);
-    p.bc_vec = vector_rows(a->B, a->token_dtype, 16, p.B_ts, p.B_hs) && (!a->C || vector_rows(a->C, a->token_dtype, 16, p.C_ts, p.C_hs));
-    p.a_vec = p.a_vs == 1 && vector_rows(a->A, GDR_F32, 16, p.a_hs, p.a_ks);
+    p.bc_vec = vector_rows(a->B, a->token_dtype, four, p.B_ts, p.B_hs) &&
+               (!a->out || vector_rows(a->C, a->token_dtype, four, p.C_ts, p.C_hs));
     p.seg = plan_scan(a);
     if (p.seg && (!a->workspace || a->workspace_bytes < scan_bytes(a, p.seg))) p.seg = 0;
     p.ws = static_cast<float *>(a->workspace);
     const bool db = a->dt_dtype == GDR_BF16;
     if (a->max_row_len >= 1 && a->max_row_len <= kShortRow) {
-        const bool all = vec && a->K % (a->K <= 16 ? 4 : a->K <= 32 ? 8 : a->K <= 64 ? 16 : 32) == 0 && vector_rows(a->B, a->token_dtype, 4 * esize(a->token_dtype), p.B_ts, p.B_hs) &&
-                         (!a->out || vector_rows(a->C, a->token_dtype, 4 * esize(a->token_dtype), p.C_ts, p.C_hs));
+        // four warps have KT states each: vectors where all of them do, or none
+        const int KT = a->K <= 16 ? 4 : a->K <= 32 ? 8 : a->K <= 64 ? 16 : 32;
+        const bool all = vec && p.bc_vec && a->K % KT == 0;
         return launched(gdr::launch_scan_step(p, tb, db, all, static_cast<cudaStream_t>(stream)), fn);
     }
     return launched(gdr::launch_scan(p, tb, db, vec, static_cast<cudaStream_t>(stream)), fn);

@@ -69,7 +69,7 @@ __device__ __forceinline__ unsigned scan_longest(const ScanParams &p, unsigned n
 // A block's shared memory, in bytes: a ring of raw chunks, then two chunks' operands in
 // float32 and the readout's partial sums.
 template <typename TT, typename DT, int KT, int NW> struct ScanShared {
-    static constexpr int W = kScanTile, KP = KT * NW, N = kScanChunk, ring = 4;
+    static constexpr int W = kScanTile, KP = KT * NW, N = kScanChunk, ring = 5;
     static constexpr int x = 0, z = x + N * W * (int)sizeof(TT), dt = z + N * W * (int)sizeof(TT), B = dt + N * W * (int)sizeof(DT),
                          C = B + N * KP * (int)sizeof(TT), stage = C + N * KP * (int)sizeof(TT);
     static constexpr int fd = ring * stage, fx = fd + 2 * 4 * N * W, fB = fx + 2 * 4 * N * W, fC = fB + 2 * 4 * N * KP,
@@ -294,9 +294,9 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
             fb_at[i] = v < N * KP ? bp + w / KP * p.B_ts + w % KP : cp + w / KP * p.C_ts + w % KP;
         }
     const long long dx = N * p.x_ts, dz = N * p.z_ts, dd = N * p.dt_ts;
-    int ahead = 0;  // tokens asked for
+    long long ahead = 0;  // tokens asked for
     auto fetch = [&](int f_at) {
-        const int n = u.len - ahead;
+        const int n = (int)(u.len - ahead);
         if (n > 0) {
             unsigned char *const to = shared + f_at;
             const int mine = mon ? n - mt : 0;
@@ -409,9 +409,9 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
             }
         }
     };
-    // Turn k finishes chunk k - 1, makes chunk k + 1 ready and asks for chunk k + Dist, which takes chunk
-    // k - 1's place in the ring.
-    constexpr int Dist = R - 1;
+    // Turn k finishes chunk k - 1, makes chunk k + 1 ready and asks for chunk k + Dist, which takes the
+    // place of chunk k - 2 in the ring: a barrier lies between a place's last use and its next.
+    constexpr int Dist = R - 2;
     for (int k = 0; k < Dist; ++k) {
         fetch(k * Sh::stage);
         land(k * Sh::stage);
@@ -427,13 +427,34 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
         states(shared, 0, u.len);
     }
     __syncthreads();
-    int done_at = (R - 1) * Sh::stage, next_at = Sh::stage;  // chunks k - 1 and k + 1 in the ring
+    int free_at = (R - 2) * Sh::stage, done_at = (R - 1) * Sh::stage, next_at = Sh::stage;  // chunks k - 2, k - 1 and k + 1 in the ring
     TT *out = READ ? op - (long long)N * p.o_ts : nullptr;
     const long long dout = N * p.o_ts;
+    auto ask = [&]() {  // fetch() where the chunk is whole and all values are vectors
+        unsigned char *const to = shared + free_at;
+        cp_async<4 * (int)sizeof(DT)>(reinterpret_cast<DT *>(to + Sh::dt) + at(0), fd_at);
+        cp_async<4 * (int)sizeof(TT)>(reinterpret_cast<TT *>(to + Sh::x) + at(0), fx_at);
+        if (READ && zp) cp_async<4 * (int)sizeof(TT)>(reinterpret_cast<TT *>(to + Sh::z) + at(0), fz_at);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = 4 * (id + i * kScanHelpers);
+            if (v < NB) {
+                cp_async<4 * (int)sizeof(TT)>(reinterpret_cast<TT *>(to + Sh::B) + v, fb_at[i]);
+                fb_at[i] += N * (v < N * KP ? p.B_ts : p.C_ts);
+            }
+        }
+        cp_async_commit();
+        fx_at += dx;
+        fz_at += dz;
+        fd_at += dd;
+        ahead += N;
+    };
     // WHOLE: all three chunks are whole and all values vectors, so that nothing has to be asked
     auto turn = [&](auto whole, int k) {
         constexpr bool WHOLE = decltype(whole)::value;
-        cp_async_wait<Dist - 2>();
+        if constexpr (WHOLE) ask();
+        else fetch(free_at);
+        cp_async_wait<Dist - 1>();
         const int half = (k + 1) & 1, left = u.len - k * N;  // both neighbours' half of the buffers in pairs
         [[maybe_unused]] float rx[4], rz[4], y[4];
         [[maybe_unused]] const unsigned char *const done = shared + done_at;
@@ -453,25 +474,6 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[i] += q[i];
             }
-        }
-        if constexpr (WHOLE) {
-            unsigned char *const to = shared + done_at;  // this thread's own values there are in registers by now
-            cp_async<4 * (int)sizeof(DT)>(reinterpret_cast<DT *>(to + Sh::dt) + at(0), fd_at);
-            cp_async<4 * (int)sizeof(TT)>(reinterpret_cast<TT *>(to + Sh::x) + at(0), fx_at);
-            if (READ && zp) cp_async<4 * (int)sizeof(TT)>(reinterpret_cast<TT *>(to + Sh::z) + at(0), fz_at);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int v = 4 * (id + i * kScanHelpers);
-                if (v < NB) {
-                    cp_async<4 * (int)sizeof(TT)>(reinterpret_cast<TT *>(to + Sh::B) + v, fb_at[i]);
-                    fb_at[i] += N * (v < N * KP ? p.B_ts : p.C_ts);
-                }
-            }
-            cp_async_commit();
-            fx_at += dx;
-            fz_at += dz;
-            fd_at += dd;
-            ahead += N;
         }
         steps(d, x, WHOLE ? N : left - N);
         put4(floats(Sh::fd) + half * N * W, d);
@@ -512,10 +514,8 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
             }
             out += dout;
         }
-        if constexpr (!WHOLE) {
-            fetch(done_at);
-            land(done_at);
-        }
+        if constexpr (!WHOLE) land(free_at);
+        free_at = done_at;
         done_at = done_at == (R - 1) * Sh::stage ? 0 : done_at + Sh::stage;
         next_at = next_at == (R - 1) * Sh::stage ? 0 : next_at + Sh::stage;
         __syncthreads();

@@ -112,8 +112,7 @@ struct ScanParams {
     int K, V;
     int softplus, keep;
     int st_bf16;
-    int a_vec;         // A may be read as vectors along V
-    int bc_vec;        // B and C rows may be moved as 16-byte vectors
+    int bc_vec;        // B and C rows may be moved as vectors of four
     long long T, max_len;
     const void *x, *dt, *B, *C, *z;
     long long x_ts, x_hs, dt_ts, dt_hs, dt_es, B_ts, B_hs, C_ts, C_hs, z_ts, z_hs;
@@ -136,8 +135,8 @@ struct ScanParams {
 __host__ __device__
 #endif
 inline long long scan_pieces(long long T, int seg, int batch) { return T / seg + batch; }
-// Short rows (max_len bounds them), and any.  vec: groups of 8 channels may be
-// moved as vectors everywhere.
+// Short rows (max_len bounds them), and any.  vec: four channels may be moved as one
+// vector everywhere.
 cudaError_t launch_scan_step(const ScanParams &p, bool tok_bf16, bool dt_bf16, bool vec, cudaStream_t s);
 cudaError_t launch_scan(const ScanParams &p, bool tok_bf16, bool dt_bf16, bool vec, cudaStream_t s);
 cudaError_t launch_scan_bb(const ScanParams &p, bool vec, cudaStream_t s);  // bfloat16 tokens and step sizes
