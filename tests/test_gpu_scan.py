@@ -99,6 +99,28 @@ def test_bounded_rows(types, longest):
     Case([longest, 1, 0, max(1, longest - 1), 1], 2, 4, 16, 64, types, pad=(4,), seed=longest).check(longest)
 
 
+@pytest.mark.parametrize("K,V,nk,nv", [(16, 128, 1, 8), (12, 20, 2, 6), (24, 36, 1, 9), (20, 8, 1, 4), (128, 64, 1, 2), (7, 11, 1, 30)])
+@pytest.mark.parametrize("longest", [1, 3])
+def test_many_short_rows(K, V, nk, nv, longest):
+    """Blocks that take several rows: padding, empty rows and counts among them."""
+    lens = [(7 * i) % (longest + 1) if i % 5 == 0 else longest for i in range(333)]
+    c = Case(lens, nk, nv, K, V, TYPES[1], pad=range(4, 333, 17), seed=K)
+    c.check(longest)
+    counts = [i % (n + 1) for i, n in enumerate(lens)]
+    _, pool = c.check(longest, counts=counts)
+    again = c.pool.clone()
+    assert c.run(again, counts=counts, state_only=True, max_row_len=longest)[0] is None
+    assert torch.equal(again, pool)
+
+
+def test_rows_around_the_longest_short_one():
+    """16 tokens go one by one, 17 in chunks; both take counts and leave the same kind of state."""
+    for longest in (16, 17):
+        c = Case([longest, 1, 0, longest - 1], 1, 2, 16, 32, TYPES[0], seed=longest)
+        c.check(longest)
+        c.check(longest, counts=[longest - 3, 1, 0, 2])
+
+
 @pytest.mark.parametrize("skip", [False, True])
 @pytest.mark.parametrize("gate", [False, True])
 @pytest.mark.parametrize("bias", [False, True])

@@ -213,6 +213,17 @@ def test_many_rows_and_empty_ones():
     Case([1] * 1000, 16, 3, BF16, seed=10).check()
 
 
+@pytest.mark.parametrize("longest", [1, 3, 6])
+@pytest.mark.parametrize("W", [1, 4])
+@pytest.mark.parametrize("C", [16, 13])
+def test_many_short_rows(longest, W, C):
+    """Blocks that take several rows: padding, empty rows and counts among them."""
+    lens = [(7 * i) % (longest + 1) if i % 5 == 0 else longest for i in range(4001)]
+    c = Case(lens, C, W, BF16, BF16, pad=range(4, 4001, 17), seed=11)
+    c.check(longest)
+    c.check(longest, counts=[i % (n + 1) for i, n in enumerate(lens)])
+
+
 def test_refusals():
     c = Case([3, 4], 64)
     a = c.args(c.pool)
