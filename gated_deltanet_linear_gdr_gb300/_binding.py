@@ -885,16 +885,21 @@ def _ints(t, shape, name: str, device) -> int:
 
 def _ragged(slot_idx, offsets, counts, keep_state, state_only, device):
     """(batch, slot_idx, offsets, counts) of a call over ragged rows, as pointers."""
-    if not isinstance(slot_idx, torch.Tensor):
-        _tensors(slot_idx=slot_idx)
-    shape = slot_idx.shape
-    if len(shape) != 1:
-        raise ValueError("slot_idx must be a contiguous [batch] int32 tensor")
     if not keep_state and (state_only or counts is not None):
         raise ValueError("state_only and counts need keep_state")
-    n = shape[0]
-    return (n, _ints(slot_idx, shape, "slot_idx", device), _ints(offsets, (n + 1,), "offsets", device),
-            0 if counts is None else _ints(counts, shape, "counts", device))
+    try:
+        n, = shape = slot_idx.shape
+        if (slot_idx.dtype is _I32 and offsets.dtype is _I32 and slot_idx.device == device == offsets.device and
+                offsets.shape == (n + 1,) and slot_idx.is_contiguous() and offsets.is_contiguous()):
+            return n, slot_idx.data_ptr(), offsets.data_ptr(), 0 if counts is None else _ints(counts, shape, "counts", device)
+    except (AttributeError, TypeError, ValueError):
+        pass
+    _tensors(slot_idx=slot_idx, offsets=offsets)
+    if slot_idx.dim() != 1:
+        raise ValueError("slot_idx must be a contiguous [batch] int32 tensor")
+    _ints(slot_idx, tuple(slot_idx.shape), "slot_idx", device)
+    _ints(offsets, (slot_idx.shape[0] + 1,), "offsets", device)
+    return n, slot_idx.data_ptr(), offsets.data_ptr(), 0 if counts is None else _ints(counts, shape, "counts", device)
 
 
 def _output(out, like, state_only):
@@ -916,37 +921,47 @@ def _output(out, like, state_only):
     return out, out.data_ptr(), st
 
 
+def _short_conv_refuse(x, weight, conv_state):
+    """Says what is wrong with a convolution's tensors."""
+    _tensors(x=x, weight=weight)
+    dev = x.device
+    _refuse(dev, {"weight": _F32}, x=x, weight=weight)
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be [T, channels] with a unit channel stride")
+    if weight.dim() != 2 or weight.shape[0] != x.shape[1]:
+        raise ValueError(f"weight must be [channels, width] with {x.shape[1]} channels")
+    width = weight.shape[1]
+    if width == 1:
+        raise ValueError("a convolution of width 1 has no conv_state")
+    _refuse(dev, {}, conv_state=conv_state)
+    raise ValueError(f"conv_state must be [slots, {x.shape[1]}, {width - 1}]")
+
+
 def _short_conv_args(x, weight, bias, conv_state, slot_idx, offsets, out, activation, counts, keep_state, state_only, max_row_len):
     """(packed gdr_short_conv_args, out)."""
-    if not isinstance(x, torch.Tensor):
-        _tensors(x=x)
-    dev = x.device
-    td, shape, (xt, *xc) = _float(x, "x", dev), x.shape, x.stride() or (0,)
-    if len(shape) != 2 or (xc[0] != 1 and shape[1] > 1):
-        raise ValueError("x must be [T, channels] with a unit channel stride")
-    T, C = shape
-    if not (isinstance(weight, torch.Tensor) and weight.dtype is _F32 and weight.device == dev):
-        _refuse(dev, {"weight": _F32}, weight=weight)
-    ws, wst = weight.shape, weight.stride()
-    if len(ws) != 2 or ws[0] != C:
-        raise ValueError(f"weight must be [channels, width] with {C} channels")
-    width = ws[1]
+    sp, sd, ss, sc, st, slots = 0, GDR_F32, 0, 0, 0, 1 << 30
+    try:
+        dev, td = x.device, _DTYPES[x.dtype]
+        (T, C), (xt, xc) = x.shape, x.stride()
+        (wc, width), (wsc, wst) = weight.shape, weight.stride()
+        good = (xc == 1 or C == 1) and wc == C and weight.dtype is _F32 and weight.device == dev and x.is_cuda
+        if width > 1:
+            sd = _DTYPES[conv_state.dtype]
+            (slots, cc, taps), (ss, sc, st), sp = conv_state.shape, conv_state.stride(), conv_state.data_ptr()
+            good = good and cc == C and taps == width - 1 and conv_state.device == dev
+        else:
+            good = good and conv_state is None
+    except (AttributeError, KeyError, ValueError, TypeError):
+        good = False
+    if not good:
+        _short_conv_refuse(x, weight, conv_state)
     if activation is not None and activation != "silu":
         raise ValueError('activation must be "silu" or None')
-    sp, sd, ss, sc, st, slots = 0, GDR_F32, 0, 0, 0, 1 << 30
-    if width > 1:
-        sd = _float(conv_state, "conv_state", dev)
-        cs = conv_state.shape
-        if len(cs) != 3 or cs[1] != C or cs[2] != width - 1:
-            raise ValueError(f"conv_state must be [slots, {C}, {width - 1}]")
-        sp, (ss, sc, st), slots = conv_state.data_ptr(), conv_state.stride(), cs[0]
-    elif conv_state is not None:
-        raise ValueError("a convolution of width 1 has no conv_state")
     n, slot, off, cnt = _ragged(slot_idx, offsets, counts, keep_state, state_only, dev)
     out, op, ost = _output(out, x, state_only)
     return _pack_short_conv(n, C, width, 0 if activation is None else 1, td, sd, 1 if keep_state else 0, T, int(max_row_len),
-                            x.data_ptr(), xt, weight.data_ptr(), wst[0], wst[1], _weight(bias, C, "bias", dev), op, ost[0], sp,
-                            ss, sc, st, slots, slot, off, cnt), out
+                            x.data_ptr(), xt, weight.data_ptr(), wsc, wst, _weight(bias, C, "bias", dev), op, ost[0], sp, ss, sc, st,
+                            slots, slot, off, cnt), out
 
 
 def gdr_short_conv(x, weight, bias, conv_state, slot_idx, offsets, out=None, *, activation="silu", counts=None,
@@ -1110,40 +1125,48 @@ def prepare_selective_scan(x, dt, A, B, C, state, slot_idx, offsets, out, *, D=N
                     (x, dt, A, B, C, state, slot_idx, offsets, out, D, z, dt_bias, counts, workspace), x.device)
 
 
-def _floats(t, n: int, name: str, device) -> int:
-    """The pointer of a contiguous [n] float32 tensor."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is _F32 and t.device == device):
-        _refuse(device, {name: _F32}, **{name: t})
-    if t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous [{n}] float32 tensor")
-    return t.data_ptr()
+def _accept_refuse(target, draft, tokens, offsets, uniforms, row_uniforms):
+    """Says what is wrong with a verification's tensors."""
+    _tensors(target=target, tokens=tokens, offsets=offsets, uniforms=uniforms, row_uniforms=row_uniforms)
+    dev = target.device
+    want = {"draft": target.dtype, "tokens": _I32, "offsets": _I32, "uniforms": _F32, "row_uniforms": _F32}
+    _refuse(dev, want, target=target, tokens=tokens, offsets=offsets, uniforms=uniforms, row_uniforms=row_uniforms,
+            **({} if draft is None else {"draft": draft}))
+    if target.dim() != 2 or (target.shape[1] > 1 and target.stride(1) != 1):
+        raise ValueError("target must be [T, vocab] with a unit stride along the vocabulary")
+    if draft is not None and (draft.shape != target.shape or (target.shape[1] > 1 and draft.stride(1) != 1)):
+        raise ValueError("draft must have target's shape and a unit stride along the vocabulary")
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be a contiguous [batch+1] int32 tensor")
+    T, n = target.shape[0], offsets.shape[0] - 1
+    for name, t, size in (("tokens", tokens, T), ("uniforms", uniforms, T), ("row_uniforms", row_uniforms, n), ("offsets", offsets, n + 1)):
+        if t.shape != (size,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [{size}] tensor")
+    raise ValueError("the tensors of the call do not fit together")
 
 
 def _accept_args(target, draft, tokens, offsets, uniforms, row_uniforms, max_row_len, out, counts):
     """(packed gdr_accept_args, out, counts)."""
-    if not isinstance(target, torch.Tensor):
-        _tensors(target=target)
-    dev, shape, (pt, *pc) = target.device, target.shape, target.stride() or (0,)
-    pd = _float(target, "target", dev)
-    if len(shape) != 2 or (pc[0] != 1 and shape[1] > 1):
-        raise ValueError("target must be [T, vocab] with a unit stride along the vocabulary")
-    T, vocab = shape
     qp, qt = 0, 0
-    if draft is not None:
-        if not isinstance(draft, torch.Tensor) or draft.dtype != target.dtype or draft.device != dev:
-            _refuse(dev, {"draft": target.dtype}, draft=draft)
-        if draft.shape != shape or (vocab > 1 and draft.stride(1) != 1):
-            raise ValueError("draft must have target's shape and a unit stride along the vocabulary")
-        qp, qt = draft.data_ptr(), draft.stride(0)
-    if not isinstance(offsets, torch.Tensor):
-        _tensors(offsets=offsets)
-    if offsets.dim() != 1 or offsets.shape[0] < 1:
-        raise ValueError("offsets must be a contiguous [batch+1] int32 tensor")
-    n, width = offsets.shape[0] - 1, int(max_row_len)
+    try:
+        dev, pd = target.device, _DTYPES[target.dtype]
+        (T, vocab), (pt, pc) = shape, _ = target.shape, target.stride()
+        rows, = offsets.shape
+        good = (target.is_cuda and (pc == 1 or vocab == 1) and rows >= 1 and tokens.dtype is _I32 and offsets.dtype is _I32 and
+                uniforms.dtype is _F32 and row_uniforms.dtype is _F32 and
+                dev == tokens.device == offsets.device == uniforms.device == row_uniforms.device and
+                tokens.shape == (T,) == uniforms.shape and row_uniforms.shape == (rows - 1,) and tokens.is_contiguous() and
+                offsets.is_contiguous() and uniforms.is_contiguous() and row_uniforms.is_contiguous())
+        if draft is not None:
+            (qt, qc), qp = draft.stride(), draft.data_ptr()
+            good = good and draft.dtype is target.dtype and draft.device == dev and draft.shape == shape and (qc == 1 or vocab == 1)
+    except (AttributeError, KeyError, ValueError, TypeError):
+        good = False
+    if not good:
+        _accept_refuse(target, draft, tokens, offsets, uniforms, row_uniforms)
+    n, width = rows - 1, int(max_row_len)
     if width < 1:
         raise ValueError("max_row_len must be at least 1 (it is the width of the returned tokens)")
-    off, tok = _ints(offsets, (n + 1,), "offsets", dev), _ints(tokens, (T,), "tokens", dev)
-    up, vp = _floats(uniforms, T, "uniforms", dev), _floats(row_uniforms, n, "row_uniforms", dev)
     if out is None:
         out, ot = torch.empty((n, width), dtype=_I32, device=dev), width
     else:
@@ -1157,7 +1180,8 @@ def _accept_args(target, draft, tokens, offsets, uniforms, row_uniforms, max_row
         cp = counts.data_ptr()
     else:
         cp = _ints(counts, (n,), "counts", dev)
-    return _pack_accept(n, vocab, pd, width, T, target.data_ptr(), pt, qp, qt, tok, off, up, vp, out.data_ptr(), ot, cp), out, counts
+    return _pack_accept(n, vocab, pd, width, T, target.data_ptr(), pt, qp, qt, tokens.data_ptr(), offsets.data_ptr(),
+                        uniforms.data_ptr(), row_uniforms.data_ptr(), out.data_ptr(), ot, cp), out, counts
 
 
 def gdr_accept_drafts(target, draft, tokens, offsets, uniforms, row_uniforms, *, max_row_len, out=None, counts=None):
