@@ -372,3 +372,15 @@ def test_refusals():
         gdr.gdr_selective_scan(*c.args(pool), D=c.D[:1])
     with pytest.raises(ValueError, match="z must"):
         gdr.gdr_selective_scan(*c.args(pool), z=c.z[:2])
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("K", [3, 12, 20, 27, 50, 100])
+@pytest.mark.parametrize("V", [36, 64, 128])
+def test_states_that_fill_no_vector(types, K, V):
+    """B and C come value by value while the channels come as vectors, on a GPU whose shared memory is full of NaN."""
+    full = Case([40] * 160, 1, 4, 32, 64, types, seed=1)
+    full.B.fill_(float("nan"))
+    full.C.fill_(float("nan"))
+    full.run()
+    Case([19, 3, 5, 0, 61], 2, 4, K, V, types, seed=K).check()
