@@ -35,6 +35,7 @@ bool vector_rows(const void *p, int dtype, int64_t bytes, int64_t a, int64_t b =
 
 int check_tokens(int64_t total, int32_t batch, const char *fn) {
     if (batch < 0) return fail(GDR_ERR_INVALID_ARG, "%s: batch %d < 0", fn, batch);
+    if (batch > (1 << 27)) return fail(GDR_ERR_UNSUPPORTED, "%s: batch must be at most 2^27", fn);
     if (total < 0) return fail(GDR_ERR_INVALID_ARG, "%s: total_tokens < 0", fn);
     if (total >= (1ll << 31)) return fail(GDR_ERR_UNSUPPORTED, "%s: total_tokens must be < 2^31", fn);
     return GDR_OK;
@@ -102,6 +103,8 @@ int check_scan_sizes(const gdr_scan_args *a, const char *fn) {
     if (!a) return fail(GDR_ERR_INVALID_ARG, "%s: args is NULL", fn);
     int rc = check_tokens(a->total_tokens, a->batch, fn);
     if (rc) return rc;
+    if (a->total_tokens > (1ll << 31) - 32)  // tokens are counted in whole chunks
+        return fail(GDR_ERR_UNSUPPORTED, "%s: total_tokens must be at most 2^31 - 32", fn);
     if (a->nv <= 0 || a->nk <= 0)
         return fail(GDR_ERR_INVALID_ARG, "%s: nv=%d, nk=%d must be positive", fn, a->nv, a->nk);
     if (a->nv % a->nk != 0)
@@ -306,8 +309,8 @@ int gdr_selective_scan(const gdr_scan_args *a, void *stream) {
     const bool tb = a->token_dtype == GDR_BF16;
     // vectors of four values
     const int64_t four = 4 * esize(a->token_dtype);
-    const bool vec = a->V % 4 == 0 && vector_rows(a->x, a->token_dtype, four, p.x_ts, p.x_hs) && p.dt_es == 1 &&
-                     vector_rows(a->dt, a->dt_dtype, 4 * esize(a->dt_dtype), p.dt_ts, p.dt_hs) &&
+    const bool vec = a->V % 4 == 0 && vector_rows(a->x, a->token_dtype, four, p.x_ts, p.x_hs) &&
+                     (p.dt_es == 0 || vector_rows(a->dt, a->dt_dtype, 4 * esize(a->dt_dtype), p.dt_ts, p.dt_hs)) &&
                      (!a->out || vector_rows(a->out, a->token_dtype, four, p.o_ts, p.o_hs)) &&
                      (!a->z || vector_rows(a->z, a->token_dtype, four, p.z_ts, p.z_hs)) &&
                      vector_rows(a->state, a->state_dtype, 4 * esize(a->state_dtype), p.st_slot, p.st_head, p.st_k);
@@ -317,12 +320,8 @@ int gdr_selective_scan(const gdr_scan_args *a, void *stream) {
     if (p.seg && (!a->workspace || a->workspace_bytes < scan_bytes(a, p.seg))) p.seg = 0;
     p.ws = static_cast<float *>(a->workspace);
     const bool db = a->dt_dtype == GDR_BF16;
-    if (a->max_row_len >= 1 && a->max_row_len <= kShortRow) {
-        // four warps have KT states each: vectors where all of them do, or none
-        const int KT = a->K <= 16 ? 4 : a->K <= 32 ? 8 : a->K <= 64 ? 16 : 32;
-        const bool all = vec && p.bc_vec && a->K % KT == 0;
-        return launched(gdr::launch_scan_step(p, tb, db, all, static_cast<cudaStream_t>(stream)), fn);
-    }
+    if (a->max_row_len >= 1 && a->max_row_len <= kShortRow)
+        return launched(gdr::launch_scan_step(p, tb, db, vec, static_cast<cudaStream_t>(stream)), fn);
     return launched(gdr::launch_scan(p, tb, db, vec, static_cast<cudaStream_t>(stream)), fn);
 }
 
@@ -334,7 +333,6 @@ int gdr_accept_drafts(const gdr_accept_args *a, void *stream) {
     if (a->vocab <= 0 || a->max_row_len <= 0)
         return fail(GDR_ERR_INVALID_ARG, "%s: vocab=%d and max_row_len=%d must be positive", fn, a->vocab, a->max_row_len);
     if (a->vocab > (1 << 28)) return fail(GDR_ERR_UNSUPPORTED, "%s: vocab must be at most 2^28", fn);
-    if (a->batch > (1 << 27)) return fail(GDR_ERR_UNSUPPORTED, "%s: batch must be at most 2^27", fn);
     if (!is_dtype(a->prob_dtype)) return fail(GDR_ERR_UNSUPPORTED, "%s: prob_dtype must be GDR_F32 or GDR_BF16", fn);
     if (a->batch == 0) return gdr::api_ok();
     if (!a->offsets || !a->row_uniforms || !a->out_tokens || !a->counts)

@@ -300,7 +300,11 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
         if (n > 0) {
             unsigned char *const to = shared + f_at;
             const int mine = mon ? n - mt : 0;
-            copy(reinterpret_cast<DT *>(to + Sh::dt) + at(0), fd_at, p.dt_ts, wd, mine);
+            if (VEC && !p.dt_es) {
+                if (mine > 0) wd[0] = *fd_at;
+            } else {
+                copy(reinterpret_cast<DT *>(to + Sh::dt) + at(0), fd_at, p.dt_ts, wd, mine);
+            }
             copy(reinterpret_cast<TT *>(to + Sh::x) + at(0), fx_at, p.x_ts, wx, mine);
             if (READ && zp) copy(reinterpret_cast<TT *>(to + Sh::z) + at(0), fz_at, p.z_ts, wz, mine);
             if (bc_vec) {
@@ -332,6 +336,14 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
     // drops the last one too.
     auto land = [&](int f_at) {
         unsigned char *const to = shared + f_at;
+        if constexpr (VEC) {
+            if (!p.dt_es) {  // a head's only step size
+                Pack<DT, 4> q;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q.u.e[i] = wd[0];
+                q.store(reinterpret_cast<DT *>(to + Sh::dt) + at(0));
+            }
+        }
         if constexpr (!VEC && sizeof(DT) == 2) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) reinterpret_cast<DT *>(to + Sh::dt)[at(i)] = wd[i];
@@ -525,12 +537,14 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
         next_at = next_at == (R - 1) * Sh::stage ? 0 : next_at + Sh::stage;
         __syncthreads();
     };
-    // chunks k - 1 ... k + Dist are whole for 1 <= k <= last
-    const int last = VEC && bc_vec && width == W ? u.len / N - 1 - Dist : 0;
+    // Chunks k - 1 ... k + Dist are whole for 1 <= k <= last.  One step size a head takes the other turns (8 ragged rows
+    // x 4096 channels 397 us; with whole turns for it too 385, and 383 instead of 381 for step sizes a channel).
+    const int last = VEC && bc_vec && p.dt_es && width == W ? u.len / N - 1 - Dist : 0;
     turn(std::false_type{}, 0);
     int k = 1;
-    if constexpr (VEC)
+    if constexpr (VEC) {
         for (; k <= last; ++k) turn(std::true_type{}, k);
+    }
     for (; k <= chunks; ++k) turn(std::false_type{}, k);
     if (first) {
         // each channel's step sizes, over the threads that have its tokens

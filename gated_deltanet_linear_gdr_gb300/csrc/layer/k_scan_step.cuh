@@ -1,11 +1,15 @@
 // Selective scan of single tokens and short rows (drafts): every state goes in and
 // out once, with a handful of operations on it a token: HBM bound, or bound by the
 // steps that follow one another.  A block is 128 channels of some rows.
-// Its four warps share the states, KT each, four channels a lane, so that a warp
+// Its NW warps share the states, KT each, four channels a lane, so that a warp
 // moves whole runs of 512 bytes.  What belongs to the channels (their places, the
 // rates, the bias) is worked out once for all the block's rows; the next row's
 // states are on their way while one is worked on.  The partial readouts meet in
-// shared memory, and every thread finishes one channel.
+// shared memory, and a thread a channel finishes.
+//
+// Measured, bfloat16 tokens, float32 pool, 16 states: 256 single tokens x 4096 channels 29 us on the device (4.8 TB/s of states
+// and tokens, 71% of the copy rate; waits for memory are the largest stall); with channels but not B and C in vectors
+// (27 states) 90 us, against 225 with everything one by one.
 #pragma once
 
 #include "scan_device.cuh"
@@ -13,7 +17,7 @@
 namespace gdr {
 namespace {
 
-constexpr int kStepTile = 128;  // a block's channels, and its threads
+constexpr int kStepTile = 128;  // a block's channels
 constexpr int kStepRows = 32;   // a block's rows at most
 
 // Four neighbouring values as they came, one vector (VEC) or one by one, taken apart only where
@@ -22,6 +26,7 @@ template <typename T, bool VEC> struct Four;
 template <> struct Four<uint16_t, true> {
     uint2 v;
     __device__ __forceinline__ void load(const uint16_t *p) { v = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void load_first(const uint16_t *p) { v.x = *p; }
     __device__ __forceinline__ float get(int i) const {
         const unsigned w = i < 2 ? v.x : v.y;
         return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
@@ -30,6 +35,7 @@ template <> struct Four<uint16_t, true> {
 template <> struct Four<float, true> {
     float4 v;
     __device__ __forceinline__ void load(const float *p) { v = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ void load_first(const float *p) { v.x = *p; }
     __device__ __forceinline__ float get(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 };
 template <typename T> struct Four<T, false> {
@@ -72,14 +78,14 @@ template <typename TT, typename DT, typename ST> struct StepRow {
     int kept;  // tokens after which the states are kept, 0: they are not; -1: zeros only
 };
 
-// VEC: four channels are a vector everywhere, and so are four states of B and C; K is a multiple of KT.
-// ONE: rows of one token.
-template <typename TT, typename DT, typename ST, int KT, bool VEC, bool ONE>
-__global__ void __launch_bounds__(kStepTile, KT <= 4 ? 4 : KT <= 8 ? 3 : 1)
+// VEC: four channels are a vector everywhere (dt: that, or one value a head).  BC: so are four states of B
+// and C, and K is a multiple of KT.  ONE: rows of one token.  Sixteen warps a multiprocessor, 128 registers each.
+template <typename TT, typename DT, typename ST, int KT, int NW, bool VEC, bool BC, bool ONE>
+__global__ void __launch_bounds__(32 * NW, 16 / NW)
     k_scan_step(const __grid_constant__ ScanParams p, int tiles, int rows) {
-    __shared__ __align__(16) float part[2][4][kStepTile];
+    __shared__ __align__(16) float part[2][NW][kStepTile];
     __shared__ StepRow<TT, DT, ST> info[kStepRows];
-    constexpr bool AHEAD = VEC && ONE && KT <= 8;  // there are registers for two rows' states
+    constexpr bool AHEAD = BC && ONE && KT <= 4;  // there are registers for two rows' states
     constexpr int KV = KT / 4;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const unsigned all = (unsigned)(p.nk * tiles), block = blockIdx.x / all, tg = blockIdx.x - block * all;
@@ -129,7 +135,8 @@ __global__ void __launch_bounds__(kStepTile, KT <= 4 ? 4 : KT <= 8 ? 3 : 1)
 
     struct Token {
         Four<DT, VEC> d;
-        Four<TT, VEC> x, B[KV], C[KV];
+        Four<TT, VEC> x;
+        Four<TT, BC> B[KV], C[KV];
         TT mx, mz;
     };
     struct Row {
@@ -138,12 +145,20 @@ __global__ void __launch_bounds__(kStepTile, KT <= 4 ? 4 : KT <= 8 ? 3 : 1)
     };
     auto ask_token = [&](const StepRow<TT, DT, ST> &w, int t, Token &v) {
         if (have > 0) {
-            gather4(w.dt + t * p.dt_ts, d_at, on, v.d);
+            if constexpr (VEC) {
+                if (on[0]) {
+                    const DT *const d = w.dt + t * p.dt_ts + d_at[0];
+                    if (p.dt_es) v.d.load(d);
+                    else v.d.load_first(d);  // the head's only one
+                }
+            } else {
+                gather4(w.dt + t * p.dt_ts, d_at, on, v.d);
+            }
             gather4(w.x + t * p.x_ts, x_at, on, v.x);
             const TT *const b = w.B + t * p.B_ts + k0, *const c = w.C + t * p.C_ts + k0;
 #pragma unroll
             for (int i = 0; i < KV; ++i) {
-                if constexpr (VEC) {
+                if constexpr (BC) {
                     v.B[i].load(b + 4 * i);
                     if (p.out) v.C[i].load(c + 4 * i);
                 } else {
@@ -191,13 +206,13 @@ __global__ void __launch_bounds__(kStepTile, KT <= 4 ? 4 : KT <= 8 ? 3 : 1)
                 float d[4], in[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    d[e] = now.d.get(e) + bias[e];
+                    d[e] = (VEC && !p.dt_es ? now.d.get(0) : now.d.get(e)) + bias[e];
                     if (p.softplus) d[e] = softplus<TT>(d[e]);
                     in[e] = d[e] * now.x.get(e);
                 }
 #pragma unroll
                 for (int i = 0; i < KT; ++i) {
-                    if (!VEC && i >= have) continue;
+                    if (!BC && i >= have) continue;
                     const float B = now.B[i / 4].get(i % 4), C = now.C[i / 4].get(i % 4);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -212,11 +227,14 @@ __global__ void __launch_bounds__(kStepTile, KT <= 4 ? 4 : KT <= 8 ? 3 : 1)
                 }
             }
             if (p.out) {
-                float (&q)[4][kStepTile] = part[exchanges++ & 1];
+                float (&q)[NW][kStepTile] = part[exchanges++ & 1];
                 *reinterpret_cast<float4 *>(&q[warp][lane * 4]) = make_float4(y[0], y[1], y[2], y[3]);
                 __syncthreads();
                 if (mon) {
-                    float o = fmaf(D, to_f32(now.mx), (q[0][tid] + q[1][tid]) + (q[2][tid] + q[3][tid]));
+                    float o = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < NW; i += 4) o += (q[i][tid] + q[i + 1][tid]) + (q[i + 2][tid] + q[i + 3][tid]);
+                    o = fmaf(D, to_f32(now.mx), o);
                     if (gate) o *= silu(to_f32(now.mz));
                     w.out[t * p.o_ts + mo_at] = from_f32<TT>(o);
                 }
@@ -244,27 +262,31 @@ __global__ void __launch_bounds__(kStepTile, KT <= 4 ? 4 : KT <= 8 ? 3 : 1)
     }
 }
 
-template <typename TT, typename DT, typename ST, int KT, bool VEC, bool ONE> cudaError_t go(const ScanParams &p, cudaStream_t s) {
+template <typename TT, typename DT, typename ST, int KT, int NW, bool VEC, bool BC, bool ONE>
+cudaError_t go(const ScanParams &p, cudaStream_t s) {
     const long long tiles = ((long long)p.r * p.V + kStepTile - 1) / kStepTile, heads = p.nk * tiles;
     // as many rows a block as leaves each multiprocessor its blocks once over
-    const long long at_once = 152 * (KT <= 4 ? 4 : KT <= 8 ? 3 : 1);
+    const long long at_once = 152 * (16 / NW);
     long long rows = (p.batch * heads + at_once - 1) / at_once;
     if (rows > kStepRows) rows = kStepRows;
     const long long blocks = (p.batch + rows - 1) / rows * heads;
     if (blocks >= 1ll << 31) return cudaErrorInvalidConfiguration;
-    k_scan_step<TT, DT, ST, KT, VEC, ONE><<<(unsigned)blocks, kStepTile, 0, s>>>(p, (int)tiles, (int)rows);
+    k_scan_step<TT, DT, ST, KT, NW, VEC, BC, ONE><<<(unsigned)blocks, 32 * NW, 0, s>>>(p, (int)tiles, (int)rows);
     return cudaGetLastError();
 }
-template <typename TT, typename DT, typename ST, int KT> cudaError_t step_form(const ScanParams &p, bool vec, cudaStream_t s) {
-    if (!vec) return go<TT, DT, ST, KT, false, false>(p, s);
-    return p.max_len == 1 ? go<TT, DT, ST, KT, true, true>(p, s) : go<TT, DT, ST, KT, true, false>(p, s);
+template <typename TT, typename DT, typename ST, int KT, int NW> cudaError_t step_form(const ScanParams &p, bool vec, cudaStream_t s) {
+    if (!vec) return go<TT, DT, ST, KT, NW, false, false, false>(p, s);
+    if (!p.bc_vec || p.K % KT != 0) return go<TT, DT, ST, KT, NW, true, false, false>(p, s);
+    return p.max_len == 1 ? go<TT, DT, ST, KT, NW, true, true, true>(p, s) : go<TT, DT, ST, KT, NW, true, true, false>(p, s);
 }
-// States a warp has, by K.
+// States a warp has and warps, by K.  Four states a warp wherever they fit leave registers for the next row's.  Measured
+// against four warps of 8, 16 and 32 states, 256 single tokens x 4096 channels, us: 32 states 61 / 78; x 2048 channels: 64 states
+// 64 / 82, 128 states 121 / 371; 64 rows of 2 to 8 tokens, 128 states: 184 / 527.
 template <typename TT, typename DT, typename ST> cudaError_t step_states(const ScanParams &p, bool vec, cudaStream_t s) {
-    if (p.K <= 16) return step_form<TT, DT, ST, 4>(p, vec, s);
-    if (p.K <= 32) return step_form<TT, DT, ST, 8>(p, vec, s);
-    if (p.K <= 64) return step_form<TT, DT, ST, 16>(p, vec, s);
-    return step_form<TT, DT, ST, 32>(p, vec, s);
+    if (p.K <= 16) return step_form<TT, DT, ST, 4, 4>(p, vec, s);
+    if (p.K <= 32) return step_form<TT, DT, ST, 4, 8>(p, vec, s);
+    if (p.K <= 64) return step_form<TT, DT, ST, 4, 16>(p, vec, s);
+    return step_form<TT, DT, ST, 8, 16>(p, vec, s);
 }
 template <typename TT, typename DT> cudaError_t scan_step(const ScanParams &p, bool vec, cudaStream_t s) {
     return p.st_bf16 ? step_states<TT, DT, uint16_t>(p, vec, s) : step_states<TT, DT, float>(p, vec, s);

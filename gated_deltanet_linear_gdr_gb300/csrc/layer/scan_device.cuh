@@ -23,7 +23,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 // A state's decay from d and its rate.  ex2.approx errs to one side by a fraction
 // of an ulp, which a slow state adds up over its memory (1000 tokens: 3e-5); that
 // is nothing beside bfloat16 tokens, and float32 tokens take expf, which does not.
-template <typename TT> __device__ __forceinline__ float rate(float a) { return sizeof(TT) == 2 ? a * kLog2e : a; }
+// Rates are finite, so that tokens that are not there (d = 0) decay nothing; what an infinite one does to
+// others stays the same.
+template <typename TT> __device__ __forceinline__ float rate(float a) {
+    const float r = sizeof(TT) == 2 ? a * kLog2e : a, most = 3.4028235e38f;
+    return r > most ? most : r < -most ? -most : r;
+}
 template <typename TT> __device__ __forceinline__ float decay(float e) { return sizeof(TT) == 2 ? ex2(e) : expf(e); }
 
 // log(1 + e^v) without cancellation: max(v, 0) + log1p(e^-|v|).  bfloat16 tokens: log1p(e) / e by its Chebyshev
@@ -86,20 +91,6 @@ __device__ __forceinline__ bool scan_row(const ScanParams &p, int b, bool leader
         if (u.len == 0) return false;
     }
     return true;
-}
-
-// The readout of four channels a lane, over the LK lanes that share them: two exchanges
-// leave lane lk channel lk % 4, the rest add up.
-template <int LK> __device__ __forceinline__ float scan_readout(const float (&y)[4], int lk) {
-    const bool up = lk & 2, odd = lk & 1;
-    float a = up ? y[2] : y[0], b = up ? y[3] : y[1];
-    a += __shfl_xor_sync(kFull, up ? y[0] : y[2], 2);
-    b += __shfl_xor_sync(kFull, up ? y[1] : y[3], 2);
-    float v = odd ? b : a;
-    v += __shfl_xor_sync(kFull, odd ? a : b, 1);
-#pragma unroll
-    for (int m = 4; m < LK; m <<= 1) v += __shfl_xor_sync(kFull, v, m);
-    return v;
 }
 
 }  // namespace gdr

@@ -560,6 +560,7 @@ int gdr_short_conv(const gdr_short_conv_args *args, void *stream);
  *     out     = y                  (z given: y * z / (1 + exp(-z)))
  *
  * x, z, out  [total_tokens, nv, V] in token_dtype, unit channel stride; z NULL: none.
+ *          out may be x or z itself (with its strides) and lies on no other input.
  * dt       [total_tokens, nv, V] in dt_dtype (token_dtype or float32); dt_elem_stride
  *          1, or 0 for one step size a head.
  * B, C     [total_tokens, nk, K] in token_dtype, unit stride along K.
@@ -576,7 +577,7 @@ int gdr_short_conv(const gdr_short_conv_args *args, void *stream);
  *          counted tokens are).  A verify pass of drafts runs without keep_state,
  *          the accepted tokens then go in by such a call.
  * workspace  as in gdr_linattn_args, by gdr_selective_scan_workspace_bytes().
- * K is 1 to 128, V any.  A bfloat16 pool and bfloat16 outputs are rounded to
+ * No two rows of a call move the same slot.  K is 1 to 128, V any.  A bfloat16 pool and bfloat16 outputs are rounded to
  * nearest-even once.  A non-finite value spoils its own row only.
  */
 typedef struct gdr_scan_args {

@@ -384,3 +384,42 @@ def test_states_that_fill_no_vector(types, K, V):
     full.C.fill_(float("nan"))
     full.run()
     Case([19, 3, 5, 0, 61], 2, 4, K, V, types, seed=K).check()
+
+
+@pytest.mark.parametrize("types", TYPES[:2])
+@pytest.mark.parametrize("lens,bound,K,V", [([1] * 9, 1, 16, 64), ([5, 1, 7], 8, 16, 64), ([100, 3, 41], 0, 16, 64),
+                                            ([100, 3, 41], 0, 5, 33), ([2500], 0, 16, 64)])
+@pytest.mark.parametrize("on", ["x", "z"])
+def test_output_in_place_of_an_input(types, lens, bound, K, V, on):
+    c = Case(lens, 1, 4, K, V, types, seed=17)
+    want, state = c.run(max_row_len=bound)
+    c.z = c.z.contiguous()
+    pool, out = c.pool.clone(), getattr(c, on)
+    assert c.run(pool, max_row_len=bound, out=out)[0] is out
+    assert torch.equal(out, want) and torch.equal(pool, state)
+
+
+@pytest.mark.parametrize("types", TYPES[:2])
+@pytest.mark.parametrize("lens,bound", [([1] * 3, 1), ([5, 1, 7], 8), ([100, 3, 41], 0)])
+def test_infinite_rates_forget(types, lens, bound):
+    """A = -inf: a state is its last token's alone, as with a decay that float32 rounds to 0 (d >= 1/2, A = -1000)."""
+    c = Case(lens, 1, 2, 16, 36, types, seed=18, bias=False, softplus=False)
+    c.dt.clamp_(min=0.5)
+    c.A[:, 3] = -1000.0
+    want, state = c.run(max_row_len=bound)
+    c.A[:, 3] = float("-inf")
+    got, pool = c.run(max_row_len=bound)
+    assert torch.equal(got, want) and torch.equal(pool, state)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("lens,bound", [([1] * 9, 1), ([5, 1, 7, 0, 8], 8), ([100, 3, 41], 0), ([1500], 0)])
+@pytest.mark.parametrize("K,V,nk,nv", [(16, 64, 1, 2), (12, 36, 2, 6), (27, 20, 1, 3)])
+def test_one_step_size_a_head(types, lens, bound, K, V, nk, nv):
+    """dt of one value a head beside channels in vectors: the same results as with the value at every channel."""
+    c = Case(lens, nk, nv, K, V, types, seed=19)
+    c.dt = c.dt[:, :, 3:4].expand(-1, -1, V)
+    got, pool = c.check(bound, cut=256) if max(lens) > 256 else c.check(bound)
+    c.dt = c.dt.contiguous()
+    want, state = c.run(max_row_len=bound)
+    assert torch.equal(got, want) and torch.equal(pool, state)

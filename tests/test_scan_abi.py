@@ -55,6 +55,7 @@ def conv(**over):
 
 @pytest.mark.parametrize("over,code", [
     (dict(batch=-1), INV), (dict(total_tokens=-1), INV), (dict(total_tokens=1 << 31), UNS), (dict(channels=0), INV),
+    (dict(batch=(1 << 27) + 1), UNS),
     (dict(channels=1 << 29), UNS), (dict(width=0), UNS), (dict(width=5), UNS), (dict(activation=2), INV), (dict(token_dtype=2), UNS),
     (dict(state_dtype=-1), UNS), (dict(slot_idx=None), INV), (dict(offsets=None), INV), (dict(weight=None), INV),
     (dict(max_slots=0), INV), (dict(weight_tap_stride=-1), INV), (dict(weight=FAKE + 2), UNS), (dict(bias=FAKE + 2), UNS),
@@ -81,6 +82,7 @@ def scan(**over):
     (dict(batch=-1), INV), (dict(nv=0), INV), (dict(nk=3), INV), (dict(K=0), UNS), (dict(K=129), UNS), (dict(V=0), UNS),
     (dict(V=1 << 23), UNS), (dict(token_dtype=2), UNS), (dict(dt_dtype=2), UNS), (dict(token_dtype=B.GDR_F32), UNS),
     (dict(state_dtype=-1), UNS), (dict(total_tokens=-1), INV), (dict(total_tokens=1 << 31), UNS), (dict(state=None), INV),
+    (dict(total_tokens=(1 << 31) - 31), UNS), (dict(batch=(1 << 27) + 1), UNS),
     (dict(slot_idx=None), INV), (dict(offsets=None), INV), (dict(A=None), INV), (dict(max_slots=0), INV),
     (dict(state_vdim_stride=2), UNS), (dict(state_kdim_stride=0), INV), (dict(A_vdim_stride=-1), INV), (dict(D_head_stride=-1), INV),
     (dict(state=FAKE + 2), UNS), (dict(A=FAKE + 2), UNS), (dict(D=FAKE + 2), UNS), (dict(dt_bias=FAKE + 1), UNS),
