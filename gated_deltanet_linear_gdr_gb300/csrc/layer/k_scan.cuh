@@ -13,6 +13,11 @@
 // chunk of 8 tokens ahead and behind: they copy raw chunks into a ring, make d and d x of
 // them once a channel, add up the NW partial readouts, apply D and the gate and store.
 // One barrier a chunk hands both sides' buffers over.
+//
+// Measured, bfloat16 tokens, 16 states, 8 ragged rows, 17702 tokens x 4096 channels: 380 us, where the bytes
+// alone would take 86 and the exponentials 124.  No one unit is full (counters: shared memory 63% of its
+// cycles, FMA 45%, exponentials 39%, an instruction issued in 62%); a token's chain of barriers and shared memory
+// reads, and their instructions, bound it.
 #pragma once
 
 #include "scan_device.cuh"

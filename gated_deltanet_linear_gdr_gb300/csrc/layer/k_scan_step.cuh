@@ -5,7 +5,7 @@
 // moves whole runs of 512 bytes.  What belongs to the channels (their places, the
 // rates, the bias) is worked out once for all the block's rows; the next row's
 // states are on their way while one is worked on.  The partial readouts meet in
-// shared memory, and a thread a channel finishes.
+// shared memory, and one thread finishes each channel.
 //
 // Measured, bfloat16 tokens, float32 pool, 16 states: 256 single tokens x 4096 channels 29 us on the device (4.8 TB/s of states
 // and tokens, 71% of the copy rate; waits for memory are the largest stall); with channels but not B and C in vectors

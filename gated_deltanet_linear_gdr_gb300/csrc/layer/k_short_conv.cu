@@ -16,6 +16,9 @@
 // token, past the end of its run where they lie there.  Its threads also write
 // the slot, from the row's last inputs: nobody else touches it, so old inputs
 // are not overwritten before they are used, in one launch.
+//
+// Measured, bfloat16 tokens x 8192 channels, float32 pool: 8 ragged rows, 17702 tokens, 105 us (5.6 TB/s, 82% of
+// the copy rate); 256 single tokens 15 us (8.4 at the copy rate; the call itself takes the host 11).
 #include "scan_device.cuh"
 
 namespace gdr {
