@@ -423,3 +423,40 @@ def test_one_step_size_a_head(types, lens, bound, K, V, nk, nv):
     c.dt = c.dt.contiguous()
     want, state = c.run(max_row_len=bound)
     assert torch.equal(got, want) and torch.equal(pool, state)
+
+
+@pytest.mark.parametrize("types", [TYPES[0], TYPES[3]])
+@pytest.mark.parametrize("lens,bound", [([1, 1], 1), ([3, 0, 7], 7), ([40, 9], 0), ([700], 0)])
+@pytest.mark.parametrize("nk,nv,K,V", [(1, 1, 1, 1), (64, 64, 4, 4), (2, 6, 31, 4), (1, 2, 128, 68), (3, 3, 65, 130)])
+@pytest.mark.parametrize("shared", ["xz", "BA", "xzBAd"])
+def test_inputs_that_are_shared(types, lens, bound, nk, nv, K, V, shared):
+    """Strides of 0: over tokens (x, C), heads (z, B), channels (A, D, dt)."""
+    c = Case(lens, nk, nv, K, V, types, seed=20)
+    T = sum(lens)
+    if "x" in shared:
+        c.x, c.z = c.x[:1].expand(T, -1, -1), c.z[:, :1].expand(-1, nv, -1)
+    if "B" in shared:
+        c.B, c.C = c.B[:, :1].expand(-1, nk, -1), c.C[:1].expand(T, -1, -1)
+        c.A, c.D = c.A[:1, :, :1].expand(nv, K, V), c.D[:1, :1].expand(nv, V)
+    if "d" in shared:
+        c.dt = c.dt[:, :1, :1].expand(-1, nv, V)
+    c.check(bound, cut=max(lens))
+
+
+def test_very_many_rows():
+    n, h = 200001, 100000
+    c = Case([1] * n, 1, 1, 8, 8, seed=21)
+    got, pool = c.run(max_row_len=1)
+    other, state = c.run()  # by chunks
+    assert torch.equal(pool, state)
+    halves = c.pool.clone()
+    first = gdr.gdr_selective_scan(c.x[:h], c.dt[:h], c.A, c.B[:h], c.C[:h], halves, c.slot[:h], c.off[:h + 1], D=c.D, z=c.z[:h],
+                                   dt_bias=c.bias, max_row_len=1)
+    second = gdr.gdr_selective_scan(c.x[h:], c.dt[h:], c.A, c.B[h:], c.C[h:], halves, c.slot[h:], c.off[h:] - h, D=c.D, z=c.z[h:],
+                                    dt_bias=c.bias, max_row_len=1)
+    assert torch.equal(got, torch.cat([first, second])) and torch.equal(pool, halves)
+    # the readout's eight products add up in another order: 8 roundings of the largest partial sum, and bfloat16's own
+    terms = (c.C.float()[:, :, :, None].abs() * pool[c.slot.long()].abs()).sum(2) + (c.D * c.x.float()).abs()
+    gate = c.z.float() * torch.sigmoid(c.z.float())
+    tol = 2 * 12 * 2.0 ** -24 * terms * gate.abs() + 2.0 ** -7 * got.float().abs() + 1e-6
+    assert bool(((got.float() - other.float()).abs() <= tol).all())
