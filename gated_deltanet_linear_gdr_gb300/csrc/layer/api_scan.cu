@@ -167,28 +167,40 @@ int check_scan(const gdr_scan_args *a, const char *fn) {
 // 27 / 101, of 8 64 / 107, of 12 89 / 115, of 16 111 / 121.
 constexpr int kShortRow = 16;
 
+// float32 tokens over a bfloat16 pool: what a call leaves is rounded so that a state's last bit counts (scan_device.cuh),
+// and joined segments would have others than the row's own order of operations.  The states of a cut row go through it
+// in its order, eight of them a block, and only the outputs are computed by segments.
+bool scan_ordered(const gdr_scan_args *a) { return a->token_dtype == GDR_F32 && a->state_dtype == GDR_BF16; }
+
 // Tokens a segment for rows that are cut, or 0.  A block does 64 channels of a row from end to end, so a call
 // lasts as long as its longest row, or as the fullest multiprocessor; a token of a block that has its
 // multiprocessor to itself takes 0.6 of the time of one that shares it with a second.  Cut rows spread evenly, and
 // cost a pass for the segments' own states (0.65 of a token's time a token), 48 tokens' time a segment to
 // begin and end and 250 tokens' for two more launches.  Measured, cut against whole, 16 states, us: 16383 tokens x 2048
 // channels 287 (864 tokens a segment; 2048: 330, 304: 320) against 915, 2048 x 2048 61 (256) / 123, 4 rows of 1024 to 4096 x 512 86 / 235;
-// left whole by this rule: 2 rows of 4096 x 4096 287 / 237.
+// left whole by this rule: 2 rows of 4096 x 4096 287 / 237.  Where states go through in order, a token of them takes
+// a third of the time of a token of 16 states, less beside more states.  Measured, cut against whole, float32, us: 16383
+// tokens x 2048 channels 1254 / 1695, 8192 x 1024 channels x 64 states 757 / 2208, 2500 x 64 channels 167 / 269.
 int plan_scan(const gdr_scan_args *a) {
+    const bool ordered = scan_ordered(a);
+    if (ordered && !a->out) return 0;
     if (a->batch < 1 || a->batch > 32 || !a->total_tokens || (a->max_row_len >= 1 && a->max_row_len <= kShortRow)) return 0;
     const double tiles = a->nk * std::ceil((double)a->nv / a->nk * a->V / 64), T = (double)a->total_tokens;
     const double sms = 152.0, slots = a->K <= 32 ? 2 * sms : sms;
     double longest = a->max_row_len > 0 ? (double)a->max_row_len : std::ceil(T / a->batch);
     if (longest > T) longest = T;
-    constexpr double kAlone = 0.6, kFirst = 0.65, kUnit = 48.0, kExtra = 250.0;
+    constexpr double kAlone = 0.6, kFirst = 0.65, kUnit = 48.0, kExtra = 250.0, kStates = 0.34;
     const auto share = [&](double blocks) { return blocks <= sms ? kAlone : 1.0; };
     double best = std::fmax(longest * share(a->batch * tiles), T * tiles / slots);
+    const double parts = std::ceil(a->K / 8.0) * tiles;
+    const double states = kStates / std::fmax(1.0, a->K / 32.0) * std::fmax(longest, T * parts / sms);
     int seg = 0;
     for (int n = 2; n <= 64; ++n) {
         const double len = std::ceil(longest / n / 8) * 8;
         if (len < 128) break;
         const double blocks = std::ceil(T / len + 0.5 * (a->batch - 1)) * tiles;
-        const double cost = std::ceil(blocks / slots) * (len + kUnit) * share(blocks) * (1 + kFirst) + kExtra;
+        const double main = std::ceil(blocks / slots) * (len + kUnit) * share(blocks);
+        const double cost = ordered ? main + states + kExtra / 2 : main * (1 + kFirst) + kExtra;
         if (cost < 0.9 * best) {
             best = cost / 0.9;
             seg = (int)len;
@@ -198,7 +210,7 @@ int plan_scan(const gdr_scan_args *a) {
 }
 
 int64_t scan_bytes(const gdr_scan_args *a, int seg) {
-    return gdr::scan_pieces(a->total_tokens, seg, a->batch) * (int64_t)a->nv * a->V * (a->K + 1) * 4;
+    return gdr::scan_pieces(a->total_tokens, seg, a->batch) * (int64_t)a->nv * a->V * (a->K + (scan_ordered(a) ? 0 : 1)) * 4;
 }
 
 }  // namespace
@@ -318,6 +330,7 @@ int gdr_selective_scan(const gdr_scan_args *a, void *stream) {
                (!a->out || vector_rows(a->C, a->token_dtype, four, p.C_ts, p.C_hs));
     p.seg = plan_scan(a);
     if (p.seg && (!a->workspace || a->workspace_bytes < scan_bytes(a, p.seg))) p.seg = 0;
+    p.ordered = scan_ordered(a);
     p.ws = static_cast<float *>(a->workspace);
     const bool db = a->dt_dtype == GDR_BF16;
     if (a->max_row_len >= 1 && a->max_row_len <= kShortRow)

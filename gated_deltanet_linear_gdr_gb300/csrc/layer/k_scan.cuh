@@ -55,9 +55,17 @@ __device__ __forceinline__ bool scan_piece(const ScanParams &p, long long piece,
     const long long left = u.len - from, kept = u.kept - from;
     u.last = left <= p.seg;
     u.len = (int)(left < p.seg ? left : p.seg);
-    u.kept = kept <= 0 || kept > u.len ? 0 : (int)kept;
+    u.kept = kept <= 0 || kept > u.len || p.ordered ? 0 : (int)kept;
     u.piece = piece;
     return true;
+}
+
+// The first segment of row b among all rows' segments.
+__device__ __forceinline__ long long scan_first_piece(const ScanParams &p, int b, int lane) {
+    ScanUnit r;
+    int n = 0;
+    if (lane < b && scan_row(p, lane, false, r)) n = pieces(r.len, p.seg);
+    return (long long)__reduce_add_sync(kFull, (unsigned)n);
 }
 
 // The n-th longest of up to 32 rows: blocks run in their order, and what comes last should be short.
@@ -81,27 +89,33 @@ template <typename TT, typename DT, int KT, int NW> struct ScanShared {
                          fy = fC + 2 * 4 * N * KP, bytes = fy + 2 * 4 * NW * N * W;
 };
 
-// READ: with outputs.  Without them states move only: into the slots, or (first != 0)
-// each segment's own state, from zero, and the sum of its step sizes into the workspace.
+// READ: with outputs.  Without them states move only: into the slots, or (kOwn) each segment's own state, from zero, and
+// the sum of its step sizes into the workspace, or (kOrdered) into the slots and each segment's start state into the
+// workspace, a block KP of the states: without a readout they have nothing to do with one another.
+enum ScanPass { kMain, kOwn, kOrdered };
 template <typename TT, typename DT, int KT, int NW, bool VEC, bool READ>
 __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT * NW <= 32 ? 2 : 1)
-    k_scan(const __grid_constant__ ScanParams p, int tiles, int first) {
+    k_scan(const __grid_constant__ ScanParams p, int tiles, int pass) {
     using Sh = ScanShared<TT, DT, KT, NW>;
     constexpr int W = Sh::W, KP = Sh::KP, N = Sh::N, R = Sh::ring;
     extern __shared__ __align__(16) unsigned char shared[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const unsigned all = (unsigned)(p.nk * tiles);
+    const bool first = !READ && pass == kOwn, ordered = !READ && pass == kOrdered;
+    const unsigned parts = ordered ? (unsigned)(p.K + KP - 1) / KP : 1;  // blocks that share the states
+    const unsigned all = (unsigned)(p.nk * tiles) * parts;
     unsigned row = blockIdx.x / all;
-    const unsigned tg = blockIdx.x - row * all;
+    const unsigned part = ordered ? (blockIdx.x - row * all) % parts : 0, tg = (blockIdx.x - row * all) / parts;
+    const int kbase = (int)part * KP, K = p.K - kbase;  // this block's states
     const int g = (int)(tg / (unsigned)tiles), tile = (int)(tg - (unsigned)g * (unsigned)tiles);
     ScanUnit u;
-    if (!p.seg && p.batch <= 32) row = scan_longest(p, row, lane);
-    if (p.seg) {
+    if ((!p.seg || ordered) && p.batch <= 32) row = scan_longest(p, row, lane);
+    if (p.seg && !ordered) {
         if (!scan_piece(p, row, tg == 0 && warp == 0 && !first, lane, u)) return;
         if (first && u.last) return;  // no segment starts from its state
     } else if (!scan_row(p, (int)row, tg == 0 && tid == 0, u)) {
         return;
     }
+    if (ordered) u.piece = scan_first_piece(p, (int)row, lane);
     const int c0 = tile * W, width = min(W, p.r * p.V - c0);  // channels of the key head's value heads, this block's first
     // A channel of the block as (value head, channel).
     auto head = [&](int c, int &j) {
@@ -124,12 +138,12 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
             cj[e] = 0;
             ch[e] = on[e] ? head(2 * lane + e, cj[e]) : 0;
         }
-        const int have = min(KT, p.K - warp * KT);  // states that there are
-        const long long k0 = (long long)warp * KT;
+        const int have = min(KT, K - warp * KT);  // states that there are
+        const long long k0 = kbase + warp * KT;
         const long long st0 = (long long)u.slot * p.st_slot + (long long)ch[0] * p.st_head + cj[0] + k0 * p.st_k;
         const long long st1 = (long long)u.slot * p.st_slot + (long long)ch[1] * p.st_head + cj[1] + k0 * p.st_k;
-        const long long ws0 = ((u.piece * p.nv + ch[0]) * p.K + k0) * p.V + cj[0];  // in the workspace, [nv, K, V] a segment
-        const long long ws1 = ((u.piece * p.nv + ch[1]) * p.K + k0) * p.V + cj[1];
+        long long ws0 = ((u.piece * p.nv + ch[0]) * p.K + k0) * p.V + cj[0];  // in the workspace, [nv, K, V] a segment
+        long long ws1 = ((u.piece * p.nv + ch[1]) * p.K + k0) * p.V + cj[1];
 #pragma unroll
         for (int i = 0; i < KT; ++i) {
             S[i] = A[i] = make_float2(0.0f, 0.0f);
@@ -137,7 +151,7 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
             if (on[0]) A[i].x = rate<TT>(p.A[ch[0] * p.a_hs + cj[0] * p.a_vs + (k0 + i) * p.a_ks]);
             if (on[1]) A[i].y = rate<TT>(p.A[ch[1] * p.a_hs + cj[1] * p.a_vs + (k0 + i) * p.a_ks]);
             if (first) continue;
-            if (p.seg) {
+            if (p.seg && !ordered) {
                 if (on[0]) S[i].x = p.ws[ws0 + (long long)i * p.V];
                 if (on[1]) S[i].y = p.ws[ws1 + (long long)i * p.V];
             } else if (p.st_bf16) {
@@ -151,11 +165,11 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
             }
         }
         // the states into their slot, or a segment's into the workspace
-        auto put = [&]() {
+        auto put = [&](bool ws) {
 #pragma unroll
             for (int i = 0; i < KT; ++i) {
                 if (i >= have) continue;
-                if (first) {
+                if (ws) {
                     if (on[0]) p.ws[ws0 + (long long)i * p.V] = S[i].x;
                     if (on[1]) p.ws[ws1 + (long long)i * p.V] = S[i].y;
                 } else if (p.st_bf16) {
@@ -187,7 +201,7 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
 #pragma unroll
             for (int i = 0; i < KT; ++i) {
                 const float2 e = __fmul2_rn(dv, A[i]);
-                S[i] = __ffma2_rn(make_float2(decay<TT>(e.x), decay<TT>(e.y)), S[i], __fmul2_rn(xv, make_float2(Bv[i], Bv[i])));
+                S[i] = advance<TT>(make_float2(decay<TT>(e.x), decay<TT>(e.y)), S[i], __fmul2_rn(xv, make_float2(Bv[i], Bv[i])));
                 if (READ) {
                     y = __ffma2_rn(make_float2(Cv[i], Cv[i]), S[i], y);
                 }
@@ -205,7 +219,7 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
                 for (int t = 0; t < N; ++t) {
                     const float2 v = token(d + t * W, x + t * W, b + t * KP, q + t * KP);
                     if (READ) *reinterpret_cast<float2 *>(y + t * W) = v;
-                    if (t + 1 == cut) put();
+                    if (t + 1 == cut) put(false);
                 }
                 return;
             }
@@ -219,20 +233,37 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
 #pragma unroll
                     for (int t = 0; t < 4; ++t) *reinterpret_cast<float2 *>(y + (t0 + t) * W) = v[t];
             }
-            if (here) put();  // behind the chunk, or behind the row's last token
+            if (here) put(false);  // behind the chunk, or behind the row's last token
         };
         __syncthreads();
         int n = u.len, cut = first ? 0 : u.kept;
+        // segments begin where chunks do
+        int until = 0;
+        long long left = ordered ? scan_pieces(p.T, p.seg, p.batch) - u.piece : 0;  // places for their states
+        auto begins = [&]() {
+            if (!ordered || until-- > 0) return;
+            until = p.seg / N - 1;
+            if (left-- <= 0) return;
+            put(true);
+            ws0 += (long long)p.nv * p.K * p.V;
+            ws1 += (long long)p.nv * p.K * p.V;
+        };
         for (int k = 0; k <= chunks; ++k) {
-            if (k < chunks) chunk(std::integral_constant<int, 0>{}, n, cut);
+            if (k < chunks) {
+                begins();
+                chunk(std::integral_constant<int, 0>{}, n, cut);
+            }
             __syncthreads();
             if (++k > chunks) break;
-            if (k < chunks) chunk(std::integral_constant<int, 1>{}, n - N, cut - N);
+            if (k < chunks) {
+                begins();
+                chunk(std::integral_constant<int, 1>{}, n - N, cut - N);
+            }
             __syncthreads();
             n -= 2 * N;
             cut -= 2 * N;
         }
-        if (first) put();
+        if (first) put(true);
         return;
     }
 
@@ -257,7 +288,7 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
     const TT *const xp = static_cast<const TT *>(p.x) + (u.t0 + mt) * p.x_ts + (long long)mh * p.x_hs + mj;
     const TT *const zp = READ && p.z ? static_cast<const TT *>(p.z) + (u.t0 + mt) * p.z_ts + (long long)mh * p.z_hs + mj : nullptr;
     const DT *const dp = static_cast<const DT *>(p.dt) + (u.t0 + mt) * p.dt_ts + (long long)mh * p.dt_hs + mj * p.dt_es;
-    const TT *const bp = static_cast<const TT *>(p.B) + u.t0 * p.B_ts + (long long)g * p.B_hs;
+    const TT *const bp = static_cast<const TT *>(p.B) + u.t0 * p.B_ts + (long long)g * p.B_hs + kbase;
     const TT *const cp = READ ? static_cast<const TT *>(p.C) + u.t0 * p.C_ts + (long long)g * p.C_hs : nullptr;
     float bias[4], D[4];
 #pragma unroll
@@ -267,7 +298,7 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
         D[i] = READ && mon && p.D ? p.D[mh * p.d_hs + j * p.d_vs] : 0.0f;
     }
     constexpr int NB = (READ ? 2 : 1) * N * KP;  // values of B and C in a chunk
-    const bool bc_vec = p.bc_vec && p.K == KP;
+    const bool bc_vec = p.bc_vec && (ordered ? K >= KP : K == KP);
     // a thread's of them: NV vectors of four, or NT one by one
     constexpr int NV = (NB / 4 + kScanHelpers - 1) / kScanHelpers, NT = (NB + kScanHelpers - 1) / kScanHelpers;
     // Values that no asynchronous copy can move (2 bytes, not as vectors) wait here for a chunk's time.
@@ -323,7 +354,7 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     const int v = id + i * kScanHelpers, w = v % (N * KP), s = w / KP;
-                    if (v < NB && s < n && w % KP < p.K) {
+                    if (v < NB && s < n && w % KP < K) {
                         const TT *from = v < N * KP ? bp + (long long)(ahead + s) * p.B_ts + w % KP : cp + (long long)(ahead + s) * p.C_ts + w % KP;
                         if constexpr (!slow) cp_async<4>(reinterpret_cast<TT *>(to + Sh::B) + v, from);
                         else wbc[i] = *from;
@@ -427,7 +458,7 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 const int v = id + i * kScanHelpers, w = v % (N * KP);
-                if (v < NB) *place(v) = w / KP < n && w % KP < p.K ? to_f32(rb[v]) : 0.0f;
+                if (v < NB) *place(v) = w / KP < n && w % KP < K ? to_f32(rb[v]) : 0.0f;
             }
         }
     };
@@ -570,30 +601,37 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
     }
 }
 
-template <typename TT, typename DT, int KT, int NW, bool VEC> cudaError_t scan_go(const ScanParams &p, cudaStream_t s) {
+template <typename TT, typename DT, int KT, int NW, bool VEC, bool READ>
+cudaError_t scan_launch(const ScanParams &p, long long rows, int parts, int pass, cudaStream_t s) {
     using Sh = ScanShared<TT, DT, KT, NW>;
     static_assert(Sh::bytes <= 227 << 10, "a block's shared memory");
-    constexpr int threads = 32 * NW + kScanHelpers;
+    constexpr auto kernel = k_scan<TT, DT, KT, NW, VEC, READ>;
     static LaunchCache cache;
     LaunchInfo info;
-    cudaError_t e = launch_info(cache, &info, [](LaunchInfo &) {
-        const cudaError_t f = cudaFuncSetAttribute(k_scan<TT, DT, KT, NW, VEC, false>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::bytes);
-        if (f != cudaSuccess) return f;
-        return cudaFuncSetAttribute(k_scan<TT, DT, KT, NW, VEC, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::bytes);
+    const cudaError_t e = launch_info(cache, &info, [](LaunchInfo &) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::bytes);
     });
     if (e != cudaSuccess) return e;
-    const long long tiles = ((long long)p.r * p.V + Sh::W - 1) / Sh::W;
-    const long long rows = p.seg ? scan_pieces(p.T, p.seg, p.batch) : p.batch, blocks = rows * p.nk * tiles;
+    const long long tiles = ((long long)p.r * p.V + Sh::W - 1) / Sh::W, blocks = rows * p.nk * tiles * parts;
     if (blocks >= 1ll << 31) return cudaErrorInvalidConfiguration;
-    if (p.seg) {
-        k_scan<TT, DT, KT, NW, VEC, false><<<(unsigned)blocks, threads, Sh::bytes, s>>>(p, (int)tiles, 1);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    kernel<<<(unsigned)blocks, 32 * NW + kScanHelpers, Sh::bytes, s>>>(p, (int)tiles, pass);
+    return cudaGetLastError();
+}
+
+template <typename TT, typename DT, int KT, int NW, bool VEC> cudaError_t scan_go(const ScanParams &p, cudaStream_t s) {
+    const long long rows = p.seg ? scan_pieces(p.T, p.seg, p.batch) : p.batch;
+    cudaError_t e;
+    if (p.seg && p.ordered) {
+        if constexpr (sizeof(TT) == 4) {
+            // eight states a block, two a warp, whatever K
+            e = scan_launch<TT, DT, 2, 4, VEC, false>(p, p.batch, (p.K + 7) / 8, kOrdered, s);
+            if (e != cudaSuccess) return e;
+        }
+    } else if (p.seg) {
+        if ((e = scan_launch<TT, DT, KT, NW, VEC, false>(p, rows, 1, kOwn, s)) != cudaSuccess) return e;
         if ((e = launch_scan_join(p, s)) != cudaSuccess) return e;
     }
-    if (p.out) k_scan<TT, DT, KT, NW, VEC, true><<<(unsigned)blocks, threads, Sh::bytes, s>>>(p, (int)tiles, 0);
-    else k_scan<TT, DT, KT, NW, VEC, false><<<(unsigned)blocks, threads, Sh::bytes, s>>>(p, (int)tiles, 0);
-    return cudaGetLastError();
+    return p.out ? scan_launch<TT, DT, KT, NW, VEC, true>(p, rows, 1, kMain, s) : scan_launch<TT, DT, KT, NW, VEC, false>(p, rows, 1, kMain, s);
 }
 
 // States a warp and warps, by K.

@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW)
                 for (int e = 0; e < 4; ++e) {
                     d[e] = (VEC && !p.dt_es ? now.d.get(0) : now.d.get(e)) + bias[e];
                     if (p.softplus) d[e] = softplus<TT>(d[e]);
-                    in[e] = d[e] * now.x.get(e);
+                    in[e] = __fmul_rn(d[e], now.x.get(e));
                 }
 #pragma unroll
                 for (int i = 0; i < KT; ++i) {
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW)
                     const float B = now.B[i / 4].get(i % 4), C = now.C[i / 4].get(i % 4);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        S[i][e] = fmaf(decay<TT>(d[e] * A[i][e]), S[i][e], in[e] * B);
+                        S[i][e] = advance<TT>(decay<TT>(__fmul_rn(d[e], A[i][e])), S[i][e], __fmul_rn(in[e], B));
                         y[e] = fmaf(C, S[i][e], y[e]);  // of no meaning, and not used, where there are no outputs
                     }
                 }

@@ -127,6 +127,7 @@ struct ScanParams {
     // rows cut into segments of `seg` tokens (0: whole): ws holds, for each of them,
     // its own state from zero, which becomes its start state, and the sum of its step sizes
     int seg;
+    int ordered;       // segments' start states are left by one pass through each row, in its order; ws has nothing else
     float *ws;
     unsigned *status;
 };

@@ -31,10 +31,24 @@ template <typename TT> __device__ __forceinline__ float rate(float a) {
 }
 template <typename TT> __device__ __forceinline__ float decay(float e) { return sizeof(TT) == 2 ? ex2(e) : expf(e); }
 
+// A state's step from its decay and the token's own part.  float32 tokens round the product and the sum one by one, as
+// they do every operation on the way to a state, so that all forms of a call, and plain float32 arithmetic, have the
+// same states bit for bit: a bfloat16 pool can make neighbours, 2^16 times as far apart, of states that differ in their
+// last bit, and the next call starts from them.  bfloat16 outputs do not show that; bfloat16 tokens take the fused form,
+// half the instructions.
+template <typename TT> __device__ __forceinline__ float advance(float power, float S, float own) {
+    return sizeof(TT) == 2 ? fmaf(power, S, own) : __fadd_rn(__fmul_rn(power, S), own);
+}
+template <typename TT> __device__ __forceinline__ float2 advance(float2 power, float2 S, float2 own) {
+    if (sizeof(TT) == 2) return __ffma2_rn(power, S, own);
+    const float2 m = __fmul2_rn(power, S);  // added one by one: nvcc 13.0 makes one instruction of __fadd2_rn and this
+    return make_float2(__fadd_rn(m.x, own.x), __fadd_rn(m.y, own.y));
+}
+
 // log(1 + e^v) without cancellation: max(v, 0) + log1p(e^-|v|).  bfloat16 tokens: log1p(e) / e by its Chebyshev
 // interpolation of degree 8 over [0, 1], off by 2^-22 at most.
 template <typename TT> __device__ __forceinline__ float softplus(float v) {
-    if (sizeof(TT) == 4) return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v)));
+    if (sizeof(TT) == 4) return __fadd_rn(fmaxf(v, 0.0f), log1pf(expf(-fabsf(v))));
     const float e = ex2(-kLog2e * fabsf(v));
     float q = 5.126102143e-03f;
     q = fmaf(q, e, -2.907406469e-02f);

@@ -577,8 +577,21 @@ int gdr_short_conv(const gdr_short_conv_args *args, void *stream);
  *          counted tokens are).  A verify pass of drafts runs without keep_state,
  *          the accepted tokens then go in by such a call.
  * workspace  as in gdr_linattn_args, by gdr_selective_scan_workspace_bytes().
- * No two rows of a call move the same slot.  K is 1 to 128, V any.  A bfloat16 pool and bfloat16 outputs are rounded to
- * nearest-even once.  A non-finite value spoils its own row only.
+ * No two rows of a call move the same slot.  K is 1 to 128, V any.  A non-finite value spoils its own row only.
+ *
+ * Precision.  States and sums are float32 inside a call; a bfloat16 pool and
+ * bfloat16 outputs are rounded to nearest-even once.
+ *   float32 tokens: expf and log1pf, and every operation that leads to a state
+ *   is rounded by itself, in the order above (softplus(v) = max(v, 0) +
+ *   log1p(e^-|v|); d x before B): states are those of plain float32 arithmetic,
+ *   bit for bit.  Only a row that is cut over a float32 pool (see below) has the
+ *   roundings of its joined decays in them.
+ *   bfloat16 tokens, whose own rounding is 2^-8: softplus(v) is off by up to
+ *   2^-21 of itself (for v < 0 by |v| 2^-24 more), a decay e^-a by up to 2^-22
+ *   and a 2^-23.  A decay's error is downwards mostly, so that a state that
+ *   remembers n tokens is low by some n 2^-25 of itself (1000 tokens: 3e-5), in a
+ *   float32 pool too.
+ *   The gate, either type: off by up to (2 |z| + 12) 2^-24 of itself.
  */
 typedef struct gdr_scan_args {
     int32_t batch;
