@@ -140,8 +140,8 @@ template <typename PT> struct Weights {
 };
 
 // Of up to 32 parts, part `lane`'s weight `mine`: the one at which `before` and the running sum pass `share`,
-// the last one with a weight where none does, -1 where there is no weight; `base`: the sum ahead of it;
-// `passed`: whether one does.
+// the last one with a weight where none does, -1 where there is no weight; `base`: the sum ahead of it, which is at
+// most the share, although the running sums' roundings may put it above; `passed`: whether one does.
 __device__ __forceinline__ int part_of(double mine, double before, double share, int lane, double &base, bool &passed) {
     double upto = mine;
 #pragma unroll
@@ -152,7 +152,7 @@ __device__ __forceinline__ int part_of(double mine, double before, double share,
     const unsigned some = __ballot_sync(kFull, mine > 0.0), past = __ballot_sync(kFull, mine > 0.0 && before + upto > share);
     const int which = past ? __ffs(past) - 1 : 31 - __clz(some);
     passed = past != 0;
-    base = before + __shfl_sync(kFull, upto - mine, which < 0 ? 0 : which);
+    base = fmin(before + __shfl_sync(kFull, upto - mine, which < 0 ? 0 : which), share);
     return which;
 }
 
@@ -287,7 +287,9 @@ template <typename PT> __global__ void __launch_bounds__(kThreads, 2) k_accept(c
                 double first;
                 bool passed;
                 const int l = part_of(own.value(), ahead, share, lane, first, passed);
-                int found = -1;  // the token past the share; the last one with a weight, where rounding leaves none
+                // the token past the share: the last one with a weight and no more than the share ahead of it, as the
+                // lane's first weight has it in any case
+                int found = -1;
                 if (lane == l) {
 #pragma unroll
                     for (int j = 0; j < C; ++j) {
@@ -299,7 +301,7 @@ template <typename PT> __global__ void __launch_bounds__(kThreads, 2) k_accept(c
                 }
             }
             if (joint_passed) break;
-            base += joint_sum;
+            base = fmin(base + joint_sum, share);  // not passed, but for the roundings of this sum
         }
     }
     if (rank == 0) {
