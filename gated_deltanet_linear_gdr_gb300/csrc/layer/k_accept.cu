@@ -13,12 +13,14 @@
 // The token has to be the one that exact arithmetic finds: with a vocabulary of
 // 1e5 a float32 sum would miss it in a few draws of a hundred.  Differences are
 // kept as (difference, its rounding error) and sums as (sum, error) of float32 pairs by
-// two-sum (Knuth, The Art of Computer Programming 2, 4.2.2), good to 46 bits and
-// more: 14 additions a token, which the FP32 pipes do while memory delivers it; the
-// FP64 pipes (2 operations a cycle and multiprocessor) would take several times as
-// long.  Only single warps, at the joints, work in double.
+// two-sum (Knuth, The Art of Computer Programming 2, 4.2.2): 14 additions a token, which
+// the FP32 pipes do while memory delivers it; the FP64 pipes (2 operations a cycle and
+// multiprocessor) would take several times as long.  The error is itself a sum that is
+// rounded: after n additions it has lost n^2/2 2^-48 of the sum at worst.  So a lane
+// begins a new pair every 64 tokens: good to 2^-37 at worst, to 2^-45 by chance, however
+// many tokens there are.  Beside that only single warps, at the joints, work in double.
 //
-// Measured, float32 probabilities: 256 rows of 5 to 8 tokens against 32000 tokens 23 us (9.3 at the copy rate), one
+// Measured, float32 probabilities: 256 rows of 5 to 8 tokens against 32000 tokens 24 us (9.3 at the copy rate), one
 // row against 131072 13 us, of which the host takes 11.
 #include <cooperative_groups.h>
 
@@ -63,6 +65,38 @@ struct Sum {
     __device__ __forceinline__ double value() const { return (double)s + (double)c; }
 };
 
+// A lane's sum over any number of tokens: pairs of kFold of them at most, added up as normalised pairs (each of which
+// adds 3 2^-48 at most: Joldes, Muller and Popescu 2017, tight and rigorous error bounds for basic building blocks of
+// double-word arithmetic), kFold of those at most in double.
+constexpr int kFold = 64;
+struct LongSum {
+    Sum part, mid;
+    double all = 0.0;
+    int folds = 0;
+    __device__ __forceinline__ void fold() {
+        const float h = __fadd_rn(part.s, part.c), l = __fsub_rn(part.c, __fsub_rn(h, part.s));
+        const float t = __fadd_rn(mid.s, h), b = __fsub_rn(t, mid.s);
+        const float e = __fadd_rn(__fsub_rn(mid.s, __fsub_rn(t, b)), __fsub_rn(h, b));
+        const float w = __fadd_rn(e, __fadd_rn(mid.c, l));
+        mid.s = __fadd_rn(t, w);
+        mid.c = __fsub_rn(w, __fsub_rn(mid.s, t));
+        part = Sum();
+        if (++folds % kFold == 0) {
+            all += mid.value();
+            mid = Sum();
+        }
+    }
+    __device__ __forceinline__ Sum pair() {
+        if (folds == 0) return part;
+        fold();
+        if (folds <= kFold) return mid;
+        all += mid.value();
+        mid.s = (float)all;
+        mid.c = (float)(all - (double)mid.s);
+        return mid;
+    }
+};
+
 // What a row's draw goes by: the weights of tokens [0, vocab).
 template <typename PT> struct Weights {
     static constexpr int C = 16 / (int)sizeof(PT);  // tokens of a vector
@@ -85,15 +119,20 @@ template <typename PT> struct Weights {
     }
     // The sum of a lane's part of [i0, i1), C tokens or one at a time.
     __device__ __forceinline__ Sum slow(int i0, int i1, int lane) const {
-        Sum a;
-        for (int i = i0 + lane; i < i1; i += 32)
-            if (i >= 0) one(a, i);
-        return a;
+        LongSum a;
+        int n = 0;
+        for (int i = i0 + lane; i < i1; i += 32) {
+            if (i >= 0) one(a.part, i);
+            if (++n % kFold == 0) a.fold();
+        }
+        return a.pair();
     }
     // The same by vectors.  Values that do not count leave a NaN in `odd`: then the sum is not to be used.
     template <bool DIFF> __device__ __forceinline__ Sum fast(int i0, int i1, int lane, float &odd) const {
         constexpr int U = 2;
-        Sum a;
+        LongSum sum;
+        Sum &a = sum.part;
+        int n = 0;
         // whole vectors lie in [a0, a1); before them there are tokens only at the row's beginning, behind them only at its end
         const int a0 = i0 < 0 ? i0 + C : i0, a1 = i1 - (i1 - start) % C;
         if (i0 < 0 && lane < a0 && lane < i1) one(a, lane);
@@ -126,8 +165,9 @@ template <typename PT> struct Weights {
                     }
                 }
             }
+            if (++n % (kFold / (C * U)) == 0) sum.fold();
         }
-        return a;
+        return sum.pair();
     }
     // The sum of a warp's stretch [i0, i1), in every lane.
     __device__ __forceinline__ Sum stretch(int i0, int i1, int lane) const {

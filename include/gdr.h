@@ -673,8 +673,11 @@ int64_t gdr_selective_scan_workspace_bytes(const gdr_scan_args *args);
  *
  * (none, by a number of 1 or more: the last x with a weight; numbers below 0 and
  * NaN count as 0, for which it is the first).  So the tokens are distributed as
- * the target's own.  Comparisons and differences are exact, sums carry 46 bits at
- * least; weights need not sum to 1, but to less than 2^127.
+ * the target's own.  Comparisons and differences are exact; a sum is off by at
+ * most 2^-36 of itself (by chance 2^-45) for any vocabulary, so that the token is
+ * the rule's unless its share lies that near a running sum: then it is a
+ * neighbouring token with a weight.  Weights need not sum to 1, but to less than
+ * 2^127.
  *
  * out_tokens [batch, max_row_len] int32: the accepted drafts, the drawn token, -1
  *          behind it.  counts [batch] int32: the accepted drafts and 1, which is

@@ -41,3 +41,24 @@ def test_a_share_on_a_border_draws_a_token(dtype, rows, vocab):
             mine, before = upto.gather(1, got[:, None]), upto.gather(1, got[:, None]) - p.double().gather(1, got[:, None])
             near = 2.0 ** -36 * total
             assert bool((before <= total / 2 + near).all()) and bool((mine >= total / 2 - near).all())
+
+
+@pytest.mark.parametrize("behind", [False, True])
+def test_sums_of_many_tokens_by_one_block(behind):
+    """2^27 weights of a row that one block sums up, 2^18 of them a lane: halves of equal sums, one of them larger by
+    2^-34 of the total.  The share then lies 2^-35 of it away from the border between the halves, and a sum is good to
+    2^-36 at worst: 64 additions to a pair of float32 lose 64^2 / 2 * 2^-48 of it, joining 64 such parts as pairs
+    64 * 3 * 2^-48, and those in double, the warp's lanes and the warps far less."""
+    n = 1 << 27
+    g = torch.Generator(device=DEV).manual_seed(3)
+    w = torch.exp(3 * torch.randn(n // 2, generator=g, device=DEV))
+    w[777], w[-1] = 1.0, 100.0  # which takes the difference, and the weights beside the border
+    p = torch.cat([w, w.flip(0)])
+    at = n - 1 - 777 if behind else 777
+    p[at] = 1.0 + float(p.double().sum()) * 2.0 ** -34
+    exact = p.double()
+    first, whole = exact[:n // 2].sum(), exact.sum()
+    border = float((whole / 2 - first) / whole)
+    assert 2.0 ** -35.1 < (border if behind else -border) < 2.0 ** -34.9
+    got = _draw(p[None, :].expand(160, n), 0.5)
+    assert got.tolist() == [n // 2 if behind else n // 2 - 1] * 160
