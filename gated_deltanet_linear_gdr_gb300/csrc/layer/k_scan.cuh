@@ -197,16 +197,21 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
                     if (READ) *reinterpret_cast<float4 *>(Cv + i) = *reinterpret_cast<const float4 *>(q + i);
                 }
             }
-            float2 y = make_float2(0.0f, 0.0f);
+            constexpr int G = scan_group(KT);
+            float2 y[KT / G];
 #pragma unroll
             for (int i = 0; i < KT; ++i) {
                 const float2 e = __fmul2_rn(dv, A[i]);
                 S[i] = advance<TT>(make_float2(decay<TT>(e.x), decay<TT>(e.y)), S[i], __fmul2_rn(xv, make_float2(Bv[i], Bv[i])));
-                if (READ) {
-                    y = __ffma2_rn(make_float2(Cv[i], Cv[i]), S[i], y);
-                }
+                if (READ) y[i / G] = __ffma2_rn(make_float2(Cv[i], Cv[i]), S[i], i % G ? y[i / G] : make_float2(0.0f, 0.0f));
             }
-            return y;
+            if constexpr (READ) {
+#pragma unroll
+                for (int m = 1; m < KT / G; m *= 2)
+#pragma unroll
+                    for (int i = 0; i < KT / G; i += 2 * m) y[i] = __fadd2_rn(y[i], y[i + m]);
+            }
+            return y[0];
         };
         auto chunk = [&](auto half, int n, int cut) {  // tokens from the chunk on, and those of them before the slot's state
             constexpr int H = decltype(half)::value;
@@ -519,13 +524,20 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
             four(reinterpret_cast<const TT *>(done + Sh::x), rx);
             if (zp) four(reinterpret_cast<const TT *>(done + Sh::z), rz);
             const float *const fy = floats(Sh::fy) + half * NW * N * W;
-            four(fy, y);
+            // warps whose sums make up sixteen states' (four groups')
+            constexpr int Q = 4 * scan_group(KT) / KT;
 #pragma unroll
-            for (int w = 1; w < NW; ++w) {
-                float q[4];
-                four(fy + w * N * W, q);
+            for (int w = 0; w < NW; w += Q) {
+                float q[Q][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[i] += q[i];
+                for (int j = 0; j < Q; ++j) four(fy + (w + j) * N * W, q[j]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float sum = q[0][i];
+                    if constexpr (Q == 2) sum = q[0][i] + q[1][i];
+                    if constexpr (Q == 4) sum = (q[0][i] + q[1][i]) + (q[2][i] + q[3][i]);
+                    y[i] = w ? y[i] + sum : sum;
+                }
             }
         }
         steps(d, x, WHOLE ? N : left - N);

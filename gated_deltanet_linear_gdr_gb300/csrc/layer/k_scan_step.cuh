@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW)
     // this lane's four channels, and the one this thread finishes
     const int have = min(KT, p.K - warp * KT);  // states that there are, 0 or less: none
     const long long k0 = (long long)warp * KT;
+    const bool pairs = KT == 4 && p.K <= 8;  // groups of two states
     long long st_at[4], x_at[4], d_at[4];
     bool on[4];
     float A[KT][4], bias[4];
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW)
             Token next;
             if (!ONE && t + 1 < len) ask_token(w, t + 1, next);
             float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            [[maybe_unused]] float first[4];  // the sum of a group that another follows
             if (have > 0) {
                 float d[4], in[4];
 #pragma unroll
@@ -217,9 +219,16 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         S[i][e] = advance<TT>(decay<TT>(__fmul_rn(d[e], A[i][e])), S[i][e], __fmul_rn(in[e], B));
+                        if (KT == 8 ? i == 4 : i == 2 && pairs) {
+                            first[e] = y[e];
+                            y[e] = 0.0f;
+                        }
                         y[e] = fmaf(C, S[i][e], y[e]);  // of no meaning, and not used, where there are no outputs
                     }
                 }
+                if (KT == 8 ? have > 4 : have > 2 && pairs)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = first[e] + y[e];
                 if (t + 1 == w.kept) {
 #pragma unroll
                     for (int i = 0; i < KT; ++i)
@@ -233,7 +242,8 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW)
                 if (mon) {
                     float o = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < NW; i += 4) o += (q[i][tid] + q[i + 1][tid]) + (q[i + 2][tid] + q[i + 3][tid]);
+                    for (int i = 0; i < NW; i += KT == 8 ? 2 : 4)
+                        o += KT == 8 ? q[i][tid] + q[i + 1][tid] : (q[i][tid] + q[i + 1][tid]) + (q[i + 2][tid] + q[i + 3][tid]);
                     o = fmaf(D, to_f32(now.mx), o);
                     if (gate) o *= silu(to_f32(now.mz));
                     w.out[t * p.o_ts + mo_at] = from_f32<TT>(o);

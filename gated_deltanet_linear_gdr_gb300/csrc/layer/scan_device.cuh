@@ -45,6 +45,10 @@ template <typename TT> __device__ __forceinline__ float2 advance(float2 power, f
     return make_float2(__fadd_rn(m.x, own.x), __fadd_rn(m.y, own.y));
 }
 
+// The readout's order, the same in every form, so that a row has the same bits in any call: groups of four states (up to
+// 8 states: of two) by multiply-adds from 0; four groups as (0 + 1) + (2 + 3); these sums one after the other.
+__device__ constexpr int scan_group(int states_a_warp) { return states_a_warp < 4 ? 2 : 4; }
+
 // log(1 + e^v) without cancellation: max(v, 0) + log1p(e^-|v|).  bfloat16 tokens: log1p(e) / e by its Chebyshev
 // interpolation of degree 8 over [0, 1], off by 2^-22 at most.
 template <typename TT> __device__ __forceinline__ float softplus(float v) {

@@ -38,7 +38,8 @@
  *     in the device status word (GDR_STATUS_*), read with gdr_get_status().
  *   - Results do not depend on how a batch is composed or on which kernel the
  *     library picks: every pass uses one fixed order of float32 operations per
- *     (row, head), so the same row gives the same bits in any call.
+ *     (row, head), so the same row gives the same bits in any call.  (Exceptions
+ *     stand at their calls: gdr_linattn_args, gdr_scan_args, gdr_accept_args.)
  *   - Two live rows of one call must not share a pool slot (they would race).
  *   - Head sizes: K in {16, 32, 64, 128}; V = K, or V = 2K or (for K >= 32)
  *     V = K/2 for the forward, dense and snapshot passes and rollback
@@ -592,6 +593,13 @@ int gdr_short_conv(const gdr_short_conv_args *args, void *stream);
  *   remembers n tokens is low by some n 2^-25 of itself (1000 tokens: 3e-5), in a
  *   float32 pool too.
  *   The gate, either type: off by up to (2 |z| + 12) 2^-24 of itself.
+ *
+ * The same row gives the same bits in any call of the same K and types, but where
+ * it is cut: with a workspace, rows of a call of at most 32 are computed by
+ * segments whose number follows from the call's sizes, joined by powers of
+ * their decays, exp(A sum d), and differ from whole rows by the roundings of
+ * these.  Without a workspace no row is cut; float32 tokens over a bfloat16 pool
+ * have the same bits either way.
  */
 typedef struct gdr_scan_args {
     int32_t batch;

@@ -7,7 +7,7 @@ import torch
 
 import gated_deltanet_linear_gdr_gb300 as gdr
 from tests.state_space_helpers import U32, silu_error
-from tests.test_gpu_scan import BF16, DEV, F32, Case, _clean_status, _cut  # noqa: F401
+from tests.test_gpu_scan import BF16, DEV, F32, TYPES, Case, _clean_status, _cut, _ints  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +85,31 @@ def test_float32_tokens_bfloat16_pool_long_rows(lens, K, V):
     assert torch.equal(alone, half)
     out, _ = c.run(alone, keep_state=False, max_row_len=max(lens))
     assert torch.equal(alone, half)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("K", [3, 8, 16, 27, 32, 50, 64, 100, 128])
+@pytest.mark.parametrize("V", [32, 33])
+def test_rows_have_the_same_bits_in_every_form(types, K, V):
+    """Rows of up to 16 tokens, by the form for short rows, by chunks, alone, and among so many that blocks share
+    their states out another way."""
+    lens = [16, 1, 9, 2]
+    c = Case(lens, 1, 2, K, V, types, seed=K)
+    out, pool = c.run(max_row_len=16)
+    by_chunks, state = c.run(max_row_len=0)
+    assert torch.equal(out, by_chunks) and torch.equal(pool, state)
+    T, copies = sum(lens), 60
+    many = c.pool.repeat(copies, 1, 1, 1)
+    slot = torch.cat([c.slot + i * c.pool.shape[0] for i in range(copies)])
+    off = torch.cat([c.off[:-1] + i * T for i in range(copies)] + [_ints([T * copies])])
+    wide = [None if t is None else t.repeat(copies, 1, 1) for t in (c.x, c.dt, c.B, c.C, c.z)]
+    for bound in (0, 16):
+        moved = many.clone()
+        got = gdr.gdr_selective_scan(wide[0], wide[1], c.A, wide[2], wide[3], moved, slot, off, z=wide[4], D=c.D, dt_bias=c.bias,
+                                     max_row_len=bound)
+        assert torch.equal(got, out.repeat(copies, 1, 1)) and torch.equal(moved, pool.repeat(copies, 1, 1, 1))
+    ones = Case([1] * 5, 1, 2, K, V, types, seed=K)
+    single, kept = ones.run(max_row_len=1)
+    for bound in (0, 2):
+        got, state = ones.run(max_row_len=bound)
+        assert torch.equal(got, single) and torch.equal(state, kept)
