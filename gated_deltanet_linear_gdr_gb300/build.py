@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libgdr.so")
 SOURCES = ["api.cu", "k_decode.cu", "k_short.cu", "k_chain.cu", "k_chain_fwd.cu", "k_chain_fwd_kv.cu", "k_chain_conv.cu", "k_chain_verify.cu",
            "k_chain_snap.cu", "k_fold.cu", "k_probe.cu",
            "layer/api_layer.cu", "layer/k_norm.cu", "layer/k_norm_odd.cu", "layer/k_norm_pairs.cu", "layer/k_la_step.cu", "layer/k_la_chunk.cu", "layer/k_la_small.cu",
-           "layer/api_scan.cu", "layer/k_short_conv.cu", "layer/k_scan.cu", "layer/k_scan_bb.cu", "layer/k_scan_bf.cu", "layer/k_scan_ff.cu", "layer/k_scan_step_bb.cu", "layer/k_scan_step_bf.cu",
+           "layer/api_scan.cu", "layer/k_short_conv.cu", "layer/k_scan.cu", "layer/k_scan_bb.cu", "layer/k_scan_bf.cu", "layer/k_scan_ff.cu", "layer/k_scan_fx.cu", "layer/k_scan_step_bb.cu", "layer/k_scan_step_bf.cu",
            "layer/k_scan_step_ff.cu",
            "layer/k_accept.cu"]
 HEADERS = ["gdr_internal.h", "gdr_device.cuh", "gdr_pipe.cuh", "gdr_state.cuh", "k_chain.cuh", "gdr.map",

@@ -330,7 +330,6 @@ int gdr_selective_scan(const gdr_scan_args *a, void *stream) {
                (!a->out || vector_rows(a->C, a->token_dtype, four, p.C_ts, p.C_hs));
     p.seg = plan_scan(a);
     if (p.seg && (!a->workspace || a->workspace_bytes < scan_bytes(a, p.seg))) p.seg = 0;
-    p.ordered = scan_ordered(a);
     p.ws = static_cast<float *>(a->workspace);
     const bool db = a->dt_dtype == GDR_BF16;
     if (a->max_row_len >= 1 && a->max_row_len <= kShortRow)

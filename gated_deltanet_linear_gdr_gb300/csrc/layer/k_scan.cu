@@ -57,7 +57,7 @@ cudaError_t launch_scan_join(const ScanParams &p, cudaStream_t s) {
 }
 
 cudaError_t launch_scan(const ScanParams &p, bool tok_bf16, bool dt_bf16, bool vec, cudaStream_t s) {
-    if (!tok_bf16) return launch_scan_ff(p, vec, s);
+    if (!tok_bf16) return p.st_bf16 ? launch_scan_fx(p, vec, s) : launch_scan_ff(p, vec, s);
     return dt_bf16 ? launch_scan_bb(p, vec, s) : launch_scan_bf(p, vec, s);
 }
 

@@ -35,7 +35,7 @@ template <int BYTES> __device__ __forceinline__ void cp_async(void *to, const vo
 }
 
 // Segment `piece` of all rows' segments, for calls of at most 32 rows: lane l counts row l's.
-__device__ __forceinline__ bool scan_piece(const ScanParams &p, long long piece, bool leader, int lane, ScanUnit &u) {
+template <bool EXACT> __device__ __forceinline__ bool scan_piece(const ScanParams &p, long long piece, bool leader, int lane, ScanUnit &u) {
     ScanUnit r;
     bool live = false;
     if (lane < p.batch) live = scan_row(p, lane, leader && piece == 0, r);
@@ -55,7 +55,7 @@ __device__ __forceinline__ bool scan_piece(const ScanParams &p, long long piece,
     const long long left = u.len - from, kept = u.kept - from;
     u.last = left <= p.seg;
     u.len = (int)(left < p.seg ? left : p.seg);
-    u.kept = kept <= 0 || kept > u.len || p.ordered ? 0 : (int)kept;
+    u.kept = kept <= 0 || kept > u.len || EXACT ? 0 : (int)kept;
     u.piece = piece;
     return true;
 }
@@ -93,14 +93,14 @@ template <typename TT, typename DT, int KT, int NW> struct ScanShared {
 // the sum of its step sizes into the workspace, or (kOrdered) into the slots and each segment's start state into the
 // workspace, a block KP of the states: without a readout they have nothing to do with one another.
 enum ScanPass { kMain, kOwn, kOrdered };
-template <typename TT, typename DT, int KT, int NW, bool VEC, bool READ>
+template <typename TT, typename DT, int KT, int NW, bool VEC, bool READ, bool EXACT>
 __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT * NW <= 32 ? 2 : 1)
     k_scan(const __grid_constant__ ScanParams p, int tiles, int pass) {
     using Sh = ScanShared<TT, DT, KT, NW>;
     constexpr int W = Sh::W, KP = Sh::KP, N = Sh::N, R = Sh::ring;
     extern __shared__ __align__(16) unsigned char shared[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const bool first = !READ && pass == kOwn, ordered = !READ && pass == kOrdered;
+    const bool first = !READ && !EXACT && pass == kOwn, ordered = !READ && EXACT && pass == kOrdered;
     const unsigned parts = ordered ? (unsigned)(p.K + KP - 1) / KP : 1;  // blocks that share the states
     const unsigned all = (unsigned)(p.nk * tiles) * parts;
     unsigned row = blockIdx.x / all;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
     ScanUnit u;
     if ((!p.seg || ordered) && p.batch <= 32) row = scan_longest(p, row, lane);
     if (p.seg && !ordered) {
-        if (!scan_piece(p, row, tg == 0 && warp == 0 && !first, lane, u)) return;
+        if (!scan_piece<EXACT>(p, row, tg == 0 && warp == 0 && !first, lane, u)) return;
         if (first && u.last) return;  // no segment starts from its state
     } else if (!scan_row(p, (int)row, tg == 0 && tid == 0, u)) {
         return;
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
 #pragma unroll
             for (int i = 0; i < KT; ++i) {
                 const float2 e = __fmul2_rn(dv, A[i]);
-                S[i] = advance<TT>(make_float2(decay<TT>(e.x), decay<TT>(e.y)), S[i], __fmul2_rn(xv, make_float2(Bv[i], Bv[i])));
+                S[i] = advance<EXACT>(make_float2(decay<TT>(e.x), decay<TT>(e.y)), S[i], __fmul2_rn(xv, make_float2(Bv[i], Bv[i])));
                 if (READ) y[i / G] = __ffma2_rn(make_float2(Cv[i], Cv[i]), S[i], i % G ? y[i / G] : make_float2(0.0f, 0.0f));
             }
             if constexpr (READ) {
@@ -524,19 +524,17 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
             four(reinterpret_cast<const TT *>(done + Sh::x), rx);
             if (zp) four(reinterpret_cast<const TT *>(done + Sh::z), rz);
             const float *const fy = floats(Sh::fy) + half * NW * N * W;
-            // warps whose sums make up sixteen states' (four groups')
-            constexpr int Q = 4 * scan_group(KT) / KT;
+            // a warp's sum, or two warps' where a warp has one group
+            constexpr int Q = KT == 2 || (KT == 4 && sizeof(TT) == 2) ? 2 : 1;
 #pragma unroll
             for (int w = 0; w < NW; w += Q) {
-                float q[Q][4];
-#pragma unroll
-                for (int j = 0; j < Q; ++j) four(fy + (w + j) * N * W, q[j]);
+                float a[4], q[4];
+                four(fy + w * N * W, a);
+                if constexpr (Q == 2) four(fy + (w + 1) * N * W, q);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float sum = q[0][i];
-                    if constexpr (Q == 2) sum = q[0][i] + q[1][i];
-                    if constexpr (Q == 4) sum = (q[0][i] + q[1][i]) + (q[2][i] + q[3][i]);
-                    y[i] = w ? y[i] + sum : sum;
+                    if constexpr (Q == 2) a[i] += q[i];
+                    y[i] = w ? y[i] + a[i] : a[i];
                 }
             }
         }
@@ -613,11 +611,11 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
     }
 }
 
-template <typename TT, typename DT, int KT, int NW, bool VEC, bool READ>
+template <typename TT, typename DT, int KT, int NW, bool VEC, bool READ, bool EXACT>
 cudaError_t scan_launch(const ScanParams &p, long long rows, int parts, int pass, cudaStream_t s) {
     using Sh = ScanShared<TT, DT, KT, NW>;
     static_assert(Sh::bytes <= 227 << 10, "a block's shared memory");
-    constexpr auto kernel = k_scan<TT, DT, KT, NW, VEC, READ>;
+    constexpr auto kernel = k_scan<TT, DT, KT, NW, VEC, READ, EXACT>;
     static LaunchCache cache;
     LaunchInfo info;
     const cudaError_t e = launch_info(cache, &info, [](LaunchInfo &) {
@@ -630,39 +628,38 @@ cudaError_t scan_launch(const ScanParams &p, long long rows, int parts, int pass
     return cudaGetLastError();
 }
 
-template <typename TT, typename DT, int KT, int NW, bool VEC> cudaError_t scan_go(const ScanParams &p, cudaStream_t s) {
+template <typename TT, typename DT, int KT, int NW, bool VEC, bool EXACT> cudaError_t scan_go(const ScanParams &p, cudaStream_t s) {
     const long long rows = p.seg ? scan_pieces(p.T, p.seg, p.batch) : p.batch;
-    cudaError_t e;
-    if (p.seg && p.ordered) {
-        if constexpr (sizeof(TT) == 4) {
-            // eight states a block, two a warp, whatever K
-            e = scan_launch<TT, DT, 2, 4, VEC, false>(p, p.batch, (p.K + 7) / 8, kOrdered, s);
-            if (e != cudaSuccess) return e;
-        }
+    cudaError_t e = cudaSuccess;
+    if (p.seg && EXACT) {
+        // eight states a block, two a warp, whatever K
+        if constexpr (EXACT) e = scan_launch<TT, DT, 2, 4, VEC, false, true>(p, p.batch, (p.K + 7) / 8, kOrdered, s);
+        if (e != cudaSuccess) return e;
     } else if (p.seg) {
-        if ((e = scan_launch<TT, DT, KT, NW, VEC, false>(p, rows, 1, kOwn, s)) != cudaSuccess) return e;
-        if ((e = launch_scan_join(p, s)) != cudaSuccess) return e;
+        if constexpr (!EXACT) e = scan_launch<TT, DT, KT, NW, VEC, false, false>(p, rows, 1, kOwn, s);
+        if (e != cudaSuccess || (e = launch_scan_join(p, s)) != cudaSuccess) return e;
     }
-    return p.out ? scan_launch<TT, DT, KT, NW, VEC, true>(p, rows, 1, kMain, s) : scan_launch<TT, DT, KT, NW, VEC, false>(p, rows, 1, kMain, s);
+    return p.out ? scan_launch<TT, DT, KT, NW, VEC, true, EXACT>(p, rows, 1, kMain, s)
+                 : scan_launch<TT, DT, KT, NW, VEC, false, EXACT>(p, rows, 1, kMain, s);
 }
 
 // States a warp and warps, by K.
-template <typename TT, typename DT, bool VEC> cudaError_t scan_states(const ScanParams &p, cudaStream_t s) {
-    if (p.K <= 8) return scan_go<TT, DT, 2, 4, VEC>(p, s);
-    if (p.K <= 16) return scan_go<TT, DT, 4, 4, VEC>(p, s);
+template <typename TT, typename DT, bool VEC, bool EXACT> cudaError_t scan_states(const ScanParams &p, cudaStream_t s) {
+    if (p.K <= 8) return scan_go<TT, DT, 2, 4, VEC, EXACT>(p, s);
+    if (p.K <= 16) return scan_go<TT, DT, 4, 4, VEC, EXACT>(p, s);
     if (p.K <= 32) {
         // Eight warps of four states take half the steps for a token, four of eight read shared memory less often.
         // Measured with 32 states, us: 8 ragged rows x 4096 channels bfloat16 615 / 555, float32 1202 / 1294; 45 blocks
         // of 5 rows of up to 301 tokens, float32 55 / 82.
         const long long tiles = ((long long)p.r * p.V + kScanTile - 1) / kScanTile;
-        if (sizeof(TT) == 4 || (long long)p.batch * p.nk * tiles <= 152) return scan_go<TT, DT, 4, 8, VEC>(p, s);
-        if constexpr (sizeof(TT) == 2) return scan_go<TT, DT, 8, 4, VEC>(p, s);
+        if (sizeof(TT) == 4 || (long long)p.batch * p.nk * tiles <= 152) return scan_go<TT, DT, 4, 8, VEC, EXACT>(p, s);
+        if constexpr (sizeof(TT) == 2) return scan_go<TT, DT, 8, 4, VEC, EXACT>(p, s);
     }
-    if (p.K <= 64) return scan_go<TT, DT, 8, 8, VEC>(p, s);
-    return scan_go<TT, DT, 16, 8, VEC>(p, s);
+    if (p.K <= 64) return scan_go<TT, DT, 8, 8, VEC, EXACT>(p, s);
+    return scan_go<TT, DT, 16, 8, VEC, EXACT>(p, s);
 }
-template <typename TT, typename DT> cudaError_t scan_vec(const ScanParams &p, bool vec, cudaStream_t s) {
-    return vec ? scan_states<TT, DT, true>(p, s) : scan_states<TT, DT, false>(p, s);
+template <typename TT, typename DT, bool EXACT = false> cudaError_t scan_vec(const ScanParams &p, bool vec, cudaStream_t s) {
+    return vec ? scan_states<TT, DT, true, EXACT>(p, s) : scan_states<TT, DT, false, EXACT>(p, s);
 }
 
 }  // namespace gdr

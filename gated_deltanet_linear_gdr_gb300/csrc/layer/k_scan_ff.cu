@@ -1,4 +1,4 @@
-// Selective scan, float32 tokens and step sizes.
+// Selective scan, float32 tokens and pool.
 #include "k_scan.cuh"
 
 namespace gdr {

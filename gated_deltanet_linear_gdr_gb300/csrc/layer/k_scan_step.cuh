@@ -79,14 +79,15 @@ template <typename TT, typename DT, typename ST> struct StepRow {
 };
 
 // VEC: four channels are a vector everywhere (dt: that, or one value a head).  BC: so are four states of B
-// and C, and K is a multiple of KT.  ONE: rows of one token.  Sixteen warps a multiprocessor, 128 registers each.
-template <typename TT, typename DT, typename ST, int KT, int NW, bool VEC, bool BC, bool ONE>
+// and C, and K is a multiple of KT.  ONE: rows of one token.  PAIRS: up to 8 states, read out by groups of two.  Sixteen warps a multiprocessor, 128 registers each.
+template <typename TT, typename DT, typename ST, int KT, int NW, bool VEC, bool BC, bool ONE, bool PAIRS>
 __global__ void __launch_bounds__(32 * NW, 16 / NW)
     k_scan_step(const __grid_constant__ ScanParams p, int tiles, int rows) {
     __shared__ __align__(16) float part[2][NW][kStepTile];
     __shared__ StepRow<TT, DT, ST> info[kStepRows];
     constexpr bool AHEAD = BC && ONE && KT <= 4;  // there are registers for two rows' states
-    constexpr int KV = KT / 4;
+    constexpr bool EXACT = sizeof(TT) == 4 && sizeof(ST) == 2;
+    constexpr int KV = KT / 4, G = PAIRS ? 2 : 4, Q = PAIRS || (sizeof(TT) == 4 && NW <= 8) ? 1 : 2;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const unsigned all = (unsigned)(p.nk * tiles), block = blockIdx.x / all, tg = blockIdx.x - block * all;
     const int g = (int)(tg / (unsigned)tiles), tile = (int)(tg - (unsigned)g * (unsigned)tiles);
@@ -112,7 +113,6 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW)
     // this lane's four channels, and the one this thread finishes
     const int have = min(KT, p.K - warp * KT);  // states that there are, 0 or less: none
     const long long k0 = (long long)warp * KT;
-    const bool pairs = KT == 4 && p.K <= 8;  // groups of two states
     long long st_at[4], x_at[4], d_at[4];
     bool on[4];
     float A[KT][4], bias[4];
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW)
             Token next;
             if (!ONE && t + 1 < len) ask_token(w, t + 1, next);
             float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            [[maybe_unused]] float first[4];  // the sum of a group that another follows
+            [[maybe_unused]] float first[4];  // the first of a warp's two groups
             if (have > 0) {
                 float d[4], in[4];
 #pragma unroll
@@ -218,17 +218,20 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW)
                     const float B = now.B[i / 4].get(i % 4), C = now.C[i / 4].get(i % 4);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        S[i][e] = advance<TT>(decay<TT>(__fmul_rn(d[e], A[i][e])), S[i][e], __fmul_rn(in[e], B));
-                        if (KT == 8 ? i == 4 : i == 2 && pairs) {
+                        S[i][e] = advance<EXACT>(decay<TT>(__fmul_rn(d[e], A[i][e])), S[i][e], __fmul_rn(in[e], B));
+                        if (G < KT && i == G) {
                             first[e] = y[e];
                             y[e] = 0.0f;
                         }
                         y[e] = fmaf(C, S[i][e], y[e]);  // of no meaning, and not used, where there are no outputs
                     }
                 }
-                if (KT == 8 ? have > 4 : have > 2 && pairs)
+                if constexpr (G < KT) {
+                    if (have > G) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = first[e] + y[e];
+                        for (int e = 0; e < 4; ++e) y[e] = first[e] + y[e];
+                    }
+                }
                 if (t + 1 == w.kept) {
 #pragma unroll
                     for (int i = 0; i < KT; ++i)
@@ -242,8 +245,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW)
                 if (mon) {
                     float o = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < NW; i += KT == 8 ? 2 : 4)
-                        o += KT == 8 ? q[i][tid] + q[i + 1][tid] : (q[i][tid] + q[i + 1][tid]) + (q[i + 2][tid] + q[i + 3][tid]);
+                    for (int i = 0; i < NW; i += Q) o += Q == 1 ? q[i][tid] : q[i][tid] + q[i + 1][tid];
                     o = fmaf(D, to_f32(now.mx), o);
                     if (gate) o *= silu(to_f32(now.mz));
                     w.out[t * p.o_ts + mo_at] = from_f32<TT>(o);
@@ -272,7 +274,7 @@ __global__ void __launch_bounds__(32 * NW, 16 / NW)
     }
 }
 
-template <typename TT, typename DT, typename ST, int KT, int NW, bool VEC, bool BC, bool ONE>
+template <typename TT, typename DT, typename ST, int KT, int NW, bool VEC, bool BC, bool ONE, bool PAIRS>
 cudaError_t go(const ScanParams &p, cudaStream_t s) {
     const long long tiles = ((long long)p.r * p.V + kStepTile - 1) / kStepTile, heads = p.nk * tiles;
     // as many rows a block as leaves each multiprocessor its blocks once over
@@ -281,18 +283,20 @@ cudaError_t go(const ScanParams &p, cudaStream_t s) {
     if (rows > kStepRows) rows = kStepRows;
     const long long blocks = (p.batch + rows - 1) / rows * heads;
     if (blocks >= 1ll << 31) return cudaErrorInvalidConfiguration;
-    k_scan_step<TT, DT, ST, KT, NW, VEC, BC, ONE><<<(unsigned)blocks, 32 * NW, 0, s>>>(p, (int)tiles, (int)rows);
+    k_scan_step<TT, DT, ST, KT, NW, VEC, BC, ONE, PAIRS><<<(unsigned)blocks, 32 * NW, 0, s>>>(p, (int)tiles, (int)rows);
     return cudaGetLastError();
 }
-template <typename TT, typename DT, typename ST, int KT, int NW> cudaError_t step_form(const ScanParams &p, bool vec, cudaStream_t s) {
-    if (!vec) return go<TT, DT, ST, KT, NW, false, false, false>(p, s);
-    if (!p.bc_vec || p.K % KT != 0) return go<TT, DT, ST, KT, NW, true, false, false>(p, s);
-    return p.max_len == 1 ? go<TT, DT, ST, KT, NW, true, true, true>(p, s) : go<TT, DT, ST, KT, NW, true, true, false>(p, s);
+template <typename TT, typename DT, typename ST, int KT, int NW, bool PAIRS = false>
+cudaError_t step_form(const ScanParams &p, bool vec, cudaStream_t s) {
+    if (!vec) return go<TT, DT, ST, KT, NW, false, false, false, PAIRS>(p, s);
+    if (!p.bc_vec || p.K % KT != 0) return go<TT, DT, ST, KT, NW, true, false, false, PAIRS>(p, s);
+    return p.max_len == 1 ? go<TT, DT, ST, KT, NW, true, true, true, PAIRS>(p, s) : go<TT, DT, ST, KT, NW, true, true, false, PAIRS>(p, s);
 }
 // States a warp has and warps, by K.  Four states a warp wherever they fit leave registers for the next row's.  Measured
 // against four warps of 8, 16 and 32 states, 256 single tokens x 4096 channels, us: 32 states 61 / 78; x 2048 channels: 64 states
 // 64 / 82, 128 states 121 / 371; 64 rows of 2 to 8 tokens, 128 states: 184 / 527.
 template <typename TT, typename DT, typename ST> cudaError_t step_states(const ScanParams &p, bool vec, cudaStream_t s) {
+    if (p.K <= 8) return step_form<TT, DT, ST, 4, 4, true>(p, vec, s);
     if (p.K <= 16) return step_form<TT, DT, ST, 4, 4>(p, vec, s);
     if (p.K <= 32) return step_form<TT, DT, ST, 4, 8>(p, vec, s);
     if (p.K <= 64) return step_form<TT, DT, ST, 4, 16>(p, vec, s);

@@ -125,9 +125,9 @@ struct ScanParams {
     long long max_slots;
     const int *slot_idx, *offsets, *counts;
     // rows cut into segments of `seg` tokens (0: whole): ws holds, for each of them,
-    // its own state from zero, which becomes its start state, and the sum of its step sizes
+    // its own state from zero, which becomes its start state, and the sum of its step sizes; float32 tokens over
+    // a bfloat16 pool: its start state alone, left by one pass through the row
     int seg;
-    int ordered;       // segments' start states are left by one pass through each row, in its order; ws has nothing else
     float *ws;
     unsigned *status;
 };
@@ -142,7 +142,8 @@ cudaError_t launch_scan_step(const ScanParams &p, bool tok_bf16, bool dt_bf16, b
 cudaError_t launch_scan(const ScanParams &p, bool tok_bf16, bool dt_bf16, bool vec, cudaStream_t s);
 cudaError_t launch_scan_bb(const ScanParams &p, bool vec, cudaStream_t s);  // bfloat16 tokens and step sizes
 cudaError_t launch_scan_bf(const ScanParams &p, bool vec, cudaStream_t s);  // bfloat16 tokens, float32 step sizes
-cudaError_t launch_scan_ff(const ScanParams &p, bool vec, cudaStream_t s);  // float32
+cudaError_t launch_scan_ff(const ScanParams &p, bool vec, cudaStream_t s);  // float32, float32 pool
+cudaError_t launch_scan_fx(const ScanParams &p, bool vec, cudaStream_t s);  // float32, bfloat16 pool
 cudaError_t launch_scan_join(const ScanParams &p, cudaStream_t s);
 cudaError_t launch_scan_step_bb(const ScanParams &p, bool vec, cudaStream_t s);
 cudaError_t launch_scan_step_bf(const ScanParams &p, bool vec, cudaStream_t s);

@@ -31,22 +31,24 @@ template <typename TT> __device__ __forceinline__ float rate(float a) {
 }
 template <typename TT> __device__ __forceinline__ float decay(float e) { return sizeof(TT) == 2 ? ex2(e) : expf(e); }
 
-// A state's step from its decay and the token's own part.  float32 tokens round the product and the sum one by one, as
-// they do every operation on the way to a state, so that all forms of a call, and plain float32 arithmetic, have the
-// same states bit for bit: a bfloat16 pool can make neighbours, 2^16 times as far apart, of states that differ in their
-// last bit, and the next call starts from them.  bfloat16 outputs do not show that; bfloat16 tokens take the fused form,
-// half the instructions.
-template <typename TT> __device__ __forceinline__ float advance(float power, float S, float own) {
-    return sizeof(TT) == 2 ? fmaf(power, S, own) : __fadd_rn(__fmul_rn(power, S), own);
+// A state's step from its decay and the token's own part.  EXACT (float32 tokens over a bfloat16 pool): product and sum are
+// rounded one by one, as is every operation on the way to a state, so that all forms of a call, and plain
+// float32 arithmetic, have the same states bit for bit.  Such a pool can make neighbours, 2^16 times as far apart, of states
+// that differ in their last bit, and the next call starts from them.  A float32 pool does not, nor do bfloat16
+// outputs show it: others take the fused form, half the instructions.
+template <bool EXACT> __device__ __forceinline__ float advance(float power, float S, float own) {
+    return EXACT ? __fadd_rn(__fmul_rn(power, S), own) : fmaf(power, S, own);
 }
-template <typename TT> __device__ __forceinline__ float2 advance(float2 power, float2 S, float2 own) {
-    if (sizeof(TT) == 2) return __ffma2_rn(power, S, own);
+template <bool EXACT> __device__ __forceinline__ float2 advance(float2 power, float2 S, float2 own) {
+    if (!EXACT) return __ffma2_rn(power, S, own);
     const float2 m = __fmul2_rn(power, S);  // added one by one: nvcc 13.0 makes one instruction of __fadd2_rn and this
     return make_float2(__fadd_rn(m.x, own.x), __fadd_rn(m.y, own.y));
 }
 
 // The readout's order, the same in every form, so that a row has the same bits in any call: groups of four states (up to
-// 8 states: of two) by multiply-adds from 0; four groups as (0 + 1) + (2 + 3); these sums one after the other.
+// 8 states: of two) by multiply-adds from 0; their sums by pairs (past 64 states by fours, as (0 + 1) + (2 + 3); float32
+// tokens, 9 to 32 states: one by one); and those one after the other.  Warps have one group or two by the form, so bfloat16
+// tokens need the pairs; for float32 they cost 1% (8 ragged rows x 4096 channels 654 us without).
 __device__ constexpr int scan_group(int states_a_warp) { return states_a_warp < 4 ? 2 : 4; }
 
 // log(1 + e^v) without cancellation: max(v, 0) + log1p(e^-|v|).  bfloat16 tokens: log1p(e) / e by its Chebyshev

@@ -582,11 +582,12 @@ int gdr_short_conv(const gdr_short_conv_args *args, void *stream);
  *
  * Precision.  States and sums are float32 inside a call; a bfloat16 pool and
  * bfloat16 outputs are rounded to nearest-even once.
- *   float32 tokens: expf and log1pf, and every operation that leads to a state
- *   is rounded by itself, in the order above (softplus(v) = max(v, 0) +
- *   log1p(e^-|v|); d x before B): states are those of plain float32 arithmetic,
- *   bit for bit.  Only a row that is cut over a float32 pool (see below) has the
- *   roundings of its joined decays in them.
+ *   float32 tokens: expf and log1pf, and S's product and sum as one fused
+ *   multiply-add.  Over a bfloat16 pool every operation that leads to a state is
+ *   rounded by itself, in the order above (softplus(v) = max(v, 0) +
+ *   log1p(e^-|v|); d x before B): its states are those of plain float32
+ *   arithmetic, bit for bit, so that its own rounding, which makes much of a
+ *   last bit, goes the same way as there.
  *   bfloat16 tokens, whose own rounding is 2^-8: softplus(v) is off by up to
  *   2^-21 of itself (for v < 0 by |v| 2^-24 more), a decay e^-a by up to 2^-22
  *   and a 2^-23.  A decay's error is downwards mostly, so that a state that

@@ -1,5 +1,5 @@
-"""Which bits a row of the selective scan has: float32 tokens move states by float32 operations rounded one by one,
-and a row's results are the same in whatever form and company it is computed."""
+"""Which bits a row of the selective scan has: float32 tokens move the states of a bfloat16 pool by float32 operations
+rounded one by one, and a row's results are the same in whatever form and company it is computed."""
 from __future__ import annotations
 
 import pytest
@@ -44,14 +44,13 @@ def _plain(c, pool):
     return out, 1.01 * bound
 
 
-@pytest.mark.parametrize("pool", [BF16, F32])
 @pytest.mark.parametrize("lens,bound", [([1] * 9, 1), ([5, 1, 7, 0, 16], 16), ([40, 3, 0, 41], 0), ([2, 17, 1], 0)])
 @pytest.mark.parametrize("K,V,nk,nv", [(16, 64, 1, 2), (64, 32, 1, 1), (27, 33, 3, 3), (8, 20, 1, 2), (128, 8, 1, 1)])
-def test_float32_tokens_call_after_call(pool, lens, bound, K, V, nk, nv):
+def test_float32_tokens_call_after_call(lens, bound, K, V, nk, nv):
     """Call after call on one pool.  A bfloat16 pool rounds what a call leaves: states that differ in their last float32
     bit can become neighbouring bfloat16 values, 2^16 times as far apart, and the next call starts there.  With the
     same bits nothing grows."""
-    c = Case(lens, nk, nv, K, V, (F32, F32, pool), pad=(1,), seed=K + V)
+    c = Case(lens, nk, nv, K, V, (F32, F32, BF16), pad=(1,), seed=K + V)
     got, want = c.pool.clone(), c.pool.clone()
     for call in range(6):
         c.x, c.dt = c.x.roll(1, 0), c.dt.roll(1, 0)
