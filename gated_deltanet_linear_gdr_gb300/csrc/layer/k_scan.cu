@@ -11,12 +11,13 @@ __global__ void __launch_bounds__(256) k_scan_join(const __grid_constant__ ScanP
     const long long per = (long long)p.nv * p.K * p.V, i = (long long)blockIdx.x * 256 + threadIdx.x;
     if (i >= per) return;
     const long long most = scan_pieces(p.T, p.seg, p.batch);
+    const int seg = scan_segment(p);
     long long piece = 0;
     ScanUnit u;
     int n = 0;
     for (int b = 0; b <= (int)blockIdx.y; ++b) {
         piece += n;
-        n = scan_row(p, b, false, u) ? pieces(u.len, p.seg) : 0;
+        n = scan_row(p, b, false, u) ? pieces(u.len, seg) : 0;
     }
     if (n == 0 || u.slot < 0) return;
     const long long kv = (long long)p.K * p.V, kj = i % kv;
@@ -28,7 +29,6 @@ __global__ void __launch_bounds__(256) k_scan_join(const __grid_constant__ ScanP
     const float *sum = p.ws + most * per + piece * p.nv * p.V + (long long)h * p.V + v;
     // eight segments' values on their way at a time
     constexpr int kAhead = 8;
-    n = (int)(most - piece < n ? most - piece : n);
     for (int s = 0; s < n; s += kAhead) {
         float o[kAhead], d[kAhead];
 #pragma unroll

@@ -39,7 +39,10 @@ template <bool EXACT> __device__ __forceinline__ bool scan_piece(const ScanParam
     ScanUnit r;
     bool live = false;
     if (lane < p.batch) live = scan_row(p, lane, leader && piece == 0, r);
-    int n = live ? pieces(r.len, p.seg) : 0, upto = n;
+    // as scan_segment(), a row a lane
+    const bool decreases = lane < p.batch && p.offsets[lane] > p.offsets[lane + 1];
+    const int seg = __any_sync(kFull, decreases) ? 0x7fffffff : p.seg;
+    int n = live ? pieces(r.len, seg) : 0, upto = n;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
         const int o = __shfl_up_sync(kFull, upto, m);
@@ -50,21 +53,21 @@ template <bool EXACT> __device__ __forceinline__ bool scan_piece(const ScanParam
     const int b = __ffs(behind) - 1;
     const int s = (int)piece - __shfl_sync(kFull, upto - n, b);
     if (!scan_row(p, b, false, u)) return false;
-    const long long from = (long long)s * p.seg;
+    const long long from = (long long)s * seg;
     u.t0 += from;
     const long long left = u.len - from, kept = u.kept - from;
-    u.last = left <= p.seg;
-    u.len = (int)(left < p.seg ? left : p.seg);
+    u.last = left <= seg;
+    u.len = (int)(left < seg ? left : seg);
     u.kept = kept <= 0 || kept > u.len || EXACT ? 0 : (int)kept;
     u.piece = piece;
     return true;
 }
 
 // The first segment of row b among all rows' segments.
-__device__ __forceinline__ long long scan_first_piece(const ScanParams &p, int b, int lane) {
+__device__ __forceinline__ long long scan_first_piece(const ScanParams &p, int b, int seg, int lane) {
     ScanUnit r;
     int n = 0;
-    if (lane < b && scan_row(p, lane, false, r)) n = pieces(r.len, p.seg);
+    if (lane < b && scan_row(p, lane, false, r)) n = pieces(r.len, seg);
     return (long long)__reduce_add_sync(kFull, (unsigned)n);
 }
 
@@ -115,7 +118,8 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
     } else if (!scan_row(p, (int)row, tg == 0 && tid == 0, u)) {
         return;
     }
-    if (ordered) u.piece = scan_first_piece(p, (int)row, lane);
+    const int seg = ordered ? scan_segment(p) : 0;
+    if (ordered) u.piece = scan_first_piece(p, (int)row, seg, lane);
     const int c0 = tile * W, width = min(W, p.r * p.V - c0);  // channels of the key head's value heads, this block's first
     // A channel of the block as (value head, channel).
     auto head = [&](int c, int &j) {
@@ -244,11 +248,9 @@ __global__ void __launch_bounds__(32 * NW + kScanHelpers, KT * NW <= 16 ? 2 : KT
         int n = u.len, cut = first ? 0 : u.kept;
         // segments begin where chunks do
         int until = 0;
-        long long left = ordered ? scan_pieces(p.T, p.seg, p.batch) - u.piece : 0;  // places for their states
         auto begins = [&]() {
             if (!ordered || until-- > 0) return;
-            until = p.seg / N - 1;
-            if (left-- <= 0) return;
+            until = seg / N - 1;
             put(true);
             ws0 += (long long)p.nv * p.K * p.V;
             ws1 += (long long)p.nv * p.K * p.V;

@@ -113,4 +113,12 @@ __device__ __forceinline__ bool scan_row(const ScanParams &p, int b, bool leader
     return true;
 }
 
+// Tokens a segment in a call that is cut.  Rows lie on one another only where offsets decrease (a row that is flagged);
+// their segments may then be more than the workspace has places for, and every row is one segment, however long.
+__device__ __forceinline__ int scan_segment(const ScanParams &p) {
+    bool ordered = true;
+    for (int b = 0; b < p.batch; ++b) ordered &= p.offsets[b] <= p.offsets[b + 1];
+    return ordered ? p.seg : 0x7fffffff;
+}
+
 }  // namespace gdr

@@ -579,6 +579,8 @@ int gdr_short_conv(const gdr_short_conv_args *args, void *stream);
  *          the accepted tokens then go in by such a call.
  * workspace  as in gdr_linattn_args, by gdr_selective_scan_workspace_bytes().
  * No two rows of a call move the same slot.  K is 1 to 128, V any.  A non-finite value spoils its own row only.
+ * Rows have tokens in common only where offsets decrease: each then moves its
+ * slot by all of its tokens, and such a token's output is either row's.
  *
  * Precision.  States and sums are float32 inside a call; a bfloat16 pool and
  * bfloat16 outputs are rounded to nearest-even once.
