@@ -320,16 +320,23 @@ __global__ void __launch_bounds__(kThreads) k_short_conv(const __grid_constant__
                 if (problem) flag(p.status, problem);
             }
         const long long t0 = (long long)block * p.run, t1 = t0 + p.run < p.T ? t0 + p.run : p.T;
-        // the row of the first token: the last one that does not begin behind it
+        // the row of the first token: the last one that does not begin behind it.  Where offsets decrease that
+        // finds nothing, and the block goes through all of the rows.
         int b = -1;
+        bool ascend = true;
         for (int i = 0; i <= p.batch; i += kThreads) {
-            const bool before = i + tid <= p.batch && p.offsets[i + tid] <= t0;
-            b += __syncthreads_count(before);
+            const int at = i + tid;
+            const bool some = at <= p.batch;
+            const int o = some ? p.offsets[at] : 0;
+            ascend &= !some || at == 0 || p.offsets[at - 1] <= o;
+            b += __syncthreads_count(some && o <= t0);
         }
+        ascend = __syncthreads_and(ascend);
         if (!on) return;
         th.weights();
-        for (b = b < 0 ? 0 : b; b < p.batch && p.offsets[b] < t1; ++b) {
+        for (b = b < 0 || !ascend ? 0 : b; b < p.batch && (!ascend || p.offsets[b] < t1); ++b) {
             const ConvRow r = conv_row(p, b);
+            if (r.lo >= t1) continue;
             const bool first = r.lo >= t0;  // the row begins in this run
             const long long head = r.lo + (W - 1);
             const long long s = first ? r.lo : (t0 > head ? t0 : head), end = first && head > t1 ? head : t1;

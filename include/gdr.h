@@ -509,7 +509,8 @@ int gdr_block_norm(const gdr_norm_args *args, void *stream);
  * conv_state [max_slots, channels, width-1] in state_dtype (bfloat16 loses
  *          nothing of bfloat16 inputs), any positive strides, not lying on x or
  *          out; unused when width == 1.
- * slot_idx, offsets, max_row_len  as in gdr_step_args.
+ * slot_idx, offsets, max_row_len  as in gdr_step_args.  (Where offsets decrease, rows
+ * may have tokens in common: such a token's output is either row's.)
  * keep_state, counts  which inputs a row leaves in its slot: with keep_state the
  *          last width-1 of (old state, the row's first counts[b] inputs), where
  *          counts NULL means all of the row; counts[b] = 0 leaves the slot as it
@@ -580,7 +581,8 @@ int gdr_short_conv(const gdr_short_conv_args *args, void *stream);
  * workspace  as in gdr_linattn_args, by gdr_selective_scan_workspace_bytes().
  * No two rows of a call move the same slot.  K is 1 to 128, V any.  A non-finite value spoils its own row only.
  * Rows have tokens in common only where offsets decrease: each then moves its
- * slot by all of its tokens, and such a token's output is either row's.
+ * slot by all of its tokens (out apart from x and z), and such a token's output is
+ * either row's.
  *
  * Precision.  States and sums are float32 inside a call; a bfloat16 pool and
  * bfloat16 outputs are rounded to nearest-even once.

@@ -5,10 +5,11 @@ import pytest
 import torch
 
 import gated_deltanet_linear_gdr_gb300 as gdr
-from tests.state_space_helpers import accept_ref, check_close, scan_ref
-from tests.test_gpu_scan import DEV, TYPES, _cut, _ints
+from tests.state_space_helpers import accept_ref, check_close, conv_ref, scan_ref
+from tests.test_gpu_scan import BF16, DEV, F32, TYPES, _cut, _ints
 from tests.test_gpu_scan import Case as ScanCase
 from tests.test_gpu_accept import Case as AcceptCase
+from tests.test_gpu_short_conv import Case as ConvCase
 
 pytestmark = pytest.mark.gpu
 
@@ -40,6 +41,24 @@ def _apart(off, T, slots):
     for _, lo, hi in rows:
         ends.append(ends[-1] + hi - lo)
     return torch.tensor(order, device=DEV), _ints(ends), slots[[b for b, _, _ in rows]]
+
+
+@pytest.mark.parametrize("off,T", BAD)
+@pytest.mark.parametrize("C,tok", [(64, BF16), (33, F32), (2056, BF16)])
+@pytest.mark.parametrize("bound", [0, 400])
+def test_convolution(off, T, C, tok, bound):
+    c = ConvCase([1] * (len(off) - 1), C, 4, tok, seed=1)
+    c.x = torch.randn(T, C, generator=torch.Generator(device=DEV).manual_seed(2), device=DEV).to(tok)
+    c.off = _ints(off)
+    pool, out = c.pool.clone(), torch.zeros_like(c.x)
+    gdr.gdr_short_conv(*c.args(pool), out, max_row_len=bound)
+    order, ends, slots = _apart(off, T, c.slot)
+    want, bound, state = conv_ref(c.x[order], c.w, c.bias, c.pool, slots, ends)
+    check_close(out[order], want, bound, "out")
+    assert torch.equal(pool, state)
+    again = c.pool.clone()
+    gdr.gdr_short_conv(*c.args(again), state_only=True)
+    assert torch.equal(again, pool)
 
 
 @pytest.mark.parametrize("off,T", BAD)
