@@ -18,7 +18,8 @@
 // are not overwritten before they are used, in one launch.
 //
 // Measured, bfloat16 tokens x 8192 channels, float32 pool: 8 ragged rows, 17702 tokens, 105 us (5.6 TB/s, 82% of
-// the copy rate); 256 single tokens 15 us (8.4 at the copy rate; the call itself takes the host 11).
+// the copy rate); 256 single tokens 15 us (8.4 at the copy rate, though most of the states come from L2 there; the call itself
+// takes the host 11).  200000 rows of 5 tokens x 512 channels, lengths not bounded, 1031 us (664 at the copy rate).
 #include "scan_device.cuh"
 
 namespace gdr {
@@ -314,26 +315,33 @@ __global__ void __launch_bounds__(kThreads) k_short_conv(const __grid_constant__
             row(i + 1, b);
         }
     } else {
-        if (blockIdx.x == 0)  // one block looks at every row
-            for (int b = tid; b < p.batch; b += kThreads) {
-                const unsigned problem = conv_row(p, b).problem;
+        const long long t0 = (long long)block * p.run, t1 = t0 + p.run < p.T ? t0 + p.run : p.T;
+        if (tile == 0) {  // the blocks look at every row between them
+            const long long runs = (p.T + p.run - 1) / p.run;
+            for (long long b = (long long)block * kThreads + tid; b < p.batch; b += runs * kThreads) {
+                const unsigned problem = conv_row(p, (int)b).problem;
                 if (problem) flag(p.status, problem);
             }
-        const long long t0 = (long long)block * p.run, t1 = t0 + p.run < p.T ? t0 + p.run : p.T;
+        }
         // the row of the first token: the last one that does not begin behind it.  Where offsets decrease that
         // finds nothing, and the block goes through all of the rows.
-        int b = -1;
+        __shared__ int before[kThreads / 32];
+        int n = 0;
         bool ascend = true;
-        for (int i = 0; i <= p.batch; i += kThreads) {
-            const int at = i + tid;
-            const bool some = at <= p.batch;
-            const int o = some ? p.offsets[at] : 0;
-            ascend &= !some || at == 0 || p.offsets[at - 1] <= o;
-            b += __syncthreads_count(some && o <= t0);
+#pragma unroll 8
+        for (int i = tid; i <= p.batch; i += kThreads) {
+            const int o = p.offsets[i];
+            n += o <= t0;
+            ascend &= i == 0 || p.offsets[i - 1] <= o;
         }
+        n = __reduce_add_sync(kFull, n);
+        if (tid % 32 == 0) before[tid / 32] = n;
         ascend = __syncthreads_and(ascend);
         if (!on) return;
         th.weights();
+        int b = -1;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) b += before[i];
         for (b = b < 0 || !ascend ? 0 : b; b < p.batch && (!ascend || p.offsets[b] < t1); ++b) {
             const ConvRow r = conv_row(p, b);
             if (r.lo >= t1) continue;
@@ -375,6 +383,9 @@ template <typename TT, int W> cudaError_t go(ConvOpParams p, cudaStream_t s) {
         // runs of up to 64 tokens, shorter ones where they would leave multiprocessors without work
         p.run = 64;
         while (p.run > 8 && (p.T + p.run - 1) / p.run * p.tiles < 152 * 12) p.run /= 2;
+        // Every block reads all offsets, kThreads at a time: a token for each of those steps at least.
+        const int steps = p.batch / kThreads + 1;
+        if (p.run < steps) p.run = steps;
         blocks = (p.T + p.run - 1) / p.run;
     }
     blocks *= p.tiles;
