@@ -55,6 +55,51 @@ bool rows_overlap(const void *a, int64_t as, const void *b, int64_t bs, int64_t 
     return d < width * es || d > (as - width) * es;
 }
 
+// A tensor of [tokens, heads] runs of bytes, strides in bytes.
+struct Runs {
+    int64_t at, tokens, token_stride, heads, head_stride, run;
+};
+Runs runs(const void *p, int dtype, int64_t tokens, int64_t ts, int64_t heads, int64_t hs, int64_t width) {
+    const int64_t es = esize(dtype);
+    if (ts == 0) tokens = 1;  // all of them the same run
+    if (hs == 0) heads = 1;
+    return {(int64_t)reinterpret_cast<uintptr_t>(p), tokens, ts * es, heads, hs * es, width * es};
+}
+
+// Whether two such tensors have bytes in common.  Exact where they are parts of one projection (tokens of one stride, and
+// heads of one stride or apart within a token, or the other way round); else their whole ranges must be apart.
+bool runs_overlap(const Runs &a, const Runs &b) {
+    struct Level {
+        int64_t n, stride;
+    };
+    const bool tokens_outside = a.token_stride * (a.tokens > 1) >= a.head_stride * (a.heads > 1);
+    const Level ao = tokens_outside ? Level{a.tokens, a.token_stride} : Level{a.heads, a.head_stride};
+    const Level ai = tokens_outside ? Level{a.heads, a.head_stride} : Level{a.tokens, a.token_stride};
+    const Level bo = tokens_outside ? Level{b.tokens, b.token_stride} : Level{b.heads, b.head_stride};
+    const Level bi = tokens_outside ? Level{b.heads, b.head_stride} : Level{b.tokens, b.token_stride};
+    const auto length = [](const Level &l, int64_t each) { return (l.n - 1) * l.stride + each; };
+    const auto apart = [](int64_t la, int64_t lb, int64_t d) { return d >= la || -d >= lb; };  // b begins d behind a
+    const auto one_stride = [](const Level &x, const Level &y, int64_t lx, int64_t ly) {
+        const int64_t stride = x.n > 1 ? x.stride : y.stride;
+        return (x.n > 1 || y.n > 1) && (x.n == 1 || y.n == 1 || x.stride == y.stride) && lx <= stride && ly <= stride ? stride : 0;
+    };
+    // runs of two inner levels, the second's first one d behind the first's
+    const auto inner = [&](int64_t d) {
+        if (apart(length(ai, a.run), length(bi, b.run), d)) return false;
+        const int64_t stride = one_stride(ai, bi, a.run, b.run);
+        if (!stride) return true;
+        const int64_t m = (d % stride + stride) % stride;
+        return !apart(a.run, b.run, m) || !apart(a.run, b.run, m - stride);
+    };
+    const int64_t la = length(ai, a.run), lb = length(bi, b.run), d = b.at - a.at;
+    if (apart(length(ao, la), length(bo, lb), d)) return false;
+    if (ao.n == 1 && bo.n == 1) return inner(d);
+    const int64_t stride = one_stride(ao, bo, la, lb);
+    if (!stride) return true;
+    const int64_t m = (d % stride + stride) % stride;
+    return inner(m) || inner(m - stride);
+}
+
 int check_conv(const gdr_short_conv_args *a, const char *fn) {
     if (!a) return fail(GDR_ERR_INVALID_ARG, "%s: args is NULL", fn);
     int rc = check_tokens(a->total_tokens, a->batch, fn);
@@ -159,6 +204,25 @@ int check_scan(const gdr_scan_args *a, const char *fn) {
     if (a->workspace_bytes < 0) return fail(GDR_ERR_INVALID_ARG, "%s: workspace_bytes < 0", fn);
     if (a->workspace && !aligned(a->workspace, 16))
         return fail(GDR_ERR_UNSUPPORTED, "%s: workspace must be 16-byte aligned", fn);
+    if (a->out && a->total_tokens > 0) {
+        const auto wide = [&](const void *p, int64_t ts, int64_t hs) {
+            return runs(p, a->token_dtype, a->total_tokens, ts, a->nv, hs, a->V);
+        };
+        const Runs out = wide(a->out, a->out_seq_stride, a->out_head_stride);
+        const auto lies_on = [&](const void *p, int64_t ts, int64_t hs) {  // x or z, but not their place itself
+            const bool itself = p == a->out && (ts == a->out_seq_stride || a->total_tokens == 1) &&
+                                (hs == a->out_head_stride || a->nv == 1);
+            return p && !itself && runs_overlap(out, wide(p, ts, hs));
+        };
+        const char *on = nullptr;
+        if (lies_on(a->x, a->x_seq_stride, a->x_head_stride)) on = "x";
+        else if (lies_on(a->z, a->z_seq_stride, a->z_head_stride)) on = "z";
+        else if (runs_overlap(out, runs(a->dt, a->dt_dtype, a->total_tokens, a->dt_seq_stride, a->nv, a->dt_head_stride,
+                                        a->dt_elem_stride ? a->V : 1))) on = "dt";
+        else if (runs_overlap(out, runs(a->B, a->token_dtype, a->total_tokens, a->B_seq_stride, a->nk, a->B_head_stride, a->K))) on = "B";
+        else if (runs_overlap(out, runs(a->C, a->token_dtype, a->total_tokens, a->C_seq_stride, a->nk, a->C_head_stride, a->K))) on = "C";
+        if (on) return fail(GDR_ERR_INVALID_ARG, "%s: out lies on %s", fn, on);
+    }
     return GDR_OK;
 }
 
