@@ -28,9 +28,9 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kAhead = 8;      // tokens of a batch
 // Rows up to here are taken whole, vectors of channels and others.  Measured, whole against runs, us: 256 rows x 8192 channels, one
-// token 18.4 / 20.5, 2 tokens 22.5 / 24.6, 8 tokens 36.9 / 32.8, 16 tokens 57 / 43; 64 rows of 2 to 8 tokens x 2047 channels, two
-// calls, 14.3 / 18.5.
-constexpr int kShortRow = 4, kShortOddRow = 8;
+// token 14.9 / 18.3, 5 tokens 26.7 / 31.6, 7 tokens 32.7 / 41.0, 8 tokens 34.4 / 30.7, 16 tokens 56 / 41; 1000 rows of 7 tokens x
+// 4096 channels 54.9 / 69.0; 64 rows of 2 to 8 tokens x 2047 channels, two calls, 14.3 / 18.5.
+constexpr int kShortRow = 7, kShortOddRow = 8;
 constexpr int kRows = 16;  // by blocks of so many at most
 
 struct ConvRow {

@@ -26,3 +26,15 @@ def test_very_many_rows_of_any_length():
         assert torch.equal(got, out[start:start + T])
         start += T
     assert torch.equal(pool, again)
+
+
+@pytest.mark.parametrize("tok", [BF16, torch.float32])
+@pytest.mark.parametrize("C", [64, 1028, 33])
+@pytest.mark.parametrize("longest", range(1, 10))
+def test_rows_have_the_same_bits_in_either_form(tok, C, longest):
+    """Rows that are taken whole, and the same ones by runs of tokens."""
+    lens = [longest, 0, 1] + [1 + (7 * i) % longest for i in range(40)]
+    c = Case(lens, C, 4, tok, seed=longest)
+    pool, again = c.pool.clone(), c.pool.clone()
+    out = gdr.gdr_short_conv(*c.args(pool), max_row_len=longest)
+    assert torch.equal(gdr.gdr_short_conv(*c.args(again)), out) and torch.equal(again, pool)
