@@ -228,7 +228,7 @@ int check_scan(const gdr_scan_args *a, const char *fn) {
 
 // Rows up to here go token by token (k_scan_step.cuh), longer ones by chunks (k_scan.cuh).  Measured, 64 rows x 32
 // heads of 128 channels, 16 states, a pass with outputs and one without, us, steps against chunks: rows of 2
-// 27 / 101, of 8 64 / 107, of 12 89 / 115, of 16 111 / 121.
+// 30 / 100, of 8 62 / 107, of 12 88 / 125, of 16 113 / 127.
 constexpr int kShortRow = 16;
 
 // float32 tokens over a bfloat16 pool: what a call leaves is rounded so that a state's last bit counts (scan_device.cuh),
@@ -241,10 +241,10 @@ bool scan_ordered(const gdr_scan_args *a) { return a->token_dtype == GDR_F32 && 
 // multiprocessor to itself takes 0.6 of the time of one that shares it with a second.  Cut rows spread evenly, and
 // cost a pass for the segments' own states (0.65 of a token's time a token), 48 tokens' time a segment to
 // begin and end and 250 tokens' for two more launches.  Measured, cut against whole, 16 states, us: 16383 tokens x 2048
-// channels 287 (864 tokens a segment; 2048: 330, 304: 320) against 915, 2048 x 2048 61 (256) / 123, 4 rows of 1024 to 4096 x 512 86 / 235;
+// channels 285 (864 tokens a segment; 2048: 330, 304: 320) against 948, 2048 x 2048 53 (256) / 123, 4 rows of 1024 to 4096 x 512 62 / 238;
 // left whole by this rule: 2 rows of 4096 x 4096 287 / 237.  Where states go through in order, a token of them takes
 // a third of the time of a token of 16 states, less beside more states.  Measured, cut against whole, float32, us: 16383
-// tokens x 2048 channels 1254 / 1695, 8192 x 1024 channels x 64 states 757 / 2208, 2500 x 64 channels 167 / 269.
+// tokens x 2048 channels 1200 / 1679, 8192 x 1024 channels x 64 states 734 / 2232, 2500 x 64 channels 158 / 265.
 int plan_scan(const gdr_scan_args *a) {
     const bool ordered = scan_ordered(a);
     if (ordered && !a->out) return 0;

@@ -17,11 +17,11 @@
 // the FP32 pipes do while memory delivers it; the FP64 pipes (2 operations a cycle and
 // multiprocessor) would take several times as long.  The error is itself a sum that is
 // rounded: after n additions it has lost n^2/2 2^-48 of the sum at worst.  So a lane
-// begins a new pair every 64 tokens: good to 2^-37 at worst, to 2^-45 by chance, however
+// begins a new pair every 64 tokens: good to 2^-36 at worst, to 2^-45 by chance, however
 // many tokens there are.  Beside that only single warps, at the joints, work in double.
 //
 // Measured, float32 probabilities: 256 rows of 5 to 8 tokens against 32000 tokens 24 us (9.3 at the copy rate), one
-// row against 131072 13 us, of which the host takes 11.
+// row against 131072 15 us, of which the host takes 11.
 #include <cooperative_groups.h>
 
 #include "../gdr_device.cuh"
@@ -360,7 +360,7 @@ template <typename PT> __global__ void __launch_bounds__(kThreads, 2) k_accept(c
 
 template <typename PT> cudaError_t go(const AcceptParams &p, cudaStream_t s) {
     // blocks a row: as many as run at once (two a multiprocessor), up to the largest portable cluster.  Measured, against
-    // one block a row: one row of 131072 tokens 16 / 41 us, 33 rows of 50257 16 / 20.
+    // one block a row: one row of 131072 tokens 15 / 33 us, 33 rows of 50257 15 / 16 (the host's call is 11 of each).
     int blocks = 1;
     while (blocks < 8 && (long long)p.batch * blocks * 2 <= 2 * 152) blocks *= 2;
     if ((long long)p.batch * blocks >= 1ll << 31) return cudaErrorInvalidConfiguration;

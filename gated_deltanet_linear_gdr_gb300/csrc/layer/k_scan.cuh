@@ -14,9 +14,9 @@
 // them once a channel, add up the NW partial readouts, apply D and the gate and store.
 // One barrier a chunk hands both sides' buffers over.
 //
-// Measured, bfloat16 tokens, 16 states, 8 ragged rows, 17702 tokens x 4096 channels: 380 us, where the bytes
-// alone would take 86 and the exponentials 124.  No one unit is full (counters: shared memory 63% of its
-// cycles, FMA 45%, exponentials 39%, an instruction issued in 62%); a token's chain of barriers and shared memory
+// Measured, bfloat16 tokens, 16 states, 8 ragged rows, 17702 tokens x 4096 channels: 372 us, where the bytes
+// alone would take 86 and the exponentials 124.  No one unit is full (counters: shared memory 64% of its
+// cycles, FMA 46%, exponentials 39%, an instruction issued in 63%); a token's chain of barriers and shared memory
 // reads, and their instructions, bound it.
 #pragma once
 
@@ -651,8 +651,8 @@ template <typename TT, typename DT, bool VEC, bool EXACT> cudaError_t scan_state
     if (p.K <= 16) return scan_go<TT, DT, 4, 4, VEC, EXACT>(p, s);
     if (p.K <= 32) {
         // Eight warps of four states take half the steps for a token, four of eight read shared memory less often.
-        // Measured with 32 states, us: 8 ragged rows x 4096 channels bfloat16 615 / 555, float32 1202 / 1294; 45 blocks
-        // of 5 rows of up to 301 tokens, float32 55 / 82.
+        // Measured with 32 states, us: 8 ragged rows x 4096 channels bfloat16 606 / 567, float32 1193 / 1327; 45 blocks
+        // of 5 rows of up to 301 tokens, float32 51 / 77.
         const long long tiles = ((long long)p.r * p.V + kScanTile - 1) / kScanTile;
         if (sizeof(TT) == 4 || (long long)p.batch * p.nk * tiles <= 152) return scan_go<TT, DT, 4, 8, VEC, EXACT>(p, s);
         if constexpr (sizeof(TT) == 2) return scan_go<TT, DT, 8, 4, VEC, EXACT>(p, s);

@@ -7,9 +7,10 @@
 // states are on their way while one is worked on.  The partial readouts meet in
 // shared memory, and one thread finishes each channel.
 //
-// Measured, bfloat16 tokens, float32 pool, 16 states: 256 single tokens x 4096 channels 29 us on the device (4.8 TB/s of states
-// and tokens, 71% of the copy rate; waits for memory are the largest stall); with channels but not B and C in vectors
-// (27 states) 90 us, against 225 with everything one by one.
+// Measured, bfloat16 tokens, float32 pool, 16 states: 256 single tokens x 4096 channels 33 us a call with pools in
+// turn (4.2 TB/s of states and tokens, 62% of the copy rate), 28 on the device alone, where half of the states come from L2;
+// waits for memory are the largest stall.  With channels but not B and C in vectors (27 states) 85 us, against 225 with
+// everything one by one.
 #pragma once
 
 #include "scan_device.cuh"
@@ -293,8 +294,8 @@ cudaError_t step_form(const ScanParams &p, bool vec, cudaStream_t s) {
     return p.max_len == 1 ? go<TT, DT, ST, KT, NW, true, true, true, PAIRS>(p, s) : go<TT, DT, ST, KT, NW, true, true, false, PAIRS>(p, s);
 }
 // States a warp has and warps, by K.  Four states a warp wherever they fit leave registers for the next row's.  Measured
-// against four warps of 8, 16 and 32 states, 256 single tokens x 4096 channels, us: 32 states 61 / 78; x 2048 channels: 64 states
-// 64 / 82, 128 states 121 / 371; 64 rows of 2 to 8 tokens, 128 states: 184 / 527.
+// against four warps of 8, 16 and 32 states, 256 single tokens x 4096 channels, us: 32 states 59 / 78; x 2048 channels: 64 states
+// 61 / 82, 128 states 118 / 371.
 template <typename TT, typename DT, typename ST> cudaError_t step_states(const ScanParams &p, bool vec, cudaStream_t s) {
     if (p.K <= 8) return step_form<TT, DT, ST, 4, 4, true>(p, vec, s);
     if (p.K <= 16) return step_form<TT, DT, ST, 4, 4>(p, vec, s);

@@ -17,7 +17,7 @@
 // the slot, from the row's last inputs: nobody else touches it, so old inputs
 // are not overwritten before they are used, in one launch.
 //
-// Measured, bfloat16 tokens x 8192 channels, float32 pool: 8 ragged rows, 17702 tokens, 105 us (5.6 TB/s, 82% of
+// Measured, bfloat16 tokens x 8192 channels, float32 pool: 8 ragged rows, 17702 tokens, 103 us (5.7 TB/s, 84% of
 // the copy rate); 256 single tokens 15 us (8.4 at the copy rate, though most of the states come from L2 there; the call itself
 // takes the host 11).  200000 rows of 5 tokens x 512 channels, lengths not bounded, 1031 us (664 at the copy rate).
 #include "scan_device.cuh"
